@@ -8,16 +8,32 @@ streams.
     import torch, accelerator_row_major_gb300 as g
     C = g.matmul(A, B)                     # A, B: contiguous fp32 CUDA tensors
     g.gemm_f32(A, B, C, M, N, K, stream)   # the C-ABI call, same arguments
+
+The rows of a language model next to those products (fp32 or bfloat16):
+
+    y, mean, rstd = g.layer_norm(x, weight, bias)
+    dx, dweight, dbias = g.layer_norm_grad(dy, x, weight, mean, rstd)
 """
 from ._binding import (FLAG_CTA_PAIR, FLAG_FORCE_STAGED, FLAG_SINGLE_CTA, FLAG_TILE64, FLAG_TILE128, FLAG_TILE256,  # noqa: F401
                        FLAG_NO_SPLIT_K, FLAG_ONE_TILE_PER_CTA, FLAG_TEST_DROP_COPY, GEMM_F32_EDEVICE, GEMM_F32_EINVAL,
-                       GEMM_F32_ELAUNCH, GEMM_F32_ESCRATCH, GEMM_F32_ETIMEOUT, GEMM_F32_OK, LIB_PATH, MODE_FFMA,
+                       GEMM_F32_ELAUNCH, GEMM_F32_ESCRATCH, GEMM_F32_ETARGET, GEMM_F32_ETIMEOUT, GEMM_F32_OK, LIB_PATH, MODE_FFMA,
                        MODE_TC1X, MODE_TC3X, MODES, GemmError, check, declared_symbols,
                        gemm_f32, gemm_f32_ex, gemm_f32_general, gemm_f32_host, gemm_f32_ladder, gemm_f32_last_kernel, gemm_f32_last_launches,
                        gemm_f32_noalloc, LADDER_STEPS,
                        gemm_f32_release, NOALLOC_SCRATCH_BYTES,
                        gemm_f32_clock_record, gemm_f32_status, gemm_f32_unit_rates,
                        gemm_f32_version)
+
+_LM = ("layer_norm", "layer_norm_grad")
+
+
+def __getattr__(name):
+    """The operators of _lm, imported on first use (they need torch; the C-ABI calls do not)."""
+    if name in _LM:
+        from . import _lm
+        globals().update({n: getattr(_lm, n) for n in _LM})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 def matmul(A, B, out=None, mode="tc3x", flags: int = 0, stream=None):

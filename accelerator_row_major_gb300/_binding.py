@@ -15,6 +15,7 @@ import re
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("GEMM_F32_LIBRARY") or os.path.join(_PKG, "libgemm_f32.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "gemm_f32.h")
+LM_HEADER = os.path.join(os.path.dirname(_PKG), "include", "gemm_f32_lm.h")
 
 GEMM_F32_OK = 0
 GEMM_F32_EINVAL = -1
@@ -22,12 +23,19 @@ GEMM_F32_EDEVICE = -2
 GEMM_F32_ELAUNCH = -3
 GEMM_F32_ETIMEOUT = -4
 GEMM_F32_ESCRATCH = -5
+GEMM_F32_ETARGET = -6
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 MODE_TC3X = 0
 MODE_FFMA = 1
 MODE_TC1X = 2
 MODES = {"tc3x": MODE_TC3X, "ffma": MODE_FFMA, "tc1x": MODE_TC1X}
+
+TYPE_F32 = 0
+TYPE_BF16 = 1
+SUM = 0
+MEAN = 1
+REDUCTIONS = {"sum": SUM, "mean": MEAN}
 
 FLAG_FORCE_STAGED = 0x1
 FLAG_TILE64 = 0x10
@@ -45,7 +53,8 @@ _ERRORS = {
     GEMM_F32_EDEVICE: "unsupported device (needs sm_103, GB300)",
     GEMM_F32_ELAUNCH: "kernel launch refused by the CUDA runtime",
     GEMM_F32_ETIMEOUT: "a bounded device-side wait ran out",
-    GEMM_F32_ESCRATCH: "the product needs more scratch than the library's fixed array",
+    GEMM_F32_ESCRATCH: "not enough scratch memory",
+    GEMM_F32_ETARGET: "a target outside the vocabulary",
 }
 
 
@@ -94,6 +103,11 @@ def _load() -> ctypes.CDLL:
     lib.gemm_f32_version.restype = ctypes.c_char_p
     lib.gemm_f32_unit_rates.argtypes = [ctypes.POINTER(UnitRates)]
     lib.gemm_f32_unit_rates.restype = ci
+    cl = ctypes.c_longlong
+    lib.gemm_f32_layer_norm.argtypes = [ci, ci, cl, ci, vp, cl, vp, vp, cf, vp, cl, vp, vp, vp]
+    lib.gemm_f32_layer_norm.restype = ci
+    lib.gemm_f32_layer_norm_grad.argtypes = [ci, ci, cl, ci, vp, cl, vp, cl, vp, vp, vp, vp, cl, vp, vp, vp]
+    lib.gemm_f32_layer_norm_grad.restype = ci
     u64p = ctypes.POINTER(ctypes.c_ulonglong)
     lib.gemm_f32_clock_record.argtypes = [vp, u64p, u64p]
     lib.gemm_f32_clock_record.restype = ci

@@ -45,7 +45,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        [os.path.join(os.path.dirname(PKG), "include", "gemm_f32.h"), __file__]
+        glob.glob(os.path.join(os.path.dirname(PKG), "include", "*.h")) + [__file__]
 
 
 def up_to_date(lib: str = LIB) -> bool:

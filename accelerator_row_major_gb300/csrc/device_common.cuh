@@ -88,7 +88,13 @@ enum BoundsSite : unsigned {
   kSiteBoundsC = 18,        // a read or write of C outside its window's extent
   kSiteBoundsWork = 19,     // a partial tile outside the split-tail workspace
   kSiteBoundsPack = 20,     // operand packing outside its source or destination
+  kSiteBoundsRows = 21,     // a row of a layer norm or a loss outside its matrix
+  kSiteBoundsScratch = 22,  // a layer norm's or a loss's scratch outside its part
 };
+
+// A target outside the vocabulary (data, not a failure of the kernels):
+// gemm_f32_status() reports it as GEMM_F32_ETARGET.
+constexpr unsigned kSiteTarget = 32;
 
 #ifdef GEMM_BOUNDS_CHECK
 __device__ __forceinline__ bool in_extent(size_t index, size_t extent, unsigned* err,

@@ -33,6 +33,8 @@ struct Workspace {
   size_t bytes = 0;
   void* pack = nullptr;           // repacked operands for the TMA path
   size_t pack_bytes = 0;
+  void* scratch = nullptr;        // layer norm and vocabulary loss (gemm_f32_lm.h)
+  size_t scratch_bytes = 0;
 };
 
 struct DeviceState {
@@ -212,27 +214,66 @@ int zero_fill(float* C, int M, int N, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+// *p, grown to at least `bytes` (1 MiB granules); nullptr if the memory
+// cannot be had.
+void* grow_buffer(void** p, size_t* have, size_t bytes) {
+  if (*have < bytes) {
+    if (*p) {
+      (void)cudaFree(*p);   // synchronises the device: no kernel still uses it
+      *p = nullptr;
+      *have = 0;
+    }
+    const size_t want = (bytes + (1u << 20) - 1) & ~static_cast<size_t>((1u << 20) - 1);
+    void* q = nullptr;
+    if (cudaMalloc(&q, want) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
+    *p = q;
+    *have = want;
+  }
+  return *p;
+}
+
+}  // namespace
+
 void* gemm_f32_impl::acquire_pack_buffer(int device, cudaStream_t stream, size_t bytes) {
   if (device < 0 || device >= kMaxDevices) return nullptr;
   DeviceState& st = g_devices[device];
   std::lock_guard<std::mutex> lock(st.ws_mu);
   Workspace& w = st.ws[stream];
-  if (w.pack_bytes < bytes) {
-    if (w.pack) {
-      (void)cudaFree(w.pack);   // synchronises the device: no kernel still uses it
-      w.pack = nullptr;
-      w.pack_bytes = 0;
-    }
-    const size_t want = (bytes + (1u << 20) - 1) & ~static_cast<size_t>((1u << 20) - 1);
-    void* p = nullptr;
-    if (cudaMalloc(&p, want) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return nullptr;
-    }
-    w.pack = p;
-    w.pack_bytes = want;
+  return grow_buffer(&w.pack, &w.pack_bytes, bytes);
+}
+
+void* gemm_f32_impl::acquire_scratch(int device, cudaStream_t stream, size_t bytes) {
+  if (device < 0 || device >= kMaxDevices) return nullptr;
+  try {
+    DeviceState& st = g_devices[device];
+    std::lock_guard<std::mutex> lock(st.ws_mu);
+    Workspace& w = st.ws[stream];
+    return grow_buffer(&w.scratch, &w.scratch_bytes, bytes);
+  } catch (...) {   // the map's own memory
+    return nullptr;
   }
-  return w.pack;
+}
+
+bool gemm_f32_impl::current_device(int* device, int* num_sms, unsigned** err) {
+  const DeviceState* const st = device_state(device);
+  if (!st || st->status != GEMM_F32_OK) return false;
+  *num_sms = st->num_sms;
+  *err = st->err;
+  return true;
+}
+
+void gemm_f32_impl::note_launches(int launches, const char* kernel) {
+  t_last_launches = launches;
+  t_last_kernel = kernel;
+}
+
+bool gemm_f32_impl::ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  return overlaps(a, a_bytes, b, b_bytes);
 }
 
 extern "C" int gemm_f32_ex(const float* A, const float* B, float* C, int M, int N, int K, int mode,
@@ -592,6 +633,7 @@ extern "C" int gemm_f32_status(gemm_f32_stream_t stream_handle, unsigned* site) 
     return GEMM_F32_ELAUNCH;
   }
   if (site) *site = word;
+  if (word == gemm_f32_dev::kSiteTarget) return GEMM_F32_ETARGET;
   return word ? GEMM_F32_ETIMEOUT : GEMM_F32_OK;
 }
 
@@ -632,6 +674,7 @@ extern "C" int gemm_f32_release(void) {
   for (auto& kv : st->ws) {
     if (kv.second.ptr) (void)cudaFree(kv.second.ptr);
     if (kv.second.pack) (void)cudaFree(kv.second.pack);
+    if (kv.second.scratch) (void)cudaFree(kv.second.scratch);
   }
   st->ws.clear();
   host_pipe_free(g_pipes[dev]);

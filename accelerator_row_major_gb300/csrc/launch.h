@@ -117,6 +117,21 @@ int pack_for_tma(GemmArgs& g, cudaStream_t stream, int* launches);
 // grows); nullptr when the memory cannot be had.  Freed by gemm_f32_release.
 void* acquire_pack_buffer(int device, cudaStream_t stream, size_t bytes);
 
+// The library's scratch buffer for `stream` on `device`, which the calls of
+// gemm_f32_lm.h lay out as they need: as acquire_pack_buffer, with a buffer
+// of its own.
+void* acquire_scratch(int device, cudaStream_t stream, size_t bytes);
+
+// The current device, set up on first use: its ordinal, multiprocessor count
+// and error word.  False when it is not an sm_103 part or a query failed.
+bool current_device(int* device, int* num_sms, unsigned** err);
+
+// What gemm_f32_last_launches() and gemm_f32_last_kernel() report next.
+void note_launches(int launches, const char* kernel);
+
+// Whether two byte ranges share a byte.
+bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes);
+
 // Small products (at most kSmallMaxWork multiply-adds, K <= kSmallMaxK) on a
 // latency-lean CUDA-core kernel, in every mode: below these sizes launch and
 // pipeline set-up dominate the tensor-core kernels' time.

@@ -58,10 +58,14 @@ enum gemm_f32_status_code {
                                calls are not affected: the split-tail
                                bookkeeping the call left half done is
                                ignored by the next call on its own          */
-    GEMM_F32_ESCRATCH = -5  /* gemm_f32_noalloc(): the product would need
+    GEMM_F32_ESCRATCH = -5, /* gemm_f32_noalloc(): the product would need
                                more scratch than the library's fixed array
-                               (GEMM_F32_NOALLOC_SCRATCH_BYTES); nothing was
-                               launched                                     */
+                               (GEMM_F32_NOALLOC_SCRATCH_BYTES); the calls of
+                               gemm_f32_lm.h: their scratch cannot be
+                               allocated.  Nothing was launched             */
+    GEMM_F32_ETARGET = -6   /* gemm_f32_status(): a loss call of
+                               gemm_f32_lm.h met a target outside the
+                               vocabulary (the row was left out)            */
 };
 
 /* Arithmetic modes of gemm_f32_ex. */
@@ -205,8 +209,8 @@ int gemm_f32_host(const float* A, const float* B, float* C, int M, int N, int K,
 /* Frees the current device's workspaces (split-tail partials, the copies of
  * operands the tensor-memory accelerator cannot read — odd strides,
  * unaligned bases or stored transposes in products of at least 2^27
- * multiply-adds are copied once into aligned buffers first — and
- * gemm_f32_host's device slots) after synchronising the device.
+ * multiply-adds are copied once into aligned buffers first —,
+ * gemm_f32_host's device slots and the scratch of gemm_f32_lm.h's calls) after synchronising the device.
  * Returns 0, or GEMM_F32_EDEVICE / GEMM_F32_ELAUNCH on a CUDA error. */
 int gemm_f32_release(void);
 
@@ -331,10 +335,11 @@ int gemm_f32_unit_rates(gemm_f32_unit_rates_t* rates);
  * built with -DGEMM_BOUNDS_CHECK (libgemm_f32_checked.so) appends
  * " bounds-checked".  In that build every hand-indexed global load and store
  * is checked against its array's extent: an index outside records site
- * 16 (A), 17 (B), 18 (C), 19 (split-tail partials) or 20 (operand copies)
- * in the error word that gemm_f32_status() reads, and the access is
- * skipped, as out-of-range elements are in "Lesson 10: shared-memory tiled
- * GEMM" (hpc.payai.win, section 3). */
+ * 16 (A), 17 (B), 18 (C), 19 (split-tail partials), 20 (operand copies), 21
+ * (rows of a layer norm or a loss) or 22 (their scratch) in the error word
+ * that gemm_f32_status() reads, and the access is skipped, as out-of-range
+ * elements are in "Lesson 10: shared-memory tiled GEMM" (hpc.payai.win,
+ * section 3). */
 const char* gemm_f32_version(void);
 
 #ifdef __cplusplus

@@ -1,0 +1,80 @@
+/*
+ * gemm_f32_lm -- layer norm and the loss over a vocabulary, with their
+ * gradients, on row-major matrices for NVIDIA GB300 (sm_103a): the last rows
+ * of a language model, next to the products of gemm_f32.h and in the same
+ * library.
+ *
+ * The rules of gemm_f32.h hold here too: caller-owned device pointers, every
+ * call asynchronous on `stream` and never synchronising the host, return code
+ * 0 or a negative GEMM_F32_E* code, nothing printed or thrown, device-side
+ * failures read later through gemm_f32_status(), gemm_f32_last_kernel() and
+ * gemm_f32_last_launches() for what the call launched.
+ *
+ * Types: matrices hold fp32 (GEMM_F32_TYPE_F32) or bfloat16
+ * (GEMM_F32_TYPE_BF16) elements, with a row stride in elements of at least
+ * the row's length.  Pointers are aligned to their element.  Row statistics,
+ * losses and every sum are fp32; an output in bfloat16 is rounded once, from
+ * its fp32 value.
+ *
+ * Scratch: the library owns one scratch buffer per (device, stream), grown
+ * with cudaMalloc (which synchronises the device) by the first call that
+ * needs more, kept for the next calls and freed by gemm_f32_release().  Make
+ * one call of a shape before capturing the same call into a CUDA graph.
+ * Where the memory cannot be had the call returns GEMM_F32_ESCRATCH and
+ * launches nothing.
+ *
+ * Every sum is taken in a fixed order: the same call on the same inputs
+ * gives the same bits.
+ */
+#ifndef GEMM_F32_LM_H
+#define GEMM_F32_LM_H
+
+#include <stddef.h>
+
+#include "gemm_f32.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum gemm_f32_type {
+    GEMM_F32_TYPE_F32 = 0,
+    GEMM_F32_TYPE_BF16 = 1
+};
+
+/* Layer norm of each row of x (rows x width):
+ *     mean = sum_d x_d / width
+ *     rstd = 1 / sqrt(sum_d (x_d - mean)^2 / width + eps)
+ *     y_d  = (x_d - mean) * rstd * weight_d + bias_d
+ * x and y hold `type`, weight and bias (width elements) `weight_type`, which
+ * is `type` or fp32.  weight may be NULL (1), bias may be NULL (0); mean and
+ * rstd (rows fp32 values each, what the gradient needs) may be NULL.  y may
+ * be x itself, with the same stride.  The variance is summed from the
+ * centred values.  rows == 0 does nothing.
+ * Returns 0, GEMM_F32_EINVAL (unknown type, width < 1, rows < 0, a stride
+ * below width, eps negative or not finite, a null or misaligned pointer, y
+ * overlapping x otherwise), GEMM_F32_EDEVICE or GEMM_F32_ELAUNCH. */
+int gemm_f32_layer_norm(int type, int weight_type, long long rows, int width, const void* x,
+                        long long ldx, const void* weight, const void* bias, float eps, void* y,
+                        long long ldy, float* mean, float* rstd, gemm_f32_stream_t stream);
+
+/* Gradients of gemm_f32_layer_norm for dy, the gradient of y.  With
+ * hat_d = (x_d - mean) * rstd and g_d = dy_d * weight_d, per row:
+ *     dx_d = rstd * (g_d - sum(g) / width - hat_d * sum(g * hat) / width)
+ * and over the rows:
+ *     dweight_d = sum dy_d * hat_d,   dbias_d = sum dy_d
+ * mean and rstd are those of the forward call.  dx holds `type`, dweight and
+ * dbias `weight_type`; each of the three may be NULL when it is not wanted.
+ * dx may be dy or x itself, with the same stride.  rows == 0 writes zeros
+ * into dweight and dbias.  Returns as gemm_f32_layer_norm, and
+ * GEMM_F32_ESCRATCH. */
+int gemm_f32_layer_norm_grad(int type, int weight_type, long long rows, int width, const void* dy,
+                             long long lddy, const void* x, long long ldx, const void* weight,
+                             const float* mean, const float* rstd, void* dx, long long lddx,
+                             void* dweight, void* dbias, gemm_f32_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GEMM_F32_LM_H */
