@@ -9,9 +9,11 @@ streams.
     C = g.matmul(A, B)                     # A, B: contiguous fp32 CUDA tensors
     g.gemm_f32(A, B, C, M, N, K, stream)   # the C-ABI call, same arguments
 
-The rows of a language model next to those products (fp32 or bfloat16):
+The rows of a language model next to those products (layer norm, the loss
+over a vocabulary, and their gradients; fp32 or bfloat16 rows):
 
     y, mean, rstd = g.layer_norm(x, weight, bias)
+    total, loss, lse, dy, dw = g.vocab_loss_grad(y, w, targets)
     dx, dweight, dbias = g.layer_norm_grad(dy, x, weight, mean, rstd)
 """
 from ._binding import (FLAG_CTA_PAIR, FLAG_FORCE_STAGED, FLAG_SINGLE_CTA, FLAG_TILE64, FLAG_TILE128, FLAG_TILE256,  # noqa: F401
@@ -24,7 +26,7 @@ from ._binding import (FLAG_CTA_PAIR, FLAG_FORCE_STAGED, FLAG_SINGLE_CTA, FLAG_T
                        gemm_f32_clock_record, gemm_f32_status, gemm_f32_unit_rates,
                        gemm_f32_version)
 
-_LM = ("layer_norm", "layer_norm_grad")
+_LM = ("layer_norm", "layer_norm_grad", "vocab_loss", "vocab_loss_grad")
 
 
 def __getattr__(name):

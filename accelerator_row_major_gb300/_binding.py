@@ -108,6 +108,11 @@ def _load() -> ctypes.CDLL:
     lib.gemm_f32_layer_norm.restype = ci
     lib.gemm_f32_layer_norm_grad.argtypes = [ci, ci, cl, ci, vp, cl, vp, cl, vp, vp, vp, vp, cl, vp, vp, vp]
     lib.gemm_f32_layer_norm_grad.restype = ci
+    lib.gemm_f32_vocab_loss.argtypes = [ci, cl, ci, ci, vp, cl, vp, cl, vp, ci, cl, ci, vp, vp, vp, vp]
+    lib.gemm_f32_vocab_loss.restype = ci
+    lib.gemm_f32_vocab_loss_grad.argtypes = [ci, cl, ci, ci, vp, cl, vp, cl, vp, ci, cl, ci, cf, vp, vp, vp,
+                                             vp, cl, vp, cl, ctypes.c_size_t, vp]
+    lib.gemm_f32_vocab_loss_grad.restype = ci
     u64p = ctypes.POINTER(ctypes.c_ulonglong)
     lib.gemm_f32_clock_record.argtypes = [vp, u64p, u64p]
     lib.gemm_f32_clock_record.restype = ci

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from ._binding import TYPE_BF16, TYPE_F32, _stream, check, lib
+from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, _stream, check, lib
 
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
 
@@ -105,3 +105,50 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, stream=None):
                                          x.data_ptr(), ldx, pw, pm, pr, out.data_ptr(), ldo, dweight.data_ptr(),
                                          dbias.data_ptr(), _queue(stream, x.device)), "layer_norm_grad")
     return out, dweight, dbias
+
+
+def _loss_args(x, w, targets, reduction):
+    ldx, ldw = _matrix("x", x), _matrix("w", w)
+    if w.dtype != x.dtype or w.device != x.device or w.shape[1] != x.shape[1]:
+        raise ValueError("w must be a %s matrix on %s with x's %d columns" % (x.dtype, x.device, x.shape[1]))
+    if x.shape[1] < 1 or w.shape[0] < 1:
+        raise ValueError("x and w must have at least one column and w one row")
+    pt = _vector("targets", targets, x.shape[0], x.device, (torch.int64, torch.int32))
+    if reduction not in REDUCTIONS:
+        raise ValueError("reduction must be one of %s" % ", ".join(sorted(REDUCTIONS)))
+    loss = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    lse = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    total = torch.empty((), dtype=torch.float32, device=x.device)
+    return (_TYPES[x.dtype], x.shape[0], x.shape[1], w.shape[0], x.data_ptr(), ldx, w.data_ptr(), ldw, pt,
+            64 if targets.dtype == torch.int64 else 32), loss, lse, total
+
+
+def vocab_loss(x, w, targets, ignore_index=-100, reduction="mean", stream=None):
+    """(total, loss, lse): softmax cross entropy of the logits x @ w.T, which are never stored.
+
+    x: rows x width, w: vocab x width, of one type; targets: int64 or int32,
+    one per row.  loss and lse are float32 per row (loss 0 where the target
+    is ignore_index), total their sum, or mean over the rows that count.  A
+    target outside the vocabulary counts as ignored and is reported by
+    gemm_f32_status()."""
+    args, loss, lse, total = _loss_args(x, w, targets, reduction)
+    check(lib().gemm_f32_vocab_loss(*args, ignore_index, REDUCTIONS[reduction], loss.data_ptr(), lse.data_ptr(),
+                                    total.data_ptr(), _queue(stream, x.device)), "vocab_loss")
+    return total, loss, lse
+
+
+def vocab_loss_grad(x, w, targets, ignore_index=-100, reduction="mean", grad_scale=1.0, need_dx=True, need_dw=True,
+                    piece_bytes=0, stream=None):
+    """(total, loss, lse, dx, dw): vocab_loss and the gradients of grad_scale * total.
+
+    dx and dw hold x's type; need_dx / need_dw False leaves one out (None).
+    piece_bytes bounds the scratch that holds a piece of the rows (0: the
+    library's default)."""
+    args, loss, lse, total = _loss_args(x, w, targets, reduction)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if need_dw else None
+    check(lib().gemm_f32_vocab_loss_grad(*args, ignore_index, REDUCTIONS[reduction], grad_scale, loss.data_ptr(),
+                                         lse.data_ptr(), total.data_ptr(), dx.data_ptr() if need_dx else 0,
+                                         x.shape[1], dw.data_ptr() if need_dw else 0, x.shape[1], piece_bytes,
+                                         _queue(stream, x.device)), "vocab_loss_grad")
+    return total, loss, lse, dx, dw

@@ -1,0 +1,691 @@
+// bfloat16 tensor-core product on CTA pairs (tcgen05 cta_group::2) for
+// sm_103a: D = A B^T with fp32 accumulation, stored scaled, or reduced to
+// the softmax statistics of its rows without being stored.
+//
+// A tile of 256 x 256 is computed by a cluster of two CTAs on two SMs: CTA r
+// holds rows 128 r .. +127 of the A tile and of the B tile in shared memory
+// and the accumulator of its 128 rows of D by all 256 columns in tensor
+// memory; one M = 256 MMA issued by the even CTA works on both.  Every
+// operand byte a CTA loads feeds 256 multiply-adds, half the loads of a
+// 128 x 256 tile per CTA.  Operands come by TMA in 128-byte swizzled slices
+// 64 deep along K, K-major or MN-major as they are stored (the MMA reads
+// either, so nothing is ever transposed), six stages of 32 KB in flight.
+// The accumulator is double buffered (2 x 256 of the 512 columns of tensor
+// memory), so a tile's epilogue runs under the next tile's MMAs.
+//
+// Roles per CTA (384 threads): warp 0 TMA producer (its own halves; both
+// CTAs' bytes are counted on the even CTA's barrier), warp 1 tensor memory
+// and, in the even CTA, the MMAs; warps 4 .. 11 epilogue: four warps for
+// each half of the columns, one row of D per thread and half.
+//
+// fp32 operands (PARTS = 3): each is the sum of three bfloat16 parts, hi +
+// mid + lo, 24 significant bits.  Of the nine products the six that reach
+// fp32's precision are taken: lo hi, hi lo, mid mid, mid hi, hi mid, hi hi
+// (the dropped ones are below 2^-24 of the product).  The tensor core adds
+// into its accumulator by truncation (measured: a sum over K drifts towards
+// zero by about 1e-9 K of its size), so the accumulator takes only 256 of K
+// at a time, smallest products first, and the epilogue warps add these
+// partial sums in registers, rounding to nearest.
+//
+// Work: whole tiles round robin over the pairs; the tiles of the last,
+// partial wave are split along K over all pairs, whose partial tiles a
+// second kernel adds in order.  Logits are not split (their epilogue needs
+// the whole sum).  Every wait is bounded, as in the library's other kernels.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "../../include/gemm_f32.h"
+#include "device_common.cuh"
+#include "half_gemm.h"
+#include "launch.h"
+#include "pair_common.cuh"
+#include "row_common.cuh"
+
+namespace gemm_f32_impl {
+using namespace gemm_f32_dev;
+
+namespace {
+
+constexpr int kHalf = 128;               // rows of A and of B per CTA
+constexpr int kTile = 256;
+constexpr int kBK = 64;                  // 128 bytes of K per stage
+constexpr int kStages = 6;
+constexpr int kOperandBytes = kHalf * kBK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kSmem = 1024 + kStages * kStageBytes + 1024;
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarp0 = 4;
+constexpr int kEpilogueWarps = 8;
+constexpr int kTmemCols = 512;
+constexpr int kRasterGroup = 8;
+constexpr int kSumBlocks = 4;            // K blocks per accumulator sum of PARTS = 3
+constexpr int kMinSplitBlocks = 16;      // least K blocks per pair in the split tail
+constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int kEpiStore = 0;
+constexpr int kEpiLogits = 1;
+
+struct Params {
+  int M, N;
+  int tiles_m, tiles_n;
+  int k_blocks;                          // of 64
+  int k_iters;                           // units of the work list: blocks, or groups of kSumBlocks
+  int dp_tiles, sk_ctas, max_seg;
+  long long sk_work;
+  float* partials;                       // [tail][max_seg][256][256]
+  void* c;
+  long long ldc;
+  int c_f32, c_vec;                      // c_vec: rows of C take 16-byte stores
+  const float* scale;
+  const float* add;
+  long long ldadd;
+  float2* stats;
+  long long ld_stats;
+  void* exps;
+  long long ld_exps;
+  const int* labels;
+  float* label_logit;
+  unsigned* err;
+};
+
+// ---------------------------------------------------------------- primitives
+// 3-D tiled copy into this CTA's shared memory whose bytes are counted on a
+// barrier of either CTA of the pair (a shared::cluster address).  The inner
+// coordinate x is a multiple of 64 elements (128 bytes).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* desc, uint32_t bar, int x,
+                                              int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(desc), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16, bfloat16 operands, fp32 accumulator
+// (fields as idesc_tf32; format 1 = bfloat16).
+constexpr uint32_t idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((static_cast<uint32_t>(n) >> 3) << 17) | ((static_cast<uint32_t>(m) >> 4) << 24);
+}
+
+// Descriptor of the 16-deep K slice kk of a staged operand of 128 x 64.
+// K-major: 128 rows of 128 bytes, eight rows per swizzle atom (stride 1024);
+// slice kk starts 32 bytes further in the row.  MN-major: two chunks (8 KB
+// apart, the leading offset) of 64 K rows of 64 MN elements, eight K rows
+// per atom (stride 1024); slice kk starts 16 rows further.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int kk) {
+  return MN ? smem_desc(addr + kk * 2048, 8192, 1024, 2) : smem_desc(addr + kk * 32, 16, 1024, 2);
+}
+
+struct PairItems {
+  int unit, units, next_dp;
+  long long x, x_end;
+
+  __device__ __forceinline__ explicit PairItems(const Params& p) {
+    unit = static_cast<int>(blockIdx.x >> 1);
+    units = static_cast<int>(gridDim.x >> 1);
+    next_dp = unit;
+    x = x_end = 0;
+    if (unit < p.sk_ctas) {
+      x = sk_start(unit, p.sk_ctas, p.sk_work);
+      x_end = sk_start(unit + 1, p.sk_ctas, p.sk_work);
+    }
+  }
+
+  __device__ __forceinline__ bool next(const Params& p, WorkItem& w) {
+    if (next_dp < p.dp_tiles) {
+      w.tile = next_dp;
+      w.k0 = 0;
+      w.k1 = p.k_iters;
+      w.tail = -1;
+      w.seg = 0;
+      w.nseg = 1;
+      next_dp += units;
+      return true;
+    }
+    if (x >= x_end) return false;
+    const long long ki = p.k_iters;
+    const int i = static_cast<int>(x / ki);
+    w.tile = p.dp_tiles + i;
+    w.tail = i;
+    w.k0 = static_cast<int>(x - i * ki);
+    w.k1 = static_cast<int>(min(ki, w.k0 + (x_end - x)));
+    const int first = sk_owner(i * ki, p.sk_ctas, p.sk_work);
+    w.seg = unit - first;
+    w.nseg = sk_owner((i + 1) * ki - 1, p.sk_ctas, p.sk_work) - first + 1;
+    x += w.k1 - w.k0;
+    return true;
+  }
+};
+
+// NC consecutive columns of one row of C from their sums.
+template <int NC>
+__device__ __forceinline__ void store_c(const Params& p, int row, int col, float (&v)[NC]) {
+  const size_t at = static_cast<size_t>(row) * p.ldc + col;
+  [[maybe_unused]] const size_t extent = stored_extent(p.M, p.N, p.ldc);
+  const float s = p.scale ? __ldg(p.scale) : 1.0f;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) v[j] *= s;
+  if (p.add) {
+    const float* const add = p.add + static_cast<size_t>(row) * p.ldadd + col;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (col + j < p.N) v[j] += add[j];
+  }
+  if (p.c_vec && col + NC <= p.N) {
+    if (!GEMM_IN_EXTENT(at + NC - 1, extent, p.err, kSiteBoundsC)) return;
+    if (p.c_f32) {
+      if constexpr (NC % 4 == 0) store_vec<float, NC>(static_cast<float*>(p.c) + at, v);
+    } else if constexpr (NC % 8 == 0) {
+      store_vec<__nv_bfloat16, NC>(static_cast<__nv_bfloat16*>(p.c) + at, v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    if (col + j >= p.N || !GEMM_IN_EXTENT(at + j, extent, p.err, kSiteBoundsC)) continue;
+    if (p.c_f32)
+      static_cast<float*>(p.c)[at + j] = v[j];
+    else
+      static_cast<__nv_bfloat16*>(p.c)[at + j] = __float2bfloat16_rn(v[j]);
+  }
+}
+
+// ---------------------------------------------------------------- kernel
+template <bool A_MN, bool B_MN, int PARTS, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    half_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const Params p) {
+  constexpr int S = kStages;
+  extern __shared__ uint8_t smem_dyn[];
+  const uint32_t dyn0 = smem_addr(smem_dyn);
+  const uint32_t base = (dyn0 + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_dyn + (base - dyn0);
+  const uint32_t bars = base + S * kStageBytes;
+  auto full_bar = [&](int s) { return bars + 8u * s; };          // both CTAs' bytes (even CTA's)
+  auto empty_bar = [&](int s) { return bars + 8u * (S + s); };   // MMAs done with the stage
+  auto accf_bar = [&](int b) { return bars + 8u * (2 * S + b); };      // accumulator complete
+  auto acce_bar = [&](int b) { return bars + 8u * (2 * S + 2 + b); };  // drained (even CTA's)
+  const uint32_t drain_bar = bars + 8u * (2 * S + 4);
+  const uint32_t tmem_slot = bars + 8u * (2 * S + 5);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1);
+      mbar_init(acce_bar(b), 2 * kEpilogueWarps);
+    }
+    mbar_init(drain_bar, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();      // barriers of both CTAs exist before any remote arrive
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base));
+  grid_launch_dependents();
+  grid_dependency_wait();   // global memory from here on
+
+  // K blocks of unit u of the work list, and how often they are passed over
+  constexpr int kCombos = PARTS == 3 ? 6 : 1;
+  auto first_block = [&](int u) { return PARTS == 3 ? u * kSumBlocks : u; };
+  auto end_block = [&](int u) {
+    return PARTS == 3 ? min((u + 1) * kSumBlocks, p.k_blocks) : u + 1;
+  };
+
+  WorkItem w;
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (own halves)
+    if (lane == 0) {
+      const uint32_t leader_full0 = map_rank(full_bar(0), 0);
+      int s = 0;
+      uint32_t ph = 0, armed = 0, last_ph = 0;
+      bool ok = true;
+      PairItems list(p);
+      while (ok && list.next(p, w)) {
+        const TileCoord c = tile_coord(w.tile, p.tiles_m, p.tiles_n, kRasterGroup, true);
+        const int m0 = c.tm * kTile + static_cast<int>(rank) * kHalf;
+        const int n0 = c.tn * kTile + static_cast<int>(rank) * kHalf;
+        for (int u = w.k0; ok && u < w.k1; ++u) {
+          for (int combo = 0; ok && combo < kCombos; ++combo) {
+            // (lo, hi), (hi, lo), (mid, mid), (mid, hi), (hi, mid), (hi, hi)
+            const int pa = PARTS == 3 ? (0x001102 >> (4 * combo)) & 3 : 0;
+            const int pb = PARTS == 3 ? (0x010120 >> (4 * combo)) & 3 : 0;
+            for (int kb = first_block(u); kb < end_block(u); ++kb) {
+              if (!mbar_wait(empty_bar(s), ph ^ 1u, p.err, kSiteProducerEmpty)) {
+                ok = false;
+                break;
+              }
+              const uint32_t st = base + s * kStageBytes;
+              const uint32_t bar = leader_full0 + 8u * s;
+              if (rank == 0) {
+                mbar_arrive_expect_tx(full_bar(s), 2 * kStageBytes);
+                armed |= 1u << s;
+                last_ph = (last_ph & ~(1u << s)) | (ph << s);
+              }
+              const int k = kb * kBK;
+              if (A_MN) {
+                tma_load_pair(st, &tmA, bar, m0, k, pa);
+                tma_load_pair(st + 8192, &tmA, bar, m0 + 64, k, pa);
+              } else {
+                tma_load_pair(st, &tmA, bar, k, m0, pa);
+              }
+              if (B_MN) {
+                tma_load_pair(st + kOperandBytes, &tmB, bar, n0, k, pb);
+                tma_load_pair(st + kOperandBytes + 8192, &tmB, bar, n0 + 64, k, pb);
+              } else {
+                tma_load_pair(st + kOperandBytes, &tmB, bar, k, n0, pb);
+              }
+              if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+              }
+            }
+          }
+        }
+      }
+      // both CTAs' copies have landed before either CTA's memory goes away
+      for (int q = 0; q < S; ++q)
+        if (armed & (1u << q)) mbar_wait(full_bar(q), (last_ph >> q) & 1u, p.err, kSiteDrainTma);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(2 * kHalf, kTile, A_MN, B_MN);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true;
+      // One accumulator's sum: over the whole item, or over one unit of it.
+      auto open = [&]() {
+        if (!mbar_wait_cluster(acce_bar(buf), acc_ph ^ 1u, p.err, kSiteMmaAccEmpty)) return false;
+        tc_fence_after_sync();
+        return true;
+      };
+      auto close = [&]() {
+        mma_commit_both(accf_bar(buf));
+        buf ^= 1;
+        if (buf == 0) acc_ph ^= 1u;
+      };
+      PairItems list(p);
+      while (ok && list.next(p, w)) {
+        uint32_t more = 0;
+        if (PARTS == 1 && !open()) break;
+        for (int u = w.k0; ok && u < w.k1; ++u) {
+          if (PARTS == 3) {
+            more = 0;
+            if (!open()) {
+              ok = false;
+              break;
+            }
+          }
+          const int blocks = kCombos * (end_block(u) - first_block(u));
+          for (int i = 0; i < blocks; ++i) {
+            if (!mbar_wait_cluster(full_bar(s), ph, p.err, kSiteMmaReady)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t st = base + s * kStageBytes;
+            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * kTile);
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+              mma_bf16_pair(acc, operand_desc<A_MN>(st, kk),
+                            operand_desc<B_MN>(st + kOperandBytes, kk), idesc, more);
+              more = 1u;
+            }
+            mma_commit_both(empty_bar(s));
+            if (++s == S) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (PARTS == 3 && ok) close();
+        }
+        if (PARTS == 1 && ok) close();
+      }
+      mma_commit_local(drain_bar);
+      mbar_wait(drain_bar, 0, p.err, kSiteDrainMma);
+    }
+    __syncwarp();
+  } else if (warp >= kEpilogueWarp0) {
+    // ------------------------------------------------------------ epilogue (own rows)
+    const int q = warp & 3;                                    // 32 lanes of tensor memory
+    const int half = (warp - kEpilogueWarp0) >> 2;             // 128 of the 256 columns
+    const uint32_t t_mine =
+        tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kHalf);
+    const uint32_t leader_acce0 = map_rank(acce_bar(0), 0);
+    int buf = 0;
+    uint32_t acc_ph = 0;
+    bool ok = true;
+    auto wait_full = [&]() {
+      const bool got = mbar_wait(accf_bar(buf), acc_ph, p.err, kSiteEpilogueFull);
+      tc_fence_after_sync();
+      return __all_sync(0xFFFFFFFFu, got) != 0;
+    };
+    auto release = [&]() {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_acce0 + 8u * buf);
+      buf ^= 1;
+      if (buf == 0) acc_ph ^= 1u;
+    };
+    PairItems list(p);
+    while (ok && list.next(p, w)) {
+      const TileCoord c = tile_coord(w.tile, p.tiles_m, p.tiles_n, kRasterGroup, true);
+      const int local = static_cast<int>(rank) * kHalf + q * 32 + lane;
+      const int row = c.tm * kTile + local;
+      const int n0 = c.tn * kTile + half * kHalf;
+      [[maybe_unused]] float acc[PARTS == 3 ? kHalf : 1];
+      if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) acc[j] = 0.0f;
+        for (int u = w.k0; u < w.k1; ++u) {
+          if (!wait_full()) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t v[32];
+            tmem_ld_32cols(t_mine + static_cast<uint32_t>(buf * kTile + ch * 32), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[ch * 32 + j] += __uint_as_float(v[j]);
+          }
+          release();
+        }
+        if (!ok) break;
+      } else {
+        if (!wait_full()) break;
+      }
+      // 32 columns of this thread's row
+      auto take = [&](int ch, float(&v)[32]) {
+        if constexpr (PARTS == 3) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = acc[ch * 32 + j];
+        } else {
+          uint32_t u[32];
+          tmem_ld_32cols(t_mine + static_cast<uint32_t>(buf * kTile + ch * 32), u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+        }
+      };
+      if constexpr (EPI == kEpiStore) {
+        if (w.nseg > 1) {
+          float* const part = p.partials +
+                              (static_cast<size_t>(w.tail) * p.max_seg + w.seg) * (kTile * kTile) +
+                              static_cast<size_t>(local) * kTile + half * kHalf;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            float v[32];
+            take(ch, v);
+            store_vec<float, 32>(part + ch * 32, v);
+          }
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            float v[32];
+            take(ch, v);
+            if (row < p.M && n0 + ch * 32 < p.N) store_c<32>(p, row, n0 + ch * 32, v);
+          }
+        }
+      } else {
+        const bool row_ok = row < p.M;
+        float top = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          float v[32];
+          take(ch, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (n0 + ch * 32 + j < p.N) top = fmaxf(top, v[j]);
+        }
+        // nothing above -inf: any finite reference gives powers of 0
+        const float m2 = top == -INFINITY ? 0.0f : top * kLog2e;
+        const int label = row_ok ? __ldg(p.labels + row) - n0 : -1;
+        // one part: powers times 2^15, which keep their 11 bits in fp16 down to 2^-29
+        constexpr float kUp = PARTS == 3 ? 0.0f : 15.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          float v[32];
+          take(ch, v);
+          if (__any_sync(0xFFFFFFFFu, label >= ch * 32 && label < ch * 32 + 32)) {
+            float z = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z = label == ch * 32 + j ? v[j] : z;
+            if (label >= ch * 32 && label < ch * 32 + 32) p.label_logit[row] = z;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            v[j] = n0 + ch * 32 + j < p.N ? exp2f(fmaf(v[j], kLog2e, kUp - m2)) : 0.0f;
+            sum += v[j];
+          }
+          if (p.exps && row_ok) {
+            const size_t at = static_cast<size_t>(row) * p.ld_exps + n0 + ch * 32;
+            if (!GEMM_IN_EXTENT(at + 31, static_cast<size_t>(p.M) * p.ld_exps, p.err,
+                                kSiteBoundsScratch))
+              continue;
+            if constexpr (PARTS == 3) {
+              store_vec<float, 32>(static_cast<float*>(p.exps) + at, v);
+            } else {
+              uint4* const dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.exps) + at);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __half2 x = __floats2half2_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+                  h[j] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+                dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+          }
+        }
+        if (row_ok)
+          p.stats[static_cast<size_t>(2 * c.tn + half) * p.ld_stats + row] =
+              make_float2(m2, PARTS == 3 ? sum : sum * (1.0f / 32768.0f));
+      }
+      if constexpr (PARTS == 1) release();
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();   // the even CTA's MMAs and both CTAs' copies have finished
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// C of the split tiles: each tile's partials added in segment order.  One
+// CTA per 4 rows of a tile, 4 columns per thread.
+__global__ void __launch_bounds__(256) half_gemm_reduce_kernel(const Params p) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int tail = blockIdx.x / 64;
+  const int local = (blockIdx.x % 64) * 4 + threadIdx.x / 64;
+  const int col = (threadIdx.x % 64) * 4;
+  const long long ki = p.k_iters;
+  const int nseg = sk_owner((tail + 1) * ki - 1, p.sk_ctas, p.sk_work) -
+                   sk_owner(tail * ki, p.sk_ctas, p.sk_work) + 1;
+  if (nseg == 1) return;   // its one pair stored it
+  const TileCoord c = tile_coord(p.dp_tiles + tail, p.tiles_m, p.tiles_n, kRasterGroup, true);
+  const int row = c.tm * kTile + local, n = c.tn * kTile + col;
+  if (row >= p.M || n >= p.N) return;
+  const float* src = p.partials + static_cast<size_t>(tail) * p.max_seg * (kTile * kTile) +
+                     static_cast<size_t>(local) * kTile + col;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < nseg; ++s, src += kTile * kTile) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+    v[0] += x.x;
+    v[1] += x.y;
+    v[2] += x.z;
+    v[3] += x.w;
+  }
+  Params q = p;
+  if (!p.c_f32) q.c_vec = 0;   // four bfloat16 are less than a 16-byte store
+  store_c<4>(q, row, n, v);
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kMaxDevices = 64;
+
+int blocks_of(int n, int per) { return (n - 1) / per + 1; }
+
+// Tiles, K units and the split of the last wave; returns the bytes of
+// partial tiles.
+size_t plan(Params& p, int M, int N, int K, int parts, int num_sms, bool split) {
+  p.M = M;
+  p.N = N;
+  p.tiles_m = blocks_of(M, kTile);
+  p.tiles_n = blocks_of(N, kTile);
+  p.k_blocks = blocks_of(K, kBK);
+  p.k_iters = parts == 3 ? blocks_of(p.k_blocks, kSumBlocks) : p.k_blocks;
+  const long tiles = static_cast<long>(p.tiles_m) * p.tiles_n;
+  p.dp_tiles = static_cast<int>(tiles);
+  p.sk_ctas = 0;
+  p.sk_work = 0;
+  p.max_seg = 1;
+  if (!split) return 0;
+  const size_t bytes =
+      plan_split_tail(p, tiles, num_sms / 2, sizeof(float) * kTile * kTile,
+                      parts == 3 ? kMinSplitBlocks / (6 * kSumBlocks) + 1 : kMinSplitBlocks);
+  return bytes;
+}
+
+// [parts][rows][cols] bfloat16, box of 64 columns by box_rows rows of one part.
+bool encode(CUtensorMap* map, const HalfOperand& o, int rows, int cols, int parts, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tma_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(parts)};
+  const cuuint64_t row_bytes = static_cast<cuuint64_t>(o.ld) * 2u;
+  const cuuint64_t strides[2] = {
+      row_bytes, parts > 1 ? static_cast<cuuint64_t>(o.plane) * 2u : row_bytes * dims[1]};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t step[3] = {1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.ptr), dims, strides, box,
+             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool A_MN, bool B_MN, int PARTS, int EPI>
+int launch_one(const HalfGemm& g, const Params& p, const CUtensorMap& ma, const CUtensorMap& mb,
+               int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};   // bit per device
+  auto kern = half_gemm_kernel<A_MN, B_MN, PARTS, EPI>;
+  const unsigned long long bit = 1ull << (g.device % kMaxDevices);
+  if (!(configured.load() & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return GEMM_F32_ELAUNCH;
+    }
+    configured.fetch_or(bit);
+  }
+  if (launch_dependent(kern, dim3(grid), dim3(kThreads), kSmem, stream, ma, mb, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GEMM_F32_ELAUNCH;
+  }
+  return GEMM_F32_OK;
+}
+
+template <int PARTS>
+int launch_form(const HalfGemm& g, const Params& p, const CUtensorMap& ma, const CUtensorMap& mb,
+                int grid, cudaStream_t stream) {
+  if (!g.c) return launch_one<false, false, PARTS, kEpiLogits>(g, p, ma, mb, grid, stream);
+  if (!g.a.mn_major) return launch_one<false, true, PARTS, kEpiStore>(g, p, ma, mb, grid, stream);
+  return launch_one<true, true, PARTS, kEpiStore>(g, p, ma, mb, grid, stream);
+}
+
+}  // namespace
+
+size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms) {
+  Params p = {};
+  return plan(p, M, N, K, parts, num_sms, true);
+}
+
+int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
+  const int pairs = g.num_sms / 2;
+  if (pairs < 1) return GEMM_F32_EDEVICE;
+  // the forms compiled: logits K-major x K-major, products (either) x MN-major
+  if (g.c ? !g.b.mn_major : g.a.mn_major || g.b.mn_major) return GEMM_F32_EINVAL;
+  Params p = {};
+  plan(p, g.M, g.N, g.K, g.parts, g.num_sms, g.c != nullptr);
+  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  if (tiles > 0x7fffffffLL) return GEMM_F32_EINVAL;
+  p.partials = g.partials;
+  p.c = g.c;
+  p.ldc = g.ldc;
+  p.c_f32 = g.c_f32;
+  p.c_vec = reinterpret_cast<uintptr_t>(g.c) % 16 == 0 && g.ldc * (g.c_f32 ? 4 : 2) % 16 == 0;
+  p.scale = g.scale;
+  p.add = g.add;
+  p.ldadd = g.ldadd;
+  p.stats = g.stats;
+  p.ld_stats = g.ld_stats;
+  p.exps = g.exps;
+  p.ld_exps = g.ld_exps;
+  p.labels = g.labels;
+  p.label_logit = g.label_logit;
+  p.err = g.err;
+  alignas(64) CUtensorMap ma, mb;
+  const bool maps =
+      (g.a.mn_major ? encode(&ma, g.a, g.K, g.M, g.parts, 64) : encode(&ma, g.a, g.M, g.K, g.parts, kHalf)) &&
+      (g.b.mn_major ? encode(&mb, g.b, g.K, g.N, g.parts, 64) : encode(&mb, g.b, g.N, g.K, g.parts, kHalf));
+  if (!maps) return GEMM_F32_ELAUNCH;
+  const int units = p.sk_ctas > 0 ? pairs : static_cast<int>(std::min<long long>(tiles, pairs));
+  const int rc = g.parts == 3 ? launch_form<3>(g, p, ma, mb, 2 * units, stream)
+                              : launch_form<1>(g, p, ma, mb, 2 * units, stream);
+  if (rc != GEMM_F32_OK) return rc;
+  ++*launches;
+  if (p.sk_ctas > 0) {
+    const unsigned tail = static_cast<unsigned>(tiles - p.dp_tiles);
+    if (launch_dependent(half_gemm_reduce_kernel, dim3(tail * 64), dim3(256), 0, stream, p) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return GEMM_F32_ELAUNCH;
+    }
+    ++*launches;
+  }
+  return GEMM_F32_OK;
+}
+
+}  // namespace gemm_f32_impl

@@ -1,0 +1,58 @@
+// Private interface of the bfloat16 tensor-core product on CTA pairs
+// (half_gemm.cu), used by the vocabulary loss.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace gemm_f32_impl {
+
+// One operand: `parts` stored row-major bfloat16 matrices of rows x cols
+// elements with row stride ld, `plane` elements apart, whose sum is the
+// operand.  K-major: rows run along M (or N), columns along K.  MN-major:
+// the stored matrix is K x M (or K x N).  The base is 16-byte aligned and ld
+// and plane are multiples of 8.
+struct HalfOperand {
+  const void* ptr;
+  long long ld;
+  long long plane;
+  bool mn_major;
+};
+
+// What becomes of a finished tile of D = A B^T (D is M x N).
+struct HalfGemm {
+  int M, N, K;
+  int parts;                    // 1, or 3 (fp32 operands split into three parts)
+  HalfOperand a, b;
+  // -- a stored product: C = *scale * D (+ add)
+  void* c = nullptr;
+  long long ldc = 0;
+  bool c_f32 = false;           // fp32, else bfloat16
+  const float* scale = nullptr; // device
+  const float* add = nullptr;   // fp32, row stride ldadd; may be c itself
+  long long ldadd = 0;
+  float* partials = nullptr;    // half_gemm_scratch() bytes
+  // -- or logits (c == nullptr): per row and 128 columns the maximum m of
+  // z log2(e) and the sum of 2^(z log2(e) - m); with `exps`, those powers
+  // too (fp16 times 2^15 for one part, fp32 for three), zero from column N on
+  float2* stats = nullptr;      // [2 ceil(N / 256)][ld_stats]
+  long long ld_stats = 0;
+  void* exps = nullptr;         // M rows of ld_exps >= 256 ceil(N / 256) elements
+  long long ld_exps = 0;
+  const int* labels = nullptr;  // per row a column, or -1
+  float* label_logit = nullptr; // per row the logit at its label
+  // --
+  int num_sms, device;
+  unsigned* err;
+};
+
+// Bytes of partial tiles that the stored product of this shape needs (0 when
+// its last wave is not split along K).
+size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms);
+
+// Returns 0 or a negative GEMM_F32_E* code; counts its kernels in *launches.
+int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
+
+}  // namespace gemm_f32_impl

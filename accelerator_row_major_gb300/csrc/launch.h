@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 #include <utility>
@@ -96,6 +97,9 @@ void* fixed_scratch_address();
 // False when the driver entry point or the encoding fails.
 bool tma_encode_2d(CUtensorMap* map, const float* ptr, int rows, int cols, int ld, int box_cols,
                    int box_rows, CUtensorMapSwizzle swz);
+
+// The driver's tensor-map encoder (nullptr if it cannot be had).
+PFN_cuTensorMapEncodeTiled_v12000 tma_encoder();
 
 // CUDA-core FFMA path.
 int launch_ffma(GemmArgs& g, cudaStream_t stream, int* launches);

@@ -1,0 +1,609 @@
+// Softmax cross entropy over a vocabulary, with its gradients (sm_103a).
+//
+//   z = x w^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,y(t)
+//   g = exp(z - lse) - onehot(y),  dx = s g w,  dw = s g^T x
+//
+// The logits are a product of 2 T V D operations whose result is only needed
+// through its rows' maxima and sums of exponentials, so its epilogue
+// (half_gemm.cu) reduces each 128 columns to a maximum m and a sum of
+// exponentials relative to m, in base 2, and the rows join these:
+//   M = max m_i,  S = sum s_i 2^(m_i - M),  lse = (M + log2 S) / log2 e.
+// What bounds it: few rows, the read of w; many rows, the tensor cores.
+//
+// With gradients the logits are computed once too (6 T V D operations in
+// all, not 8): for a piece of the rows at a time the epilogue keeps
+// e = 2^(z log2 e - m), the rescaling pass turns it in place into
+//   g = e 2^(m - M) / S - onehot
+// and two more products give dx = s g w and dw += s g^T x.  e is kept in
+// fp16 (times 2^15: 11 bits for whatever lies within 2^-29 of its tile's
+// maximum) and g in bfloat16, the operand type of the products: one rounding
+// of a probability (2^-8 of it at most), of the size of the rounding of the
+// results, and none of the -1 of the target unless its probability is large.  The row
+// scale s is applied in fp32 to the finished sums.  fp32 operands keep e in
+// fp32 and g as three bfloat16 parts.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/gemm_f32_lm.h"
+#include "device_common.cuh"
+#include "half_gemm.h"
+#include "launch.h"
+#include "row_common.cuh"
+
+namespace gemm_f32_impl {
+using namespace gemm_f32_dev;
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kPiece = 128;                         // columns per statistic
+constexpr size_t kDefaultPieceBytes = size_t{4} << 30;
+constexpr size_t kMostStatsBytes = size_t{256} << 20;
+
+// Factors of one call, on the device.
+struct Factors {
+  float grad;      // s: grad_scale, divided for the mean
+  float total;     // 1, or 1 / rows that count
+};
+
+// Labels (a row's target, or -1 where the row does not count) and factors.
+template <class I>
+__global__ void __launch_bounds__(1024) loss_labels_kernel(const I* targets, int rows, int vocab,
+                                                           long long ignore, int mean,
+                                                           float grad_scale, int* labels,
+                                                           Factors* factors, unsigned* err) {
+  __shared__ int counts[32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  int n = 0;
+  for (unsigned t = threadIdx.x; t < static_cast<unsigned>(rows); t += 1024) {
+    const long long y = targets[t];
+    const bool counted = y != ignore;
+    const bool inside = y >= 0 && y < vocab;
+    if (counted && !inside) record_error(err, kSiteTarget);
+    labels[t] = counted && inside ? static_cast<int>(y) : -1;
+    n += counted && inside;
+  }
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = n;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    n = 0;
+    for (int i = 0; i < 32; ++i) n += counts[i];
+    const float per = mean ? static_cast<float>(n > 1 ? n : 1) : 1.0f;
+    factors->grad = grad_scale / per;
+    factors->total = 1.0f / per;
+  }
+}
+
+// ---------------------------------------------------------------- joining
+// Running (maximum, sum) of base-2 exponentials; an empty one has sum 0 and
+// does not count (so a piece with nothing above -inf leaves the maximum
+// alone), and a NaN sum stays.
+struct TopSum {
+  float m, s;
+};
+
+__device__ __forceinline__ TopSum join(TopSum a, TopSum b) {
+  if (b.s == 0.0f) return a;
+  if (a.s == 0.0f) return b;
+  const float m = fmaxf(a.m, b.m);
+  return {m, a.s * exp2f(a.m - m) + b.s * exp2f(b.m - m)};
+}
+
+__device__ __forceinline__ float lse_of(TopSum t) {
+  return t.s == 0.0f ? -INFINITY : kLn2 * (t.m + log2f(t.s));
+}
+
+// lse and loss of 32 rows per CTA: warp c joins pieces c, c + 32, ... of the
+// row of its lane, then the 32 chains are joined in order.
+__global__ void __launch_bounds__(1024) loss_join_kernel(const float2* stats, long long ld,
+                                                         int pieces, int rows, const int* labels,
+                                                         const float* label_logit, float* loss,
+                                                         float* lse) {
+  __shared__ float2 chains[32][33];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, chain = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  TopSum t = {0.0f, 0.0f};
+  if (row < rows)
+    for (int i = chain; i < pieces; i += 32) {
+      const float2 p = __ldg(stats + i * ld + row);
+      t = join(t, {p.x, p.y});
+    }
+  chains[chain][lane] = make_float2(t.m, t.s);
+  __syncthreads();
+  if (chain == 0 && row < rows) {
+    for (int c = 1; c < 32; ++c) t = join(t, {chains[c][lane].x, chains[c][lane].y});
+    const float l = lse_of(t);
+    if (lse) lse[row] = l;
+    loss[row] = labels[row] < 0 ? 0.0f : l - label_logit[row];
+  }
+}
+
+// The rescaling pass of the gradient: 4 rows per CTA row (their statistics
+// share a 32-byte sector), a band of the columns per CTA column.  Every CTA
+// joins its rows' statistics itself.
+constexpr int kRescaleThreads = 256;
+constexpr int kRescaleRows = 4;
+
+template <int PARTS>
+__global__ void __launch_bounds__(kRescaleThreads)
+    loss_rescale_kernel(const float2* stats, long long ld_stats, int pieces, int rows, int band,
+                        const int* labels, const float* label_logit, float* loss, float* lse,
+                        void* exps, long long ld, bf16* parts, long long plane, unsigned* err) {
+  constexpr int kChains = kRescaleThreads / kRescaleRows;
+  __shared__ float2 chains[kRescaleRows][kChains];
+  __shared__ float2 joined[kRescaleRows];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int row0 = blockIdx.x * kRescaleRows;
+  {
+    const int r = threadIdx.x % kRescaleRows, chain = threadIdx.x / kRescaleRows;
+    TopSum t = {0.0f, 0.0f};
+    if (row0 + r < rows)
+      for (int i = chain; i < pieces; i += kChains) {
+        const float2 p = __ldg(stats + i * ld_stats + row0 + r);
+        t = join(t, {p.x, p.y});
+      }
+    chains[r][chain] = make_float2(t.m, t.s);
+  }
+  __syncthreads();
+  if (threadIdx.x < kRescaleRows) {
+    const int r = threadIdx.x, row = row0 + r;
+    TopSum t = {chains[r][0].x, chains[r][0].y};
+    for (int c = 1; c < kChains; ++c) t = join(t, {chains[r][c].x, chains[r][c].y});
+    joined[r] = make_float2(t.m, 1.0f / t.s);
+    if (blockIdx.y == 0 && row < rows) {
+      const float l = lse_of(t);
+      if (lse) lse[row] = l;
+      loss[row] = labels[row] < 0 ? 0.0f : l - label_logit[row];
+    }
+  }
+  __syncthreads();
+  [[maybe_unused]] const size_t extent = static_cast<size_t>(rows) * ld;
+  const int c_end = min(static_cast<int>(ld), (static_cast<int>(blockIdx.y) + 1) * band);
+  for (int r = 0; r < kRescaleRows && row0 + r < rows; ++r) {
+    const int row = row0 + r;
+    const int label = labels[row];
+    const float m = joined[r].x, inv = joined[r].y * (PARTS == 3 ? 1.0f : 1.0f / 32768.0f);
+    for (int c = blockIdx.y * band + threadIdx.x * 8; c < c_end; c += kRescaleThreads * 8) {
+      const size_t at = static_cast<size_t>(row) * ld + c;
+      if (!GEMM_IN_EXTENT(at + 7, extent, err, kSiteBoundsScratch)) continue;
+      const float f = exp2f(__ldg(&stats[(c / kPiece) * ld_stats + row].x) - m) * inv;
+      float g[8];
+      if constexpr (PARTS == 3) {
+        const float4* const e = reinterpret_cast<const float4*>(static_cast<float*>(exps) + at);
+        const float4 a = __ldcs(e), b = __ldcs(e + 1);
+        g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+        g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+      } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<__half*>(exps) + at);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          g[2 * j] = h.x;
+          g[2 * j + 1] = h.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[j] *= f;
+        if (c + j == label) g[j] -= 1.0f;
+        if (label < 0) g[j] = 0.0f;
+      }
+      if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          store_vec<bf16, 8>(parts + part * plane + at, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] -= __bfloat162float(__float2bfloat16_rn(g[j]));
+        }
+      } else {
+        store_vec<bf16, 8>(static_cast<bf16*>(exps) + at, g);
+      }
+    }
+  }
+}
+
+// total = factor * sum of the rows' losses, in 64 bits and a fixed order.
+__global__ void __launch_bounds__(1024) loss_total_kernel(const float* loss, int rows,
+                                                          const Factors* factors, float* total) {
+  __shared__ double sums[32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  double s = 0.0;
+  for (unsigned t = threadIdx.x; t < static_cast<unsigned>(rows); t += 1024) s += loss[t];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 32; ++i) s += sums[i];
+    *total = static_cast<float>(s * factors->total);
+  }
+}
+
+// ---------------------------------------------------------------- operands
+// Copies a matrix into PARTS bfloat16 planes whose rows TMA can read.  An
+// fp32 value becomes hi + mid + lo: hi is the value truncated to bfloat16 (so
+// that it never overflows), mid and lo round what is left to nearest; the
+// rest is below 2^-25 of the value.
+template <class T, int PARTS>
+__global__ void __launch_bounds__(256) loss_split_kernel(const T* src, int rows, int cols,
+                                                         long long ld, bf16* dst, long long ld_dst,
+                                                         long long plane, int vectors,
+                                                         unsigned* err) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int per_row = (cols + 7) / 8;
+  const long long all = static_cast<long long>(rows) * per_row;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < all; i += gridDim.x * 256LL) {
+    const int r = static_cast<int>(i / per_row), c = static_cast<int>(i % per_row) * 8;
+    const size_t at = static_cast<size_t>(r) * ld + c;
+    float v[8];
+    if (vectors && c + 8 <= cols) {
+      if (!GEMM_IN_EXTENT(at + 7, stored_extent(rows, cols, ld), err, kSiteBoundsRows)) continue;
+      Raw<T, 8> raw;
+      raw.load_once(src + at);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = raw.at(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = c + j < cols &&
+                       GEMM_IN_EXTENT(at + j, stored_extent(rows, cols, ld), err, kSiteBoundsRows)
+                   ? to_f32(src[at + j])
+                   : 0.0f;
+    }
+    bf16* const out = dst + static_cast<size_t>(r) * ld_dst + c;
+    if constexpr (PARTS == 3) {
+      float hi[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        hi[j] = __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);
+        v[j] -= hi[j];
+      }
+      store_vec<bf16, 8>(out, hi);
+#pragma unroll
+      for (int part = 1; part < 3; ++part) {
+        store_vec<bf16, 8>(out + part * plane, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+      }
+    } else {
+      store_vec<bf16, 8>(out, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+template <class Kernel, class... Args>
+int launch(Kernel kernel, dim3 grid, int threads, cudaStream_t stream, int* launches,
+           Args... args) {
+  if (launch_dependent(kernel, grid, dim3(threads), 0, stream, args...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GEMM_F32_ELAUNCH;
+  }
+  ++*launches;
+  return GEMM_F32_OK;
+}
+
+struct Call {
+  int type;
+  int rows, width, vocab;
+  const void* x;
+  long long ldx;
+  const void* w;
+  long long ldw;
+  const void* targets;
+  int target_bits;
+  long long ignore;
+  int reduction;
+  float grad_scale;
+  float *loss, *lse, *total;
+  void* dx;
+  long long lddx;
+  void* dw;
+  long long lddw;
+  size_t piece_bytes;
+};
+
+size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+// Parts of the scratch buffer, handed out in order.
+struct Layout {
+  size_t bytes = 0;
+  size_t take(size_t n) {
+    const size_t at = bytes;
+    bytes += round_up(n, 256);
+    return at;
+  }
+};
+
+// An operand as TMA reads it: where it lies, or packed into scratch.
+struct Operand {
+  bool packed = false;
+  size_t at = 0;           // in scratch
+  long long ld = 0, plane = 0;
+};
+
+Operand plan_operand(const void* p, long long ld, int rows, int cols, int type, Layout& layout) {
+  Operand o;
+  o.packed = type == GEMM_F32_TYPE_F32 || reinterpret_cast<uintptr_t>(p) % 16 != 0 || ld % 8 != 0;
+  o.ld = ld;
+  if (o.packed) {
+    o.ld = static_cast<long long>(round_up(cols, 8));
+    o.plane = o.ld * rows;
+    o.at = layout.take(static_cast<size_t>(o.plane) * (type == GEMM_F32_TYPE_F32 ? 3 : 1) * 2);
+  }
+  return o;
+}
+
+int pack(const Operand& o, const void* src, long long ld, int rows, int cols, int type, char* scratch,
+         int num_sms, unsigned* err, cudaStream_t stream, int* launches) {
+  if (!o.packed) return GEMM_F32_OK;
+  const long long work = static_cast<long long>(rows) * ((cols + 7) / 8);
+  const unsigned grid = static_cast<unsigned>(std::min<long long>((work + 255) / 256, 16LL * num_sms));
+  bf16* const dst = reinterpret_cast<bf16*>(scratch + o.at);
+  const size_t size = type == GEMM_F32_TYPE_F32 ? 4 : 2;
+  const int vectors = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld * size % 16 == 0;
+  return type == GEMM_F32_TYPE_F32
+             ? launch(loss_split_kernel<float, 3>, dim3(grid), 256, stream, launches,
+                      static_cast<const float*>(src), rows, cols, ld, dst, o.ld, o.plane, vectors, err)
+             : launch(loss_split_kernel<bf16, 1>, dim3(grid), 256, stream, launches,
+                      static_cast<const bf16*>(src), rows, cols, ld, dst, o.ld, o.plane, vectors, err);
+}
+
+int run(const Call& c, cudaStream_t stream, int* launches) {
+  int device = 0, num_sms = 0;
+  unsigned* err = nullptr;
+  if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
+  const bool f32 = c.type == GEMM_F32_TYPE_F32, grad = c.dx || c.dw;
+  const int parts = f32 ? 3 : 1;
+  const long long ld_exps = static_cast<long long>(round_up(c.vocab, 256));
+  const int pieces = static_cast<int>(ld_exps / kPiece);
+
+  // rows per piece: bounded by the exponentials (and the parts of g), or by
+  // the statistics alone
+  const size_t row_bytes = grad ? static_cast<size_t>(ld_exps) * (f32 ? 4 + 6 : 2)
+                                : static_cast<size_t>(pieces) * sizeof(float2);
+  const size_t most = grad ? (c.piece_bytes ? c.piece_bytes : kDefaultPieceBytes) : kMostStatsBytes;
+  const size_t fit = std::max<size_t>(256, most / row_bytes / 256 * 256);
+  const size_t n_pieces = (static_cast<size_t>(c.rows) + fit - 1) / fit;
+  const int step = static_cast<int>(std::min<size_t>(
+      round_up((static_cast<size_t>(c.rows) + n_pieces - 1) / n_pieces, 256), c.rows));
+  const bool sum_dw = c.dw && !f32 && step < c.rows;   // bfloat16 dw of several pieces
+
+  Layout layout;
+  const size_t at_factors = layout.take(sizeof(Factors));
+  const size_t at_labels = layout.take(sizeof(int) * c.rows);
+  const size_t at_logit = layout.take(sizeof(float) * c.rows);
+  const size_t at_loss = c.loss ? 0 : layout.take(sizeof(float) * c.rows);
+  const long long ld_stats = static_cast<long long>(round_up(step, 32));
+  const size_t at_stats = layout.take(sizeof(float2) * pieces * ld_stats);
+  const Operand ox = plan_operand(c.x, c.ldx, c.rows, c.width, c.type, layout);
+  const Operand ow = plan_operand(c.w, c.ldw, c.vocab, c.width, c.type, layout);
+  size_t at_exps = 0, at_g = 0, at_partials = 0, at_sum = 0;
+  if (grad) {
+    at_exps = layout.take(static_cast<size_t>(step) * ld_exps * (f32 ? 4 : 2));
+    at_g = f32 ? layout.take(static_cast<size_t>(step) * ld_exps * 6) : at_exps;
+    size_t partial = 0;
+    for (long long r = 0; r < c.rows; r += step) {
+      const int n = static_cast<int>(std::min<long long>(step, c.rows - r));
+      if (c.dx) partial = std::max(partial, half_gemm_scratch(n, c.width, c.vocab, parts, num_sms));
+      if (c.dw) partial = std::max(partial, half_gemm_scratch(c.vocab, c.width, n, parts, num_sms));
+    }
+    at_partials = layout.take(partial);
+    if (sum_dw) at_sum = layout.take(sizeof(float) * static_cast<size_t>(c.vocab) * c.width);
+  }
+  char* const scratch = static_cast<char*>(acquire_scratch(device, stream, layout.bytes));
+  if (!scratch) return GEMM_F32_ESCRATCH;
+
+  Factors* const factors = reinterpret_cast<Factors*>(scratch + at_factors);
+  int* const labels = reinterpret_cast<int*>(scratch + at_labels);
+  float* const logit = reinterpret_cast<float*>(scratch + at_logit);
+  float* const loss = c.loss ? c.loss : reinterpret_cast<float*>(scratch + at_loss);
+  float2* const stats = reinterpret_cast<float2*>(scratch + at_stats);
+  const int mean = c.reduction == GEMM_F32_MEAN;
+  int rc = c.target_bits == 64
+               ? launch(loss_labels_kernel<long long>, dim3(1), 1024, stream, launches,
+                        static_cast<const long long*>(c.targets), c.rows, c.vocab, c.ignore, mean,
+                        c.grad_scale, labels, factors, err)
+               : launch(loss_labels_kernel<int>, dim3(1), 1024, stream, launches,
+                        static_cast<const int*>(c.targets), c.rows, c.vocab, c.ignore, mean,
+                        c.grad_scale, labels, factors, err);
+  if (rc == GEMM_F32_OK)
+    rc = pack(ox, c.x, c.ldx, c.rows, c.width, c.type, scratch, num_sms, err, stream, launches);
+  if (rc == GEMM_F32_OK)
+    rc = pack(ow, c.w, c.ldw, c.vocab, c.width, c.type, scratch, num_sms, err, stream, launches);
+
+  const HalfOperand w = {ow.packed ? scratch + ow.at : c.w, ow.ld, ow.plane, false};
+  for (long long r = 0; rc == GEMM_F32_OK && r < c.rows; r += step) {
+    const int n = static_cast<int>(std::min<long long>(step, c.rows - r));
+    HalfGemm base = {};
+    base.parts = parts;
+    base.num_sms = num_sms;
+    base.device = device;
+    base.err = err;
+    const char* const xp = static_cast<const char*>(ox.packed ? scratch + ox.at : c.x);
+    const HalfOperand x = {xp + static_cast<size_t>(r) * ox.ld * 2, ox.ld, ox.plane, false};
+
+    HalfGemm z = base;   // logits
+    z.M = n;
+    z.N = c.vocab;
+    z.K = c.width;
+    z.a = x;
+    z.b = w;
+    z.stats = stats;
+    z.ld_stats = ld_stats;
+    z.exps = grad ? scratch + at_exps : nullptr;
+    z.ld_exps = ld_exps;
+    z.labels = labels + r;
+    z.label_logit = logit + r;
+    rc = launch_half_gemm(z, stream, launches);
+    if (rc != GEMM_F32_OK) break;
+    float* const lse = c.lse ? c.lse + r : nullptr;
+    if (!grad) {
+      rc = launch(loss_join_kernel, dim3((n + 31) / 32), 1024, stream, launches,
+                  static_cast<const float2*>(stats), ld_stats, pieces, n,
+                  static_cast<const int*>(labels + r), static_cast<const float*>(logit + r), loss + r,
+                  lse);
+      continue;
+    }
+
+    // bands of columns: about two CTAs per SM where the rows alone give fewer
+    const int groups = (n + kRescaleRows - 1) / kRescaleRows;
+    const int most_bands = static_cast<int>(ld_exps / (kRescaleThreads * 8)) + 1;
+    const int bands = std::max(1, std::min(most_bands, 2 * num_sms / groups));
+    const int band = static_cast<int>(round_up((ld_exps + bands - 1) / bands, kRescaleThreads * 8));
+    const dim3 grid(groups, static_cast<unsigned>((ld_exps + band - 1) / band));
+    bf16* const gp = reinterpret_cast<bf16*>(scratch + at_g);
+    const long long plane = f32 ? static_cast<long long>(step) * ld_exps : 0;
+    rc = f32 ? launch(loss_rescale_kernel<3>, grid, kRescaleThreads, stream, launches,
+                      static_cast<const float2*>(stats), ld_stats, pieces, n, band,
+                      static_cast<const int*>(labels + r), static_cast<const float*>(logit + r),
+                      loss + r, lse, static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err)
+             : launch(loss_rescale_kernel<1>, grid, kRescaleThreads, stream, launches,
+                      static_cast<const float2*>(stats), ld_stats, pieces, n, band,
+                      static_cast<const int*>(labels + r), static_cast<const float*>(logit + r),
+                      loss + r, lse, static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err);
+    if (rc != GEMM_F32_OK) break;
+
+    base.scale = &factors->grad;
+    base.partials = reinterpret_cast<float*>(scratch + at_partials);
+    if (c.dx) {   // dx = s g w: K runs along the vocabulary
+      HalfGemm d = base;
+      d.M = n;
+      d.N = c.width;
+      d.K = c.vocab;
+      d.a = {gp, ld_exps, plane, false};
+      d.b = {w.ptr, w.ld, w.plane, true};
+      d.c = static_cast<char*>(c.dx) + static_cast<size_t>(r) * c.lddx * (f32 ? 4 : 2);
+      d.ldc = c.lddx;
+      d.c_f32 = f32;
+      rc = launch_half_gemm(d, stream, launches);
+      if (rc != GEMM_F32_OK) break;
+    }
+    if (c.dw) {   // dw += s g^T x: K runs along the rows
+      HalfGemm d = base;
+      d.M = c.vocab;
+      d.N = c.width;
+      d.K = n;
+      d.a = {gp, ld_exps, plane, true};
+      d.b = {x.ptr, x.ld, x.plane, true};
+      const bool last = r + step >= c.rows;
+      float* const sum = reinterpret_cast<float*>(scratch + at_sum);
+      const bool to_sum = sum_dw && !last;
+      d.c = to_sum ? static_cast<void*>(sum) : c.dw;
+      d.ldc = to_sum ? c.width : c.lddw;
+      d.c_f32 = f32 || to_sum;
+      if (r > 0) {
+        d.add = sum_dw ? sum : static_cast<const float*>(c.dw);
+        d.ldadd = sum_dw ? c.width : c.lddw;
+      }
+      rc = launch_half_gemm(d, stream, launches);
+    }
+  }
+  if (rc == GEMM_F32_OK && c.total)
+    rc = launch(loss_total_kernel, dim3(1), 1024, stream, launches, static_cast<const float*>(loss),
+                c.rows, static_cast<const Factors*>(factors), c.total);
+  return rc;
+}
+
+bool aligned_to(const void* p, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
+size_t matrix_bytes(int rows, int width, long long ld, size_t size) {
+  return (static_cast<size_t>(rows - 1) * ld + width) * size;
+}
+
+int checked(Call& c, long long rows, gemm_f32_stream_t stream_handle) {
+  note_launches(0, "none");
+  if (c.type != GEMM_F32_TYPE_F32 && c.type != GEMM_F32_TYPE_BF16) return GEMM_F32_EINVAL;
+  if (c.reduction != GEMM_F32_SUM && c.reduction != GEMM_F32_MEAN) return GEMM_F32_EINVAL;
+  if (c.target_bits != 32 && c.target_bits != 64) return GEMM_F32_EINVAL;
+  if (rows < 0 || rows > INT_MAX || c.width < 1 || c.vocab < 1) return GEMM_F32_EINVAL;
+  if (c.vocab > INT_MAX - 256 || !std::isfinite(c.grad_scale)) return GEMM_F32_EINVAL;
+  if (!aligned_to(c.loss, 4) || !aligned_to(c.lse, 4) || !aligned_to(c.total, 4))
+    return GEMM_F32_EINVAL;
+  const size_t size = c.type == GEMM_F32_TYPE_F32 ? 4 : 2;
+  c.rows = static_cast<int>(rows);
+  if (!c.w || !aligned_to(c.w, size) || c.ldw < c.width) return GEMM_F32_EINVAL;
+  if (c.dw && (!aligned_to(c.dw, size) || c.lddw < c.width)) return GEMM_F32_EINVAL;
+  if (rows > 0) {
+    if (!c.x || !aligned_to(c.x, size) || c.ldx < c.width) return GEMM_F32_EINVAL;
+    if (!c.targets || !aligned_to(c.targets, c.target_bits / 8)) return GEMM_F32_EINVAL;
+    if (c.dx && (!aligned_to(c.dx, size) || c.lddx < c.width)) return GEMM_F32_EINVAL;
+  }
+  const size_t w_bytes = matrix_bytes(c.vocab, c.width, c.ldw, size);
+  const size_t x_bytes = rows ? matrix_bytes(c.rows, c.width, c.ldx, size) : 0;
+  const size_t dw_bytes = c.dw ? matrix_bytes(c.vocab, c.width, c.lddw, size) : 0;
+  const size_t dx_bytes = c.dx && rows ? matrix_bytes(c.rows, c.width, c.lddx, size) : 0;
+  if (ranges_overlap(c.dw, dw_bytes, c.w, w_bytes) || ranges_overlap(c.dw, dw_bytes, c.x, x_bytes) ||
+      ranges_overlap(c.dx, dx_bytes, c.w, w_bytes) || ranges_overlap(c.dx, dx_bytes, c.x, x_bytes) ||
+      ranges_overlap(c.dx, dx_bytes, c.dw, dw_bytes))
+    return GEMM_F32_EINVAL;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+  if (rows == 0) {   // an empty sum
+    int device = 0, num_sms = 0, launches = 0;
+    unsigned* err = nullptr;
+    if (!c.total && !c.dw) return GEMM_F32_OK;
+    if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
+    if (c.total && cudaMemsetAsync(c.total, 0, sizeof(float), stream) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return GEMM_F32_ELAUNCH;
+    }
+    launches += c.total ? 1 : 0;
+    if (c.dw) {
+      if (cudaMemset2DAsync(c.dw, c.lddw * size, 0, c.width * size, c.vocab, stream) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GEMM_F32_ELAUNCH;
+      }
+      ++launches;
+    }
+    note_launches(launches, "memset");
+    return GEMM_F32_OK;
+  }
+  int launches = 0;
+  const int rc = run(c, stream, &launches);
+  if (rc == GEMM_F32_OK) note_launches(launches, "half_gemm_kernel");
+  return rc;
+}
+
+}  // namespace
+}  // namespace gemm_f32_impl
+
+using namespace gemm_f32_impl;
+
+extern "C" int gemm_f32_vocab_loss(int type, long long rows, int width, int vocab, const void* x,
+                                   long long ldx, const void* w, long long ldw, const void* targets,
+                                   int target_bits, long long ignore_index, int reduction, float* loss,
+                                   float* lse, float* total, gemm_f32_stream_t stream) {
+  Call c = {type, 0,    width, vocab, x,       ldx, w, ldw,     targets, target_bits, ignore_index, reduction,
+            1.0f, loss, lse,   total, nullptr, 0,   nullptr, 0, 0};
+  return checked(c, rows, stream);
+}
+
+extern "C" int gemm_f32_vocab_loss_grad(int type, long long rows, int width, int vocab, const void* x,
+                                        long long ldx, const void* w, long long ldw,
+                                        const void* targets, int target_bits, long long ignore_index,
+                                        int reduction, float grad_scale, float* loss, float* lse,
+                                        float* total, void* dx, long long lddx, void* dw,
+                                        long long lddw, size_t piece_bytes,
+                                        gemm_f32_stream_t stream) {
+  Call c = {type,       0,    width, vocab, x,  ldx,  w,  ldw,  targets, target_bits, ignore_index, reduction,
+            grad_scale, loss, lse,   total, dx, lddx, dw, lddw, piece_bytes};
+  return checked(c, rows, stream);
+}

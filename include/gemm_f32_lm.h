@@ -73,6 +73,51 @@ int gemm_f32_layer_norm_grad(int type, int weight_type, long long rows, int widt
                              const float* mean, const float* rstd, void* dx, long long lddx,
                              void* dweight, void* dbias, gemm_f32_stream_t stream);
 
+enum gemm_f32_reduction {
+    GEMM_F32_SUM = 0,
+    GEMM_F32_MEAN = 1    /* divided by the number of rows that count (at least 1) */
+};
+
+/* Softmax cross entropy over a vocabulary:
+ *     z = x w^T                 x: rows x width, w: vocab x width
+ *     lse_t  = log sum_v exp(z_tv)
+ *     loss_t = lse_t - z_t,targets[t],   0 where targets[t] == ignore_index
+ *     total  = sum_t loss_t, divided for GEMM_F32_MEAN
+ * The logits z are never stored: each tile of them leaves its row maxima and
+ * sums of exponentials, which are joined per row.  x and w hold `type`; with
+ * fp32 the products are computed from three-part bfloat16 splits of the
+ * operands on the tensor cores, to about fp32's own rounding (an infinite
+ * operand gives NaN).  targets are 32- or 64-bit integers (target_bits).  A
+ * target outside [0, vocab) that is not ignore_index counts as ignored and
+ * is reported by gemm_f32_status() as GEMM_F32_ETARGET.
+ * loss (rows), lse (rows) and total (1) are fp32; each may be NULL.
+ * rows == 0 sets total to 0.
+ * Returns 0, GEMM_F32_EINVAL (unknown type, reduction or target_bits, a
+ * negative size, width or vocab < 1, a stride below width, a null or
+ * misaligned pointer), GEMM_F32_ESCRATCH, GEMM_F32_EDEVICE or
+ * GEMM_F32_ELAUNCH. */
+int gemm_f32_vocab_loss(int type, long long rows, int width, int vocab, const void* x,
+                        long long ldx, const void* w, long long ldw, const void* targets,
+                        int target_bits, long long ignore_index, int reduction, float* loss,
+                        float* lse, float* total, gemm_f32_stream_t stream);
+
+/* The same with the gradients of grad_scale * total:
+ *     g_tv = s * (exp(z_tv - lse_t) - [v == targets[t]]),  0 in ignored rows
+ *     dx = g w,   dw = g^T x        (s = grad_scale, divided for GEMM_F32_MEAN)
+ * dx (rows x width) and dw (vocab x width) hold `type`; either may be NULL.
+ * Neither may overlap an input.  The logits are computed once, for a piece of
+ * the rows at a time: of a piece the library keeps exp(z - maximum of its
+ * tile) in scratch, in 16 bits for bfloat16 operands, and turns it into
+ * g / s in place.  `piece_bytes` bounds that part of the scratch (0: 4 GiB);
+ * pieces are at least 256 rows.  With more than one piece and bfloat16
+ * operands, dw is summed in fp32 scratch. */
+int gemm_f32_vocab_loss_grad(int type, long long rows, int width, int vocab, const void* x,
+                             long long ldx, const void* w, long long ldw, const void* targets,
+                             int target_bits, long long ignore_index, int reduction,
+                             float grad_scale, float* loss, float* lse, float* total, void* dx,
+                             long long lddx, void* dw, long long lddw, size_t piece_bytes,
+                             gemm_f32_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
