@@ -59,33 +59,44 @@ constexpr int kBK = 64;                  // 128 bytes of K per stage
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kHalf * kBK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kSmem = 1024 + kStages * kStageBytes + 1024;
+constexpr int kStagingBytes = 4096;      // per epilogue warp: 32 rows of 128 bytes
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
 constexpr int kEpilogueWarps = 8;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
+static_assert(kSmem <= 232448, "shared memory of one CTA");
 constexpr int kTmemCols = 512;
 constexpr int kRasterGroup = 8;
-constexpr int kSumBlocks = 4;            // K blocks per accumulator sum of PARTS = 3
 constexpr int kMinSplitBlocks = 16;      // least K blocks per pair in the split tail
+// K blocks that one accumulator sums before its sum goes on in registers:
+// 256 of K for fp32 operands, and 1024 for the logits of bfloat16 ones with
+// more than kWholeLogits of K (0: the whole of K).
+constexpr int kSumF32 = 4;
+constexpr int kSumLogits = 16;
+constexpr int kWholeLogits = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kEpiStore = 0;
-constexpr int kEpiLogits = 1;
+// Epilogues
+constexpr int kLogits = 0;
+constexpr int kStoreBf16 = 1;
+constexpr int kStoreF32 = 2;
 
 struct Params {
   int M, N;
   int tiles_m, tiles_n;
   int k_blocks;                          // of 64
-  int k_iters;                           // units of the work list: blocks, or groups of kSumBlocks
+  int k_iters;                           // units of the work list: blocks, or sums of SUM blocks
   int dp_tiles, sk_ctas, max_seg;
   long long sk_work;
   float* partials;                       // [tail][max_seg][256][256]
   void* c;
   long long ldc;
-  int c_f32, c_vec;                      // c_vec: rows of C take 16-byte stores
+  int c_f32;
+  int c_tma;                             // TMA can write C (tmC), else stores of single elements
   const float* scale;
   const float* add;
   long long ldadd;
+  int add_vec;                           // rows of `add` take 16-byte loads
   float2* stats;
   long long ld_stats;
   void* exps;
@@ -106,6 +117,24 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* desc, ui
       ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(desc), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// 2-D tiled copy of 32 rows of 128 bytes out of shared memory; columns and
+// rows outside the map are not written.
+__device__ __forceinline__ void tma_store(const void* desc, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(desc),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// This thread's stores have read their shared memory / have been made.
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -176,50 +205,105 @@ struct PairItems {
   }
 };
 
-// NC consecutive columns of one row of C from their sums.
+// The sums of NC consecutive columns of one row of C, scaled and added to.
 template <int NC>
-__device__ __forceinline__ void store_c(const Params& p, int row, int col, float (&v)[NC]) {
-  const size_t at = static_cast<size_t>(row) * p.ldc + col;
-  [[maybe_unused]] const size_t extent = stored_extent(p.M, p.N, p.ldc);
-  const float s = p.scale ? __ldg(p.scale) : 1.0f;
+__device__ __forceinline__ void finish_c(const Params& p, int row, int col, float s, float (&v)[NC]) {
 #pragma unroll
   for (int j = 0; j < NC; ++j) v[j] *= s;
-  if (p.add) {
-    const float* const add = p.add + static_cast<size_t>(row) * p.ldadd + col;
+  if (p.add == nullptr || row >= p.M) return;
+  const float* const add = p.add + static_cast<size_t>(row) * p.ldadd + col;
+  if (p.add_vec && col + NC <= p.N) {
+#pragma unroll
+    for (int j = 0; j < NC / 4; ++j) {
+      const float4 a = reinterpret_cast<const float4*>(add)[j];
+      v[4 * j] += a.x;
+      v[4 * j + 1] += a.y;
+      v[4 * j + 2] += a.z;
+      v[4 * j + 3] += a.w;
+    }
+  } else {
 #pragma unroll
     for (int j = 0; j < NC; ++j)
       if (col + j < p.N) v[j] += add[j];
   }
-  if (p.c_vec && col + NC <= p.N) {
-    if (!GEMM_IN_EXTENT(at + NC - 1, extent, p.err, kSiteBoundsC)) return;
-    if (p.c_f32) {
-      if constexpr (NC % 4 == 0) store_vec<float, NC>(static_cast<float*>(p.c) + at, v);
-    } else if constexpr (NC % 8 == 0) {
-      store_vec<__nv_bfloat16, NC>(static_cast<__nv_bfloat16*>(p.c) + at, v);
-    }
-    return;
-  }
+}
+
+// 16-byte chunk c of row r of a staging buffer (32 rows of 128 bytes in the
+// 128-byte swizzle that TMA undoes).
+__device__ __forceinline__ uint32_t staged(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// Two values as bfloat16 or fp16, or chunks of them.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_fp16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// This lane's row of 32 values into its staging buffer: a whole row of 32
+// fp32 values, or half (0, 1) of a row of 64 16-bit ones.
+__device__ __forceinline__ void stage_f32(uint8_t* buf, int lane, const float (&v)[32]) {
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    if (col + j >= p.N || !GEMM_IN_EXTENT(at + j, extent, p.err, kSiteBoundsC)) continue;
-    if (p.c_f32)
-      static_cast<float*>(p.c)[at + j] = v[j];
-    else
-      static_cast<__nv_bfloat16*>(p.c)[at + j] = __float2bfloat16_rn(v[j]);
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(buf + staged(lane, c)) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+template <bool FP16>
+__device__ __forceinline__ void stage_16(uint8_t* buf, int lane, int half, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      u[j] = FP16 ? pack_fp16(v[8 * c + 2 * j], v[8 * c + 2 * j + 1])
+                  : pack_bf16(v[8 * c + 2 * j], v[8 * c + 2 * j + 1]);
+    *reinterpret_cast<uint4*>(buf + staged(lane, 4 * half + c)) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
+// Writes a staged block to C rows row0 .., columns col0 ..: one TMA store,
+// or, where TMA cannot address C, one row after the other with the lanes
+// along the columns.
+template <class T>
+__device__ __forceinline__ void write_staged(const Params& p, const void* tmC, const uint8_t* buf,
+                                             int lane, int row0, int col0) {
+  constexpr int kCols = 128 / static_cast<int>(sizeof(T)), kPer = 16 / static_cast<int>(sizeof(T));
+  if (row0 >= p.M || col0 >= p.N) return;
+  if (p.c_tma) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store(tmC, smem_addr(buf), col0, row0);
+    return;
+  }
+  __syncwarp();
+  T* const c = static_cast<T*>(p.c);
+  const int rows = min(32, p.M - row0);
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r)
+#pragma unroll
+    for (int j = lane; j < kCols; j += 32) {
+      const size_t at = static_cast<size_t>(row0 + r) * p.ldc + col0 + j;
+      if (col0 + j < p.N && GEMM_IN_EXTENT(at, stored_extent(p.M, p.N, p.ldc), p.err, kSiteBoundsC))
+        c[at] = *reinterpret_cast<const T*>(buf + staged(r, j / kPer) + (j % kPer) * sizeof(T));
+    }
+}
+
 // ---------------------------------------------------------------- kernel
-template <bool A_MN, bool B_MN, int PARTS, int EPI>
+template <bool A_MN, bool B_MN, int PARTS, int SUM, int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     half_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const Params p) {
+                     const __grid_constant__ CUtensorMap tmC, const Params p) {
   constexpr int S = kStages;
   extern __shared__ uint8_t smem_dyn[];
   const uint32_t dyn0 = smem_addr(smem_dyn);
   const uint32_t base = (dyn0 + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_dyn + (base - dyn0);
-  const uint32_t bars = base + S * kStageBytes;
+  uint8_t* const staging = base_ptr + S * kStageBytes;
+  const uint32_t bars = base + S * kStageBytes + kEpilogueWarps * kStagingBytes;
   auto full_bar = [&](int s) { return bars + 8u * s; };          // both CTAs' bytes (even CTA's)
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };   // MMAs done with the stage
   auto accf_bar = [&](int b) { return bars + 8u * (2 * S + b); };      // accumulator complete
@@ -259,10 +343,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // K blocks of unit u of the work list, and how often they are passed over
   constexpr int kCombos = PARTS == 3 ? 6 : 1;
-  auto first_block = [&](int u) { return PARTS == 3 ? u * kSumBlocks : u; };
-  auto end_block = [&](int u) {
-    return PARTS == 3 ? min((u + 1) * kSumBlocks, p.k_blocks) : u + 1;
-  };
+  auto first_block = [&](int u) { return SUM ? u * SUM : u; };
+  auto end_block = [&](int u) { return SUM ? min((u + 1) * SUM, p.k_blocks) : u + 1; };
 
   WorkItem w;
   if (warp == 0) {
@@ -341,9 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       PairItems list(p);
       while (ok && list.next(p, w)) {
         uint32_t more = 0;
-        if (PARTS == 1 && !open()) break;
+        if (!SUM && !open()) break;
         for (int u = w.k0; ok && u < w.k1; ++u) {
-          if (PARTS == 3) {
+          if (SUM) {
             more = 0;
             if (!open()) {
               ok = false;
@@ -371,9 +453,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ph ^= 1u;
             }
           }
-          if (PARTS == 3 && ok) close();
+          if (SUM && ok) close();
         }
-        if (PARTS == 1 && ok) close();
+        if (!SUM && ok) close();
       }
       mma_commit_local(drain_bar);
       mbar_wait(drain_bar, 0, p.err, kSiteDrainMma);
@@ -401,14 +483,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       buf ^= 1;
       if (buf == 0) acc_ph ^= 1u;
     };
+    uint8_t* const stage = staging + (warp - kEpilogueWarp0) * kStagingBytes;
+    auto stage_free = [&]() {   // the buffer's last store has read it
+      if (lane == 0) tma_store_wait_read();
+      __syncwarp();
+    };
+    [[maybe_unused]] const float scale = p.scale ? __ldg(p.scale) : 1.0f;
     PairItems list(p);
     while (ok && list.next(p, w)) {
       const TileCoord c = tile_coord(w.tile, p.tiles_m, p.tiles_n, kRasterGroup, true);
       const int local = static_cast<int>(rank) * kHalf + q * 32 + lane;
       const int row = c.tm * kTile + local;
       const int n0 = c.tn * kTile + half * kHalf;
-      [[maybe_unused]] float acc[PARTS == 3 ? kHalf : 1];
-      if constexpr (PARTS == 3) {
+      [[maybe_unused]] float acc[SUM ? kHalf : 1];
+      if constexpr (SUM != 0) {
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) acc[j] = 0.0f;
         for (int u = w.k0; u < w.k1; ++u) {
@@ -432,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // 32 columns of this thread's row
       auto take = [&](int ch, float(&v)[32]) {
-        if constexpr (PARTS == 3) {
+        if constexpr (SUM != 0) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = acc[ch * 32 + j];
         } else {
@@ -443,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
         }
       };
-      if constexpr (EPI == kEpiStore) {
+      if constexpr (EPI != kLogits) {
         if (w.nseg > 1) {
           float* const part = p.partials +
                               (static_cast<size_t>(w.tail) * p.max_seg + w.seg) * (kTile * kTile) +
@@ -459,7 +547,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int ch = 0; ch < 4; ++ch) {
             float v[32];
             take(ch, v);
-            if (row < p.M && n0 + ch * 32 < p.N) store_c<32>(p, row, n0 + ch * 32, v);
+            finish_c<32>(p, row, n0 + ch * 32, scale, v);
+            if (EPI == kStoreF32 || ch % 2 == 0) stage_free();
+            if constexpr (EPI == kStoreF32) {
+              stage_f32(stage, lane, v);
+              write_staged<float>(p, &tmC, stage, lane, row - lane, n0 + ch * 32);
+            } else {
+              stage_16<false>(stage, lane, ch % 2, v);
+              if (ch % 2)
+                write_staged<__nv_bfloat16>(p, &tmC, stage, lane, row - lane, n0 + (ch - 1) * 32);
+            }
           }
         }
       } else {
@@ -494,25 +591,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             v[j] = n0 + ch * 32 + j < p.N ? exp2f(fmaf(v[j], kLog2e, kUp - m2)) : 0.0f;
             sum += v[j];
           }
-          if (p.exps && row_ok) {
-            const size_t at = static_cast<size_t>(row) * p.ld_exps + n0 + ch * 32;
-            if (!GEMM_IN_EXTENT(at + 31, static_cast<size_t>(p.M) * p.ld_exps, p.err,
-                                kSiteBoundsScratch))
-              continue;
+          if (p.exps) {   // C is the matrix of exponentials: fp32, or fp16
+            if (PARTS == 3 || ch % 2 == 0) stage_free();
             if constexpr (PARTS == 3) {
-              store_vec<float, 32>(static_cast<float*>(p.exps) + at, v);
+              stage_f32(stage, lane, v);
+              write_staged<float>(p, &tmC, stage, lane, row - lane, n0 + ch * 32);
             } else {
-              uint4* const dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.exps) + at);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const __half2 x = __floats2half2_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                  h[j] = *reinterpret_cast<const uint32_t*>(&x);
-                }
-                dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
-              }
+              stage_16<true>(stage, lane, ch % 2, v);
+              if (ch % 2) write_staged<__half>(p, &tmC, stage, lane, row - lane, n0 + (ch - 1) * 32);
             }
           }
         }
@@ -520,8 +606,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           p.stats[static_cast<size_t>(2 * c.tn + half) * p.ld_stats + row] =
               make_float2(m2, PARTS == 3 ? sum : sum * (1.0f / 32768.0f));
       }
-      if constexpr (PARTS == 1) release();
+      if constexpr (SUM == 0) release();
     }
+    if (lane == 0) tma_store_wait();
   }
 
   // ---------------------------------------------------------------- teardown
@@ -559,9 +646,26 @@ __global__ void __launch_bounds__(256) half_gemm_reduce_kernel(const Params p) {
     v[2] += x.z;
     v[3] += x.w;
   }
-  Params q = p;
-  if (!p.c_f32) q.c_vec = 0;   // four bfloat16 are less than a 16-byte store
-  store_c<4>(q, row, n, v);
+  finish_c<4>(p, row, n, p.scale ? __ldg(p.scale) : 1.0f, v);
+  const size_t at = static_cast<size_t>(row) * p.ldc + n;
+  if (p.c_tma && n + 4 <= p.N) {   // rows on 16-byte boundaries
+    if (!GEMM_IN_EXTENT(at + 3, stored_extent(p.M, p.N, p.ldc), p.err, kSiteBoundsC)) return;
+    if (p.c_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.c) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.c) + at) =
+          make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (n + j >= p.N || !GEMM_IN_EXTENT(at + j, stored_extent(p.M, p.N, p.ldc), p.err, kSiteBoundsC))
+      continue;
+    if (p.c_f32)
+      static_cast<float*>(p.c)[at + j] = v[j];
+    else
+      static_cast<__nv_bfloat16*>(p.c)[at + j] = __float2bfloat16_rn(v[j]);
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -571,23 +675,36 @@ int blocks_of(int n, int per) { return (n - 1) / per + 1; }
 
 // Tiles, K units and the split of the last wave; returns the bytes of
 // partial tiles.
-size_t plan(Params& p, int M, int N, int K, int parts, int num_sms, bool split) {
+size_t plan(Params& p, int M, int N, int K, int sum, int parts, int num_sms, bool split) {
   p.M = M;
   p.N = N;
   p.tiles_m = blocks_of(M, kTile);
   p.tiles_n = blocks_of(N, kTile);
   p.k_blocks = blocks_of(K, kBK);
-  p.k_iters = parts == 3 ? blocks_of(p.k_blocks, kSumBlocks) : p.k_blocks;
+  p.k_iters = sum ? blocks_of(p.k_blocks, sum) : p.k_blocks;
   const long tiles = static_cast<long>(p.tiles_m) * p.tiles_n;
   p.dp_tiles = static_cast<int>(tiles);
   p.sk_ctas = 0;
   p.sk_work = 0;
   p.max_seg = 1;
   if (!split) return 0;
-  const size_t bytes =
-      plan_split_tail(p, tiles, num_sms / 2, sizeof(float) * kTile * kTile,
-                      parts == 3 ? kMinSplitBlocks / (6 * kSumBlocks) + 1 : kMinSplitBlocks);
-  return bytes;
+  return plan_split_tail(p, tiles, num_sms / 2, sizeof(float) * kTile * kTile,
+                         parts == 3 ? 1 : kMinSplitBlocks);
+}
+
+// 2-D map of what the epilogue writes (rows on 16-byte boundaries): boxes of
+// 32 rows of 128 bytes.
+bool encode_c(CUtensorMap* map, const void* c, long long ldc, int rows, long long cols,
+              CUtensorMapDataType type, int size) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tma_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldc) * size};
+  const cuuint32_t box[2] = {128u / size, 32u};
+  const cuuint32_t step[2] = {1u, 1u};
+  return enc(map, type, 2, const_cast<void*>(c), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [parts][rows][cols] bfloat16, box of 64 columns by box_rows rows of one part.
@@ -606,11 +723,14 @@ bool encode(CUtensorMap* map, const HalfOperand& o, int rows, int cols, int part
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool A_MN, bool B_MN, int PARTS, int EPI>
-int launch_one(const HalfGemm& g, const Params& p, const CUtensorMap& ma, const CUtensorMap& mb,
-               int grid, cudaStream_t stream) {
+struct Maps {
+  CUtensorMap a, b, c;
+};
+
+template <bool A_MN, bool B_MN, int PARTS, int SUM, int EPI>
+int launch_one(const HalfGemm& g, const Params& p, const Maps& m, int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};   // bit per device
-  auto kern = half_gemm_kernel<A_MN, B_MN, PARTS, EPI>;
+  auto kern = half_gemm_kernel<A_MN, B_MN, PARTS, SUM, EPI>;
   const unsigned long long bit = 1ull << (g.device % kMaxDevices);
   if (!(configured.load() & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
@@ -620,45 +740,64 @@ int launch_one(const HalfGemm& g, const Params& p, const CUtensorMap& ma, const 
     }
     configured.fetch_or(bit);
   }
-  if (launch_dependent(kern, dim3(grid), dim3(kThreads), kSmem, stream, ma, mb, p) != cudaSuccess) {
+  if (launch_dependent(kern, dim3(grid), dim3(kThreads), kSmem, stream, m.a, m.b, m.c, p) !=
+      cudaSuccess) {
     (void)cudaGetLastError();
     return GEMM_F32_ELAUNCH;
   }
   return GEMM_F32_OK;
 }
 
-template <int PARTS>
-int launch_form(const HalfGemm& g, const Params& p, const CUtensorMap& ma, const CUtensorMap& mb,
-                int grid, cudaStream_t stream) {
-  if (!g.c) return launch_one<false, false, PARTS, kEpiLogits>(g, p, ma, mb, grid, stream);
-  if (!g.a.mn_major) return launch_one<false, true, PARTS, kEpiStore>(g, p, ma, mb, grid, stream);
-  return launch_one<true, true, PARTS, kEpiStore>(g, p, ma, mb, grid, stream);
+int sum_blocks(bool logits, int parts, int K) {
+  if (parts == 3) return kSumF32;
+  return logits && K > kWholeLogits ? kSumLogits : 0;
+}
+
+// The forms the vocabulary loss needs: logits of K-major operands, and
+// products with an MN-major right operand.
+int launch_form(const HalfGemm& g, const Params& p, const Maps& m, int grid, cudaStream_t stream) {
+  const int sum = sum_blocks(!g.c, g.parts, g.K);
+  if (!g.c) {
+    if (g.parts == 3) return launch_one<false, false, 3, kSumF32, kLogits>(g, p, m, grid, stream);
+    if (sum) return launch_one<false, false, 1, kSumLogits, kLogits>(g, p, m, grid, stream);
+    return launch_one<false, false, 1, 0, kLogits>(g, p, m, grid, stream);
+  }
+  if (g.parts == 3) {
+    if (!g.c_f32) return GEMM_F32_EINVAL;
+    return g.a.mn_major ? launch_one<true, true, 3, kSumF32, kStoreF32>(g, p, m, grid, stream)
+                        : launch_one<false, true, 3, kSumF32, kStoreF32>(g, p, m, grid, stream);
+  }
+  if (g.c_f32) {
+    if (!g.a.mn_major) return GEMM_F32_EINVAL;
+    return launch_one<true, true, 1, 0, kStoreF32>(g, p, m, grid, stream);
+  }
+  return g.a.mn_major ? launch_one<true, true, 1, 0, kStoreBf16>(g, p, m, grid, stream)
+                      : launch_one<false, true, 1, 0, kStoreBf16>(g, p, m, grid, stream);
 }
 
 }  // namespace
 
 size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms) {
   Params p = {};
-  return plan(p, M, N, K, parts, num_sms, true);
+  return plan(p, M, N, K, sum_blocks(false, parts, K), parts, num_sms, true);
 }
 
 int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
   const int pairs = g.num_sms / 2;
   if (pairs < 1) return GEMM_F32_EDEVICE;
-  // the forms compiled: logits K-major x K-major, products (either) x MN-major
   if (g.c ? !g.b.mn_major : g.a.mn_major || g.b.mn_major) return GEMM_F32_EINVAL;
   Params p = {};
-  plan(p, g.M, g.N, g.K, g.parts, g.num_sms, g.c != nullptr);
+  plan(p, g.M, g.N, g.K, sum_blocks(!g.c, g.parts, g.K), g.parts, g.num_sms, g.c != nullptr);
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x7fffffffLL) return GEMM_F32_EINVAL;
   p.partials = g.partials;
   p.c = g.c;
   p.ldc = g.ldc;
   p.c_f32 = g.c_f32;
-  p.c_vec = reinterpret_cast<uintptr_t>(g.c) % 16 == 0 && g.ldc * (g.c_f32 ? 4 : 2) % 16 == 0;
   p.scale = g.scale;
   p.add = g.add;
   p.ldadd = g.ldadd;
+  p.add_vec = reinterpret_cast<uintptr_t>(g.add) % 16 == 0 && g.ldadd % 4 == 0;
   p.stats = g.stats;
   p.ld_stats = g.ld_stats;
   p.exps = g.exps;
@@ -666,14 +805,26 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
   p.labels = g.labels;
   p.label_logit = g.label_logit;
   p.err = g.err;
-  alignas(64) CUtensorMap ma, mb;
-  const bool maps =
-      (g.a.mn_major ? encode(&ma, g.a, g.K, g.M, g.parts, 64) : encode(&ma, g.a, g.M, g.K, g.parts, kHalf)) &&
-      (g.b.mn_major ? encode(&mb, g.b, g.K, g.N, g.parts, 64) : encode(&mb, g.b, g.N, g.K, g.parts, kHalf));
-  if (!maps) return GEMM_F32_ELAUNCH;
+  Maps m = {};
+  if (!(g.a.mn_major ? encode(&m.a, g.a, g.K, g.M, g.parts, 64)
+                     : encode(&m.a, g.a, g.M, g.K, g.parts, kHalf)) ||
+      !(g.b.mn_major ? encode(&m.b, g.b, g.K, g.N, g.parts, 64)
+                     : encode(&m.b, g.b, g.N, g.K, g.parts, kHalf)))
+    return GEMM_F32_ELAUNCH;
+  if (g.c) {
+    const int size = g.c_f32 ? 4 : 2;
+    p.c_tma = reinterpret_cast<uintptr_t>(g.c) % 16 == 0 && g.ldc * size % 16 == 0 &&
+              encode_c(&m.c, g.c, g.ldc, g.M, g.N,
+                       g.c_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, size);
+  } else if (g.exps) {   // all ceil(N / 256) 256 columns
+    const bool f32 = g.parts == 3;
+    if (!encode_c(&m.c, g.exps, g.ld_exps, g.M, g.ld_exps,
+                  f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, f32 ? 4 : 2))
+      return GEMM_F32_ELAUNCH;
+    p.c_tma = 1;
+  }
   const int units = p.sk_ctas > 0 ? pairs : static_cast<int>(std::min<long long>(tiles, pairs));
-  const int rc = g.parts == 3 ? launch_form<3>(g, p, ma, mb, 2 * units, stream)
-                              : launch_form<1>(g, p, ma, mb, 2 * units, stream);
+  const int rc = launch_form(g, p, m, 2 * units, stream);
   if (rc != GEMM_F32_OK) return rc;
   ++*launches;
   if (p.sk_ctas > 0) {

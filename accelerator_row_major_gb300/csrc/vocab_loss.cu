@@ -136,10 +136,24 @@ __global__ void __launch_bounds__(1024) loss_join_kernel(const float2* stats, lo
 constexpr int kRescaleThreads = 256;
 constexpr int kRescaleRows = 4;
 
+// How e is held: fp32, or fp16 bits.
+template <int PARTS>
+struct Exps {
+  using type = float;
+  static __device__ __forceinline__ float value(const Raw<float, 8>& r, int j) { return r.at(j); }
+};
+template <>
+struct Exps<1> {
+  using type = uint16_t;
+  static __device__ __forceinline__ float value(const Raw<uint16_t, 8>& r, int j) {
+    return __half2float(__ushort_as_half(static_cast<uint16_t>(r.w[j >> 1] >> (16 * (j & 1)))));
+  }
+};
+
 template <int PARTS>
 __global__ void __launch_bounds__(kRescaleThreads)
-    loss_rescale_kernel(const float2* stats, long long ld_stats, int pieces, int rows, int band,
-                        const int* labels, const float* label_logit, float* loss, float* lse,
+    loss_rescale_kernel(const float2* stats, long long ld_stats, int pieces, int rows, int cols,
+                        int band,                        const int* labels, const float* label_logit, float* loss, float* lse,
                         void* exps, long long ld, bf16* parts, long long plane, unsigned* err) {
   constexpr int kChains = kRescaleThreads / kRescaleRows;
   __shared__ float2 chains[kRescaleRows][kChains];
@@ -171,36 +185,40 @@ __global__ void __launch_bounds__(kRescaleThreads)
   }
   __syncthreads();
   [[maybe_unused]] const size_t extent = static_cast<size_t>(rows) * ld;
-  const int c_end = min(static_cast<int>(ld), (static_cast<int>(blockIdx.y) + 1) * band);
-  for (int r = 0; r < kRescaleRows && row0 + r < rows; ++r) {
-    const int row = row0 + r;
-    const int label = labels[row];
-    const float m = joined[r].x, inv = joined[r].y * (PARTS == 3 ? 1.0f : 1.0f / 32768.0f);
-    for (int c = blockIdx.y * band + threadIdx.x * 8; c < c_end; c += kRescaleThreads * 8) {
-      const size_t at = static_cast<size_t>(row) * ld + c;
-      if (!GEMM_IN_EXTENT(at + 7, extent, err, kSiteBoundsScratch)) continue;
-      const float f = exp2f(__ldg(&stats[(c / kPiece) * ld_stats + row].x) - m) * inv;
-      float g[8];
-      if constexpr (PARTS == 3) {
-        const float4* const e = reinterpret_cast<const float4*>(static_cast<float*>(exps) + at);
-        const float4 a = __ldcs(e), b = __ldcs(e + 1);
-        g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-        g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
-      } else {
-        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<__half*>(exps) + at);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  int label[kRescaleRows];
+  float m[kRescaleRows], inv[kRescaleRows];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-          g[2 * j] = h.x;
-          g[2 * j + 1] = h.y;
-        }
-      }
+  for (int r = 0; r < kRescaleRows; ++r) {
+    label[r] = row0 + r < rows ? __ldg(labels + row0 + r) : -1;
+    m[r] = joined[r].x;
+    inv[r] = joined[r].y * (PARTS == 3 ? 1.0f : 1.0f / 32768.0f);
+  }
+  const int c_end = min(cols, (static_cast<int>(blockIdx.y) + 1) * band);
+  for (int c = blockIdx.y * band + threadIdx.x * 8; c < c_end; c += kRescaleThreads * 8) {
+    // the rows' loads first, so that one round trip covers them
+    Raw<typename Exps<PARTS>::type, 8> e[kRescaleRows];
+    float f[kRescaleRows];
+#pragma unroll
+    for (int r = 0; r < kRescaleRows; ++r) {
+      const size_t at = static_cast<size_t>(row0 + r) * ld + c;
+      e[r].zero();
+      f[r] = 0.0f;
+      if (row0 + r >= rows || !GEMM_IN_EXTENT(at + 7, extent, err, kSiteBoundsScratch)) continue;
+      e[r].load_once(static_cast<const typename Exps<PARTS>::type*>(exps) + at);
+      f[r] = __ldg(&stats[(c / kPiece) * ld_stats + row0 + r].x);
+    }
+#pragma unroll
+    for (int r = 0; r < kRescaleRows; ++r) {
+      if (row0 + r >= rows) break;
+      const size_t at = static_cast<size_t>(row0 + r) * ld + c;
+      if (!GEMM_IN_EXTENT(at + 7, extent, err, kSiteBoundsScratch)) continue;
+      const float by = exp2f(f[r] - m[r]) * inv[r];
+      float g[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        g[j] *= f;
-        if (c + j == label) g[j] -= 1.0f;
-        if (label < 0) g[j] = 0.0f;
+        g[j] = Exps<PARTS>::value(e[r], j) * by;
+        if (c + j == label[r]) g[j] -= 1.0f;
+        if (label[r] < 0) g[j] = 0.0f;
       }
       if constexpr (PARTS == 3) {
 #pragma unroll
@@ -462,20 +480,20 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
       continue;
     }
 
-    // bands of columns: about two CTAs per SM where the rows alone give fewer
+    // bands of columns: some eight CTAs per SM where the rows alone give fewer
     const int groups = (n + kRescaleRows - 1) / kRescaleRows;
-    const int most_bands = static_cast<int>(ld_exps / (kRescaleThreads * 8)) + 1;
-    const int bands = std::max(1, std::min(most_bands, 2 * num_sms / groups));
-    const int band = static_cast<int>(round_up((ld_exps + bands - 1) / bands, kRescaleThreads * 8));
-    const dim3 grid(groups, static_cast<unsigned>((ld_exps + band - 1) / band));
+    const int cols = static_cast<int>(round_up(c.vocab, 8));
+    const int bands = 8 * num_sms / groups + 1;
+    const int band = static_cast<int>(round_up((cols + bands - 1) / bands, kRescaleThreads * 8));
+    const dim3 grid(groups, static_cast<unsigned>((cols + band - 1) / band));
     bf16* const gp = reinterpret_cast<bf16*>(scratch + at_g);
     const long long plane = f32 ? static_cast<long long>(step) * ld_exps : 0;
     rc = f32 ? launch(loss_rescale_kernel<3>, grid, kRescaleThreads, stream, launches,
-                      static_cast<const float2*>(stats), ld_stats, pieces, n, band,
+                      static_cast<const float2*>(stats), ld_stats, pieces, n, cols, band,
                       static_cast<const int*>(labels + r), static_cast<const float*>(logit + r),
                       loss + r, lse, static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err)
              : launch(loss_rescale_kernel<1>, grid, kRescaleThreads, stream, launches,
-                      static_cast<const float2*>(stats), ld_stats, pieces, n, band,
+                      static_cast<const float2*>(stats), ld_stats, pieces, n, cols, band,
                       static_cast<const int*>(labels + r), static_cast<const float*>(logit + r),
                       loss + r, lse, static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err);
     if (rc != GEMM_F32_OK) break;
