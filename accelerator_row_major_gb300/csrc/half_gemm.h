@@ -55,4 +55,37 @@ size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms);
 // Returns 0 or a negative GEMM_F32_E* code; counts its kernels in *launches.
 int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
 
+// The same two products for few rows (at most kFewRows), where reading w is
+// what takes the time (few_gemm.cu).  w is read as it is stored, fp32
+// included (f32: its three parts are made on the way to the tensor cores);
+// its rows start on 16-byte boundaries.
+constexpr int kFewRows = 128;
+constexpr int kFewPiece = 32;     // columns per statistic of its logits
+
+struct FewGemm {
+  bool f32;
+  int rows, width, vocab;
+  const void* w;                  // vocab x width
+  long long ldw;
+  HalfOperand b;                  // K-major, rows x (width for logits, vocab for dx)
+  // -- logits: as HalfGemm, with statistics per kFewPiece columns
+  float2* stats = nullptr;        // [ceil(vocab / kFewPiece)][ld_stats]
+  long long ld_stats = 0;
+  void* exps = nullptr;
+  long long ld_exps = 0;
+  const int* labels = nullptr;
+  float* label_logit = nullptr;
+  // -- or dx = *scale * b w (dx != nullptr)
+  void* dx = nullptr;
+  long long lddx = 0;
+  const float* scale = nullptr;
+  float* partials = nullptr;      // few_gemm_scratch() bytes
+  // --
+  int num_sms, device;
+  unsigned* err;
+};
+
+size_t few_gemm_scratch(int rows, int width, int vocab, int num_sms);   // of dx
+int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches);
+
 }  // namespace gemm_f32_impl

@@ -44,7 +44,9 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kPiece = 128;                         // columns per statistic
+constexpr int kPieceBits = 7;                       // 128 columns per statistic,
+constexpr int kFewPieceBits = 5;                    // 32 with few rows
+static_assert(1 << kFewPieceBits == kFewPiece, "columns per statistic");
 constexpr size_t kDefaultPieceBytes = size_t{4} << 30;
 constexpr size_t kMostStatsBytes = size_t{256} << 20;
 
@@ -85,54 +87,59 @@ __global__ void __launch_bounds__(1024) loss_labels_kernel(const I* targets, int
 }
 
 // ---------------------------------------------------------------- joining
-// Running (maximum, sum) of base-2 exponentials; an empty one has sum 0 and
-// does not count (so a piece with nothing above -inf leaves the maximum
-// alone), and a NaN sum stays.
-struct TopSum {
-  float m, s;
-};
+// lse and loss of 4 rows per CTA (4 statistics of a piece share a 32-byte
+// sector): the largest maximum M of a row's pieces, then S = sum s 2^(m - M).
+// A piece with sum 0 has nothing above -inf (its m stands for nothing) and
+// does not count; a NaN sum does.  joined (may be null) receives (M, 1 / S).
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 4;
 
-__device__ __forceinline__ TopSum join(TopSum a, TopSum b) {
-  if (b.s == 0.0f) return a;
-  if (a.s == 0.0f) return b;
-  const float m = fmaxf(a.m, b.m);
-  return {m, a.s * exp2f(a.m - m) + b.s * exp2f(b.m - m)};
-}
-
-__device__ __forceinline__ float lse_of(TopSum t) {
-  return t.s == 0.0f ? -INFINITY : kLn2 * (t.m + log2f(t.s));
-}
-
-// lse and loss of 32 rows per CTA: warp c joins pieces c, c + 32, ... of the
-// row of its lane, then the 32 chains are joined in order.
-__global__ void __launch_bounds__(1024) loss_join_kernel(const float2* stats, long long ld,
-                                                         int pieces, int rows, const int* labels,
-                                                         const float* label_logit, float* loss,
-                                                         float* lse) {
-  __shared__ float2 chains[32][33];
+__global__ void __launch_bounds__(kJoinThreads)
+    loss_join_kernel(const float2* stats, long long ld, int pieces, int rows, const int* labels,
+                     const float* label_logit, float* loss, float* lse, float2* joined) {
+  constexpr int kChains = kJoinThreads / kJoinRows, kWarps = kJoinThreads / 32;
+  __shared__ float tops[kWarps][kJoinRows], sums[kWarps][kJoinRows];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, chain = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
-  TopSum t = {0.0f, 0.0f};
-  if (row < rows)
-    for (int i = chain; i < pieces; i += 32) {
-      const float2 p = __ldg(stats + i * ld + row);
-      t = join(t, {p.x, p.y});
-    }
-  chains[chain][lane] = make_float2(t.m, t.s);
-  __syncthreads();
-  if (chain == 0 && row < rows) {
-    for (int c = 1; c < 32; ++c) t = join(t, {chains[c][lane].x, chains[c][lane].y});
-    const float l = lse_of(t);
-    if (lse) lse[row] = l;
-    loss[row] = labels[row] < 0 ? 0.0f : l - label_logit[row];
+  const int r = threadIdx.x % kJoinRows, chain = threadIdx.x / kJoinRows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * kJoinRows + r;
+  const float2* const mine = stats + row;
+  const int end = row < rows ? pieces : 0;
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int i = chain; i < end; i += kChains) {
+    const float2 p = __ldg(mine + i * ld);
+    top = p.y != 0.0f ? fmaxf(top, p.x) : top;
   }
+#pragma unroll
+  for (int o = kJoinRows; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if (lane < kJoinRows) tops[warp][lane] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w][r]);
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int i = chain; i < end; i += kChains) {
+    const float2 p = __ldg(mine + i * ld);
+    sum += p.y != 0.0f ? p.y * exp2f(p.x - top) : 0.0f;
+  }
+#pragma unroll
+  for (int o = kJoinRows; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane < kJoinRows) sums[warp][lane] = sum;
+  __syncthreads();
+  if (chain != 0 || row >= rows) return;
+  sum = sums[0][r];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) sum += sums[w][r];
+  const float l = sum == 0.0f ? -INFINITY : kLn2 * (top + log2f(sum));
+  if (lse) lse[row] = l;
+  loss[row] = labels[row] < 0 ? 0.0f : l - label_logit[row];
+  if (joined) joined[row] = make_float2(top, 1.0f / sum);
 }
 
-// The rescaling pass of the gradient: 4 rows per CTA row (their statistics
-// share a 32-byte sector), a band of the columns per CTA column.  Every CTA
-// joins its rows' statistics itself.
+// The rescaling pass of the gradient, g = e 2^(m - M) / S - onehot: 4 rows by
+// a band of the columns per CTA.
 constexpr int kRescaleThreads = 256;
 constexpr int kRescaleRows = 4;
 
@@ -152,46 +159,22 @@ struct Exps<1> {
 
 template <int PARTS>
 __global__ void __launch_bounds__(kRescaleThreads)
-    loss_rescale_kernel(const float2* stats, long long ld_stats, int pieces, int rows, int cols,
-                        int band,                        const int* labels, const float* label_logit, float* loss, float* lse,
-                        void* exps, long long ld, bf16* parts, long long plane, unsigned* err) {
-  constexpr int kChains = kRescaleThreads / kRescaleRows;
-  __shared__ float2 chains[kRescaleRows][kChains];
-  __shared__ float2 joined[kRescaleRows];
+    loss_rescale_kernel(const float2* stats, long long ld_stats, int piece_bits, const float2* joined,
+                        int rows, int cols, int band, const int* labels, void* exps, long long ld,
+                        bf16* parts, long long plane, unsigned* err) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int row0 = blockIdx.x * kRescaleRows;
-  {
-    const int r = threadIdx.x % kRescaleRows, chain = threadIdx.x / kRescaleRows;
-    TopSum t = {0.0f, 0.0f};
-    if (row0 + r < rows)
-      for (int i = chain; i < pieces; i += kChains) {
-        const float2 p = __ldg(stats + i * ld_stats + row0 + r);
-        t = join(t, {p.x, p.y});
-      }
-    chains[r][chain] = make_float2(t.m, t.s);
-  }
-  __syncthreads();
-  if (threadIdx.x < kRescaleRows) {
-    const int r = threadIdx.x, row = row0 + r;
-    TopSum t = {chains[r][0].x, chains[r][0].y};
-    for (int c = 1; c < kChains; ++c) t = join(t, {chains[r][c].x, chains[r][c].y});
-    joined[r] = make_float2(t.m, 1.0f / t.s);
-    if (blockIdx.y == 0 && row < rows) {
-      const float l = lse_of(t);
-      if (lse) lse[row] = l;
-      loss[row] = labels[row] < 0 ? 0.0f : l - label_logit[row];
-    }
-  }
-  __syncthreads();
   [[maybe_unused]] const size_t extent = static_cast<size_t>(rows) * ld;
   int label[kRescaleRows];
   float m[kRescaleRows], inv[kRescaleRows];
 #pragma unroll
   for (int r = 0; r < kRescaleRows; ++r) {
-    label[r] = row0 + r < rows ? __ldg(labels + row0 + r) : -1;
-    m[r] = joined[r].x;
-    inv[r] = joined[r].y * (PARTS == 3 ? 1.0f : 1.0f / 32768.0f);
+    const int row = min(row0 + r, rows - 1);
+    const float2 j = __ldg(joined + row);
+    label[r] = __ldg(labels + row);
+    m[r] = j.x;
+    inv[r] = j.y * (PARTS == 3 ? 1.0f : 1.0f / 32768.0f);
   }
   const int c_end = min(cols, (static_cast<int>(blockIdx.y) + 1) * band);
   for (int c = blockIdx.y * band + threadIdx.x * 8; c < c_end; c += kRescaleThreads * 8) {
@@ -205,7 +188,7 @@ __global__ void __launch_bounds__(kRescaleThreads)
       f[r] = 0.0f;
       if (row0 + r >= rows || !GEMM_IN_EXTENT(at + 7, extent, err, kSiteBoundsScratch)) continue;
       e[r].load_once(static_cast<const typename Exps<PARTS>::type*>(exps) + at);
-      f[r] = __ldg(&stats[(c / kPiece) * ld_stats + row0 + r].x);
+      f[r] = __ldg(&stats[(c >> piece_bits) * ld_stats + row0 + r].x);
     }
 #pragma unroll
     for (int r = 0; r < kRescaleRows; ++r) {
@@ -253,13 +236,13 @@ __global__ void __launch_bounds__(1024) loss_total_kernel(const float* loss, int
 }
 
 // ---------------------------------------------------------------- operands
-// Copies a matrix into PARTS bfloat16 planes whose rows TMA can read.  An
-// fp32 value becomes hi + mid + lo: hi is the value truncated to bfloat16 (so
+// Copies a matrix into rows that TMA can read: as it is (PARTS = 1), or fp32
+// into PARTS = 3 planes of bfloat16.  A value becomes hi + mid + lo: hi is the value truncated to bfloat16 (so
 // that it never overflows), mid and lo round what is left to nearest; the
 // rest is below 2^-25 of the value.
-template <class T, int PARTS>
+template <class T, int PARTS, class O>
 __global__ void __launch_bounds__(256) loss_split_kernel(const T* src, int rows, int cols,
-                                                         long long ld, bf16* dst, long long ld_dst,
+                                                         long long ld, O* dst, long long ld_dst,
                                                          long long plane, int vectors,
                                                          unsigned* err) {
   grid_launch_dependents();
@@ -284,7 +267,7 @@ __global__ void __launch_bounds__(256) loss_split_kernel(const T* src, int rows,
                    ? to_f32(src[at + j])
                    : 0.0f;
     }
-    bf16* const out = dst + static_cast<size_t>(r) * ld_dst + c;
+    O* const out = dst + static_cast<size_t>(r) * ld_dst + c;
     if constexpr (PARTS == 3) {
       float hi[8];
 #pragma unroll
@@ -300,7 +283,7 @@ __global__ void __launch_bounds__(256) loss_split_kernel(const T* src, int rows,
         for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
       }
     } else {
-      store_vec<bf16, 8>(out, v);
+      store_vec<O, 8>(out, v);
     }
   }
 }
@@ -349,38 +332,50 @@ struct Layout {
   }
 };
 
-// An operand as TMA reads it: where it lies, or packed into scratch.
+// An operand as TMA reads it: where it lies, or copied into scratch because
+// its rows are not on 16-byte boundaries, or as three parts of fp32.
 struct Operand {
-  bool packed = false;
+  enum Form { kAsIs, kCopied, kSplit } form = kAsIs;
   size_t at = 0;           // in scratch
   long long ld = 0, plane = 0;
+  const void* in(const void* p, const char* scratch) const { return form == kAsIs ? p : scratch + at; }
 };
 
-Operand plan_operand(const void* p, long long ld, int rows, int cols, int type, Layout& layout) {
+Operand plan_operand(const void* p, long long ld, int rows, int cols, bool f32, bool split,
+                     Layout& layout) {
   Operand o;
-  o.packed = type == GEMM_F32_TYPE_F32 || reinterpret_cast<uintptr_t>(p) % 16 != 0 || ld % 8 != 0;
+  const int size = f32 ? 4 : 2;
+  if (split)
+    o.form = Operand::kSplit;
+  else if (reinterpret_cast<uintptr_t>(p) % 16 != 0 || ld * size % 16 != 0)
+    o.form = Operand::kCopied;
   o.ld = ld;
-  if (o.packed) {
+  if (o.form != Operand::kAsIs) {
     o.ld = static_cast<long long>(round_up(cols, 8));
     o.plane = o.ld * rows;
-    o.at = layout.take(static_cast<size_t>(o.plane) * (type == GEMM_F32_TYPE_F32 ? 3 : 1) * 2);
+    o.at = layout.take(static_cast<size_t>(o.plane) * (split ? 6 : size));
   }
   return o;
 }
 
-int pack(const Operand& o, const void* src, long long ld, int rows, int cols, int type, char* scratch,
+int pack(const Operand& o, const void* src, long long ld, int rows, int cols, bool f32, char* scratch,
          int num_sms, unsigned* err, cudaStream_t stream, int* launches) {
-  if (!o.packed) return GEMM_F32_OK;
+  if (o.form == Operand::kAsIs) return GEMM_F32_OK;
   const long long work = static_cast<long long>(rows) * ((cols + 7) / 8);
   const unsigned grid = static_cast<unsigned>(std::min<long long>((work + 255) / 256, 16LL * num_sms));
-  bf16* const dst = reinterpret_cast<bf16*>(scratch + o.at);
-  const size_t size = type == GEMM_F32_TYPE_F32 ? 4 : 2;
-  const int vectors = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld * size % 16 == 0;
-  return type == GEMM_F32_TYPE_F32
-             ? launch(loss_split_kernel<float, 3>, dim3(grid), 256, stream, launches,
-                      static_cast<const float*>(src), rows, cols, ld, dst, o.ld, o.plane, vectors, err)
-             : launch(loss_split_kernel<bf16, 1>, dim3(grid), 256, stream, launches,
-                      static_cast<const bf16*>(src), rows, cols, ld, dst, o.ld, o.plane, vectors, err);
+  void* const dst = scratch + o.at;
+  const int vectors = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld * (f32 ? 4 : 2) % 16 == 0;
+  if (o.form == Operand::kSplit)
+    return launch(loss_split_kernel<float, 3, bf16>, dim3(grid), 256, stream, launches,
+                  static_cast<const float*>(src), rows, cols, ld, static_cast<bf16*>(dst), o.ld, o.plane,
+                  vectors, err);
+  if (f32)
+    return launch(loss_split_kernel<float, 1, float>, dim3(grid), 256, stream, launches,
+                  static_cast<const float*>(src), rows, cols, ld, static_cast<float*>(dst), o.ld, o.plane,
+                  vectors, err);
+  return launch(loss_split_kernel<bf16, 1, bf16>, dim3(grid), 256, stream, launches,
+                static_cast<const bf16*>(src), rows, cols, ld, static_cast<bf16*>(dst), o.ld, o.plane,
+                vectors, err);
 }
 
 int run(const Call& c, cudaStream_t stream, int* launches) {
@@ -388,9 +383,11 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   unsigned* err = nullptr;
   if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
   const bool f32 = c.type == GEMM_F32_TYPE_F32, grad = c.dx || c.dw;
+  const bool few = c.rows <= kFewRows;
   const int parts = f32 ? 3 : 1;
   const long long ld_exps = static_cast<long long>(round_up(c.vocab, 256));
-  const int pieces = static_cast<int>(ld_exps / kPiece);
+  const int piece_bits = few ? kFewPieceBits : kPieceBits;
+  const int pieces = few ? (c.vocab + kFewPiece - 1) / kFewPiece : static_cast<int>(ld_exps >> kPieceBits);
 
   // rows per piece: bounded by the exponentials (and the parts of g), or by
   // the statistics alone
@@ -410,8 +407,9 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   const size_t at_loss = c.loss ? 0 : layout.take(sizeof(float) * c.rows);
   const long long ld_stats = static_cast<long long>(round_up(step, 32));
   const size_t at_stats = layout.take(sizeof(float2) * pieces * ld_stats);
-  const Operand ox = plan_operand(c.x, c.ldx, c.rows, c.width, c.type, layout);
-  const Operand ow = plan_operand(c.w, c.ldw, c.vocab, c.width, c.type, layout);
+  const size_t at_joined = grad ? layout.take(sizeof(float2) * step) : 0;
+  const Operand ox = plan_operand(c.x, c.ldx, c.rows, c.width, f32, f32, layout);
+  const Operand ow = plan_operand(c.w, c.ldw, c.vocab, c.width, f32, f32 && !few, layout);
   size_t at_exps = 0, at_g = 0, at_partials = 0, at_sum = 0;
   if (grad) {
     at_exps = layout.take(static_cast<size_t>(step) * ld_exps * (f32 ? 4 : 2));
@@ -419,7 +417,9 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     size_t partial = 0;
     for (long long r = 0; r < c.rows; r += step) {
       const int n = static_cast<int>(std::min<long long>(step, c.rows - r));
-      if (c.dx) partial = std::max(partial, half_gemm_scratch(n, c.width, c.vocab, parts, num_sms));
+      if (c.dx)
+        partial = std::max(partial, few ? few_gemm_scratch(n, c.width, c.vocab, num_sms)
+                                        : half_gemm_scratch(n, c.width, c.vocab, parts, num_sms));
       if (c.dw) partial = std::max(partial, half_gemm_scratch(c.vocab, c.width, n, parts, num_sms));
     }
     at_partials = layout.take(partial);
@@ -442,11 +442,11 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
                         static_cast<const int*>(c.targets), c.rows, c.vocab, c.ignore, mean,
                         c.grad_scale, labels, factors, err);
   if (rc == GEMM_F32_OK)
-    rc = pack(ox, c.x, c.ldx, c.rows, c.width, c.type, scratch, num_sms, err, stream, launches);
+    rc = pack(ox, c.x, c.ldx, c.rows, c.width, f32, scratch, num_sms, err, stream, launches);
   if (rc == GEMM_F32_OK)
-    rc = pack(ow, c.w, c.ldw, c.vocab, c.width, c.type, scratch, num_sms, err, stream, launches);
+    rc = pack(ow, c.w, c.ldw, c.vocab, c.width, f32, scratch, num_sms, err, stream, launches);
 
-  const HalfOperand w = {ow.packed ? scratch + ow.at : c.w, ow.ld, ow.plane, false};
+  const HalfOperand w = {ow.in(c.w, scratch), ow.ld, ow.plane, false};
   for (long long r = 0; rc == GEMM_F32_OK && r < c.rows; r += step) {
     const int n = static_cast<int>(std::min<long long>(step, c.rows - r));
     HalfGemm base = {};
@@ -454,31 +454,51 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     base.num_sms = num_sms;
     base.device = device;
     base.err = err;
-    const char* const xp = static_cast<const char*>(ox.packed ? scratch + ox.at : c.x);
+    const char* const xp = static_cast<const char*>(ox.in(c.x, scratch));
     const HalfOperand x = {xp + static_cast<size_t>(r) * ox.ld * 2, ox.ld, ox.plane, false};
 
-    HalfGemm z = base;   // logits
-    z.M = n;
-    z.N = c.vocab;
-    z.K = c.width;
-    z.a = x;
-    z.b = w;
-    z.stats = stats;
-    z.ld_stats = ld_stats;
-    z.exps = grad ? scratch + at_exps : nullptr;
-    z.ld_exps = ld_exps;
-    z.labels = labels + r;
-    z.label_logit = logit + r;
-    rc = launch_half_gemm(z, stream, launches);
-    if (rc != GEMM_F32_OK) break;
-    float* const lse = c.lse ? c.lse + r : nullptr;
-    if (!grad) {
-      rc = launch(loss_join_kernel, dim3((n + 31) / 32), 1024, stream, launches,
-                  static_cast<const float2*>(stats), ld_stats, pieces, n,
-                  static_cast<const int*>(labels + r), static_cast<const float*>(logit + r), loss + r,
-                  lse);
-      continue;
+    FewGemm few_base = {};
+    few_base.f32 = f32;
+    few_base.rows = n;
+    few_base.width = c.width;
+    few_base.vocab = c.vocab;
+    few_base.w = w.ptr;
+    few_base.ldw = w.ld;
+    few_base.num_sms = num_sms;
+    few_base.device = device;
+    few_base.err = err;
+    if (few) {
+      FewGemm z = few_base;
+      z.b = x;
+      z.stats = stats;
+      z.ld_stats = ld_stats;
+      z.exps = grad ? scratch + at_exps : nullptr;
+      z.ld_exps = ld_exps;
+      z.labels = labels;
+      z.label_logit = logit;
+      rc = launch_few_gemm(z, stream, launches);
+    } else {
+      HalfGemm z = base;
+      z.M = n;
+      z.N = c.vocab;
+      z.K = c.width;
+      z.a = x;
+      z.b = w;
+      z.stats = stats;
+      z.ld_stats = ld_stats;
+      z.exps = grad ? scratch + at_exps : nullptr;
+      z.ld_exps = ld_exps;
+      z.labels = labels + r;
+      z.label_logit = logit + r;
+      rc = launch_half_gemm(z, stream, launches);
     }
+    if (rc != GEMM_F32_OK) break;
+    float2* const joined = grad ? reinterpret_cast<float2*>(scratch + at_joined) : nullptr;
+    rc = launch(loss_join_kernel, dim3((n + kJoinRows - 1) / kJoinRows), kJoinThreads, stream, launches,
+                static_cast<const float2*>(stats), ld_stats, pieces, n, static_cast<const int*>(labels + r),
+                static_cast<const float*>(logit + r), loss + r, c.lse ? c.lse + r : nullptr, joined);
+    if (rc != GEMM_F32_OK) break;
+    if (!grad) continue;
 
     // bands of columns: some eight CTAs per SM where the rows alone give fewer
     const int groups = (n + kRescaleRows - 1) / kRescaleRows;
@@ -488,19 +508,24 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     const dim3 grid(groups, static_cast<unsigned>((cols + band - 1) / band));
     bf16* const gp = reinterpret_cast<bf16*>(scratch + at_g);
     const long long plane = f32 ? static_cast<long long>(step) * ld_exps : 0;
-    rc = f32 ? launch(loss_rescale_kernel<3>, grid, kRescaleThreads, stream, launches,
-                      static_cast<const float2*>(stats), ld_stats, pieces, n, cols, band,
-                      static_cast<const int*>(labels + r), static_cast<const float*>(logit + r),
-                      loss + r, lse, static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err)
-             : launch(loss_rescale_kernel<1>, grid, kRescaleThreads, stream, launches,
-                      static_cast<const float2*>(stats), ld_stats, pieces, n, cols, band,
-                      static_cast<const int*>(labels + r), static_cast<const float*>(logit + r),
-                      loss + r, lse, static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err);
+    rc = launch(f32 ? loss_rescale_kernel<3> : loss_rescale_kernel<1>, grid, kRescaleThreads, stream,
+                launches, static_cast<const float2*>(stats), ld_stats, piece_bits,
+                static_cast<const float2*>(joined), n, cols, band, static_cast<const int*>(labels + r),
+                static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err);
     if (rc != GEMM_F32_OK) break;
 
     base.scale = &factors->grad;
     base.partials = reinterpret_cast<float*>(scratch + at_partials);
-    if (c.dx) {   // dx = s g w: K runs along the vocabulary
+    if (c.dx && few) {
+      FewGemm d = few_base;
+      d.b = {gp, ld_exps, plane, false};
+      d.dx = c.dx;
+      d.lddx = c.lddx;
+      d.scale = base.scale;
+      d.partials = base.partials;
+      rc = launch_few_gemm(d, stream, launches);
+      if (rc != GEMM_F32_OK) break;
+    } else if (c.dx) {   // dx = s g w: K runs along the vocabulary
       HalfGemm d = base;
       d.M = n;
       d.N = c.width;
