@@ -585,6 +585,21 @@ __device__ __forceinline__ void mma_tf32_tmem_a(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
+// One lane of a converged warp, always the same one.  A warp that issues MMAs
+// walks its loop with all lanes and lets this lane alone issue: the operands
+// then stay warp-uniform values, which the MMA takes as they are.  In a
+// branch that one lane enters they are moved to uniform registers before
+// every MMA, about 100 clocks each (measured on GB300).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t chosen;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(chosen));
+  return chosen != 0;
+}
+
 // The mbarrier receives one arrive once every tcgen05 operation this thread
 // issued before has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {

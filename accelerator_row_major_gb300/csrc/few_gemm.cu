@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_slot = more_bars + 8u * 13;
   static_assert(8 * (2 * SW + 2 * kMostRings + 14) <= 1024, "barriers");
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);   // warp-uniform
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < SW; ++s) {
@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base));
+  const uint32_t tmem_base = __shfl_sync(
+      0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base)), 0);
   const uint32_t parts0 = tmem_base + static_cast<uint32_t>(2 * p.acc_cols);
   grid_launch_dependents();
   grid_dependency_wait();   // global memory from here on
@@ -381,34 +382,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      // bfloat16 operands, fp32 accumulator, M = 128, N = n_pad; A in tensor
-      // memory is K-major
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MN && !F32 ? 1u : 0u) << 15) |
-                             (static_cast<uint32_t>(p.n_pad >> 3) << 17) | ((kTile >> 4) << 24);
-      int sa = 0, sb = 0, buf = 0;       // sa: stage of w, or of its parts
-      uint32_t pha = 0, phb = 0, acc_ph = 0;
-      const int SA = F32 ? p.p_stages : SW;
-      bool ok = true;
-      Items<MN> list(p);
-      while (ok && list.next(p, w)) {
-        for (int kb = w.k0; kb < w.k1; ++kb) {
-          const bool open = (kb - w.k0) % SUM == 0;
-          if (open && !mbar_wait(acce(buf), acc_ph ^ 1u, p.err, kSiteMmaAccEmpty)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait(bfull(sb), phb, p.err, kSiteMmaReady) ||
-              !mbar_wait(F32 ? pfull(sa) : wfull(sa), pha, p.err, kSiteMmaReady)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * p.acc_cols);
-          const uint32_t bst = b_base + static_cast<uint32_t>(sb) * b_stage_bytes;
+    // bfloat16 operands, fp32 accumulator, M = 128, N = n_pad; A in tensor
+    // memory is K-major
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MN && !F32 ? 1u : 0u) << 15) |
+                           (static_cast<uint32_t>(p.n_pad >> 3) << 17) | ((kTile >> 4) << 24);
+    const bool issuer = elect_lane();
+    int sa = 0, sb = 0, buf = 0;         // sa: stage of w, or of its parts
+    uint32_t pha = 0, phb = 0, acc_ph = 0;
+    const int SA = F32 ? p.p_stages : SW;
+    bool ok = true;
+    Items<MN> list(p);
+    while (ok && list.next(p, w)) {
+      for (int kb = w.k0; kb < w.k1; ++kb) {
+        const bool open = (kb - w.k0) % SUM == 0;
+        const bool got = (!open || mbar_wait(acce(buf), acc_ph ^ 1u, p.err, kSiteMmaAccEmpty)) &&
+                         mbar_wait(bfull(sb), phb, p.err, kSiteMmaReady) &&
+                         mbar_wait(F32 ? pfull(sa) : wfull(sa), pha, p.err, kSiteMmaReady);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * p.acc_cols);
+        const uint32_t bst = b_base + static_cast<uint32_t>(sb) * b_stage_bytes;
+        const bool close = (kb - w.k0) % SUM == SUM - 1 || kb == w.k1 - 1;
+        const uint32_t at = F32 ? parts0 + static_cast<uint32_t>(sa * 3 * kPartCols)
+                                : base + sa * C::kWBytes;
+        if (issuer) {
           uint32_t more = open ? 0u : 1u;
           if (F32) {
-            const uint32_t at = parts0 + static_cast<uint32_t>(sa * 3 * kPartCols);
             // (lo, hi), (hi, lo), (mid, mid), (mid, hi), (hi, mid), (hi, hi)
 #pragma unroll
             for (int combo = 0; combo < 6; ++combo) {
@@ -422,31 +424,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mma_commit(pempty(sa));
           } else {
-            const uint32_t st = base + sa * C::kWBytes;
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk) {
-              mma_bf16(acc, MN ? smem_desc(st + kk * 2048, 8192, 1024, 2) : smem_desc(st + kk * 32, 16, 1024, 2),
+              mma_bf16(acc, MN ? smem_desc(at + kk * 2048, 8192, 1024, 2) : smem_desc(at + kk * 32, 16, 1024, 2),
                        smem_desc(bst + kk * 32, 16, 1024, 2), idesc, more);
               more = 1u;
             }
             mma_commit(wempty(sa));
           }
           mma_commit(bempty(sb));
-          if (++sa == SA) {
-            sa = 0;
-            pha ^= 1u;
-          }
-          if (++sb == SB) {
-            sb = 0;
-            phb ^= 1u;
-          }
-          if ((kb - w.k0) % SUM == SUM - 1 || kb == w.k1 - 1) {
-            mma_commit(accf(buf));
-            buf ^= 1;
-            if (buf == 0) acc_ph ^= 1u;
-          }
+          if (close) mma_commit(accf(buf));
+        }
+        __syncwarp();
+        if (++sa == SA) {
+          sa = 0;
+          pha ^= 1u;
+        }
+        if (++sb == SB) {
+          sb = 0;
+          phb ^= 1u;
+        }
+        if (close) {
+          buf ^= 1;
+          if (buf == 0) acc_ph ^= 1u;
         }
       }
+    }
+    if (issuer) {
       mma_commit(drain_bar);
       mbar_wait(drain_bar, 0, p.err, kSiteDrainMma);
     }

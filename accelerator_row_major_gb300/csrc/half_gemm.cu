@@ -311,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t drain_bar = bars + 8u * (2 * S + 4);
   const uint32_t tmem_slot = bars + 8u * (2 * S + 5);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);   // warp-uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
@@ -337,7 +337,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();      // barriers of both CTAs exist before any remote arrive
   tc_fence_after_sync();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base));
+  const uint32_t tmem_base = __shfl_sync(
+      0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base)), 0);
   grid_launch_dependents();
   grid_dependency_wait();   // global memory from here on
 
@@ -404,19 +405,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16(2 * kHalf, kTile, A_MN, B_MN);
+      const bool issuer = elect_lane();
       int s = 0, buf = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true;
       // One accumulator's sum: over the whole item, or over one unit of it.
       auto open = [&]() {
-        if (!mbar_wait_cluster(acce_bar(buf), acc_ph ^ 1u, p.err, kSiteMmaAccEmpty)) return false;
+        const bool got = mbar_wait_cluster(acce_bar(buf), acc_ph ^ 1u, p.err, kSiteMmaAccEmpty);
         tc_fence_after_sync();
-        return true;
+        return __all_sync(0xFFFFFFFFu, got) != 0;
       };
       auto close = [&]() {
-        mma_commit_both(accf_bar(buf));
+        if (issuer) mma_commit_both(accf_bar(buf));
+        __syncwarp();
         buf ^= 1;
         if (buf == 0) acc_ph ^= 1u;
       };
@@ -434,20 +437,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const int blocks = kCombos * (end_block(u) - first_block(u));
           for (int i = 0; i < blocks; ++i) {
-            if (!mbar_wait_cluster(full_bar(s), ph, p.err, kSiteMmaReady)) {
+            const bool got = mbar_wait_cluster(full_bar(s), ph, p.err, kSiteMmaReady);
+            if (!__all_sync(0xFFFFFFFFu, got)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
             const uint32_t st = base + s * kStageBytes;
             const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * kTile);
+            if (issuer) {
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              mma_bf16_pair(acc, operand_desc<A_MN>(st, kk),
-                            operand_desc<B_MN>(st + kOperandBytes, kk), idesc, more);
-              more = 1u;
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                mma_bf16_pair(acc, operand_desc<A_MN>(st, kk),
+                              operand_desc<B_MN>(st + kOperandBytes, kk), idesc, kk ? 1u : more);
+              mma_commit_both(empty_bar(s));
             }
-            mma_commit_both(empty_bar(s));
+            __syncwarp();
+            more = 1u;
             if (++s == S) {
               s = 0;
               ph ^= 1u;
@@ -457,8 +463,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!SUM && ok) close();
       }
-      mma_commit_local(drain_bar);
-      mbar_wait(drain_bar, 0, p.err, kSiteDrainMma);
+      if (issuer) {
+        mma_commit_local(drain_bar);
+        mbar_wait(drain_bar, 0, p.err, kSiteDrainMma);
+      }
     }
     __syncwarp();
   } else if (warp >= kEpilogueWarp0) {
