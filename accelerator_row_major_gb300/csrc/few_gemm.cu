@@ -13,9 +13,14 @@
 // never stored in parts; eight warps read each landed tile of 128 x 64, split
 // every value into hi + mid + lo (24 bits) and write the parts to tensor
 // memory, where the MMA takes its A operand.  The six products of half_gemm.cu
-// are summed for 64 of K, the smallest first, and the sums are added in
-// registers to nearest, since the tensor core's own additions truncate.
-// bfloat16 sums 1024 of K that way.
+// are summed for a stretch of K and the sums are added in registers to
+// nearest, since the tensor core's own additions truncate.  Up to 64 rows the
+// parts of b lie one below the other as one operand of 3 n, so three MMAs
+// make the six products, [hi | mid | lo] by hi, [hi | mid] by mid, [hi] by
+// lo, into three accumulators by size, each 512 of K long (an MMA was
+// measured to cost n / 2 + 26 clocks); above, tensor memory has no room for
+// them and six MMAs go into one accumulator, smallest first, 64 of K long.
+// bfloat16 operands sum 1024 of K.
 //
 // Roles (640 threads): warp 0 loads w, warp 2 loads b, warp 1 tensor memory
 // and MMAs, warps 4 .. 11 epilogue (4 warps of 32 lanes for each 64 rows),
@@ -53,7 +58,10 @@ constexpr int kGroupWarps = 4;           // 32 lanes of tensor memory each
 constexpr int kTmemCols = 512;
 constexpr int kPartCols = 32;            // one part of a 128 x 64 tile in tensor memory
 constexpr int kMostRings = 8;            // stages of b; of parts at most 4
-constexpr int kSumBlocks = 16;           // K blocks per accumulator sum (bfloat16)
+constexpr int kSumBf16 = 16;             // K blocks per accumulator sum
+constexpr int kSumStacked = 8;
+constexpr int kStackedRows = 64;         // most rows with the parts of b stacked
+constexpr int sum_blocks(bool f32, bool stacked) { return !f32 ? kSumBf16 : stacked ? kSumStacked : 1; }
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool F32>
@@ -69,7 +77,7 @@ struct Cfg {
 
 struct FewParams {
   int rows, n_pad;                       // T and the MMA's N
-  int acc_cols;                          // columns of one accumulator: 64 or 128
+  int acc_cols, acc_bufs;                // columns of an accumulator (or three), buffers of it
   int b_stages, p_stages;                // stages of b, and of parts in tensor memory
   int width, vocab;
   int k_blocks;
@@ -237,13 +245,13 @@ __device__ __forceinline__ void logits_out(const FewParams& p, int piece, int la
 }
 
 // ---------------------------------------------------------------- kernel
-template <bool MN, bool F32>
+template <bool MN, bool F32, bool STACKED>
 __global__ void __launch_bounds__(kThreads, 1)
     few_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
                     const FewParams p) {
   using C = Cfg<F32>;
   constexpr int SW = C::kWStages, PARTS = C::kParts;
-  constexpr int SUM = F32 ? 1 : kSumBlocks;
+  constexpr int SUM = sum_blocks(F32, STACKED);
   extern __shared__ uint8_t smem_dyn[];
   const uint32_t dyn0 = smem_addr(smem_dyn);
   const uint32_t base = (dyn0 + 1023u) & ~1023u;
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem_base = __shfl_sync(
       0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base)), 0);
-  const uint32_t parts0 = tmem_base + static_cast<uint32_t>(2 * p.acc_cols);
+  const uint32_t parts0 = tmem_base + static_cast<uint32_t>(p.acc_bufs * p.acc_cols);
   grid_launch_dependents();
   grid_dependency_wait();   // global memory from here on
 
@@ -384,8 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     // bfloat16 operands, fp32 accumulator, M = 128, N = n_pad; A in tensor
     // memory is K-major
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MN && !F32 ? 1u : 0u) << 15) |
-                           (static_cast<uint32_t>(p.n_pad >> 3) << 17) | ((kTile >> 4) << 24);
+    const uint32_t idesc_n = static_cast<uint32_t>(p.n_pad >> 3) << 17;
+    const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((MN && !F32 ? 1u : 0u) << 15) |
+                            ((kTile >> 4) << 24);
+    const uint32_t idesc = idesc0 + idesc_n;
     const bool issuer = elect_lane();
     int sa = 0, sb = 0, buf = 0;         // sa: stage of w, or of its parts
     uint32_t pha = 0, phb = 0, acc_ph = 0;
@@ -405,12 +415,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * p.acc_cols);
         const uint32_t bst = b_base + static_cast<uint32_t>(sb) * b_stage_bytes;
-        const bool close = (kb - w.k0) % SUM == SUM - 1 || kb == w.k1 - 1;
+        const bool close = (kb - w.k0 + 1) % SUM == 0 || kb == w.k1 - 1;
         const uint32_t at = F32 ? parts0 + static_cast<uint32_t>(sa * 3 * kPartCols)
                                 : base + sa * C::kWBytes;
         if (issuer) {
           uint32_t more = open ? 0u : 1u;
-          if (F32) {
+          if constexpr (STACKED) {
+            // by hi, mid and lo of w: 3, 2 and 1 parts of b
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                mma_bf16_tmem_a(acc + static_cast<uint32_t>(part * p.n_pad),
+                                at + static_cast<uint32_t>(part * kPartCols + kk * 8),
+                                smem_desc(bst + kk * 32, 16, 1024, 2), idesc0 + (3 - part) * idesc_n, more);
+                more = 1u;
+              }
+            mma_commit(pempty(sa));
+          } else if constexpr (F32) {
             // (lo, hi), (hi, lo), (mid, mid), (mid, hi), (hi, mid), (hi, hi)
 #pragma unroll
             for (int combo = 0; combo < 6; ++combo) {
@@ -444,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           sb = 0;
           phb ^= 1u;
         }
-        if (close) {
-          buf ^= 1;
-          if (buf == 0) acc_ph ^= 1u;
+        if (close && ++buf == p.acc_bufs) {
+          buf = 0;
+          acc_ph ^= 1u;
         }
       }
     }
@@ -482,17 +504,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
           if (ch * 16 < cols) {
+            const uint32_t at = t_mine + static_cast<uint32_t>(buf * p.acc_cols + ch * 16);
             uint32_t v[16];
-            tmem_ld_16cols(t_mine + static_cast<uint32_t>(buf * p.acc_cols + ch * 16), v);
-            tmem_wait_ld();
+            tmem_ld_16cols(at, v);
+            if constexpr (STACKED) {   // the two smaller sums first
+              uint32_t mid[16], low[16];
+              tmem_ld_16cols(at + static_cast<uint32_t>(p.n_pad), mid);
+              tmem_ld_16cols(at + static_cast<uint32_t>(2 * p.n_pad), low);
+              tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[ch * 16 + j] += __uint_as_float(v[j]);
+              for (int j = 0; j < 16; ++j)
+                acc[ch * 16 + j] += __uint_as_float(v[j]) + (__uint_as_float(mid[j]) + __uint_as_float(low[j]));
+            } else {
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[ch * 16 + j] += __uint_as_float(v[j]);
+            }
           }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(acce(buf));
-        buf ^= 1;
-        if (buf == 0) acc_ph ^= 1u;
+        if (++buf == p.acc_bufs) {
+          buf = 0;
+          acc_ph ^= 1u;
+        }
       }
       if (!ok) break;
       if (MN) {
@@ -661,11 +696,11 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* pt
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool MN, bool F32>
+template <bool MN, bool F32, bool STACKED>
 int launch_one(const FewGemm& g, const FewParams& p, const CUtensorMap& mw, const CUtensorMap& mb,
                int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};   // bit per device
-  auto kern = few_gemm_kernel<MN, F32>;
+  auto kern = few_gemm_kernel<MN, F32, STACKED>;
   const unsigned long long bit = 1ull << (g.device % kMaxDevices);
   if (!(configured.load() & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<F32>::kSmem) !=
@@ -681,6 +716,14 @@ int launch_one(const FewGemm& g, const FewParams& p, const CUtensorMap& mw, cons
     return GEMM_F32_ELAUNCH;
   }
   return GEMM_F32_OK;
+}
+
+template <bool MN>
+int launch_type(const FewGemm& g, bool stacked, const FewParams& p, const CUtensorMap& mw,
+                const CUtensorMap& mb, int grid, cudaStream_t stream) {
+  if (!g.f32) return launch_one<MN, false, false>(g, p, mw, mb, grid, stream);
+  return stacked ? launch_one<MN, true, true>(g, p, mw, mb, grid, stream)
+                 : launch_one<MN, true, false>(g, p, mw, mb, grid, stream);
 }
 
 }  // namespace
@@ -714,8 +757,12 @@ int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches) {
     p.label_logit = g.label_logit;
   }
   p.n_pad = blocks_of(g.rows, 16) * 16;
-  p.acc_cols = p.n_pad <= 64 ? 64 : 128;
-  p.p_stages = std::min(4, (kTmemCols - 2 * p.acc_cols) / (3 * kPartCols));
+  // tensor memory: accumulators, then stages of parts (at least two, and a
+  // second accumulator where that leaves three)
+  const bool stacked = g.f32 && p.n_pad <= kStackedRows;
+  p.acc_cols = stacked ? 3 * p.n_pad : p.n_pad;
+  p.acc_bufs = stacked && 2 * p.acc_cols + 9 * kPartCols > kTmemCols ? 1 : 2;
+  p.p_stages = std::min(4, (kTmemCols - p.acc_bufs * p.acc_cols) / (3 * kPartCols));
   p.b_stages = std::min(kMostRings, Cfg<true>::kBBytes / ((g.f32 ? 3 : 1) * p.n_pad * kBK * 2));
   p.err = g.err;
   CUtensorMap mw, mb;
@@ -726,13 +773,8 @@ int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches) {
       !encode(&mb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.b.ptr, g.b.ld, g.rows,
               dx ? g.vocab : g.width, g.f32 ? 3 : 1, g.b.plane, kBK, p.n_pad, CU_TENSOR_MAP_SWIZZLE_128B))
     return GEMM_F32_ELAUNCH;
-  int rc;
-  if (dx)
-    rc = g.f32 ? launch_one<true, true>(g, p, mw, mb, grid, stream)
-               : launch_one<true, false>(g, p, mw, mb, grid, stream);
-  else
-    rc = g.f32 ? launch_one<false, true>(g, p, mw, mb, grid, stream)
-               : launch_one<false, false>(g, p, mw, mb, grid, stream);
+  const int rc = dx ? launch_type<true>(g, stacked, p, mw, mb, grid, stream)
+                    : launch_type<false>(g, stacked, p, mw, mb, grid, stream);
   if (rc != GEMM_F32_OK) return rc;
   ++*launches;
   if (dx) {
