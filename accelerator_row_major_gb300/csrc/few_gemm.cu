@@ -89,7 +89,7 @@ struct FewParams {
   long long ld_stats;
   void* exps;
   long long ld_exps;
-  const int* labels;
+  LossTargets targets;
   float* label_logit;
   unsigned* err;
 };
@@ -224,7 +224,7 @@ __device__ __forceinline__ void logits_out(const FewParams& p, int piece, int la
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const int t = t0 + j;
-    if (t < p.rows && in && __ldg(p.labels + t) == v) p.label_logit[t] = acc[at + j];
+    if (t < p.rows && in && label_at(p.targets, t) == v) p.label_logit[t] = acc[at + j];
     if (t >= p.rows || p.exps == nullptr) continue;
     const size_t to = static_cast<size_t>(t) * p.ld_exps + v;
     if (!GEMM_IN_EXTENT(to, static_cast<size_t>(p.rows) * p.ld_exps, p.err, kSiteBoundsScratch))
@@ -753,7 +753,7 @@ int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches) {
     p.ld_stats = g.ld_stats;
     p.exps = g.exps;
     p.ld_exps = g.ld_exps;
-    p.labels = g.labels;
+    p.targets = g.targets;
     p.label_logit = g.label_logit;
   }
   p.n_pad = blocks_of(g.rows, 16) * 16;

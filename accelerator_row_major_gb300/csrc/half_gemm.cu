@@ -101,7 +101,7 @@ struct Params {
   long long ld_stats;
   void* exps;
   long long ld_exps;
-  const int* labels;
+  LossTargets targets;
   float* label_logit;
   unsigned* err;
 };
@@ -580,7 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // nothing above -inf: any finite reference gives powers of 0
         const float m2 = top == -INFINITY ? 0.0f : top * kLog2e;
-        const int label = row_ok ? __ldg(p.labels + row) - n0 : -1;
+        const int label = row_ok ? label_at(p.targets, row) - n0 : -1;
         // one part: powers times 2^15, which keep their 11 bits in fp16 down to 2^-29
         constexpr float kUp = PARTS == 3 ? 0.0f : 15.0f;
         float sum = 0.0f;
@@ -810,7 +810,7 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
   p.ld_stats = g.ld_stats;
   p.exps = g.exps;
   p.ld_exps = g.ld_exps;
-  p.labels = g.labels;
+  p.targets = g.targets;
   p.label_logit = g.label_logit;
   p.err = g.err;
   Maps m = {};

@@ -7,6 +7,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "launch.h"
+
 namespace gemm_f32_impl {
 
 // One operand: `parts` stored row-major bfloat16 matrices of rows x cols
@@ -41,8 +43,8 @@ struct HalfGemm {
   long long ld_stats = 0;
   void* exps = nullptr;         // M rows of ld_exps >= 256 ceil(N / 256) elements
   long long ld_exps = 0;
-  const int* labels = nullptr;  // per row a column, or -1
-  float* label_logit = nullptr; // per row the logit at its label
+  LossTargets targets = {};     // of its rows
+  float* label_logit = nullptr; // per row the logit at its target
   // --
   int num_sms, device;
   unsigned* err;
@@ -73,7 +75,7 @@ struct FewGemm {
   long long ld_stats = 0;
   void* exps = nullptr;
   long long ld_exps = 0;
-  const int* labels = nullptr;
+  LossTargets targets = {};
   float* label_logit = nullptr;
   // -- or dx = *scale * b w (dx != nullptr)
   void* dx = nullptr;

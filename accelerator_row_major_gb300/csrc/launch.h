@@ -136,6 +136,18 @@ void note_launches(int launches, const char* kernel);
 // Whether two byte ranges share a byte.
 bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes);
 
+// Bytes at the start of every scratch buffer that are zero when it is
+// allocated; the first word counts arrivals and is zero between kernels.
+constexpr size_t kScratchHeader = 256;
+
+// Targets of a loss: 32- or 64-bit integers.
+struct LossTargets {
+  const void* p;
+  int bits;
+  int vocab;
+  long long ignore;
+};
+
 // Small products (at most kSmallMaxWork multiply-adds, K <= kSmallMaxK) on a
 // latency-lean CUDA-core kernel, in every mode: below these sizes launch and
 // pipeline set-up dominate the tensor-core kernels' time.

@@ -458,6 +458,7 @@ int grad(NormArgs a, bool vectors, void* dweight, void* dbias, int device, int n
     scratch = static_cast<float*>(
         acquire_scratch(device, stream, (part_floats + sums_floats) * sizeof(float)));
     if (!scratch) return GEMM_F32_ESCRATCH;
+    scratch += kScratchHeader / sizeof(float);
   }
   float* const parts = columns ? scratch : nullptr;
   int ctas = 0, rc;

@@ -9,8 +9,10 @@
 #include <cstdint>
 
 #include "device_common.cuh"
+#include "launch.h"
 
 namespace gemm_f32_dev {
+using gemm_f32_impl::LossTargets;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -110,6 +112,14 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
       reinterpret_cast<uint4*>(p)[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
   }
+}
+
+// The label of a row of a loss: its target, or -1 where the row does not
+// count (its target is the ignored one, or outside the vocabulary).
+__device__ __forceinline__ int label_at(const LossTargets& t, long long row) {
+  const long long y = t.bits == 64 ? __ldg(static_cast<const long long*>(t.p) + row)
+                                   : __ldg(static_cast<const int*>(t.p) + row);
+  return y != t.ignore && y >= 0 && y < t.vocab ? static_cast<int>(y) : -1;
 }
 
 template <int N>

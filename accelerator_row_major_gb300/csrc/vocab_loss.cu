@@ -50,66 +50,64 @@ static_assert(1 << kFewPieceBits == kFewPiece, "columns per statistic");
 constexpr size_t kDefaultPieceBytes = size_t{4} << 30;
 constexpr size_t kMostStatsBytes = size_t{256} << 20;
 
-// Factors of one call, on the device.
+// What a call computes for its own later kernels.
 struct Factors {
   float grad;      // s: grad_scale, divided for the mean
-  float total;     // 1, or 1 / rows that count
 };
-
-// Labels (a row's target, or -1 where the row does not count) and factors.
-template <class I>
-__global__ void __launch_bounds__(1024) loss_labels_kernel(const I* targets, int rows, int vocab,
-                                                           long long ignore, int mean,
-                                                           float grad_scale, int* labels,
-                                                           Factors* factors, unsigned* err) {
-  __shared__ int counts[32];
-  grid_launch_dependents();
-  grid_dependency_wait();
-  int n = 0;
-  for (unsigned t = threadIdx.x; t < static_cast<unsigned>(rows); t += 1024) {
-    const long long y = targets[t];
-    const bool counted = y != ignore;
-    const bool inside = y >= 0 && y < vocab;
-    if (counted && !inside) record_error(err, kSiteTarget);
-    labels[t] = counted && inside ? static_cast<int>(y) : -1;
-    n += counted && inside;
-  }
-  n = __reduce_add_sync(0xFFFFFFFFu, n);
-  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = n;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    n = 0;
-    for (int i = 0; i < 32; ++i) n += counts[i];
-    const float per = mean ? static_cast<float>(n > 1 ? n : 1) : 1.0f;
-    factors->grad = grad_scale / per;
-    factors->total = 1.0f / per;
-  }
-}
 
 // ---------------------------------------------------------------- joining
 // lse and loss of 4 rows per CTA (4 statistics of a piece share a 32-byte
 // sector): the largest maximum M of a row's pieces, then S = sum s 2^(m - M).
 // A piece with sum 0 has nothing above -inf (its m stands for nothing) and
 // does not count; a NaN sum does.  joined (may be null) receives (M, 1 / S).
+//
+// The CTA that finishes last adds up what the call needs of all rows: the
+// factors (in the first piece of the rows) and the total (in the last), from
+// the CTAs' partial sums in a fixed order.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;
 
-__global__ void __launch_bounds__(kJoinThreads)
-    loss_join_kernel(const float2* stats, long long ld, int pieces, int rows, const int* labels,
-                     const float* label_logit, float* loss, float* lse, float2* joined) {
+struct JoinArgs {
+  const float2* stats;
+  long long ld;
+  int pieces, rows;
+  LossTargets targets;       // of these rows, as what follows
+  const float* label_logit;
+  float* loss;
+  float* lse;
+  float2* joined;
+  double* sums;              // per CTA: its rows' losses, and how many count
+  int* counts;
+  // the whole call
+  LossTargets all_targets;
+  int all_rows;
+  const double* all_sums;
+  const int* all_counts;
+  bool first, last, mean;
+  float grad_scale;
+  Factors* factors;
+  float* total;
+  unsigned* arrived;         // 0 before and after every launch
+  unsigned* err;
+};
+
+__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const JoinArgs a) {
   constexpr int kChains = kJoinThreads / kJoinRows, kWarps = kJoinThreads / 32;
   __shared__ float tops[kWarps][kJoinRows], sums[kWarps][kJoinRows];
+  __shared__ double part_sum[kWarps];
+  __shared__ int part_count[kWarps];
+  __shared__ bool finish;
   grid_launch_dependents();
   grid_dependency_wait();
   const int r = threadIdx.x % kJoinRows, chain = threadIdx.x / kJoinRows;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * kJoinRows + r;
-  const float2* const mine = stats + row;
-  const int end = row < rows ? pieces : 0;
+  const float2* const mine = a.stats + row;
+  const int end = row < a.rows ? a.pieces : 0;
   float top = -INFINITY;
 #pragma unroll 8
   for (int i = chain; i < end; i += kChains) {
-    const float2 p = __ldg(mine + i * ld);
+    const float2 p = __ldg(mine + i * a.ld);
     top = p.y != 0.0f ? fmaxf(top, p.x) : top;
   }
 #pragma unroll
@@ -121,21 +119,79 @@ __global__ void __launch_bounds__(kJoinThreads)
   float sum = 0.0f;
 #pragma unroll 8
   for (int i = chain; i < end; i += kChains) {
-    const float2 p = __ldg(mine + i * ld);
+    const float2 p = __ldg(mine + i * a.ld);
     sum += p.y != 0.0f ? p.y * exp2f(p.x - top) : 0.0f;
   }
 #pragma unroll
   for (int o = kJoinRows; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (lane < kJoinRows) sums[warp][lane] = sum;
   __syncthreads();
-  if (chain != 0 || row >= rows) return;
-  sum = sums[0][r];
+  if (warp == 0) {
+    float loss = 0.0f;
+    int label = -1;
+    if (lane < kJoinRows && row < a.rows) {
+      sum = sums[0][r];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) sum += sums[w][r];
-  const float l = sum == 0.0f ? -INFINITY : kLn2 * (top + log2f(sum));
-  if (lse) lse[row] = l;
-  loss[row] = labels[row] < 0 ? 0.0f : l - label_logit[row];
-  if (joined) joined[row] = make_float2(top, 1.0f / sum);
+      for (int w = 1; w < kWarps; ++w) sum += sums[w][r];
+      const float l = sum == 0.0f ? -INFINITY : kLn2 * (top + log2f(sum));
+      label = label_at(a.targets, row);
+      if (label >= 0) loss = l - a.label_logit[row];
+      if (label < 0) {
+        const long long y = a.targets.bits == 64 ? static_cast<const long long*>(a.targets.p)[row]
+                                                 : static_cast<const int*>(a.targets.p)[row];
+        if (y != a.targets.ignore) record_error(a.err, kSiteTarget);
+      }
+      if (a.lse) a.lse[row] = l;
+      if (a.loss) a.loss[row] = loss;
+      if (a.joined) a.joined[row] = make_float2(top, 1.0f / sum);
+    }
+    double s = loss;
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, label >= 0));
+    if (lane == 0) {
+      a.sums[blockIdx.x] = s;
+      a.counts[blockIdx.x] = n;
+      __threadfence();
+      finish = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!finish) return;
+  __threadfence();
+  // ---- the last CTA
+  if (threadIdx.x == 0) *a.arrived = 0u;
+  if (!a.first && !a.last) return;
+  double s = 0.0;
+  int n = 0;
+  if (a.first && !a.last) {   // later pieces of the rows are not joined yet
+#pragma unroll 8
+    for (unsigned t = threadIdx.x; t < static_cast<unsigned>(a.all_rows); t += kJoinThreads)
+      n += label_at(a.all_targets, t) >= 0;
+  } else {
+    const int groups = (a.all_rows - 1) / kJoinRows + 1;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < groups; i += kJoinThreads) {
+      s += __ldcg(a.all_sums + i);
+      n += __ldcg(a.all_counts + i);
+    }
+  }
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) {
+    part_sum[warp] = s;
+    part_count[warp] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < kWarps; ++w) {
+    s += part_sum[w];
+    n += part_count[w];
+  }
+  const float per = a.mean ? static_cast<float>(n > 1 ? n : 1) : 1.0f;
+  if (a.first && a.factors) a.factors->grad = a.grad_scale / per;
+  if (a.last && a.total) *a.total = static_cast<float>(s / per);
 }
 
 // The rescaling pass of the gradient, g = e 2^(m - M) / S - onehot: 4 rows by
@@ -160,7 +216,7 @@ struct Exps<1> {
 template <int PARTS>
 __global__ void __launch_bounds__(kRescaleThreads)
     loss_rescale_kernel(const float2* stats, long long ld_stats, int piece_bits, const float2* joined,
-                        int rows, int cols, int band, const int* labels, void* exps, long long ld,
+                        int rows, int cols, int band, LossTargets targets, void* exps, long long ld,
                         bf16* parts, long long plane, unsigned* err) {
   grid_launch_dependents();
   grid_dependency_wait();
@@ -172,7 +228,7 @@ __global__ void __launch_bounds__(kRescaleThreads)
   for (int r = 0; r < kRescaleRows; ++r) {
     const int row = min(row0 + r, rows - 1);
     const float2 j = __ldg(joined + row);
-    label[r] = __ldg(labels + row);
+    label[r] = label_at(targets, row);
     m[r] = j.x;
     inv[r] = j.y * (PARTS == 3 ? 1.0f : 1.0f / 32768.0f);
   }
@@ -214,24 +270,6 @@ __global__ void __launch_bounds__(kRescaleThreads)
         store_vec<bf16, 8>(static_cast<bf16*>(exps) + at, g);
       }
     }
-  }
-}
-
-// total = factor * sum of the rows' losses, in 64 bits and a fixed order.
-__global__ void __launch_bounds__(1024) loss_total_kernel(const float* loss, int rows,
-                                                          const Factors* factors, float* total) {
-  __shared__ double sums[32];
-  grid_launch_dependents();
-  grid_dependency_wait();
-  double s = 0.0;
-  for (unsigned t = threadIdx.x; t < static_cast<unsigned>(rows); t += 1024) s += loss[t];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 32; ++i) s += sums[i];
-    *total = static_cast<float>(s * factors->total);
   }
 }
 
@@ -326,7 +364,7 @@ size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 struct Layout {
   size_t bytes = 0;
   size_t take(size_t n) {
-    const size_t at = bytes;
+    const size_t at = kScratchHeader + bytes;
     bytes += round_up(n, 256);
     return at;
   }
@@ -402,9 +440,10 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
 
   Layout layout;
   const size_t at_factors = layout.take(sizeof(Factors));
-  const size_t at_labels = layout.take(sizeof(int) * c.rows);
   const size_t at_logit = layout.take(sizeof(float) * c.rows);
-  const size_t at_loss = c.loss ? 0 : layout.take(sizeof(float) * c.rows);
+  const int groups_all = (c.rows - 1) / kJoinRows + 1;
+  const size_t at_sums = layout.take(sizeof(double) * groups_all);
+  const size_t at_counts = layout.take(sizeof(int) * groups_all);
   const long long ld_stats = static_cast<long long>(round_up(step, 32));
   const size_t at_stats = layout.take(sizeof(float2) * pieces * ld_stats);
   const size_t at_joined = grad ? layout.take(sizeof(float2) * step) : 0;
@@ -429,20 +468,10 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   if (!scratch) return GEMM_F32_ESCRATCH;
 
   Factors* const factors = reinterpret_cast<Factors*>(scratch + at_factors);
-  int* const labels = reinterpret_cast<int*>(scratch + at_labels);
   float* const logit = reinterpret_cast<float*>(scratch + at_logit);
-  float* const loss = c.loss ? c.loss : reinterpret_cast<float*>(scratch + at_loss);
   float2* const stats = reinterpret_cast<float2*>(scratch + at_stats);
-  const int mean = c.reduction == GEMM_F32_MEAN;
-  int rc = c.target_bits == 64
-               ? launch(loss_labels_kernel<long long>, dim3(1), 1024, stream, launches,
-                        static_cast<const long long*>(c.targets), c.rows, c.vocab, c.ignore, mean,
-                        c.grad_scale, labels, factors, err)
-               : launch(loss_labels_kernel<int>, dim3(1), 1024, stream, launches,
-                        static_cast<const int*>(c.targets), c.rows, c.vocab, c.ignore, mean,
-                        c.grad_scale, labels, factors, err);
-  if (rc == GEMM_F32_OK)
-    rc = pack(ox, c.x, c.ldx, c.rows, c.width, f32, scratch, num_sms, err, stream, launches);
+  const LossTargets all = {c.targets, c.target_bits, c.vocab, c.ignore};
+  int rc = pack(ox, c.x, c.ldx, c.rows, c.width, f32, scratch, num_sms, err, stream, launches);
   if (rc == GEMM_F32_OK)
     rc = pack(ow, c.w, c.ldw, c.vocab, c.width, f32, scratch, num_sms, err, stream, launches);
 
@@ -456,6 +485,8 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     base.err = err;
     const char* const xp = static_cast<const char*>(ox.in(c.x, scratch));
     const HalfOperand x = {xp + static_cast<size_t>(r) * ox.ld * 2, ox.ld, ox.plane, false};
+    LossTargets targets = all;
+    targets.p = static_cast<const char*>(all.p) + r * (c.target_bits / 8);
 
     FewGemm few_base = {};
     few_base.f32 = f32;
@@ -474,7 +505,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
       z.ld_stats = ld_stats;
       z.exps = grad ? scratch + at_exps : nullptr;
       z.ld_exps = ld_exps;
-      z.labels = labels;
+      z.targets = targets;
       z.label_logit = logit;
       rc = launch_few_gemm(z, stream, launches);
     } else {
@@ -488,15 +519,37 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
       z.ld_stats = ld_stats;
       z.exps = grad ? scratch + at_exps : nullptr;
       z.ld_exps = ld_exps;
-      z.labels = labels + r;
+      z.targets = targets;
       z.label_logit = logit + r;
       rc = launch_half_gemm(z, stream, launches);
     }
     if (rc != GEMM_F32_OK) break;
     float2* const joined = grad ? reinterpret_cast<float2*>(scratch + at_joined) : nullptr;
-    rc = launch(loss_join_kernel, dim3((n + kJoinRows - 1) / kJoinRows), kJoinThreads, stream, launches,
-                static_cast<const float2*>(stats), ld_stats, pieces, n, static_cast<const int*>(labels + r),
-                static_cast<const float*>(logit + r), loss + r, c.lse ? c.lse + r : nullptr, joined);
+    JoinArgs j = {};
+    j.stats = stats;
+    j.ld = ld_stats;
+    j.pieces = pieces;
+    j.rows = n;
+    j.targets = targets;
+    j.label_logit = logit + r;
+    j.loss = c.loss ? c.loss + r : nullptr;
+    j.lse = c.lse ? c.lse + r : nullptr;
+    j.joined = joined;
+    j.all_sums = reinterpret_cast<double*>(scratch + at_sums);
+    j.all_counts = reinterpret_cast<int*>(scratch + at_counts);
+    j.sums = reinterpret_cast<double*>(scratch + at_sums) + r / kJoinRows;
+    j.counts = reinterpret_cast<int*>(scratch + at_counts) + r / kJoinRows;
+    j.all_targets = all;
+    j.all_rows = c.rows;
+    j.first = r == 0;
+    j.last = r + step >= c.rows;
+    j.mean = c.reduction == GEMM_F32_MEAN;
+    j.grad_scale = c.grad_scale;
+    j.factors = factors;
+    j.total = c.total;
+    j.arrived = reinterpret_cast<unsigned*>(scratch);
+    j.err = err;
+    rc = launch(loss_join_kernel, dim3((n + kJoinRows - 1) / kJoinRows), kJoinThreads, stream, launches, j);
     if (rc != GEMM_F32_OK) break;
     if (!grad) continue;
 
@@ -510,7 +563,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     const long long plane = f32 ? static_cast<long long>(step) * ld_exps : 0;
     rc = launch(f32 ? loss_rescale_kernel<3> : loss_rescale_kernel<1>, grid, kRescaleThreads, stream,
                 launches, static_cast<const float2*>(stats), ld_stats, piece_bits,
-                static_cast<const float2*>(joined), n, cols, band, static_cast<const int*>(labels + r),
+                static_cast<const float2*>(joined), n, cols, band, targets,
                 static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err);
     if (rc != GEMM_F32_OK) break;
 
@@ -558,9 +611,6 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
       rc = launch_half_gemm(d, stream, launches);
     }
   }
-  if (rc == GEMM_F32_OK && c.total)
-    rc = launch(loss_total_kernel, dim3(1), 1024, stream, launches, static_cast<const float*>(loss),
-                c.rows, static_cast<const Factors*>(factors), c.total);
   return rc;
 }
 

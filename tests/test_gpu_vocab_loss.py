@@ -104,7 +104,7 @@ def test_against_64_bits(rows, width, vocab, kind):
     x, w, y = _inputs(rows, width, vocab, kind, rows + width + vocab)
     exact = _exact(x, w, y, kind)
     got = g.vocab_loss(x, w, y)
-    assert g.gemm_f32_last_launches() >= 3
+    assert g.gemm_f32_last_launches() >= 2
     _check(got, exact)
     full = g.vocab_loss_grad(x, w, y)
     assert g.gemm_f32_status(None) == (0, 0)
