@@ -13,25 +13,14 @@ import torch
 from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, _stream, check, lib
 
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
+_F32 = torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream      # current_stream(i).cuda_stream, without the objects
 
 
-def _type(name, t):
-    if not t.is_cuda or t.dtype not in _TYPES:
-        raise ValueError("%s must be a float32 or bfloat16 CUDA tensor" % name)
-    return _TYPES[t.dtype]
-
-
-def _matrix(name, t, like=None):
-    """Row stride of a matrix operand, checked (against `like`: its shape, type and device)."""
-    if like is None:
-        _type(name, t)
-    elif t.dtype != like.dtype or t.device != like.device:
-        raise ValueError("%s must be a %s tensor on %s" % (name, like.dtype, like.device))
-    if t.dim() != 2 or (like is not None and t.shape != like.shape):
-        raise ValueError("%s must be a matrix%s" % (name, "" if like is None else " of shape %s" % (tuple(like.shape),)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _stride(name, t, width):
+    """Row stride of a matrix that is not contiguous."""
+    if width > 1 and t.stride(1) != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    width = max(1, t.shape[1])
     if t.shape[0] <= 1:
         return width
     if t.stride(0) < width:
@@ -39,24 +28,39 @@ def _matrix(name, t, like=None):
     return t.stride(0)
 
 
-def _vector(name, t, n, device, dtypes):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of %d elements on %s"
-                         % (name, " or ".join(str(d) for d in dtypes), n, device))
+def _matrix(name, t):
+    """(type, device index, rows, width, row stride) of an input matrix."""
+    kind = _TYPES.get(t.dtype)
+    if kind is None or not t.is_cuda:
+        raise ValueError("%s must be a float32 or bfloat16 CUDA tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    rows, width = t.shape
+    if width < 1:
+        raise ValueError("%s must have at least one column" % name)
+    return kind, t.get_device(), rows, width, width if t.is_contiguous() else _stride(name, t, width)
+
+
+def _like(name, t, x):
+    """Row stride of a matrix of x's shape, type and device."""
+    if t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != x.get_device():
+        raise ValueError("%s must be a %s matrix of shape %s on %s" % (name, x.dtype, tuple(x.shape), x.device))
+    return t.shape[1] if t.is_contiguous() else _stride(name, t, t.shape[1])
+
+
+def _vector(name, t, n, dev, dtypes):
+    """Address of a contiguous vector of n elements."""
+    if t.dtype not in dtypes or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on device %d"
+                         % (name, " or ".join(str(d) for d in dtypes), n, dev))
     return t.data_ptr()
 
 
-def _queue(stream, device):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
-
-
-def _weights(x, named):
-    """(their type, their addresses) of a norm's vectors: of one type, x's or float32; None gives address 0."""
-    given = [t for _, t in named if t is not None]
-    dtype = given[0].dtype if given else x.dtype
-    allowed = (dtype,) if dtype in (x.dtype, torch.float32) else (x.dtype, torch.float32)
-    at = [0 if t is None else _vector(n, t, x.shape[1], x.device, allowed) for n, t in named]
-    return dtype, at
+def _weight_type(x, weight):
+    dtype = weight.dtype
+    if dtype is not x.dtype and dtype is not _F32:
+        raise ValueError("weight and bias must hold x's type or float32")
+    return dtype
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
@@ -64,19 +68,25 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
 
     weight and bias hold x's type or float32 (None: 1 and 0); mean and rstd
     are float32, one value per row.  `out` may be x itself."""
-    ldx = _matrix("x", x)
-    if x.shape[1] < 1:
-        raise ValueError("x must have at least one column")
-    wtype, (pw, pb) = _weights(x, (("weight", weight), ("bias", bias)))
+    kind, dev, rows, width, ldx = _matrix("x", x)
+    wtype, pw, pb = x.dtype, 0, 0
+    if weight is not None:
+        wtype = _weight_type(x, weight)
+        pw = _vector("weight", weight, width, dev, (wtype,))
+    if bias is not None:
+        if weight is None:
+            wtype = _weight_type(x, bias)
+        pb = _vector("bias", bias, width, dev, (wtype,))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    ldo = _matrix("out", out, x)
-    rows, width = x.shape
-    mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    check(lib().gemm_f32_layer_norm(_TYPES[x.dtype], _TYPES[wtype], rows, width, x.data_ptr(), ldx, pw, pb, eps,
-                                    out.data_ptr(), ldo, mean.data_ptr(), rstd.data_ptr(),
-                                    _queue(stream, x.device)), "layer_norm")
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ldo = width
+    else:
+        ldo = _like("out", out, x)
+    mean = torch.empty(rows, dtype=_F32, device=x.device)
+    rstd = torch.empty_like(mean)
+    check(lib().gemm_f32_layer_norm(kind, _TYPES[wtype], rows, width, x.data_ptr(), ldx, pw, pb, eps, out.data_ptr(),
+                                    ldo, mean.data_ptr(), rstd.data_ptr(),
+                                    _raw_stream(dev) if stream is None else _stream(stream)), "layer_norm")
     return out, mean, rstd
 
 
@@ -86,41 +96,41 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, stream=None):
 
     dweight and dbias hold weight's type (float32 for weight None).  `out`,
     the tensor for dx, may be dy or x itself."""
-    ldx = _matrix("x", x)
-    if x.shape[1] < 1:
-        raise ValueError("x must have at least one column")
-    lddy = _matrix("dy", dy, x)
-    rows, width = x.shape
-    wtype, (pw,) = _weights(x, (("weight", weight),))
-    if weight is None:
-        wtype = torch.float32
-    f32 = (torch.float32,)
-    pm, pr = _vector("mean", mean, rows, x.device, f32), _vector("rstd", rstd, rows, x.device, f32)
+    kind, dev, rows, width, ldx = _matrix("x", x)
+    lddy = _like("dy", dy, x)
+    wtype, pw = _F32, 0
+    if weight is not None:
+        wtype = _weight_type(x, weight)
+        pw = _vector("weight", weight, width, dev, (wtype,))
+    pm, pr = _vector("mean", mean, rows, dev, (_F32,)), _vector("rstd", rstd, rows, dev, (_F32,))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    ldo = _matrix("out", out, x)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ldo = width
+    else:
+        ldo = _like("out", out, x)
     dweight = torch.empty(width, dtype=wtype, device=x.device)
-    dbias = torch.empty(width, dtype=wtype, device=x.device)
-    check(lib().gemm_f32_layer_norm_grad(_TYPES[x.dtype], _TYPES[wtype], rows, width, dy.data_ptr(), lddy,
-                                         x.data_ptr(), ldx, pw, pm, pr, out.data_ptr(), ldo, dweight.data_ptr(),
-                                         dbias.data_ptr(), _queue(stream, x.device)), "layer_norm_grad")
+    dbias = torch.empty_like(dweight)
+    check(lib().gemm_f32_layer_norm_grad(kind, _TYPES[wtype], rows, width, dy.data_ptr(), lddy, x.data_ptr(), ldx, pw,
+                                         pm, pr, out.data_ptr(), ldo, dweight.data_ptr(), dbias.data_ptr(),
+                                         _raw_stream(dev) if stream is None else _stream(stream)), "layer_norm_grad")
     return out, dweight, dbias
 
 
 def _loss_args(x, w, targets, reduction):
-    ldx, ldw = _matrix("x", x), _matrix("w", w)
-    if w.dtype != x.dtype or w.device != x.device or w.shape[1] != x.shape[1]:
-        raise ValueError("w must be a %s matrix on %s with x's %d columns" % (x.dtype, x.device, x.shape[1]))
-    if x.shape[1] < 1 or w.shape[0] < 1:
-        raise ValueError("x and w must have at least one column and w one row")
-    pt = _vector("targets", targets, x.shape[0], x.device, (torch.int64, torch.int32))
+    """The C call's arguments up to target_bits, the reduction's code, x's device and the outputs of both calls."""
+    kind, dev, rows, width, ldx = _matrix("x", x)
+    wkind, wdev, vocab, wwidth, ldw = _matrix("w", w)
+    if wkind != kind or wdev != dev or wwidth != width:
+        raise ValueError("w must be a %s matrix on %s with x's %d columns" % (x.dtype, x.device, width))
+    if vocab < 1:
+        raise ValueError("w must have at least one row")
+    pt = _vector("targets", targets, rows, dev, (torch.int64, torch.int32))
     if reduction not in REDUCTIONS:
         raise ValueError("reduction must be one of %s" % ", ".join(sorted(REDUCTIONS)))
-    loss = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-    lse = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-    total = torch.empty((), dtype=torch.float32, device=x.device)
-    return (_TYPES[x.dtype], x.shape[0], x.shape[1], w.shape[0], x.data_ptr(), ldx, w.data_ptr(), ldw, pt,
-            64 if targets.dtype == torch.int64 else 32), loss, lse, total
+    loss = torch.empty(rows, dtype=_F32, device=x.device)
+    return ((kind, rows, width, vocab, x.data_ptr(), ldx, w.data_ptr(), ldw, pt,
+             64 if targets.dtype is torch.int64 else 32), REDUCTIONS[reduction], dev, loss, torch.empty_like(loss),
+            torch.empty((), dtype=_F32, device=x.device))
 
 
 def vocab_loss(x, w, targets, ignore_index=-100, reduction="mean", stream=None):
@@ -131,9 +141,9 @@ def vocab_loss(x, w, targets, ignore_index=-100, reduction="mean", stream=None):
     is ignore_index), total their sum, or mean over the rows that count.  A
     target outside the vocabulary counts as ignored and is reported by
     gemm_f32_status()."""
-    args, loss, lse, total = _loss_args(x, w, targets, reduction)
-    check(lib().gemm_f32_vocab_loss(*args, ignore_index, REDUCTIONS[reduction], loss.data_ptr(), lse.data_ptr(),
-                                    total.data_ptr(), _queue(stream, x.device)), "vocab_loss")
+    args, code, dev, loss, lse, total = _loss_args(x, w, targets, reduction)
+    check(lib().gemm_f32_vocab_loss(*args, ignore_index, code, loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
+                                    _raw_stream(dev) if stream is None else _stream(stream)), "vocab_loss")
     return total, loss, lse
 
 
@@ -144,11 +154,11 @@ def vocab_loss_grad(x, w, targets, ignore_index=-100, reduction="mean", grad_sca
     dx and dw hold x's type; need_dx / need_dw False leaves one out (None).
     piece_bytes bounds the scratch that holds a piece of the rows (0: the
     library's default)."""
-    args, loss, lse, total = _loss_args(x, w, targets, reduction)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
-    dw = torch.empty(w.shape, dtype=w.dtype, device=w.device) if need_dw else None
-    check(lib().gemm_f32_vocab_loss_grad(*args, ignore_index, REDUCTIONS[reduction], grad_scale, loss.data_ptr(),
-                                         lse.data_ptr(), total.data_ptr(), dx.data_ptr() if need_dx else 0,
-                                         x.shape[1], dw.data_ptr() if need_dw else 0, x.shape[1], piece_bytes,
-                                         _queue(stream, x.device)), "vocab_loss_grad")
+    args, code, dev, loss, lse, total = _loss_args(x, w, targets, reduction)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+    dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
+    check(lib().gemm_f32_vocab_loss_grad(*args, ignore_index, code, grad_scale, loss.data_ptr(), lse.data_ptr(),
+                                         total.data_ptr(), dx.data_ptr() if need_dx else 0, args[2],
+                                         dw.data_ptr() if need_dw else 0, args[2], piece_bytes,
+                                         _raw_stream(dev) if stream is None else _stream(stream)), "vocab_loss_grad")
     return total, loss, lse, dx, dw

@@ -15,13 +15,17 @@
 // CTA, which a second kernel adds in CTA order (no atomics: the result does
 // not depend on timing).
 //
-// Rows wider than the registers hold (kMostWidth) take kernels that read x
-// again for each pass; rows that do not start on 16-byte boundaries are read
-// element by element.
+// Many rows on 16-byte boundaries are streamed: each group of threads keeps a
+// ring of rows in shared memory that bulk copies fill (cp.async.bulk on
+// mbarriers), so that the bytes in flight do not depend on registers.  Few
+// rows, and rows that do not start on 16-byte boundaries, are loaded by the
+// threads, the latter element by element.  Rows wider than the registers hold
+// take kernels that read x again for each pass.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -126,6 +130,169 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) layer_norm_kernel(const Nor
   }
 }
 
+// ---------------------------------------------------------------- streaming
+// One CTA of 512 threads (1024 for the widest gradients) per SM, and shared
+// memory for its rings.  Threads hold 32 elements of a row in the forward
+// pass and 16 in the gradient (8 where that takes 1024 threads: 8192 x 8192
+// fp32 131 us, with 16 137): what a row costs besides its elements (the
+// reductions, the barriers) is then paid by few warps, and the arithmetic is
+// done two elements at a time (f32x2).  With 8 elements a thread the issue of
+// instructions bound both kernels (65536 x 1024 bfloat16: 60 and 91 us).
+constexpr int stream_threads(int g) { return g < 512 ? 512 : g; }
+constexpr size_t kStreamBytes = 200 * 1024;
+constexpr int kMostStages = 8;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// The ring of one group: `arrays` rows per stage (x, or x and dy), filled for
+// rows first, first + step, ... of the group, `stages` ahead.
+template <class T, int G, int ARRAYS>
+struct RowRing {
+  const NormArgs& a;
+  uint8_t* data;
+  uint32_t bars, row_bytes;
+  int stages, s = 0;
+  uint32_t ph = 0;
+  bool lost = false;
+  long long next, step;
+
+  __device__ __forceinline__ RowRing(const NormArgs& args, uint8_t* smem, int group, int groups, int st)
+      : a(args), row_bytes(static_cast<uint32_t>(args.width * sizeof(T))), stages(st) {
+    data = smem + static_cast<size_t>(group) * st * ARRAYS * row_bytes;
+    bars = smem_addr(smem) + static_cast<uint32_t>(groups) * st * ARRAYS * row_bytes +
+           static_cast<uint32_t>(group) * st * 8u;
+    step = static_cast<long long>(gridDim.x) * groups;
+    next = static_cast<long long>(blockIdx.x) * groups + group;
+  }
+  // One thread of the group, before the group's first barrier.
+  __device__ __forceinline__ void init() {
+    for (int i = 0; i < stages; ++i) mbar_init(bars + 8u * i, 1);
+    fence_mbar_init();
+  }
+  // One thread: the copies of row `next` into stage `at`.
+  __device__ __forceinline__ void load(int at) {
+    if (next < a.rows) {
+      const uint32_t bar = bars + 8u * at;
+      const uint32_t dst = smem_addr(data) + static_cast<uint32_t>(at) * ARRAYS * row_bytes;
+      mbar_arrive_expect_tx(bar, ARRAYS * row_bytes);
+      bulk_load(dst, static_cast<const T*>(a.x) + next * a.ldx, row_bytes, bar);
+      if (ARRAYS == 2)
+        bulk_load(dst + row_bytes, static_cast<const T*>(a.dy) + next * a.lddy, row_bytes, bar);
+    }
+    next += step;
+  }
+  // A wait that runs out is recorded, and the thread goes on (the result is
+  // undefined, as the status says): the group's barriers need all of it.
+  __device__ __forceinline__ void wait() {
+    if (!lost) lost = !mbar_wait(bars + 8u * s, ph, a.err, kSiteTransformFull);
+  }
+  __device__ __forceinline__ const T* row(int array) const {
+    return reinterpret_cast<const T*>(data + (static_cast<size_t>(s) * ARRAYS + array) * row_bytes);
+  }
+  __device__ __forceinline__ void advance() {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// A thread's pairs of weight or bias (NV vectors of 16 / sizeof(T) elements).
+template <class T, class WT, int G, int NV>
+__device__ __forceinline__ void load_weights(const void* p, int width, int t, float none,
+                                             Pair (&w)[NV][8 / sizeof(T)]) {
+  constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int d = (i * G + t) * VEC;
+    float f[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = none;
+    if (p && d < width) load_cached<WT, VEC>(static_cast<const WT*>(p) + d, f);
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) w[i][j] = pair_of(f[2 * j], f[2 * j + 1]);
+  }
+}
+
+__device__ __forceinline__ float sum_of(Pair p) {
+  float a, b;
+  unpair(p, a, b);
+  return a + b;
+}
+
+template <class T, class WT, int G, int NV>
+__global__ void __launch_bounds__(stream_threads(G), 1)
+    layer_norm_stream_kernel(const NormArgs a, int stages) {
+  constexpr int kGroups = stream_threads(G) / G;
+  constexpr int VEC = 16 / static_cast<int>(sizeof(T)), NP = VEC / 2;
+  extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ float part[2][kGroups][G / 32];
+  const int group = threadIdx.x / G, t = threadIdx.x % G;
+  RowRing<T, G, 1> ring(a, smem_rows, group, kGroups, stages);
+  if (t == 0) ring.init();
+  __syncthreads();
+  grid_launch_dependents();
+  grid_dependency_wait();
+  long long row = ring.next;
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) ring.load(i);
+  const float inv = 1.0f / static_cast<float>(a.width);
+  Pair w[NV][NP], b[NV][NP];
+  load_weights<T, WT, G, NV>(a.weight, a.width, t, 1.0f, w);
+  load_weights<T, WT, G, NV>(a.bias, a.width, t, 0.0f, b);
+  for (; row < a.rows; row += ring.step) {
+    ring.wait();
+    Pair x[NV][NP], sum = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int d = (i * G + t) * VEC;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) x[i][j] = 0;
+      if (d < a.width) load_pairs<T>(ring.row(0) + d, x[i]);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) sum = add2(sum, x[i][j]);
+    }
+    float s[1] = {sum_of(sum)};
+    group_sum<1, G>(s, part[0][group], group);
+    if (t == 0) ring.load(ring.s);      // the group has read this stage
+    ring.advance();
+    const float mean = s[0] * inv;
+    const Pair minus = pair_of(-mean, -mean);
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if ((i * G + t) * VEC >= a.width) break;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        x[i][j] = add2(x[i][j], minus);
+        sum = fma2(x[i][j], x[i][j], sum);
+      }
+    }
+    s[0] = sum_of(sum);
+    group_sum<1, G>(s, part[1][group], group);
+    const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    const Pair by = pair_of(rstd, rstd);
+    T* const y = static_cast<T*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int d = (i * G + t) * VEC;
+      if (d >= a.width) break;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) x[i][j] = fma2(mul2(x[i][j], by), w[i][j], b[i][j]);
+      if (row_ok<T>(a, row * a.ldo + d, VEC, a.ldo)) store_pairs<T>(y + d, x[i]);
+    }
+  }
+}
+
 // Rows of any width: the row is read once for each of the three steps (from
 // L2 after the first).
 constexpr int kWideThreads = 1024;
@@ -171,6 +338,42 @@ __global__ void __launch_bounds__(kWideThreads) layer_norm_wide_kernel(const Nor
 // The next row's x and dy are loaded before the current row is reduced.
 template <int G>
 constexpr int kGradThreads = G < 512 ? 512 : G;
+
+// The groups' column sums, added in group order: one row of partials per CTA.
+// `cols` holds the sums of one array, kGroups G NV VEC floats.
+template <class T, int VEC, int G, int NV, int THREADS>
+__device__ __forceinline__ void write_columns(const NormArgs& a, float* cols, int group, int t,
+                                              const float (&dw)[NV][VEC], const float (&db)[NV][VEC]) {
+  constexpr int kGroups = THREADS / G, E = NV * VEC;
+  if (!a.partials) return;
+  float* const mine = a.partials + static_cast<size_t>(blockIdx.x) * 2 * a.width;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if constexpr (kGroups > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          cols[group * (G * E) + (i * G + t) * VEC + j] = which ? db[i][j] : dw[i][j];
+      __syncthreads();
+      for (int d = threadIdx.x; d < a.width; d += THREADS) {
+        float v = cols[d];
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) v += cols[g * (G * E) + d];
+        mine[which * a.width + d] = v;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int d = (i * G + t) * VEC;
+        if (d < a.width)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) mine[which * a.width + d + j] = which ? db[i][j] : dw[i][j];
+      }
+    }
+  }
+}
 
 template <class T, class WT, int VEC, int G, int NV>
 __global__ void __launch_bounds__(kGradThreads<G>) layer_norm_grad_kernel(const NormArgs a) {
@@ -260,35 +463,96 @@ __global__ void __launch_bounds__(kGradThreads<G>) layer_norm_grad_kernel(const 
     mean = mean_n;
     rstd = rstd_n;
   }
-  if (!a.partials) return;
-  // the groups' column sums, added in group order, one row of partials per CTA
-  float* const mine = a.partials + static_cast<size_t>(blockIdx.x) * 2 * a.width;
+  write_columns<T, VEC, G, NV, kThreads>(a, cols, group, t, dw, db);
+}
+
+template <class T, class WT, int G, int NV>
+__global__ void __launch_bounds__(stream_threads(G), 1)
+    layer_norm_grad_stream_kernel(const NormArgs a, int stages) {
+  constexpr int kThreads = stream_threads(G);
+  constexpr int kGroups = kThreads / G;
+  constexpr int VEC = 16 / static_cast<int>(sizeof(T)), NP = VEC / 2;
+  extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ float part[2][kGroups][2 * (G / 32)];
+  const int group = threadIdx.x / G, t = threadIdx.x % G;
+  RowRing<T, G, 2> ring(a, smem_rows, group, kGroups, stages);
+  if (t == 0) ring.init();
+  __syncthreads();
+  grid_launch_dependents();
+  grid_dependency_wait();
+  long long row = ring.next;
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) ring.load(i);
+  const float inv = 1.0f / static_cast<float>(a.width);
+  Pair w[NV][NP], dw[NV][NP], db[NV][NP];
+  load_weights<T, WT, G, NV>(a.weight, a.width, t, 1.0f, w);
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if constexpr (kGroups > 1) {
-      __syncthreads();
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+    for (int j = 0; j < NP; ++j) dw[i][j] = db[i][j] = 0;
+  int flip = 0;
+  float mean = 0.0f, rstd = 0.0f;
+  if (row < a.rows) {
+    mean = __ldg(a.mean + row);
+    rstd = __ldg(a.rstd + row);
+  }
+  for (; row < a.rows; row += ring.step) {
+    ring.wait();
+    float mean_n = 0.0f, rstd_n = 0.0f;      // the next row's, under this row's work
+    if (row + ring.step < a.rows) {
+      mean_n = __ldg(a.mean + row + ring.step);
+      rstd_n = __ldg(a.rstd + row + ring.step);
+    }
+    const Pair minus = pair_of(-mean, -mean), by = pair_of(rstd, rstd);
+    Pair hat[NV][NP], g[NV][NP], sg = 0, sgh = 0;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          cols[group * (G * E) + (i * G + t) * VEC + j] = which ? db[i][j] : dw[i][j];
-      __syncthreads();
-      for (int d = threadIdx.x; d < a.width; d += kThreads) {
-        float v = cols[d];
+    for (int i = 0; i < NV; ++i) {
+      const int d = (i * G + t) * VEC;
+      if (d >= a.width) break;
+      load_pairs<T>(ring.row(0) + d, hat[i]);
+      load_pairs<T>(ring.row(1) + d, g[i]);
 #pragma unroll
-        for (int g = 1; g < kGroups; ++g) v += cols[g * (G * E) + d];
-        mine[which * a.width + d] = v;
+      for (int j = 0; j < NP; ++j) {
+        hat[i][j] = mul2(add2(hat[i][j], minus), by);
+        dw[i][j] = fma2(g[i][j], hat[i][j], dw[i][j]);
+        db[i][j] = add2(db[i][j], g[i][j]);
+        g[i][j] = mul2(g[i][j], w[i][j]);
+        sg = add2(sg, g[i][j]);
+        sgh = fma2(g[i][j], hat[i][j], sgh);
       }
-    } else {
+    }
+    float s[2] = {sum_of(sg), sum_of(sgh)};
+    group_sum<2, G>(s, part[flip][group], group);
+    flip ^= 1;
+    if (t == 0) ring.load(ring.s);           // the group has read this stage
+    ring.advance();
+    if (a.out) {
+      const float c1 = -s[0] * inv, c2 = -s[1] * inv;
+      const Pair minus_c1 = pair_of(c1, c1), minus_c2 = pair_of(c2, c2);
+      T* const dx = static_cast<T*>(a.out) + row * a.ldo;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int d = (i * G + t) * VEC;
-        if (d < a.width)
+        if (d >= a.width) break;
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) mine[which * a.width + d + j] = which ? db[i][j] : dw[i][j];
+        for (int j = 0; j < NP; ++j)
+          g[i][j] = mul2(fma2(hat[i][j], minus_c2, add2(g[i][j], minus_c1)), by);
+        if (row_ok<T>(a, row * a.ldo + d, VEC, a.ldo)) store_pairs<T>(dx + d, g[i]);
       }
     }
+    mean = mean_n;
+    rstd = rstd_n;
   }
+  __syncthreads();                           // the rings become the groups' column sums
+  float fw[NV][VEC], fb[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      unpair(dw[i][j], fw[i][2 * j], fw[i][2 * j + 1]);
+      unpair(db[i][j], fb[i][2 * j], fb[i][2 * j + 1]);
+    }
+  write_columns<T, VEC, G, NV, kThreads>(a, reinterpret_cast<float*>(smem_rows), group, t, fw, fb);
 }
 
 // dweight and dbias: the sums over `count` rows of partials, 32 columns per
@@ -404,12 +668,72 @@ int launch_forward(const NormArgs& a, cudaStream_t stream) {
                 stream, a);
 }
 
+// Rows per group of a full grid from which on the streaming kernels are taken.
+constexpr int kStreamRows = 4;
+
+// Launches a streaming kernel when the rows are many; 1 when they are not.
+template <int G, int ARRAYS, class Kernel>
+int launch_stream(Kernel kernel, const NormArgs& a, size_t size, size_t least_smem, int device,
+                  int num_sms, int* ctas, cudaStream_t stream) {
+  constexpr int kGroups = stream_threads(G) / G;
+  const int grid = num_sms;
+  const size_t row = static_cast<size_t>(a.width) * size * ARRAYS;
+  const int stages = static_cast<int>(std::min<size_t>(kMostStages, kStreamBytes / (kGroups * (row + 8))));
+  if (a.rows < static_cast<long long>(kStreamRows) * grid * kGroups || stages < 2) return 1;
+  const size_t smem = std::max(least_smem, kGroups * stages * (row + 8));
+  static std::atomic<unsigned long long> configured{0};   // bit per device
+  const unsigned long long bit = 1ull << (device % 64);
+  if (!(configured.load() & bit)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kStreamBytes)) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return GEMM_F32_ELAUNCH;
+    }
+    configured.fetch_or(bit);
+  }
+  *ctas = grid;
+  if (launch_dependent(kernel, dim3(grid), dim3(stream_threads(G)), smem, stream, a, stages) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return GEMM_F32_ELAUNCH;
+  }
+  return GEMM_F32_OK;
+}
+
+template <class T, class WT, int G, int NV>
+int stream_forward(const NormArgs& a, int device, int num_sms, cudaStream_t stream) {
+  int ctas;
+  return launch_stream<G, 1>(layer_norm_stream_kernel<T, WT, G, NV>, a, sizeof(T), 0, device, num_sms,
+                             &ctas, stream);
+}
+
+template <class T, class WT, int G, int NV>
+int stream_grad(NormArgs a, float* scratch, int device, int num_sms, int* ctas, cudaStream_t stream) {
+  a.partials = scratch;
+  constexpr size_t kColumns = sizeof(float) * stream_threads(G) * NV * (16 / sizeof(T));
+  return launch_stream<G, 2>(layer_norm_grad_stream_kernel<T, WT, G, NV>, a, sizeof(T), kColumns, device,
+                             num_sms, ctas, stream);
+}
+
 // The narrowest group of threads whose registers hold the row: up to 4
 // vectors a thread, or 8 elements where they are read one by one.
 template <class T, class WT>
-int forward(const NormArgs& a, bool vectors, int num_sms, cudaStream_t stream) {
+int forward(const NormArgs& a, bool vectors, int device, int num_sms, cudaStream_t stream) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
+  constexpr int N = 8 / V;                 // vectors of 8 elements
   const int n = vectors ? (a.width + V - 1) / V : a.width;
+  if (vectors) {
+    const int e = a.width;
+    const int rc = e <= 256     ? stream_forward<T, WT, 32, N>(a, device, num_sms, stream)
+                   : e <= 512   ? stream_forward<T, WT, 32, 2 * N>(a, device, num_sms, stream)
+                   : e <= 1024  ? stream_forward<T, WT, 32, 4 * N>(a, device, num_sms, stream)
+                   : e <= 2048  ? stream_forward<T, WT, 64, 4 * N>(a, device, num_sms, stream)
+                   : e <= 4096  ? stream_forward<T, WT, 128, 4 * N>(a, device, num_sms, stream)
+                   : e <= 8192  ? stream_forward<T, WT, 256, 4 * N>(a, device, num_sms, stream)
+                   : e <= 16384 ? stream_forward<T, WT, 512, 4 * N>(a, device, num_sms, stream)
+                                : 1;
+    if (rc != 1) return rc;
+  }
   if (vectors) {
     if (n <= 32) return launch_forward<T, WT, V, 32, 1>(a, stream);
     if (n <= 64) return launch_forward<T, WT, V, 32, 2>(a, stream);
@@ -465,7 +789,19 @@ int grad(NormArgs a, bool vectors, void* dweight, void* dbias, int device, int n
   if (a.rows == 0) {
     rc = GEMM_F32_OK;
   } else if (!wide) {
-    if (vectors && V == 8) {
+    constexpr int N = 8 / V;
+    const int e = a.width;
+    rc = !vectors     ? 1
+         : e <= 256   ? stream_grad<T, WT, 32, N>(a, parts, device, num_sms, &ctas, stream)
+         : e <= 512   ? stream_grad<T, WT, 32, 2 * N>(a, parts, device, num_sms, &ctas, stream)
+         : e <= 1024  ? stream_grad<T, WT, 64, 2 * N>(a, parts, device, num_sms, &ctas, stream)
+         : e <= 2048  ? stream_grad<T, WT, 128, 2 * N>(a, parts, device, num_sms, &ctas, stream)
+         : e <= 4096  ? stream_grad<T, WT, 256, 2 * N>(a, parts, device, num_sms, &ctas, stream)
+         : e <= 8192  ? stream_grad<T, WT, 1024, N>(a, parts, device, num_sms, &ctas, stream)
+         : e <= 16384 ? stream_grad<T, WT, 1024, 2 * N>(a, parts, device, num_sms, &ctas, stream)
+                      : 1;
+    if (rc != 1) {
+    } else if (vectors && V == 8) {
       if (n <= 32) rc = launch_grad<T, WT, V, 32, 1>(a, parts, num_sms, &ctas, stream);
       else if (n <= 64) rc = launch_grad<T, WT, V, 32, 2>(a, parts, num_sms, &ctas, stream);
       else if (n <= 128) rc = launch_grad<T, WT, V, 128, 1>(a, parts, num_sms, &ctas, stream);
@@ -592,11 +928,11 @@ extern "C" int gemm_f32_layer_norm(int type, int weight_type, long long rows, in
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
   int rc;
   if (type == GEMM_F32_TYPE_F32)
-    rc = forward<float, float>(a, vectors, num_sms, stream);
+    rc = forward<float, float>(a, vectors, device, num_sms, stream);
   else if (weight_type == GEMM_F32_TYPE_F32)
-    rc = forward<bf16, float>(a, vectors, num_sms, stream);
+    rc = forward<bf16, float>(a, vectors, device, num_sms, stream);
   else
-    rc = forward<bf16, bf16>(a, vectors, num_sms, stream);
+    rc = forward<bf16, bf16>(a, vectors, device, num_sms, stream);
   if (rc == GEMM_F32_OK) note_launches(1, "layer_norm_kernel");
   return rc;
 }

@@ -68,6 +68,49 @@ struct Raw {
   }
 };
 
+// Two fp32 values in one 64-bit register: the packed operations do both in
+// one instruction, each rounded to nearest as by itself.
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ void unpair(Pair p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The 16 bytes at p (shared or global memory) as pairs: 2 of fp32, 4 of bfloat16.
+template <class T>
+__device__ __forceinline__ void load_pairs(const T* p, Pair (&v)[8 / sizeof(T)]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (sizeof(T) == 4) {
+    v[0] = pair_of(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    v[1] = pair_of(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = pair_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+}
+
 // N consecutive elements as fp32, through the cache (weights that every row reads).
 template <class T, int N>
 __device__ __forceinline__ void load_cached(const T* p, float (&v)[N]) {
@@ -112,6 +155,15 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[N]) {
       reinterpret_cast<uint4*>(p)[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
   }
+}
+
+template <class T>
+__device__ __forceinline__ void store_pairs(T* p, const Pair (&v)[8 / sizeof(T)]) {
+  constexpr int N = 8 / sizeof(T);
+  float f[2 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) unpair(v[i], f[2 * i], f[2 * i + 1]);
+  store_vec<T, 2 * N>(p, f);
 }
 
 // The label of a row of a loss: its target, or -1 where the row does not
