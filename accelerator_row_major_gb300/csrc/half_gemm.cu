@@ -9,7 +9,7 @@
 // operand byte a CTA loads feeds 256 multiply-adds, half the loads of a
 // 128 x 256 tile per CTA.  Operands come by TMA in 128-byte swizzled slices
 // 64 deep along K, K-major or MN-major as they are stored (the MMA reads
-// either, so nothing is ever transposed), six stages of 32 KB in flight.
+// either, so nothing is ever transposed), five stages of 32 KB in flight.
 // The accumulator is double buffered (2 x 256 of the 512 columns of tensor
 // memory), so a tile's epilogue runs under the next tile's MMAs.
 //
@@ -56,14 +56,15 @@ namespace {
 constexpr int kHalf = 128;               // rows of A and of B per CTA
 constexpr int kTile = 256;
 constexpr int kBK = 64;                  // 128 bytes of K per stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOperandBytes = kHalf * kBK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStagingBytes = 4096;      // per epilogue warp: 32 rows of 128 bytes
+constexpr int kStagingBytes = 4096;      // 32 rows of 128 bytes; two per epilogue warp
+constexpr int kStagingBuffers = 2;
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarp0 = 4;
 constexpr int kEpilogueWarps = 8;
-constexpr int kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStagingBytes + 1024;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStagingBuffers * kStagingBytes + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 constexpr int kTmemCols = 512;
 constexpr int kRasterGroup = 8;
@@ -126,12 +127,15 @@ __device__ __forceinline__ void tma_store(const void* desc, uint32_t src, int x,
       "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(desc),
       "r"(src), "r"(x), "r"(y)
       : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// This thread's stores have read their shared memory / have been made.
+// All but this thread's latest group of stores have read their shared memory
+// / all have been made.
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -272,13 +276,17 @@ template <class T>
 __device__ __forceinline__ void write_staged(const Params& p, const void* tmC, const uint8_t* buf,
                                              int lane, int row0, int col0) {
   constexpr int kCols = 128 / static_cast<int>(sizeof(T)), kPer = 16 / static_cast<int>(sizeof(T));
-  if (row0 >= p.M || col0 >= p.N) return;
+  const bool any = row0 < p.M && col0 < p.N;
   if (p.c_tma) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) tma_store(tmC, smem_addr(buf), col0, row0);
+    if (lane == 0) {
+      if (any) tma_store(tmC, smem_addr(buf), col0, row0);
+      tma_store_commit();   // one group per block, empty or not: the waits count groups
+    }
     return;
   }
+  if (!any) return;
   __syncwarp();
   T* const c = static_cast<T*>(p.c);
   const int rows = min(32, p.M - row0);
@@ -303,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t base = (dyn0 + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_dyn + (base - dyn0);
   uint8_t* const staging = base_ptr + S * kStageBytes;
-  const uint32_t bars = base + S * kStageBytes + kEpilogueWarps * kStagingBytes;
+  const uint32_t bars = base + S * kStageBytes + kEpilogueWarps * kStagingBuffers * kStagingBytes;
   auto full_bar = [&](int s) { return bars + 8u * s; };          // both CTAs' bytes (even CTA's)
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };   // MMAs done with the stage
   auto accf_bar = [&](int b) { return bars + 8u * (2 * S + b); };      // accumulator complete
@@ -491,8 +499,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       buf ^= 1;
       if (buf == 0) acc_ph ^= 1u;
     };
-    uint8_t* const stage = staging + (warp - kEpilogueWarp0) * kStagingBytes;
-    auto stage_free = [&]() {   // the buffer's last store has read it
+    uint8_t* const stages = staging + (warp - kEpilogueWarp0) * (kStagingBuffers * kStagingBytes);
+    uint8_t* stage = stages;
+    auto stage_free = [&]() {   // on to the other buffer, whose last store has read it
+      stage = stage == stages ? stages + kStagingBytes : stages;
       if (lane == 0) tma_store_wait_read();
       __syncwarp();
     };
