@@ -495,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto release = [&]() {
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_acce0 + 8u * buf);
+      if (lane == 0) mbar_arrive_pair(leader_acce0 + 8u * buf);
       buf ^= 1;
       if (buf == 0) acc_ph ^= 1u;
     };
@@ -536,8 +536,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         if (!wait_full()) break;
       }
-      // 32 columns of this thread's row
-      auto take = [&](int ch, float(&v)[32]) {
+      // 32 columns of this thread's row; the last load frees the accumulator
+      auto take = [&](int ch, float(&v)[32], bool last) {
         if constexpr (SUM != 0) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = acc[ch * 32 + j];
@@ -545,6 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t u[32];
           tmem_ld_32cols(t_mine + static_cast<uint32_t>(buf * kTile + ch * 32), u);
           tmem_wait_ld();
+          if (last) release();
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
         }
@@ -557,14 +558,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
             float v[32];
-            take(ch, v);
+            take(ch, v, ch == 3);
             store_vec<float, 32>(part + ch * 32, v);
           }
         } else {
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
             float v[32];
-            take(ch, v);
+            take(ch, v, ch == 3);
             finish_c<32>(p, row, n0 + ch * 32, scale, v);
             if (EPI == kStoreF32 || ch % 2 == 0) stage_free();
             if constexpr (EPI == kStoreF32) {
@@ -583,7 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           float v[32];
-          take(ch, v);
+          take(ch, v, false);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (n0 + ch * 32 + j < p.N) top = fmaxf(top, v[j]);
@@ -597,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           float v[32];
-          take(ch, v);
+          take(ch, v, ch == 3);
           if (__any_sync(0xFFFFFFFFu, label >= ch * 32 && label < ch * 32 + 32)) {
             float z = 0.0f;
 #pragma unroll
@@ -624,7 +625,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           p.stats[static_cast<size_t>(2 * c.tn + half) * p.ld_stats + row] =
               make_float2(m2, PARTS == 3 ? sum : sum * (1.0f / 32768.0f));
       }
-      if constexpr (SUM == 0) release();
     }
     if (lane == 0) tma_store_wait();
   }

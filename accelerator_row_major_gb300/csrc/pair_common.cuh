@@ -33,6 +33,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same with release at CTA scope, for an arrive that publishes nothing
+// written to memory (a drained accumulator: its loads have completed).  A
+// release at cluster scope waits for every store the thread has in flight.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 // Non-blocking test: the waits below spin on it, since a blocking try_wait
 // on a barrier that another SM arrives on was measured to wake late.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
