@@ -219,7 +219,7 @@ __device__ __forceinline__ void logits_out(const FewParams& p, int piece, int la
     const float top = warp_max(z);
     // nothing above -inf: any finite reference gives powers of 0
     m2[j] = top == -INFINITY ? 0.0f : top * kLog2e;
-    e[j] = exp2f(fmaf(z, kLog2e, kUp - m2[j]));
+    e[j] = exp2_approx(fmaf(z, kLog2e, kUp - m2[j]));
   }
 #pragma unroll
   for (int j = 0; j < 16; ++j) {

@@ -232,6 +232,12 @@ __device__ __forceinline__ void finish_c(const Params& p, int row, int col, floa
   }
 }
 
+// Columns from `valid` on become -inf (a power of 0).
+__device__ __forceinline__ void mask_columns(float (&v)[32], int valid) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = j < valid ? v[j] : -INFINITY;
+}
+
 // 16-byte chunk c of row r of a staging buffer (32 rows of 128 bytes in the
 // 128-byte swizzle that TMA undoes).
 __device__ __forceinline__ uint32_t staged(int r, int c) {
@@ -580,25 +586,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         const bool row_ok = row < p.M;
+        const bool whole = n0 + kHalf <= p.N;      // else columns from N on are masked
         float top = -INFINITY;
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           float v[32];
           take(ch, v, false);
+          if (!whole) mask_columns(v, p.N - n0 - ch * 32);
+          float t[4] = {v[0], v[1], v[2], v[3]};   // four chains
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (n0 + ch * 32 + j < p.N) top = fmaxf(top, v[j]);
+          for (int j = 4; j < 32; ++j) t[j % 4] = fmaxf(t[j % 4], v[j]);
+          top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
         }
         // nothing above -inf: any finite reference gives powers of 0
         const float m2 = top == -INFINITY ? 0.0f : top * kLog2e;
         const int label = row_ok ? label_at(p.targets, row) - n0 : -1;
         // one part: powers times 2^15, which keep their 11 bits in fp16 down to 2^-29
         constexpr float kUp = PARTS == 3 ? 0.0f : 15.0f;
-        float sum = 0.0f;
+        const Pair by = pair_of(kLog2e, kLog2e), minus = pair_of(kUp - m2, kUp - m2);
+        Pair sums = 0;
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           float v[32];
           take(ch, v, ch == 3);
+          if (!whole) mask_columns(v, p.N - n0 - ch * 32);
           if (__any_sync(0xFFFFFFFFu, label >= ch * 32 && label < ch * 32 + 32)) {
             float z = 0.0f;
 #pragma unroll
@@ -606,9 +617,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (label >= ch * 32 && label < ch * 32 + 32) p.label_logit[row] = z;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            v[j] = n0 + ch * 32 + j < p.N ? exp2f(fmaf(v[j], kLog2e, kUp - m2)) : 0.0f;
-            sum += v[j];
+          for (int j = 0; j < 32; j += 2) {
+            unpair(fma2(pair_of(v[j], v[j + 1]), by, minus), v[j], v[j + 1]);
+            v[j] = exp2_approx(v[j]);
+            v[j + 1] = exp2_approx(v[j + 1]);
+            sums = add2(sums, pair_of(v[j], v[j + 1]));
           }
           if (p.exps) {   // C is the matrix of exponentials: fp32, or fp16
             if (PARTS == 3 || ch % 2 == 0) stage_free();
@@ -623,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (row_ok)
           p.stats[static_cast<size_t>(2 * c.tn + half) * p.ld_stats + row] =
-              make_float2(m2, PARTS == 3 ? sum : sum * (1.0f / 32768.0f));
+              make_float2(m2, PARTS == 3 ? sum_of(sums) : sum_of(sums) * (1.0f / 32768.0f));
       }
     }
     if (lane == 0) tma_store_wait();

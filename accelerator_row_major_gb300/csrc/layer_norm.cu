@@ -219,12 +219,6 @@ __device__ __forceinline__ void load_weights(const void* p, int width, int t, fl
   }
 }
 
-__device__ __forceinline__ float sum_of(Pair p) {
-  float a, b;
-  unpair(p, a, b);
-  return a + b;
-}
-
 template <class T, class WT, int G, int NV>
 __global__ void __launch_bounds__(stream_threads(G), 1)
     layer_norm_stream_kernel(const NormArgs a, int stages) {

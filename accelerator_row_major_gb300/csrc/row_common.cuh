@@ -96,6 +96,19 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   return d;
 }
 
+__device__ __forceinline__ float sum_of(Pair p) {
+  float a, b;
+  unpair(p, a, b);
+  return a + b;
+}
+
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The 16 bytes at p (shared or global memory) as pairs: 2 of fp32, 4 of bfloat16.
 template <class T>
 __device__ __forceinline__ void load_pairs(const T* p, Pair (&v)[8 / sizeof(T)]) {

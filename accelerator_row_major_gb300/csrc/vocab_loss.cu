@@ -64,8 +64,9 @@ struct Factors {
 // The CTA that finishes last adds up what the call needs of all rows: the
 // factors (in the first piece of the rows) and the total (in the last), from
 // the CTAs' partial sums in a fixed order.
-constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;
+constexpr int kJoinThreads = 256;      // 1024 where the rows alone leave SMs idle
+constexpr int kJoinThreadsFew = 1024;
 
 struct JoinArgs {
   const float2* stats;
@@ -91,8 +92,9 @@ struct JoinArgs {
   unsigned* err;
 };
 
-__global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const JoinArgs a) {
-  constexpr int kChains = kJoinThreads / kJoinRows, kWarps = kJoinThreads / 32;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
+  constexpr int kChains = THREADS / kJoinRows, kWarps = THREADS / 32;
   __shared__ float tops[kWarps][kJoinRows], sums[kWarps][kJoinRows];
   __shared__ double part_sum[kWarps];
   __shared__ int part_count[kWarps];
@@ -166,12 +168,12 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const JoinArgs 
   int n = 0;
   if (a.first && !a.last) {   // later pieces of the rows are not joined yet
 #pragma unroll 8
-    for (unsigned t = threadIdx.x; t < static_cast<unsigned>(a.all_rows); t += kJoinThreads)
+    for (unsigned t = threadIdx.x; t < static_cast<unsigned>(a.all_rows); t += THREADS)
       n += label_at(a.all_targets, t) >= 0;
   } else {
     const int groups = (a.all_rows - 1) / kJoinRows + 1;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < groups; i += kJoinThreads) {
+    for (int i = threadIdx.x; i < groups; i += THREADS) {
       s += __ldcg(a.all_sums + i);
       n += __ldcg(a.all_counts + i);
     }
@@ -549,7 +551,10 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     j.total = c.total;
     j.arrived = reinterpret_cast<unsigned*>(scratch);
     j.err = err;
-    rc = launch(loss_join_kernel, dim3((n + kJoinRows - 1) / kJoinRows), kJoinThreads, stream, launches, j);
+    const int join_ctas = (n + kJoinRows - 1) / kJoinRows;
+    rc = join_ctas <= num_sms
+             ? launch(loss_join_kernel<kJoinThreadsFew>, dim3(join_ctas), kJoinThreadsFew, stream, launches, j)
+             : launch(loss_join_kernel<kJoinThreads>, dim3(join_ctas), kJoinThreads, stream, launches, j);
     if (rc != GEMM_F32_OK) break;
     if (!grad) continue;
 
