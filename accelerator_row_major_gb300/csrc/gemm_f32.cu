@@ -255,7 +255,8 @@ void* gemm_f32_impl::acquire_scratch(int device, cudaStream_t stream, size_t byt
     Workspace& w = st.ws[stream];
     const void* const before = w.scratch;
     void* const p = grow_buffer(&w.scratch, &w.scratch_bytes, bytes + kScratchHeader);
-    if (p && (p != before) && cudaMemset(p, 0, kScratchHeader) != cudaSuccess) {
+    if (p && p != before &&
+        (cudaMemset(p, 0, kScratchHeader) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)) {
       (void)cudaGetLastError();
       (void)cudaFree(p);
       w.scratch = nullptr;

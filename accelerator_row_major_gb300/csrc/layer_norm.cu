@@ -221,7 +221,7 @@ __device__ __forceinline__ void load_weights(const void* p, int width, int t, fl
 
 template <class T, class WT, int G, int NV>
 __global__ void __launch_bounds__(stream_threads(G), 1)
-    layer_norm_stream_kernel(const NormArgs a, int stages) {
+    layer_norm_stream_kernel(NormArgs a, int stages) {
   constexpr int kGroups = stream_threads(G) / G;
   constexpr int VEC = 16 / static_cast<int>(sizeof(T)), NP = VEC / 2;
   extern __shared__ __align__(128) uint8_t smem_rows[];
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kGradThreads<G>) layer_norm_grad_kernel(const 
 
 template <class T, class WT, int G, int NV>
 __global__ void __launch_bounds__(stream_threads(G), 1)
-    layer_norm_grad_stream_kernel(const NormArgs a, int stages) {
+    layer_norm_grad_stream_kernel(NormArgs a, int stages) {
   constexpr int kThreads = stream_threads(G);
   constexpr int kGroups = kThreads / G;
   constexpr int VEC = 16 / static_cast<int>(sizeof(T)), NP = VEC / 2;
@@ -666,8 +666,8 @@ int launch_forward(const NormArgs& a, cudaStream_t stream) {
 constexpr int kStreamRows = 4;
 
 // Launches a streaming kernel when the rows are many; 1 when they are not.
-template <int G, int ARRAYS, class Kernel>
-int launch_stream(Kernel kernel, const NormArgs& a, size_t size, size_t least_smem, int device,
+template <int G, int ARRAYS, void (*kernel)(NormArgs, int)>
+int launch_stream(const NormArgs& a, size_t size, size_t least_smem, int device,
                   int num_sms, int* ctas, cudaStream_t stream) {
   constexpr int kGroups = stream_threads(G) / G;
   const int grid = num_sms;
@@ -675,7 +675,7 @@ int launch_stream(Kernel kernel, const NormArgs& a, size_t size, size_t least_sm
   const int stages = static_cast<int>(std::min<size_t>(kMostStages, kStreamBytes / (kGroups * (row + 8))));
   if (a.rows < static_cast<long long>(kStreamRows) * grid * kGroups || stages < 2) return 1;
   const size_t smem = std::max(least_smem, kGroups * stages * (row + 8));
-  static std::atomic<unsigned long long> configured{0};   // bit per device
+  static std::atomic<unsigned long long> configured{0};   // of this kernel: a bit per device
   const unsigned long long bit = 1ull << (device % 64);
   if (!(configured.load() & bit)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -697,16 +697,16 @@ int launch_stream(Kernel kernel, const NormArgs& a, size_t size, size_t least_sm
 template <class T, class WT, int G, int NV>
 int stream_forward(const NormArgs& a, int device, int num_sms, cudaStream_t stream) {
   int ctas;
-  return launch_stream<G, 1>(layer_norm_stream_kernel<T, WT, G, NV>, a, sizeof(T), 0, device, num_sms,
-                             &ctas, stream);
+  return launch_stream<G, 1, layer_norm_stream_kernel<T, WT, G, NV>>(a, sizeof(T), 0, device, num_sms, &ctas,
+                                                                     stream);
 }
 
 template <class T, class WT, int G, int NV>
 int stream_grad(NormArgs a, float* scratch, int device, int num_sms, int* ctas, cudaStream_t stream) {
   a.partials = scratch;
   constexpr size_t kColumns = sizeof(float) * stream_threads(G) * NV * (16 / sizeof(T));
-  return launch_stream<G, 2>(layer_norm_grad_stream_kernel<T, WT, G, NV>, a, sizeof(T), kColumns, device,
-                             num_sms, ctas, stream);
+  return launch_stream<G, 2, layer_norm_grad_stream_kernel<T, WT, G, NV>>(a, sizeof(T), kColumns, device, num_sms,
+                                                                          ctas, stream);
 }
 
 // The narrowest group of threads whose registers hold the row: up to 4

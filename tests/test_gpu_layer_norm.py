@@ -109,6 +109,21 @@ def test_many_rows(rows, width, kind):
     assert all(torch.equal(a, c) for a, c in zip((dx, dw, db), again))   # a fixed order of sums
 
 
+@pytest.mark.parametrize("kind,wkind", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_streamed_rows_of_every_width(kind, wkind):
+    """Enough rows for the streaming kernels at each of their widths, in one process and in this order:
+    every kernel sets up its own shared memory."""
+    g = lib()
+    for width in (1024, 256, 8, 512, 264, 2048, 1032, 4096, 8192, 4104, 16384, 8200):
+        rows = max(700, 20000 * 128 // width)
+        x, dy, w, b = _inputs(rows, width, kind, wkind, width)
+        y, mean, rstd = g.layer_norm(x, w, b)
+        _check_forward(x, w, b, 1e-5, y, mean, rstd, kind)
+        dx, dw, db = g.layer_norm_grad(dy, x, w, mean, rstd)
+        _check_grad(x, dy, w, mean, rstd, dx, dw, db, kind, wkind)
+        assert g.gemm_f32_status(None) == (0, 0)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("width,pad,first", [(256, 8, 0), (256, 1, 0), (96, 5, 3), (1000, 16, 8), (9000, 7, 1)])
 def test_strided_rows(width, pad, first, kind):

@@ -93,7 +93,8 @@ def _check(got, exact, names=("total", "loss", "lse", "dx", "dw")):
 
 
 SHAPES = [(1, 1, 1), (1, 8, 2), (2, 64, 100), (3, 100, 257), (1, 4096, 1000), (37, 777, 1001), (129, 64, 128),
-          (256, 256, 256), (257, 72, 513), (300, 520, 5003), (64, 4096, 2048), (513, 33, 3001), (1000, 1024, 2000)]
+          (256, 256, 256), (257, 72, 513), (300, 520, 5003), (64, 4096, 2048), (513, 33, 3001), (1000, 1024, 2000),
+          (128, 200, 1000), (200, 2500, 1111), (17, 5000, 700), (129, 8, 5), (2049, 16, 40)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
