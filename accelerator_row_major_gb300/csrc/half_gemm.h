@@ -61,7 +61,11 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
 // what takes the time (few_gemm.cu).  w is read as it is stored, fp32
 // included (f32: its three parts are made on the way to the tensor cores);
 // its rows start on 16-byte boundaries.
-constexpr int kFewRows = 128;
+constexpr int kFewRows = 128;     // fp32: the pair kernel would first store w in three parts
+                                  // (64 x 4096 x 65536 920 us against 250)
+constexpr int kFewRowsBf16 = 32;  // 4096 x 65536: 105 us against the pair kernel's 175 with one
+                                  // row, 111 each with 32, 116 against 111 with 64, 137 against
+                                  // 113 with 128
 constexpr int kFewPiece = 32;     // columns per statistic of its logits
 
 struct FewGemm {

@@ -423,7 +423,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   unsigned* err = nullptr;
   if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
   const bool f32 = c.type == GEMM_F32_TYPE_F32, grad = c.dx || c.dw;
-  const bool few = c.rows <= kFewRows;
+  const bool few = c.rows <= (f32 ? kFewRows : kFewRowsBf16);
   const int parts = f32 ? 3 : 1;
   const long long ld_exps = static_cast<long long>(round_up(c.vocab, 256));
   const int piece_bits = few ? kFewPieceBits : kPieceBits;
