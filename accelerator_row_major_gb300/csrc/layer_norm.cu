@@ -15,12 +15,12 @@
 // CTA, which a second kernel adds in CTA order (no atomics: the result does
 // not depend on timing).
 //
-// Many rows on 16-byte boundaries are streamed: each group of threads keeps a
-// ring of rows in shared memory that bulk copies fill (cp.async.bulk on
-// mbarriers), so that the bytes in flight do not depend on registers.  Few
-// rows, and rows that do not start on 16-byte boundaries, are loaded by the
-// threads, the latter element by element.  Rows wider than the registers hold
-// take kernels that read x again for each pass.
+// Many rows are streamed (layer_norm_stream.cuh): each group of threads keeps
+// a ring of rows in shared memory that bulk copies fill, so that the bytes in
+// flight do not depend on registers.  Few rows are loaded by the threads
+// here, element by element where they do not start on 16-byte boundaries.
+// Rows wider than the registers hold take kernels that read x again for each
+// pass.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,37 +32,13 @@
 #include "../../include/gemm_f32_lm.h"
 #include "device_common.cuh"
 #include "launch.h"
+#include "layer_norm_stream.cuh"
 #include "row_common.cuh"
 
 namespace gemm_f32_impl {
 using namespace gemm_f32_dev;
 
 namespace {
-
-using bf16 = __nv_bfloat16;
-
-struct NormArgs {
-  long long rows;
-  int width;
-  const void* x;
-  const void* dy;          // gradient only
-  long long ldx, lddy;
-  const void* weight;
-  const void* bias;        // forward only
-  float eps;
-  void* out;               // y, or dx
-  long long ldo;
-  float* mean;             // written by the forward pass, read by the gradient
-  float* rstd;
-  float* partials;         // gradient: [CTA][2][width]
-  float* row_sums;         // gradient of wide rows: [rows][2]
-  unsigned* err;
-};
-
-template <class T>
-__device__ __forceinline__ bool row_ok(const NormArgs& a, size_t at, int n, long long ld) {
-  return GEMM_IN_EXTENT(at + n - 1, stored_extent(a.rows, a.width, ld), a.err, kSiteBoundsRows);
-}
 
 // ---------------------------------------------------------------- forward
 // G threads per row, NV vectors of VEC elements each: vector i of thread t
@@ -127,163 +103,6 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) layer_norm_kernel(const Nor
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = fmaf((raw[i].at(j) - mean) * rstd, w[j], b[j]);
     if (row_ok<T>(a, row * a.ldo + d, VEC, a.ldo)) store_vec<T, VEC>(y + d, v);
-  }
-}
-
-// ---------------------------------------------------------------- streaming
-// One CTA of 512 threads (1024 for the widest gradients) per SM, and shared
-// memory for its rings.  Threads hold 32 elements of a row in the forward
-// pass and 16 in the gradient (8 where that takes 1024 threads: 8192 x 8192
-// fp32 131 us, with 16 137): what a row costs besides its elements (the
-// reductions, the barriers) is then paid by few warps, and the arithmetic is
-// done two elements at a time (f32x2).  With 8 elements a thread the issue of
-// instructions bound both kernels (65536 x 1024 bfloat16: 60 and 91 us).
-constexpr int stream_threads(int g) { return g < 512 ? 512 : g; }
-constexpr size_t kStreamBytes = 200 * 1024;
-constexpr int kMostStages = 8;
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// The ring of one group: `arrays` rows per stage (x, or x and dy), filled for
-// rows first, first + step, ... of the group, `stages` ahead.
-template <class T, int G, int ARRAYS>
-struct RowRing {
-  const NormArgs& a;
-  uint8_t* data;
-  uint32_t bars, row_bytes;
-  int stages, s = 0;
-  uint32_t ph = 0;
-  bool lost = false;
-  long long next, step;
-
-  __device__ __forceinline__ RowRing(const NormArgs& args, uint8_t* smem, int group, int groups, int st)
-      : a(args), row_bytes(static_cast<uint32_t>(args.width * sizeof(T))), stages(st) {
-    data = smem + static_cast<size_t>(group) * st * ARRAYS * row_bytes;
-    bars = smem_addr(smem) + static_cast<uint32_t>(groups) * st * ARRAYS * row_bytes +
-           static_cast<uint32_t>(group) * st * 8u;
-    step = static_cast<long long>(gridDim.x) * groups;
-    next = static_cast<long long>(blockIdx.x) * groups + group;
-  }
-  // One thread of the group, before the group's first barrier.
-  __device__ __forceinline__ void init() {
-    for (int i = 0; i < stages; ++i) mbar_init(bars + 8u * i, 1);
-    fence_mbar_init();
-  }
-  // One thread: the copies of row `next` into stage `at`.
-  __device__ __forceinline__ void load(int at) {
-    if (next < a.rows) {
-      const uint32_t bar = bars + 8u * at;
-      const uint32_t dst = smem_addr(data) + static_cast<uint32_t>(at) * ARRAYS * row_bytes;
-      mbar_arrive_expect_tx(bar, ARRAYS * row_bytes);
-      bulk_load(dst, static_cast<const T*>(a.x) + next * a.ldx, row_bytes, bar);
-      if (ARRAYS == 2)
-        bulk_load(dst + row_bytes, static_cast<const T*>(a.dy) + next * a.lddy, row_bytes, bar);
-    }
-    next += step;
-  }
-  // A wait that runs out is recorded, and the thread goes on (the result is
-  // undefined, as the status says): the group's barriers need all of it.
-  __device__ __forceinline__ void wait() {
-    if (!lost) lost = !mbar_wait(bars + 8u * s, ph, a.err, kSiteTransformFull);
-  }
-  __device__ __forceinline__ const T* row(int array) const {
-    return reinterpret_cast<const T*>(data + (static_cast<size_t>(s) * ARRAYS + array) * row_bytes);
-  }
-  __device__ __forceinline__ void advance() {
-    if (++s == stages) {
-      s = 0;
-      ph ^= 1u;
-    }
-  }
-};
-
-// A thread's pairs of weight or bias (NV vectors of 16 / sizeof(T) elements).
-template <class T, class WT, int G, int NV>
-__device__ __forceinline__ void load_weights(const void* p, int width, int t, float none,
-                                             Pair (&w)[NV][8 / sizeof(T)]) {
-  constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int d = (i * G + t) * VEC;
-    float f[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = none;
-    if (p && d < width) load_cached<WT, VEC>(static_cast<const WT*>(p) + d, f);
-#pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) w[i][j] = pair_of(f[2 * j], f[2 * j + 1]);
-  }
-}
-
-template <class T, class WT, int G, int NV>
-__global__ void __launch_bounds__(stream_threads(G), 1)
-    layer_norm_stream_kernel(NormArgs a, int stages) {
-  constexpr int kGroups = stream_threads(G) / G;
-  constexpr int VEC = 16 / static_cast<int>(sizeof(T)), NP = VEC / 2;
-  extern __shared__ __align__(128) uint8_t smem_rows[];
-  __shared__ float part[2][kGroups][G / 32];
-  const int group = threadIdx.x / G, t = threadIdx.x % G;
-  RowRing<T, G, 1> ring(a, smem_rows, group, kGroups, stages);
-  if (t == 0) ring.init();
-  __syncthreads();
-  grid_launch_dependents();
-  grid_dependency_wait();
-  long long row = ring.next;
-  if (t == 0)
-    for (int i = 0; i < stages; ++i) ring.load(i);
-  const float inv = 1.0f / static_cast<float>(a.width);
-  Pair w[NV][NP], b[NV][NP];
-  load_weights<T, WT, G, NV>(a.weight, a.width, t, 1.0f, w);
-  load_weights<T, WT, G, NV>(a.bias, a.width, t, 0.0f, b);
-  for (; row < a.rows; row += ring.step) {
-    ring.wait();
-    Pair x[NV][NP], sum = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int d = (i * G + t) * VEC;
-#pragma unroll
-      for (int j = 0; j < NP; ++j) x[i][j] = 0;
-      if (d < a.width) load_pairs<T>(ring.row(0) + d, x[i]);
-#pragma unroll
-      for (int j = 0; j < NP; ++j) sum = add2(sum, x[i][j]);
-    }
-    float s[1] = {sum_of(sum)};
-    group_sum<1, G>(s, part[0][group], group);
-    if (t == 0) ring.load(ring.s);      // the group has read this stage
-    ring.advance();
-    const float mean = s[0] * inv;
-    const Pair minus = pair_of(-mean, -mean);
-    sum = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if ((i * G + t) * VEC >= a.width) break;
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        x[i][j] = add2(x[i][j], minus);
-        sum = fma2(x[i][j], x[i][j], sum);
-      }
-    }
-    s[0] = sum_of(sum);
-    group_sum<1, G>(s, part[1][group], group);
-    const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
-    if (t == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
-    }
-    const Pair by = pair_of(rstd, rstd);
-    T* const y = static_cast<T*>(a.out) + row * a.ldo;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int d = (i * G + t) * VEC;
-      if (d >= a.width) break;
-#pragma unroll
-      for (int j = 0; j < NP; ++j) x[i][j] = fma2(mul2(x[i][j], by), w[i][j], b[i][j]);
-      if (row_ok<T>(a, row * a.ldo + d, VEC, a.ldo)) store_pairs<T>(y + d, x[i]);
-    }
   }
 }
 
@@ -460,95 +279,6 @@ __global__ void __launch_bounds__(kGradThreads<G>) layer_norm_grad_kernel(const 
   write_columns<T, VEC, G, NV, kThreads>(a, cols, group, t, dw, db);
 }
 
-template <class T, class WT, int G, int NV>
-__global__ void __launch_bounds__(stream_threads(G), 1)
-    layer_norm_grad_stream_kernel(NormArgs a, int stages) {
-  constexpr int kThreads = stream_threads(G);
-  constexpr int kGroups = kThreads / G;
-  constexpr int VEC = 16 / static_cast<int>(sizeof(T)), NP = VEC / 2;
-  extern __shared__ __align__(128) uint8_t smem_rows[];
-  __shared__ float part[2][kGroups][2 * (G / 32)];
-  const int group = threadIdx.x / G, t = threadIdx.x % G;
-  RowRing<T, G, 2> ring(a, smem_rows, group, kGroups, stages);
-  if (t == 0) ring.init();
-  __syncthreads();
-  grid_launch_dependents();
-  grid_dependency_wait();
-  long long row = ring.next;
-  if (t == 0)
-    for (int i = 0; i < stages; ++i) ring.load(i);
-  const float inv = 1.0f / static_cast<float>(a.width);
-  Pair w[NV][NP], dw[NV][NP], db[NV][NP];
-  load_weights<T, WT, G, NV>(a.weight, a.width, t, 1.0f, w);
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < NP; ++j) dw[i][j] = db[i][j] = 0;
-  int flip = 0;
-  float mean = 0.0f, rstd = 0.0f;
-  if (row < a.rows) {
-    mean = __ldg(a.mean + row);
-    rstd = __ldg(a.rstd + row);
-  }
-  for (; row < a.rows; row += ring.step) {
-    ring.wait();
-    float mean_n = 0.0f, rstd_n = 0.0f;      // the next row's, under this row's work
-    if (row + ring.step < a.rows) {
-      mean_n = __ldg(a.mean + row + ring.step);
-      rstd_n = __ldg(a.rstd + row + ring.step);
-    }
-    const Pair minus = pair_of(-mean, -mean), by = pair_of(rstd, rstd);
-    Pair hat[NV][NP], g[NV][NP], sg = 0, sgh = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int d = (i * G + t) * VEC;
-      if (d >= a.width) break;
-      load_pairs<T>(ring.row(0) + d, hat[i]);
-      load_pairs<T>(ring.row(1) + d, g[i]);
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        hat[i][j] = mul2(add2(hat[i][j], minus), by);
-        dw[i][j] = fma2(g[i][j], hat[i][j], dw[i][j]);
-        db[i][j] = add2(db[i][j], g[i][j]);
-        g[i][j] = mul2(g[i][j], w[i][j]);
-        sg = add2(sg, g[i][j]);
-        sgh = fma2(g[i][j], hat[i][j], sgh);
-      }
-    }
-    float s[2] = {sum_of(sg), sum_of(sgh)};
-    group_sum<2, G>(s, part[flip][group], group);
-    flip ^= 1;
-    if (t == 0) ring.load(ring.s);           // the group has read this stage
-    ring.advance();
-    if (a.out) {
-      const float c1 = -s[0] * inv, c2 = -s[1] * inv;
-      const Pair minus_c1 = pair_of(c1, c1), minus_c2 = pair_of(c2, c2);
-      T* const dx = static_cast<T*>(a.out) + row * a.ldo;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int d = (i * G + t) * VEC;
-        if (d >= a.width) break;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-          g[i][j] = mul2(fma2(hat[i][j], minus_c2, add2(g[i][j], minus_c1)), by);
-        if (row_ok<T>(a, row * a.ldo + d, VEC, a.ldo)) store_pairs<T>(dx + d, g[i]);
-      }
-    }
-    mean = mean_n;
-    rstd = rstd_n;
-  }
-  __syncthreads();                           // the rings become the groups' column sums
-  float fw[NV][VEC], fb[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      unpair(dw[i][j], fw[i][2 * j], fw[i][2 * j + 1]);
-      unpair(db[i][j], fb[i][2 * j], fb[i][2 * j + 1]);
-    }
-  write_columns<T, VEC, G, NV, kThreads>(a, reinterpret_cast<float*>(smem_rows), group, t, fw, fb);
-}
-
 // dweight and dbias: the sums over `count` rows of partials, 32 columns per
 // CTA, row by row in 32 interleaved chains that are then added in order.
 template <class WT>
@@ -665,15 +395,19 @@ int launch_forward(const NormArgs& a, cudaStream_t stream) {
 // Rows per group of a full grid from which on the streaming kernels are taken.
 constexpr int kStreamRows = 4;
 
-// Launches a streaming kernel when the rows are many; 1 when they are not.
-template <int G, int ARRAYS, void (*kernel)(NormArgs, int)>
-int launch_stream(const NormArgs& a, size_t size, size_t least_smem, int device,
-                  int num_sms, int* ctas, cudaStream_t stream) {
+// Launches a streaming kernel when the rows are many and two stages of its
+// rings fit; 1 when not.
+template <int G, int ARRAYS, int CTAS, void (*kernel)(NormArgs, int, int)>
+int launch_stream(const NormArgs& a, bool ragged, size_t size, size_t least_smem, int device, int num_sms,
+                  int* parts, cudaStream_t stream) {
   constexpr int kGroups = stream_threads(G) / G;
-  const int grid = num_sms;
-  const size_t row = static_cast<size_t>(a.width) * size * ARRAYS;
+  // a multiple of 8 groups on ragged rows: of one start each
+  constexpr int kWhole = 8 / kGroups > 1 ? 8 / kGroups : 1;
+  const int units = ragged ? num_sms / CTAS / kWhole * kWhole : num_sms / CTAS, grid = units * CTAS;
+  const int slice = CTAS == 1 ? a.width : ((a.width + CTAS - 1) / CTAS + 7) / 8 * 8;
+  const size_t row = ring_row_bytes(slice, size, ragged) * ARRAYS;
   const int stages = static_cast<int>(std::min<size_t>(kMostStages, kStreamBytes / (kGroups * (row + 8))));
-  if (a.rows < static_cast<long long>(kStreamRows) * grid * kGroups || stages < 2) return 1;
+  if (a.rows < static_cast<long long>(kStreamRows) * units * kGroups || stages < 2 || units == 0) return 1;
   const size_t smem = std::max(least_smem, kGroups * stages * (row + 8));
   static std::atomic<unsigned long long> configured{0};   // of this kernel: a bit per device
   const unsigned long long bit = 1ull << (device % 64);
@@ -685,8 +419,8 @@ int launch_stream(const NormArgs& a, size_t size, size_t least_smem, int device,
     }
     configured.fetch_or(bit);
   }
-  *ctas = grid;
-  if (launch_dependent(kernel, dim3(grid), dim3(stream_threads(G)), smem, stream, a, stages) !=
+  *parts = units;
+  if (launch_dependent(kernel, dim3(grid), dim3(stream_threads(G)), smem, stream, a, stages, slice) !=
       cudaSuccess) {
     (void)cudaGetLastError();
     return GEMM_F32_ELAUNCH;
@@ -694,37 +428,48 @@ int launch_stream(const NormArgs& a, size_t size, size_t least_smem, int device,
   return GEMM_F32_OK;
 }
 
-template <class T, class WT, int G, int NV>
-int stream_forward(const NormArgs& a, int device, int num_sms, cudaStream_t stream) {
-  int ctas;
-  return launch_stream<G, 1, layer_norm_stream_kernel<T, WT, G, NV>>(a, sizeof(T), 0, device, num_sms, &ctas,
-                                                                     stream);
+// How the rows of a call's matrices lie: all on 16-byte boundaries, or row by
+// row equally far from one in every matrix, or neither (which the streaming
+// kernels do not take).
+enum class Rows { kVectors, kRagged, kUneven };
+
+// E elements of a row per thread.
+template <class T, class WT, int G, int E>
+int stream_forward(const NormArgs& a, Rows rows, int device, int num_sms, cudaStream_t stream) {
+  int parts;
+  return rows == Rows::kVectors ? launch_stream<G, 1, 1, layer_norm_stream_kernel<T, WT, G, E / 2, false>>(
+                       a, false, sizeof(T), 0, device, num_sms, &parts, stream)
+                 : launch_stream<G, 1, 1, layer_norm_stream_kernel<T, WT, G, E / 2, true>>(
+                       a, true, sizeof(T), 0, device, num_sms, &parts, stream);
 }
 
-template <class T, class WT, int G, int NV>
-int stream_grad(NormArgs a, float* scratch, int device, int num_sms, int* ctas, cudaStream_t stream) {
+template <class T, class WT, int G, int E, int CTAS = 1>
+int stream_grad(NormArgs a, Rows rows, float* scratch, int device, int num_sms, int* parts,
+                cudaStream_t stream) {
   a.partials = scratch;
-  constexpr size_t kColumns = sizeof(float) * stream_threads(G) * NV * (16 / sizeof(T));
-  return launch_stream<G, 2, layer_norm_grad_stream_kernel<T, WT, G, NV>>(a, sizeof(T), kColumns, device, num_sms,
-                                                                          ctas, stream);
+  constexpr size_t kColumns = sizeof(float) * stream_threads(G) * E;
+  return rows == Rows::kVectors ? launch_stream<G, 2, CTAS, layer_norm_grad_stream_kernel<T, WT, G, E / 2, false, CTAS>>(
+                       a, false, sizeof(T), kColumns, device, num_sms, parts, stream)
+                 : launch_stream<G, 2, CTAS, layer_norm_grad_stream_kernel<T, WT, G, E / 2, true, CTAS>>(
+                       a, true, sizeof(T), kColumns, device, num_sms, parts, stream);
 }
 
 // The narrowest group of threads whose registers hold the row: up to 4
 // vectors a thread, or 8 elements where they are read one by one.
 template <class T, class WT>
-int forward(const NormArgs& a, bool vectors, int device, int num_sms, cudaStream_t stream) {
+int forward(const NormArgs& a, Rows rows, int device, int num_sms, cudaStream_t stream) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
-  constexpr int N = 8 / V;                 // vectors of 8 elements
+  const bool vectors = rows == Rows::kVectors;
   const int n = vectors ? (a.width + V - 1) / V : a.width;
-  if (vectors) {
-    const int e = a.width;
-    const int rc = e <= 256     ? stream_forward<T, WT, 32, N>(a, device, num_sms, stream)
-                   : e <= 512   ? stream_forward<T, WT, 32, 2 * N>(a, device, num_sms, stream)
-                   : e <= 1024  ? stream_forward<T, WT, 32, 4 * N>(a, device, num_sms, stream)
-                   : e <= 2048  ? stream_forward<T, WT, 64, 4 * N>(a, device, num_sms, stream)
-                   : e <= 4096  ? stream_forward<T, WT, 128, 4 * N>(a, device, num_sms, stream)
-                   : e <= 8192  ? stream_forward<T, WT, 256, 4 * N>(a, device, num_sms, stream)
-                   : e <= 16384 ? stream_forward<T, WT, 512, 4 * N>(a, device, num_sms, stream)
+  if (rows != Rows::kUneven) {
+    const int e = a.width + (vectors ? 0 : V - 1);   // a row's start may take part of a vector
+    const int rc = e <= 256     ? stream_forward<T, WT, 32, 8>(a, rows, device, num_sms, stream)
+                   : e <= 512   ? stream_forward<T, WT, 32, 16>(a, rows, device, num_sms, stream)
+                   : e <= 1024  ? stream_forward<T, WT, 32, 32>(a, rows, device, num_sms, stream)
+                   : e <= 2048  ? stream_forward<T, WT, 64, 32>(a, rows, device, num_sms, stream)
+                   : e <= 4096  ? stream_forward<T, WT, 128, 32>(a, rows, device, num_sms, stream)
+                   : e <= 8192  ? stream_forward<T, WT, 256, 32>(a, rows, device, num_sms, stream)
+                   : e <= 16384 ? stream_forward<T, WT, 512, 32>(a, rows, device, num_sms, stream)
                                 : 1;
     if (rc != 1) return rc;
   }
@@ -761,14 +506,14 @@ int launch_grad(NormArgs a, float* scratch, int num_sms, int* ctas, cudaStream_t
 }
 
 template <class T, class WT>
-int grad(NormArgs a, bool vectors, void* dweight, void* dbias, int device, int num_sms,
+int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_sms,
          cudaStream_t stream, int* launches) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
-  const bool columns = dweight || dbias;
+  const bool columns = dweight || dbias, vectors = rows == Rows::kVectors;
   const int n = vectors ? (a.width + V - 1) / V : a.width;
   // vectors (elements where unaligned) that the widest register kernel holds
   const bool wide = n > (vectors ? 16384 / V : 8192);
-  const long long bands = std::min<long long>(a.rows, wide ? kWideBands : 2LL * num_sms);
+  const long long bands = std::min<long long>(a.rows, 2LL * num_sms);   // at most, in any kernel
   const size_t part_floats = columns ? static_cast<size_t>(bands) * 2 * a.width : 0;
   const size_t sums_floats = wide ? 2 * static_cast<size_t>(a.rows) : 0;
   float* scratch = nullptr;
@@ -782,20 +527,22 @@ int grad(NormArgs a, bool vectors, void* dweight, void* dbias, int device, int n
   int ctas = 0, rc;
   if (a.rows == 0) {
     rc = GEMM_F32_OK;
-  } else if (!wide) {
-    constexpr int N = 8 / V;
-    const int e = a.width;
-    rc = !vectors     ? 1
-         : e <= 256   ? stream_grad<T, WT, 32, N>(a, parts, device, num_sms, &ctas, stream)
-         : e <= 512   ? stream_grad<T, WT, 32, 2 * N>(a, parts, device, num_sms, &ctas, stream)
-         : e <= 1024  ? stream_grad<T, WT, 64, 2 * N>(a, parts, device, num_sms, &ctas, stream)
-         : e <= 2048  ? stream_grad<T, WT, 128, 2 * N>(a, parts, device, num_sms, &ctas, stream)
-         : e <= 4096  ? stream_grad<T, WT, 256, 2 * N>(a, parts, device, num_sms, &ctas, stream)
-         : e <= 8192  ? stream_grad<T, WT, 1024, N>(a, parts, device, num_sms, &ctas, stream)
-         : e <= 16384 ? stream_grad<T, WT, 1024, 2 * N>(a, parts, device, num_sms, &ctas, stream)
+  } else {
+    const int e = a.width + (vectors ? 0 : V - 1);
+    rc = rows == Rows::kUneven ? 1
+         : e <= 256   ? stream_grad<T, WT, 32, 8>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 512   ? stream_grad<T, WT, 32, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 1024  ? stream_grad<T, WT, 64, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 2048  ? stream_grad<T, WT, 128, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 4096  ? stream_grad<T, WT, 256, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 8192  ? stream_grad<T, WT, 512, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 16384 ? stream_grad<T, WT, 512, 16, 2>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 32768 ? stream_grad<T, WT, 512, 16, 4>(a, rows, parts, device, num_sms, &ctas, stream)
                       : 1;
-    if (rc != 1) {
-    } else if (vectors && V == 8) {
+    if (rc != 1) ++*launches;
+  }
+  if (rc == 1 && !wide) {
+    if (vectors && V == 8) {
       if (n <= 32) rc = launch_grad<T, WT, V, 32, 1>(a, parts, num_sms, &ctas, stream);
       else if (n <= 64) rc = launch_grad<T, WT, V, 32, 2>(a, parts, num_sms, &ctas, stream);
       else if (n <= 128) rc = launch_grad<T, WT, V, 128, 1>(a, parts, num_sms, &ctas, stream);
@@ -820,7 +567,7 @@ int grad(NormArgs a, bool vectors, void* dweight, void* dbias, int device, int n
       else rc = launch_grad<T, WT, 1, 1024, 8>(a, parts, num_sms, &ctas, stream);
     }
     ++*launches;
-  } else {
+  } else if (rc == 1) {
     const unsigned grid = static_cast<unsigned>(std::min<long long>(a.rows, 2LL * num_sms));
     a.row_sums = scratch + part_floats;
     rc = GEMM_F32_OK;
@@ -829,7 +576,7 @@ int grad(NormArgs a, bool vectors, void* dweight, void* dbias, int device, int n
       ++*launches;
     }
     if (rc == GEMM_F32_OK && columns) {
-      ctas = static_cast<int>(bands);
+      ctas = static_cast<int>(std::min<long long>(a.rows, kWideBands));
       a.partials = parts;
       rc = launch(norm_grad_wide_columns_kernel<T>,
                   dim3((a.width + 255u) / 256u, static_cast<unsigned>(ctas)), 256, stream, a);
@@ -876,6 +623,12 @@ bool vector_rows(const void* p, long long ld, int width, size_t size) {
   return aligned_to(p, 16) && ld * size % 16 == 0 && width * size % 16 == 0;
 }
 
+// Row by row as far from a 16-byte boundary as in the other matrix.
+bool alike(const void* p, long long ldp, const void* q, long long ldq, size_t size) {
+  return (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) % 16 == 0 &&
+         (ldp - ldq) * static_cast<long long>(size) % 16 == 0;
+}
+
 // An output that is an input matrix itself, or apart from it.
 bool same_or_apart(const void* out, long long ldo, const void* in, long long ldi, long long rows,
                    int width, size_t size) {
@@ -919,14 +672,17 @@ extern "C" int gemm_f32_layer_norm(int type, int weight_type, long long rows, in
   a.rstd = rstd;
   const bool vectors = vector_rows(x, ldx, width, es) && vector_rows(y, ldy, width, es) &&
                        aligned_to(weight, 16) && aligned_to(bias, 16);
+  const Rows how = vectors                       ? Rows::kVectors
+                   : alike(x, ldx, y, ldy, es)   ? Rows::kRagged
+                                                 : Rows::kUneven;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
   int rc;
   if (type == GEMM_F32_TYPE_F32)
-    rc = forward<float, float>(a, vectors, device, num_sms, stream);
+    rc = forward<float, float>(a, how, device, num_sms, stream);
   else if (weight_type == GEMM_F32_TYPE_F32)
-    rc = forward<bf16, float>(a, vectors, device, num_sms, stream);
+    rc = forward<bf16, float>(a, how, device, num_sms, stream);
   else
-    rc = forward<bf16, bf16>(a, vectors, device, num_sms, stream);
+    rc = forward<bf16, bf16>(a, how, device, num_sms, stream);
   if (rc == GEMM_F32_OK) note_launches(1, "layer_norm_kernel");
   return rc;
 }
@@ -970,14 +726,17 @@ extern "C" int gemm_f32_layer_norm_grad(int type, int weight_type, long long row
   a.ldo = lddx;
   const bool vectors = vector_rows(x, ldx, width, es) && vector_rows(dy, lddy, width, es) &&
                        (!dx || vector_rows(dx, lddx, width, es)) && aligned_to(weight, 16);
+  const Rows how = vectors ? Rows::kVectors
+                   : alike(x, ldx, dy, lddy, es) && (!dx || alike(x, ldx, dx, lddx, es)) ? Rows::kRagged
+                                                                                        : Rows::kUneven;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
   int rc, launches = 0;
   if (type == GEMM_F32_TYPE_F32)
-    rc = grad<float, float>(a, vectors, dweight, dbias, device, num_sms, stream, &launches);
+    rc = grad<float, float>(a, how, dweight, dbias, device, num_sms, stream, &launches);
   else if (weight_type == GEMM_F32_TYPE_F32)
-    rc = grad<bf16, float>(a, vectors, dweight, dbias, device, num_sms, stream, &launches);
+    rc = grad<bf16, float>(a, how, dweight, dbias, device, num_sms, stream, &launches);
   else
-    rc = grad<bf16, bf16>(a, vectors, dweight, dbias, device, num_sms, stream, &launches);
+    rc = grad<bf16, bf16>(a, how, dweight, dbias, device, num_sms, stream, &launches);
   if (rc == GEMM_F32_OK) note_launches(launches, "layer_norm_grad_kernel");
   return rc;
 }

@@ -1,0 +1,465 @@
+// Layer norm over many rows: the streaming kernels (sm_103a).
+//
+// Each group of G threads works on one row at a time and keeps the next rows
+// in a ring in shared memory, filled by bulk copies (cp.async.bulk on
+// mbarriers).  One CTA of 512 threads per SM.
+// Threads hold 32 elements of a row in the forward pass and 16 in the
+// gradient: what a row costs besides its elements (reductions, barriers) is then
+// paid by few warps, and the arithmetic is done two elements at a time
+// (f32x2).  With 8 elements a thread the issue of instructions bound both
+// kernels (65536 x 1024 bfloat16: 60 and 91 us against 47 and 70; the copy
+// rate allows 40 and 59).
+//
+// RAGGED: rows that do not all start and end on 16-byte boundaries.  A row is
+// copied from the boundary below its start to the one above its end (never
+// beyond the matrix: what is left at its first and last bytes is copied by a
+// thread), and threads take the 16-byte vectors of that copy, of which the
+// first and the last hold elements of other rows.  Rows start 0 to 14 bytes
+// above a boundary, each of 16 / gcd(16, stride) rows differently; the number
+// of groups is a multiple of that, so that a group meets rows of one start
+// only, and its threads keep their columns.  (65536 x 777 fp32: 71 and 117 us,
+// copies 60 and 90; 65536 x 1001 bfloat16: 75 and 113 us, copies 39 and 58.
+// Before, with the elements read one by one by the threads, 65536 x 1023
+// bfloat16 took 119 and 144.)
+//
+// CTAS > 1 (gradient of rows wider than 8192): a cluster shares a row, each
+// CTA a slice of its columns, and exchanges the two sums of the row through
+// distributed shared memory.  (Computing a row's dx only after the next row's
+// sums, from the ring again, so that the exchange overlaps them, was measured
+// no faster: 4096 x 16384 fp32 170 us against 172.)
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "device_common.cuh"
+#include "pair_common.cuh"
+#include "row_common.cuh"
+
+namespace gemm_f32_impl {
+using namespace gemm_f32_dev;
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+struct NormArgs {
+  long long rows;
+  int width;
+  const void* x;
+  const void* dy;          // gradient only
+  long long ldx, lddy;
+  const void* weight;
+  const void* bias;        // forward only
+  float eps;
+  void* out;               // y, or dx
+  long long ldo;
+  float* mean;             // written by the forward pass, read by the gradient
+  float* rstd;
+  float* partials;         // gradient: [CTA][2][width]
+  float* row_sums;         // gradient of wide rows: [rows][2]
+  unsigned* err;
+};
+
+template <class T>
+__device__ __forceinline__ bool row_ok(const NormArgs& a, size_t at, int n, long long ld) {
+  return GEMM_IN_EXTENT(at + n - 1, stored_extent(a.rows, a.width, ld), a.err, kSiteBoundsRows);
+}
+
+// ---------------------------------------------------------------- rings
+constexpr int stream_threads(int g) { return g < 512 ? 512 : g; }
+constexpr size_t kStreamBytes = 200 * 1024;
+constexpr int kMostStages = 8;
+
+// Shared memory of one row of a ring.
+__host__ __device__ __forceinline__ size_t ring_row_bytes(int width, size_t size, bool ragged) {
+  return ragged ? (width * size + 15) / 16 * 16 + 16 : width * size;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// The ring of one group: ARRAYS rows per stage (x, or x and dy), filled for
+// the group's rows first, first + step, ..., `stages` ahead.  Of each row the
+// `width` elements from column `col0` on.
+template <class T, int ARRAYS, bool RAGGED>
+struct RowRing {
+  const NormArgs& a;
+  uint8_t* data;
+  uint32_t bars, row_bytes;
+  int width, col0, stages, s = 0;
+  uint32_t ph = 0;
+  bool lost = false;
+  long long next, step;
+
+  __device__ __forceinline__ RowRing(const NormArgs& args, uint8_t* smem, int group, int groups, int st,
+                                     int slice, int first_col, int ctas)
+      : a(args), width(min(slice, args.width - first_col)), col0(first_col), stages(st) {
+    row_bytes = static_cast<uint32_t>(ring_row_bytes(slice, sizeof(T), RAGGED));
+    data = smem + static_cast<size_t>(group) * st * ARRAYS * row_bytes;
+    bars = smem_addr(smem) + static_cast<uint32_t>(groups) * st * ARRAYS * row_bytes +
+           static_cast<uint32_t>(group) * st * 8u;
+    step = static_cast<long long>(gridDim.x / ctas) * groups;
+    next = static_cast<long long>(blockIdx.x / ctas) * groups + group;
+  }
+  // One thread of the group, before the group's first barrier.
+  __device__ __forceinline__ void init() {
+    for (int i = 0; i < stages; ++i) mbar_init(bars + 8u * i, 1);
+    fence_mbar_init();
+  }
+  __device__ __forceinline__ const T* source(int array, long long row) const {
+    return (array == 0 ? static_cast<const T*>(a.x) + row * a.ldx
+                       : static_cast<const T*>(a.dy) + row * a.lddy) + col0;
+  }
+  // One thread: the copies of row `next` into stage `at`.
+  __device__ __forceinline__ void load(int at) {
+    if (next < a.rows) {
+      const uint32_t bar = bars + 8u * at;
+      uint8_t* const dst = data + static_cast<size_t>(at) * ARRAYS * row_bytes;
+      if constexpr (RAGGED) {
+        uint32_t bytes[ARRAYS];
+        uintptr_t from[ARRAYS];
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i) edges(i, dst + i * row_bytes, from[i], bytes[i]);
+        mbar_arrive_expect_tx(bar, ARRAYS == 2 ? bytes[0] + bytes[ARRAYS - 1] : bytes[0]);
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i)
+          if (bytes[i])
+            bulk_load(smem_addr(dst) + i * row_bytes +
+                          static_cast<uint32_t>(from[i] - (reinterpret_cast<uintptr_t>(source(i, next)) & ~uintptr_t{15})),
+                      reinterpret_cast<const void*>(from[i]), bytes[i], bar);
+      } else {
+        const uint32_t bytes = static_cast<uint32_t>(width * sizeof(T));
+        mbar_arrive_expect_tx(bar, ARRAYS * bytes);
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i)
+          bulk_load(smem_addr(dst) + i * row_bytes, source(i, next), bytes, bar);
+      }
+    }
+    next += step;
+  }
+  // The 16-byte blocks of row `next` that lie within the matrix go by one bulk
+  // copy (`bytes` from `from` on); its elements outside them, at the matrix's
+  // two ends only, are copied here.
+  __device__ __forceinline__ void edges(int array, uint8_t* dst, uintptr_t& from, uint32_t& bytes) {
+    const T* const row = source(array, next);
+    const uintptr_t first = reinterpret_cast<uintptr_t>(row), last = first + width * sizeof(T);
+    const long long ld = array == 0 ? a.ldx : a.lddy;
+    const uintptr_t lowest = reinterpret_cast<uintptr_t>(array == 0 ? a.x : a.dy);
+    const uintptr_t end = lowest + stored_extent(a.rows, a.width, ld) * sizeof(T);
+    uintptr_t lo = first & ~uintptr_t{15}, hi = (last + 15) & ~uintptr_t{15};
+    if (lo < lowest) lo += 16;
+    if (hi > end) hi -= 16;
+    T* const at = reinterpret_cast<T*>(dst + (first & 15));
+    if (lo >= hi) {       // no whole block
+      lo = hi = first;
+      for (int d = 0; d < width; ++d) at[d] = row[d];
+    } else {
+      for (uintptr_t p = first; p < lo; p += sizeof(T)) at[(p - first) / sizeof(T)] = *reinterpret_cast<const T*>(p);
+      for (uintptr_t p = hi; p < last; p += sizeof(T)) at[(p - first) / sizeof(T)] = *reinterpret_cast<const T*>(p);
+    }
+    from = lo;
+    bytes = static_cast<uint32_t>(hi - lo);
+  }
+  // A wait that runs out is recorded, and the thread goes on (the result is
+  // undefined, as the status says): the group's barriers need all of it.
+  __device__ __forceinline__ void wait() {
+    if (!lost) lost = !mbar_wait(bars + 8u * s, ph, a.err, kSiteTransformFull);
+  }
+  // The stage's copy of an array's row.
+  __device__ __forceinline__ const uint8_t* at(int array) const {
+    return data + (static_cast<size_t>(s) * ARRAYS + array) * row_bytes;
+  }
+  // Elements by which the group's rows start above a 16-byte boundary.
+  __device__ __forceinline__ int shift() const {
+    return RAGGED ? static_cast<int>((reinterpret_cast<uintptr_t>(source(0, next)) & 15) / sizeof(T)) : 0;
+  }
+  __device__ __forceinline__ void advance() {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// ---------------------------------------------------------------- a thread's part of a row
+// NP pairs of elements: vector i of thread t holds the elements from column
+// (i G + t) VEC - shift on.
+template <class T, int G, int NP, bool RAGGED>
+struct Part {
+  static constexpr int kPer = 8 / static_cast<int>(sizeof(T));   // pairs per vector
+  static constexpr int kVec = 2 * kPer;
+  static constexpr int NV = NP / kPer;
+  int width, first;                      // columns of the row, column of vector 0
+  int last = -1;                         // a vector that ends outside the row
+  bool edge = false;                     // a vector of this thread lies partly in the row
+
+  __device__ __forceinline__ Part(int w, int shift, int t) : width(w), first(t * kVec - shift) {
+    if constexpr (RAGGED) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (any(i) && col(i) + kVec > width) last = i;
+      edge = first < 0 || last >= 0;
+    }
+  }
+  __device__ __forceinline__ int col(int i) const { return i * (G * kVec) + first; }
+  __device__ __forceinline__ bool any(int i) const {
+    return RAGGED ? col(i) + kVec > 0 && col(i) < width : col(i) < width;
+  }
+  __device__ __forceinline__ bool in(int d) const { return d >= 0 && d < width; }
+
+  // Whether vector i lies partly in the row: the first or the last one.
+  __device__ __forceinline__ bool cut(int i) const { return i == last || (i == 0 && first < 0); }
+
+  // 0 for what lies outside the row: behind a branch that hardly a thread
+  // takes, and only in the vectors that are cut.
+  __device__ __forceinline__ void mask(Pair (&x)[NP]) const {
+    if (!RAGGED || !edge) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cut(i)) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          float u, v;
+          unpair(x[i * kPer + j], u, v);
+          x[i * kPer + j] = pair_of(in(col(i) + 2 * j) ? u : 0.0f, in(col(i) + 2 * j + 1) ? v : 0.0f);
+        }
+      }
+  }
+
+  __device__ __forceinline__ void load(const uint8_t* copy, int t, Pair (&x)[NP]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Pair v[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = 0;
+      if (any(i)) load_pairs<T>(reinterpret_cast<const T*>(copy) + (i * G + t) * kVec, v);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[i * kPer + j] = v[j];
+    }
+    mask(x);
+  }
+
+  template <class WT>
+  __device__ __forceinline__ void load_weights(const void* p, float none, Pair (&w)[NP]) const {
+    const WT* const v = static_cast<const WT*>(p);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[kVec];
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) f[j] = none;
+      if constexpr (RAGGED) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (p && in(col(i) + j)) f[j] = to_f32(v[col(i) + j]);
+      } else {
+        if (p && any(i)) load_cached<WT, kVec>(v + col(i), f);
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) w[i * kPer + j] = pair_of(f[2 * j], f[2 * j + 1]);
+    }
+  }
+
+  __device__ __forceinline__ void store(T* y, const Pair (&x)[NP]) const {
+    if (RAGGED && edge) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cut(i)) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int d = col(i) + 2 * j;
+            float u, v;
+            unpair(x[i * kPer + j], u, v);
+            if (in(d)) y[d] = from_f32<T>(u);
+            if (in(d + 1)) y[d + 1] = from_f32<T>(v);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Pair v[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = x[i * kPer + j];
+      if (any(i) && !(RAGGED && cut(i))) store_pairs<T>(y + col(i), v);
+    }
+  }
+};
+
+// ---------------------------------------------------------------- kernels
+template <class T, class WT, int G, int NP, bool RAGGED>
+__global__ void __launch_bounds__(stream_threads(G), 1)
+    layer_norm_stream_kernel(NormArgs a, int stages, int slice) {
+  constexpr int kGroups = stream_threads(G) / G;
+  extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ float part[2][kGroups][G / 32];
+  const int group = threadIdx.x / G, t = threadIdx.x % G;
+  RowRing<T, 1, RAGGED> ring(a, smem_rows, group, kGroups, stages, slice, 0, 1);
+  if (t == 0) ring.init();
+  __syncthreads();
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const Part<T, G, NP, RAGGED> mine(a.width, ring.shift(), t);
+  long long row = ring.next;
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) ring.load(i);
+  const float inv = 1.0f / static_cast<float>(a.width);
+  Pair w[NP], b[NP];
+  mine.template load_weights<WT>(a.weight, 1.0f, w);
+  mine.template load_weights<WT>(a.bias, 0.0f, b);
+  for (; row < a.rows; row += ring.step) {
+    ring.wait();
+    Pair x[NP], sum = 0;
+    mine.load(ring.at(0), t, x);
+#pragma unroll
+    for (int q = 0; q < NP; ++q) sum = add2(sum, x[q]);
+    float s[1] = {sum_of(sum)};
+    group_sum<1, G>(s, part[0][group], group);
+    if (t == 0) ring.load(ring.s);      // the group has read this stage
+    ring.advance();
+    const float mean = s[0] * inv;
+    const Pair minus = pair_of(-mean, -mean);
+    sum = 0;
+#pragma unroll
+    for (int q = 0; q < NP; ++q) x[q] = add2(x[q], minus);
+    mine.mask(x);
+#pragma unroll
+    for (int q = 0; q < NP; ++q)
+      if (mine.any(q / mine.kPer)) sum = fma2(x[q], x[q], sum);
+    s[0] = sum_of(sum);
+    group_sum<1, G>(s, part[1][group], group);
+    const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    const Pair by = pair_of(rstd, rstd);
+#pragma unroll
+    for (int q = 0; q < NP; ++q) x[q] = fma2(mul2(x[q], by), w[q], b[q]);
+    if (GEMM_IN_EXTENT(row * a.ldo + a.width - 1, stored_extent(a.rows, a.width, a.ldo), a.err, kSiteBoundsRows))
+      mine.store(static_cast<T*>(a.out) + row * a.ldo, x);
+  }
+}
+
+template <class T, class WT, int G, int NP, bool RAGGED, int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G), 1)
+    layer_norm_grad_stream_kernel(NormArgs a, int stages, int slice) {
+  constexpr int kThreads = stream_threads(G);
+  constexpr int kGroups = kThreads / G;
+  static_assert(CTAS == 1 || kGroups == 1, "a cluster works on one row");
+  extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ float part[2][kGroups][2 * (G / 32)];
+  __shared__ float2 shared_sums[2][CTAS];              // of the CTAs of the cluster
+  const int group = threadIdx.x / G, t = threadIdx.x % G;
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int col0 = rank * slice;
+  RowRing<T, 2, RAGGED> ring(a, smem_rows, group, kGroups, stages, slice, col0, CTAS);
+  const int width = ring.width;                        // of this CTA's slice
+  if (t == 0) ring.init();
+  __syncthreads();
+  if (CTAS > 1) cluster_sync();              // every CTA of the cluster runs
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const Part<T, G, NP, RAGGED> mine(width, ring.shift(), t);
+  long long row = ring.next;
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) ring.load(i);
+  const float inv = 1.0f / static_cast<float>(a.width);
+  Pair w[NP], dw[NP], db[NP];
+  mine.template load_weights<WT>(a.weight ? static_cast<const WT*>(a.weight) + col0 : nullptr, 1.0f, w);
+#pragma unroll
+  for (int q = 0; q < NP; ++q) dw[q] = db[q] = 0;
+  int flip = 0;
+  float mean = 0.0f, rstd = 0.0f;
+  if (row < a.rows) {
+    mean = __ldg(a.mean + row);
+    rstd = __ldg(a.rstd + row);
+  }
+  for (; row < a.rows; row += ring.step) {
+    ring.wait();
+    float mean_n = 0.0f, rstd_n = 0.0f;      // the next row's, under this row's work
+    if (row + ring.step < a.rows) {
+      mean_n = __ldg(a.mean + row + ring.step);
+      rstd_n = __ldg(a.rstd + row + ring.step);
+    }
+    const Pair minus = pair_of(-mean, -mean), by = pair_of(rstd, rstd);
+    Pair hat[NP], g[NP], sg = 0, sgh = 0;
+    mine.load(ring.at(0), t, hat);
+    mine.load(ring.at(1), t, g);
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {           // dy is 0 outside the row
+      hat[q] = mul2(add2(hat[q], minus), by);
+      dw[q] = fma2(g[q], hat[q], dw[q]);
+      db[q] = add2(db[q], g[q]);
+      g[q] = mul2(g[q], w[q]);
+      sg = add2(sg, g[q]);
+      sgh = fma2(g[q], hat[q], sgh);
+    }
+    float s[2] = {sum_of(sg), sum_of(sgh)};
+    group_sum<2, G>(s, part[flip][group], group);
+    if (t == 0) ring.load(ring.s);           // the group has read this stage
+    ring.advance();
+    if constexpr (CTAS > 1) {                // every CTA adds the slices' sums in order
+      if (t < CTAS) {
+        const uint32_t to = map_rank(smem_addr(&shared_sums[flip][rank]), static_cast<uint32_t>(t));
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(s[0]), "f"(s[1]) : "memory");
+      }
+      __syncwarp();
+      cluster_sync();
+      s[0] = s[1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < CTAS; ++i) {
+        s[0] += shared_sums[flip][i].x;
+        s[1] += shared_sums[flip][i].y;
+      }
+    }
+    flip ^= 1;
+    if (a.out) {
+      const float c1 = -s[0] * inv, c2 = -s[1] * inv;
+      const Pair minus_c1 = pair_of(c1, c1), minus_c2 = pair_of(c2, c2);
+#pragma unroll
+      for (int q = 0; q < NP; ++q) g[q] = mul2(fma2(hat[q], minus_c2, add2(g[q], minus_c1)), by);
+      if (GEMM_IN_EXTENT(row * a.ldo + a.width - 1, stored_extent(a.rows, a.width, a.ldo), a.err,
+                         kSiteBoundsRows))
+        mine.store(static_cast<T*>(a.out) + row * a.ldo + col0, g);
+    }
+    mean = mean_n;
+    rstd = rstd_n;
+  }
+  if (CTAS > 1) cluster_sync();              // no CTA leaves while another may write to it
+  if (!a.partials) return;
+  // the groups' column sums, added in group order: one row of partials per
+  // CTA (or cluster); the rings make room
+  float* const cols = reinterpret_cast<float*>(smem_rows);
+  float* const to = a.partials + static_cast<size_t>(blockIdx.x / CTAS) * 2 * a.width + col0;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+    float* const own = cols + group * width;
+#pragma unroll
+    for (int i = 0; i < mine.NV; ++i)
+#pragma unroll
+      for (int j = 0; j < mine.kPer; ++j) {
+        const int q = i * mine.kPer + j, d = mine.col(i) + 2 * j;
+        float u, v;
+        unpair(which ? db[q] : dw[q], u, v);
+        if (mine.in(d)) own[d] = u;
+        if (mine.in(d + 1)) own[d + 1] = v;
+      }
+    __syncthreads();
+    for (int d = threadIdx.x; d < width; d += kThreads) {
+      float v = cols[d];
+#pragma unroll
+      for (int g2 = 1; g2 < kGroups; ++g2) v += cols[g2 * width + d];
+      to[static_cast<size_t>(which) * a.width + d] = v;
+    }
+  }
+}
+
+}  // namespace
+}  // namespace gemm_f32_impl

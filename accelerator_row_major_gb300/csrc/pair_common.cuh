@@ -15,7 +15,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// Every thread of both CTAs.
+// Every thread of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");

@@ -111,17 +111,47 @@ def test_many_rows(rows, width, kind):
 
 @pytest.mark.parametrize("kind,wkind", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
 def test_streamed_rows_of_every_width(kind, wkind):
-    """Enough rows for the streaming kernels at each of their widths, in one process and in this order:
-    every kernel sets up its own shared memory."""
+    """Enough rows for the streaming kernels at each of their widths, on 16-byte rows and others, in one
+    process and in this order: every kernel sets up its own shared memory."""
     g = lib()
-    for width in (1024, 256, 8, 512, 264, 2048, 1032, 4096, 8192, 4104, 16384, 8200):
-        rows = max(700, 20000 * 128 // width)
+    for width in (1024, 256, 8, 512, 264, 2048, 1032, 4096, 8192, 4104, 16384, 8200, 20000,
+                  1023, 255, 3, 511, 259, 2047, 1025, 4095, 8190, 4097, 16383, 8201, 20001):
+        rows = 10000 if width <= 1024 else 5000 if width <= 2048 else 2500 if width <= 4096 else 1300
         x, dy, w, b = _inputs(rows, width, kind, wkind, width)
         y, mean, rstd = g.layer_norm(x, w, b)
         _check_forward(x, w, b, 1e-5, y, mean, rstd, kind)
         dx, dw, db = g.layer_norm_grad(dy, x, w, mean, rstd)
         _check_grad(x, dy, w, mean, rstd, dx, dw, db, kind, wkind)
         assert g.gemm_f32_status(None) == (0, 0)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("apart", [0, 1])
+@pytest.mark.parametrize("width,offset", [(777, 1), (777, 3), (1024, 5), (100, 7), (33, 2), (258, 4)])
+def test_streamed_rows_at_every_alignment(width, offset, apart, kind):
+    """Dense rows of which the first starts off a 16-byte boundary, equally far in x, dy and the results
+    (streamed) or not (loaded by the threads)."""
+    torch, types = _torch()
+    g = lib()
+    rows = 10000
+    x, dy, w, b = _inputs(rows, width, kind, "f32", width + offset)
+
+    def shifted(t, by):
+        buf = torch.full((rows * width + 32,), 7.0, device="cuda", dtype=types[kind])
+        view = buf[by:by + rows * width].view(rows, width)
+        if t is not None:
+            view.copy_(t)
+        return buf, view
+
+    (_, xs), (_, ds) = shifted(x, offset), shifted(dy, (offset + apart) % 8)
+    buf, out = shifted(None, (offset + 2 * apart) % 8)
+    y, mean, rstd = g.layer_norm(xs, w, b, out=out)
+    _check_forward(x, w, b, 1e-5, y, mean, rstd, kind)
+    dbuf, dout = shifted(None, (offset + 4 * apart) % 8)
+    dx, dw, db = g.layer_norm_grad(ds, xs, w, mean, rstd, out=dout)
+    _check_grad(x, dy, w, mean, rstd, dx, dw, db, kind, "f32")
+    for t, by in ((buf, (offset + 2 * apart) % 8), (dbuf, (offset + 4 * apart) % 8)):
+        assert (t[:by] == 7).all() and (t[by + rows * width:] == 7).all()
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
