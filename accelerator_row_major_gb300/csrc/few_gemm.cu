@@ -94,6 +94,11 @@ struct FewParams {
   unsigned* err;
 };
 
+// Elements of the partial tiles, for the checked build.
+__device__ __forceinline__ size_t partials_extent(const FewParams& p) {
+  return static_cast<size_t>(p.tiles) * p.max_seg * p.rows * kTile;
+}
+
 // K blocks [k0, k1) of the tile of w that starts at row (or column) m0.
 struct Item {
   int m0, units, k0, k1, tile, seg;
@@ -239,8 +244,10 @@ __device__ __forceinline__ void logits_out(const FewParams& p, int piece, int la
 #pragma unroll
   for (int j = 1; j < 16; ++j) m = lane >> 1 == j ? m2[j] : m;
   const int t = t0 + (lane >> 1);
-  if ((lane & 1) == 0 && t < p.rows)
-    p.stats[static_cast<size_t>(piece) * p.ld_stats + t] =
+  const size_t stat = static_cast<size_t>(piece) * p.ld_stats + t;
+  if ((lane & 1) == 0 && t < p.rows &&
+      GEMM_IN_EXTENT(stat, static_cast<size_t>(p.units) * p.ld_stats, p.err, kSiteBoundsScratch))
+    p.stats[stat] =
         make_float2(m, F32 ? sum : sum * (1.0f / 32768.0f));
 }
 
@@ -536,7 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             q * 32 + lane;
 #pragma unroll
         for (int j = 0; j < 64; ++j)
-          if (j < cols && col0 + j < p.rows) part[static_cast<size_t>(col0 + j) * kTile] = acc[j];
+          if (j < cols && col0 + j < p.rows &&
+              GEMM_IN_EXTENT(part + static_cast<size_t>(col0 + j) * kTile - p.partials, partials_extent(p),
+                             p.err, kSiteBoundsWork))
+            part[static_cast<size_t>(col0 + j) * kTile] = acc[j];
       } else if (q < w.units) {
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
@@ -650,7 +660,9 @@ __global__ void __launch_bounds__(256)
   const size_t step = static_cast<size_t>(p.rows) * kTile;
   const float* src = p.partials + tile * p.max_seg * step + static_cast<size_t>(t) * kTile + l;
   float v = 0.0f;
-  for (int s = 0; s < nseg; ++s) v += __ldcg(src + s * step);
+  for (int s = 0; s < nseg; ++s)
+    if (GEMM_IN_EXTENT(src + s * step - p.partials, partials_extent(p), p.err, kSiteBoundsWork))
+      v += __ldcg(src + s * step);
   const size_t at = static_cast<size_t>(t) * lddx + d;
   if (GEMM_IN_EXTENT(at, stored_extent(p.rows, p.width, lddx), p.err, kSiteBoundsRows))
     dx[at] = from_f32<T>(v * __ldg(scale));

@@ -209,6 +209,11 @@ struct PairItems {
   }
 };
 
+// Elements of the partial tiles, for the checked build.
+__device__ __forceinline__ size_t partials_extent(const Params& p) {
+  return static_cast<size_t>(p.tiles_m * p.tiles_n - p.dp_tiles) * p.max_seg * (kTile * kTile);
+}
+
 // The sums of NC consecutive columns of one row of C, scaled and added to.
 template <int NC>
 __device__ __forceinline__ void finish_c(const Params& p, int row, int col, float s, float (&v)[NC]) {
@@ -565,7 +570,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int ch = 0; ch < 4; ++ch) {
             float v[32];
             take(ch, v, ch == 3);
-            store_vec<float, 32>(part + ch * 32, v);
+            if (GEMM_IN_EXTENT(part + ch * 32 + 31 - p.partials, partials_extent(p), p.err, kSiteBoundsWork))
+              store_vec<float, 32>(part + ch * 32, v);
           }
         } else {
 #pragma unroll
@@ -634,8 +640,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (row_ok)
-          p.stats[static_cast<size_t>(2 * c.tn + half) * p.ld_stats + row] =
+        const size_t stat = static_cast<size_t>(2 * c.tn + half) * p.ld_stats + row;
+        if (row_ok && GEMM_IN_EXTENT(stat, 2 * static_cast<size_t>(p.tiles_n) * p.ld_stats, p.err,
+                                     kSiteBoundsScratch))
+          p.stats[stat] =
               make_float2(m2, PARTS == 3 ? sum_of(sums) : sum_of(sums) * (1.0f / 32768.0f));
       }
     }
@@ -671,6 +679,7 @@ __global__ void __launch_bounds__(256) half_gemm_reduce_kernel(const Params p) {
                      static_cast<size_t>(local) * kTile + col;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = 0; s < nseg; ++s, src += kTile * kTile) {
+    if (!GEMM_IN_EXTENT(src + 3 - p.partials, partials_extent(p), p.err, kSiteBoundsWork)) return;
     const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
     v[0] += x.x;
     v[1] += x.y;
