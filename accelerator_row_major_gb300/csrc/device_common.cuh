@@ -88,13 +88,7 @@ enum BoundsSite : unsigned {
   kSiteBoundsC = 18,        // a read or write of C outside its window's extent
   kSiteBoundsWork = 19,     // a partial tile outside the split-tail workspace
   kSiteBoundsPack = 20,     // operand packing outside its source or destination
-  kSiteBoundsRows = 21,     // a row of a layer norm or a loss outside its matrix
-  kSiteBoundsScratch = 22,  // a layer norm's or a loss's scratch outside its part
 };
-
-// A target outside the vocabulary (data, not a failure of the kernels):
-// gemm_f32_status() reports it as GEMM_F32_ETARGET.
-constexpr unsigned kSiteTarget = 32;
 
 #ifdef GEMM_BOUNDS_CHECK
 __device__ __forceinline__ bool in_extent(size_t index, size_t extent, unsigned* err,
@@ -583,21 +577,6 @@ __device__ __forceinline__ void mma_tf32_tmem_a(uint32_t d_tmem, uint32_t a_tmem
       "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// One lane of a converged warp, always the same one.  A warp that issues MMAs
-// walks its loop with all lanes and lets this lane alone issue: the operands
-// then stay warp-uniform values, which the MMA takes as they are.  In a
-// branch that one lane enters they are moved to uniform registers before
-// every MMA, about 100 clocks each (measured on GB300).
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t chosen;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(chosen));
-  return chosen != 0;
 }
 
 // The mbarrier receives one arrive once every tcgen05 operation this thread

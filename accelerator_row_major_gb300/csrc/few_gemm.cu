@@ -39,6 +39,7 @@
 #include "device_common.cuh"
 #include "half_gemm.h"
 #include "launch.h"
+#include "pair_common.cuh"
 #include "row_common.cuh"
 
 namespace gemm_f32_impl {

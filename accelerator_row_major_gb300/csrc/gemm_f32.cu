@@ -643,7 +643,7 @@ extern "C" int gemm_f32_status(gemm_f32_stream_t stream_handle, unsigned* site) 
     return GEMM_F32_ELAUNCH;
   }
   if (site) *site = word;
-  if (word == gemm_f32_dev::kSiteTarget) return GEMM_F32_ETARGET;
+  if (word == gemm_f32_impl::kSiteTarget) return GEMM_F32_ETARGET;
   return word ? GEMM_F32_ETIMEOUT : GEMM_F32_OK;
 }
 

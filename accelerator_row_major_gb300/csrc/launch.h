@@ -4,7 +4,6 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <cstdint>
 #include <utility>
@@ -98,9 +97,6 @@ void* fixed_scratch_address();
 bool tma_encode_2d(CUtensorMap* map, const float* ptr, int rows, int cols, int ld, int box_cols,
                    int box_rows, CUtensorMapSwizzle swz);
 
-// The driver's tensor-map encoder (nullptr if it cannot be had).
-PFN_cuTensorMapEncodeTiled_v12000 tma_encoder();
-
 // CUDA-core FFMA path.
 int launch_ffma(GemmArgs& g, cudaStream_t stream, int* launches);
 
@@ -129,6 +125,10 @@ void* acquire_scratch(int device, cudaStream_t stream, size_t bytes);
 // The current device, set up on first use: its ordinal, multiprocessor count
 // and error word.  False when it is not an sm_103 part or a query failed.
 bool current_device(int* device, int* num_sms, unsigned** err);
+
+// A target outside the vocabulary recorded in the error word (data, not a
+// failure of the kernels): gemm_f32_status() reports it as GEMM_F32_ETARGET.
+constexpr unsigned kSiteTarget = 32;
 
 // What gemm_f32_last_launches() and gemm_f32_last_kernel() report next.
 void note_launches(int launches, const char* kernel);

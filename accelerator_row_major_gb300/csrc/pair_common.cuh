@@ -1,7 +1,12 @@
-// Primitives of the kernels that run on CTA pairs (clusters of two, tcgen05
-// cta_group::2): cluster barriers, remote mbarrier arrives, tensor memory of
-// the pair, commits to both CTAs.
+// Primitives of clusters (barriers, remote mbarrier arrives) and of MMAs on
+// CTA pairs (tcgen05 cta_group::2: tensor memory of the pair, commits to both
+// CTAs) for the bfloat16 products and the streaming norms, the choice of the
+// lane that issues MMAs, and the tensor-map encoder.
 #pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 
@@ -102,4 +107,39 @@ __device__ __forceinline__ void mma_commit_local(uint32_t bar) {
                : "memory");
 }
 
+// One lane of a converged warp, always the same one.  A warp that issues MMAs
+// walks its loop with all lanes and lets this lane alone issue: the operands
+// then stay warp-uniform values, which the MMA takes as they are.  In a
+// branch that one lane enters they are moved to uniform registers before
+// every MMA, about 100 clocks each (measured on GB300).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t chosen;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(chosen));
+  return chosen != 0;
+}
+
 }  // namespace gemm_f32_dev
+
+namespace gemm_f32_impl {
+
+// The driver's tensor-map encoder, looked up once (nullptr if it cannot be had).
+inline PFN_cuTensorMapEncodeTiled_v12000 tma_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      fn = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  return encode;
+}
+
+}  // namespace gemm_f32_impl

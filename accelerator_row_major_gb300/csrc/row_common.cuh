@@ -12,7 +12,12 @@
 #include "launch.h"
 
 namespace gemm_f32_dev {
+using gemm_f32_impl::kSiteTarget;
 using gemm_f32_impl::LossTargets;
+
+// Sites of the checked build, after those of device_common.cuh.
+constexpr unsigned kSiteBoundsRows = 21;      // a row of a layer norm or a loss outside its matrix
+constexpr unsigned kSiteBoundsScratch = 22;   // a layer norm's or a loss's scratch outside its part
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -747,8 +747,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 
 }  // namespace
 
-PFN_cuTensorMapEncodeTiled_v12000 tma_encoder() { return encoder(); }
-
 // 2-D fp32 map of a row-major [rows x cols] matrix with row stride ld
 // (elements), box [box_rows x box_cols]; out-of-bounds boxes read as zero.
 bool tma_encode_2d(CUtensorMap* map, const float* ptr, int rows, int cols, int ld, int box_cols,
