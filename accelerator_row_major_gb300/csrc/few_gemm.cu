@@ -96,7 +96,7 @@ struct FewParams {
 };
 
 // Elements of the partial tiles, for the checked build.
-__device__ __forceinline__ size_t partials_extent(const FewParams& p) {
+[[maybe_unused]] __device__ __forceinline__ size_t partials_extent(const FewParams& p) {
   return static_cast<size_t>(p.tiles) * p.max_seg * p.rows * kTile;
 }
 

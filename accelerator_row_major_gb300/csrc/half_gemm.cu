@@ -210,7 +210,7 @@ struct PairItems {
 };
 
 // Elements of the partial tiles, for the checked build.
-__device__ __forceinline__ size_t partials_extent(const Params& p) {
+[[maybe_unused]] __device__ __forceinline__ size_t partials_extent(const Params& p) {
   return static_cast<size_t>(p.tiles_m * p.tiles_n - p.dp_tiles) * p.max_seg * (kTile * kTile);
 }
 

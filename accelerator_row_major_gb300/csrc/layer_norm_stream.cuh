@@ -220,17 +220,19 @@ struct Part {
   // 0 for what lies outside the row: behind a branch that hardly a thread
   // takes, and only in the vectors that are cut.
   __device__ __forceinline__ void mask(Pair (&x)[NP]) const {
-    if (!RAGGED || !edge) return;
+    if constexpr (RAGGED) {
+      if (!edge) return;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (cut(i)) {
+      for (int i = 0; i < NV; ++i)
+        if (cut(i)) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          float u, v;
-          unpair(x[i * kPer + j], u, v);
-          x[i * kPer + j] = pair_of(in(col(i) + 2 * j) ? u : 0.0f, in(col(i) + 2 * j + 1) ? v : 0.0f);
+          for (int j = 0; j < kPer; ++j) {
+            float u, v;
+            unpair(x[i * kPer + j], u, v);
+            x[i * kPer + j] = pair_of(in(col(i) + 2 * j) ? u : 0.0f, in(col(i) + 2 * j + 1) ? v : 0.0f);
+          }
         }
-      }
+    }
   }
 
   __device__ __forceinline__ void load(const uint8_t* copy, int t, Pair (&x)[NP]) const {

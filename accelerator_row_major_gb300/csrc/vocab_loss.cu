@@ -280,21 +280,31 @@ __global__ void __launch_bounds__(kRescaleThreads)
 // into PARTS = 3 planes of bfloat16.  A value becomes hi + mid + lo: hi is the value truncated to bfloat16 (so
 // that it never overflows), mid and lo round what is left to nearest; the
 // rest is below 2^-25 of the value.
+// One launch takes x and w where both need it.
+struct Packing {
+  const void* src;
+  void* dst;
+  long long ld, ld_dst, plane;
+  int rows, cols;
+  int vectors;              // rows of src take 16-byte loads
+};
+
 template <class T, int PARTS, class O>
-__global__ void __launch_bounds__(256) loss_split_kernel(const T* src, int rows, int cols,
-                                                         long long ld, O* dst, long long ld_dst,
-                                                         long long plane, int vectors,
-                                                         unsigned* err) {
+__global__ void __launch_bounds__(256) loss_pack_kernel(Packing x, Packing w, unsigned* err) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int per_row = (cols + 7) / 8;
-  const long long all = static_cast<long long>(rows) * per_row;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < all; i += gridDim.x * 256LL) {
+  const long long all_x = static_cast<long long>(x.rows) * ((x.cols + 7) / 8);
+  const long long all = all_x + static_cast<long long>(w.rows) * ((w.cols + 7) / 8);
+  for (long long n = blockIdx.x * 256LL + threadIdx.x; n < all; n += gridDim.x * 256LL) {
+    const Packing& m = n < all_x ? x : w;
+    const long long i = n < all_x ? n : n - all_x;
+    const int per_row = (m.cols + 7) / 8;
     const int r = static_cast<int>(i / per_row), c = static_cast<int>(i % per_row) * 8;
-    const size_t at = static_cast<size_t>(r) * ld + c;
+    const T* const src = static_cast<const T*>(m.src);
+    const size_t at = static_cast<size_t>(r) * m.ld + c;
     float v[8];
-    if (vectors && c + 8 <= cols) {
-      if (!GEMM_IN_EXTENT(at + 7, stored_extent(rows, cols, ld), err, kSiteBoundsRows)) continue;
+    if (m.vectors && c + 8 <= m.cols) {
+      if (!GEMM_IN_EXTENT(at + 7, stored_extent(m.rows, m.cols, m.ld), err, kSiteBoundsRows)) continue;
       Raw<T, 8> raw;
       raw.load_once(src + at);
 #pragma unroll
@@ -302,12 +312,11 @@ __global__ void __launch_bounds__(256) loss_split_kernel(const T* src, int rows,
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[j] = c + j < cols &&
-                       GEMM_IN_EXTENT(at + j, stored_extent(rows, cols, ld), err, kSiteBoundsRows)
+        v[j] = c + j < m.cols && GEMM_IN_EXTENT(at + j, stored_extent(m.rows, m.cols, m.ld), err, kSiteBoundsRows)
                    ? to_f32(src[at + j])
                    : 0.0f;
     }
-    O* const out = dst + static_cast<size_t>(r) * ld_dst + c;
+    O* const out = static_cast<O*>(m.dst) + static_cast<size_t>(r) * m.ld_dst + c;
     if constexpr (PARTS == 3) {
       float hi[8];
 #pragma unroll
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(256) loss_split_kernel(const T* src, int rows,
       store_vec<bf16, 8>(out, hi);
 #pragma unroll
       for (int part = 1; part < 3; ++part) {
-        store_vec<bf16, 8>(out + part * plane, v);
+        store_vec<bf16, 8>(out + part * m.plane, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
       }
@@ -398,24 +407,23 @@ Operand plan_operand(const void* p, long long ld, int rows, int cols, bool f32, 
   return o;
 }
 
-int pack(const Operand& o, const void* src, long long ld, int rows, int cols, bool f32, char* scratch,
-         int num_sms, unsigned* err, cudaStream_t stream, int* launches) {
-  if (o.form == Operand::kAsIs) return GEMM_F32_OK;
-  const long long work = static_cast<long long>(rows) * ((cols + 7) / 8);
-  const unsigned grid = static_cast<unsigned>(std::min<long long>((work + 255) / 256, 16LL * num_sms));
-  void* const dst = scratch + o.at;
-  const int vectors = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld * (f32 ? 4 : 2) % 16 == 0;
-  if (o.form == Operand::kSplit)
-    return launch(loss_split_kernel<float, 3, bf16>, dim3(grid), 256, stream, launches,
-                  static_cast<const float*>(src), rows, cols, ld, static_cast<bf16*>(dst), o.ld, o.plane,
-                  vectors, err);
-  if (f32)
-    return launch(loss_split_kernel<float, 1, float>, dim3(grid), 256, stream, launches,
-                  static_cast<const float*>(src), rows, cols, ld, static_cast<float*>(dst), o.ld, o.plane,
-                  vectors, err);
-  return launch(loss_split_kernel<bf16, 1, bf16>, dim3(grid), 256, stream, launches,
-                static_cast<const bf16*>(src), rows, cols, ld, static_cast<bf16*>(dst), o.ld, o.plane,
-                vectors, err);
+Packing packing(const Operand& o, const void* src, long long ld, int rows, int cols, bool f32,
+                char* scratch) {
+  Packing m = {src, scratch + o.at, ld, o.ld, o.plane, rows, cols, 0};
+  m.vectors = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld * (f32 ? 4 : 2) % 16 == 0;
+  return m;
+}
+
+// Packs x and w, which take the same form, or one of them (the other has no rows).
+int pack(Operand::Form form, const Packing& x, const Packing& w, bool f32, int num_sms, unsigned* err,
+         cudaStream_t stream, int* launches) {
+  const long long work = static_cast<long long>(x.rows) * ((x.cols + 7) / 8) +
+                         static_cast<long long>(w.rows) * ((w.cols + 7) / 8);
+  const dim3 grid(static_cast<unsigned>(std::min<long long>((work + 255) / 256, 16LL * num_sms)));
+  return form == Operand::kSplit
+             ? launch(loss_pack_kernel<float, 3, bf16>, grid, 256, stream, launches, x, w, err)
+         : f32 ? launch(loss_pack_kernel<float, 1, float>, grid, 256, stream, launches, x, w, err)
+               : launch(loss_pack_kernel<bf16, 1, bf16>, grid, 256, stream, launches, x, w, err);
 }
 
 int run(const Call& c, cudaStream_t stream, int* launches) {
@@ -473,9 +481,16 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   float* const logit = reinterpret_cast<float*>(scratch + at_logit);
   float2* const stats = reinterpret_cast<float2*>(scratch + at_stats);
   const LossTargets all = {c.targets, c.target_bits, c.vocab, c.ignore};
-  int rc = pack(ox, c.x, c.ldx, c.rows, c.width, f32, scratch, num_sms, err, stream, launches);
-  if (rc == GEMM_F32_OK)
-    rc = pack(ow, c.w, c.ldw, c.vocab, c.width, f32, scratch, num_sms, err, stream, launches);
+  const Packing px = packing(ox, c.x, c.ldx, c.rows, c.width, f32, scratch);
+  const Packing pw = packing(ow, c.w, c.ldw, c.vocab, c.width, f32, scratch);
+  int rc = GEMM_F32_OK;
+  if (ox.form == ow.form && ox.form != Operand::kAsIs) {
+    rc = pack(ox.form, px, pw, f32, num_sms, err, stream, launches);
+  } else {
+    if (ox.form != Operand::kAsIs) rc = pack(ox.form, px, Packing{}, f32, num_sms, err, stream, launches);
+    if (rc == GEMM_F32_OK && ow.form != Operand::kAsIs)
+      rc = pack(ow.form, Packing{}, pw, f32, num_sms, err, stream, launches);
+  }
 
   const HalfOperand w = {ow.in(c.w, scratch), ow.ld, ow.plane, false};
   for (long long r = 0; rc == GEMM_F32_OK && r < c.rows; r += step) {
