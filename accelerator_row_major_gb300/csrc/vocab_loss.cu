@@ -77,12 +77,12 @@ struct JoinArgs {
   float* loss;
   float* lse;
   float2* joined;
-  double* sums;              // per CTA: its rows' losses, and how many count
+  float* sums;               // per CTA: its rows' losses, and how many count
   int* counts;
   // the whole call
   LossTargets all_targets;
   int all_rows;
-  const double* all_sums;
+  const float* all_sums;
   const int* all_counts;
   bool first, last, mean;
   float grad_scale;
@@ -96,7 +96,7 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
   constexpr int kChains = THREADS / kJoinRows, kWarps = THREADS / 32;
   __shared__ float tops[kWarps][kJoinRows], sums[kWarps][kJoinRows];
-  __shared__ double part_sum[kWarps];
+  __shared__ float part_sum[kWarps];
   __shared__ int part_count[kWarps];
   __shared__ bool finish;
   grid_launch_dependents();
@@ -106,6 +106,15 @@ __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
   const int row = blockIdx.x * kJoinRows + r;
   const float2* const mine = a.stats + row;
   const int end = row < a.rows ? a.pieces : 0;
+  // this row's label and logit, for the lanes that finish it: loaded first,
+  // under the statistics
+  const bool finisher = warp == 0 && lane < kJoinRows && row < a.rows;
+  int label = -1;
+  float logit = 0.0f;
+  if (finisher) {
+    label = label_at(a.targets, row);
+    logit = a.label_logit[row];       // of a row that does not count: not used
+  }
   float top = -INFINITY;
 #pragma unroll 8
   for (int i = chain; i < end; i += kChains) {
@@ -128,72 +137,75 @@ __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
   for (int o = kJoinRows; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (lane < kJoinRows) sums[warp][lane] = sum;
   __syncthreads();
+  float s = 0.0f;
+  int n = 0;
   if (warp == 0) {
-    float loss = 0.0f;
-    int label = -1;
-    if (lane < kJoinRows && row < a.rows) {
+    if (finisher) {
       sum = sums[0][r];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) sum += sums[w][r];
       const float l = sum == 0.0f ? -INFINITY : kLn2 * (top + log2f(sum));
-      label = label_at(a.targets, row);
-      if (label >= 0) loss = l - a.label_logit[row];
-      if (label < 0) {
+      if (label >= 0) {
+        s = l - logit;
+      } else {
         const long long y = a.targets.bits == 64 ? static_cast<const long long*>(a.targets.p)[row]
                                                  : static_cast<const int*>(a.targets.p)[row];
         if (y != a.targets.ignore) record_error(a.err, kSiteTarget);
       }
       if (a.lse) a.lse[row] = l;
-      if (a.loss) a.loss[row] = loss;
+      if (a.loss) a.loss[row] = s;
       if (a.joined) a.joined[row] = make_float2(top, 1.0f / sum);
     }
-    double s = loss;
     s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
     s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, label >= 0));
-    if (lane == 0) {
+    n = __popc(__ballot_sync(0xFFFFFFFFu, label >= 0));
+  }
+  if (a.all_rows > kJoinRows) {         // else this CTA has all of them
+    if (threadIdx.x == 0) {
       a.sums[blockIdx.x] = s;
       a.counts[blockIdx.x] = n;
       __threadfence();
       finish = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
     }
-  }
-  __syncthreads();
-  if (!finish) return;
-  __threadfence();
-  // ---- the last CTA
-  if (threadIdx.x == 0) *a.arrived = 0u;
-  if (!a.first && !a.last) return;
-  double s = 0.0;
-  int n = 0;
-  if (a.first && !a.last) {   // later pieces of the rows are not joined yet
+    __syncthreads();
+    if (!finish) return;
+    __threadfence();
+    // ---- the last CTA
+    if (threadIdx.x == 0) *a.arrived = 0u;
+    if (!a.first && !a.last) return;
+    s = 0.0f;
+    n = 0;
+    if (a.first && !a.last) {           // later pieces of the rows are not joined yet
 #pragma unroll 8
-    for (unsigned t = threadIdx.x; t < static_cast<unsigned>(a.all_rows); t += THREADS)
-      n += label_at(a.all_targets, t) >= 0;
-  } else {
-    const int groups = (a.all_rows - 1) / kJoinRows + 1;
+      for (unsigned t = threadIdx.x; t < static_cast<unsigned>(a.all_rows); t += THREADS)
+        n += label_at(a.all_targets, t) >= 0;
+    } else {
+      const int groups = (a.all_rows - 1) / kJoinRows + 1;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < groups; i += THREADS) {
-      s += __ldcg(a.all_sums + i);
-      n += __ldcg(a.all_counts + i);
+      for (int i = threadIdx.x; i < groups; i += THREADS) {
+        s += __ldcg(a.all_sums + i);
+        n += __ldcg(a.all_counts + i);
+      }
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    float v[1] = {s};
+    warp_sum<1>(v);
+    if (lane == 0) {
+      part_sum[warp] = v[0];
+      part_count[warp] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      v[0] = lane < kWarps ? part_sum[lane] : 0.0f;
+      warp_sum<1>(v);
+      s = v[0];
+      n = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? part_count[lane] : 0);
     }
   }
-  n = __reduce_add_sync(0xFFFFFFFFu, n);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (lane == 0) {
-    part_sum[warp] = s;
-    part_count[warp] = n;
-  }
-  __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int w = 1; w < kWarps; ++w) {
-    s += part_sum[w];
-    n += part_count[w];
-  }
   const float per = a.mean ? static_cast<float>(n > 1 ? n : 1) : 1.0f;
   if (a.first && a.factors) a.factors->grad = a.grad_scale / per;
-  if (a.last && a.total) *a.total = static_cast<float>(s / per);
+  if (a.last && a.total) *a.total = s / per;
 }
 
 // The rescaling pass of the gradient, g = e 2^(m - M) / S - onehot: 4 rows by
@@ -452,7 +464,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   const size_t at_factors = layout.take(sizeof(Factors));
   const size_t at_logit = layout.take(sizeof(float) * c.rows);
   const int groups_all = (c.rows - 1) / kJoinRows + 1;
-  const size_t at_sums = layout.take(sizeof(double) * groups_all);
+  const size_t at_sums = layout.take(sizeof(float) * groups_all);
   const size_t at_counts = layout.take(sizeof(int) * groups_all);
   const long long ld_stats = static_cast<long long>(round_up(step, 32));
   const size_t at_stats = layout.take(sizeof(float2) * pieces * ld_stats);
@@ -552,9 +564,9 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     j.loss = c.loss ? c.loss + r : nullptr;
     j.lse = c.lse ? c.lse + r : nullptr;
     j.joined = joined;
-    j.all_sums = reinterpret_cast<double*>(scratch + at_sums);
+    j.all_sums = reinterpret_cast<float*>(scratch + at_sums);
     j.all_counts = reinterpret_cast<int*>(scratch + at_counts);
-    j.sums = reinterpret_cast<double*>(scratch + at_sums) + r / kJoinRows;
+    j.sums = reinterpret_cast<float*>(scratch + at_sums) + r / kJoinRows;
     j.counts = reinterpret_cast<int*>(scratch + at_counts) + r / kJoinRows;
     j.all_targets = all;
     j.all_rows = c.rows;
