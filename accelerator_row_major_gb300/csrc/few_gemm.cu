@@ -5,6 +5,12 @@
 //
 //   logits  D[v][t] = sum_d w[v][d] x[t][d]: A = w, K-major.  Each CTA takes
 //           an even share of w's rows (in units of 32), in tiles of up to 128.
+//           TMA reads rows whose distance is a multiple of 16 bytes from a
+//           16-byte boundary on.  Where w's own are not (an odd width), every
+//           8th (or 4th, 2nd) row has the same distance from a boundary, so
+//           these classes of rows are read as matrices of their own, from the
+//           boundary below: the elements in front of a row become zeros in
+//           the tile, and x is there once for each class, shifted alike.
 //   dx      D[d][t] = sum_v w[v][d] g[t][v]: A = w^T, MN-major.  Tiles of 128
 //           columns; their K (the vocabulary) is shared evenly by all CTAs,
 //           and a second kernel adds the partial tiles in order.
@@ -82,7 +88,8 @@ struct FewParams {
   int b_stages, p_stages;                // stages of b, and of parts in tensor memory
   int width, vocab;
   int k_blocks;
-  int units;                             // logits: ceil(vocab / 32)
+  int units;                             // logits: of all classes
+  FewClasses classes;
   int tiles, max_seg;                    // dx: ceil(width / 128), partials per tile
   long long sk_work;
   float* partials;                       // dx: [tile][max_seg][rows][128]
@@ -100,9 +107,17 @@ struct FewParams {
   return static_cast<size_t>(p.tiles) * p.max_seg * p.rows * kTile;
 }
 
-// K blocks [k0, k1) of the tile of w that starts at row (or column) m0.
+// K blocks [k0, k1) of the tile of w that starts at row (or column) m0; for
+// the logits row m0 of class cls, whose first `shift` columns are not its own.
 struct Item {
   int m0, units, k0, k1, tile, seg;
+  int cls, shift, unit;
+};
+
+// w as the kernel's maps read it.
+template <int N>
+struct WMaps {
+  CUtensorMap of[N];
 };
 
 template <bool MN>
@@ -124,14 +139,20 @@ struct Items {
       w.k0 = static_cast<int>(x - w.tile * ki);
       w.k1 = static_cast<int>(min(ki, w.k0 + (end - x)));
       w.seg = static_cast<int>(blockIdx.x) - sk_owner(w.tile * ki, gridDim.x, p.sk_work);
+      w.cls = w.shift = w.unit = 0;
       x += w.k1 - w.k0;
-    } else {   // the least number of tiles, of about equal height
+    } else {   // within a class the least number of tiles, of about equal height
       constexpr int kMost = kTile / kUnit;
-      const int left = static_cast<int>(end - x), tiles = (left + kMost - 1) / kMost;
-      w.m0 = static_cast<int>(x) * kUnit;
+      w.unit = static_cast<int>(x);
+      w.cls = w.unit / p.classes.units;
+      const int in_class = w.unit - w.cls * p.classes.units;
+      const int left = static_cast<int>(min(end - x, static_cast<long long>(p.classes.units - in_class)));
+      const int tiles = (left + kMost - 1) / kMost;
+      w.m0 = in_class * kUnit;
       w.units = (left + tiles - 1) / tiles;
+      w.shift = (p.classes.shift0 + w.cls * p.classes.step) & p.classes.mask;
       w.k0 = 0;
-      w.k1 = p.k_blocks;
+      w.k1 = (p.width + w.shift + kBK - 1) / kBK;
       w.tile = w.seg = 0;
       x += w.units;
     }
@@ -209,13 +230,12 @@ __device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
   return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
 }
 
-// Logits of one piece (a vocabulary entry per lane) for 16 rows from t0 on,
+// Logits of one unit (a vocabulary entry v per lane) for 16 rows from t0 on,
 // acc[at ..]: their statistics, powers and labels.  The 16 rows are
 // independent, so that their reductions overlap.
 template <bool F32>
-__device__ __forceinline__ void logits_out(const FewParams& p, int piece, int lane, int t0,
+__device__ __forceinline__ void logits_out(const FewParams& p, int piece, int v, int lane, int t0,
                                            const float (&acc)[64], int at) {
-  const int v = piece * kUnit + lane;
   const bool in = v < p.vocab;
   constexpr float kUp = F32 ? 0.0f : 15.0f;   // one part: powers times 2^15 (fp16)
   float m2[16], e[16];
@@ -252,11 +272,16 @@ __device__ __forceinline__ void logits_out(const FewParams& p, int piece, int la
         make_float2(m, F32 ? sum : sum * (1.0f / 32768.0f));
 }
 
+// Bits of bfloat16 elements 2 i and 2 i + 1 that are not the first `shift`.
+__device__ __forceinline__ uint32_t front_mask(int shift, int i) {
+  return (2 * i >= shift ? 0xFFFFu : 0u) | (2 * i + 1 >= shift ? 0xFFFF0000u : 0u);
+}
+
 // ---------------------------------------------------------------- kernel
 template <bool MN, bool F32, bool STACKED>
 __global__ void __launch_bounds__(kThreads, 1)
-    few_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
-                    const FewParams p) {
+    few_gemm_kernel(const __grid_constant__ WMaps<MN ? 1 : kFewMostClasses> tmW,
+                    const __grid_constant__ CUtensorMap tmB, const FewParams p) {
   using C = Cfg<F32>;
   constexpr int SW = C::kWStages, PARTS = C::kParts;
   constexpr int SUM = sum_blocks(F32, STACKED);
@@ -300,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain_bar, 1);
     fence_mbar_init();
-    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmW.of[0]);
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
@@ -343,16 +368,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kBox = kBK * 128;
 #pragma unroll
             for (int i = 0; i < kTile / kCols; ++i)
-              tma_load_3d(st + i * kBox, &tmW, wfull(s), w.m0 + i * kCols, k, 0);
+              tma_load_3d(st + i * kBox, &tmW.of[0], wfull(s), w.m0 + i * kCols, k, 0);
           } else {
             constexpr uint32_t kBox = kUnit * 128;
+            const CUtensorMap* const map = &tmW.of[w.cls];
             mbar_arrive_expect_tx(wfull(s), static_cast<uint32_t>(w.units) * kBox * (F32 ? 2 : 1));
             for (int u = 0; u < w.units; ++u) {
               if (F32) {
-                tma_load_3d(st + (2 * u) * kBox, &tmW, wfull(s), k, w.m0 + u * kUnit, 0);
-                tma_load_3d(st + (2 * u + 1) * kBox, &tmW, wfull(s), k + 32, w.m0 + u * kUnit, 0);
+                tma_load_3d(st + (2 * u) * kBox, map, wfull(s), k, w.m0 + u * kUnit, 0);
+                tma_load_3d(st + (2 * u + 1) * kBox, map, wfull(s), k + 32, w.m0 + u * kUnit, 0);
               } else {
-                tma_load_3d(st + u * kBox, &tmW, wfull(s), k, w.m0 + u * kUnit, 0);
+                tma_load_3d(st + u * kBox, map, wfull(s), k, w.m0 + u * kUnit, 0);
               }
             }
           }
@@ -385,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(bfull(s), b_stage_bytes);
 #pragma unroll
           for (int part = 0; part < PARTS; ++part)
-            tma_load_3d(st + part * b_part_bytes, &tmB, bfull(s), kb * kBK, 0, part);
+            tma_load_3d(st + part * b_part_bytes, &tmB, bfull(s), kb * kBK, 0, w.cls * PARTS + part);
           if (++s == SB) {
             s = 0;
             ph ^= 1u;
@@ -426,6 +452,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool close = (kb - w.k0 + 1) % SUM == 0 || kb == w.k1 - 1;
         const uint32_t at = F32 ? parts0 + static_cast<uint32_t>(sa * 3 * kPartCols)
                                 : base + sa * C::kWBytes;
+        if (!MN && !F32 && kb == 0 && w.shift != 0) {
+          // what lies in front of the rows (the first of eight 16-byte pieces,
+          // swizzled) might be infinite or no number: x's zeros do not do
+          for (int r = lane; r < w.units * kUnit; r += 32) {
+            uint4* const front =
+                reinterpret_cast<uint4*>(base_ptr + sa * C::kWBytes + r * 128 + ((r & 7) << 4));
+            uint4 f = *front;
+            f.x &= front_mask(w.shift, 0);
+            f.y &= front_mask(w.shift, 1);
+            f.z &= front_mask(w.shift, 2);
+            f.w &= front_mask(w.shift, 3);
+            *front = f;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
         if (issuer) {
           uint32_t more = open ? 0u : 1u;
           if constexpr (STACKED) {
@@ -549,10 +591,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                              p.err, kSiteBoundsWork))
             part[static_cast<size_t>(col0 + j) * kTile] = acc[j];
       } else if (q < w.units) {
+        const int v = w.cls + p.classes.count * (w.m0 + q * kUnit + lane);
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
           if (ch * 16 < cols)
-            logits_out<F32>(p, w.m0 / kUnit + q, lane, col0 + ch * 16, acc, ch * 16);
+            logits_out<F32>(p, w.unit + q, v, lane, col0 + ch * 16, acc, ch * 16);
       }
     }
   } else if (F32 && warp >= kSplitWarp0) {
@@ -591,6 +634,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x[4 * c + 1] = f.y;
                 x[4 * c + 2] = f.z;
                 x[4 * c + 3] = f.w;
+              }
+              if (half == 0 && kb == 0) {   // what lies in front of the row
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                  if (k < w.shift) x[k] = 0.0f;
               }
             }
             if (half == 1) {   // the tile is in registers
@@ -709,9 +757,28 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* pt
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The maps of w: for the logits one per class, its rows from the boundary
+// below row c on.
+bool encode_w(const FewGemm& g, bool mn, CUtensorMap* maps) {
+  const CUtensorMapDataType type = g.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int size = g.f32 ? 4 : 2, box_cols = 128 / size;
+  if (mn)
+    return encode(maps, type, size, g.w, g.ldw, g.vocab, g.width, 1, 0, box_cols, kBK,
+                  g.f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+  const FewClasses& k = g.classes;
+  for (int c = 0; c < k.count; ++c) {
+    const int shift = (k.shift0 + c * k.step) & k.mask;
+    const char* const first = static_cast<const char*>(g.w) + (c * g.ldw - shift) * size;
+    if (!encode(maps + c, type, size, first, g.ldw * k.count, (g.vocab - c + k.count - 1) / k.count,
+                g.width + shift, 1, 0, box_cols, kUnit, CU_TENSOR_MAP_SWIZZLE_128B))
+      return false;
+  }
+  return true;
+}
+
 template <bool MN, bool F32, bool STACKED>
-int launch_one(const FewGemm& g, const FewParams& p, const CUtensorMap& mw, const CUtensorMap& mb,
-               int grid, cudaStream_t stream) {
+int launch_one(const FewGemm& g, const FewParams& p, const WMaps<MN ? 1 : kFewMostClasses>& mw,
+               const CUtensorMap& mb, int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};   // bit per device
   auto kern = few_gemm_kernel<MN, F32, STACKED>;
   const unsigned long long bit = 1ull << (g.device % kMaxDevices);
@@ -732,14 +799,26 @@ int launch_one(const FewGemm& g, const FewParams& p, const CUtensorMap& mw, cons
 }
 
 template <bool MN>
-int launch_type(const FewGemm& g, bool stacked, const FewParams& p, const CUtensorMap& mw,
-                const CUtensorMap& mb, int grid, cudaStream_t stream) {
+int launch_type(const FewGemm& g, bool stacked, const FewParams& p, const CUtensorMap& mb, int grid,
+                cudaStream_t stream) {
+  WMaps<MN ? 1 : kFewMostClasses> mw = {};
+  if (!encode_w(g, MN, mw.of)) return GEMM_F32_ELAUNCH;
   if (!g.f32) return launch_one<MN, false, false>(g, p, mw, mb, grid, stream);
   return stacked ? launch_one<MN, true, true>(g, p, mw, mb, grid, stream)
                  : launch_one<MN, true, false>(g, p, mw, mb, grid, stream);
 }
 
 }  // namespace
+
+FewClasses few_classes(bool f32, const void* w, long long ldw, int vocab) {
+  const int size = f32 ? 4 : 2;
+  FewClasses c = {1, 0, 0, 0, 16 / size - 1};
+  while (c.count * ldw * size % 16 != 0) c.count *= 2;
+  c.units = blocks_of(blocks_of(vocab, c.count), kUnit);
+  c.shift0 = static_cast<int>(reinterpret_cast<uintptr_t>(w) % 16) / size;
+  c.step = static_cast<int>(ldw & c.mask);
+  return c;
+}
 
 size_t few_gemm_scratch(int rows, int width, int vocab, int num_sms) {
   FewParams p = {};
@@ -759,8 +838,9 @@ int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches) {
     p.rows = g.rows;
     p.width = g.width;
     p.vocab = g.vocab;
-    p.k_blocks = blocks_of(g.width, kBK);
-    p.units = blocks_of(g.vocab, kUnit);
+    p.classes = g.classes;
+    p.units = p.classes.count * p.classes.units;
+    if (g.vocab < p.classes.count) return GEMM_F32_EINVAL;
     grid = std::min(p.units, g.num_sms);
     p.stats = g.stats;
     p.ld_stats = g.ld_stats;
@@ -778,16 +858,15 @@ int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches) {
   p.p_stages = std::min(4, (kTmemCols - p.acc_bufs * p.acc_cols) / (3 * kPartCols));
   p.b_stages = std::min(kMostRings, Cfg<true>::kBBytes / ((g.f32 ? 3 : 1) * p.n_pad * kBK * 2));
   p.err = g.err;
-  CUtensorMap mw, mb;
-  const int box_cols = g.f32 ? 32 : 64;   // 128 bytes
-  if (!encode(&mw, g.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              g.f32 ? 4 : 2, g.w, g.ldw, g.vocab, g.width, 1, 0, box_cols, dx ? kBK : kUnit,
-              dx && g.f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode(&mb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.b.ptr, g.b.ld, g.rows,
-              dx ? g.vocab : g.width, g.f32 ? 3 : 1, g.b.plane, kBK, p.n_pad, CU_TENSOR_MAP_SWIZZLE_128B))
+  CUtensorMap mb;
+  const int parts = g.f32 ? 3 : 1, copies = dx ? 1 : p.classes.count;
+  const bool shifted = !dx && !p.classes.aligned();
+  if (!encode(&mb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.b.ptr, g.b.ld, g.rows,
+              dx ? g.vocab : shifted ? static_cast<int>(g.b.ld) : g.width, copies * parts, g.b.plane, kBK,
+              p.n_pad, CU_TENSOR_MAP_SWIZZLE_128B))
     return GEMM_F32_ELAUNCH;
-  const int rc = dx ? launch_type<true>(g, stacked, p, mw, mb, grid, stream)
-                    : launch_type<false>(g, stacked, p, mw, mb, grid, stream);
+  const int rc = dx ? launch_type<true>(g, stacked, p, mb, grid, stream)
+                    : launch_type<false>(g, stacked, p, mb, grid, stream);
   if (rc != GEMM_F32_OK) return rc;
   ++*launches;
   if (dx) {

@@ -59,8 +59,9 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
 
 // The same two products for few rows (at most kFewRows), where reading w is
 // what takes the time (few_gemm.cu).  w is read as it is stored, fp32
-// included (f32: its three parts are made on the way to the tensor cores);
-// its rows start on 16-byte boundaries.
+// included (f32: its three parts are made on the way to the tensor cores).
+// For dx its rows start on 16-byte boundaries; for the logits they may not:
+// the rows then fall into classes, and b holds a copy of x for each.
 constexpr int kFewRows = 128;     // fp32: the pair kernel would first store w in three parts
                                   // (64 x 4096 x 65536 920 us against 250)
 constexpr int kFewRowsBf16 = 32;  // 4096 x 65536: 105 us against the pair kernel's 175 with one
@@ -68,14 +69,32 @@ constexpr int kFewRowsBf16 = 32;  // 4096 x 65536: 105 us against the pair kerne
                                   // 113 with 128
 constexpr int kFewPiece = 32;     // columns per statistic of its logits
 
+// Rows of w as TMA reads them: every `count`-th row has the same distance
+// from a 16-byte boundary, so that class c, the rows c, c + count, ..., is a
+// matrix that begins shift(c) elements before row c.  Units of kFewPiece rows
+// of a class make the logits' work and statistics: class by class, unit by
+// unit, `units` of each.
+struct FewClasses {
+  int count, units;
+  int shift0, step, mask;         // shift(c) = (shift0 + c step) & mask
+  bool aligned() const { return count == 1 && shift0 == 0; }
+};
+constexpr int kFewMostClasses = 8;
+
+FewClasses few_classes(bool f32, const void* w, long long ldw, int vocab);
+
 struct FewGemm {
   bool f32;
   int rows, width, vocab;
   const void* w;                  // vocab x width
   long long ldw;
   HalfOperand b;                  // K-major, rows x (width for logits, vocab for dx)
-  // -- logits: as HalfGemm, with statistics per kFewPiece columns
-  float2* stats = nullptr;        // [ceil(vocab / kFewPiece)][ld_stats]
+  // -- logits: as HalfGemm, with statistics per unit.  Unless classes is
+  // aligned, b has class c's copy of x (or of its parts) c parts planes on,
+  // shift(c) columns to the right between zeros, all b.ld columns of it
+  // written; vocab >= classes.count and exps is null.
+  FewClasses classes = {};
+  float2* stats = nullptr;        // [classes.count units][ld_stats]
   long long ld_stats = 0;
   void* exps = nullptr;
   long long ld_exps = 0;

@@ -292,43 +292,51 @@ __global__ void __launch_bounds__(kRescaleThreads)
 // into PARTS = 3 planes of bfloat16.  A value becomes hi + mid + lo: hi is the value truncated to bfloat16 (so
 // that it never overflows), mid and lo round what is left to nearest; the
 // rest is below 2^-25 of the value.
-// One launch takes x and w where both need it.
+// One launch takes x and w where both need it.  `copies` of x serve a w whose
+// rows are not on 16-byte boundaries (few_gemm.cu): copy c, its parts c PARTS
+// planes on, lies shift(c) columns to the right, with zeros on both sides.
 struct Packing {
   const void* src;
   void* dst;
   long long ld, ld_dst, plane;
   int rows, cols;
   int vectors;              // rows of src take 16-byte loads
+  int copies, shift0, step, mask;
+
+  __host__ __device__ long long vecs() const { return copies * rows * (ld_dst / 8); }
 };
 
 template <class T, int PARTS, class O>
 __global__ void __launch_bounds__(256) loss_pack_kernel(Packing x, Packing w, unsigned* err) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const long long all_x = static_cast<long long>(x.rows) * ((x.cols + 7) / 8);
-  const long long all = all_x + static_cast<long long>(w.rows) * ((w.cols + 7) / 8);
+  const long long all_x = x.vecs(), all = all_x + w.vecs();
   for (long long n = blockIdx.x * 256LL + threadIdx.x; n < all; n += gridDim.x * 256LL) {
     const Packing& m = n < all_x ? x : w;
     const long long i = n < all_x ? n : n - all_x;
-    const int per_row = (m.cols + 7) / 8;
-    const int r = static_cast<int>(i / per_row), c = static_cast<int>(i % per_row) * 8;
-    const T* const src = static_cast<const T*>(m.src);
-    const size_t at = static_cast<size_t>(r) * m.ld + c;
+    const int per_row = static_cast<int>(m.ld_dst / 8);
+    const int line = static_cast<int>(i / per_row);      // at most kFewRows kFewMostClasses, or rows
+    const int copy = line / m.rows, r = line - copy * m.rows;
+    const int shift = (m.shift0 + copy * m.step) & m.mask;
+    const int to = static_cast<int>(i - static_cast<long long>(line) * per_row) * 8, c = to - shift;
+    const T* const src = static_cast<const T*>(m.src) + static_cast<size_t>(r) * m.ld;
+    const size_t at = static_cast<size_t>(r) * m.ld;
     float v[8];
-    if (m.vectors && c + 8 <= m.cols) {
-      if (!GEMM_IN_EXTENT(at + 7, stored_extent(m.rows, m.cols, m.ld), err, kSiteBoundsRows)) continue;
+    if (m.vectors && shift == 0 && c + 8 <= m.cols) {
+      if (!GEMM_IN_EXTENT(at + c + 7, stored_extent(m.rows, m.cols, m.ld), err, kSiteBoundsRows)) continue;
       Raw<T, 8> raw;
-      raw.load_once(src + at);
+      raw.load_once(src + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = raw.at(j);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[j] = c + j < m.cols && GEMM_IN_EXTENT(at + j, stored_extent(m.rows, m.cols, m.ld), err, kSiteBoundsRows)
-                   ? to_f32(src[at + j])
+        v[j] = c + j >= 0 && c + j < m.cols &&
+                       GEMM_IN_EXTENT(at + c + j, stored_extent(m.rows, m.cols, m.ld), err, kSiteBoundsRows)
+                   ? to_f32(src[c + j])
                    : 0.0f;
     }
-    O* const out = static_cast<O*>(m.dst) + static_cast<size_t>(r) * m.ld_dst + c;
+    O* const out = static_cast<O*>(m.dst) + copy * PARTS * m.plane + static_cast<size_t>(r) * m.ld_dst + to;
     if constexpr (PARTS == 3) {
       float hi[8];
 #pragma unroll
@@ -402,35 +410,44 @@ struct Operand {
   const void* in(const void* p, const char* scratch) const { return form == kAsIs ? p : scratch + at; }
 };
 
+bool on_boundaries(const void* p, long long ld, int size) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+}
+
+// `classes`: of a w that x's copies serve, or null.
 Operand plan_operand(const void* p, long long ld, int rows, int cols, bool f32, bool split,
-                     Layout& layout) {
+                     const FewClasses* classes, Layout& layout) {
   Operand o;
   const int size = f32 ? 4 : 2;
   if (split)
     o.form = Operand::kSplit;
-  else if (reinterpret_cast<uintptr_t>(p) % 16 != 0 || ld * size % 16 != 0)
+  else if (classes || !on_boundaries(p, ld, size))
     o.form = Operand::kCopied;
   o.ld = ld;
   if (o.form != Operand::kAsIs) {
-    o.ld = static_cast<long long>(round_up(cols, 8));
+    o.ld = static_cast<long long>(round_up(static_cast<size_t>(cols) + (classes ? classes->mask : 0), 8));
     o.plane = o.ld * rows;
-    o.at = layout.take(static_cast<size_t>(o.plane) * (split ? 6 : size));
+    o.at = layout.take(static_cast<size_t>(o.plane) * (split ? 6 : size) * (classes ? classes->count : 1));
   }
   return o;
 }
 
 Packing packing(const Operand& o, const void* src, long long ld, int rows, int cols, bool f32,
-                char* scratch) {
-  Packing m = {src, scratch + o.at, ld, o.ld, o.plane, rows, cols, 0};
-  m.vectors = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld * (f32 ? 4 : 2) % 16 == 0;
+                const FewClasses* classes, char* scratch) {
+  Packing m = {src, scratch + o.at, ld, o.ld, o.plane, rows, cols, on_boundaries(src, ld, f32 ? 4 : 2), 1, 0, 0, 0};
+  if (classes) {
+    m.copies = classes->count;
+    m.shift0 = classes->shift0;
+    m.step = classes->step;
+    m.mask = classes->mask;
+  }
   return m;
 }
 
 // Packs x and w, which take the same form, or one of them (the other has no rows).
 int pack(Operand::Form form, const Packing& x, const Packing& w, bool f32, int num_sms, unsigned* err,
          cudaStream_t stream, int* launches) {
-  const long long work = static_cast<long long>(x.rows) * ((x.cols + 7) / 8) +
-                         static_cast<long long>(w.rows) * ((w.cols + 7) / 8);
+  const long long work = x.vecs() + w.vecs();
   const dim3 grid(static_cast<unsigned>(std::min<long long>((work + 255) / 256, 16LL * num_sms)));
   return form == Operand::kSplit
              ? launch(loss_pack_kernel<float, 3, bf16>, grid, 256, stream, launches, x, w, err)
@@ -443,11 +460,19 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   unsigned* err = nullptr;
   if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
   const bool f32 = c.type == GEMM_F32_TYPE_F32, grad = c.dx || c.dw;
-  const bool few = c.rows <= (f32 ? kFewRows : kFewRowsBf16);
+  // the losses alone of few rows read a w off 16-byte boundaries where it lies
+  // (bfloat16 x 4095 x 65535: 8 rows 114 us against 339 with w copied first,
+  // 128 rows 159 against 350); with gradients dx needs the copy anyway
+  const FewClasses by_class = few_classes(f32, c.w, c.ldw, c.vocab);
+  const bool direct = !grad && !by_class.aligned() && c.rows <= kFewRows && c.vocab >= by_class.count;
+  const bool few = direct || c.rows <= (f32 ? kFewRows : kFewRowsBf16);
   const int parts = f32 ? 3 : 1;
   const long long ld_exps = static_cast<long long>(round_up(c.vocab, 256));
   const int piece_bits = few ? kFewPieceBits : kPieceBits;
-  const int pieces = few ? (c.vocab + kFewPiece - 1) / kFewPiece : static_cast<int>(ld_exps >> kPieceBits);
+  const FewClasses* const classes = direct ? &by_class : nullptr;
+  const int pieces = direct ? by_class.count * by_class.units
+                     : few  ? (c.vocab + kFewPiece - 1) / kFewPiece
+                            : static_cast<int>(ld_exps >> kPieceBits);
 
   // rows per piece: bounded by the exponentials (and the parts of g), or by
   // the statistics alone
@@ -469,8 +494,10 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   const long long ld_stats = static_cast<long long>(round_up(step, 32));
   const size_t at_stats = layout.take(sizeof(float2) * pieces * ld_stats);
   const size_t at_joined = grad ? layout.take(sizeof(float2) * step) : 0;
-  const Operand ox = plan_operand(c.x, c.ldx, c.rows, c.width, f32, f32, layout);
-  const Operand ow = plan_operand(c.w, c.ldw, c.vocab, c.width, f32, f32 && !few, layout);
+  const Operand ox = plan_operand(c.x, c.ldx, c.rows, c.width, f32, f32, classes, layout);
+  Operand ow;
+  ow.ld = c.ldw;
+  if (!direct) ow = plan_operand(c.w, c.ldw, c.vocab, c.width, f32, f32 && !few, nullptr, layout);
   size_t at_exps = 0, at_g = 0, at_partials = 0, at_sum = 0;
   if (grad) {
     at_exps = layout.take(static_cast<size_t>(step) * ld_exps * (f32 ? 4 : 2));
@@ -493,8 +520,8 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   float* const logit = reinterpret_cast<float*>(scratch + at_logit);
   float2* const stats = reinterpret_cast<float2*>(scratch + at_stats);
   const LossTargets all = {c.targets, c.target_bits, c.vocab, c.ignore};
-  const Packing px = packing(ox, c.x, c.ldx, c.rows, c.width, f32, scratch);
-  const Packing pw = packing(ow, c.w, c.ldw, c.vocab, c.width, f32, scratch);
+  const Packing px = packing(ox, c.x, c.ldx, c.rows, c.width, f32, classes, scratch);
+  const Packing pw = packing(ow, c.w, c.ldw, c.vocab, c.width, f32, nullptr, scratch);
   int rc = GEMM_F32_OK;
   if (ox.form == ow.form && ox.form != Operand::kAsIs) {
     rc = pack(ox.form, px, pw, f32, num_sms, err, stream, launches);
@@ -530,6 +557,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     if (few) {
       FewGemm z = few_base;
       z.b = x;
+      z.classes = few_classes(f32, z.w, z.ldw, c.vocab);
       z.stats = stats;
       z.ld_stats = ld_stats;
       z.exps = grad ? scratch + at_exps : nullptr;

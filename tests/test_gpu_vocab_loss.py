@@ -151,6 +151,47 @@ def test_strided_operands(pad, first, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,width,vocab", [(1, 1, 8), (1, 7, 9), (2, 63, 5), (16, 65, 300), (33, 1023, 2051),
+                                              (31, 1022, 2049), (65, 1020, 1000), (128, 509, 1777), (129, 509, 1777),
+                                              (5, 2049, 5001), (8, 121, 40000), (3, 60, 8)])
+@pytest.mark.parametrize("first", [0, 1, 3])
+def test_strided_few_rows_off_boundaries(rows, width, vocab, first, kind):
+    """Rows of w at every distance from a 16-byte boundary, between NaN; every class of them has a label."""
+    torch, types = _torch()
+    g = lib()
+    x, w, y = _inputs(rows, width, vocab, kind, width + first, ignored=0.0)
+    if rows > 8:
+        y[:8] = torch.arange(vocab - 8, vocab, device="cuda").clamp(min=0)
+    flat = torch.full((first + vocab * width + 16,), float("nan"), device="cuda", dtype=types[kind])
+    wide = flat[first:first + vocab * width].view(vocab, width)
+    wide.copy_(w)
+    _check(g.vocab_loss(x, wide, y), _exact(x, w, y, kind))
+    pitch = width + 1 + first
+    flat = torch.full((first + vocab * pitch + 16,), float("nan"), device="cuda", dtype=types[kind])
+    wide = flat[first:first + vocab * pitch].view(vocab, pitch)[:, :width]
+    wide.copy_(w)
+    got = g.vocab_loss(x, wide, y)
+    _check(got, _exact(x, w, y, kind))
+    assert all(torch.equal(a, b) for a, b in zip(got, g.vocab_loss(x, wide, y)))
+    assert g.gemm_f32_status(None) == (0, 0)
+
+
+@pytest.mark.parametrize("width", [67, 130])
+def test_an_infinite_row_of_w_off_boundaries(width):
+    """One row of w gives a logit of -inf (a vocabulary entry that is never taken); its neighbours keep theirs.
+    In bfloat16, whose products are single ones (an infinite operand in parts gives NaN)."""
+    torch, _ = _torch()
+    g = lib()
+    kind = "bf16"
+    x, w, y = _inputs(6, width, 400, kind, 5, ignored=0.0)
+    x, y = x.abs() + 0.25, y.clamp(max=300)
+    keep = torch.arange(400, device="cuda") != 333
+    want = _exact(x, w[keep], torch.where(y > 333, y - 1, y), kind)
+    w[333] = float("-inf")
+    _check(g.vocab_loss(x, w, y), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_rows_that_do_not_count(kind):
     """No row, one row and no counted row; int32 targets; another ignore_index; a target outside the vocabulary."""
     torch, _ = _torch()
