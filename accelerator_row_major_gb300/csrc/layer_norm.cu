@@ -403,22 +403,33 @@ int launch_stream(const NormArgs& a, bool ragged, size_t size, size_t least_smem
   constexpr int kGroups = stream_threads(G) / G;
   // a multiple of 8 groups on ragged rows: of one start each
   constexpr int kWhole = 8 / kGroups > 1 ? 8 / kGroups : 1;
-  const int units = ragged ? num_sms / CTAS / kWhole * kWhole : num_sms / CTAS, grid = units * CTAS;
-  const int slice = CTAS == 1 ? a.width : ((a.width + CTAS - 1) / CTAS + 7) / 8 * 8;
-  const size_t row = ring_row_bytes(slice, size, ragged) * ARRAYS;
-  const int stages = static_cast<int>(std::min<size_t>(kMostStages, kStreamBytes / (kGroups * (row + 8))));
-  if (a.rows < static_cast<long long>(kStreamRows) * units * kGroups || stages < 2 || units == 0) return 1;
-  const size_t smem = std::max(least_smem, kGroups * stages * (row + 8));
-  static std::atomic<unsigned long long> configured{0};   // of this kernel: a bit per device
-  const unsigned long long bit = 1ull << (device % 64);
-  if (!(configured.load() & bit)) {
+  static std::atomic<int> resident[64];    // of this kernel: CTAs or clusters at a time, per device
+  int most = resident[device % 64].load();
+  if (most == 0) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kStreamBytes)) != cudaSuccess) {
       (void)cudaGetLastError();
       return GEMM_F32_ELAUNCH;
     }
-    configured.fetch_or(bit);
+    most = num_sms;
+    if (CTAS > 1) {   // as many as run at once (36 of four CTAs: 2048 x 32768 bfloat16 96 us, 167 with 38)
+      cudaLaunchConfig_t config = {};
+      config.gridDim = dim3(num_sms / CTAS * CTAS);
+      config.blockDim = dim3(stream_threads(G));
+      config.dynamicSmemBytes = kStreamBytes;
+      if (cudaOccupancyMaxActiveClusters(&most, kernel, &config) != cudaSuccess || most < 1) {
+        (void)cudaGetLastError();
+        return GEMM_F32_ELAUNCH;
+      }
+    }
+    resident[device % 64].store(most);
   }
+  const int units = ragged ? most / kWhole * kWhole : most, grid = units * CTAS;
+  const int slice = CTAS == 1 ? a.width : ((a.width + CTAS - 1) / CTAS + 7) / 8 * 8;
+  const size_t row = ring_row_bytes(slice, size, ragged) * ARRAYS;
+  const int stages = static_cast<int>(std::min<size_t>(kMostStages, kStreamBytes / (kGroups * (row + 8))));
+  if (a.rows < static_cast<long long>(kStreamRows) * units * kGroups || stages < 2 || units == 0) return 1;
+  const size_t smem = std::max(least_smem, kGroups * stages * (row + 8));
   *parts = units;
   if (launch_dependent(kernel, dim3(grid), dim3(stream_threads(G)), smem, stream, a, stages, slice) !=
       cudaSuccess) {
