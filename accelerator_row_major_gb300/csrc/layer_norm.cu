@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <numeric>
 #include <cstdint>
 
 #include "../../include/gemm_f32_lm.h"
@@ -402,7 +403,7 @@ int launch_stream(const NormArgs& a, bool ragged, size_t size, size_t least_smem
                   int* parts, cudaStream_t stream) {
   constexpr int kGroups = stream_threads(G) / G;
   // a multiple of 8 groups on ragged rows: of one start each
-  constexpr int kWhole = 8 / kGroups > 1 ? 8 / kGroups : 1;
+  constexpr int kWhole = 8 / std::gcd(8, kGroups);
   static std::atomic<int> resident[64];    // of this kernel: CTAs or clusters at a time, per device
   int most = resident[device % 64].load();
   if (most == 0) {
@@ -476,10 +477,15 @@ int forward(const NormArgs& a, Rows rows, int device, int num_sms, cudaStream_t 
     const int e = a.width + (vectors ? 0 : V - 1);   // a row's start may take part of a vector
     const int rc = e <= 256     ? stream_forward<T, WT, 32, 8>(a, rows, device, num_sms, stream)
                    : e <= 512   ? stream_forward<T, WT, 32, 16>(a, rows, device, num_sms, stream)
+                   : e <= 768   ? stream_forward<T, WT, 32, 24>(a, rows, device, num_sms, stream)
                    : e <= 1024  ? stream_forward<T, WT, 32, 32>(a, rows, device, num_sms, stream)
+                   : e <= 1536  ? stream_forward<T, WT, 64, 24>(a, rows, device, num_sms, stream)
                    : e <= 2048  ? stream_forward<T, WT, 64, 32>(a, rows, device, num_sms, stream)
+                   : e <= 3072  ? stream_forward<T, WT, 128, 24>(a, rows, device, num_sms, stream)
                    : e <= 4096  ? stream_forward<T, WT, 128, 32>(a, rows, device, num_sms, stream)
+                   : e <= 6144  ? stream_forward<T, WT, 256, 24>(a, rows, device, num_sms, stream)
                    : e <= 8192  ? stream_forward<T, WT, 256, 32>(a, rows, device, num_sms, stream)
+                   : e <= 12288 ? stream_forward<T, WT, 512, 24>(a, rows, device, num_sms, stream)
                    : e <= 16384 ? stream_forward<T, WT, 512, 32>(a, rows, device, num_sms, stream)
                                 : 1;
     if (rc != 1) return rc;
@@ -544,9 +550,13 @@ int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_
          : e <= 256   ? stream_grad<T, WT, 32, 8>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 512   ? stream_grad<T, WT, 32, 16>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 1024  ? stream_grad<T, WT, 64, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 1536  ? stream_grad<T, WT, 96, 16>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 2048  ? stream_grad<T, WT, 128, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 3072  ? stream_grad<T, WT, 192, 16>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 4096  ? stream_grad<T, WT, 256, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 6144  ? stream_grad<T, WT, 384, 16>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 8192  ? stream_grad<T, WT, 512, 16>(a, rows, parts, device, num_sms, &ctas, stream)
+         : e <= 12288 ? stream_grad<T, WT, 384, 16, 2>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 16384 ? stream_grad<T, WT, 512, 16, 2>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 32768 ? stream_grad<T, WT, 512, 16, 4>(a, rows, parts, device, num_sms, &ctas, stream)
                       : 1;

@@ -2,13 +2,17 @@
 //
 // Each group of G threads works on one row at a time and keeps the next rows
 // in a ring in shared memory, filled by bulk copies (cp.async.bulk on
-// mbarriers).  One CTA of 512 threads per SM.
-// Threads hold 32 elements of a row in the forward pass and 16 in the
+// mbarriers).  One CTA of 512 threads (or the groups that 512 make) per SM.
+// Threads hold up to 32 elements of a row in the forward pass and 16 in the
 // gradient: what a row costs besides its elements (reductions, barriers) is then
 // paid by few warps, and the arithmetic is done two elements at a time
 // (f32x2).  With 8 elements a thread the issue of instructions bound both
 // kernels (65536 x 1024 bfloat16: 60 and 91 us against 47 and 70; the copy
-// rate allows 40 and 59).
+// rate allows 40 and 59).  What the row leaves of a group's elements costs as
+// much as the row's, so besides the powers of 2 there are groups that hold
+// 3/4 of them: 24 elements a thread, or in the gradient, whose registers hold
+// no more than 16, three warps for four (1280 columns of 52428 rows in
+// bfloat16: 52 and 79 us against 59 and 100 with room for 2048).
 //
 // RAGGED: rows that do not all start and end on 16-byte boundaries.  A row is
 // copied from the boundary below its start to the one above its end (never
@@ -70,7 +74,7 @@ __device__ __forceinline__ bool row_ok(const NormArgs& a, size_t at, int n, long
 }
 
 // ---------------------------------------------------------------- rings
-constexpr int stream_threads(int g) { return g < 512 ? 512 : g; }
+constexpr int stream_threads(int g) { return 512 / g * g; }   // whole groups
 constexpr size_t kStreamBytes = 200 * 1024;
 constexpr int kMostStages = 8;
 
