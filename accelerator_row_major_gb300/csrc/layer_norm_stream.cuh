@@ -21,10 +21,9 @@
 // first and the last hold elements of other rows.  Rows start 0 to 14 bytes
 // above a boundary, each of 16 / gcd(16, stride) rows differently; the number
 // of groups is a multiple of that, so that a group meets rows of one start
-// only, and its threads keep their columns.  (65536 x 777 fp32: 71 and 117 us,
-// copies 60 and 90; 65536 x 1001 bfloat16: 75 and 113 us, copies 39 and 58.
-// Before, with the elements read one by one by the threads, 65536 x 1023
-// bfloat16 took 119 and 144.)
+// only, and its threads keep their columns.  (65536 x 777 fp32: 71 and 102 us,
+// copies 60 and 90; 65536 x 1001 bfloat16: 62 and 87 us, copies 39 and 58,
+// bound by the instructions that the rows' ends cost.)
 //
 // CTAS > 1 (gradient of rows wider than 8192): a cluster shares a row, each
 // CTA a slice of its columns, and exchanges the two sums of the row through
@@ -98,6 +97,7 @@ struct RowRing {
   const NormArgs& a;
   uint8_t* data;
   uint32_t bars, row_bytes;
+  uint32_t around = 0;          // RAGGED: bytes of the 16-byte blocks around a row of this group
   int width, col0, stages, s = 0;
   uint32_t ph = 0;
   bool lost = false;
@@ -112,6 +112,7 @@ struct RowRing {
            static_cast<uint32_t>(group) * st * 8u;
     step = static_cast<long long>(gridDim.x / ctas) * groups;
     next = static_cast<long long>(blockIdx.x / ctas) * groups + group;
+    if (RAGGED) around = ((shift() + width) * static_cast<uint32_t>(sizeof(T)) + 15u) & ~15u;
   }
   // One thread of the group, before the group's first barrier.
   __device__ __forceinline__ void init() {
@@ -127,7 +128,14 @@ struct RowRing {
     if (next < a.rows) {
       const uint32_t bar = bars + 8u * at;
       uint8_t* const dst = data + static_cast<size_t>(at) * ARRAYS * row_bytes;
-      if constexpr (RAGGED) {
+      if (RAGGED && next > 0 && next < a.rows - 1) {   // the blocks around the row are the matrix's
+        mbar_arrive_expect_tx(bar, ARRAYS * around);
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i)
+          bulk_load(smem_addr(dst) + i * row_bytes,
+                    reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(source(i, next)) & ~uintptr_t{15}),
+                    around, bar);
+      } else if constexpr (RAGGED) {
         uint32_t bytes[ARRAYS];
         uintptr_t from[ARRAYS];
 #pragma unroll
@@ -194,23 +202,69 @@ struct RowRing {
 };
 
 // ---------------------------------------------------------------- a thread's part of a row
+// RAGGED: which elements of a 16-byte vector are the row's, as bits and as
+// factors.  Entry 0: all; entry e < 8: all but the first e; entry 8 + n: the
+// first n.
+template <class T>
+struct Edges {
+  static constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  T cut[16][2][kVec];                    // of each warp: its cut vectors, as stored
+  uint4 bits[16];
+  float ones[16][kVec];
+
+  __device__ __forceinline__ void fill() {
+    const int e = threadIdx.x;
+    if (e >= 16) return;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const bool in = e < 8 ? i >= e : i < e - 8;
+      ones[e][i] = in ? 1.0f : 0.0f;
+      if (in) w[i * static_cast<int>(sizeof(T)) / 4] |= sizeof(T) == 4 ? ~0u : 0xFFFFu << (16 * (i & 1));
+    }
+    bits[e] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+__device__ __forceinline__ void keep(uint4& q, const uint4& bits) {
+  q.x &= bits.x;
+  q.y &= bits.y;
+  q.z &= bits.z;
+  q.w &= bits.w;
+}
+
 // NP pairs of elements: vector i of thread t holds the elements from column
-// (i G + t) VEC - shift on.
-template <class T, int G, int NP, bool RAGGED>
+// (i G + t) VEC - shift on.  Of a ragged row the first vector of thread 0 and
+// vector i_last of one thread are cut.  All threads take these two vectors
+// through masks (of all elements, but for the threads that hold the cut ones):
+// less work for a warp than branches of one thread (65536 x 1001 bfloat16:
+// 77 and 108 us against 75 and 113, then 69 and 87 with the rows inside the
+// matrix copied without a look at its ends, 62 forward with staged stores).
+template <class T, int G, int NP, bool RAGGED, bool STAGED>
 struct Part {
   static constexpr int kPer = 8 / static_cast<int>(sizeof(T));   // pairs per vector
   static constexpr int kVec = 2 * kPer;
   static constexpr int NV = NP / kPer;
+  Edges<T>& edges;
   int width, first;                      // columns of the row, column of vector 0
-  int last = -1;                         // a vector that ends outside the row
-  bool edge = false;                     // a vector of this thread lies partly in the row
+  int i_last = -1;
+  int head = 0, tail = 0;                // entries of the masks
+  int cut_col = -1;                      // STAGED: column of the element of a cut vector that this lane stores
 
-  __device__ __forceinline__ Part(int w, int shift, int t) : width(w), first(t * kVec - shift) {
+  __device__ __forceinline__ Part(Edges<T>& e, int w, int shift, int t)
+      : edges(e), width(w), first(t * kVec - shift) {
     if constexpr (RAGGED) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (any(i) && col(i) + kVec > width) last = i;
-      edge = first < 0 || last >= 0;
+      const int last = (w + shift - 1) / kVec, part = (w + shift) % kVec;
+      i_last = last / G;
+      if (t == 0) head = shift;
+      if (t == last % G && part != 0) tail = 8 + part;
+      if constexpr (STAGED) {           // lanes 0 .. VEC - 1 the first vector, the next VEC the last
+        const int at = t % kVec, of = t % 32 / kVec;
+        const bool both = last == 0 && part != 0;              // one vector, cut at both ends
+        if (of == 0 && t < 32 && at >= shift && shift != 0 && !both) cut_col = at - shift;
+        if (of == 1 && t / 32 == last % G / 32 && at < part && (last != 0 || at >= shift))
+          cut_col = last * kVec + at - shift;
+      }
     }
   }
   __device__ __forceinline__ int col(int i) const { return i * (G * kVec) + first; }
@@ -219,38 +273,50 @@ struct Part {
   }
   __device__ __forceinline__ bool in(int d) const { return d >= 0 && d < width; }
 
-  // Whether vector i lies partly in the row: the first or the last one.
-  __device__ __forceinline__ bool cut(int i) const { return i == last || (i == 0 && first < 0); }
-
-  // 0 for what lies outside the row: behind a branch that hardly a thread
-  // takes, and only in the vectors that are cut.
-  __device__ __forceinline__ void mask(Pair (&x)[NP]) const {
-    if constexpr (RAGGED) {
-      if (!edge) return;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (cut(i)) {
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            float u, v;
-            unpair(x[i * kPer + j], u, v);
-            x[i * kPer + j] = pair_of(in(col(i) + 2 * j) ? u : 0.0f, in(col(i) + 2 * j + 1) ? v : 0.0f);
-          }
-        }
-    }
-  }
-
+  // The row's elements, 0 for what lies outside it.
   __device__ __forceinline__ void load(const uint8_t* copy, int t, Pair (&x)[NP]) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       Pair v[kPer];
+      if constexpr (RAGGED) {
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (any(i)) q = *reinterpret_cast<const uint4*>(copy + (i * G + t) * 16);
+        if (i == 0) keep(q, edges.bits[head]);
+        if (i == i_last) keep(q, edges.bits[tail]);
+        pairs_of<T>(q, v);
+      } else {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) v[j] = 0;
-      if (any(i)) load_pairs<T>(reinterpret_cast<const T*>(copy) + (i * G + t) * kVec, v);
+        for (int j = 0; j < kPer; ++j) v[j] = 0;
+        if (any(i)) pairs_of<T>(*reinterpret_cast<const uint4*>(copy + (i * G + t) * 16), v);
+      }
 #pragma unroll
       for (int j = 0; j < kPer; ++j) x[i * kPer + j] = v[j];
     }
-    mask(x);
+  }
+
+  // sum plus the squares of a ragged row's elements; what lies outside is finite.
+  __device__ __forceinline__ Pair add_squares(const Pair (&x)[NP], Pair sum) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Pair v[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = x[i * kPer + j];
+      if (i == 0) scale(v, edges.ones[head]);
+      if (i == i_last) scale(v, edges.ones[tail]);
+      if (any(i)) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum = fma2(v[j], x[i * kPer + j], sum);
+      }
+    }
+    return sum;
+  }
+  static __device__ __forceinline__ void scale(Pair (&v)[kPer], const float* by) {
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) {
+      const float4 f = *reinterpret_cast<const float4*>(by + 2 * j);
+      v[j] = mul2(v[j], pair_of(f.x, f.y));
+      v[j + 1] = mul2(v[j + 1], pair_of(f.z, f.w));
+    }
   }
 
   template <class WT>
@@ -273,27 +339,85 @@ struct Part {
     }
   }
 
+  // Cut vectors: staged, through shared memory, from where as many lanes
+  // store an element each; else a few stores by the thread that holds them,
+  // which take a warp more instructions but no register (65472 x 1025
+  // bfloat16 forward 81 us against 97; gradient of 32880 x 2041 97 against 87).
   __device__ __forceinline__ void store(T* y, const Pair (&x)[NP]) const {
-    if (RAGGED && edge) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (cut(i)) {
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const int d = col(i) + 2 * j;
-            float u, v;
-            unpair(x[i * kPer + j], u, v);
-            if (in(d)) y[d] = from_f32<T>(u);
-            if (in(d + 1)) y[d + 1] = from_f32<T>(v);
-          }
-        }
-    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       Pair v[kPer];
 #pragma unroll
       for (int j = 0; j < kPer; ++j) v[j] = x[i * kPer + j];
-      if (any(i) && !(RAGGED && cut(i))) store_pairs<T>(y + col(i), v);
+      bool whole = any(i);
+      if constexpr (RAGGED) {
+        const bool from = i == 0 && head != 0, to = i == i_last && tail != 0;
+        if constexpr (STAGED) {
+          if (from) store_pairs(edges.cut[threadIdx.x / 32][0], v);
+          if (to) store_pairs(edges.cut[threadIdx.x / 32][1], v);
+          if (from || to) whole = false;
+        } else if (from || to) {
+          store_cut(y + col(i), v, from ? head : 0, to ? tail - 8 : kVec);
+          whole = false;
+        }
+      }
+      if (whole) store_pairs(y + col(i), v);
+    }
+    if constexpr (STAGED) {
+      __syncwarp();
+      if (cut_col >= 0) y[cut_col] = (&edges.cut[threadIdx.x / 32][0][0])[threadIdx.x % 32];
+      __syncwarp();                     // read, before the next row's are written
+    }
+  }
+  // Elements [b, e) of the vector at y, one of whose ends is the vector's (of
+  // a row of a few elements neither may be), as 2, 4 and 8 bytes.
+  static __device__ __forceinline__ void store_cut(T* y, const Pair (&v)[kPer], int b, int e) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      float f, g;
+      unpair(v[j], f, g);
+      if constexpr (sizeof(T) == 4) {
+        w[2 * j] = __float_as_uint(f);
+        w[2 * j + 1] = __float_as_uint(g);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f, g);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    const auto put = [&](int j) {                               // element j
+      if constexpr (sizeof(T) == 4)
+        reinterpret_cast<uint32_t*>(y)[j] = w[j];
+      else
+        reinterpret_cast<uint16_t*>(y)[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    };
+    if (b != 0 && e != kVec) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (j >= b && j < e) put(j);
+      return;
+    }
+    constexpr int kWord = 4 / static_cast<int>(sizeof(T));      // elements in 4 bytes
+    uint32_t* const words = reinterpret_cast<uint32_t*>(y);
+    // the odd element, the odd word and the half that make up the part
+    const int n = e - b, odd_at = b != 0 ? b : e - 1;
+    const int word = b != 0 ? (b + kWord - 1) / kWord : e / kWord - 1;   // of the part's whole words, the outermost
+    const int whole = n / kWord;                                         // whole words: 0 .. 3
+    if (kWord == 2 && (n & 1)) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (j == odd_at) put(j);
+    }
+    if (whole & 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j == word) words[j] = w[j];
+    }
+    if (whole & 2) {
+      if (b != 0)
+        reinterpret_cast<uint2*>(y)[1] = make_uint2(w[2], w[3]);
+      else
+        reinterpret_cast<uint2*>(y)[0] = make_uint2(w[0], w[1]);
     }
   }
 };
@@ -304,14 +428,16 @@ __global__ void __launch_bounds__(stream_threads(G), 1)
     layer_norm_stream_kernel(NormArgs a, int stages, int slice) {
   constexpr int kGroups = stream_threads(G) / G;
   extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ Edges<T> edges;
   __shared__ float part[2][kGroups][G / 32];
   const int group = threadIdx.x / G, t = threadIdx.x % G;
   RowRing<T, 1, RAGGED> ring(a, smem_rows, group, kGroups, stages, slice, 0, 1);
   if (t == 0) ring.init();
+  if (RAGGED) edges.fill();
   __syncthreads();
   grid_launch_dependents();
   grid_dependency_wait();
-  const Part<T, G, NP, RAGGED> mine(a.width, ring.shift(), t);
+  const Part<T, G, NP, RAGGED, RAGGED> mine(edges, a.width, ring.shift(), t);
   long long row = ring.next;
   if (t == 0)
     for (int i = 0; i < stages; ++i) ring.load(i);
@@ -331,13 +457,16 @@ __global__ void __launch_bounds__(stream_threads(G), 1)
     ring.advance();
     const float mean = s[0] * inv;
     const Pair minus = pair_of(-mean, -mean);
-    sum = 0;
 #pragma unroll
     for (int q = 0; q < NP; ++q) x[q] = add2(x[q], minus);
-    mine.mask(x);
+    sum = 0;
+    if constexpr (RAGGED) {
+      sum = mine.add_squares(x, sum);
+    } else {
 #pragma unroll
-    for (int q = 0; q < NP; ++q)
-      if (mine.any(q / mine.kPer)) sum = fma2(x[q], x[q], sum);
+      for (int q = 0; q < NP; ++q)
+        if (mine.any(q / mine.kPer)) sum = fma2(x[q], x[q], sum);
+    }
     s[0] = sum_of(sum);
     group_sum<1, G>(s, part[1][group], group);
     const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
@@ -368,6 +497,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G)
   constexpr int kGroups = kThreads / G;
   static_assert(CTAS == 1 || kGroups == 1, "a cluster works on one row");
   extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ Edges<T> edges;
   __shared__ float part[2][kGroups][2 * (G / 32)];
   __shared__ float2 shared_sums[2][CTAS];              // of the CTAs of the cluster
   __shared__ uint64_t shared_bars[2];
@@ -380,11 +510,12 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G)
   if (threadIdx.x == 0 && CTAS > 1)
     for (int i = 0; i < 2; ++i) mbar_init(bars + 8u * i, 1);
   if (t == 0) ring.init();
+  if (RAGGED) edges.fill();
   __syncthreads();
   if (CTAS > 1) cluster_sync();              // every CTA of the cluster runs
   grid_launch_dependents();
   grid_dependency_wait();
-  const Part<T, G, NP, RAGGED> mine(width, ring.shift(), t);
+  const Part<T, G, NP, RAGGED, false> mine(edges, width, ring.shift(), t);
   long long row = ring.next;
   if (t == 0)
     for (int i = 0; i < stages; ++i) ring.load(i);

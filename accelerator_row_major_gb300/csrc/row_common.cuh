@@ -114,10 +114,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// The 16 bytes at p (shared or global memory) as pairs: 2 of fp32, 4 of bfloat16.
+// 16 bytes as pairs: 2 of fp32, 4 of bfloat16.
 template <class T>
-__device__ __forceinline__ void load_pairs(const T* p, Pair (&v)[8 / sizeof(T)]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void pairs_of(const uint4& q, Pair (&v)[8 / sizeof(T)]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   if constexpr (sizeof(T) == 4) {
     v[0] = pair_of(__uint_as_float(w[0]), __uint_as_float(w[1]));
