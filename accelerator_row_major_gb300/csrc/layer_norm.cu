@@ -426,7 +426,9 @@ int launch_stream(const NormArgs& a, bool ragged, size_t size, size_t least_smem
     resident[device % 64].store(most);
   }
   const int units = ragged ? most / kWhole * kWhole : most, grid = units * CTAS;
-  const int slice = CTAS == 1 ? a.width : ((a.width + CTAS - 1) / CTAS + 7) / 8 * 8;
+  // of a shared row: whole 16-byte blocks, of which a ragged row may take one more than its elements fill
+  const int blocks = a.width + (ragged ? 16 / static_cast<int>(size) - 1 : 0);
+  const int slice = CTAS == 1 ? a.width : ((blocks + CTAS - 1) / CTAS + 7) / 8 * 8;
   const size_t row = ring_row_bytes(slice, size, ragged) * ARRAYS;
   const int stages = static_cast<int>(std::min<size_t>(kMostStages, kStreamBytes / (kGroups * (row + 8))));
   if (a.rows < static_cast<long long>(kStreamRows) * units * kGroups || stages < 2 || units == 0) return 1;

@@ -26,7 +26,7 @@
 // bound by the instructions that the rows' ends cost.)
 //
 // CTAS > 1 (gradient of rows wider than 8192): a cluster shares a row, each
-// CTA a slice of its columns, and exchanges the two sums of the row through
+// CTA a slice of its columns (cut on 16-byte boundaries), and exchanges the two sums of the row through
 // distributed shared memory: asynchronous stores that a barrier at their
 // destination counts.  A barrier of the cluster in their place would wait for
 // every store of dx in flight (4096 x 16384 bfloat16 133 us against 90, fp32
@@ -91,7 +91,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // The ring of one group: ARRAYS rows per stage (x, or x and dy), filled for
 // the group's rows first, first + step, ..., `stages` ahead.  Of each row the
-// `width` elements from column `col0` on.
+// `width` elements from column `col0` on: all of it, or where `ctas` CTAs
+// share a row the slice of CTA `rank`.  Slices are cut on 16-byte boundaries,
+// so that no CTA has more than `slice` elements of whole blocks to hold: a row
+// that starts above a boundary leaves the first CTA so many elements fewer.
 template <class T, int ARRAYS, bool RAGGED>
 struct RowRing {
   const NormArgs& a;
@@ -104,14 +107,19 @@ struct RowRing {
   long long next, step;
 
   __device__ __forceinline__ RowRing(const NormArgs& args, uint8_t* smem, int group, int groups, int st,
-                                     int slice, int first_col, int ctas)
-      : a(args), width(min(slice, args.width - first_col)), col0(first_col), stages(st) {
+                                     int slice, int rank, int ctas)
+      : a(args), width(args.width), col0(0), stages(st) {
     row_bytes = static_cast<uint32_t>(ring_row_bytes(slice, sizeof(T), RAGGED));
     data = smem + static_cast<size_t>(group) * st * ARRAYS * row_bytes;
     bars = smem_addr(smem) + static_cast<uint32_t>(groups) * st * ARRAYS * row_bytes +
            static_cast<uint32_t>(group) * st * 8u;
     step = static_cast<long long>(gridDim.x / ctas) * groups;
     next = static_cast<long long>(blockIdx.x / ctas) * groups + group;
+    if (ctas > 1) {
+      const int lead = shift();            // of the whole row
+      if (rank > 0) col0 = rank * slice - lead;
+      width = min(rank > 0 ? slice : slice - lead, args.width - col0);
+    }
     if (RAGGED) around = ((shift() + width) * static_cast<uint32_t>(sizeof(T)) + 15u) & ~15u;
   }
   // One thread of the group, before the group's first barrier.
@@ -189,7 +197,7 @@ struct RowRing {
   __device__ __forceinline__ const uint8_t* at(int array) const {
     return data + (static_cast<size_t>(s) * ARRAYS + array) * row_bytes;
   }
-  // Elements by which the group's rows start above a 16-byte boundary.
+  // Elements by which the group's rows (or slices) start above a 16-byte boundary.
   __device__ __forceinline__ int shift() const {
     return RAGGED ? static_cast<int>((reinterpret_cast<uintptr_t>(source(0, next)) & 15) / sizeof(T)) : 0;
   }
@@ -503,9 +511,8 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G)
   __shared__ uint64_t shared_bars[2];
   const int group = threadIdx.x / G, t = threadIdx.x % G;
   const int rank = CTAS > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int col0 = rank * slice;
-  RowRing<T, 2, RAGGED> ring(a, smem_rows, group, kGroups, stages, slice, col0, CTAS);
-  const int width = ring.width;                        // of this CTA's slice
+  RowRing<T, 2, RAGGED> ring(a, smem_rows, group, kGroups, stages, slice, rank, CTAS);
+  const int width = ring.width, col0 = ring.col0;      // of this CTA's slice
   const uint32_t bars = smem_addr(shared_bars);
   if (threadIdx.x == 0 && CTAS > 1)
     for (int i = 0; i < 2; ++i) mbar_init(bars + 8u * i, 1);

@@ -1,0 +1,40 @@
+"""Gradient of wide norms whose rows a cluster shares: rows off 16-byte
+boundaries at the widths where a slice fills the threads that hold it.
+Inputs, tolerances and the 64-bit forms are those of test_gpu_layer_norm.py."""
+import pytest
+
+from tests._gpu import lib
+from tests.test_gpu_layer_norm import _check_grad, _inputs, _torch
+
+pytestmark = pytest.mark.gpu
+
+ROWS = 330          # above four rows for each cluster of two CTAs (76 of them)
+
+
+def _at(t, first):
+    """t's values in a dense matrix that starts `first` elements above a boundary, between sevens."""
+    torch, _ = _torch()
+    buf = torch.full((t.numel() + first + 16,), 7.0, device="cuda", dtype=t.dtype)
+    view = buf[first:first + t.numel()].view(t.shape)
+    view.copy_(t)
+    return buf, view
+
+
+def _gradient(x, dy, w, mean, rstd, first, kind, wkind):
+    """layer_norm_grad on copies `first` elements above a boundary; nothing outside dx is written."""
+    g = lib()
+    (_, xs), (_, ds), (buf, out) = _at(x, first), _at(dy, first), _at(x * 0 + 5, first)
+    dx, dw, db = g.layer_norm_grad(ds, xs, w, mean, rstd, out=out)
+    _check_grad(x, dy, w, mean, rstd, dx, dw, db, kind, wkind)
+    assert (buf[:first] == 7).all() and (buf[first + out.numel():] == 7).all()
+    assert g.gemm_f32_status(None) == (0, 0)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [12273, 12277, 12280, 12281, 12285, 12288, 16369, 16376, 16377, 16381, 16384,
+                                   32737, 32744, 32761, 32765, 32768])
+def test_full_slices_at_every_alignment(width, kind):
+    x, dy, w, b = _inputs(ROWS, width, kind, "f32", width)
+    _, mean, rstd = lib().layer_norm(x, w, b)
+    for first in (0, 1, 2, 3) if kind == "f32" else (0, 1, 3, 4, 7):
+        _gradient(x, dy, w, mean, rstd, first, kind, "f32")
