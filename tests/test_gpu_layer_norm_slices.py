@@ -1,10 +1,11 @@
 """Gradient of wide norms whose rows a cluster shares: rows off 16-byte
-boundaries at the widths where a slice fills the threads that hold it.
-Inputs, tolerances and the 64-bit forms are those of test_gpu_layer_norm.py."""
+boundaries at the widths where a slice fills the threads that hold it; and
+many rows at the widths of every streaming group.  Inputs, tolerances and the
+64-bit forms are those of test_gpu_layer_norm.py."""
 import pytest
 
 from tests._gpu import lib
-from tests.test_gpu_layer_norm import _check_grad, _inputs, _torch
+from tests.test_gpu_layer_norm import _check_forward, _check_grad, _inputs, _torch
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,20 @@ def test_full_slices_at_every_alignment(width, kind):
     _, mean, rstd = lib().layer_norm(x, w, b)
     for first in (0, 1, 2, 3) if kind == "f32" else (0, 1, 3, 4, 7):
         _gradient(x, dy, w, mean, rstd, first, kind, "f32")
+
+
+@pytest.mark.parametrize("kind,wkind", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,width", [(10000, 513), (10000, 600), (10000, 761), (10000, 768), (5000, 1281), (5000, 1535),
+                                        (2500, 2049), (2500, 2500), (2500, 2503), (2500, 3065), (1300, 4603), (1300, 6136),
+                                        (1300, 8185), (ROWS, 9001), (ROWS, 12001), (ROWS, 12293), (ROWS, 14000),
+                                        (ROWS, 14001), (1300, 12293), (1300, 16001)])
+def test_many_rows_of_every_group(rows, width, kind, wkind):
+    """Forward and backward, rows on boundaries and off them."""
+    g = lib()
+    x, dy, w, b = _inputs(rows, width, kind, wkind, width)
+    for first in (0, 3):
+        (_, xs), (buf, out) = _at(x, first), _at(x * 0 + 5, first)
+        y, mean, rstd = g.layer_norm(xs, w, b, out=out)
+        _check_forward(x, w, b, 1e-5, y, mean, rstd, kind)
+        assert (buf[:first] == 7).all() and (buf[first + out.numel():] == 7).all()
+        _gradient(x, dy, w, mean, rstd, first, kind, wkind)
