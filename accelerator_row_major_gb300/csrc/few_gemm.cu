@@ -99,6 +99,7 @@ struct FewParams {
   long long ld_exps;
   LossTargets targets;
   float* label_logit;
+  unsigned* arrived;
   unsigned* err;
 };
 
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t parts0 = tmem_base + static_cast<uint32_t>(p.acc_bufs * p.acc_cols);
   grid_launch_dependents();
   grid_dependency_wait();   // global memory from here on
+  if (!MN && blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0u;
 
   const uint32_t b_part_bytes = static_cast<uint32_t>(p.n_pad) * (kBK * 2);
   const uint32_t b_stage_bytes = PARTS * b_part_bytes;
@@ -848,6 +850,7 @@ int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches) {
     p.ld_exps = g.ld_exps;
     p.targets = g.targets;
     p.label_logit = g.label_logit;
+    p.arrived = g.arrived;
   }
   p.n_pad = blocks_of(g.rows, 16) * 16;
   // tensor memory: accumulators, then stages of parts (at least two, and a

@@ -253,17 +253,7 @@ void* gemm_f32_impl::acquire_scratch(int device, cudaStream_t stream, size_t byt
     DeviceState& st = g_devices[device];
     std::lock_guard<std::mutex> lock(st.ws_mu);
     Workspace& w = st.ws[stream];
-    const void* const before = w.scratch;
-    void* const p = grow_buffer(&w.scratch, &w.scratch_bytes, bytes + kScratchHeader);
-    if (p && p != before &&
-        (cudaMemset(p, 0, kScratchHeader) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)) {
-      (void)cudaGetLastError();
-      (void)cudaFree(p);
-      w.scratch = nullptr;
-      w.scratch_bytes = 0;
-      return nullptr;
-    }
-    return p;
+    return grow_buffer(&w.scratch, &w.scratch_bytes, bytes);
   } catch (...) {   // the map's own memory
     return nullptr;
   }

@@ -114,6 +114,7 @@ struct Params {
   long long ld_exps;
   LossTargets targets;
   float* label_logit;
+  unsigned* arrived;
   unsigned* err;
 };
 
@@ -371,6 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base)), 0);
   grid_launch_dependents();
   grid_dependency_wait();   // global memory from here on
+  if (EPI == kLogits && blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0u;
 
   // K blocks of unit u of the work list, and how often they are passed over
   constexpr int kCombos = PARTS == 3 ? 6 : 1;
@@ -865,6 +867,7 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
   p.ld_exps = g.ld_exps;
   p.targets = g.targets;
   p.label_logit = g.label_logit;
+  p.arrived = g.arrived;
   p.err = g.err;
   Maps m = {};
   if (!(g.a.mn_major ? encode(&m.a, g.a, g.K, g.M, g.parts, 64)

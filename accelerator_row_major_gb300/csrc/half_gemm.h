@@ -45,6 +45,7 @@ struct HalfGemm {
   long long ld_exps = 0;
   LossTargets targets = {};     // of its rows
   float* label_logit = nullptr; // per row the logit at its target
+  unsigned* arrived = nullptr;  // set to 0, for the kernel that counts arrivals next
   // --
   int num_sms, device;
   unsigned* err;
@@ -100,6 +101,7 @@ struct FewGemm {
   long long ld_exps = 0;
   LossTargets targets = {};
   float* label_logit = nullptr;
+  unsigned* arrived = nullptr;
   // -- or dx = *scale * b w (dx != nullptr)
   void* dx = nullptr;
   long long lddx = 0;

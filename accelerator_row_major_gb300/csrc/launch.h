@@ -119,7 +119,7 @@ void* acquire_pack_buffer(int device, cudaStream_t stream, size_t bytes);
 
 // The library's scratch buffer for `stream` on `device`, which the calls of
 // gemm_f32_lm.h lay out as they need: as acquire_pack_buffer, with a buffer
-// of its own.
+// of its own.  What it holds is undefined.
 void* acquire_scratch(int device, cudaStream_t stream, size_t bytes);
 
 // The current device, set up on first use: its ordinal, multiprocessor count
@@ -135,10 +135,6 @@ void note_launches(int launches, const char* kernel);
 
 // Whether two byte ranges share a byte.
 bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes);
-
-// Bytes at the start of every scratch buffer that are zero when it is
-// allocated; the first word counts arrivals and is zero between kernels.
-constexpr size_t kScratchHeader = 256;
 
 // Targets of a loss: 32- or 64-bit integers.
 struct LossTargets {

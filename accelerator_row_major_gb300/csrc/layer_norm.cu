@@ -540,7 +540,6 @@ int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_
     scratch = static_cast<float*>(
         acquire_scratch(device, stream, (part_floats + sums_floats) * sizeof(float)));
     if (!scratch) return GEMM_F32_ESCRATCH;
-    scratch += kScratchHeader / sizeof(float);
   }
   float* const parts = columns ? scratch : nullptr;
   int ctas = 0, rc;

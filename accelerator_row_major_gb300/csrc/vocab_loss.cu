@@ -88,7 +88,7 @@ struct JoinArgs {
   float grad_scale;
   Factors* factors;
   float* total;
-  unsigned* arrived;         // 0 before and after every launch
+  unsigned* arrived;         // set to 0 by the logits' kernel
   unsigned* err;
 };
 
@@ -171,7 +171,6 @@ __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
     if (!finish) return;
     __threadfence();
     // ---- the last CTA
-    if (threadIdx.x == 0) *a.arrived = 0u;
     if (!a.first && !a.last) return;
     s = 0.0f;
     n = 0;
@@ -395,7 +394,7 @@ size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 struct Layout {
   size_t bytes = 0;
   size_t take(size_t n) {
-    const size_t at = kScratchHeader + bytes;
+    const size_t at = bytes;
     bytes += round_up(n, 256);
     return at;
   }
@@ -486,6 +485,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   const bool sum_dw = c.dw && !f32 && step < c.rows;   // bfloat16 dw of several pieces
 
   Layout layout;
+  const size_t at_arrived = layout.take(sizeof(unsigned));
   const size_t at_factors = layout.take(sizeof(Factors));
   const size_t at_logit = layout.take(sizeof(float) * c.rows);
   const int groups_all = (c.rows - 1) / kJoinRows + 1;
@@ -517,6 +517,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   if (!scratch) return GEMM_F32_ESCRATCH;
 
   Factors* const factors = reinterpret_cast<Factors*>(scratch + at_factors);
+  unsigned* const arrived = reinterpret_cast<unsigned*>(scratch + at_arrived);
   float* const logit = reinterpret_cast<float*>(scratch + at_logit);
   float2* const stats = reinterpret_cast<float2*>(scratch + at_stats);
   const LossTargets all = {c.targets, c.target_bits, c.vocab, c.ignore};
@@ -564,6 +565,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
       z.ld_exps = ld_exps;
       z.targets = targets;
       z.label_logit = logit;
+      z.arrived = arrived;
       rc = launch_few_gemm(z, stream, launches);
     } else {
       HalfGemm z = base;
@@ -578,6 +580,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
       z.ld_exps = ld_exps;
       z.targets = targets;
       z.label_logit = logit + r;
+      z.arrived = arrived;
       rc = launch_half_gemm(z, stream, launches);
     }
     if (rc != GEMM_F32_OK) break;
@@ -604,7 +607,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
     j.grad_scale = c.grad_scale;
     j.factors = factors;
     j.total = c.total;
-    j.arrived = reinterpret_cast<unsigned*>(scratch);
+    j.arrived = arrived;
     j.err = err;
     const int join_ctas = (n + kJoinRows - 1) / kJoinRows;
     rc = join_ctas <= num_sms
