@@ -10,11 +10,11 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
-#include <unordered_map>
 
 #include "../../include/gemm_f32.h"
 #include "device_common.cuh"
 #include "launch.h"
+#include "workspace.h"
 
 namespace {
 
@@ -28,14 +28,78 @@ __device__ __align__(16) unsigned g_device_words[8];
 
 constexpr int kMaxDevices = 64;
 
-struct Workspace {
-  void* ptr = nullptr;
-  size_t bytes = 0;
-  void* pack = nullptr;           // repacked operands for the TMA path
-  size_t pack_bytes = 0;
-  void* scratch = nullptr;        // layer norm and vocabulary loss (gemm_f32_lm.h)
-  size_t scratch_bytes = 0;
+// The CUDA runtime as workspace.h needs it.  Another thread, or this one on
+// another stream, may be capturing in a mode that forbids allocations; these
+// have nothing to do with what it captures.
+struct CudaMemory {
+  using Stream = cudaStream_t;
+  using Graph = cudaGraph_t;
+
+  class Relaxed {
+   public:
+    Relaxed() { (void)cudaThreadExchangeStreamCaptureMode(&mode_); }
+    ~Relaxed() { (void)cudaThreadExchangeStreamCaptureMode(&mode_); }
+
+   private:
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+  };
+
+  static cudaStream_t per_thread() { return cudaStreamPerThread; }
+  static bool capturing(cudaStream_t stream, unsigned long long* id, cudaGraph_t* graph) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamGetCaptureInfo(stream, &status, id, graph, nullptr, nullptr, nullptr) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    return status == cudaStreamCaptureStatusActive;
+  }
+  static void* alloc(size_t bytes) {
+    const Relaxed relaxed;
+    void* p = nullptr;
+    if (cudaMalloc(&p, bytes) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
+    return p;
+  }
+  static void free(void* p) {
+    const Relaxed relaxed;
+    if (cudaFree(p) != cudaSuccess) (void)cudaGetLastError();
+  }
+  // On a stream of its own, and done when this returns.
+  static bool zero(void* p, size_t bytes) {
+    const Relaxed relaxed;
+    cudaStream_t s = nullptr;
+    bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+    ok = ok && cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess;
+    ok = ok && cudaStreamSynchronize(s) == cudaSuccess;
+    if (s) ok = cudaStreamDestroy(s) == cudaSuccess && ok;
+    if (!ok) (void)cudaGetLastError();
+    return ok;
+  }
+  // Calls done(arg) once the graph and everything made from it are gone.
+  static bool retain(cudaGraph_t graph, void (*done)(void*), void* arg) {
+    cudaUserObject_t object = nullptr;
+    if (cudaUserObjectCreate(&object, arg, done, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+      (void)cudaGetLastError();
+      (void)cudaUserObjectRelease(object, 1);
+      return false;
+    }
+    return true;
+  }
 };
+
+using Workspaces = gemm_f32_impl::Workspaces<CudaMemory>;
+
+// Never destroyed: graphs may outlive the library's other statics.
+Workspaces& workspaces(int device) {
+  static Workspaces* const all = new Workspaces[kMaxDevices];
+  return all[device];
+}
 
 struct DeviceState {
   std::once_flag once;
@@ -44,8 +108,6 @@ struct DeviceState {
   unsigned* err = nullptr;        // device address of g_device_words
   std::mutex fixed_mu;
   void* fixed_scratch = nullptr;  // device address of gemm_f32_noalloc's array
-  std::mutex ws_mu;
-  std::unordered_map<cudaStream_t, Workspace> ws;  // one per stream
 };
 
 DeviceState g_devices[kMaxDevices];
@@ -127,30 +189,17 @@ constexpr unsigned kKnownFlags = GEMM_F32_FLAG_FORCE_STAGED | GEMM_F32_FLAG_TILE
 
 void* gemm_f32_impl::acquire_workspace(int device, cudaStream_t stream, size_t bytes) {
   if (device < 0 || device >= kMaxDevices) return nullptr;
-  DeviceState& st = g_devices[device];
-  std::lock_guard<std::mutex> lock(st.ws_mu);
-  Workspace& w = st.ws[stream];
-  if (w.bytes < bytes) {
-    if (w.ptr) {
-      (void)cudaFree(w.ptr);   // synchronises the device: no kernel still uses it
-      w.ptr = nullptr;
-      w.bytes = 0;
-    }
-    const size_t want = (bytes + (1u << 20) - 1) & ~static_cast<size_t>((1u << 20) - 1);
-    void* p = nullptr;
-    if (cudaMalloc(&p, want) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return nullptr;
-    }
-    if (cudaMemset(p, 0, want) != cudaSuccess) {
-      (void)cudaGetLastError();
-      (void)cudaFree(p);
-      return nullptr;
-    }
-    w.ptr = p;
-    w.bytes = want;
-  }
-  return w.ptr;
+  return workspaces(device).acquire(stream, gemm_f32_impl::Memory::kSplitTail, bytes);
+}
+
+void* gemm_f32_impl::acquire_pack_buffer(int device, cudaStream_t stream, size_t bytes) {
+  if (device < 0 || device >= kMaxDevices) return nullptr;
+  return workspaces(device).acquire(stream, gemm_f32_impl::Memory::kPack, bytes);
+}
+
+void* gemm_f32_impl::acquire_scratch(int device, cudaStream_t stream, size_t bytes) {
+  if (device < 0 || device >= kMaxDevices) return nullptr;
+  return workspaces(device).acquire(stream, gemm_f32_impl::Memory::kScratch, bytes);
 }
 
 namespace {
@@ -214,51 +263,6 @@ int zero_fill(float* C, int M, int N, cudaStream_t stream) {
 
 }  // namespace
 
-namespace {
-
-// *p, grown to at least `bytes` (1 MiB granules); nullptr if the memory
-// cannot be had.
-void* grow_buffer(void** p, size_t* have, size_t bytes) {
-  if (*have < bytes) {
-    if (*p) {
-      (void)cudaFree(*p);   // synchronises the device: no kernel still uses it
-      *p = nullptr;
-      *have = 0;
-    }
-    const size_t want = (bytes + (1u << 20) - 1) & ~static_cast<size_t>((1u << 20) - 1);
-    void* q = nullptr;
-    if (cudaMalloc(&q, want) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return nullptr;
-    }
-    *p = q;
-    *have = want;
-  }
-  return *p;
-}
-
-}  // namespace
-
-void* gemm_f32_impl::acquire_pack_buffer(int device, cudaStream_t stream, size_t bytes) {
-  if (device < 0 || device >= kMaxDevices) return nullptr;
-  DeviceState& st = g_devices[device];
-  std::lock_guard<std::mutex> lock(st.ws_mu);
-  Workspace& w = st.ws[stream];
-  return grow_buffer(&w.pack, &w.pack_bytes, bytes);
-}
-
-void* gemm_f32_impl::acquire_scratch(int device, cudaStream_t stream, size_t bytes) {
-  if (device < 0 || device >= kMaxDevices) return nullptr;
-  try {
-    DeviceState& st = g_devices[device];
-    std::lock_guard<std::mutex> lock(st.ws_mu);
-    Workspace& w = st.ws[stream];
-    return grow_buffer(&w.scratch, &w.scratch_bytes, bytes);
-  } catch (...) {   // the map's own memory
-    return nullptr;
-  }
-}
-
 bool gemm_f32_impl::current_device(int* device, int* num_sms, unsigned** err) {
   const DeviceState* const st = device_state(device);
   if (!st || st->status != GEMM_F32_OK) return false;
@@ -315,6 +319,7 @@ extern "C" int gemm_f32_ex(const float* A, const float* B, float* C, int M, int 
   g.flags = flags;
   int launches = 0;
   int rc;
+  const gemm_f32_impl::WorkspaceCall call;
   if (flags == 0 && gemm_f32_impl::small_suits(g))
     rc = gemm_f32_impl::launch_small(g, stream, &launches);
   else if (mode == GEMM_F32_MODE_FFMA)
@@ -426,6 +431,7 @@ extern "C" int gemm_f32_general(int trans_a, int trans_b, int M, int N, int K, f
   g.device = dev;
   g.flags = 0;
   int launches = 0;
+  const gemm_f32_impl::WorkspaceCall call;
   const int rc = mode == GEMM_F32_MODE_FFMA
                      ? gemm_f32_impl::launch_ffma(g, stream, &launches)
                      : gemm_f32_impl::launch_tc(g, mode == GEMM_F32_MODE_TC1X ? 1 : 3, stream,
@@ -665,18 +671,12 @@ extern "C" int gemm_f32_release(void) {
   if (!st || st->status != GEMM_F32_OK) return GEMM_F32_EDEVICE;
   // same lock order as gemm_f32_host: its pipe, then the workspaces
   std::lock_guard<std::mutex> hlock(g_pipes[dev].mu);
-  std::lock_guard<std::mutex> lock(st->ws_mu);
   int rc = GEMM_F32_OK;
   if (cudaDeviceSynchronize() != cudaSuccess) {
     (void)cudaGetLastError();
     rc = GEMM_F32_ELAUNCH;
   }
-  for (auto& kv : st->ws) {
-    if (kv.second.ptr) (void)cudaFree(kv.second.ptr);
-    if (kv.second.pack) (void)cudaFree(kv.second.pack);
-    if (kv.second.scratch) (void)cudaFree(kv.second.scratch);
-  }
-  st->ws.clear();
+  workspaces(dev).release();
   host_pipe_free(g_pipes[dev]);
   return rc;
 }

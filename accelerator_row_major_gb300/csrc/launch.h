@@ -62,12 +62,13 @@ inline bool tma_addressable(const GemmArgs& g) {
          reinterpret_cast<uintptr_t>(g.A) % 16 == 0 && reinterpret_cast<uintptr_t>(g.B) % 16 == 0;
 }
 
-// The library's workspace for `stream` on `device` (one per device and
-// stream), grown to at least `bytes` with cudaMalloc when needed (which
-// synchronises the device) and zeroed when allocated.  Its split-tail
-// counters stay valid from call to call, even after a kernel gave up on a
-// bounded wait (device_common.cuh).  Returns nullptr if the memory cannot be
-// had; the caller then does without.
+// The library's memory for the call in progress (workspace.h) on `stream` of
+// `device`: the split tail's workspace, grown to at least `bytes` with
+// cudaMalloc when needed (which synchronises the device) and zeroed when
+// allocated.  Its split-tail counters stay valid from call to call, even
+// after a kernel gave up on a bounded wait (device_common.cuh).  Returns
+// nullptr if the memory cannot be had, or would have to be allocated during a
+// capture; the caller then does without.
 void* acquire_workspace(int device, cudaStream_t stream, size_t bytes);
 
 // Tensor-core path (tcgen05.mma kind::tf32).  nprod = 3 (split hi/lo, three
@@ -112,14 +113,11 @@ int pack_operand(const float* src, int rows, int cols, int ld_src, bool transpos
                  int ld_dst, int num_sms, unsigned* err, cudaStream_t stream);
 int pack_for_tma(GemmArgs& g, cudaStream_t stream, int* launches);
 
-// The library's pack buffer for `stream` on `device`, grown to at least
-// `bytes` (1 MiB granules, cudaMalloc, which synchronises the device when it
-// grows); nullptr when the memory cannot be had.  Freed by gemm_f32_release.
+// The same for the copies of operands; what it holds is undefined.
 void* acquire_pack_buffer(int device, cudaStream_t stream, size_t bytes);
 
-// The library's scratch buffer for `stream` on `device`, which the calls of
-// gemm_f32_lm.h lay out as they need: as acquire_pack_buffer, with a buffer
-// of its own.  What it holds is undefined.
+// The same for the calls of gemm_f32_lm.h, which lay it out as they need; in
+// a capture it is memory of the captured graph's own.
 void* acquire_scratch(int device, cudaStream_t stream, size_t bytes);
 
 // The current device, set up on first use: its ordinal, multiprocessor count

@@ -35,6 +35,7 @@
 #include "launch.h"
 #include "layer_norm_stream.cuh"
 #include "row_common.cuh"
+#include "workspace.h"
 
 namespace gemm_f32_impl {
 using namespace gemm_f32_dev;
@@ -753,6 +754,7 @@ extern "C" int gemm_f32_layer_norm_grad(int type, int weight_type, long long row
                                                                                         : Rows::kUneven;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
   int rc, launches = 0;
+  const WorkspaceCall call;
   if (type == GEMM_F32_TYPE_F32)
     rc = grad<float, float>(a, how, dweight, dbias, device, num_sms, stream, &launches);
   else if (weight_type == GEMM_F32_TYPE_F32)

@@ -35,6 +35,7 @@
 #include "half_gemm.h"
 #include "launch.h"
 #include "row_common.cuh"
+#include "workspace.h"
 
 namespace gemm_f32_impl {
 using namespace gemm_f32_dev;
@@ -733,6 +734,7 @@ int checked(Call& c, long long rows, gemm_f32_stream_t stream_handle) {
     return GEMM_F32_OK;
   }
   int launches = 0;
+  const WorkspaceCall call;
   const int rc = run(c, stream, &launches);
   if (rc == GEMM_F32_OK) note_launches(launches, "half_gemm_kernel");
   return rc;

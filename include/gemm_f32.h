@@ -20,8 +20,13 @@
  * tiles then go through a workspace the library owns, one per (device,
  * stream).  The first call that needs it (or a larger one) allocates it with
  * cudaMalloc, which synchronises the device, so make such a call once before
- * capturing a stream into a CUDA graph; gemm_f32_release() frees it.  Calls
- * on different streams use different workspaces.
+ * capturing a stream into a CUDA graph (a captured call allocates nothing:
+ * without a workspace it takes whole tiles); gemm_f32_release() frees it.
+ * Calls on different streams use different workspaces, and host threads may
+ * call on one stream.  A captured product uses the workspace of the stream it
+ * was captured on: its replays must not run beside products on that stream or
+ * other graphs captured there.  A larger call leaves it that workspace;
+ * gemm_f32_release() does not.
  *
  * Streams: every call is asynchronous on `stream` (0 = legacy default
  * stream) and never synchronises the host, like the stream-taking launcher
@@ -210,7 +215,10 @@ int gemm_f32_host(const float* A, const float* B, float* C, int M, int N, int K,
  * operands the tensor-memory accelerator cannot read — odd strides,
  * unaligned bases or stored transposes in products of at least 2^27
  * multiply-adds are copied once into aligned buffers first —,
- * gemm_f32_host's device slots and the scratch of gemm_f32_lm.h's calls) after synchronising the device.
+ * gemm_f32_host's device slots and the scratch of gemm_f32_lm.h's calls, but
+ * for what graphs hold of it) after synchronising the device and once calls in
+ * progress on other host threads have returned.  Graphs that captured products
+ * of this library must not be replayed afterwards.
  * Returns 0, or GEMM_F32_EDEVICE / GEMM_F32_ELAUNCH on a CUDA error. */
 int gemm_f32_release(void);
 

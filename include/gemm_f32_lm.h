@@ -18,10 +18,14 @@
  *
  * Scratch: the library owns one scratch buffer per (device, stream), grown
  * with cudaMalloc (which synchronises the device) by the first call that
- * needs more, kept for the next calls and freed by gemm_f32_release().  Make
- * one call of a shape before capturing the same call into a CUDA graph.
- * Where the memory cannot be had the call returns GEMM_F32_ESCRATCH and
- * launches nothing.
+ * needs more, kept for the next calls and freed by gemm_f32_release().  A
+ * call that is captured into a CUDA graph takes memory of the graph's own
+ * instead, during the capture: no call before it is needed, replays run
+ * beside any other call, and the memory comes back to the library when the
+ * graph and what was instantiated from it are destroyed.  Host threads may
+ * call on one stream: each call's kernels are queued together.  Where the
+ * memory cannot be had the call returns GEMM_F32_ESCRATCH and launches
+ * nothing.
  *
  * Every sum is taken in a fixed order: the same call on the same inputs
  * gives the same bits.
