@@ -45,11 +45,19 @@ def matmul(A, B, out=None, mode="tc3x", flags: int = 0, stream=None):
     non-zero return code."""
     import torch
 
+    from ._binding import elsewhere
+
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[0]:
         raise ValueError("shapes %s and %s do not chain" % (tuple(A.shape), tuple(B.shape)))
     for name, t in (("A", A), ("B", B)):
         if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError("%s must be a contiguous float32 CUDA tensor" % name)
+    if B.get_device() != A.get_device() or (out is not None and out.get_device() != A.get_device()):
+        raise ValueError("A, B and out must be on one device")
+    there = elsewhere(A.get_device())
+    if there is not None:
+        with there:
+            return matmul(A, B, out, mode, flags, stream)
     M, K = A.shape
     N = B.shape[1]
     if out is None:

@@ -156,6 +156,14 @@ def _stream(s) -> int:
     return int(s.cuda_stream)
 
 
+def elsewhere(device: int):
+    """The context in which a call on tensors of `device` is made, None where
+    that device is current: the C calls take the current one."""
+    import torch
+
+    return None if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
+
+
 def gemm_f32(A, B, C, M: int, N: int, K: int, stream=None) -> int:
     """C = A * B (row-major, default mode).  A, B, C: device pointers (int)
     or CUDA tensors; stream: int handle, torch.cuda.Stream or None."""

@@ -4,13 +4,14 @@ allocation of outputs, and the call into libgemm_f32.so (include/gemm_f32_lm.h).
 Matrices are 2-D CUDA tensors of float32 or bfloat16 with contiguous rows
 (stride(1) == 1; stride(0) may exceed the width, as in a column slice).
 Calls are queued on `stream`, or on torch's current stream of the tensors'
-device, and return without waiting for it.
+device, and return without waiting for it.  They run on the tensors' device,
+whichever is current.
 """
 from __future__ import annotations
 
 import torch
 
-from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, _stream, check, lib
+from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, _stream, check, elsewhere, lib
 
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
 _F32 = torch.float32
@@ -69,6 +70,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     weight and bias hold x's type or float32 (None: 1 and 0); mean and rstd
     are float32, one value per row.  `out` may be x itself."""
     kind, dev, rows, width, ldx = _matrix("x", x)
+    there = elsewhere(dev)
+    if there is not None:
+        with there:
+            return layer_norm(x, weight, bias, eps, out, stream)
     wtype, pw, pb = x.dtype, 0, 0
     if weight is not None:
         wtype = _weight_type(x, weight)
@@ -97,6 +102,10 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, stream=None):
     dweight and dbias hold weight's type (float32 for weight None).  `out`,
     the tensor for dx, may be dy or x itself."""
     kind, dev, rows, width, ldx = _matrix("x", x)
+    there = elsewhere(dev)
+    if there is not None:
+        with there:
+            return layer_norm_grad(dy, x, weight, mean, rstd, out, stream)
     lddy = _like("dy", dy, x)
     wtype, pw = _F32, 0
     if weight is not None:
@@ -141,6 +150,10 @@ def vocab_loss(x, w, targets, ignore_index=-100, reduction="mean", stream=None):
     is ignore_index), total their sum, or mean over the rows that count.  A
     target outside the vocabulary counts as ignored and is reported by
     gemm_f32_status()."""
+    there = elsewhere(_matrix("x", x)[1])
+    if there is not None:
+        with there:
+            return vocab_loss(x, w, targets, ignore_index, reduction, stream)
     args, code, dev, loss, lse, total = _loss_args(x, w, targets, reduction)
     check(lib().gemm_f32_vocab_loss(*args, ignore_index, code, loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
                                     _raw_stream(dev) if stream is None else _stream(stream)), "vocab_loss")
@@ -154,6 +167,10 @@ def vocab_loss_grad(x, w, targets, ignore_index=-100, reduction="mean", grad_sca
     dx and dw hold x's type; need_dx / need_dw False leaves one out (None).
     piece_bytes bounds the scratch that holds a piece of the rows (0: the
     library's default)."""
+    there = elsewhere(_matrix("x", x)[1])
+    if there is not None:
+        with there:
+            return vocab_loss_grad(x, w, targets, ignore_index, reduction, grad_scale, need_dx, need_dw, piece_bytes, stream)
     args, code, dev, loss, lse, total = _loss_args(x, w, targets, reduction)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
     dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
