@@ -41,8 +41,9 @@ def __getattr__(name):
 def matmul(A, B, out=None, mode="tc3x", flags: int = 0, stream=None):
     """C = A @ B through the C ABI for contiguous 2-D fp32 CUDA tensors.
 
-    Allocates C with torch when ``out`` is None; raises GemmError on a
-    non-zero return code."""
+    Queued on ``stream`` (a torch stream or a handle; None: torch's current
+    stream of the operands' device).  Allocates C with torch, on that stream,
+    when ``out`` is None; raises GemmError on a non-zero return code."""
     import torch
 
     from ._binding import elsewhere
@@ -54,17 +55,15 @@ def matmul(A, B, out=None, mode="tc3x", flags: int = 0, stream=None):
             raise ValueError("%s must be a contiguous float32 CUDA tensor" % name)
     if B.get_device() != A.get_device() or (out is not None and out.get_device() != A.get_device()):
         raise ValueError("A, B and out must be on one device")
-    there = elsewhere(A.get_device())
+    there = elsewhere(A.get_device(), stream)
     if there is not None:
         with there:
-            return matmul(A, B, out, mode, flags, stream)
+            return matmul(A, B, out, mode, flags)
     M, K = A.shape
     N = B.shape[1]
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
     elif out.shape != (M, N) or out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be a contiguous float32 tensor of shape (%d, %d)" % (M, N))
-    if stream is None:
-        stream = torch.cuda.current_stream(A.device)
-    check(gemm_f32_ex(A, B, out, M, N, K, mode, flags, stream))
+    check(gemm_f32_ex(A, B, out, M, N, K, mode, flags, torch.cuda.current_stream(A.device)))
     return out

@@ -156,12 +156,20 @@ def _stream(s) -> int:
     return int(s.cuda_stream)
 
 
-def elsewhere(device: int):
-    """The context in which a call on tensors of `device` is made, None where
-    that device is current: the C calls take the current one."""
+def elsewhere(device: int, stream):
+    """The context in which a call on tensors of `device` is made, with
+    `stream` (None: torch's current one) as the current stream of its device;
+    None where that is so already.  The C calls take the current device."""
     import torch
 
-    return None if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
+    if stream is None:
+        return None if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    if stream.device_index != device:
+        raise ValueError("the stream belongs to cuda:%d, the tensors to cuda:%d" % (stream.device_index, device))
+    return torch.cuda.stream(stream)
 
 
 def gemm_f32(A, B, C, M: int, N: int, K: int, stream=None) -> int:

@@ -3,15 +3,18 @@ allocation of outputs, and the call into libgemm_f32.so (include/gemm_f32_lm.h).
 
 Matrices are 2-D CUDA tensors of float32 or bfloat16 with contiguous rows
 (stride(1) == 1; stride(0) may exceed the width, as in a column slice).
-Calls are queued on `stream`, or on torch's current stream of the tensors'
-device, and return without waiting for it.  They run on the tensors' device,
-whichever is current.
+Calls are queued on `stream` (a torch stream or a handle), or on torch's
+current stream of the tensors' device, and return without waiting for it.
+They run on the tensors' device, and what they allocate belongs to the stream
+they are queued on: a caller that goes on with it on another stream, or gives
+a tensor of another stream's, orders the two and keeps the memory
+(wait_stream, record_stream), as with torch's own operators.
 """
 from __future__ import annotations
 
 import torch
 
-from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, _stream, check, elsewhere, lib
+from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, check, elsewhere, lib
 
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
 _F32 = torch.float32
@@ -70,10 +73,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     weight and bias hold x's type or float32 (None: 1 and 0); mean and rstd
     are float32, one value per row.  `out` may be x itself."""
     kind, dev, rows, width, ldx = _matrix("x", x)
-    there = elsewhere(dev)
+    there = elsewhere(dev, stream)
     if there is not None:
         with there:
-            return layer_norm(x, weight, bias, eps, out, stream)
+            return layer_norm(x, weight, bias, eps, out)
     wtype, pw, pb = x.dtype, 0, 0
     if weight is not None:
         wtype = _weight_type(x, weight)
@@ -90,8 +93,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     mean = torch.empty(rows, dtype=_F32, device=x.device)
     rstd = torch.empty_like(mean)
     check(lib().gemm_f32_layer_norm(kind, _TYPES[wtype], rows, width, x.data_ptr(), ldx, pw, pb, eps, out.data_ptr(),
-                                    ldo, mean.data_ptr(), rstd.data_ptr(),
-                                    _raw_stream(dev) if stream is None else _stream(stream)), "layer_norm")
+                                    ldo, mean.data_ptr(), rstd.data_ptr(), _raw_stream(dev)), "layer_norm")
     return out, mean, rstd
 
 
@@ -102,10 +104,10 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, stream=None):
     dweight and dbias hold weight's type (float32 for weight None).  `out`,
     the tensor for dx, may be dy or x itself."""
     kind, dev, rows, width, ldx = _matrix("x", x)
-    there = elsewhere(dev)
+    there = elsewhere(dev, stream)
     if there is not None:
         with there:
-            return layer_norm_grad(dy, x, weight, mean, rstd, out, stream)
+            return layer_norm_grad(dy, x, weight, mean, rstd, out)
     lddy = _like("dy", dy, x)
     wtype, pw = _F32, 0
     if weight is not None:
@@ -121,13 +123,13 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, stream=None):
     dbias = torch.empty_like(dweight)
     check(lib().gemm_f32_layer_norm_grad(kind, _TYPES[wtype], rows, width, dy.data_ptr(), lddy, x.data_ptr(), ldx, pw,
                                          pm, pr, out.data_ptr(), ldo, dweight.data_ptr(), dbias.data_ptr(),
-                                         _raw_stream(dev) if stream is None else _stream(stream)), "layer_norm_grad")
+                                         _raw_stream(dev)), "layer_norm_grad")
     return out, dweight, dbias
 
 
-def _loss_args(x, w, targets, reduction):
-    """The C call's arguments up to target_bits, the reduction's code, x's device and the outputs of both calls."""
-    kind, dev, rows, width, ldx = _matrix("x", x)
+def _loss_args(x, w, targets, reduction, matrix):
+    """The C call's arguments up to target_bits, the reduction's code and the outputs of both calls; `matrix` is x's."""
+    kind, dev, rows, width, ldx = matrix
     wkind, wdev, vocab, wwidth, ldw = _matrix("w", w)
     if wkind != kind or wdev != dev or wwidth != width:
         raise ValueError("w must be a %s matrix on %s with x's %d columns" % (x.dtype, x.device, width))
@@ -138,7 +140,7 @@ def _loss_args(x, w, targets, reduction):
         raise ValueError("reduction must be one of %s" % ", ".join(sorted(REDUCTIONS)))
     loss = torch.empty(rows, dtype=_F32, device=x.device)
     return ((kind, rows, width, vocab, x.data_ptr(), ldx, w.data_ptr(), ldw, pt,
-             64 if targets.dtype is torch.int64 else 32), REDUCTIONS[reduction], dev, loss, torch.empty_like(loss),
+             64 if targets.dtype is torch.int64 else 32), REDUCTIONS[reduction], loss, torch.empty_like(loss),
             torch.empty((), dtype=_F32, device=x.device))
 
 
@@ -150,13 +152,14 @@ def vocab_loss(x, w, targets, ignore_index=-100, reduction="mean", stream=None):
     is ignore_index), total their sum, or mean over the rows that count.  A
     target outside the vocabulary counts as ignored and is reported by
     gemm_f32_status()."""
-    there = elsewhere(_matrix("x", x)[1])
+    matrix = _matrix("x", x)
+    there = elsewhere(matrix[1], stream)
     if there is not None:
         with there:
-            return vocab_loss(x, w, targets, ignore_index, reduction, stream)
-    args, code, dev, loss, lse, total = _loss_args(x, w, targets, reduction)
+            return vocab_loss(x, w, targets, ignore_index, reduction)
+    args, code, loss, lse, total = _loss_args(x, w, targets, reduction, matrix)
     check(lib().gemm_f32_vocab_loss(*args, ignore_index, code, loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
-                                    _raw_stream(dev) if stream is None else _stream(stream)), "vocab_loss")
+                                    _raw_stream(matrix[1])), "vocab_loss")
     return total, loss, lse
 
 
@@ -167,15 +170,16 @@ def vocab_loss_grad(x, w, targets, ignore_index=-100, reduction="mean", grad_sca
     dx and dw hold x's type; need_dx / need_dw False leaves one out (None).
     piece_bytes bounds the scratch that holds a piece of the rows (0: the
     library's default)."""
-    there = elsewhere(_matrix("x", x)[1])
+    matrix = _matrix("x", x)
+    there = elsewhere(matrix[1], stream)
     if there is not None:
         with there:
-            return vocab_loss_grad(x, w, targets, ignore_index, reduction, grad_scale, need_dx, need_dw, piece_bytes, stream)
-    args, code, dev, loss, lse, total = _loss_args(x, w, targets, reduction)
+            return vocab_loss_grad(x, w, targets, ignore_index, reduction, grad_scale, need_dx, need_dw, piece_bytes)
+    args, code, loss, lse, total = _loss_args(x, w, targets, reduction, matrix)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
     dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
     check(lib().gemm_f32_vocab_loss_grad(*args, ignore_index, code, grad_scale, loss.data_ptr(), lse.data_ptr(),
                                          total.data_ptr(), dx.data_ptr() if need_dx else 0, args[2],
                                          dw.data_ptr() if need_dw else 0, args[2], piece_bytes,
-                                         _raw_stream(dev) if stream is None else _stream(stream)), "vocab_loss_grad")
+                                         _raw_stream(matrix[1])), "vocab_loss_grad")
     return total, loss, lse, dx, dw

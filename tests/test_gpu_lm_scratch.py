@@ -133,3 +133,26 @@ def test_threads_on_one_stream():
     if errors:
         raise errors[0]
     assert g.gemm_f32_status(s) == (0, 0)
+
+
+def test_outputs_belong_to_the_stream_that_is_given():
+    """Memory that the current stream has freed but still writes to does not become an output of another stream's
+    call."""
+    torch, _ = _torch()
+    g = lib()
+    x, w, _ = _inputs(512, 1024, 8, "f32", 1)
+    xt = x.t().contiguous()
+    want, product = g.layer_norm(x)[0], g.matmul(x, xt)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g.layer_norm(x, stream=s)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    late = torch.empty_like(x).fill_(7.0)             # some 25 ms from now
+    del late
+    y = g.layer_norm(x, stream=s)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    c = g.matmul(x, xt, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(c, product)

@@ -1,5 +1,6 @@
 """Where the calls on torch tensors run, on stand-ins for the tensors, the
-devices and the library: on the tensors' device, whichever is current."""
+devices and the library: on the tensors' device, whichever is current, and on
+the stream that is given, which owns what is allocated."""
 import contextlib
 import types
 
@@ -105,3 +106,21 @@ def test_a_call_runs_on_its_tensors_device(world, name, current):
     (called, device, stream, args), = world.calls
     assert (called, device, stream, args[-1]) == (name, 1, 20, 20)
     assert set(world.made) == {(1, 20)} and world.device == current
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("dev", [0, 1])
+@pytest.mark.parametrize("given,handle", [(lambda d: Stream(d, 77), 77), (lambda d: 78, 78), (lambda d: 0, 0)])
+def test_what_a_call_allocates_belongs_to_its_stream(world, name, dev, given, handle):
+    _calls(world.g, dev)[name](stream=given(dev))
+    (called, device, stream, args), = world.calls
+    assert (called, device, stream, args[-1]) == (name, dev, handle, handle)
+    assert set(world.made) == {(dev, handle)}
+    assert world.device == 0 and world.streams[dev].cuda_stream == 10 * (dev + 1)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_stream_of_another_device_is_refused(world, name):
+    with pytest.raises(ValueError):
+        _calls(world.g, 1)[name](stream=Stream(0, 77))
+    assert not world.calls
