@@ -21,6 +21,7 @@ namespace {
 // One block of device words per device.  Word 0 is the error word: 0, or
 // the site code of the first bounded wait (or, in the checked build, the
 // first out-of-range index) since the last gemm_f32_status() on that device.
+// Word 1: kSiteTarget where a loss has met a target outside its vocabulary.
 // Words 4..7 are the clock record (two 64-bit sums, SM clocks and
 // nanoseconds of CTA 0 of each pair and FFMA launch), read by
 // gemm_f32_clock_record().
@@ -631,16 +632,18 @@ extern "C" int gemm_f32_status(gemm_f32_stream_t stream_handle, unsigned* site) 
     (void)cudaGetLastError();
     return GEMM_F32_ELAUNCH;
   }
-  unsigned word = 0;
+  unsigned words[2] = {0, 0};
   const unsigned zero = 0;
-  if (cudaMemcpy(&word, st->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemcpy(st->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) {
+  bool ok = cudaMemcpy(words, st->err, sizeof(words), cudaMemcpyDeviceToHost) == cudaSuccess;
+  // a failure first; the target then waits for the next call
+  const int at = words[0] || !words[1] ? 0 : 1;
+  ok = ok && (!words[at] || cudaMemcpy(st->err + at, &zero, sizeof(zero), cudaMemcpyHostToDevice) == cudaSuccess);
+  if (!ok) {
     (void)cudaGetLastError();
     return GEMM_F32_ELAUNCH;
   }
-  if (site) *site = word;
-  if (word == gemm_f32_impl::kSiteTarget) return GEMM_F32_ETARGET;
-  return word ? GEMM_F32_ETIMEOUT : GEMM_F32_OK;
+  if (site) *site = words[at];
+  return !words[at] ? GEMM_F32_OK : at == 0 ? GEMM_F32_ETIMEOUT : GEMM_F32_ETARGET;
 }
 
 extern "C" int gemm_f32_clock_record(gemm_f32_stream_t stream_handle,

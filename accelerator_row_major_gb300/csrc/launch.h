@@ -124,8 +124,9 @@ void* acquire_scratch(int device, cudaStream_t stream, size_t bytes);
 // and error word.  False when it is not an sm_103 part or a query failed.
 bool current_device(int* device, int* num_sms, unsigned** err);
 
-// A target outside the vocabulary recorded in the error word (data, not a
-// failure of the kernels): gemm_f32_status() reports it as GEMM_F32_ETARGET.
+// A target outside the vocabulary, recorded in the word after the error word
+// (data, not a failure of the kernels, which it must not hide):
+// gemm_f32_status() reports it as GEMM_F32_ETARGET.
 constexpr unsigned kSiteTarget = 32;
 
 // What gemm_f32_last_launches() and gemm_f32_last_kernel() report next.

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
       } else {
         const long long y = a.targets.bits == 64 ? static_cast<const long long*>(a.targets.p)[row]
                                                  : static_cast<const int*>(a.targets.p)[row];
-        if (y != a.targets.ignore) record_error(a.err, kSiteTarget);
+        if (y != a.targets.ignore) record_error(a.err + 1, kSiteTarget);
       }
       if (a.lse) a.lse[row] = l;
       if (a.loss) a.loss[row] = s;

@@ -147,9 +147,12 @@ int gemm_f32_ex(const float* A, const float* B, float* C, int M, int N, int K,
 
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns 0, GEMM_F32_ETIMEOUT if a kernel since the last call gave up
- * on a bounded wait, or GEMM_F32_ELAUNCH if the synchronisation itself
- * reported a CUDA error.  `site` (may be NULL) receives the code of the first
- * wait that gave up (0 if none). */
+ * on a bounded wait, GEMM_F32_ETARGET if a loss of gemm_f32_lm.h met a target
+ * outside its vocabulary, or GEMM_F32_ELAUNCH if the synchronisation itself
+ * reported a CUDA error.  Where both a wait and a target are to be reported,
+ * this call reports the wait and the next one the target.  `site` (may be
+ * NULL) receives the code of the first wait that gave up, 32 for a target (0
+ * if none). */
 int gemm_f32_status(gemm_f32_stream_t stream, unsigned* site);
 
 /* The clock record of the current device.  The first thread of CTA 0 of
