@@ -472,7 +472,7 @@ int stream_grad(NormArgs a, Rows rows, float* scratch, int device, int num_sms, 
 // The narrowest group of threads whose registers hold the row: up to 4
 // vectors a thread, or 8 elements where they are read one by one.
 template <class T, class WT>
-int forward(const NormArgs& a, Rows rows, int device, int num_sms, cudaStream_t stream) {
+int forward(const NormArgs& a, Rows rows, int device, int num_sms, cudaStream_t stream, const char** kernel) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   const bool vectors = rows == Rows::kVectors;
   const int n = vectors ? (a.width + V - 1) / V : a.width;
@@ -491,8 +491,12 @@ int forward(const NormArgs& a, Rows rows, int device, int num_sms, cudaStream_t 
                    : e <= 12288 ? stream_forward<T, WT, 512, 24>(a, rows, device, num_sms, stream)
                    : e <= 16384 ? stream_forward<T, WT, 512, 32>(a, rows, device, num_sms, stream)
                                 : 1;
-    if (rc != 1) return rc;
+    if (rc != 1) {
+      *kernel = "layer_norm_stream_kernel";
+      return rc;
+    }
   }
+  *kernel = "layer_norm_kernel";
   if (vectors) {
     if (n <= 32) return launch_forward<T, WT, V, 32, 1>(a, stream);
     if (n <= 64) return launch_forward<T, WT, V, 32, 2>(a, stream);
@@ -527,7 +531,7 @@ int launch_grad(NormArgs a, float* scratch, int num_sms, int* ctas, cudaStream_t
 
 template <class T, class WT>
 int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_sms,
-         cudaStream_t stream, int* launches) {
+         cudaStream_t stream, int* launches, const char** kernel) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   const bool columns = dweight || dbias, vectors = rows == Rows::kVectors;
   const int n = vectors ? (a.width + V - 1) / V : a.width;
@@ -544,7 +548,9 @@ int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_
   }
   float* const parts = columns ? scratch : nullptr;
   int ctas = 0, rc;
+  *kernel = "layer_norm_grad_kernel";
   if (a.rows == 0) {
+    *kernel = "norm_columns_kernel";
     rc = GEMM_F32_OK;
   } else {
     const int e = a.width + (vectors ? 0 : V - 1);
@@ -562,7 +568,10 @@ int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_
          : e <= 16384 ? stream_grad<T, WT, 512, 16, 2>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 32768 ? stream_grad<T, WT, 512, 16, 4>(a, rows, parts, device, num_sms, &ctas, stream)
                       : 1;
-    if (rc != 1) ++*launches;
+    if (rc != 1) {
+      *kernel = "layer_norm_grad_stream_kernel";
+      ++*launches;
+    }
   }
   if (rc == 1 && !wide) {
     if (vectors && V == 8) {
@@ -700,13 +709,14 @@ extern "C" int gemm_f32_layer_norm(int type, int weight_type, long long rows, in
                                                  : Rows::kUneven;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
   int rc;
+  const char* kernel = "none";
   if (type == GEMM_F32_TYPE_F32)
-    rc = forward<float, float>(a, how, device, num_sms, stream);
+    rc = forward<float, float>(a, how, device, num_sms, stream, &kernel);
   else if (weight_type == GEMM_F32_TYPE_F32)
-    rc = forward<bf16, float>(a, how, device, num_sms, stream);
+    rc = forward<bf16, float>(a, how, device, num_sms, stream, &kernel);
   else
-    rc = forward<bf16, bf16>(a, how, device, num_sms, stream);
-  if (rc == GEMM_F32_OK) note_launches(1, "layer_norm_kernel");
+    rc = forward<bf16, bf16>(a, how, device, num_sms, stream, &kernel);
+  if (rc == GEMM_F32_OK) note_launches(1, kernel);
   return rc;
 }
 
@@ -754,13 +764,14 @@ extern "C" int gemm_f32_layer_norm_grad(int type, int weight_type, long long row
                                                                                         : Rows::kUneven;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
   int rc, launches = 0;
+  const char* kernel = "none";
   const WorkspaceCall call;
   if (type == GEMM_F32_TYPE_F32)
-    rc = grad<float, float>(a, how, dweight, dbias, device, num_sms, stream, &launches);
+    rc = grad<float, float>(a, how, dweight, dbias, device, num_sms, stream, &launches, &kernel);
   else if (weight_type == GEMM_F32_TYPE_F32)
-    rc = grad<bf16, float>(a, how, dweight, dbias, device, num_sms, stream, &launches);
+    rc = grad<bf16, float>(a, how, dweight, dbias, device, num_sms, stream, &launches, &kernel);
   else
-    rc = grad<bf16, bf16>(a, how, dweight, dbias, device, num_sms, stream, &launches);
-  if (rc == GEMM_F32_OK) note_launches(launches, "layer_norm_grad_kernel");
+    rc = grad<bf16, bf16>(a, how, dweight, dbias, device, num_sms, stream, &launches, &kernel);
+  if (rc == GEMM_F32_OK) note_launches(launches, kernel);
   return rc;
 }

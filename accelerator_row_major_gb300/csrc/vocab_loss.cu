@@ -455,7 +455,7 @@ int pack(Operand::Form form, const Packing& x, const Packing& w, bool f32, int n
                : launch(loss_pack_kernel<bf16, 1, bf16>, grid, 256, stream, launches, x, w, err);
 }
 
-int run(const Call& c, cudaStream_t stream, int* launches) {
+int run(const Call& c, cudaStream_t stream, int* launches, const char** kernel) {
   int device = 0, num_sms = 0;
   unsigned* err = nullptr;
   if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
@@ -466,6 +466,7 @@ int run(const Call& c, cudaStream_t stream, int* launches) {
   const FewClasses by_class = few_classes(f32, c.w, c.ldw, c.vocab);
   const bool direct = !grad && !by_class.aligned() && c.rows <= kFewRows && c.vocab >= by_class.count;
   const bool few = direct || c.rows <= (f32 ? kFewRows : kFewRowsBf16);
+  *kernel = few ? "few_gemm_kernel" : "half_gemm_kernel";
   const int parts = f32 ? 3 : 1;
   const long long ld_exps = static_cast<long long>(round_up(c.vocab, 256));
   const int piece_bits = few ? kFewPieceBits : kPieceBits;
@@ -735,8 +736,9 @@ int checked(Call& c, long long rows, gemm_f32_stream_t stream_handle) {
   }
   int launches = 0;
   const WorkspaceCall call;
-  const int rc = run(c, stream, &launches);
-  if (rc == GEMM_F32_OK) note_launches(launches, "half_gemm_kernel");
+  const char* kernel = "none";
+  const int rc = run(c, stream, &launches, &kernel);
+  if (rc == GEMM_F32_OK) note_launches(launches, kernel);
   return rc;
 }
 

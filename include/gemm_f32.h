@@ -184,8 +184,8 @@ int gemm_f32_last_launches(void);
  * "tc_gemm_kernel" (tensor cores, one SM per tile), "ffma_gemm_kernel",
  * "small_gemm_kernel" (small products), "memset" (K == 0),
  * "scale_window_kernel" (gemm_f32_general with
- * alpha == 0 or K == 0), "ladder_v0" .. "ladder_v4" (gemm_f32_ladder) or
- * "none" (nothing launched).  Static string. */
+ * alpha == 0 or K == 0), "ladder_v0" .. "ladder_v4" (gemm_f32_ladder), those
+ * that gemm_f32_lm.h lists, or "none" (nothing launched).  Static string. */
 const char* gemm_f32_last_kernel(void);
 
 /* C = A * B with A, B and C in HOST memory: copies A and B to the device,

@@ -27,6 +27,13 @@
  * memory cannot be had the call returns GEMM_F32_ESCRATCH and launches
  * nothing.
  *
+ * gemm_f32_last_kernel() names the kernel of a call's main pass: for the norms
+ * "layer_norm_stream_kernel" or "layer_norm_grad_stream_kernel" (many rows),
+ * "layer_norm_kernel" or "layer_norm_grad_kernel" (few rows, or rows too wide
+ * for the others), "norm_columns_kernel" (gradient of no rows); for the losses
+ * the kernel of the logits, "half_gemm_kernel" or, of few rows,
+ * "few_gemm_kernel"; "memset" for the loss of no rows.
+ *
  * Every sum is taken in a fixed order: the same call on the same inputs
  * gives the same bits.
  */
