@@ -760,7 +760,8 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* pt
 }
 
 // The maps of w: for the logits one per class, its rows from the boundary
-// below row c on.
+// below row c on.  (That of row 0 lies up to 14 bytes before w, in a 16-byte
+// block that also holds w's first element; its values are masked.)
 bool encode_w(const FewGemm& g, bool mn, CUtensorMap* maps) {
   const CUtensorMapDataType type = g.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int size = g.f32 ? 4 : 2, box_cols = 128 / size;

@@ -16,8 +16,8 @@
 //
 // RAGGED: rows that do not all start and end on 16-byte boundaries.  A row is
 // copied from the boundary below its start to the one above its end (never
-// beyond the matrix: what is left at its first and last bytes is copied by a
-// thread), and threads take the 16-byte vectors of that copy, of which the
+// beyond the matrix: what is left at its first and last bytes, in the first
+// and the last row or in rows closer than 16 bytes, is copied by a thread), and threads take the 16-byte vectors of that copy, of which the
 // first and the last hold elements of other rows.  Rows start 0 to 14 bytes
 // above a boundary, each of 16 / gcd(16, stride) rows differently; the number
 // of groups is a multiple of that, so that a group meets rows of one start
@@ -136,7 +136,7 @@ struct RowRing {
     if (next < a.rows) {
       const uint32_t bar = bars + 8u * at;
       uint8_t* const dst = data + static_cast<size_t>(at) * ARRAYS * row_bytes;
-      if (RAGGED && next > 0 && next < a.rows - 1) {   // the blocks around the row are the matrix's
+      if (RAGGED && inner()) {                 // the blocks around the row are the matrix's
         mbar_arrive_expect_tx(bar, ARRAYS * around);
 #pragma unroll
         for (int i = 0; i < ARRAYS; ++i)
@@ -165,8 +165,27 @@ struct RowRing {
     }
     next += step;
   }
+  // Whether row `next` has a whole block of the matrix before it and one behind
+  // it: not the first row nor the last, nor rows that lie closer than a block.
+  __device__ __forceinline__ bool inner() const {
+    constexpr long long kBlock = 16 / static_cast<int>(sizeof(T));
+    if (next == 0 || next == a.rows - 1 || a.ldx < kBlock || (ARRAYS == 2 && a.lddy < kBlock)) return false;
+#ifdef GEMM_BOUNDS_CHECK
+    for (int i = 0; i < ARRAYS; ++i) {
+      const long long ld = i == 0 ? a.ldx : a.lddy;
+      const uintptr_t lowest = reinterpret_cast<uintptr_t>(i == 0 ? a.x : a.dy);
+      const uintptr_t from = reinterpret_cast<uintptr_t>(source(i, next)) & ~uintptr_t{15};
+      // what lies before the matrix wraps round to beyond it
+      const size_t bytes = stored_extent(a.rows, a.width, ld) * sizeof(T);
+      if (!GEMM_IN_EXTENT(from - lowest, bytes, a.err, kSiteBoundsRows) ||
+          !GEMM_IN_EXTENT(from + around - 1 - lowest, bytes, a.err, kSiteBoundsRows))
+        return false;
+    }
+#endif
+    return true;
+  }
   // The 16-byte blocks of row `next` that lie within the matrix go by one bulk
-  // copy (`bytes` from `from` on); its elements outside them, at the matrix's
+  // copy (`bytes` from `from` on); its elements outside them, near the matrix's
   // two ends only, are copied here.
   __device__ __forceinline__ void edges(int array, uint8_t* dst, uintptr_t& from, uint32_t& bytes) {
     const T* const row = source(array, next);
