@@ -69,7 +69,6 @@ constexpr int kSumBf16 = 16;             // K blocks per accumulator sum
 constexpr int kSumStacked = 8;
 constexpr int kStackedRows = 64;         // most rows with the parts of b stacked
 constexpr int sum_blocks(bool f32, bool stacked) { return !f32 ? kSumBf16 : stacked ? kSumStacked : 1; }
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool F32>
 struct Cfg {
@@ -239,14 +238,12 @@ __device__ __forceinline__ void logits_out(const FewParams& p, int piece, int v,
                                            const float (&acc)[64], int at) {
   const bool in = v < p.vocab;
   constexpr float kUp = F32 ? 0.0f : 15.0f;   // one part: powers times 2^15 (fp16)
-  float m2[16], e[16];
+  float top[16], e[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const float z = in ? acc[at + j] : -INFINITY;
-    const float top = warp_max(z);
-    // nothing above -inf: any finite reference gives powers of 0
-    m2[j] = top == -INFINITY ? 0.0f : top * kLog2e;
-    e[j] = exp2_approx(fmaf(z, kLog2e, kUp - m2[j]));
+    top[j] = warp_max(z);
+    e[j] = exp2_approx(fmaf(z - reference(top[j]), kLog2e, kUp));
   }
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -262,9 +259,9 @@ __device__ __forceinline__ void logits_out(const FewParams& p, int piece, int v,
       static_cast<__half*>(p.exps)[to] = __float2half_rn(e[j]);
   }
   const float sum = warp_sum16(e, lane);
-  float m = m2[0];
+  float m = top[0];
 #pragma unroll
-  for (int j = 1; j < 16; ++j) m = lane >> 1 == j ? m2[j] : m;
+  for (int j = 1; j < 16; ++j) m = lane >> 1 == j ? top[j] : m;
   const int t = t0 + (lane >> 1);
   const size_t stat = static_cast<size_t>(piece) * p.ld_stats + t;
   if ((lane & 1) == 0 && t < p.rows &&

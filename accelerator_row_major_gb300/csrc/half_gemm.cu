@@ -83,7 +83,6 @@ constexpr int kMostTeam = 4;
 constexpr int kSumF32 = 4;
 constexpr int kSumLogits = 16;
 constexpr int kWholeLogits = 1024;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Epilogues
 constexpr int kLogits = 0;
@@ -617,12 +616,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 4; j < 32; ++j) t[j % 4] = fmaxf(t[j % 4], v[j]);
           top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
         }
-        // nothing above -inf: any finite reference gives powers of 0
-        const float m2 = top == -INFINITY ? 0.0f : top * kLog2e;
+        const float below = -reference(top);
         const int label = row_ok ? label_at(p.targets, row) - n0 : -1;
         // one part: powers times 2^15, which keep their 11 bits in fp16 down to 2^-29
         constexpr float kUp = PARTS == 3 ? 0.0f : 15.0f;
-        const Pair by = pair_of(kLog2e, kLog2e), minus = pair_of(kUp - m2, kUp - m2);
+        const Pair minus = pair_of(below, below), by = pair_of(kLog2e, kLog2e), up = pair_of(kUp, kUp);
         Pair sums = 0;
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
@@ -637,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            unpair(fma2(pair_of(v[j], v[j + 1]), by, minus), v[j], v[j + 1]);
+            unpair(fma2(add2(pair_of(v[j], v[j + 1]), minus), by, up), v[j], v[j + 1]);
             v[j] = exp2_approx(v[j]);
             v[j + 1] = exp2_approx(v[j + 1]);
             sums = add2(sums, pair_of(v[j], v[j + 1]));
@@ -657,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (row_ok && GEMM_IN_EXTENT(stat, 2 * static_cast<size_t>(p.tiles_n) * p.ld_stats, p.err,
                                      kSiteBoundsScratch))
           p.stats[stat] =
-              make_float2(m2, PARTS == 3 ? sum_of(sums) : sum_of(sums) * (1.0f / 32768.0f));
+              make_float2(top, PARTS == 3 ? sum_of(sums) : sum_of(sums) * (1.0f / 32768.0f));
       }
     }
     if (lane == 0) tma_store_wait();

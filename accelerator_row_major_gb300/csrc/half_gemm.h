@@ -36,8 +36,8 @@ struct HalfGemm {
   const float* add = nullptr;   // fp32, row stride ldadd; may be c itself
   long long ldadd = 0;
   float* partials = nullptr;    // half_gemm_scratch() bytes
-  // -- or logits (c == nullptr): per row and 128 columns the maximum m of
-  // z log2(e) and the sum of 2^(z log2(e) - m); with `exps`, those powers
+  // -- or logits (c == nullptr): per row and 128 columns the maximum m of z
+  // and the sum of 2^((z - m) log2 e); with `exps`, those powers
   // too (fp16 times 2^15 for one part, fp32 for three), zero from column N on
   float2* stats = nullptr;      // [2 ceil(N / 256)][ld_stats]
   long long ld_stats = 0;

@@ -114,6 +114,17 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Powers of the logits z of a tile relative to its maximum m are
+// 2^((z - m) log2 e).  z - m first: it is exact near the maximum, whatever its
+// size.  A product z log2 e - m log2 e by fma is off by half a last place of
+// m log2 e, which is whole powers of 2 for logits of 10^7 (masks of -10^10 gave
+// infinite sums), and it overflows from 2.36e38 on.
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What the powers are taken relative to: of a tile with nothing above -inf any
+// finite value gives powers of 0.
+__device__ __forceinline__ float reference(float top) { return top == -INFINITY ? 0.0f : top; }
+
 // 16 bytes as pairs: 2 of fp32, 4 of bfloat16.
 template <class T>
 __device__ __forceinline__ void pairs_of(const uint4& q, Pair (&v)[8 / sizeof(T)]) {

@@ -6,14 +6,14 @@
 // The logits are a product of 2 T V D operations whose result is only needed
 // through its rows' maxima and sums of exponentials, so its epilogue
 // (half_gemm.cu) reduces each 128 columns to a maximum m and a sum of
-// exponentials relative to m, in base 2, and the rows join these:
-//   M = max m_i,  S = sum s_i 2^(m_i - M),  lse = (M + log2 S) / log2 e.
+// exponentials relative to m, and the rows join these:
+//   M = max m_i,  S = sum s_i exp(m_i - M),  lse = M + log S.
 // What bounds it: few rows, the read of w; many rows, the tensor cores.
 //
 // With gradients the logits are computed once too (6 T V D operations in
 // all, not 8): for a piece of the rows at a time the epilogue keeps
-// e = 2^(z log2 e - m), the rescaling pass turns it in place into
-//   g = e 2^(m - M) / S - onehot
+// e = exp(z - m), the rescaling pass turns it in place into
+//   g = e exp(m - M) / S - onehot
 // and two more products give dx = s g w and dw += s g^T x.  e is kept in
 // fp16 (times 2^15: 11 bits for whatever lies within 2^-29 of its tile's
 // maximum) and g in bfloat16, the operand type of the products: one rounding
@@ -58,9 +58,9 @@ struct Factors {
 
 // ---------------------------------------------------------------- joining
 // lse and loss of 4 rows per CTA (4 statistics of a piece share a 32-byte
-// sector): the largest maximum M of a row's pieces, then S = sum s 2^(m - M).
-// A piece with sum 0 has nothing above -inf (its m stands for nothing) and
-// does not count; a NaN sum does.  joined (may be null) receives (M, 1 / S).
+// sector): the largest maximum M of a row's pieces, then S = sum s exp(m - M).
+// A piece with sum 0 has nothing above -inf (its m is that) and does not
+// count; a NaN sum does.  joined (may be null) receives (M, 1 / S).
 //
 // The CTA that finishes last adds up what the call needs of all rows: the
 // factors (in the first piece of the rows) and the total (in the last), from
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
 #pragma unroll 8
   for (int i = chain; i < end; i += kChains) {
     const float2 p = __ldg(mine + i * a.ld);
-    sum += p.y != 0.0f ? p.y * exp2f(p.x - top) : 0.0f;
+    sum += p.y != 0.0f ? p.y * exp2f((p.x - top) * kLog2e) : 0.0f;
   }
 #pragma unroll
   for (int o = kJoinRows; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
       sum = sums[0][r];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) sum += sums[w][r];
-      const float l = sum == 0.0f ? -INFINITY : kLn2 * (top + log2f(sum));
+      const float l = sum == 0.0f ? -INFINITY : fmaf(kLn2, log2f(sum), top);
       if (label >= 0) {
         s = l - logit;
       } else {
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(THREADS) loss_join_kernel(const JoinArgs a) {
   if (a.last && a.total) *a.total = s / per;
 }
 
-// The rescaling pass of the gradient, g = e 2^(m - M) / S - onehot: 4 rows by
+// The rescaling pass of the gradient, g = e exp(m - M) / S - onehot: 4 rows by
 // a band of the columns per CTA.
 constexpr int kRescaleThreads = 256;
 constexpr int kRescaleRows = 4;
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kRescaleThreads)
       if (row0 + r >= rows) break;
       const size_t at = static_cast<size_t>(row0 + r) * ld + c;
       if (!GEMM_IN_EXTENT(at + 7, extent, err, kSiteBoundsScratch)) continue;
-      const float by = exp2f(f[r] - m[r]) * inv[r];
+      const float by = exp2f((f[r] - m[r]) * kLog2e) * inv[r];
       float g[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
