@@ -20,6 +20,7 @@ from ._binding import (FLAG_CTA_PAIR, FLAG_FORCE_STAGED, FLAG_SINGLE_CTA, FLAG_T
                        FLAG_NO_SPLIT_K, FLAG_ONE_TILE_PER_CTA, FLAG_TEST_DROP_COPY, GEMM_F32_EDEVICE, GEMM_F32_EINVAL,
                        GEMM_F32_ELAUNCH, GEMM_F32_ESCRATCH, GEMM_F32_ETARGET, GEMM_F32_ETIMEOUT, GEMM_F32_OK, LIB_PATH, MODE_FFMA,
                        MODE_TC1X, MODE_TC3X, MODES, GemmError, check, declared_symbols,
+                       elsewhere as _elsewhere,
                        gemm_f32, gemm_f32_ex, gemm_f32_general, gemm_f32_host, gemm_f32_ladder, gemm_f32_last_kernel, gemm_f32_last_launches,
                        gemm_f32_noalloc, LADDER_STEPS,
                        gemm_f32_release, NOALLOC_SCRATCH_BYTES,
@@ -46,8 +47,6 @@ def matmul(A, B, out=None, mode="tc3x", flags: int = 0, stream=None):
     when ``out`` is None; raises GemmError on a non-zero return code."""
     import torch
 
-    from ._binding import elsewhere
-
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[0]:
         raise ValueError("shapes %s and %s do not chain" % (tuple(A.shape), tuple(B.shape)))
     for name, t in (("A", A), ("B", B)):
@@ -55,9 +54,8 @@ def matmul(A, B, out=None, mode="tc3x", flags: int = 0, stream=None):
             raise ValueError("%s must be a contiguous float32 CUDA tensor" % name)
     if B.get_device() != A.get_device() or (out is not None and out.get_device() != A.get_device()):
         raise ValueError("A, B and out must be on one device")
-    there = elsewhere(A.get_device(), stream)
-    if there is not None:
-        with there:
+    if stream is not None or torch._C._cuda_getDevice() != A.get_device():
+        with _elsewhere(A.get_device(), stream):
             return matmul(A, B, out, mode, flags)
     M, K = A.shape
     N = B.shape[1]

@@ -158,12 +158,12 @@ def _stream(s) -> int:
 
 def elsewhere(device: int, stream):
     """The context in which a call on tensors of `device` is made, with
-    `stream` (None: torch's current one) as the current stream of its device;
-    None where that is so already.  The C calls take the current device."""
+    `stream` (None: torch's current one) as the current stream of its device.
+    The C calls take the current device."""
     import torch
 
     if stream is None:
-        return None if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
+        return torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)
         stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)

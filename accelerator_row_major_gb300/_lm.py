@@ -18,6 +18,7 @@ from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, check, elsewhere, lib
 
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
 _F32 = torch.float32
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream      # current_stream(i).cuda_stream, without the objects
 
 
@@ -73,9 +74,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     weight and bias hold x's type or float32 (None: 1 and 0); mean and rstd
     are float32, one value per row.  `out` may be x itself."""
     kind, dev, rows, width, ldx = _matrix("x", x)
-    there = elsewhere(dev, stream)
-    if there is not None:
-        with there:
+    if stream is not None or _current_device() != dev:
+        with elsewhere(dev, stream):
             return layer_norm(x, weight, bias, eps, out)
     wtype, pw, pb = x.dtype, 0, 0
     if weight is not None:
@@ -104,9 +104,8 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, stream=None):
     dweight and dbias hold weight's type (float32 for weight None).  `out`,
     the tensor for dx, may be dy or x itself."""
     kind, dev, rows, width, ldx = _matrix("x", x)
-    there = elsewhere(dev, stream)
-    if there is not None:
-        with there:
+    if stream is not None or _current_device() != dev:
+        with elsewhere(dev, stream):
             return layer_norm_grad(dy, x, weight, mean, rstd, out)
     lddy = _like("dy", dy, x)
     wtype, pw = _F32, 0
@@ -153,9 +152,8 @@ def vocab_loss(x, w, targets, ignore_index=-100, reduction="mean", stream=None):
     target outside the vocabulary counts as ignored and is reported by
     gemm_f32_status()."""
     matrix = _matrix("x", x)
-    there = elsewhere(matrix[1], stream)
-    if there is not None:
-        with there:
+    if stream is not None or _current_device() != matrix[1]:
+        with elsewhere(matrix[1], stream):
             return vocab_loss(x, w, targets, ignore_index, reduction)
     args, code, loss, lse, total = _loss_args(x, w, targets, reduction, matrix)
     check(lib().gemm_f32_vocab_loss(*args, ignore_index, code, loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
@@ -171,9 +169,8 @@ def vocab_loss_grad(x, w, targets, ignore_index=-100, reduction="mean", grad_sca
     piece_bytes bounds the scratch that holds a piece of the rows (0: the
     library's default)."""
     matrix = _matrix("x", x)
-    there = elsewhere(matrix[1], stream)
-    if there is not None:
-        with there:
+    if stream is not None or _current_device() != matrix[1]:
+        with elsewhere(matrix[1], stream):
             return vocab_loss_grad(x, w, targets, ignore_index, reduction, grad_scale, need_dx, need_dw, piece_bytes)
     args, code, loss, lse, total = _loss_args(x, w, targets, reduction, matrix)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None

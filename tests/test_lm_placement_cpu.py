@@ -78,6 +78,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "default_stream", lambda d: Stream(d, 0))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: state.streams[int(str(d)[-1])])
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state.device, raising=False)
+    monkeypatch.setattr(_lm, "_current_device", lambda: state.device)
     monkeypatch.setattr(_lm, "_raw_stream", lambda d: state.streams[d].cuda_stream)
     monkeypatch.setattr(_binding, "lib", lambda: Library())
     monkeypatch.setattr(_lm, "lib", lambda: Library())
