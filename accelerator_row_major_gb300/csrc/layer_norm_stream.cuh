@@ -108,7 +108,7 @@ struct RowRing {
 
   __device__ __forceinline__ RowRing(const NormArgs& args, uint8_t* smem, int group, int groups, int st,
                                      int slice, int rank, int ctas)
-      : a(args), width(args.width), col0(0), stages(st) {
+      : a(args), width(min(slice, args.width)), col0(0), stages(st) {   // a value of its own, not a parameter: fewer spills
     row_bytes = static_cast<uint32_t>(ring_row_bytes(slice, sizeof(T), RAGGED));
     data = smem + static_cast<size_t>(group) * st * ARRAYS * row_bytes;
     bars = smem_addr(smem) + static_cast<uint32_t>(groups) * st * ARRAYS * row_bytes +
