@@ -564,19 +564,22 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G)
       rstd_n = __ldg(a.rstd + row + ring.step);
     }
     const Pair minus = pair_of(-mean, -mean), by = pair_of(rstd, rstd);
-    Pair hat[NP], g[NP], sg = 0, sgh = 0;
-    mine.load(ring.at(0), t, hat);
+    // c = x - mean in place of hat = c rstd.  Outside the row dy is 0 and c
+    // -mean: 0 in every sum, where hat might be infinite (times 0: not a
+    // number).  Where rstd is 0, squares that overflowed, so are the hats.
+    Pair c[NP], g[NP], sg = 0, sgc = 0;
+    mine.load(ring.at(0), t, c);
     mine.load(ring.at(1), t, g);
 #pragma unroll
-    for (int q = 0; q < NP; ++q) {           // dy is 0 outside the row
-      hat[q] = mul2(add2(hat[q], minus), by);
-      dw[q] = fma2(g[q], hat[q], dw[q]);
+    for (int q = 0; q < NP; ++q) {
+      c[q] = add2(c[q], minus);
+      dw[q] = fma2(mul2(g[q], by), c[q], dw[q]);
       db[q] = add2(db[q], g[q]);
       g[q] = mul2(g[q], w[q]);
       sg = add2(sg, g[q]);
-      sgh = fma2(g[q], hat[q], sgh);
+      sgc = fma2(g[q], c[q], sgc);
     }
-    float s[2] = {sum_of(sg), sum_of(sgh)};
+    float s[2] = {sum_of(sg), rstd != 0.0f ? sum_of(sgc) * rstd : 0.0f};
     group_sum<2, G>(s, part[flip][group], group);
     if (t == 0) ring.load(ring.s);           // the group has read this stage
     ring.advance();
@@ -596,10 +599,10 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G)
     }
     flip ^= 1;
     if (a.out) {
-      const float c1 = -s[0] * inv, c2 = -s[1] * inv;
+      const float c1 = -s[0] * inv, c2 = -s[1] * inv * rstd;
       const Pair minus_c1 = pair_of(c1, c1), minus_c2 = pair_of(c2, c2);
 #pragma unroll
-      for (int q = 0; q < NP; ++q) g[q] = mul2(fma2(hat[q], minus_c2, add2(g[q], minus_c1)), by);
+      for (int q = 0; q < NP; ++q) g[q] = mul2(fma2(c[q], minus_c2, add2(g[q], minus_c1)), by);
       if (GEMM_IN_EXTENT(row * a.ldo + a.width - 1, stored_extent(a.rows, a.width, a.ldo), a.err,
                          kSiteBoundsRows))
         mine.store(static_cast<T*>(a.out) + row * a.ldo + col0, g);
