@@ -208,9 +208,28 @@ struct RowRing {
     bytes = static_cast<uint32_t>(hi - lo);
   }
   // A wait that runs out is recorded, and the thread goes on (the result is
-  // undefined, as the status says): the group's barriers need all of it.
+  // undefined, as the status says): the group's barriers need all of it.  The
+  // one that issues the copies issues no more.
   __device__ __forceinline__ void wait() {
     if (!lost) lost = !mbar_wait(bars + 8u * s, ph, a.err, kSiteTransformFull);
+  }
+  // The issuing thread, after its last row (`row` is beyond it): where it gave
+  // up, it waits, again with a limit, for its copies still in flight, which
+  // would land in memory that is no longer the kernel's.  They are those of the
+  // rows from next - stages step on; the stage and phase of the first follow
+  // from those of `row`.
+  __device__ __forceinline__ void finish(long long row) const {
+    if (!lost) return;
+    const long long first = next - stages * step, since = (row - first) / step;
+    int at = static_cast<int>(((s - since) % stages + stages) % stages);
+    uint32_t parity = ph ^ (static_cast<uint32_t>((at + since) / stages) & 1u);
+    for (int k = 0; k < stages && first + k * step < a.rows; ++k) {
+      mbar_wait(bars + 8u * at, parity, a.err, kSiteDrainTma);
+      if (++at == stages) {
+        at = 0;
+        parity ^= 1u;
+      }
+    }
   }
   // The stage's copy of an array's row.
   __device__ __forceinline__ const uint8_t* at(int array) const {
@@ -480,7 +499,7 @@ __global__ void __launch_bounds__(stream_threads(G), 1)
     for (int q = 0; q < NP; ++q) sum = add2(sum, x[q]);
     float s[1] = {sum_of(sum)};
     group_sum<1, G>(s, part[0][group], group);
-    if (t == 0) ring.load(ring.s);      // the group has read this stage
+    if (t == 0 && !ring.lost) ring.load(ring.s);   // the group has read this stage
     ring.advance();
     const float mean = s[0] * inv;
     const Pair minus = pair_of(-mean, -mean);
@@ -507,6 +526,7 @@ __global__ void __launch_bounds__(stream_threads(G), 1)
     if (GEMM_IN_EXTENT(row * a.ldo + a.width - 1, stored_extent(a.rows, a.width, a.ldo), a.err, kSiteBoundsRows))
       mine.store(static_cast<T*>(a.out) + row * a.ldo, x);
   }
+  if (t == 0) ring.finish(row);
 }
 
 // Two floats into the shared memory of another CTA of the cluster, counted by
@@ -581,7 +601,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G)
     }
     float s[2] = {sum_of(sg), rstd != 0.0f ? sum_of(sgc) * rstd : 0.0f};
     group_sum<2, G>(s, part[flip][group], group);
-    if (t == 0) ring.load(ring.s);           // the group has read this stage
+    if (t == 0 && !ring.lost) ring.load(ring.s);   // the group has read this stage
     ring.advance();
     if constexpr (CTAS > 1) {                // every CTA adds the slices' sums in order
       if (t == 0) mbar_arrive_expect_tx(bars + 8u * flip, CTAS * 8u);
@@ -610,6 +630,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(stream_threads(G)
     mean = mean_n;
     rstd = rstd_n;
   }
+  if (t == 0) ring.finish(row);
   if (CTAS > 1) cluster_sync();              // no CTA leaves while another may write to it
   if (!a.partials) return;
   // the groups' column sums, added in group order: one row of partials per
