@@ -116,8 +116,8 @@ thread_local int t_last_launches = 0;
 thread_local const char* t_last_kernel = "none";
 
 // Set-up runs once per device, with that device current: checks it is an
-// sm_103 part, reads the SM count, takes the address of the error word and
-// clears it, and looks up the address of gemm_f32_noalloc's fixed scratch
+// sm_103 part, reads the SM count, takes the address of the error word, and
+// looks up the address of gemm_f32_noalloc's fixed scratch
 // array (which, under lazy module loading, loads the module that holds it:
 // the array is placed here, at the library's first call on the device, not
 // inside a later gemm_f32_noalloc call).
@@ -138,13 +138,11 @@ DeviceState* device_state(int* device_out) {
       return;
     }
     if (major != 10 || minor != 3) return;  // the kernels are built for sm_103a only
+    // this call may be one of a capture: no work is queued (the words are zero
+    // when their module is loaded)
+    const CudaMemory::Relaxed relaxed;
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_words) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return;
-    }
-    const unsigned zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (cudaMemcpy(p, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) {
       (void)cudaGetLastError();
       return;
     }

@@ -156,3 +156,45 @@ def test_outputs_belong_to_the_stream_that_is_given():
     c = g.matmul(x, xt, stream=s.cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(c, product)
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import ctypes
+import sys
+sys.path.insert(0, %r)
+import torch
+import accelerator_row_major_gb300 as g
+x = torch.randn(600, 9000, device="cuda")
+w = torch.randn(500, 9000, device="cuda") / 100
+y = torch.randint(0, 500, (600,), device="cuda")
+torch.cuda.synchronize()
+stream = torch.cuda.Stream()
+if %r:
+    handle = ctypes.c_void_p()
+    assert ctypes.CDLL("libcuda.so.1").cuStreamCreate(ctypes.byref(handle), 0) == 0
+    stream = torch.cuda.ExternalStream(handle.value)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=stream):
+    a = g.vocab_loss_grad(x, w, y)
+    n, mean, rstd = g.layer_norm(x)
+    b = g.layer_norm_grad(x, n, None, mean, rstd)
+graph.replay()
+torch.cuda.synchronize()
+n2, mean, rstd = g.layer_norm(x)
+want = g.vocab_loss_grad(x, w, y) + (n2,) + g.layer_norm_grad(x, n2, None, mean, rstd)
+assert all(torch.equal(p, q) for p, q in zip(a + (n,) + b, want))
+assert g.gemm_f32_status(None) == (0, 0)
+print("same")
+"""
+
+
+@pytest.mark.parametrize("legacy", [False, True])
+def test_first_call_of_a_process_in_a_capture(legacy):
+    """The library sets the device up in whatever call comes first; `legacy`: a capture of a stream that the legacy
+    default stream waits for, which takes no work meanwhile."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE % (root, legacy)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.strip() == "same", run.stdout + run.stderr[-3000:]
