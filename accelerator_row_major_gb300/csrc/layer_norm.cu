@@ -428,8 +428,8 @@ int launch_stream(const NormArgs& a, bool ragged, size_t size, size_t least_smem
   }
   const int units = ragged ? most / kWhole * kWhole : most, grid = units * CTAS;
   // of a shared row: whole 16-byte blocks, of which a ragged row may take one more than its elements fill
-  const int blocks = a.width + (ragged ? 16 / static_cast<int>(size) - 1 : 0);
-  const int slice = CTAS == 1 ? a.width : ((blocks + CTAS - 1) / CTAS + 7) / 8 * 8;
+  const long long blocks = a.width + (ragged ? 16 / static_cast<long long>(size) - 1 : 0);
+  const int slice = CTAS == 1 ? a.width : static_cast<int>(((blocks + CTAS - 1) / CTAS + 7) / 8 * 8);
   const size_t row = ring_row_bytes(slice, size, ragged) * ARRAYS;
   const int stages = static_cast<int>(std::min<size_t>(kMostStages, kStreamBytes / (kGroups * (row + 8))));
   if (a.rows < static_cast<long long>(kStreamRows) * units * kGroups || stages < 2 || units == 0) return 1;
@@ -475,9 +475,9 @@ template <class T, class WT>
 int forward(const NormArgs& a, Rows rows, int device, int num_sms, cudaStream_t stream, const char** kernel) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   const bool vectors = rows == Rows::kVectors;
-  const int n = vectors ? (a.width + V - 1) / V : a.width;
+  const int n = vectors ? (a.width - 1) / V + 1 : a.width;
   if (rows != Rows::kUneven) {
-    const int e = a.width + (vectors ? 0 : V - 1);   // a row's start may take part of a vector
+    const long long e = a.width + (vectors ? 0LL : V - 1LL);   // a row's start may take part of a vector
     const int rc = e <= 256     ? stream_forward<T, WT, 32, 8>(a, rows, device, num_sms, stream)
                    : e <= 512   ? stream_forward<T, WT, 32, 16>(a, rows, device, num_sms, stream)
                    : e <= 768   ? stream_forward<T, WT, 32, 24>(a, rows, device, num_sms, stream)
@@ -534,7 +534,7 @@ int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_
          cudaStream_t stream, int* launches, const char** kernel) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   const bool columns = dweight || dbias, vectors = rows == Rows::kVectors;
-  const int n = vectors ? (a.width + V - 1) / V : a.width;
+  const int n = vectors ? (a.width - 1) / V + 1 : a.width;
   // vectors (elements where unaligned) that the widest register kernel holds
   const bool wide = n > (vectors ? 16384 / V : 8192);
   const long long bands = std::min<long long>(a.rows, 2LL * num_sms);   // at most, in any kernel
@@ -553,7 +553,7 @@ int grad(NormArgs a, Rows rows, void* dweight, void* dbias, int device, int num_
     *kernel = "norm_columns_kernel";
     rc = GEMM_F32_OK;
   } else {
-    const int e = a.width + (vectors ? 0 : V - 1);
+    const long long e = a.width + (vectors ? 0LL : V - 1LL);
     rc = rows == Rows::kUneven ? 1
          : e <= 256   ? stream_grad<T, WT, 32, 8>(a, rows, parts, device, num_sms, &ctas, stream)
          : e <= 512   ? stream_grad<T, WT, 32, 16>(a, rows, parts, device, num_sms, &ctas, stream)

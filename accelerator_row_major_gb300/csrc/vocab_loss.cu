@@ -230,7 +230,7 @@ struct Exps<1> {
 template <int PARTS>
 __global__ void __launch_bounds__(kRescaleThreads)
     loss_rescale_kernel(const float2* stats, long long ld_stats, int piece_bits, const float2* joined,
-                        int rows, int cols, int band, LossTargets targets, void* exps, long long ld,
+                        int rows, int cols, unsigned band, LossTargets targets, void* exps, long long ld,
                         bf16* parts, long long plane, unsigned* err) {
   grid_launch_dependents();
   grid_dependency_wait();
@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(kRescaleThreads)
     m[r] = j.x;
     inv[r] = j.y * (PARTS == 3 ? 1.0f : 1.0f / 32768.0f);
   }
-  const int c_end = min(cols, (static_cast<int>(blockIdx.y) + 1) * band);
-  for (int c = blockIdx.y * band + threadIdx.x * 8; c < c_end; c += kRescaleThreads * 8) {
+  // unsigned: a step beyond the last column does not pass the type's end
+  const unsigned c_end = min(static_cast<unsigned>(cols), (blockIdx.y + 1u) * band);
+  for (unsigned c = blockIdx.y * band + threadIdx.x * 8; c < c_end; c += kRescaleThreads * 8) {
     // the rows' loads first, so that one round trip covers them
     Raw<typename Exps<PARTS>::type, 8> e[kRescaleRows];
     float f[kRescaleRows];
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kRescaleThreads)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         g[j] = Exps<PARTS>::value(e[r], j) * by;
-        if (c + j == label[r]) g[j] -= 1.0f;
+        if (static_cast<int>(c) + j == label[r]) g[j] -= 1.0f;
         if (label[r] < 0) g[j] = 0.0f;
       }
       if constexpr (PARTS == 3) {
@@ -622,8 +623,8 @@ int run(const Call& c, cudaStream_t stream, int* launches, const char** kernel) 
     const int groups = (n + kRescaleRows - 1) / kRescaleRows;
     const int cols = static_cast<int>(round_up(c.vocab, 8));
     const int bands = 8 * num_sms / groups + 1;
-    const int band = static_cast<int>(round_up((cols + bands - 1) / bands, kRescaleThreads * 8));
-    const dim3 grid(groups, static_cast<unsigned>((cols + band - 1) / band));
+    const unsigned band = static_cast<unsigned>(round_up((cols - 1) / bands + 1, kRescaleThreads * 8));
+    const dim3 grid(groups, (cols - 1) / band + 1);
     bf16* const gp = reinterpret_cast<bf16*>(scratch + at_g);
     const long long plane = f32 ? static_cast<long long>(step) * ld_exps : 0;
     rc = launch(f32 ? loss_rescale_kernel<3> : loss_rescale_kernel<1>, grid, kRescaleThreads, stream,
@@ -693,7 +694,8 @@ int checked(Call& c, long long rows, gemm_f32_stream_t stream_handle) {
   if (c.reduction != GEMM_F32_SUM && c.reduction != GEMM_F32_MEAN) return GEMM_F32_EINVAL;
   if (c.target_bits != 32 && c.target_bits != 64) return GEMM_F32_EINVAL;
   if (rows < 0 || rows > INT_MAX || c.width < 1 || c.vocab < 1) return GEMM_F32_EINVAL;
-  if (c.vocab > INT_MAX - 256 || !std::isfinite(c.grad_scale)) return GEMM_F32_EINVAL;
+  // tiles and row strides rounded up stay within an int
+  if (c.vocab > INT_MAX - 256 || c.width > INT_MAX - 256 || !std::isfinite(c.grad_scale)) return GEMM_F32_EINVAL;
   if (!aligned_to(c.loss, 4) || !aligned_to(c.lse, 4) || !aligned_to(c.total, 4))
     return GEMM_F32_EINVAL;
   const size_t size = c.type == GEMM_F32_TYPE_F32 ? 4 : 2;

@@ -104,8 +104,8 @@ enum gemm_f32_reduction {
  * loss (rows), lse (rows) and total (1) are fp32; each may be NULL.
  * rows == 0 sets total to 0.
  * Returns 0, GEMM_F32_EINVAL (unknown type, reduction or target_bits, a
- * negative size, width or vocab < 1, a stride below width, a null or
- * misaligned pointer), GEMM_F32_ESCRATCH, GEMM_F32_EDEVICE or
+ * negative size, width or vocab < 1 or above 2^31 - 257, a stride below
+ * width, a null or misaligned pointer), GEMM_F32_ESCRATCH, GEMM_F32_EDEVICE or
  * GEMM_F32_ELAUNCH. */
 int gemm_f32_vocab_loss(int type, long long rows, int width, int vocab, const void* x,
                         long long ldx, const void* w, long long ldw, const void* targets,
