@@ -56,3 +56,23 @@ def test_many_rows_of_every_group(rows, width, kind, wkind):
         _check_forward(x, w, b, 1e-5, y, mean, rstd, kind)
         assert (buf[:first] == 7).all() and (buf[first + out.numel():] == 7).all()
         _gradient(x, dy, w, mean, rstd, first, kind, wkind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,width", [(10000, 256), (10000, 257), (10000, 5), (2500, 2049), (1300, 8192), (ROWS, 12281),
+                                        (ROWS, 16384), (ROWS, 20001)])
+def test_in_place_streamed(rows, width, kind):
+    """Results over x or dy, rows of which one group reads while another writes their neighbours."""
+    torch, _ = _torch()
+    g = lib()
+    x, dy, w, b = _inputs(rows, width, kind, "f32", rows + width)
+    y, mean, rstd = g.layer_norm(x, w, b)
+    want = g.layer_norm_grad(dy, x, w, mean, rstd)
+    xc = x.clone()
+    got = g.layer_norm(xc, w, b, out=xc)
+    assert got[0] is xc and all(torch.equal(p, q) for p, q in zip(got, (y, mean, rstd)))
+    over = dy.clone()
+    assert all(torch.equal(p, q) for p, q in zip(g.layer_norm_grad(over, x, w, mean, rstd, out=over), want))
+    over = x.clone()
+    assert all(torch.equal(p, q) for p, q in zip(g.layer_norm_grad(dy, over, w, mean, rstd, out=over), want))
+    assert g.gemm_f32_status(None) == (0, 0)
