@@ -8,13 +8,14 @@ current stream of the tensors' device, and return without waiting for it.
 They run on the tensors' device, and what they allocate belongs to the stream
 they are queued on: a caller that goes on with it on another stream, or gives
 a tensor of another stream's, orders the two and keeps the memory
-(wait_stream, record_stream), as with torch's own operators.
+(wait_stream, record_stream), as with torch's own operators.  Their scratch is
+the library's, apart from torch's allocator, until gemm_f32_release().
 """
 from __future__ import annotations
 
 import torch
 
-from ._binding import REDUCTIONS, TYPE_BF16, TYPE_F32, check, elsewhere, lib
+from ._binding import GEMM_F32_ESCRATCH, REDUCTIONS, TYPE_BF16, TYPE_F32, check, elsewhere, lib
 
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
 _F32 = torch.float32
@@ -59,6 +60,17 @@ def _vector(name, t, n, dev, dtypes):
         raise ValueError("%s must be a contiguous %s tensor of %d elements on device %d"
                          % (name, " or ".join(str(d) for d in dtypes), n, dev))
     return t.data_ptr()
+
+
+def _call(name, *args):
+    """A call that needs scratch.  Where the library finds no memory for it, torch's allocator may hold some that is
+    free: it gives that back, once (but not during a capture)."""
+    entry = getattr(lib(), name)
+    code = entry(*args)
+    if code == GEMM_F32_ESCRATCH and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.empty_cache()
+        code = entry(*args)
+    check(code, name)
 
 
 def _weight_type(x, weight):
@@ -120,9 +132,8 @@ def layer_norm_grad(dy, x, weight, mean, rstd, out=None, stream=None):
         ldo = _like("out", out, x)
     dweight = torch.empty(width, dtype=wtype, device=x.device)
     dbias = torch.empty_like(dweight)
-    check(lib().gemm_f32_layer_norm_grad(kind, _TYPES[wtype], rows, width, dy.data_ptr(), lddy, x.data_ptr(), ldx, pw,
-                                         pm, pr, out.data_ptr(), ldo, dweight.data_ptr(), dbias.data_ptr(),
-                                         _raw_stream(dev)), "layer_norm_grad")
+    _call("gemm_f32_layer_norm_grad", kind, _TYPES[wtype], rows, width, dy.data_ptr(), lddy, x.data_ptr(), ldx, pw,
+          pm, pr, out.data_ptr(), ldo, dweight.data_ptr(), dbias.data_ptr(), _raw_stream(dev))
     return out, dweight, dbias
 
 
@@ -156,8 +167,8 @@ def vocab_loss(x, w, targets, ignore_index=-100, reduction="mean", stream=None):
         with elsewhere(matrix[1], stream):
             return vocab_loss(x, w, targets, ignore_index, reduction)
     args, code, loss, lse, total = _loss_args(x, w, targets, reduction, matrix)
-    check(lib().gemm_f32_vocab_loss(*args, ignore_index, code, loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
-                                    _raw_stream(matrix[1])), "vocab_loss")
+    _call("gemm_f32_vocab_loss", *args, ignore_index, code, loss.data_ptr(), lse.data_ptr(), total.data_ptr(),
+          _raw_stream(matrix[1]))
     return total, loss, lse
 
 
@@ -175,8 +186,7 @@ def vocab_loss_grad(x, w, targets, ignore_index=-100, reduction="mean", grad_sca
     args, code, loss, lse, total = _loss_args(x, w, targets, reduction, matrix)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
     dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
-    check(lib().gemm_f32_vocab_loss_grad(*args, ignore_index, code, grad_scale, loss.data_ptr(), lse.data_ptr(),
-                                         total.data_ptr(), dx.data_ptr() if need_dx else 0, args[2],
-                                         dw.data_ptr() if need_dw else 0, args[2], piece_bytes,
-                                         _raw_stream(matrix[1])), "vocab_loss_grad")
+    _call("gemm_f32_vocab_loss_grad", *args, ignore_index, code, grad_scale, loss.data_ptr(), lse.data_ptr(),
+          total.data_ptr(), dx.data_ptr() if need_dx else 0, args[2], dw.data_ptr() if need_dw else 0, args[2],
+          piece_bytes, _raw_stream(matrix[1]))
     return total, loss, lse, dx, dw

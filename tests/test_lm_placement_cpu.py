@@ -1,6 +1,7 @@
 """Where the calls on torch tensors run, on stand-ins for the tensors, the
 devices and the library: on the tensors' device, whichever is current, and on
-the stream that is given, which owns what is allocated."""
+the stream that is given, which owns what is allocated; and what becomes of a
+call for whose scratch there is no memory."""
 import contextlib
 import types
 
@@ -39,7 +40,7 @@ def world(monkeypatch):
     """The current device, each device's current stream, and what was called and allocated where."""
     import accelerator_row_major_gb300 as g
     from accelerator_row_major_gb300 import _binding, _lm
-    state = types.SimpleNamespace(device=0, streams={0: Stream(0, 10), 1: Stream(1, 20)}, calls=[], made=[])
+    state = types.SimpleNamespace(device=0, streams={0: Stream(0, 10), 1: Stream(1, 20)}, calls=[], made=[], answers=[], emptied=0, capturing=False)
 
     def empty(shape, dtype=None, device=None, **_):
         dev = int(str(device)[-1])
@@ -49,7 +50,7 @@ def world(monkeypatch):
     def entry(name):
         def call(*args):
             state.calls.append((name, state.device, state.streams[state.device].cuda_stream, args))
-            return 0
+            return state.answers.pop(0) if state.answers else 0
         return call
 
     @contextlib.contextmanager
@@ -69,6 +70,11 @@ def world(monkeypatch):
         def __getattr__(self, name):
             return entry(name)
 
+    def empty_cache():
+        state.emptied += 1
+
+    monkeypatch.setattr(torch.cuda, "empty_cache", empty_cache)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch, "empty_like", lambda t, **_: empty(t.shape, t.dtype, t.device))
     monkeypatch.setattr(torch.cuda, "device", device)
@@ -125,3 +131,16 @@ def test_a_stream_of_another_device_is_refused(world, name):
     with pytest.raises(ValueError):
         _calls(world.g, 1)[name](stream=Stream(0, 77))
     assert not world.calls
+
+
+@pytest.mark.parametrize("name", ["gemm_f32_layer_norm_grad", "gemm_f32_vocab_loss", "gemm_f32_vocab_loss_grad"])
+@pytest.mark.parametrize("capturing,answers,calls", [(False, [-5], 2), (False, [-5, -5], 2), (True, [-5], 1), (False, [-3], 1)])
+def test_memory_that_torch_holds_is_asked_for_once(world, name, capturing, answers, calls):
+    world.answers, world.capturing = list(answers), capturing
+    if len(answers) == calls:
+        with pytest.raises(world.g.GemmError) as e:
+            _calls(world.g, 0)[name]()
+        assert e.value.code == answers[0]
+    else:
+        _calls(world.g, 0)[name]()
+    assert len(world.calls) == calls and world.emptied == calls - 1
