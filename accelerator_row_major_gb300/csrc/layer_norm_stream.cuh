@@ -21,8 +21,8 @@
 // first and the last hold elements of other rows.  Rows start 0 to 14 bytes
 // above a boundary, each of 16 / gcd(16, stride) rows differently; the number
 // of groups is a multiple of that, so that a group meets rows of one start
-// only, and its threads keep their columns.  (65536 x 777 fp32: 71 and 102 us,
-// copies 60 and 90; 65536 x 1001 bfloat16: 62 and 87 us, copies 39 and 58,
+// only, and its threads keep their columns.  (65536 x 777 fp32: 71 and 103 us,
+// copies 60 and 90; 65536 x 1001 bfloat16: 65 and 90 us, copies 39 and 58,
 // bound by the instructions that the rows' ends cost.)
 //
 // CTAS > 1 (gradient of rows wider than 8192): a cluster shares a row, each

@@ -16,11 +16,15 @@
 //   g = e exp(m - M) / S - onehot
 // and two more products give dx = s g w and dw += s g^T x.  e is kept in
 // fp16 (times 2^15: 11 bits for whatever lies within 2^-29 of its tile's
-// maximum) and g in bfloat16, the operand type of the products: one rounding
-// of a probability (2^-8 of it at most), of the size of the rounding of the
-// results, and none of the -1 of the target unless its probability is large.  The row
-// scale s is applied in fp32 to the finished sums.  fp32 operands keep e in
-// fp32 and g as three bfloat16 parts.
+// maximum, which itself is exact) and g in bfloat16, the operand type of the
+// products: one rounding of g, by up to 2^-8 of it (at a target of small
+// probability p that is the p of g = p - 1 up to 2^-9).  It is of the size of
+// the rounding of the results, and adds to it where few terms make an element:
+// errors against 64 bits, over those of products with g in fp32, measured 1.42
+// for dw of one row x 4096 x 65536, 1.07 for 8 x 512 x 4096, 1.02 from 32 rows
+// on, 1.00 for 1001 x 777 x 32001.  Holding g in two parts would double these
+// products.  The row scale s is applied in fp32 to the finished sums.  fp32
+// operands keep e in fp32 and g as three bfloat16 parts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

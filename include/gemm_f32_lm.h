@@ -14,7 +14,8 @@
  * (GEMM_F32_TYPE_BF16) elements, with a row stride in elements of at least
  * the row's length.  Pointers are aligned to their element.  Row statistics,
  * losses and every sum are fp32; an output in bfloat16 is rounded once, from
- * its fp32 value.
+ * its fp32 value.  Two matrices overlap when the address ranges from their
+ * first to their last element do, so two column slices of one matrix overlap.
  *
  * Scratch: the library owns one scratch buffer per (device, stream), grown
  * with cudaMalloc (which synchronises the device) by the first call that
@@ -119,9 +120,13 @@ int gemm_f32_vocab_loss(int type, long long rows, int width, int vocab, const vo
  * Neither may overlap an input.  The logits are computed once, for a piece of
  * the rows at a time: of a piece the library keeps exp(z - maximum of its
  * tile) in scratch, in 16 bits for bfloat16 operands, and turns it into
- * g / s in place.  `piece_bytes` bounds that part of the scratch (0: 4 GiB);
+ * g / s in place, rounded to bfloat16 (three parts of it for fp32 operands).
+ * `piece_bytes` bounds that part of the scratch (0: 4 GiB);
  * pieces are at least 256 rows.  With more than one piece and bfloat16
- * operands, dw is summed in fp32 scratch. */
+ * operands, dw is summed in fp32 scratch.  Besides the piece the scratch holds
+ * what TMA cannot read where it lies: the three parts of fp32 operands (6 bytes
+ * an element of x, and of w with more than 128 rows), copies of matrices whose
+ * rows are not on 16-byte boundaries; and partial tiles of the products. */
 int gemm_f32_vocab_loss_grad(int type, long long rows, int width, int vocab, const void* x,
                              long long ldx, const void* w, long long ldw, const void* targets,
                              int target_bits, long long ignore_index, int reduction,
