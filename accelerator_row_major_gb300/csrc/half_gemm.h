@@ -63,11 +63,16 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
 // included (f32: its three parts are made on the way to the tensor cores).
 // For dx its rows start on 16-byte boundaries; for the logits they may not:
 // the rows then fall into classes, and b holds a copy of x for each.
-constexpr int kFewRows = 128;     // fp32: the pair kernel would first store w in three parts
-                                  // (64 x 4096 x 65536 920 us against 250)
-constexpr int kFewRowsBf16 = 32;  // 4096 x 65536: 105 us against the pair kernel's 175 with one
-                                  // row, 111 each with 32, 116 against 111 with 64, 137 against
-                                  // 113 with 128
+constexpr int kFewRows = 128;     // fp32: the pair kernel would first store w in three parts (64 x 4096
+                                  // x 65536 938 us against 249; 128 rows, width x vocabulary: 4096 x
+                                  // 65536 942 against 388, 1024 x 32768 131 against 87, 512 x 131072
+                                  // 242 against 195, 8192 x 32000 927 against 361)
+constexpr int kFewRowsBf16 = 32;  // 4096 x 65536: 103 us against the pair kernel's 158 with one row, 112
+                                  // against 110 with 32 (gradients 311 against 322), 117 against 111
+                                  // with 64, 138 against 111 with 128; 8192 x 32000 with 32 rows 105
+                                  // against 109.  With narrow rows the pair kernel is the better one
+                                  // from fewer on: 1024 x 32768 23 against 29 with one, 29 against its 25
+                                  // with 32; 512 x 131072 45 against 46 with one, 54 against 43 with 16
 constexpr int kFewPiece = 32;     // columns per statistic of its logits
 
 // Rows of w as TMA reads them: every `count`-th row has the same distance
