@@ -693,26 +693,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// dx[t][d] = scale * the tile's partials added in order; one thread per
-// element, 128 columns of 2 rows per CTA.
+// dx[t][d] = scale * the tile's partials added in order (of row t, or of rows
+// t and rows + t, the two parts'); one thread per element, 128 columns of 2
+// rows per CTA.
 template <class T>
 __global__ void __launch_bounds__(256)
-    few_reduce_kernel(const FewParams p, int ctas, T* dx, long long lddx, const float* scale) {
+    few_reduce_kernel(const FewParams p, int ctas, int rows, T* dx, long long lddx, const float* scale) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int tile = blockIdx.x, t = blockIdx.y * 2 + threadIdx.x / kTile, l = threadIdx.x % kTile;
   const int d = tile * kTile + l;
-  if (t >= p.rows || d >= p.width) return;
+  if (t >= rows || d >= p.width) return;
   const long long ki = p.k_blocks;
   const int nseg = sk_owner((tile + 1) * ki - 1, ctas, p.sk_work) - sk_owner(tile * ki, ctas, p.sk_work) + 1;
   const size_t step = static_cast<size_t>(p.rows) * kTile;
   const float* src = p.partials + tile * p.max_seg * step + static_cast<size_t>(t) * kTile + l;
-  float v = 0.0f;
+  const size_t second = static_cast<size_t>(p.rows - rows) * kTile;   // 0: one part
+  float v = 0.0f, low = 0.0f;
   for (int s = 0; s < nseg; ++s)
-    if (GEMM_IN_EXTENT(src + s * step - p.partials, partials_extent(p), p.err, kSiteBoundsWork))
+    if (GEMM_IN_EXTENT(src + s * step + second - p.partials, partials_extent(p), p.err, kSiteBoundsWork)) {
       v += __ldcg(src + s * step);
+      if (second) low += __ldcg(src + s * step + second);
+    }
+  v += low;
   const size_t at = static_cast<size_t>(t) * lddx + d;
-  if (GEMM_IN_EXTENT(at, stored_extent(p.rows, p.width, lddx), p.err, kSiteBoundsRows))
+  if (GEMM_IN_EXTENT(at, stored_extent(rows, p.width, lddx), p.err, kSiteBoundsRows))
     dx[at] = from_f32<T>(v * __ldg(scale));
 }
 
@@ -871,11 +876,12 @@ int launch_few_gemm(const FewGemm& g, cudaStream_t stream, int* launches) {
   if (rc != GEMM_F32_OK) return rc;
   ++*launches;
   if (dx) {
-    const dim3 blocks(p.tiles, (g.rows + 1) / 2);
+    const int rows = g.two ? g.rows / 2 : g.rows;
+    const dim3 blocks(p.tiles, (rows + 1) / 2);
     const cudaError_t err =
-        g.f32 ? launch_dependent(few_reduce_kernel<float>, blocks, dim3(256), 0, stream, p, grid,
+        g.f32 ? launch_dependent(few_reduce_kernel<float>, blocks, dim3(256), 0, stream, p, grid, rows,
                                  static_cast<float*>(g.dx), g.lddx, g.scale)
-              : launch_dependent(few_reduce_kernel<__nv_bfloat16>, blocks, dim3(256), 0, stream, p, grid,
+              : launch_dependent(few_reduce_kernel<__nv_bfloat16>, blocks, dim3(256), 0, stream, p, grid, rows,
                                  static_cast<__nv_bfloat16*>(g.dx), g.lddx, g.scale);
     if (err != cudaSuccess) {
       (void)cudaGetLastError();

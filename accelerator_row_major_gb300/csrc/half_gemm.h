@@ -107,8 +107,10 @@ struct FewGemm {
   LossTargets targets = {};
   float* label_logit = nullptr;
   unsigned* arrived = nullptr;
-  // -- or dx = *scale * b w (dx != nullptr)
+  // -- or dx = *scale * b w (dx != nullptr); `two`: b's rows are two parts,
+  // one below the other, of half as many rows of dx
   void* dx = nullptr;
+  bool two = false;
   long long lddx = 0;
   const float* scale = nullptr;
   float* partials = nullptr;      // few_gemm_scratch() bytes

@@ -20,11 +20,14 @@
 // products: one rounding of g, by up to 2^-8 of it (at a target of small
 // probability p that is the p of g = p - 1 up to 2^-9).  It is of the size of
 // the rounding of the results, and adds to it where few terms make an element:
-// errors against 64 bits, over those of products with g in fp32, measured 1.42
-// for dw of one row x 4096 x 65536, 1.07 for 8 x 512 x 4096, 1.02 from 32 rows
-// on, 1.00 for 1001 x 777 x 32001.  Holding g in two parts would double these
-// products.  The row scale s is applied in fp32 to the finished sums.  fp32
-// operands keep e in fp32 and g as three bfloat16 parts.
+// with one part, errors against 64 bits over those of products with g in fp32
+// measured 1.42 for dw of one row x 4096 x 65536, 1.07 for 8 x 512 x 4096, 1.02
+// from 32 rows on, 1.00 for 1001 x 777 x 32001.  So few rows (few_gemm.cu) hold
+// g in two parts, the second what the rounding left, one below the other as
+// twice as many rows of g (and of x, for dw): dx is the sum of a pair of rows.
+// With more rows that would double two of the three products.  The row scale s
+// is applied in fp32 to the finished sums.  fp32 operands keep e in fp32 and g
+// as three bfloat16 parts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -235,7 +238,7 @@ template <int PARTS>
 __global__ void __launch_bounds__(kRescaleThreads)
     loss_rescale_kernel(const float2* stats, long long ld_stats, int piece_bits, const float2* joined,
                         int rows, int cols, unsigned band, LossTargets targets, void* exps, long long ld,
-                        bf16* parts, long long plane, unsigned* err) {
+                        bf16* parts, long long plane, bool two, unsigned* err) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int row0 = blockIdx.x * kRescaleRows;
@@ -287,6 +290,11 @@ __global__ void __launch_bounds__(kRescaleThreads)
         }
       } else {
         store_vec<bf16, 8>(static_cast<bf16*>(exps) + at, g);
+        if (two) {   // the second part, `rows` rows on
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] -= __bfloat162float(__float2bfloat16_rn(g[j]));
+          store_vec<bf16, 8>(static_cast<bf16*>(exps) + static_cast<size_t>(rows) * ld + at, g);
+        }
       }
     }
   }
@@ -299,7 +307,8 @@ __global__ void __launch_bounds__(kRescaleThreads)
 // rest is below 2^-25 of the value.
 // One launch takes x and w where both need it.  `copies` of x serve a w whose
 // rows are not on 16-byte boundaries (few_gemm.cu): copy c, its parts c PARTS
-// planes on, lies shift(c) columns to the right, with zeros on both sides.
+// planes on, lies shift(c) columns to the right, with zeros on both sides; or
+// the two parts of g.
 struct Packing {
   const void* src;
   void* dst;
@@ -475,7 +484,9 @@ int run(const Call& c, cudaStream_t stream, int* launches, const char** kernel) 
   const int parts = f32 ? 3 : 1;
   const long long ld_exps = static_cast<long long>(round_up(c.vocab, 256));
   const int piece_bits = few ? kFewPieceBits : kPieceBits;
-  const FewClasses* const classes = direct ? &by_class : nullptr;
+  const bool two = grad && few && !f32;                // parts of g, one below the other
+  const FewClasses twice = {2, 0, 0, 0, 0};            // so x for dw: two copies, not shifted
+  const FewClasses* const classes = direct ? &by_class : two && c.dw ? &twice : nullptr;
   const int pieces = direct ? by_class.count * by_class.units
                      : few  ? (c.vocab + kFewPiece - 1) / kFewPiece
                             : static_cast<int>(ld_exps >> kPieceBits);
@@ -507,15 +518,15 @@ int run(const Call& c, cudaStream_t stream, int* launches, const char** kernel) 
   if (!direct) ow = plan_operand(c.w, c.ldw, c.vocab, c.width, f32, f32 && !few, nullptr, layout);
   size_t at_exps = 0, at_g = 0, at_partials = 0, at_sum = 0;
   if (grad) {
-    at_exps = layout.take(static_cast<size_t>(step) * ld_exps * (f32 ? 4 : 2));
+    at_exps = layout.take(static_cast<size_t>(step) * ld_exps * (f32 ? 4 : 2) * (two ? 2 : 1));
     at_g = f32 ? layout.take(static_cast<size_t>(step) * ld_exps * 6) : at_exps;
     size_t partial = 0;
     for (long long r = 0; r < c.rows; r += step) {
       const int n = static_cast<int>(std::min<long long>(step, c.rows - r));
       if (c.dx)
-        partial = std::max(partial, few ? few_gemm_scratch(n, c.width, c.vocab, num_sms)
+        partial = std::max(partial, few ? few_gemm_scratch(two ? 2 * n : n, c.width, c.vocab, num_sms)
                                         : half_gemm_scratch(n, c.width, c.vocab, parts, num_sms));
-      if (c.dw) partial = std::max(partial, half_gemm_scratch(c.vocab, c.width, n, parts, num_sms));
+      if (c.dw) partial = std::max(partial, half_gemm_scratch(c.vocab, c.width, two ? 2 * n : n, parts, num_sms));
     }
     at_partials = layout.take(partial);
     if (sum_dw) at_sum = layout.take(sizeof(float) * static_cast<size_t>(c.vocab) * c.width);
@@ -634,13 +645,15 @@ int run(const Call& c, cudaStream_t stream, int* launches, const char** kernel) 
     rc = launch(f32 ? loss_rescale_kernel<3> : loss_rescale_kernel<1>, grid, kRescaleThreads, stream,
                 launches, static_cast<const float2*>(stats), ld_stats, piece_bits,
                 static_cast<const float2*>(joined), n, cols, band, targets,
-                static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, err);
+                static_cast<void*>(scratch + at_exps), ld_exps, gp, plane, two, err);
     if (rc != GEMM_F32_OK) break;
 
     base.scale = &factors->grad;
     base.partials = reinterpret_cast<float*>(scratch + at_partials);
     if (c.dx && few) {
       FewGemm d = few_base;
+      d.rows = two ? 2 * n : n;
+      d.two = two;
       d.b = {gp, ld_exps, plane, false};
       d.dx = c.dx;
       d.lddx = c.lddx;
@@ -665,7 +678,7 @@ int run(const Call& c, cudaStream_t stream, int* launches, const char** kernel) 
       HalfGemm d = base;
       d.M = c.vocab;
       d.N = c.width;
-      d.K = n;
+      d.K = two ? 2 * n : n;
       d.a = {gp, ld_exps, plane, true};
       d.b = {x.ptr, x.ld, x.plane, true};
       const bool last = r + step >= c.rows;

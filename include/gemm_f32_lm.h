@@ -120,7 +120,8 @@ int gemm_f32_vocab_loss(int type, long long rows, int width, int vocab, const vo
  * Neither may overlap an input.  The logits are computed once, for a piece of
  * the rows at a time: of a piece the library keeps exp(z - maximum of its
  * tile) in scratch, in 16 bits for bfloat16 operands, and turns it into
- * g / s in place, rounded to bfloat16 (three parts of it for fp32 operands).
+ * g / s in place, rounded to bfloat16 (two parts of it with at most 32 rows,
+ * three for fp32 operands).
  * `piece_bytes` bounds that part of the scratch (0: 4 GiB);
  * pieces are at least 256 rows.  With more than one piece and bfloat16
  * operands, dw is summed in fp32 scratch.  Besides the piece the scratch holds
