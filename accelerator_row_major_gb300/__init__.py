@@ -15,6 +15,14 @@ over a vocabulary, and their gradients; fp32 or bfloat16 rows):
     y, mean, rstd = g.layer_norm(x, weight, bias)
     total, loss, lse, dy, dw = g.vocab_loss_grad(y, w, targets)
     dx, dweight, dbias = g.layer_norm_grad(dy, x, weight, mean, rstd)
+
+What stands between a model's blocks: norms fused with the residual and its
+gate, activations kept in 8 bits, and the gradients computed from them:
+
+    y, h, stats = g.block_norm(branch, residual, weight, bias)
+    saved_y, saved_h = g.checkpoint(y), g.checkpoint(h)
+    dw = g.weight_grad(dz, saved_y)        # of z = y @ w.T
+    grads = g.block_norm_grad(dy, dh, saved_h, None, stats, weight)
 """
 from ._binding import (FLAG_CTA_PAIR, FLAG_FORCE_STAGED, FLAG_SINGLE_CTA, FLAG_TILE64, FLAG_TILE128, FLAG_TILE256,  # noqa: F401
                        FLAG_NO_SPLIT_K, FLAG_ONE_TILE_PER_CTA, FLAG_TEST_DROP_COPY, GEMM_F32_EDEVICE, GEMM_F32_EINVAL,
@@ -28,13 +36,18 @@ from ._binding import (FLAG_CTA_PAIR, FLAG_FORCE_STAGED, FLAG_SINGLE_CTA, FLAG_T
                        gemm_f32_version)
 
 _LM = ("layer_norm", "layer_norm_grad", "vocab_loss", "vocab_loss_grad")
+_BLOCK = ("block_norm", "block_norm_grad", "BlockNormGrads", "checkpoint", "restore", "Checkpoint", "weight_grad")
 
 
 def __getattr__(name):
-    """The operators of _lm, imported on first use (they need torch; the C-ABI calls do not)."""
+    """The operators of _lm and _block, imported on first use (they need torch; the C-ABI calls do not)."""
     if name in _LM:
         from . import _lm
         globals().update({n: getattr(_lm, n) for n in _LM})
+        return globals()[name]
+    if name in _BLOCK:
+        from . import _block
+        globals().update({n: getattr(_block, n) for n in _BLOCK})
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 

@@ -16,6 +16,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("GEMM_F32_LIBRARY") or os.path.join(_PKG, "libgemm_f32.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "gemm_f32.h")
 LM_HEADER = os.path.join(os.path.dirname(_PKG), "include", "gemm_f32_lm.h")
+BLOCK_HEADER = os.path.join(os.path.dirname(_PKG), "include", "gemm_f32_block.h")
 
 GEMM_F32_OK = 0
 GEMM_F32_EINVAL = -1
@@ -36,6 +37,7 @@ TYPE_BF16 = 1
 SUM = 0
 MEAN = 1
 REDUCTIONS = {"sum": SUM, "mean": MEAN}
+NORMS = {"layer": 0, "rms": 1}
 
 FLAG_FORCE_STAGED = 0x1
 FLAG_TILE64 = 0x10
@@ -71,6 +73,21 @@ class UnitRates(ctypes.Structure):
                 ("ffma_flop_per_clk_sm", ctypes.c_double),
                 ("sm_mhz", ctypes.c_double),
                 ("num_sms", ctypes.c_int)]
+
+
+class Block(ctypes.Structure):
+    """gemm_f32_block_t of include/gemm_f32_block.h."""
+    _fields_ = [("type", ctypes.c_int), ("weight_type", ctypes.c_int), ("norm", ctypes.c_int), ("post", ctypes.c_int),
+                ("rows", ctypes.c_longlong), ("width", ctypes.c_int), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_longlong)]
+
+
+class Rows(ctypes.Structure):
+    """gemm_f32_rows_t of include/gemm_f32_block.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_longlong), ("codes", ctypes.c_void_p),
+                ("ld_codes", ctypes.c_longlong), ("exponents", ctypes.c_void_p), ("ld_exponents", ctypes.c_longlong)]
 
 
 def _load() -> ctypes.CDLL:
@@ -113,6 +130,17 @@ def _load() -> ctypes.CDLL:
     lib.gemm_f32_vocab_loss_grad.argtypes = [ci, cl, ci, ci, vp, cl, vp, cl, vp, ci, cl, ci, cf, vp, vp, vp,
                                              vp, cl, vp, cl, ctypes.c_size_t, vp]
     lib.gemm_f32_vocab_loss_grad.restype = ci
+    pb, pr = ctypes.POINTER(Block), ctypes.POINTER(Rows)
+    lib.gemm_f32_block_norm.argtypes = [pb, vp, cl, vp, cl, vp, cl, vp, cl, vp, vp]
+    lib.gemm_f32_block_norm.restype = ci
+    lib.gemm_f32_block_norm_grad.argtypes = [pb, vp, cl, vp, cl, pr, pr, vp, vp, cl, vp, cl, vp, cl, vp, vp, vp, vp, vp]
+    lib.gemm_f32_block_norm_grad.restype = ci
+    lib.gemm_f32_checkpoint.argtypes = [ci, cl, ci, vp, cl, vp, cl, vp, cl, vp]
+    lib.gemm_f32_checkpoint.restype = ci
+    lib.gemm_f32_restore.argtypes = [ci, cl, ci, vp, cl, vp, cl, vp, cl, vp]
+    lib.gemm_f32_restore.restype = ci
+    lib.gemm_f32_weight_grad.argtypes = [ci, cl, ci, ci, vp, cl, vp, cl, vp, cl, ci, vp, cl, ci, vp]
+    lib.gemm_f32_weight_grad.restype = ci
     u64p = ctypes.POINTER(ctypes.c_ulonglong)
     lib.gemm_f32_clock_record.argtypes = [vp, u64p, u64p]
     lib.gemm_f32_clock_record.restype = ci

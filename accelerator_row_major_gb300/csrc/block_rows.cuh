@@ -1,0 +1,397 @@
+// Rows of several matrices at once, for the norms at a block's ends: a ring
+// of rows in shared memory that bulk copies fill, a thread's part of a row,
+// and sums over the threads that share one.
+//
+// A group of `lanes` threads (whole warps, as many as a row's columns need at
+// NE elements a thread) works on one row at a time; a CTA has several groups
+// where rows are narrow, and a cluster of CTAs shares a row, each a slice of
+// its columns, where they are wide.  Lanes, groups, ring depth and cluster are
+// the launch's: a width costs the next whole warp, not the next power of 2.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "device_common.cuh"
+#include "pair_common.cuh"
+#include "row_common.cuh"
+#include "saved_rows.cuh"
+
+namespace gemm_f32_impl {
+using namespace gemm_f32_dev;
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kRowThreads = 512;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kMostCtas = 8;             // of a cluster
+constexpr int kSliceUnit = 512;          // columns: their exponents fill 16 bytes
+
+// One matrix that a row is read from.  size: bytes per element, or 0 for the
+// exponents of 8-bit rows (a byte per 32 columns).
+struct RowSource {
+  const char* p;                         // null: not there
+  const char* end;                       // one past the last byte that may be read
+  long long ld;                          // bytes from row to row
+  int size;
+  uint32_t at;                           // of its row within a stage
+};
+
+// How a launch lays out its rows.
+struct RowPlan {
+  int width, slice;                      // columns of a row, of a CTA's part
+  int lanes, groups, stages, ctas;
+  uint32_t stage_bytes;
+  uint32_t ring_at;                      // in dynamic shared memory, behind the weights
+  long long rows;
+};
+
+__host__ __device__ __forceinline__ uint32_t source_bytes(int size, int cols) {
+  return size ? static_cast<uint32_t>(size) * cols : static_cast<uint32_t>(cols + kSavedBlock - 1) / kSavedBlock;
+}
+
+// ---------------------------------------------------------------- ring
+// Of one group: N rows per stage, for the group's rows first, first + step,
+// ..., `stages` ahead.  A row is copied from the 16-byte boundary below its
+// start to the one above its end, but never beyond its matrix: elements
+// outside the matrix's whole blocks (near its two ends only) are copied by
+// the thread that issues the copies.
+template <int N>
+struct RowsRing {
+  const RowSource* in;                   // [N]
+  const RowPlan& plan;
+  unsigned* err;
+  uint8_t* data;
+  uint32_t bars;
+  int col0, width;                       // of this CTA's slice (no columns: width 0)
+  int s = 0;
+  uint32_t ph = 0;
+  bool lost = false;
+  long long next, step;
+  long long issued = 0, taken = 0, lost_at = 0;
+
+  __device__ __forceinline__ RowsRing(const RowSource* sources, const RowPlan& p, unsigned* e, uint8_t* smem,
+                                      int group, int rank)
+      : in(sources), plan(p), err(e) {
+    data = smem + p.ring_at + static_cast<size_t>(group) * p.stages * p.stage_bytes;
+    bars = smem_addr(smem + p.ring_at) + static_cast<uint32_t>(p.groups * p.stages) * p.stage_bytes +
+           static_cast<uint32_t>(group * p.stages) * 8u;
+    const int unit = static_cast<int>(blockIdx.x) / p.ctas, units = static_cast<int>(gridDim.x) / p.ctas;
+    next = static_cast<long long>(unit) * p.groups + group;
+    step = static_cast<long long>(units) * p.groups;
+    col0 = rank * p.slice;
+    width = max(0, min(p.slice, p.width - col0));
+  }
+  // One thread of the group, before the group's first barrier.
+  __device__ __forceinline__ void init() {
+    for (int i = 0; i < plan.stages; ++i) mbar_init(bars + 8u * i, 1);
+    fence_mbar_init();
+  }
+  __device__ __forceinline__ uintptr_t first_byte(const RowSource& m, long long row) const {
+    return reinterpret_cast<uintptr_t>(m.p) + row * m.ld + (m.size ? col0 * m.size : col0 / kSavedBlock);
+  }
+  // Bytes by which a row starts above a 16-byte boundary.
+  __device__ __forceinline__ uint32_t shift(int i, long long row) const {
+    return static_cast<uint32_t>(first_byte(in[i], row)) & 15u;
+  }
+  // The whole 16-byte blocks [lo, hi) of the matrix around a row's bytes.
+  __device__ __forceinline__ void blocks(const RowSource& m, uintptr_t first, uintptr_t last, uintptr_t& lo,
+                                         uintptr_t& hi) const {
+    lo = first & ~uintptr_t{15};
+    hi = (last + 15) & ~uintptr_t{15};
+    if (lo < reinterpret_cast<uintptr_t>(m.p)) lo += 16;
+    if (hi > reinterpret_cast<uintptr_t>(m.end)) hi -= 16;
+    if (lo >= hi) lo = hi = first;
+  }
+  static __device__ __forceinline__ void copy_elements(uint8_t* dst, uintptr_t from, uintptr_t to, int size) {
+    for (uintptr_t q = from; q < to; q += size, dst += size) {
+      if (size == 4)
+        *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(q);
+      else
+        *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(q);
+    }
+  }
+  // One thread: the copies of row `next` into stage `stage`.
+  __device__ __forceinline__ void load(int stage) {
+    if (next < plan.rows) {
+      const uint32_t bar = bars + 8u * stage;
+      uint8_t* const dst = data + static_cast<size_t>(stage) * plan.stage_bytes;
+      uint32_t bytes = 0;
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const RowSource& m = in[i];
+        if (!m.p) continue;
+        const uintptr_t first = first_byte(m, next), last = first + source_bytes(m.size, width);
+        uintptr_t lo, hi;
+        blocks(m, first, last, lo, hi);
+        bytes += static_cast<uint32_t>(hi - lo);
+        if (lo > first || hi < last || lo == hi) {
+          uint8_t* const at = dst + m.at + (first & 15);
+          if (lo == hi) {
+            copy_elements(at, first, last, m.size);
+          } else {
+            copy_elements(at, first, lo, m.size);          // nothing where lo is below first
+            copy_elements(at + (hi - first), hi, last, m.size);
+          }
+        }
+      }
+      mbar_arrive_expect_tx(bar, bytes);                   // releases the elements copied here, too
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const RowSource& m = in[i];
+        if (!m.p) continue;
+        const uintptr_t first = first_byte(m, next), last = first + source_bytes(m.size, width);
+        uintptr_t lo, hi;
+        blocks(m, first, last, lo, hi);
+        if (lo < hi)
+          bulk_load(smem_addr(dst) + m.at + static_cast<uint32_t>(lo - (first & ~uintptr_t{15})),
+                    reinterpret_cast<const void*>(lo), static_cast<uint32_t>(hi - lo), bar);
+      }
+      ++issued;
+    }
+    next += step;
+  }
+  // A wait that runs out is recorded, and the thread goes on (the result is
+  // undefined, as the status says): the group's barriers need all of it.  The
+  // one that issues the copies issues no more.
+  __device__ __forceinline__ void wait() {
+    if (!lost && !mbar_wait(bars + 8u * s, ph, err, kSiteTransformFull)) {
+      lost = true;
+      lost_at = taken;
+    }
+  }
+  // The stage has been read: by one thread, after a barrier of the group.
+  __device__ __forceinline__ void refill() {
+    if (!lost) load(s);
+  }
+  __device__ __forceinline__ void advance() {
+    ++taken;
+    if (++s == plan.stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+  // The issuing thread, at its end: where it gave up, it waits, again with a
+  // limit, for its copies in flight, which would land in memory that is no
+  // longer the kernel's.
+  __device__ __forceinline__ void finish() const {
+    if (!lost) return;
+    for (long long k = lost_at; k < issued; ++k)
+      mbar_wait(bars + 8u * static_cast<uint32_t>(k % plan.stages),
+                static_cast<uint32_t>(k / plan.stages) & 1u, err, kSiteDrainTma);
+  }
+  // A matrix's row in the current stage, from its 16-byte boundary on.
+  __device__ __forceinline__ const uint8_t* at(int i) const {
+    return data + static_cast<size_t>(s) * plan.stage_bytes + in[i].at;
+  }
+};
+
+// ---------------------------------------------------------------- a thread's part of a row
+// NE elements of type T.  VEC: 16-byte vectors, vector v of thread t from
+// column (v lanes + t) V on, which takes rows on 16-byte boundaries of whole
+// vectors.  Else single elements, element i of thread t in column i lanes + t:
+// 2 or 4 bytes apart from lane to lane, so that rows may start anywhere.
+template <class T, int NE, bool VEC>
+struct RowPart {
+  static constexpr int V = 16 / static_cast<int>(sizeof(T));
+  static constexpr int NP = NE / 2;      // pairs
+  int t, lanes, width;
+  bool full;                             // every thread's elements are all columns of the slice
+
+  __device__ __forceinline__ RowPart(int thread, int n, int w) : t(thread), lanes(n), width(w), full(n * NE == w) {}
+
+  static __device__ __forceinline__ int column(int t, int i, int lanes) {
+    return VEC ? ((i / V) * lanes + t) * V + i % V : i * lanes + t;
+  }
+  __device__ __forceinline__ int col(int i) const { return column(t, i, lanes); }
+  __device__ __forceinline__ bool in(int i) const { return col(i) < width; }
+
+  // The row's elements, 0 for what lies outside it.
+  __device__ __forceinline__ void load(const uint8_t* row, uint32_t shift, Pair (&x)[NP]) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NE / V; ++v) {
+        Pair p[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) p[j] = 0;
+        if (in(v * V)) pairs_of<T>(*reinterpret_cast<const uint4*>(row + col(v * V) * sizeof(T)), p);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) x[v * (V / 2) + j] = p[j];
+      }
+    } else {
+      const T* const p = reinterpret_cast<const T*>(row + shift);
+      float f[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) f[i] = in(i) ? to_f32(p[col(i)]) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) x[j] = pair_of(f[2 * j], f[2 * j + 1]);
+    }
+  }
+  // The same of a row kept in 8 bits.
+  __device__ __forceinline__ void load_saved(const uint8_t* codes, const uint8_t* exponents, Pair (&x)[NP]) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NE / V; ++v) {
+        uint32_t w[V / 4];
+        float by = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) w[j] = 0u;
+        if (in(v * V)) {
+          const int c = col(v * V);
+#pragma unroll
+          for (int j = 0; j < V / 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(codes + c + 4 * j);
+          by = power_of(exponents[c / kSavedBlock]);
+        }
+        const Pair power = pair_of(by, by);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 f = values_of((w[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+          x[v * (V / 2) + j] = mul2(pair_of(f.x, f.y), power);
+        }
+      }
+    } else {
+      float f[NE];
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        f[i] = in(i) ? values_of(codes[col(i)]).x * power_of(exponents[col(i) / kSavedBlock]) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) x[j] = pair_of(f[2 * j], f[2 * j + 1]);
+    }
+  }
+  // 0 for what lies outside the row.
+  __device__ __forceinline__ void drop(Pair (&x)[NP]) const {
+    if (full) return;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        if (!in(2 * j / V * V)) x[j] = 0;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        float a, b;
+        unpair(x[j], a, b);
+        x[j] = pair_of(in(2 * j) ? a : 0.0f, in(2 * j + 1) ? b : 0.0f);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* row, const Pair (&x)[NP]) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NE / V; ++v) {
+        Pair p[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) p[j] = x[v * (V / 2) + j];
+        if (in(v * V)) store_pairs(row + col(v * V), p);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        float a, b;
+        unpair(x[j], a, b);
+        if (in(2 * j)) row[col(2 * j)] = from_f32<T>(a);
+        if (in(2 * j + 1)) row[col(2 * j + 1)] = from_f32<T>(b);
+      }
+    }
+  }
+
+  // Values per column in shared memory, laid out as the threads hold them:
+  // elements 4q .. 4q + 3 of thread t at 4 (q lanes + t), 16 bytes from lane
+  // to lane.
+  static __device__ __forceinline__ int slots(int lanes) { return NE * lanes; }
+  static __device__ __forceinline__ int column_of_slot(int slot, int lanes) {
+    const int quad = slot / 4;
+    return column(quad % lanes, quad / lanes * 4 + slot % 4, lanes);
+  }
+  __device__ __forceinline__ float* quad(float* values, int q) const { return values + 4 * (q * lanes + t); }
+  __device__ __forceinline__ void load_columns(const float* values, Pair (&w)[NP]) const {
+#pragma unroll
+    for (int q = 0; q < NE / 4; ++q) {
+      const float4 f = *reinterpret_cast<const float4*>(values + 4 * (q * lanes + t));
+      w[2 * q] = pair_of(f.x, f.y);
+      w[2 * q + 1] = pair_of(f.z, f.w);
+    }
+  }
+};
+
+// A vector of `width` values (fp32, or T where `f32` is not set; null: `none`)
+// from column col0 on, into slots.  All threads of the CTA.
+template <class T, class Part>
+__device__ __forceinline__ void fill_columns(float* values, const void* p, bool f32, float none, int lanes, int col0,
+                                             int width) {
+  for (int slot = threadIdx.x; slot < Part::slots(lanes); slot += blockDim.x) {
+    const int c = Part::column_of_slot(slot, lanes);
+    float v = 0.0f;
+    if (c < width)
+      v = !p    ? none
+          : f32 ? __ldg(static_cast<const float*>(p) + col0 + c)
+                : to_f32(static_cast<const T*>(p)[col0 + c]);
+    values[slot] = v;
+  }
+}
+
+// ---------------------------------------------------------------- sums over a row
+// Sums of one or two values over the threads of a group and, with a cluster,
+// over its CTAs (which have one group each); every thread gets them.  Two sets
+// of buffers take turns: one is written again only after a barrier that every
+// reader has passed.  CTAs exchange theirs by asynchronous stores that a
+// barrier at the destination counts, and add them in order.
+struct RowSums {
+  float (*part)[2][kRowWarps];           // [2]: of the warps
+  float2 (*shared)[kMostCtas];           // [2]: of the CTAs
+  uint32_t bars;                         // 2
+  unsigned* err;
+  int group, lanes, ctas, rank;
+  uint32_t flip = 0, round = 0;
+  bool lost = false;
+
+  __device__ __forceinline__ void barrier() const {
+    if (lanes > 32)
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(lanes) : "memory");
+    else
+      __syncwarp();
+  }
+
+  template <int N>
+  __device__ __forceinline__ void add(float (&v)[N]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = lanes >> 5;
+    warp_sum<N>(v);
+    if (warps > 1) {
+      if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[flip][i][warp] = v[i];
+      barrier();
+      const int j = lane & 15;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = j < warps ? part[flip][i][group * warps + j] : 0.0f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+    } else {
+      barrier();
+    }
+    if (ctas > 1) {
+      const int t = threadIdx.x;
+      if (t == 0) mbar_arrive_expect_tx(bars + 8u * flip, ctas * 8u);
+      if (t < ctas)
+        store_async(map_rank(smem_addr(&shared[flip][rank]), static_cast<uint32_t>(t)), v[0], N > 1 ? v[N - 1] : 0.0f,
+                    map_rank(bars + 8u * flip, static_cast<uint32_t>(t)));
+      if (!lost) lost = !mbar_wait_cluster(bars + 8u * flip, round, err, kSiteTransformFull);
+      round ^= flip;                     // both have been waited for
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.0f;
+      for (int r = 0; r < ctas; ++r) {
+        v[0] += shared[flip][r].x;
+        if (N > 1) v[N - 1] += shared[flip][r].y;
+      }
+    }
+    flip ^= 1u;
+  }
+};
+
+}  // namespace
+}  // namespace gemm_f32_impl

@@ -1,0 +1,442 @@
+// Activations kept in 8 bits (saved_rows.cuh), brought back, and the weight
+// gradient of a product whose input was kept (sm_103a).
+//
+// Both conversions are bound by memory traffic: 3 bytes an element in bfloat16,
+// 5 in fp32, and a byte per 32 elements.  A warp takes 256 columns of a row at
+// a time, four such pieces in flight: of rows on 16-byte boundaries each lane
+// 8 columns (a block is four lanes), of others each lane one column of every
+// 32 (a block is a warp), so that loads and stores of single elements lie side
+// by side.
+//
+// The weight gradient dw = dy^T x is a product on the tensor cores
+// (half_gemm.cu) that reads both operands as they are stored.  e4m3 codes
+// times powers of two are bfloat16 numbers, so x is brought back into scratch
+// without a rounding; an fp32 dy goes in three parts, against an x that is
+// one: three products where fp32 operands take six.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "../../include/gemm_f32_block.h"
+#include "device_common.cuh"
+#include "half_gemm.h"
+#include "launch.h"
+#include "row_common.cuh"
+#include "saved_rows.cuh"
+#include "workspace.h"
+
+namespace gemm_f32_impl {
+using namespace gemm_f32_dev;
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kConvertThreads = 256;
+constexpr int kPiece = 256;              // columns of a warp's piece
+constexpr int kFlight = 4;               // pieces in flight per warp
+
+struct ConvertArgs {
+  long long rows;
+  int width;                             // columns of x; restoring: columns to write
+  const void* x;                         // keeping: read; restoring: null
+  void* out;                             // restoring: written
+  long long ld;                          // of x or out, elements
+  uint8_t* codes;
+  long long ld_codes;
+  uint8_t* exponents;
+  long long ld_exponents;
+  int pieces;                            // per row
+  unsigned* err;
+};
+
+// The pieces of one warp: every `warps`-th of rows x pieces, without a
+// division per piece.
+struct Pieces {
+  long long row;
+  int piece, per_row, d_piece;
+  long long d_row;
+
+  __device__ __forceinline__ Pieces(int per) : per_row(per) {
+    constexpr int kWarps = kConvertThreads / 32;
+    const long long first = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5);
+    const long long warps = gridDim.x * static_cast<long long>(kWarps);
+    row = first / per;
+    piece = static_cast<int>(first - row * per);
+    d_row = warps / per;
+    d_piece = static_cast<int>(warps - d_row * per);
+  }
+  __device__ __forceinline__ void next() {
+    row += d_row;
+    piece += d_piece;
+    if (piece >= per_row) {
+      piece -= per_row;
+      ++row;
+    }
+  }
+};
+
+template <class T>
+__device__ __forceinline__ bool x_ok(const ConvertArgs& a, long long row, int last) {
+  return GEMM_IN_EXTENT(row * a.ld + last, stored_extent(a.rows, a.width, a.ld), a.err, kSiteBoundsRows);
+}
+__device__ __forceinline__ bool codes_ok(const ConvertArgs& a, long long row, int last) {
+  return GEMM_IN_EXTENT(row * a.ld_codes + last, a.rows * a.ld_codes, a.err, kSiteBoundsRows) &&
+         GEMM_IN_EXTENT(row * a.ld_exponents + last / kSavedBlock, a.rows * a.ld_exponents, a.err, kSiteBoundsRows);
+}
+
+// ---------------------------------------------------------------- keeping
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kConvertThreads) checkpoint_kernel(const ConvertArgs a) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  Pieces at(a.pieces);
+  while (at.row < a.rows) {
+    // all pieces' loads first
+    long long row[kFlight];
+    int col0[kFlight];
+    Raw<T, VEC ? V : 1> x[kFlight][VEC ? 8 / V : 8];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      row[f] = at.row;
+      col0[f] = at.piece * kPiece;
+      at.next();
+      const T* const p = static_cast<const T*>(a.x) + row[f] * a.ld;
+#pragma unroll
+      for (int i = 0; i < (VEC ? 8 / V : 8); ++i) {
+        const int c = VEC ? col0[f] + lane * 8 + i * V : col0[f] + i * 32 + lane;
+        x[f][i].zero();
+        if (row[f] < a.rows && c < a.width && x_ok<T>(a, row[f], c + (VEC ? V - 1 : 0))) x[f][i].load_once(p + c);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      if (row[f] >= a.rows) break;                        // the warp's
+      uint8_t* const codes = a.codes + row[f] * a.ld_codes;
+      uint8_t* const exponents = a.exponents + row[f] * a.ld_exponents;
+      if constexpr (VEC) {
+        const int c = col0[f] + lane * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = x[f][j / V].at(j % V);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, finite_bits(v[j]));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const uint32_t e = block_exponent(top);
+        const float by = inverse_of(e);
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          w[j] = codes_of(v[4 * j] * by, v[4 * j + 1] * by) | codes_of(v[4 * j + 2] * by, v[4 * j + 3] * by) << 16;
+        if (c - lane % 4 * 8 >= a.width || !codes_ok(a, row[f], c + 7)) continue;   // no such block
+        *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+        if (lane % 4 == 0) exponents[c / kSavedBlock] = static_cast<uint8_t>(e);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = col0[f] + i * 32 + lane;
+          const float v = x[f][i].at(0);
+          const uint32_t e = block_exponent(__reduce_max_sync(0xFFFFFFFFu, finite_bits(v)));
+          if (c - lane >= a.width || !codes_ok(a, row[f], c)) continue;
+          codes[c] = static_cast<uint8_t>(codes_of(v * inverse_of(e), 0.0f));
+          if (lane == 0) exponents[c / kSavedBlock] = static_cast<uint8_t>(e);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- bringing back
+// VEC: a row's last vector may reach past its last column, where its codes
+// are 0 (scratch rows).
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertArgs a) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  Pieces at(a.pieces);
+  while (at.row < a.rows) {
+    long long row[kFlight];
+    int col0[kFlight];
+    uint2 w[kFlight];
+    uint8_t code[kFlight][VEC ? 1 : 8], e[kFlight][VEC ? 1 : 8];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      row[f] = at.row;
+      col0[f] = at.piece * kPiece;
+      at.next();
+      const uint8_t* const codes = a.codes + row[f] * a.ld_codes;
+      const uint8_t* const exponents = a.exponents + row[f] * a.ld_exponents;
+      if constexpr (VEC) {
+        const int c = col0[f] + lane * 8;
+        w[f] = make_uint2(0u, 0u);
+        e[f][0] = 1;
+        if (row[f] < a.rows && c < a.width && codes_ok(a, row[f], c + 7)) {
+          w[f] = __ldcs(reinterpret_cast<const uint2*>(codes + c));
+          e[f][0] = __ldg(exponents + c / kSavedBlock);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = col0[f] + i * 32 + lane;
+          code[f][i] = 0;
+          e[f][i] = 1;
+          if (row[f] < a.rows && c < a.width && codes_ok(a, row[f], c)) {
+            code[f][i] = __ldcs(codes + c);
+            e[f][i] = __ldg(exponents + c / kSavedBlock);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      if (row[f] >= a.rows) break;
+      T* const out = static_cast<T*>(a.out) + row[f] * a.ld;
+      if constexpr (VEC) {
+        const int c = col0[f] + lane * 8;
+        const float by = power_of(e[f][0]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = values_of(((j < 2 ? w[f].x : w[f].y) >> (16 * (j & 1))) & 0xFFFFu);
+          v[2 * j] = p.x * by;
+          v[2 * j + 1] = p.y * by;
+        }
+#pragma unroll
+        for (int i = 0; i < 8 / V; ++i) {
+          float part[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) part[j] = v[i * V + j];
+          if (c + i * V < a.width && x_ok<T>(a, row[f], c + i * V + V - 1)) store_vec<T, V>(out + c + i * V, part);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = col0[f] + i * 32 + lane;
+          if (c < a.width && x_ok<T>(a, row[f], c))
+            out[c] = from_f32<T>(values_of(code[f][i]).x * power_of(e[f][i]));
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+size_t type_size(int type) { return type == GEMM_F32_TYPE_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+bool on_boundaries(const void* p, long long ld, size_t size) { return aligned_to(p, 16) && ld * size % 16 == 0; }
+
+size_t matrix_bytes(long long rows, long long width, long long ld, size_t size) {
+  return rows > 0 ? (static_cast<size_t>(rows - 1) * ld + width) * size : 0;
+}
+
+bool addressable(long long rows, long long ld) { return rows == 0 || ld <= LLONG_MAX / 8 / rows; }
+
+bool type_ok(int type) { return type == GEMM_F32_TYPE_F32 || type == GEMM_F32_TYPE_BF16; }
+
+bool matrix_ok(const void* p, long long ld, long long rows, int width, size_t size) {
+  return p && aligned_to(p, size) && ld >= width && addressable(rows, ld);
+}
+
+bool saved_ok(const void* codes, long long ld_codes, const void* exponents, long long ld_exponents, long long rows,
+              int width) {
+  return codes && exponents && on_boundaries(codes, ld_codes, 1) && on_boundaries(exponents, ld_exponents, 1) &&
+         ld_codes >= (width + 31LL) / 32 * 32 && ld_exponents >= (width + 31LL) / 32 && addressable(rows, ld_codes) &&
+         addressable(rows, ld_exponents);
+}
+
+// A matrix apart from 8-bit rows.
+bool apart(const void* p, size_t bytes, const void* codes, long long ld_codes, const void* exponents,
+           long long ld_exponents, long long rows) {
+  return !ranges_overlap(p, bytes, codes, static_cast<size_t>(rows) * ld_codes) &&
+         !ranges_overlap(p, bytes, exponents, static_cast<size_t>(rows) * ld_exponents);
+}
+
+int launch_convert(void (*kernel)(ConvertArgs), ConvertArgs& a, int num_sms, cudaStream_t stream, int* launches) {
+  a.pieces = (a.width - 1) / kPiece + 1;
+  constexpr long long kPerCta = kConvertThreads / 32 * kFlight;
+  const long long ctas = a.rows > LLONG_MAX / a.pieces ? LLONG_MAX : (a.rows * a.pieces - 1) / kPerCta + 1;
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(ctas, 8LL * num_sms));
+  if (launch_dependent(kernel, dim3(grid), dim3(kConvertThreads), 0, stream, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GEMM_F32_ELAUNCH;
+  }
+  ++*launches;
+  return GEMM_F32_OK;
+}
+
+struct Layout {
+  size_t bytes = 0;
+  size_t take(size_t n) {
+    const size_t at = bytes;
+    bytes += (n + 255) / 256 * 256;
+    return at;
+  }
+};
+
+}  // namespace
+}  // namespace gemm_f32_impl
+
+using namespace gemm_f32_impl;
+
+extern "C" int gemm_f32_checkpoint(int type, long long rows, int width, const void* x, long long ldx,
+                                   unsigned char* codes, long long ld_codes, unsigned char* exponents,
+                                   long long ld_exponents, gemm_f32_stream_t stream_handle) {
+  note_launches(0, "none");
+  if (!type_ok(type) || rows < 0 || width < 1) return GEMM_F32_EINVAL;
+  if (rows == 0) return GEMM_F32_OK;
+  const size_t es = type_size(type);
+  if (!matrix_ok(x, ldx, rows, width, es) || !saved_ok(codes, ld_codes, exponents, ld_exponents, rows, width))
+    return GEMM_F32_EINVAL;
+  if (!apart(x, matrix_bytes(rows, width, ldx, es), codes, ld_codes, exponents, ld_exponents, rows) ||
+      ranges_overlap(codes, static_cast<size_t>(rows) * ld_codes, exponents, static_cast<size_t>(rows) * ld_exponents))
+    return GEMM_F32_EINVAL;
+  int device = 0, num_sms = 0, launches = 0;
+  ConvertArgs a = {rows, width, x, nullptr, ldx, codes, ld_codes, exponents, ld_exponents, 0, nullptr};
+  if (!current_device(&device, &num_sms, &a.err)) return GEMM_F32_EDEVICE;
+  const bool vec = on_boundaries(x, ldx, es) && width * es % 16 == 0;
+  const int rc = launch_convert(type == GEMM_F32_TYPE_F32
+                                    ? vec ? checkpoint_kernel<float, true> : checkpoint_kernel<float, false>
+                                    : vec ? checkpoint_kernel<bf16, true> : checkpoint_kernel<bf16, false>,
+                                a, num_sms, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+  if (rc == GEMM_F32_OK) note_launches(launches, "checkpoint_kernel");
+  return rc;
+}
+
+extern "C" int gemm_f32_restore(int type, long long rows, int width, const unsigned char* codes, long long ld_codes,
+                                const unsigned char* exponents, long long ld_exponents, void* out, long long ldo,
+                                gemm_f32_stream_t stream_handle) {
+  note_launches(0, "none");
+  if (!type_ok(type) || rows < 0 || width < 1) return GEMM_F32_EINVAL;
+  if (rows == 0) return GEMM_F32_OK;
+  const size_t es = type_size(type);
+  if (!matrix_ok(out, ldo, rows, width, es) || !saved_ok(codes, ld_codes, exponents, ld_exponents, rows, width) ||
+      !apart(out, matrix_bytes(rows, width, ldo, es), codes, ld_codes, exponents, ld_exponents, rows))
+    return GEMM_F32_EINVAL;
+  int device = 0, num_sms = 0, launches = 0;
+  ConvertArgs a = {rows,     width, nullptr, out, ldo, const_cast<uint8_t*>(codes), ld_codes, const_cast<uint8_t*>(exponents),
+                   ld_exponents, 0,     nullptr};
+  if (!current_device(&device, &num_sms, &a.err)) return GEMM_F32_EDEVICE;
+  const bool vec = on_boundaries(out, ldo, es) && width * es % 16 == 0;
+  const int rc = launch_convert(type == GEMM_F32_TYPE_F32 ? vec ? restore_kernel<float, true> : restore_kernel<float, false>
+                                                          : vec ? restore_kernel<bf16, true> : restore_kernel<bf16, false>,
+                                a, num_sms, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+  if (rc == GEMM_F32_OK) note_launches(launches, "restore_kernel");
+  return rc;
+}
+
+namespace gemm_f32_impl {
+namespace {
+
+struct WeightGrad {
+  bool f32;                              // dy
+  int rows, width, out;
+  const void* dy;
+  long long lddy;
+  const uint8_t* codes;
+  long long ld_codes;
+  const uint8_t* exponents;
+  long long ld_exponents;
+  bool dw_f32;
+  void* dw;
+  long long lddw;
+  bool accumulate;
+};
+
+int run_weight_grad(const WeightGrad& c, cudaStream_t stream, int* launches) {
+  int device = 0, num_sms = 0;
+  unsigned* err = nullptr;
+  if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
+  const int parts = c.f32 ? 3 : 1;
+  const long long ldx = (c.width + 7LL) / 8 * 8;
+  const bool packed = c.f32 || !on_boundaries(c.dy, c.lddy, 2);
+  const long long lddy = packed ? (c.out + 7LL) / 8 * 8 : c.lddy;
+  const bool sum_f32 = c.dw_f32 && !c.f32;
+  Layout layout;
+  const size_t at_x = layout.take(static_cast<size_t>(c.rows) * ldx * 2);
+  const size_t at_dy = packed ? layout.take(static_cast<size_t>(c.rows) * lddy * 2 * parts) : 0;
+  const size_t at_partials = layout.take(half_gemm_scratch(c.out, c.width, c.rows, parts, num_sms, sum_f32));
+  char* const scratch = static_cast<char*>(acquire_scratch(device, stream, layout.bytes));
+  if (!scratch) return GEMM_F32_ESCRATCH;
+  ConvertArgs x = {c.rows,      static_cast<int>(ldx), nullptr, scratch + at_x, ldx, const_cast<uint8_t*>(c.codes), c.ld_codes,
+                   const_cast<uint8_t*>(c.exponents), c.ld_exponents,   0,       err};
+  int rc = launch_convert(restore_kernel<bf16, true>, x, num_sms, stream, launches);
+  if (rc != GEMM_F32_OK) return rc;
+  const long long plane = lddy * c.rows;
+  if (packed) {
+    rc = pack_operand_half(c.f32, c.dy, c.lddy, c.rows, c.out, scratch + at_dy, lddy, plane, num_sms, err, stream, launches);
+    if (rc != GEMM_F32_OK) return rc;
+  }
+  HalfGemm g = {};
+  g.M = c.out;
+  g.N = c.width;
+  g.K = c.rows;
+  g.parts = parts;
+  g.a = {packed ? scratch + at_dy : c.dy, lddy, plane, true};
+  g.b = {scratch + at_x, ldx, 0, true};
+  g.b_whole = true;
+  g.sum_f32 = sum_f32;
+  g.c = c.dw;
+  g.ldc = c.lddw;
+  g.c_f32 = c.dw_f32;
+  if (c.accumulate) {
+    g.add = static_cast<const float*>(c.dw);
+    g.ldadd = c.lddw;
+  }
+  g.partials = reinterpret_cast<float*>(scratch + at_partials);
+  g.num_sms = num_sms;
+  g.device = device;
+  g.err = err;
+  return launch_half_gemm(g, stream, launches);
+}
+
+}  // namespace
+}  // namespace gemm_f32_impl
+
+extern "C" int gemm_f32_weight_grad(int type, long long rows, int width, int out, const void* dy, long long lddy,
+                                    const unsigned char* codes, long long ld_codes, const unsigned char* exponents,
+                                    long long ld_exponents, int dw_type, void* dw, long long lddw, int accumulate,
+                                    gemm_f32_stream_t stream_handle) {
+  note_launches(0, "none");
+  constexpr int kMost = INT_MAX - 256;   // tiles rounded up stay within an int
+  if (!type_ok(type) || (dw_type != type && dw_type != GEMM_F32_TYPE_F32)) return GEMM_F32_EINVAL;
+  if (accumulate != 0 && (accumulate != 1 || dw_type != GEMM_F32_TYPE_F32)) return GEMM_F32_EINVAL;
+  if (rows < 0 || rows > kMost || width < 1 || width > kMost || out < 1 || out > kMost) return GEMM_F32_EINVAL;
+  const size_t es = type_size(type), ds = type_size(dw_type);
+  if (!matrix_ok(dw, lddw, out, width, ds)) return GEMM_F32_EINVAL;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+  int launches = 0;
+  if (rows == 0) {
+    int device = 0, num_sms = 0;
+    unsigned* err = nullptr;
+    if (accumulate) return GEMM_F32_OK;
+    if (!current_device(&device, &num_sms, &err)) return GEMM_F32_EDEVICE;
+    if (cudaMemset2DAsync(dw, lddw * ds, 0, width * ds, out, stream) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return GEMM_F32_ELAUNCH;
+    }
+    note_launches(1, "memset");
+    return GEMM_F32_OK;
+  }
+  const size_t dw_bytes = matrix_bytes(out, width, lddw, ds);
+  if (!matrix_ok(dy, lddy, rows, out, es) || !saved_ok(codes, ld_codes, exponents, ld_exponents, rows, width) ||
+      !apart(dw, dw_bytes, codes, ld_codes, exponents, ld_exponents, rows) ||
+      ranges_overlap(dw, dw_bytes, dy, matrix_bytes(rows, out, lddy, es)))
+    return GEMM_F32_EINVAL;
+  const WorkspaceCall call;
+  const WeightGrad c = {type == GEMM_F32_TYPE_F32, static_cast<int>(rows), width, out, dy, lddy, codes, ld_codes,
+                        exponents, ld_exponents, dw_type == GEMM_F32_TYPE_F32, dw, lddw, accumulate != 0};
+  const int rc = run_weight_grad(c, stream, &launches);
+  if (rc == GEMM_F32_OK) note_launches(launches, "half_gemm_kernel");
+  return rc;
+}

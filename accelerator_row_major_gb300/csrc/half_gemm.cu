@@ -25,7 +25,8 @@
 // into its accumulator by truncation (measured: a sum over K drifts towards
 // zero by about 1e-9 K of its size), so the accumulator takes only 256 of K
 // at a time, smallest products first, and the epilogue warps add these
-// partial sums in registers, rounding to nearest.
+// partial sums in registers, rounding to nearest.  With a right operand that
+// is bfloat16 as it is (PARTS = kLeftParts) three products do: lo, mid, hi.
 //
 // Work: whole tiles round robin over the pairs; the tiles of the last,
 // partial wave are split along K over all pairs, whose partial tiles a
@@ -84,6 +85,7 @@ constexpr int kMostTeam = 4;
 constexpr int kSumF32 = 4;
 constexpr int kSumLogits = 16;
 constexpr int kWholeLogits = 1024;
+constexpr int kLeftParts = 2;            // PARTS: the left operand alone comes in three
 
 // Epilogues
 constexpr int kLogits = 0;
@@ -375,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (EPI == kLogits && blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0u;
 
   // K blocks of unit u of the work list, and how often they are passed over
-  constexpr int kCombos = PARTS == 3 ? 6 : 1;
+  constexpr int kCombos = PARTS == 3 ? 6 : PARTS == kLeftParts ? 3 : 1;
   auto first_block = [&](int u) { return SUM ? u * SUM : u; };
   auto end_block = [&](int u) { return SUM ? min((u + 1) * SUM, p.k_blocks) : u + 1; };
 
@@ -395,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = w.k0; ok && u < w.k1; ++u) {
           for (int combo = 0; ok && combo < kCombos; ++combo) {
             // (lo, hi), (hi, lo), (mid, mid), (mid, hi), (hi, mid), (hi, hi)
-            const int pa = PARTS == 3 ? (0x001102 >> (4 * combo)) & 3 : 0;
+            const int pa = PARTS == 3 ? (0x001102 >> (4 * combo)) & 3 : PARTS == kLeftParts ? 2 - combo : 0;
             const int pb = PARTS == 3 ? (0x010120 >> (4 * combo)) & 3 : 0;
             for (int kb = first_block(u); kb < end_block(u); ++kb) {
               if (!mbar_wait(empty_bar(s), ph ^ 1u, p.err, kSiteProducerEmpty)) {
@@ -728,7 +730,7 @@ int blocks_of(int n, int per) { return (n - 1) / per + 1; }
 
 // Tiles, K units and the split of the last wave; returns the bytes of
 // partial tiles.
-size_t plan(Params& p, int M, int N, int K, int sum, int parts, int num_sms, bool split) {
+size_t plan(Params& p, int M, int N, int K, int sum, int num_sms, bool split) {
   p.M = M;
   p.N = N;
   p.tiles_m = blocks_of(M, kTile);
@@ -748,7 +750,7 @@ size_t plan(Params& p, int M, int N, int K, int sum, int parts, int num_sms, boo
   for (int team = kMostTeam; team > 1 && p.team == 1; team /= 2)
     if (pairs % team == 0 && tail % team == 0) p.team = team;
   const size_t bytes = plan_split_tail(p, tiles / p.team, pairs / p.team, sizeof(float) * kTile * kTile * p.team,
-                                       parts == 3 ? 1 : kMinSplitBlocks);
+                                       sum ? 1 : kMinSplitBlocks);
   p.dp_tiles = bytes ? p.dp_tiles * p.team : static_cast<int>(tiles);
   if (p.dp_tiles == 0) p.raster = kSplitRaster;
   return bytes;
@@ -810,28 +812,31 @@ int launch_one(const HalfGemm& g, const Params& p, const Maps& m, int grid, cuda
   return GEMM_F32_OK;
 }
 
-int sum_blocks(bool logits, int parts, int K) {
+int sum_blocks(bool logits, int parts, int K, bool sum_f32) {
   if (parts == 3) return kSumF32;
+  if (sum_f32) return kSumLogits;
   return logits && K > kWholeLogits ? kSumLogits : 0;
 }
 
-// The forms the vocabulary loss needs: logits of K-major operands, and
-// products with an MN-major right operand.
+// The forms the vocabulary loss and the weight gradient need: logits of
+// K-major operands, and products with an MN-major right operand.
 int launch_form(const HalfGemm& g, const Params& p, const Maps& m, int grid, cudaStream_t stream) {
-  const int sum = sum_blocks(!g.c, g.parts, g.K);
+  const int sum = sum_blocks(!g.c, g.parts, g.K, g.sum_f32);
   if (!g.c) {
     if (g.parts == 3) return launch_one<false, false, 3, kSumF32, kLogits>(g, p, m, grid, stream);
     if (sum) return launch_one<false, false, 1, kSumLogits, kLogits>(g, p, m, grid, stream);
     return launch_one<false, false, 1, 0, kLogits>(g, p, m, grid, stream);
   }
   if (g.parts == 3) {
-    if (!g.c_f32) return GEMM_F32_EINVAL;
+    if (!g.c_f32 || (g.b_whole && !g.a.mn_major)) return GEMM_F32_EINVAL;
+    if (g.b_whole) return launch_one<true, true, kLeftParts, kSumF32, kStoreF32>(g, p, m, grid, stream);
     return g.a.mn_major ? launch_one<true, true, 3, kSumF32, kStoreF32>(g, p, m, grid, stream)
                         : launch_one<false, true, 3, kSumF32, kStoreF32>(g, p, m, grid, stream);
   }
   if (g.c_f32) {
     if (!g.a.mn_major) return GEMM_F32_EINVAL;
-    return launch_one<true, true, 1, 0, kStoreF32>(g, p, m, grid, stream);
+    return sum ? launch_one<true, true, 1, kSumLogits, kStoreF32>(g, p, m, grid, stream)
+               : launch_one<true, true, 1, 0, kStoreF32>(g, p, m, grid, stream);
   }
   return g.a.mn_major ? launch_one<true, true, 1, 0, kStoreBf16>(g, p, m, grid, stream)
                       : launch_one<false, true, 1, 0, kStoreBf16>(g, p, m, grid, stream);
@@ -839,9 +844,9 @@ int launch_form(const HalfGemm& g, const Params& p, const Maps& m, int grid, cud
 
 }  // namespace
 
-size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms) {
+size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms, bool sum_f32) {
   Params p = {};
-  return plan(p, M, N, K, sum_blocks(false, parts, K), parts, num_sms, true);
+  return plan(p, M, N, K, sum_blocks(false, parts, K, sum_f32), num_sms, true);
 }
 
 int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
@@ -849,7 +854,7 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
   if (pairs < 1) return GEMM_F32_EDEVICE;
   if (g.c ? !g.b.mn_major : g.a.mn_major || g.b.mn_major) return GEMM_F32_EINVAL;
   Params p = {};
-  plan(p, g.M, g.N, g.K, sum_blocks(!g.c, g.parts, g.K), g.parts, g.num_sms, g.c != nullptr);
+  plan(p, g.M, g.N, g.K, sum_blocks(!g.c, g.parts, g.K, g.sum_f32), g.num_sms, g.c != nullptr);
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x7fffffffLL) return GEMM_F32_EINVAL;
   p.partials = g.partials;
@@ -869,10 +874,11 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
   p.arrived = g.arrived;
   p.err = g.err;
   Maps m = {};
+  const int b_parts = g.b_whole ? 1 : g.parts;
   if (!(g.a.mn_major ? encode(&m.a, g.a, g.K, g.M, g.parts, 64)
                      : encode(&m.a, g.a, g.M, g.K, g.parts, kHalf)) ||
-      !(g.b.mn_major ? encode(&m.b, g.b, g.K, g.N, g.parts, 64)
-                     : encode(&m.b, g.b, g.N, g.K, g.parts, kHalf)))
+      !(g.b.mn_major ? encode(&m.b, g.b, g.K, g.N, b_parts, 64)
+                     : encode(&m.b, g.b, g.N, g.K, b_parts, kHalf)))
     return GEMM_F32_ELAUNCH;
   if (g.c) {
     const int size = g.c_f32 ? 4 : 2;

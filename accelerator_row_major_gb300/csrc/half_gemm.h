@@ -28,6 +28,9 @@ struct HalfGemm {
   int M, N, K;
   int parts;                    // 1, or 3 (fp32 operands split into three parts)
   HalfOperand a, b;
+  bool b_whole = false;         // of parts 3: b is one part, bfloat16 as it is
+  bool sum_f32 = false;         // fp32 C of one part: 1024 of K at a time are summed on the tensor cores,
+                                // these sums in registers, rounded to nearest
   // -- a stored product: C = *scale * D (+ add)
   void* c = nullptr;
   long long ldc = 0;
@@ -53,10 +56,16 @@ struct HalfGemm {
 
 // Bytes of partial tiles that the stored product of this shape needs (0 when
 // its last wave is not split along K).
-size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms);
+size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms, bool sum_f32 = false);
 
 // Returns 0 or a negative GEMM_F32_E* code; counts its kernels in *launches.
 int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
+
+// Stores a matrix as an operand that TMA can read: bfloat16 (copied), or fp32
+// in three parts of bfloat16 `plane` elements apart, in rows of ld_dst
+// elements (a multiple of 8), zero from column `cols` on.
+int pack_operand_half(bool f32, const void* src, long long ld, int rows, int cols, void* dst, long long ld_dst,
+                      long long plane, int num_sms, unsigned* err, cudaStream_t stream, int* launches);
 
 // The same two products for few rows (at most kFewRows), where reading w is
 // what takes the time (few_gemm.cu).  w is read as it is stored, fp32

@@ -82,13 +82,6 @@ __host__ __device__ __forceinline__ size_t ring_row_bytes(int width, size_t size
   return ragged ? (width * size + 15) / 16 * 16 + 16 : width * size;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // The ring of one group: ARRAYS rows per stage (x, or x and dy), filled for
 // the group's rows first, first + step, ..., `stages` ahead.  Of each row the
 // `width` elements from column `col0` on: all of it, or where `ctas` CTAs
@@ -527,14 +520,6 @@ __global__ void __launch_bounds__(stream_threads(G), 1)
       mine.store(static_cast<T*>(a.out) + row * a.ldo, x);
   }
   if (t == 0) ring.finish(row);
-}
-
-// Two floats into the shared memory of another CTA of the cluster, counted by
-// a barrier there.
-__device__ __forceinline__ void store_async(uint32_t to, float x, float y, uint32_t bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
-               "f"(x), "f"(y), "r"(bar)
-               : "memory");
 }
 
 template <class T, class WT, int G, int NP, bool RAGGED, int CTAS>

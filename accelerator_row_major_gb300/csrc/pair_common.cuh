@@ -1,4 +1,4 @@
-// Primitives of clusters (barriers, remote mbarrier arrives) and of MMAs on
+// Primitives of clusters (barriers, remote mbarrier arrives and stores), bulk copies and MMAs on
 // CTA pairs (tcgen05 cta_group::2: tensor memory of the pair, commits to both
 // CTAs) for the bfloat16 products and the streaming norms, the choice of the
 // lane that issues MMAs, and the tensor-map encoder.
@@ -74,6 +74,23 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
       return false;
     }
   }
+}
+
+// Bytes of global memory into this CTA's shared memory, counted by a barrier:
+// both addresses on 16-byte boundaries, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Two floats into the shared memory of another CTA of the cluster, counted by
+// a barrier there.
+__device__ __forceinline__ void store_async(uint32_t to, float x, float y, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+               "f"(x), "f"(y), "r"(bar)
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
