@@ -108,7 +108,7 @@ __device__ __forceinline__ bool output_ok(const Output& o, const RowPlan& plan, 
 
 // ---------------------------------------------------------------- forward
 template <class T, int NE, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, 1) block_norm_kernel(const __grid_constant__ BlockArgs a) {
+__global__ void __launch_bounds__(kAllThreads, 1) block_norm_kernel(const __grid_constant__ BlockArgs a) {
   using Part = RowPart<T, NE, VEC>;
   constexpr int NP = Part::NP;
   extern __shared__ __align__(128) uint8_t smem_rows[];
@@ -116,18 +116,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_kernel(const __grid
   const RowPlan& plan = a.plan;
   const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
   const int rank = plan.ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
-  RowsRing<kInputs> ring(a.in, plan, a.err, smem_rows, group, rank);
+  const bool producer = group == plan.groups;
+  const RingPlace ring(plan, smem_rows, rank);
   RowSums sums = row_sums(shared, plan, group, rank, a.err);
-  if (threadIdx.x == 0 && plan.ctas > 1)
-    for (int i = 0; i < 2; ++i) mbar_init(sums.bars + 8u * i, 1);
-  if (t == 0) ring.init();
+  if (threadIdx.x == 0) {
+    if (plan.ctas > 1)
+      for (int i = 0; i < 2; ++i) mbar_init(sums.bars + 8u * i, 1);
+    ring.init(plan);
+  }
   __syncthreads();
   if (plan.ctas > 1) cluster_sync();     // every CTA of the cluster runs
   grid_launch_dependents();
   grid_dependency_wait();
-  long long row = ring.next;
-  if (t == 0)
-    for (int i = 0; i < plan.stages; ++i) ring.load(i);
   float* const columns = reinterpret_cast<float*>(smem_rows);
   const int slots = Part::slots(plan.lanes);
 #pragma unroll 1
@@ -140,13 +140,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_kernel(const __grid
   const float inv = 1.0f / static_cast<float>(plan.width);
   auto vector = [&](int v, Pair(&w)[NP]) { mine.load_columns(columns + a.vectors.slot[v] * slots, w); };
 
-  bool read = false;                     // the stage has been read
-  auto after_barrier = [&]() {
-    if (read) return;
-    read = true;
-    if (t == 0) ring.refill();
-    ring.advance();
-  };
   // x around its mean (0 for rms), 1 / its root mean square there.
   auto normalise = [&](Pair(&x)[NP], float& mean, float& rstd) {
     float s[1];
@@ -157,7 +150,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_kernel(const __grid
       for (int j = 0; j < NP; ++j) sum = add2(sum, x[j]);
       s[0] = sum_of(sum);
       sums.add<1>(s);
-      after_barrier();
       mean = s[0] * inv;
 #pragma unroll
       for (int j = 0; j < NP; ++j) x[j] = add2(x[j], both(-mean));
@@ -168,18 +160,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_kernel(const __grid
     for (int j = 0; j < NP; ++j) sum = fma2(x[j], x[j], sum);
     s[0] = sum_of(sum);
     sums.add<1>(s);
-    after_barrier();
     rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
   };
 
-  for (; row < plan.rows; row += ring.step) {
-    ring.wait();
-    read = false;
+  if (producer) produce_rows(a.in, plan, ring, a.err);
+  RingReader reader = {ring, plan, a.err, group};
+  for (long long row = ring.first * plan.groups + group; !producer && row < plan.rows; row += ring.step * plan.groups) {
+    reader.wait();
     Pair p[NP], x[NP], w[NP];
-    mine.load(ring.at(kInBranch), ring.shift(kInBranch, row), p);
-    mine.load(ring.at(kInResidual), ring.shift(kInResidual, row), x);
+    mine.load(reader.at(a.in[kInBranch], row, VEC), p);
+    mine.load(reader.at(a.in[kInResidual], row, VEC), x);
     Pair gate[NP];
-    if (a.gate == kElementGate) mine.load(ring.at(kInGate), ring.shift(kInGate, row), gate);
+    if (a.gate == kElementGate) mine.load(reader.at(a.in[kInGate], row, VEC), gate);
+    reader.release();
     float mean, rstd, mean_b = 0.0f, rstd_b = 0.0f;
     if (a.post) {
       normalise(p, mean_b, rstd_b);
@@ -222,13 +215,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_kernel(const __grid
       }
     }
   }
-  if (t == 0) ring.finish();
   if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
 }
 
 // ---------------------------------------------------------------- gradient
 template <class T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, 1) block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
+__global__ void __launch_bounds__(kAllThreads, 1) block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
   constexpr int NE = 8;
   using Part = RowPart<T, NE, VEC>;
   constexpr int NP = Part::NP;
@@ -237,18 +229,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_grad_kernel(const _
   const RowPlan& plan = a.plan;
   const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
   const int rank = plan.ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
-  RowsRing<kGradInputs> ring(a.in, plan, a.err, smem_rows, group, rank);
+  const bool producer = group == plan.groups;
+  const RingPlace ring(plan, smem_rows, rank);
   RowSums sums = row_sums(shared, plan, group, rank, a.err);
-  if (threadIdx.x == 0 && plan.ctas > 1)
-    for (int i = 0; i < 2; ++i) mbar_init(sums.bars + 8u * i, 1);
-  if (t == 0) ring.init();
+  if (threadIdx.x == 0) {
+    if (plan.ctas > 1)
+      for (int i = 0; i < 2; ++i) mbar_init(sums.bars + 8u * i, 1);
+    ring.init(plan);
+  }
   __syncthreads();
   if (plan.ctas > 1) cluster_sync();     // every CTA of the cluster runs
   grid_launch_dependents();
   grid_dependency_wait();
-  long long row = ring.next;
-  if (t == 0)
-    for (int i = 0; i < plan.stages; ++i) ring.load(i);
   float* const columns = reinterpret_cast<float*>(smem_rows);
   const int slots = Part::slots(plan.lanes);
 #pragma unroll 1
@@ -273,32 +265,37 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_grad_kernel(const _
     for (int k = 0; k < 4; ++k)
       if (k < 2 || a.post) stat[k] = __ldg(a.stats + k * plan.rows + r);
   };
+  if (producer) produce_rows(a.in, plan, ring, a.err);
+  RingReader reader = {ring, plan, a.err, group};
+  const long long step = ring.step * plan.groups;
+  long long row = producer ? plan.rows : ring.first * plan.groups + group;
   load_stats(row);
-  for (; row < plan.rows; row += ring.step) {
-    ring.wait();
+  for (; row < plan.rows; row += step) {
+    reader.wait();
     const float mean = a.rms ? 0.0f : stat[0], rstd = stat[1];
     const float mean_b = a.rms ? 0.0f : stat[2], rstd_b = stat[3];
-    load_stats(row + ring.step);
-    // all of the row into registers, so that its stage is free after the first sums
+    load_stats(row + step);
+    // all of the row into registers, so that its stage is free
     Pair c[NP], g[NP], d[NP], b[NP], gate[NP], w[NP];
     if (a.in[kGradHExponents].p)
-      mine.load_saved(ring.at(kGradH), ring.at(kGradHExponents), c);
+      mine.load_saved(reader.at(a.in[kGradH], row, true), reader.at(a.in[kGradHExponents], row, true), c);
     else
-      mine.load(ring.at(kGradH), ring.shift(kGradH, row), c);
-    mine.load(ring.at(kGradDy), ring.shift(kGradDy, row), g);
+      mine.load(reader.at(a.in[kGradH], row, VEC), c);
+    mine.load(reader.at(a.in[kGradDy], row, VEC), g);
     if (a.in[kGradDh].p) {
-      mine.load(ring.at(kGradDh), ring.shift(kGradDh, row), d);
+      mine.load(reader.at(a.in[kGradDh], row, VEC), d);
     } else {
 #pragma unroll
       for (int j = 0; j < NP; ++j) d[j] = 0;
     }
     if (a.branch) {
       if (a.in[kGradBranchExponents].p)
-        mine.load_saved(ring.at(kGradBranch), ring.at(kGradBranchExponents), b);
+        mine.load_saved(reader.at(a.in[kGradBranch], row, true), reader.at(a.in[kGradBranchExponents], row, true), b);
       else
-        mine.load(ring.at(kGradBranch), ring.shift(kGradBranch, row), b);
+        mine.load(reader.at(a.in[kGradBranch], row, VEC), b);
     }
-    if (a.gate == kElementGate) mine.load(ring.at(kGradGate), ring.shift(kGradGate, row), gate);
+    if (a.gate == kElementGate) mine.load(reader.at(a.in[kGradGate], row, VEC), gate);
+    reader.release();
     // c = h - mean in place of hat = c rstd: where rstd is 0 (squares that
     // overflowed) or c is, hat is 0 and never 0 times infinity
     vector(kWeight, w);
@@ -314,8 +311,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_grad_kernel(const _
     }
     float s[2] = {sum_of(sg), rstd != 0.0f ? sum_of(sgc) * rstd : 0.0f};
     sums.add<2>(s);
-    if (t == 0) ring.refill();
-    ring.advance();
     {
       const float c1 = a.rms ? 0.0f : -s[0] * inv, c2 = -s[1] * inv * rstd;
 #pragma unroll
@@ -384,7 +379,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_grad_kernel(const _
     if (a.dbranch.p && output_ok<T>(a.dbranch, plan, row, a.err))
       mine.store(static_cast<T*>(a.dbranch.p) + row * a.dbranch.ld + ring.col0, d);
   }
-  if (t == 0) ring.finish();
   if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
   if (!a.sums) return;
   // the groups' sums, added in group order: one row of partials per CTA (or
@@ -395,7 +389,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) block_norm_grad_kernel(const _
     __syncthreads();
     float* const own = columns + group * slots;
 #pragma unroll
-    for (int q = 0; q < NE / 4; ++q) {
+    for (int q = 0; q < (producer ? 0 : NE / 4); ++q) {
       float4 f;
       unpair(total[k][2 * q], f.x, f.y);
       unpair(total[k][2 * q + 1], f.z, f.w);
@@ -671,25 +665,28 @@ bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ne, bool al
     plan.groups = static_cast<int>(std::min<long long>(ctas > 1 ? 1 : kRowThreads / plan.lanes,
                                                        (plan.rows - 1) / units + 1));
     const size_t columns = static_cast<size_t>(vectors) * ne * plan.lanes * sizeof(float);
-    size_t stage = 0;
-    for (int i = 0; i < n; ++i) {
-      if (!in[i].p) continue;
-      in[i].at = static_cast<uint32_t>(stage);
-      stage += (source_bytes(in[i].size, slice) + 15) / 16 * 16 + (aligned || in[i].size < 2 ? 0 : 16);
-    }
-    plan.stage_bytes = static_cast<uint32_t>(stage);
-    plan.ring_at = static_cast<uint32_t>(columns);
-    size_t stages = 0;
-    for (;; --plan.groups) {             // two rows in flight per group, or fewer groups
-      stages = (kMostShared - columns) / (plan.groups * (stage + 8));
+    size_t stage = 0, stages = 0;
+    for (;; --plan.groups) {             // two chunks in flight, or fewer groups
+      stage = 0;
+      for (int i = 0; i < n; ++i) {
+        if (!in[i].p) continue;
+        const size_t row = source_bytes(in[i].size, slice);
+        in[i].packed = ctas == 1 && in[i].ld == static_cast<long long>(row);
+        in[i].pitch = static_cast<uint32_t>(in[i].packed ? row : (row + 15) / 16 * 16 + (aligned || in[i].size < 2 ? 0 : 16));
+        in[i].at = static_cast<uint32_t>(stage);
+        stage += (static_cast<size_t>(plan.groups) * in[i].pitch + 15) / 16 * 16 + (in[i].packed && !aligned ? 16 : 0);
+      }
+      stages = columns < kMostShared ? (kMostShared - columns) / (stage + 16) : 0;
       if (stages >= 2 || plan.groups == 1) break;
     }
-    if (columns >= kMostShared || stages < 2) continue;
+    if (stages < 2) continue;
+    plan.stage_bytes = static_cast<uint32_t>(stage);
+    plan.ring_at = static_cast<uint32_t>(columns);
     plan.stages = static_cast<int>(std::min<size_t>(stages, kMostStages));
     const long long need = (plan.rows - 1) / plan.groups + 1;
     *grid = static_cast<int>(std::min<long long>(units, need)) * ctas;
     // the groups' sums take the place of the ring
-    *bytes = std::max(columns + plan.groups * static_cast<size_t>(plan.stages) * (stage + 8),
+    *bytes = std::max(columns + static_cast<size_t>(plan.stages) * (stage + 16),
                       static_cast<size_t>(plan.groups) * ne * plan.lanes * sizeof(float));
     return true;
   }
@@ -709,7 +706,7 @@ int launch_rows(const Args& a, int device, int* grid, size_t bytes, cudaStream_t
   int most = kept.load();
   cudaLaunchConfig_t config = {};
   config.gridDim = dim3(*grid);
-  config.blockDim = dim3(plan.groups * plan.lanes);
+  config.blockDim = dim3(plan.groups * plan.lanes + 32);
   config.dynamicSmemBytes = bytes;
   config.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -728,7 +725,7 @@ int launch_rows(const Args& a, int device, int* grid, size_t bytes, cudaStream_t
     if (plan.ctas > 1) {
       cudaLaunchConfig_t full = config;
       full.gridDim = dim3(512 / plan.ctas * plan.ctas);
-      full.blockDim = dim3(kRowThreads);
+      full.blockDim = dim3(kAllThreads);
       full.dynamicSmemBytes = kMostShared;
       full.attrs = attr + 1;
       full.numAttrs = 1;

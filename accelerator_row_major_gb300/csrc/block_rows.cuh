@@ -7,6 +7,12 @@
 // where rows are narrow, and a cluster of CTAs shares a row, each a slice of
 // its columns, where they are wide.  Lanes, groups, ring depth and cluster are
 // the launch's: a width costs the next whole warp, not the next power of 2.
+//
+// A stage of the ring holds a chunk: one row for each group, of consecutive
+// rows.  One more warp issues the copies, a lane for each matrix (or for each
+// matrix and row, where rows do not lie one behind the other): as work of the
+// threads that compute, the copies' addresses were most of a row's time
+// (65536 x 1024 bfloat16 265 us, gradient 509, against @FWD@ and @GRAD@).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -26,8 +32,9 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 512;         // that compute
 constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kAllThreads = kRowThreads + 32;
 constexpr int kMostCtas = 8;             // of a cluster
 constexpr int kSliceUnit = 512;          // columns: their exponents fill 16 bytes
 
@@ -38,7 +45,9 @@ struct RowSource {
   const char* end;                       // one past the last byte that may be read
   long long ld;                          // bytes from row to row
   int size;
-  uint32_t at;                           // of its row within a stage
+  uint32_t at;                           // of its chunk within a stage
+  uint32_t pitch;                        // there, from row to row: ld where `packed`
+  int packed;                            // rows one behind the other: a chunk is one copy
 };
 
 // How a launch lays out its rows.
@@ -55,138 +64,178 @@ __host__ __device__ __forceinline__ uint32_t source_bytes(int size, int cols) {
 }
 
 // ---------------------------------------------------------------- ring
-// Of one group: N rows per stage, for the group's rows first, first + step,
-// ..., `stages` ahead.  A row is copied from the 16-byte boundary below its
-// start to the one above its end, but never beyond its matrix: elements
-// outside the matrix's whole blocks (near its two ends only) are copied by
-// the thread that issues the copies.
-template <int N>
-struct RowsRing {
-  const RowSource* in;                   // [N]
-  const RowPlan& plan;
-  unsigned* err;
-  uint8_t* data;
-  uint32_t bars;
-  int col0, width;                       // of this CTA's slice (no columns: width 0)
-  int s = 0;
-  uint32_t ph = 0;
-  bool lost = false;
-  long long next, step;
-  long long issued = 0, taken = 0, lost_at = 0;
+// The first byte of a row's (or slice's) part of a matrix.
+__device__ __forceinline__ uintptr_t first_byte(const RowSource& m, long long row, int col0) {
+  return reinterpret_cast<uintptr_t>(m.p) + row * m.ld + (m.size ? col0 * m.size : col0 / kSavedBlock);
+}
 
-  __device__ __forceinline__ RowsRing(const RowSource* sources, const RowPlan& p, unsigned* e, uint8_t* smem,
-                                      int group, int rank)
-      : in(sources), plan(p), err(e) {
-    data = smem + p.ring_at + static_cast<size_t>(group) * p.stages * p.stage_bytes;
-    bars = smem_addr(smem + p.ring_at) + static_cast<uint32_t>(p.groups * p.stages) * p.stage_bytes +
-           static_cast<uint32_t>(group * p.stages) * 8u;
-    const int unit = static_cast<int>(blockIdx.x) / p.ctas, units = static_cast<int>(gridDim.x) / p.ctas;
-    next = static_cast<long long>(unit) * p.groups + group;
-    step = static_cast<long long>(units) * p.groups;
+// What producer and consumers of a CTA's ring know alike.
+struct RingPlace {
+  uint8_t* data;
+  uint32_t full, empty;                  // barriers: the copies have landed; all warps have read
+  int col0, width;                       // of this CTA's slice (no columns: width 0)
+  long long first, step;                 // of its chunks
+
+  __device__ __forceinline__ RingPlace(const RowPlan& p, uint8_t* smem, int rank) {
+    data = smem + p.ring_at;
+    full = smem_addr(data) + static_cast<uint32_t>(p.stages) * p.stage_bytes;
+    empty = full + 8u * p.stages;
+    first = static_cast<int>(blockIdx.x) / p.ctas;
+    step = static_cast<int>(gridDim.x) / p.ctas;
     col0 = rank * p.slice;
     width = max(0, min(p.slice, p.width - col0));
   }
-  // One thread of the group, before the group's first barrier.
-  __device__ __forceinline__ void init() {
-    for (int i = 0; i < plan.stages; ++i) mbar_init(bars + 8u * i, 1);
+  // One thread, before the CTA's first barrier.
+  __device__ __forceinline__ void init(const RowPlan& p) const {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(full + 8u * i, 1);
+      mbar_init(empty + 8u * i, static_cast<uint32_t>(p.groups * (p.lanes / 32)));
+    }
     fence_mbar_init();
   }
-  __device__ __forceinline__ uintptr_t first_byte(const RowSource& m, long long row) const {
-    return reinterpret_cast<uintptr_t>(m.p) + row * m.ld + (m.size ? col0 * m.size : col0 / kSavedBlock);
-  }
-  // Bytes by which a row starts above a 16-byte boundary.
-  __device__ __forceinline__ uint32_t shift(int i, long long row) const {
-    return static_cast<uint32_t>(first_byte(in[i], row)) & 15u;
-  }
-  // The whole 16-byte blocks [lo, hi) of the matrix around a row's bytes.
-  __device__ __forceinline__ void blocks(const RowSource& m, uintptr_t first, uintptr_t last, uintptr_t& lo,
-                                         uintptr_t& hi) const {
+};
+
+// One copy: the bytes [first, last) of a matrix, to the place in a stage that
+// lies as far above a 16-byte boundary as they do.  The whole 16-byte blocks
+// around them go by one bulk copy, but never from beyond the matrix: elements
+// outside its whole blocks (near its two ends only) are copied here.
+struct RowCopy {
+  uint8_t* dst;                          // of the block that `first` lies in
+  uintptr_t first, last, lo, hi;
+
+  __device__ __forceinline__ RowCopy(const RowSource& m, uint8_t* to, uintptr_t from, uintptr_t end)
+      : dst(to), first(from), last(end) {
     lo = first & ~uintptr_t{15};
     hi = (last + 15) & ~uintptr_t{15};
     if (lo < reinterpret_cast<uintptr_t>(m.p)) lo += 16;
     if (hi > reinterpret_cast<uintptr_t>(m.end)) hi -= 16;
     if (lo >= hi) lo = hi = first;
+    if (lo > first || hi < last) elements(m.size);
   }
-  static __device__ __forceinline__ void copy_elements(uint8_t* dst, uintptr_t from, uintptr_t to, int size) {
-    for (uintptr_t q = from; q < to; q += size, dst += size) {
+  __device__ __forceinline__ uint32_t bytes() const { return static_cast<uint32_t>(hi - lo); }
+  __device__ __forceinline__ void issue(uint32_t bar) const {
+    if (lo < hi)
+      bulk_load(smem_addr(dst) + static_cast<uint32_t>(lo - (first & ~uintptr_t{15})),
+                reinterpret_cast<const void*>(lo), bytes(), bar);
+  }
+
+ private:
+  __device__ __noinline__ void elements(int size) const {
+    for (uintptr_t q = first; q < last; q += size) {
+      if (q >= lo && q < hi) q = hi;
+      if (q >= last) break;
+      uint8_t* const at = dst + (q - (first & ~uintptr_t{15}));
       if (size == 4)
-        *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(q);
+        *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(q);
       else
-        *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(q);
+        *reinterpret_cast<uint16_t*>(at) = *reinterpret_cast<const uint16_t*>(q);
     }
   }
-  // One thread: the copies of row `next` into stage `stage`.
-  __device__ __forceinline__ void load(int stage) {
-    if (next < plan.rows) {
-      const uint32_t bar = bars + 8u * stage;
-      uint8_t* const dst = data + static_cast<size_t>(stage) * plan.stage_bytes;
-      uint32_t bytes = 0;
+};
+
+// The producer warp's work: all of the CTA's chunks, `stages` of them in
+// flight.  It gives up at a wait that runs out (recorded), and in any case
+// waits, with a limit, for its last copies: none lands in memory that is no
+// longer the kernel's.
+template <int N>
+__device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const RowPlan& plan, const RingPlace& ring,
+                                             unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  int s = 0, issued = 0;
+  uint32_t ph = 0;
+  for (long long chunk = ring.first; chunk * plan.groups < plan.rows; chunk += ring.step) {
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(ring.empty + 8u * s, ph ^ 1u, err, kSiteProducerEmpty))) break;
+    const long long row0 = chunk * plan.groups;
+    const int rows = static_cast<int>(min(static_cast<long long>(plan.groups), plan.rows - row0));
+    uint8_t* const stage = ring.data + static_cast<size_t>(s) * plan.stage_bytes;
+    const uint32_t bar = ring.full + 8u * s;
+    // lane i < N: matrix i's chunk, where it is one copy; then, matrix by
+    // matrix, the others' rows
+    const int mine = lane < N ? lane : 0;
+    const RowSource& m = in[mine];
+    const bool one = lane < N && m.p && m.packed;
+    const uintptr_t from = one ? first_byte(m, row0, ring.col0) : 0;
+    const RowCopy chunk_copy(m, stage + (one ? m.at : 0), from,
+                             one ? from + static_cast<uint32_t>(rows - 1) * m.pitch + source_bytes(m.size, ring.width) : from);
+    uint32_t bytes = chunk_copy.bytes();
+    bool rest = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) rest = rest || (in[i].p && !in[i].packed);
+    if (rest) {
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1) {
+          __syncwarp();
+          bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);   // releases the elements copied here, too
+          __syncwarp();
+          chunk_copy.issue(bar);
+        }
 #pragma unroll 1
-      for (int i = 0; i < N; ++i) {
-        const RowSource& m = in[i];
-        if (!m.p) continue;
-        const uintptr_t first = first_byte(m, next), last = first + source_bytes(m.size, width);
-        uintptr_t lo, hi;
-        blocks(m, first, last, lo, hi);
-        bytes += static_cast<uint32_t>(hi - lo);
-        if (lo > first || hi < last || lo == hi) {
-          uint8_t* const at = dst + m.at + (first & 15);
-          if (lo == hi) {
-            copy_elements(at, first, last, m.size);
-          } else {
-            copy_elements(at, first, lo, m.size);          // nothing where lo is below first
-            copy_elements(at + (hi - first), hi, last, m.size);
-          }
+        for (int i = 0; i < N; ++i) {
+          const RowSource& r = in[i];
+          if (!r.p || r.packed || lane >= rows) continue;
+          const uintptr_t at = first_byte(r, row0 + lane, ring.col0);
+          const RowCopy copy(r, stage + r.at + static_cast<uint32_t>(lane) * r.pitch, at,
+                             at + source_bytes(r.size, ring.width));
+          if (pass == 0)
+            bytes += copy.bytes();
+          else
+            copy.issue(bar);
         }
       }
-      mbar_arrive_expect_tx(bar, bytes);                   // releases the elements copied here, too
-#pragma unroll 1
-      for (int i = 0; i < N; ++i) {
-        const RowSource& m = in[i];
-        if (!m.p) continue;
-        const uintptr_t first = first_byte(m, next), last = first + source_bytes(m.size, width);
-        uintptr_t lo, hi;
-        blocks(m, first, last, lo, hi);
-        if (lo < hi)
-          bulk_load(smem_addr(dst) + m.at + static_cast<uint32_t>(lo - (first & ~uintptr_t{15})),
-                    reinterpret_cast<const void*>(lo), static_cast<uint32_t>(hi - lo), bar);
-      }
-      ++issued;
+    } else {
+      __syncwarp();
+      bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      chunk_copy.issue(bar);
     }
-    next += step;
-  }
-  // A wait that runs out is recorded, and the thread goes on (the result is
-  // undefined, as the status says): the group's barriers need all of it.  The
-  // one that issues the copies issues no more.
-  __device__ __forceinline__ void wait() {
-    if (!lost && !mbar_wait(bars + 8u * s, ph, err, kSiteTransformFull)) {
-      lost = true;
-      lost_at = taken;
-    }
-  }
-  // The stage has been read: by one thread, after a barrier of the group.
-  __device__ __forceinline__ void refill() {
-    if (!lost) load(s);
-  }
-  __device__ __forceinline__ void advance() {
-    ++taken;
+    issued = min(issued + 1, plan.stages);
     if (++s == plan.stages) {
       s = 0;
       ph ^= 1u;
     }
   }
-  // The issuing thread, at its end: where it gave up, it waits, again with a
-  // limit, for its copies in flight, which would land in memory that is no
-  // longer the kernel's.
-  __device__ __forceinline__ void finish() const {
-    if (!lost) return;
-    for (long long k = lost_at; k < issued; ++k)
-      mbar_wait(bars + 8u * static_cast<uint32_t>(k % plan.stages),
-                static_cast<uint32_t>(k / plan.stages) & 1u, err, kSiteDrainTma);
+  __syncwarp();
+  for (; issued > 0; --issued) {
+    if (--s < 0) {
+      s = plan.stages - 1;
+      ph ^= 1u;
+    }
+    mbar_wait(ring.full + 8u * s, ph, err, kSiteDrainTma);
   }
-  // A matrix's row in the current stage, from its 16-byte boundary on.
-  __device__ __forceinline__ const uint8_t* at(int i) const {
-    return data + static_cast<size_t>(s) * plan.stage_bytes + in[i].at;
+}
+
+// A computing thread's view of the ring.
+struct RingReader {
+  const RingPlace& ring;
+  const RowPlan& plan;
+  unsigned* err;
+  int group, s = 0;
+  uint32_t ph = 0;
+  bool lost = false;
+
+  // A wait that runs out is recorded, and the thread goes on (the result is
+  // undefined, as the status says): its group's barriers need all of it.
+  __device__ __forceinline__ void wait() {
+    if (!lost) lost = !mbar_wait(ring.full + 8u * s, ph, err, kSiteTransformFull);
+  }
+  // The warp has the row in registers.
+  __device__ __forceinline__ void release() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(ring.empty + 8u * s);
+    if (++s == plan.stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+  // The group's row of a matrix in the current stage; what lies `shift` bytes
+  // behind a 16-byte boundary in memory lies so in the stage.
+  __device__ __forceinline__ const uint8_t* at(const RowSource& m, long long row, bool vec) const {
+    const uint8_t* const p = ring.data + static_cast<uint32_t>(s) * plan.stage_bytes + m.at +
+                             static_cast<uint32_t>(group) * m.pitch;
+    if (vec) return p;
+    return p + (static_cast<uint32_t>(first_byte(m, m.packed ? row - group : row, ring.col0)) & 15u);
   }
 };
 
@@ -211,7 +260,7 @@ struct RowPart {
   __device__ __forceinline__ bool in(int i) const { return col(i) < width; }
 
   // The row's elements, 0 for what lies outside it.
-  __device__ __forceinline__ void load(const uint8_t* row, uint32_t shift, Pair (&x)[NP]) const {
+  __device__ __forceinline__ void load(const uint8_t* row, Pair (&x)[NP]) const {
     if constexpr (VEC) {
 #pragma unroll
       for (int v = 0; v < NE / V; ++v) {
@@ -223,7 +272,7 @@ struct RowPart {
         for (int j = 0; j < V / 2; ++j) x[v * (V / 2) + j] = p[j];
       }
     } else {
-      const T* const p = reinterpret_cast<const T*>(row + shift);
+      const T* const p = reinterpret_cast<const T*>(row);
       float f[NE];
 #pragma unroll
       for (int i = 0; i < NE; ++i) f[i] = in(i) ? to_f32(p[col(i)]) : 0.0f;
