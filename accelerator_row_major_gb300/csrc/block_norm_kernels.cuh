@@ -1,0 +1,796 @@
+// The norms at a block's ends, with its gate and residual, and their
+// gradients: the kernels (sm_103a).  Included once per element type.
+//
+//   p = branch, or its norm;  h = alpha residual + beta gate p;  y = norm(h)
+//   hat = (h - mean) rstd, g = dy weight
+//   d = dh + rstd (g - sum(g)/D - hat sum(g hat)/D),  dresidual = alpha d
+//   e = beta d gate,  dgate = beta d p,  dbranch = e, or through p's norm as d
+//
+// Bound by memory traffic: each matrix is read or written once, so a row goes
+// from its load to its results in the registers of the threads that share it
+// (block_rows.cuh), through both norms.  The next rows of all matrices are in
+// flight meanwhile, in a ring that bulk copies fill; vectors over the columns
+// (weights, a gate per channel) lie in shared memory in the order in which the
+// threads hold the columns.  The gradient's grid is persistent: a thread keeps
+// its columns and sums their shares of the vectors' gradients in registers; a
+// second kernel adds the CTAs' sums in order (no atomics).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/gemm_f32_block.h"
+#include "block_norm.h"
+#include "block_rows.cuh"
+#include "device_common.cuh"
+#include "launch.h"
+#include "row_common.cuh"
+
+namespace gemm_f32_impl {
+using namespace gemm_f32_dev;
+
+namespace {
+
+__device__ __forceinline__ Pair both(float x) { return pair_of(x, x); }
+
+template <class T>
+__device__ __forceinline__ bool output_ok(const Output& o, const RowPlan& plan, long long row, unsigned* err) {
+  return GEMM_IN_EXTENT(row * o.ld + plan.width - 1, stored_extent(plan.rows, plan.width, o.ld), err,
+                        kSiteBoundsRows);
+}
+
+// The vectors into shared memory, `slots` values each.
+template <class T, class Part>
+__device__ __forceinline__ void fill_vectors(float* columns, const VectorArgs& v, const RowPlan& plan,
+                                             const RingPlace& ring) {
+#pragma unroll 1
+  for (int i = 0; i < kVectors; ++i)
+    if (v.slot[i] >= 0)
+      fill_columns<T, Part>(columns + v.slot[i] * Part::slots(plan.lanes), v.p[i], v.f32,
+                            i == kWeight || i == kPostWeight ? 1.0f : 0.0f, plan.lanes, ring.col0, ring.width);
+}
+
+// ---------------------------------------------------------------- forward
+template <class T, int NE, bool VEC>
+__global__ void __launch_bounds__(32 * (kRowWarps + 1), 1) block_norm_kernel(const __grid_constant__ BlockArgs a) {
+  using Part = RowPart<T, NE, VEC>;
+  constexpr int NP = Part::NP;
+  extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ RowShared shared;
+  const RowPlan& plan = a.plan;
+  const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
+  const int rank = plan.ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const bool producer = group == plan.groups;
+  const RingPlace ring(plan, smem_rows, rank);
+  if (threadIdx.x == 0) {
+    if (plan.ctas > 1) RowSums::init(shared, plan);
+    ring.init(plan);
+  }
+  __syncthreads();
+  if (plan.ctas > 1) cluster_sync();     // every CTA of the cluster runs
+  grid_launch_dependents();
+  grid_dependency_wait();
+  float* const columns = reinterpret_cast<float*>(smem_rows);
+  if (producer) {
+    produce_rows(a.in, plan, ring, a.err, [&] { __syncthreads(); });
+  } else {
+    fill_vectors<T, Part>(columns, a.vectors, plan, ring);
+    __syncthreads();
+  }
+  const Part mine(t, plan.lanes, ring.width);
+  const float inv = 1.0f / static_cast<float>(plan.width);
+  const auto vector = [&](int v) { return columns + a.vectors.slot[v] * Part::slots(plan.lanes); };
+  RowSums sums = {shared, plan, a.err, group, t, rank};
+  // x around its mean (0 for rms), 1 / its root mean square there.
+  const auto normalise = [&](Pair(&x)[NP], float& mean, float& rstd) {
+    float s[1];
+    mean = 0.0f;
+    if (!a.rms) {
+      Pair sum = 0;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) sum = add2(sum, x[j]);
+      s[0] = sum_of(sum);
+      sums.add<1>(s);
+      mean = s[0] * inv;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) x[j] = add2(x[j], both(-mean));
+      mine.drop(x);
+    }
+    Pair sum = 0;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) sum = fma2(x[j], x[j], sum);
+    s[0] = sum_of(sum);
+    sums.add<1>(s);
+    rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+  };
+  // x rstd times a vector, plus another where it is there
+  const auto scale = [&](Pair(&x)[NP], float rstd, int weight, int bias) {
+    mine.each(vector(weight), [&](int j, Pair w) { x[j] = mul2(mul2(x[j], both(rstd)), w); });
+    if (a.vectors.slot[bias] >= 0) mine.each(vector(bias), [&](int j, Pair w) { x[j] = add2(x[j], w); });
+  };
+
+  RingReader reader = {ring, plan, a.err, group};
+  for (long long row = ring.first * plan.groups + group; !producer && row < plan.rows; row += ring.step * plan.groups) {
+    reader.wait();
+    Pair p[NP], x[NP];
+    float mean, rstd, mean_b = 0.0f, rstd_b = 0.0f;
+    mine.load(reader.at(a.in[kInBranch], row, VEC), p);
+    if (a.post) {
+      normalise(p, mean_b, rstd_b);
+      scale(p, rstd_b, kPostWeight, kPostBias);
+    }
+    if (a.gate == kElementGate) {
+      mine.load(reader.at(a.in[kInGate], row, VEC), x);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) p[j] = mul2(p[j], x[j]);
+    } else if (a.gate == kChannelGate) {
+      mine.each(vector(kGateVector), [&](int j, Pair w) { p[j] = mul2(p[j], w); });
+    }
+    mine.load(reader.at(a.in[kInResidual], row, VEC), x);
+    reader.release();
+#pragma unroll
+    for (int j = 0; j < NP; ++j) x[j] = fma2(p[j], both(a.beta), mul2(x[j], both(a.alpha)));
+    // an h that is an input: all of this row has been read
+    if (a.h.p && output_ok<T>(a.h, plan, row, a.err))
+      mine.store(static_cast<T*>(a.h.p) + row * a.h.ld + ring.col0, x);
+    normalise(x, mean, rstd);
+    scale(x, rstd, kWeight, kBias);
+    if (output_ok<T>(a.y, plan, row, a.err)) mine.store(static_cast<T*>(a.y.p) + row * a.y.ld + ring.col0, x);
+    if (t == 0 && rank == 0 && a.stats) {
+      a.stats[row] = mean;
+      a.stats[plan.rows + row] = rstd;
+      if (a.post) {
+        a.stats[2 * plan.rows + row] = mean_b;
+        a.stats[3 * plan.rows + row] = rstd_b;
+      }
+    }
+  }
+  if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
+}
+
+// ---------------------------------------------------------------- gradient
+// LAYER: around the means; POST: the branch was normed; CHANNEL: a gate per
+// channel (a gate per element is the launch's choice).  What a form does not
+// have costs no registers: with all sums and 16 elements a thread, 80 of them
+// hold sums alone, and 8 warps instead of 12 compute.
+template <int NE, bool LAYER, bool POST, bool CHANNEL>
+constexpr int grad_warps() {
+  return NE * ((LAYER ? 2 : 1) * (POST ? 2 : 1) + (CHANNEL ? 1 : 0)) > 32 ? 8 : kRowWarps;
+}
+
+template <class T, int NE, bool VEC, bool LAYER, bool POST, bool CHANNEL>
+__global__ void __launch_bounds__(32 * (grad_warps<NE, LAYER, POST, CHANNEL>() + 1), 1)
+    block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
+  using Part = RowPart<T, NE, VEC>;
+  constexpr int NP = Part::NP;
+  extern __shared__ __align__(128) uint8_t smem_rows[];
+  __shared__ RowShared shared;
+  const RowPlan& plan = a.plan;
+  const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
+  const int rank = plan.ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const bool producer = group == plan.groups;
+  const RingPlace ring(plan, smem_rows, rank);
+  if (threadIdx.x == 0) {
+    if (plan.ctas > 1) RowSums::init(shared, plan);
+    ring.init(plan);
+  }
+  __syncthreads();
+  if (plan.ctas > 1) cluster_sync();     // every CTA of the cluster runs
+  grid_launch_dependents();
+  grid_dependency_wait();
+  float* const columns = reinterpret_cast<float*>(smem_rows);
+  if (producer) {
+    produce_rows(a.in, plan, ring, a.err, [&] { __syncthreads(); });
+  } else {
+    fill_vectors<T, Part>(columns, a.vectors, plan, ring);
+    __syncthreads();
+  }
+  const Part mine(t, plan.lanes, ring.width);
+  const float inv = 1.0f / static_cast<float>(plan.width);
+  const auto vector = [&](int v) { return columns + a.vectors.slot[v] * Part::slots(plan.lanes); };
+  RowSums sums = {shared, plan, a.err, group, t, rank};
+  const bool gated = CHANNEL || a.gate == kElementGate, branch = POST || gated;
+  Pair total[kSums][NP];
+#pragma unroll
+  for (int k = 0; k < kSums; ++k)
+#pragma unroll
+    for (int j = 0; j < NP; ++j) total[k][j] = 0;
+
+  RingReader reader = {ring, plan, a.err, group};
+  const long long step = ring.step * plan.groups;
+  long long row = producer ? plan.rows : ring.first * plan.groups + group;
+  float stat[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // this row's, loaded under the row before
+  const auto load_stats = [&](long long r) {
+    if (r >= plan.rows) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((k < 2 || POST) && (LAYER || k % 2)) stat[k] = __ldg(a.stats + k * plan.rows + r);
+  };
+  load_stats(row);
+  for (; row < plan.rows; row += step) {
+    reader.wait();
+    const float mean = stat[0], rstd = stat[1], mean_b = stat[2], rstd_b = stat[3];
+    load_stats(row + step);
+    Pair c[NP], g[NP], d[NP];
+    if (a.in[kGradHExponents].p)
+      mine.load_saved(reader.at(a.in[kGradH], row, true), reader.at(a.in[kGradHExponents], row, true), c);
+    else
+      mine.load(reader.at(a.in[kGradH], row, VEC), c);
+    mine.load(reader.at(a.in[kGradDy], row, VEC), g);
+    // c = h - mean in place of hat = c rstd: where rstd is 0 (squares that
+    // overflowed) or c is, hat is 0 and never 0 times infinity
+    Pair sg = 0, sgc = 0;
+    mine.each(vector(kWeight), [&](int j, Pair w) {
+      if (LAYER) {
+        c[j] = add2(c[j], both(-mean));
+        total[kSumBias][j] = add2(total[kSumBias][j], g[j]);
+      }
+      total[kSumWeight][j] = fma2(mul2(g[j], both(rstd)), c[j], total[kSumWeight][j]);
+      g[j] = mul2(g[j], w);
+      if (LAYER) sg = add2(sg, g[j]);
+      sgc = fma2(g[j], c[j], sgc);
+    });
+    // sums of (g - c's share), of g alone for LAYER: the row's share of its mean
+    const auto sum = [&](Pair ones, Pair along, float by, float& c1, float& c2) {
+      const float s = by != 0.0f ? sum_of(along) * by : 0.0f;
+      if constexpr (LAYER) {
+        float v[2] = {sum_of(ones), s};
+        sums.add<2>(v);
+        c1 = -v[0] * inv;
+        c2 = -v[1] * inv * by;
+      } else {
+        float v[1] = {s};
+        sums.add<1>(v);
+        c1 = 0.0f;
+        c2 = -v[0] * inv * by;
+      }
+    };
+    float c1, c2;
+    sum(sg, sgc, rstd, c1, c2);
+    if (a.in[kGradDh].p) {
+      mine.load(reader.at(a.in[kGradDh], row, VEC), d);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) d[j] = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if (LAYER) g[j] = add2(g[j], both(c1));
+      d[j] = fma2(fma2(c[j], both(c2), g[j]), both(rstd), d[j]);
+    }
+    Pair(&b)[NP] = c;
+    if (branch) {
+      if (a.in[kGradBranchExponents].p)
+        mine.load_saved(reader.at(a.in[kGradBranch], row, true), reader.at(a.in[kGradBranchExponents], row, true), b);
+      else
+        mine.load(reader.at(a.in[kGradBranch], row, VEC), b);
+    }
+    Pair(&gate)[NP] = g;
+    if (!CHANNEL && a.gate == kElementGate) mine.load(reader.at(a.in[kGradGate], row, VEC), gate);
+    reader.release();
+    if (a.dresidual.p && output_ok<T>(a.dresidual, plan, row, a.err)) {
+      Pair out[NP];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) out[j] = mul2(d[j], both(a.alpha));
+      mine.store(static_cast<T*>(a.dresidual.p) + row * a.dresidual.ld + ring.col0, out);
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) d[j] = mul2(d[j], both(a.beta));
+    if (branch) {
+      mine.drop(d);
+      if (POST && LAYER) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) b[j] = add2(b[j], both(-mean_b));
+      }
+      if (gated) {
+        Pair p[NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) p[j] = b[j];
+        if (POST) {
+          mine.each(vector(kPostWeight), [&](int j, Pair w) { p[j] = mul2(mul2(p[j], both(rstd_b)), w); });
+          if (LAYER && a.vectors.slot[kPostBias] >= 0)
+            mine.each(vector(kPostBias), [&](int j, Pair w) { p[j] = add2(p[j], w); });
+        }
+        if (CHANNEL) {
+          mine.each(vector(kGateVector), [&](int j, Pair w) {
+            total[kSumGate][j] = fma2(d[j], p[j], total[kSumGate][j]);
+            d[j] = mul2(d[j], w);
+          });
+        } else {
+          if (a.dgate.p && output_ok<T>(a.dgate, plan, row, a.err)) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) p[j] = mul2(d[j], p[j]);
+            mine.store(static_cast<T*>(a.dgate.p) + row * a.dgate.ld + ring.col0, p);
+          }
+#pragma unroll
+          for (int j = 0; j < NP; ++j) d[j] = mul2(d[j], gate[j]);
+        }
+      }
+      if (POST) {
+        Pair se = 0, seb = 0;
+        mine.each(vector(kPostWeight), [&](int j, Pair w) {
+          total[kSumPostWeight][j] = fma2(mul2(d[j], both(rstd_b)), b[j], total[kSumPostWeight][j]);
+          if (LAYER) total[kSumPostBias][j] = add2(total[kSumPostBias][j], d[j]);
+          d[j] = mul2(d[j], w);
+          if (LAYER) se = add2(se, d[j]);
+          seb = fma2(d[j], b[j], seb);
+        });
+        sum(se, seb, rstd_b, c1, c2);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          if (LAYER) d[j] = add2(d[j], both(c1));
+          d[j] = mul2(fma2(b[j], both(c2), d[j]), both(rstd_b));
+        }
+      }
+    }
+    if (a.dbranch.p && output_ok<T>(a.dbranch, plan, row, a.err))
+      mine.store(static_cast<T*>(a.dbranch.p) + row * a.dbranch.ld + ring.col0, d);
+  }
+  if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
+  if (!a.sums) return;
+  // the groups' sums, added in group order: one row of partials per CTA (or
+  // cluster) and vector; what was the ring makes room
+  const int slots = Part::slots(plan.lanes);
+#pragma unroll
+  for (int k = 0; k < kSums; ++k) {
+    const bool there = k == kSumWeight || (k == kSumBias && LAYER) || (k == kSumGate && CHANNEL) ||
+                       (k == kSumPostWeight && POST) || (k == kSumPostBias && POST && LAYER);
+    if (!there || a.sum[k] < 0) continue;
+    __syncthreads();
+    if (!producer) {
+#pragma unroll
+      for (int q = 0; q < NE / 4; ++q) {
+        float4 f;
+        unpair(total[k][2 * q], f.x, f.y);
+        unpair(total[k][2 * q + 1], f.z, f.w);
+        *reinterpret_cast<float4*>(mine.quad(columns + group * slots, q)) = f;
+      }
+    }
+    __syncthreads();
+    float* const to = a.partials +
+                      (static_cast<size_t>(blockIdx.x / plan.ctas) * a.sums + a.sum[k]) * plan.width + ring.col0;
+    for (int slot = threadIdx.x; slot < slots; slot += blockDim.x) {
+      const int col = Part::column_of_slot(slot, plan.lanes);
+      if (col >= ring.width) continue;
+      float v = columns[slot];
+      for (int i = 1; i < plan.groups; ++i) v += columns[i * slots + slot];
+      to[col] = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- rows wider than the ring's
+// A CTA per row that reads its matrices again for each of the row's sums.
+constexpr int kWideThreads = 512;
+
+template <class T>
+__device__ __forceinline__ float element(const RowSource& m, long long row, int d) {
+  return to_f32(reinterpret_cast<const T*>(m.p + row * m.ld)[d]);
+}
+template <class T>
+__device__ __forceinline__ float element(const RowSource& m, const RowSource& exponents, long long row, int d) {
+  if (!exponents.p) return element<T>(m, row, d);
+  const uint32_t code = reinterpret_cast<const uint8_t*>(m.p + row * m.ld)[d];
+  return values_of(code).x *
+         power_of(reinterpret_cast<const uint8_t*>(exponents.p + row * exponents.ld)[d / kSavedBlock]);
+}
+
+// Value d of a vector.
+template <class T>
+__device__ __forceinline__ float vector_at(const VectorArgs& a, int v, int d) {
+  if (a.slot[v] < 0) return 0.0f;
+  if (!a.p[v]) return v == kWeight || v == kPostWeight ? 1.0f : 0.0f;
+  return a.f32 ? __ldg(static_cast<const float*>(a.p[v]) + d) : to_f32(static_cast<const T*>(a.p[v])[d]);
+}
+
+template <int N>
+__device__ __forceinline__ void wide_sum(float (&v)[N], float (&part)[2][kWideThreads / 32]) {
+  warp_sum<N>(v);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) part[i][warp] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = part[i][lane & 15];
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const __grid_constant__ BlockArgs a) {
+  __shared__ float part[2][kWideThreads / 32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int width = a.plan.width;
+  const float inv = 1.0f / static_cast<float>(width);
+  for (long long row = blockIdx.x; row < a.plan.rows; row += gridDim.x) {
+    auto statistics = [&](auto value, float& mean, float& rstd) {
+      float s[1] = {0.0f};
+      mean = 0.0f;
+      if (!a.rms) {
+        for (int d = threadIdx.x; d < width; d += kWideThreads) s[0] += value(d);
+        wide_sum<1>(s, part);
+        mean = s[0] * inv;
+        s[0] = 0.0f;
+      }
+      for (int d = threadIdx.x; d < width; d += kWideThreads) {
+        const float x = value(d) - mean;
+        s[0] = fmaf(x, x, s[0]);
+      }
+      wide_sum<1>(s, part);
+      rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+    };
+    float mean, rstd, mean_b = 0.0f, rstd_b = 0.0f;
+    if (a.post) statistics([&](int d) { return element<T>(a.in[kInBranch], row, d); }, mean_b, rstd_b);
+    auto h = [&](int d) {
+      float p = element<T>(a.in[kInBranch], row, d);
+      if (a.post)
+        p = (p - mean_b) * rstd_b * vector_at<T>(a.vectors, kPostWeight, d) + vector_at<T>(a.vectors, kPostBias, d);
+      if (a.gate == kChannelGate) p *= vector_at<T>(a.vectors, kGateVector, d);
+      if (a.gate == kElementGate) p *= element<T>(a.in[kInGate], row, d);
+      return fmaf(p, a.beta, element<T>(a.in[kInResidual], row, d) * a.alpha);
+    };
+    statistics(h, mean, rstd);
+    // an output that is an input: each thread reads its elements before it writes them
+    for (int d = threadIdx.x; d < width; d += kWideThreads) {
+      const float x = h(d);
+      if (a.h.p && output_ok<T>(a.h, a.plan, row, a.err))
+        static_cast<T*>(a.h.p)[row * a.h.ld + d] = from_f32<T>(x);
+      if (output_ok<T>(a.y, a.plan, row, a.err))
+        static_cast<T*>(a.y.p)[row * a.y.ld + d] = from_f32<T>(
+            (x - mean) * rstd * vector_at<T>(a.vectors, kWeight, d) + vector_at<T>(a.vectors, kBias, d));
+    }
+    if (threadIdx.x == 0 && a.stats) {
+      a.stats[row] = mean;
+      a.stats[a.plan.rows + row] = rstd;
+      if (a.post) {
+        a.stats[2 * a.plan.rows + row] = mean_b;
+        a.stats[3 * a.plan.rows + row] = rstd_b;
+      }
+    }
+  }
+}
+
+// The vectors' gradients are summed in the CTA's own partials.
+template <class T>
+__global__ void __launch_bounds__(kWideThreads) block_norm_grad_wide_kernel(const __grid_constant__ BlockGradArgs a) {
+  __shared__ float part[2][kWideThreads / 32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int width = a.plan.width;
+  const float inv = 1.0f / static_cast<float>(width);
+  for (long long row = blockIdx.x; row < a.plan.rows; row += gridDim.x) {
+    const float mean = a.rms ? 0.0f : a.stats[row], rstd = a.stats[a.plan.rows + row];
+    const float mean_b = a.post && !a.rms ? a.stats[2 * a.plan.rows + row] : 0.0f;
+    const float rstd_b = a.post ? a.stats[3 * a.plan.rows + row] : 0.0f;
+    auto centred = [&](int d) { return element<T>(a.in[kGradH], a.in[kGradHExponents], row, d) - mean; };
+    auto branch = [&](int d) { return element<T>(a.in[kGradBranch], a.in[kGradBranchExponents], row, d) - mean_b; };
+    auto normed = [&](int d) { return element<T>(a.in[kGradDy], row, d) * vector_at<T>(a.vectors, kWeight, d); };
+    auto gate = [&](int d) {
+      return a.gate == kChannelGate   ? vector_at<T>(a.vectors, kGateVector, d)
+             : a.gate == kElementGate ? element<T>(a.in[kGradGate], row, d)
+                                      : 1.0f;
+    };
+    float s[2] = {0.0f, 0.0f};
+    for (int d = threadIdx.x; d < width; d += kWideThreads) {
+      const float g = normed(d);
+      s[0] += g;
+      s[1] = fmaf(g, centred(d), s[1]);
+    }
+    s[1] = rstd != 0.0f ? s[1] * rstd : 0.0f;
+    wide_sum<2>(s, part);
+    const float c1 = a.rms ? 0.0f : -s[0] * inv, c2 = -s[1] * inv * rstd;
+    auto through = [&](int d) {
+      const float dh = a.in[kGradDh].p ? element<T>(a.in[kGradDh], row, d) : 0.0f;
+      return fmaf(fmaf(centred(d), c2, normed(d) + c1), rstd, dh);
+    };
+    float c3 = 0.0f, c4 = 0.0f;
+    if (a.post) {
+      s[0] = s[1] = 0.0f;
+      for (int d = threadIdx.x; d < width; d += kWideThreads) {
+        const float e = through(d) * a.beta * gate(d) * vector_at<T>(a.vectors, kPostWeight, d);
+        s[0] += e;
+        s[1] = fmaf(e, branch(d), s[1]);
+      }
+      s[1] = rstd_b != 0.0f ? s[1] * rstd_b : 0.0f;
+      wide_sum<2>(s, part);
+      c3 = a.rms ? 0.0f : -s[0] * inv;
+      c4 = -s[1] * inv * rstd_b;
+    }
+    // an output that is an input: each thread reads its elements before it writes them
+    for (int d = threadIdx.x; d < width; d += kWideThreads) {
+      const float dy = element<T>(a.in[kGradDy], row, d), c = centred(d), dd = through(d);
+      const float e = dd * a.beta;
+      const float b = a.branch ? branch(d) : 0.0f, by = gate(d), pw = vector_at<T>(a.vectors, kPostWeight, d);
+      const float p = a.post ? b * rstd_b * pw + vector_at<T>(a.vectors, kPostBias, d) : b;
+      auto add = [&](int k, float v) {
+        if (a.sum[k] < 0) return;
+        float* const to = a.partials + (static_cast<size_t>(blockIdx.x) * a.sums + a.sum[k]) * width + d;
+        *to = row == blockIdx.x ? v : *to + v;
+      };
+      add(kSumWeight, dy * rstd * c);
+      add(kSumBias, dy);
+      if (a.gate == kChannelGate) add(kSumGate, e * p);
+      add(kSumPostWeight, e * by * rstd_b * b);
+      add(kSumPostBias, e * by);
+      if (a.dresidual.p && output_ok<T>(a.dresidual, a.plan, row, a.err))
+        static_cast<T*>(a.dresidual.p)[row * a.dresidual.ld + d] = from_f32<T>(dd * a.alpha);
+      if (a.dgate.p && a.gate == kElementGate && output_ok<T>(a.dgate, a.plan, row, a.err))
+        static_cast<T*>(a.dgate.p)[row * a.dgate.ld + d] = from_f32<T>(e * p);
+      const float db = a.post ? rstd_b * fmaf(b, c4, e * by * pw + c3) : e * by;
+      if (a.dbranch.p && output_ok<T>(a.dbranch, a.plan, row, a.err))
+        static_cast<T*>(a.dbranch.p)[row * a.dbranch.ld + d] = from_f32<T>(db);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- vectors' gradients
+// Partial sums of 32 columns of one vector per CTA, added in CTA order: 32
+// chains of every 32nd CTA, then the chains in order.
+struct ColumnArgs {
+  const float* partials;
+  void* out[kSums];                      // by their place in the partials
+  int sums, ctas, width;
+};
+
+template <class WT>
+__global__ void __launch_bounds__(1024) block_columns_kernel(const ColumnArgs a) {
+  __shared__ float chains[32][33];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, chain = threadIdx.x >> 5;
+  const int k = blockIdx.y;
+  const long long d = blockIdx.x * 32LL + lane;
+  float v = 0.0f;
+  if (d < a.width)
+    for (int c = chain; c < a.ctas; c += 32) v += __ldcg(a.partials + (static_cast<size_t>(c) * a.sums + k) * a.width + d);
+  chains[chain][lane] = v;
+  __syncthreads();
+  float s[1] = {chains[lane][chain]};    // lane: the chain
+  warp_sum<1>(s);
+  const long long to = blockIdx.x * 32LL + chain;
+  if (lane == 0 && to < a.width) static_cast<WT*>(a.out[k])[to] = from_f32<WT>(s[0]);
+}
+
+// ---------------------------------------------------------------- host side
+constexpr size_t kMostShared = 220 * 1024;   // dynamic; RowShared fits beside it
+constexpr int kMostStages = 8;
+
+// Lays out the rows of `in` over `warps` warps of lanes of `ne` elements,
+// groups and ring; false where a row is too wide.
+bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ne, int warps, bool aligned, int num_sms,
+               size_t* bytes, int* grid) {
+  for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
+    if (ctas > num_sms) return false;
+    const int slice = ctas == 1 ? plan.width : ((plan.width - 1) / ctas / kSliceUnit + 1) * kSliceUnit;
+    if (slice > warps * 32 * ne) continue;
+    plan.ctas = ctas;
+    plan.slice = slice;
+    plan.lanes = 32 * ((slice - 1) / (32 * ne) + 1);
+    const long long units = num_sms / ctas;
+    plan.groups = static_cast<int>(std::min<long long>(warps * 32 / plan.lanes, (plan.rows - 1) / units + 1));
+    const size_t columns = static_cast<size_t>(vectors) * ne * plan.lanes * sizeof(float);
+    size_t stage = 0, stages = 0;
+    for (;; --plan.groups) {             // two chunks in flight, or fewer groups
+      stage = 0;
+      for (int i = 0; i < n; ++i) {
+        if (!in[i].p) continue;
+        const size_t row = source_bytes(in[i].size, slice);
+        in[i].packed = ctas == 1 && in[i].ld == static_cast<long long>(row);
+        in[i].pitch = static_cast<uint32_t>(in[i].packed ? row : (row + 15) / 16 * 16 + (aligned || in[i].size < 2 ? 0 : 16));
+        in[i].at = static_cast<uint32_t>(stage);
+        stage += (static_cast<size_t>(plan.groups) * in[i].pitch + 15) / 16 * 16 + (in[i].packed && !aligned ? 16 : 0);
+      }
+      stages = columns < kMostShared ? (kMostShared - columns) / (stage + 16) : 0;
+      if (stages >= 2 || plan.groups == 1) break;
+    }
+    if (stages < 2) continue;
+    plan.stages = static_cast<int>(std::min<size_t>(stages, kMostStages));
+    plan.stage_bytes = static_cast<uint32_t>(stage);
+    plan.ring_at = static_cast<uint32_t>(columns);
+    const long long need = (plan.rows - 1) / plan.groups + 1;
+    *grid = static_cast<int>(std::min<long long>(units, need)) * ctas;
+    // the groups' sums take the place of the ring
+    *bytes = std::max(columns + static_cast<size_t>(plan.stages) * (stage + 16),
+                      static_cast<size_t>(plan.groups) * ne * plan.lanes * sizeof(float));
+    return true;
+  }
+  return false;
+}
+
+// A layout's price: what a row takes its threads, by the rows that are worked
+// on at a time.  A row costs a warp some 250 instructions besides 16 for each
+// of its elements (counted: 380 of 8 elements).
+constexpr int kRowCost = 250, kElementCost = 16;
+
+long long price(const RowPlan& plan, int ne) {
+  return (kRowCost + static_cast<long long>(kElementCost) * ne) * plan.ctas * kRowWarps / plan.groups;
+}
+
+constexpr int kMaxDevices = 64;
+
+// Sets a kernel's shared memory up, once per device, and launches it; where
+// CTAs form clusters, with no more of them than run at once (`grid` is
+// reduced to that).
+template <auto Kernel, class Args>
+int launch_rows(const Args& a, int device, int* grid, size_t bytes, cudaStream_t stream) {
+  static std::atomic<int> clusters[kMaxDevices][4];   // at a time, per log2 of their CTAs; 1 for single CTAs
+  const RowPlan& plan = a.plan;
+  std::atomic<int>& kept = clusters[device % kMaxDevices][plan.ctas == 1 ? 0 : plan.ctas == 2 ? 1 : plan.ctas == 4 ? 2 : 3];
+  int most = kept.load();
+  cudaLaunchConfig_t config = {};
+  config.blockDim = dim3(plan.groups * plan.lanes + 32);
+  config.dynamicSmemBytes = bytes;
+  config.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = plan.ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  if (most == 0) {
+    most = 1;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostShared)) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return GEMM_F32_ELAUNCH;
+    }
+    if (plan.ctas > 1) {
+      cudaLaunchConfig_t full = config;
+      full.gridDim = dim3(512 / plan.ctas * plan.ctas);
+      full.dynamicSmemBytes = kMostShared;
+      full.attrs = attr + 1;
+      full.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&most, Kernel, &full) != cudaSuccess || most < 1) {
+        (void)cudaGetLastError();
+        return GEMM_F32_ELAUNCH;
+      }
+    }
+    kept.store(most);
+  }
+  if (plan.ctas > 1) *grid = std::min(*grid, most * plan.ctas);
+  config.gridDim = dim3(*grid);
+  config.attrs = attr;
+  config.numAttrs = plan.ctas > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&config, Kernel, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GEMM_F32_ELAUNCH;
+  }
+  return GEMM_F32_OK;
+}
+
+template <class Kernel, class Args>
+int launch_plain(Kernel kernel, dim3 grid, int threads, cudaStream_t stream, const Args& a) {
+  if (launch_dependent(kernel, grid, dim3(threads), 0, stream, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GEMM_F32_ELAUNCH;
+  }
+  return GEMM_F32_OK;
+}
+
+// A row layout that a call may take.
+template <int N>
+struct Layout {
+  RowPlan plan;
+  RowSource in[N];
+  size_t bytes = 0;
+  int grid = 0, ne = 0;
+};
+
+// The cheapest of the layouts with `ne[i]` elements a thread on `warps[i]`
+// warps; ne 0: there is none.
+template <int N, int K>
+Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], const int (&warps)[K],
+                      const BlockLaunch& l) {
+  Layout<N> best = {};
+  long long least = 0;
+  for (int i = 0; i < K; ++i) {
+    Layout<N> c = {};
+    c.plan = plan;
+    std::copy(in, in + N, c.in);
+    c.ne = ne[i];
+    if (!plan_rows(c.plan, c.in, N, l.vectors, ne[i], warps[i], l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
+    const long long cost = price(c.plan, ne[i]);
+    if (best.ne == 0 || cost < least) {
+      best = c;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <class T, int NE>
+int forward_form(const BlockArgs& a, const BlockLaunch& l, Layout<kInputs>& best) {
+  return l.aligned ? launch_rows<block_norm_kernel<T, NE, true>>(a, l.device, &best.grid, best.bytes, l.stream)
+                   : launch_rows<block_norm_kernel<T, NE, false>>(a, l.device, &best.grid, best.bytes, l.stream);
+}
+
+template <class T>
+int forward(BlockArgs& a, const BlockLaunch& l) {
+  const int ne[3] = {8, 16, 32}, warps[3] = {kRowWarps, kRowWarps, kRowWarps};
+  Layout<kInputs> best = best_layout(a.plan, a.in, ne, warps, l);
+  ++*l.launches;
+  if (best.ne == 0) {
+    *l.kernel = "block_norm_wide_kernel";
+    return launch_plain(block_norm_wide_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>(a.plan.rows, 4LL * l.num_sms))),
+                        kWideThreads, l.stream, a);
+  }
+  *l.kernel = "block_norm_kernel";
+  a.plan = best.plan;
+  std::copy(best.in, best.in + kInputs, a.in);
+  if (best.ne == 8) return forward_form<T, 8>(a, l, best);
+  return best.ne == 16 ? forward_form<T, 16>(a, l, best) : forward_form<T, 32>(a, l, best);
+}
+
+template <class T, int NE, bool LAYER, bool POST, bool CHANNEL>
+int gradient_form(const BlockGradArgs& a, const BlockLaunch& l, Layout<kGradInputs>& best) {
+  return l.aligned
+             ? launch_rows<block_norm_grad_kernel<T, NE, true, LAYER, POST, CHANNEL>>(a, l.device, &best.grid, best.bytes, l.stream)
+             : launch_rows<block_norm_grad_kernel<T, NE, false, LAYER, POST, CHANNEL>>(a, l.device, &best.grid, best.bytes, l.stream);
+}
+
+// f with the three choices as template arguments.
+template <class F>
+int with_form(bool layer, bool post, bool channel, F f) {
+  const auto third = [&](auto x, auto y) { return channel ? f(x, y, std::true_type{}) : f(x, y, std::false_type{}); };
+  const auto second = [&](auto x) { return post ? third(x, std::true_type{}) : third(x, std::false_type{}); };
+  return layer ? second(std::true_type{}) : second(std::false_type{});
+}
+
+template <class T>
+int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLaunch& l) {
+  ColumnArgs c = {};
+  c.width = a.plan.width;
+  for (int k = 0; k < kSums; ++k) {
+    a.sum[k] = vectors_out[k] ? a.sums++ : -1;
+    if (vectors_out[k]) c.out[a.sum[k]] = vectors_out[k];
+  }
+  int rc = GEMM_F32_OK;
+  *l.kernel = "block_columns_kernel";
+  if (a.plan.rows > 0) {
+    rc = with_form(!a.rms, a.post, a.gate == kChannelGate, [&](auto layer, auto post, auto channel) -> int {
+      constexpr bool kLayer = decltype(layer)::value, kPost = decltype(post)::value, kChannel = decltype(channel)::value;
+      const int ne[2] = {8, 16}, warps[2] = {grad_warps<8, kLayer, kPost, kChannel>(), grad_warps<16, kLayer, kPost, kChannel>()};
+      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, warps, l);
+      c.ctas = best.ne ? best.grid / best.plan.ctas : static_cast<int>(std::min<long long>(a.plan.rows, 2LL * l.num_sms));
+      if (a.sums) {
+        a.partials = static_cast<float*>(acquire_scratch(
+            l.device, l.stream, sizeof(float) * static_cast<size_t>(c.ctas) * a.sums * a.plan.width));
+        if (!a.partials) return GEMM_F32_ESCRATCH;
+      }
+      ++*l.launches;
+      if (best.ne == 0) {
+        *l.kernel = "block_norm_grad_wide_kernel";
+        return launch_plain(block_norm_grad_wide_kernel<T>, dim3(c.ctas), kWideThreads, l.stream, a);
+      }
+      *l.kernel = "block_norm_grad_kernel";
+      a.plan = best.plan;
+      std::copy(best.in, best.in + kGradInputs, a.in);
+      const int got = best.ne == 8 ? gradient_form<T, 8, kLayer, kPost, kChannel>(a, l, best)
+                                   : gradient_form<T, 16, kLayer, kPost, kChannel>(a, l, best);
+      c.ctas = best.grid / best.plan.ctas;
+      return got;
+    });
+  }
+  if (rc == GEMM_F32_OK && a.sums) {
+    c.partials = a.partials;
+    c.sums = a.sums;
+    const dim3 blocks(static_cast<unsigned>((c.width + 31LL) / 32), a.sums);
+    rc = l.weights_f32 ? launch_plain(block_columns_kernel<float>, blocks, 1024, l.stream, c)
+                       : launch_plain(block_columns_kernel<T>, blocks, 1024, l.stream, c);
+    ++*l.launches;
+  }
+  return rc;
+}
+
+}  // namespace
+}  // namespace gemm_f32_impl

@@ -20,6 +20,7 @@
 
 #include <cstdint>
 
+#include "block_norm.h"
 #include "device_common.cuh"
 #include "pair_common.cuh"
 #include "row_common.cuh"
@@ -31,33 +32,6 @@ using namespace gemm_f32_dev;
 namespace {
 
 using bf16 = __nv_bfloat16;
-
-constexpr int kRowThreads = 512;         // that compute
-constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kAllThreads = kRowThreads + 32;
-constexpr int kMostCtas = 8;             // of a cluster
-constexpr int kSliceUnit = 512;          // columns: their exponents fill 16 bytes
-
-// One matrix that a row is read from.  size: bytes per element, or 0 for the
-// exponents of 8-bit rows (a byte per 32 columns).
-struct RowSource {
-  const char* p;                         // null: not there
-  const char* end;                       // one past the last byte that may be read
-  long long ld;                          // bytes from row to row
-  int size;
-  uint32_t at;                           // of its chunk within a stage
-  uint32_t pitch;                        // there, from row to row: ld where `packed`
-  int packed;                            // rows one behind the other: a chunk is one copy
-};
-
-// How a launch lays out its rows.
-struct RowPlan {
-  int width, slice;                      // columns of a row, of a CTA's part
-  int lanes, groups, stages, ctas;
-  uint32_t stage_bytes;
-  uint32_t ring_at;                      // in dynamic shared memory, behind the weights
-  long long rows;
-};
 
 __host__ __device__ __forceinline__ uint32_t source_bytes(int size, int cols) {
   return size ? static_cast<uint32_t>(size) * cols : static_cast<uint32_t>(cols + kSavedBlock - 1) / kSavedBlock;
@@ -136,14 +110,19 @@ struct RowCopy {
 // The producer warp's work: all of the CTA's chunks, `stages` of them in
 // flight.  It gives up at a wait that runs out (recorded), and in any case
 // waits, with a limit, for its last copies: none lands in memory that is no
-// longer the kernel's.
-template <int N>
+// longer the kernel's.  filled(): a barrier of the CTA, behind the first copies.
+template <int N, class F>
 __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const RowPlan& plan, const RingPlace& ring,
-                                             unsigned* err) {
+                                             unsigned* err, F filled) {
+  bool met = false;                      // the others, who fill the vectors under the first copies
   const int lane = threadIdx.x & 31;
   int s = 0, issued = 0;
   uint32_t ph = 0;
   for (long long chunk = ring.first; chunk * plan.groups < plan.rows; chunk += ring.step) {
+    if (!met && issued == plan.stages) {
+      filled();
+      met = true;
+    }
     if (!__all_sync(0xFFFFFFFFu, mbar_wait(ring.empty + 8u * s, ph ^ 1u, err, kSiteProducerEmpty))) break;
     const long long row0 = chunk * plan.groups;
     const int rows = static_cast<int>(min(static_cast<long long>(plan.groups), plan.rows - row0));
@@ -196,6 +175,7 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
       ph ^= 1u;
     }
   }
+  if (!met) filled();
   __syncwarp();
   for (; issued > 0; --issued) {
     if (--s < 0) {
@@ -356,22 +336,24 @@ struct RowPart {
     return column(quad % lanes, quad / lanes * 4 + slot % 4, lanes);
   }
   __device__ __forceinline__ float* quad(float* values, int q) const { return values + 4 * (q * lanes + t); }
-  __device__ __forceinline__ void load_columns(const float* values, Pair (&w)[NP]) const {
+  // Calls f(j, w) for every pair j of elements with the pair's two values.
+  template <class F>
+  __device__ __forceinline__ void each(const float* values, F f) const {
 #pragma unroll
     for (int q = 0; q < NE / 4; ++q) {
-      const float4 f = *reinterpret_cast<const float4*>(values + 4 * (q * lanes + t));
-      w[2 * q] = pair_of(f.x, f.y);
-      w[2 * q + 1] = pair_of(f.z, f.w);
+      const float4 v = *reinterpret_cast<const float4*>(values + 4 * (q * lanes + t));
+      f(2 * q, pair_of(v.x, v.y));
+      f(2 * q + 1, pair_of(v.z, v.w));
     }
   }
 };
 
 // A vector of `width` values (fp32, or T where `f32` is not set; null: `none`)
-// from column col0 on, into slots.  All threads of the CTA.
+// from column col0 on, into slots.  All threads of the CTA but the producer's.
 template <class T, class Part>
 __device__ __forceinline__ void fill_columns(float* values, const void* p, bool f32, float none, int lanes, int col0,
                                              int width) {
-  for (int slot = threadIdx.x; slot < Part::slots(lanes); slot += blockDim.x) {
+  for (int slot = threadIdx.x; slot < Part::slots(lanes); slot += blockDim.x - 32) {
     const int c = Part::column_of_slot(slot, lanes);
     float v = 0.0f;
     if (c < width)
@@ -383,62 +365,94 @@ __device__ __forceinline__ void fill_columns(float* values, const void* p, bool 
 }
 
 // ---------------------------------------------------------------- sums over a row
+struct RowShared {
+  float2 warps[2][kRowWarps];            // two sets of buffers, which take turns
+  float2 ctas[2][kRowWarps][kMostCtas];  // of each group
+  uint64_t bars[2][kRowWarps];
+};
+
 // Sums of one or two values over the threads of a group and, with a cluster,
-// over its CTAs (which have one group each); every thread gets them.  Two sets
-// of buffers take turns: one is written again only after a barrier that every
-// reader has passed.  CTAs exchange theirs by asynchronous stores that a
-// barrier at the destination counts, and add them in order.
+// over the CTAs that share its row; every thread gets them.  A set of buffers
+// is written again only after a barrier that every reader has passed.  CTAs
+// exchange theirs by asynchronous stores that a barrier at the destination
+// counts, and add them in order: a barrier of the cluster would wait for every
+// store in flight.
 struct RowSums {
-  float (*part)[2][kRowWarps];           // [2]: of the warps
-  float2 (*shared)[kMostCtas];           // [2]: of the CTAs
-  uint32_t bars;                         // 2
+  RowShared& shared;
+  const RowPlan& plan;
   unsigned* err;
-  int group, lanes, ctas, rank;
+  int group, t, rank;
   uint32_t flip = 0, round = 0;
   bool lost = false;
 
-  __device__ __forceinline__ void barrier() const {
-    if (lanes > 32)
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(lanes) : "memory");
-    else
-      __syncwarp();
+  // One thread, before the CTA's first barrier.
+  static __device__ __forceinline__ void init(RowShared& shared, const RowPlan& plan) {
+    for (int f = 0; f < 2; ++f)
+      for (int i = 0; i < plan.groups; ++i) mbar_init(smem_addr(&shared.bars[f][i]), 1);
   }
-
   template <int N>
   __device__ __forceinline__ void add(float (&v)[N]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = lanes >> 5;
-    warp_sum<N>(v);
-    if (warps > 1) {
-      if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) part[flip][i][warp] = v[i];
-      barrier();
-      const int j = lane & 15;
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = j < warps ? part[flip][i][group * warps + j] : 0.0f;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+    static_assert(N == 1 || N == 2, "one or two values");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = plan.lanes >> 5;
+    float x;                             // N == 2: lanes below 16 sum the first value, the others the second
+    if constexpr (N == 2) {
+      x = (lane < 16 ? v[0] : v[1]) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? v[1] : v[0], 16);
     } else {
-      barrier();
+      x = v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
     }
-    if (ctas > 1) {
-      const int t = threadIdx.x;
-      if (t == 0) mbar_arrive_expect_tx(bars + 8u * flip, ctas * 8u);
-      if (t < ctas)
-        store_async(map_rank(smem_addr(&shared[flip][rank]), static_cast<uint32_t>(t)), v[0], N > 1 ? v[N - 1] : 0.0f,
-                    map_rank(bars + 8u * flip, static_cast<uint32_t>(t)));
-      if (!lost) lost = !mbar_wait_cluster(bars + 8u * flip, round, err, kSiteTransformFull);
-      round ^= flip;                     // both have been waited for
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.0f;
-      for (int r = 0; r < ctas; ++r) {
-        v[0] += shared[flip][r].x;
-        if (N > 1) v[N - 1] += shared[flip][r].y;
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    if (warps > 1) {
+      if (lane % 16 == 0 && (N == 2 || lane == 0)) (&shared.warps[flip][warp].x)[lane / 16] = x;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(plan.lanes) : "memory");
+      const float2* const of = shared.warps[flip] + group * warps;
+      if (warps <= 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= warps) break;
+          const float2 f = of[j];
+          v[0] += f.x;
+          if (N == 2) v[N - 1] += f.y;
+        }
+      } else {
+        const int j = lane & 15;
+        const float2 f = j < warps ? of[j] : make_float2(0.0f, 0.0f);
+        v[0] = f.x;
+        if (N == 2) v[N - 1] = f.y;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
       }
+    } else if constexpr (N == 2) {
+      v[0] = __shfl_sync(0xFFFFFFFFu, x, 0);
+      v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
+    } else {
+      v[0] = x;
     }
+    if (plan.ctas > 1) exchange<N>(v);
     flip ^= 1u;
+  }
+
+ private:
+  template <int N>
+  __device__ __forceinline__ void exchange(float (&v)[N]) {
+    const uint32_t bar = smem_addr(&shared.bars[flip][group]);
+    if (t == 0) mbar_arrive_expect_tx(bar, plan.ctas * 8u);
+    if (t < plan.ctas)
+      store_async(map_rank(smem_addr(&shared.ctas[flip][group][rank]), static_cast<uint32_t>(t)), v[0],
+                  N > 1 ? v[N - 1] : 0.0f, map_rank(bar, static_cast<uint32_t>(t)));
+    if (!lost) lost = !mbar_wait_cluster(bar, round, err, kSiteTransformFull);
+    round ^= flip;                       // both have been waited for
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    for (int r = 0; r < plan.ctas; ++r) {
+      const float2 f = shared.ctas[flip][group][r];
+      v[0] += f.x;
+      if (N > 1) v[N - 1] += f.y;
+    }
   }
 };
 
