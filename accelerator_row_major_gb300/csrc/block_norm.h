@@ -11,9 +11,11 @@
 
 namespace gemm_f32_impl {
 
-constexpr int kRowWarps = 12;            // that compute, at most: with the producer 13, four for each
-                                         // quarter of an SM, which leaves 128 registers a thread
+constexpr int kRowWarps = 16;            // that compute, at most
+constexpr int kForwardWarps = 12;        // in the forward pass: with the producer 13, four for each quarter
+                                         // of an SM, which leaves 128 registers a thread
 constexpr int kMostCtas = 8;             // of a cluster
+constexpr int kStats = 4;                // per row: mean and rstd of h, of the branch
 constexpr int kSliceUnit = 512;          // columns: their exponents fill 16 bytes
 
 // One matrix that a row is read from.  size: bytes per element, or 0 for the
@@ -34,6 +36,7 @@ struct RowPlan {
   int lanes, groups, stages, ctas;
   uint32_t stage_bytes;
   uint32_t ring_at;                      // in dynamic shared memory, behind the weights
+  uint32_t stats_at;                     // of the rows' statistics within a stage; 0: they do not come this way
   long long rows;
 };
 

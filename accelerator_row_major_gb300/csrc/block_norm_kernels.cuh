@@ -44,28 +44,30 @@ __device__ __forceinline__ bool output_ok(const Output& o, const RowPlan& plan, 
                         kSiteBoundsRows);
 }
 
-// The vectors into shared memory, `slots` values each.
+// The vectors into shared memory, by the threads that compute.
 template <class T, class Part>
 __device__ __forceinline__ void fill_vectors(float* columns, const VectorArgs& v, const RowPlan& plan,
                                              const RingPlace& ring) {
+  const int threads = plan.groups * plan.lanes;
+  if (static_cast<int>(threadIdx.x) >= threads) return;
 #pragma unroll 1
   for (int i = 0; i < kVectors; ++i)
     if (v.slot[i] >= 0)
       fill_columns<T, Part>(columns + v.slot[i] * Part::slots(plan.lanes), v.p[i], v.f32,
-                            i == kWeight || i == kPostWeight ? 1.0f : 0.0f, plan.lanes, ring.col0, ring.width);
+                            i == kWeight || i == kPostWeight ? 1.0f : 0.0f, plan.lanes, threads, ring.col0, ring.width);
 }
 
 // ---------------------------------------------------------------- forward
 template <class T, int NE, bool VEC>
-__global__ void __launch_bounds__(32 * (kRowWarps + 1), 1) block_norm_kernel(const __grid_constant__ BlockArgs a) {
+__global__ void __launch_bounds__(32 * (kForwardWarps + 1), 1) block_norm_kernel(const __grid_constant__ BlockArgs a) {
   using Part = RowPart<T, NE, VEC>;
-  constexpr int NP = Part::NP;
+  constexpr int NP = Part::NP, NC = Part::NC, CP = Part::CP;
   extern __shared__ __align__(128) uint8_t smem_rows[];
   __shared__ RowShared shared;
   const RowPlan& plan = a.plan;
   const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
   const int rank = plan.ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const bool producer = group == plan.groups;
+  const bool producer = group == plan.groups;            // the last warp
   const RingPlace ring(plan, smem_rows, rank);
   if (threadIdx.x == 0) {
     if (plan.ctas > 1) RowSums::init(shared, plan);
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(32 * (kRowWarps + 1), 1) block_norm_kernel(con
   grid_dependency_wait();
   float* const columns = reinterpret_cast<float*>(smem_rows);
   if (producer) {
-    produce_rows(a.in, plan, ring, a.err, [&] { __syncthreads(); });
+    produce_rows(a.in, plan, ring, nullptr, 0u, a.err, [&] { __syncthreads(); });
   } else {
     fill_vectors<T, Part>(columns, a.vectors, plan, ring);
     __syncthreads();
@@ -98,8 +100,12 @@ __global__ void __launch_bounds__(32 * (kRowWarps + 1), 1) block_norm_kernel(con
       sums.add<1>(s);
       mean = s[0] * inv;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) x[j] = add2(x[j], both(-mean));
-      mine.drop(x);
+      for (int v = 0; v < NC; ++v) {
+        Pair(&c)[CP] = *reinterpret_cast<Pair(*)[CP]>(&x[v * CP]);
+#pragma unroll
+        for (int j = 0; j < CP; ++j) c[j] = add2(c[j], both(-mean));
+        mine.drop(v, c);
+      }
     }
     Pair sum = 0;
 #pragma unroll
@@ -108,39 +114,61 @@ __global__ void __launch_bounds__(32 * (kRowWarps + 1), 1) block_norm_kernel(con
     sums.add<1>(s);
     rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
   };
-  // x rstd times a vector, plus another where it is there
-  const auto scale = [&](Pair(&x)[NP], float rstd, int weight, int bias) {
-    mine.each(vector(weight), [&](int j, Pair w) { x[j] = mul2(mul2(x[j], both(rstd)), w); });
-    if (a.vectors.slot[bias] >= 0) mine.each(vector(bias), [&](int j, Pair w) { x[j] = add2(x[j], w); });
+  // a chunk of x rstd times a vector, plus another where it is there
+  const auto scale = [&](int v, Pair(&x)[CP], float rstd, int weight, int bias) {
+    Pair w[CP];
+    mine.columns(vector(weight), v, w);
+#pragma unroll
+    for (int j = 0; j < CP; ++j) x[j] = mul2(mul2(x[j], both(rstd)), w[j]);
+    if (a.vectors.slot[bias] < 0) return;
+    mine.columns(vector(bias), v, w);
+#pragma unroll
+    for (int j = 0; j < CP; ++j) x[j] = add2(x[j], w[j]);
   };
+  const auto chunk = [](Pair(&x)[NP], int v) -> Pair(&)[CP] { return *reinterpret_cast<Pair(*)[CP]>(&x[v * CP]); };
 
   RingReader reader = {ring, plan, a.err, group};
   for (long long row = ring.first * plan.groups + group; !producer && row < plan.rows; row += ring.step * plan.groups) {
     reader.wait();
-    Pair p[NP], x[NP];
+    Pair x[NP];
     float mean, rstd, mean_b = 0.0f, rstd_b = 0.0f;
-    mine.load(reader.at(a.in[kInBranch], row, VEC), p);
-    if (a.post) {
-      normalise(p, mean_b, rstd_b);
-      scale(p, rstd_b, kPostWeight, kPostBias);
-    }
-    if (a.gate == kElementGate) {
-      mine.load(reader.at(a.in[kInGate], row, VEC), x);
+    const uint8_t* const branch = reader.at(a.in[kInBranch], row, VEC);
+    const uint8_t* const residual = reader.at(a.in[kInResidual], row, VEC);
+    const uint8_t* const gate = a.gate == kElementGate ? reader.at(a.in[kInGate], row, VEC) : nullptr;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) p[j] = mul2(p[j], x[j]);
-    } else if (a.gate == kChannelGate) {
-      mine.each(vector(kGateVector), [&](int j, Pair w) { p[j] = mul2(p[j], w); });
+    for (int v = 0; v < NC; ++v) mine.load(branch, v, chunk(x, v));
+    if (a.post) normalise(x, mean_b, rstd_b);
+#pragma unroll
+    for (int v = 0; v < NC; ++v) {
+      Pair(&p)[CP] = chunk(x, v);
+      Pair w[CP];
+      if (a.post) scale(v, p, rstd_b, kPostWeight, kPostBias);
+      if (a.gate != kNoGate) {
+        if (a.gate == kElementGate)
+          mine.load(gate, v, w);
+        else
+          mine.columns(vector(kGateVector), v, w);
+#pragma unroll
+        for (int j = 0; j < CP; ++j) p[j] = mul2(p[j], w[j]);
+      }
+      mine.load(residual, v, w);
+#pragma unroll
+      for (int j = 0; j < CP; ++j) p[j] = fma2(p[j], both(a.beta), mul2(w[j], both(a.alpha)));
     }
-    mine.load(reader.at(a.in[kInResidual], row, VEC), x);
     reader.release();
-#pragma unroll
-    for (int j = 0; j < NP; ++j) x[j] = fma2(p[j], both(a.beta), mul2(x[j], both(a.alpha)));
     // an h that is an input: all of this row has been read
-    if (a.h.p && output_ok<T>(a.h, plan, row, a.err))
-      mine.store(static_cast<T*>(a.h.p) + row * a.h.ld + ring.col0, x);
+    if (a.h.p && output_ok<T>(a.h, plan, row, a.err)) {
+#pragma unroll
+      for (int v = 0; v < NC; ++v) mine.store(static_cast<T*>(a.h.p) + row * a.h.ld + ring.col0, v, chunk(x, v));
+    }
     normalise(x, mean, rstd);
-    scale(x, rstd, kWeight, kBias);
-    if (output_ok<T>(a.y, plan, row, a.err)) mine.store(static_cast<T*>(a.y.p) + row * a.y.ld + ring.col0, x);
+    if (output_ok<T>(a.y, plan, row, a.err)) {
+#pragma unroll
+      for (int v = 0; v < NC; ++v) {
+        scale(v, chunk(x, v), rstd, kWeight, kBias);
+        mine.store(static_cast<T*>(a.y.p) + row * a.y.ld + ring.col0, v, chunk(x, v));
+      }
+    }
     if (t == 0 && rank == 0 && a.stats) {
       a.stats[row] = mean;
       a.stats[plan.rows + row] = rstd;
@@ -156,24 +184,25 @@ __global__ void __launch_bounds__(32 * (kRowWarps + 1), 1) block_norm_kernel(con
 // ---------------------------------------------------------------- gradient
 // LAYER: around the means; POST: the branch was normed; CHANNEL: a gate per
 // channel (a gate per element is the launch's choice).  What a form does not
-// have costs no registers: with all sums and 16 elements a thread, 80 of them
-// hold sums alone, and 8 warps instead of 12 compute.
-template <int NE, bool LAYER, bool POST, bool CHANNEL>
-constexpr int grad_warps() {
-  return NE * ((LAYER ? 2 : 1) * (POST ? 2 : 1) + (CHANNEL ? 1 : 0)) > 32 ? 8 : kRowWarps;
-}
+// have costs no registers.  16 warps compute with 112 registers a thread, of
+// which the warps beside the producer leave them theirs: with the producer as
+// a 17th warp of a plain launch there would be 96.
+constexpr int kProducerThreads = 128;    // a warpgroup, whose first warp works
+constexpr int kProducerRegisters = 32, kComputeRegisters = 112;
+static_assert(kProducerThreads * kProducerRegisters + 32 * kRowWarps * kComputeRegisters <=
+                  96 * (kProducerThreads + 32 * kRowWarps),
+              "registers of a launch of 96 a thread");
+constexpr int kComputeBarrier = 15;      // of the threads that compute; no group has it (at most 8 groups meet at theirs)
 
 template <class T, int NE, bool VEC, bool LAYER, bool POST, bool CHANNEL>
-__global__ void __launch_bounds__(32 * (grad_warps<NE, LAYER, POST, CHANNEL>() + 1), 1)
+__global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
   using Part = RowPart<T, NE, VEC>;
-  constexpr int NP = Part::NP;
+  constexpr int NP = Part::NP, NC = Part::NC, CP = Part::CP;
   extern __shared__ __align__(128) uint8_t smem_rows[];
   __shared__ RowShared shared;
   const RowPlan& plan = a.plan;
-  const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
   const int rank = plan.ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const bool producer = group == plan.groups;
   const RingPlace ring(plan, smem_rows, rank);
   if (threadIdx.x == 0) {
     if (plan.ctas > 1) RowSums::init(shared, plan);
@@ -183,13 +212,21 @@ __global__ void __launch_bounds__(32 * (grad_warps<NE, LAYER, POST, CHANNEL>() +
   if (plan.ctas > 1) cluster_sync();     // every CTA of the cluster runs
   grid_launch_dependents();
   grid_dependency_wait();
-  float* const columns = reinterpret_cast<float*>(smem_rows);
-  if (producer) {
-    produce_rows(a.in, plan, ring, a.err, [&] { __syncthreads(); });
-  } else {
-    fill_vectors<T, Part>(columns, a.vectors, plan, ring);
-    __syncthreads();
+  if (threadIdx.x >= blockDim.x - kProducerThreads) {
+    // ------------------------------------------------------------ producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegisters));
+    if (threadIdx.x < blockDim.x - kProducerThreads + 32)
+      produce_rows(a.in, plan, ring, a.stats, (LAYER ? 3u : 2u) * (POST ? 5u : 1u), a.err, [&] { __syncthreads(); });
+    else
+      __syncthreads();
+    if (plan.ctas > 1) cluster_sync();
+    return;
   }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegisters));
+  const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
+  float* const columns = reinterpret_cast<float*>(smem_rows);
+  fill_vectors<T, Part>(columns, a.vectors, plan, ring);
+  __syncthreads();
   const Part mine(t, plan.lanes, ring.width);
   const float inv = 1.0f / static_cast<float>(plan.width);
   const auto vector = [&](int v) { return columns + a.vectors.slot[v] * Part::slots(plan.lanes); };
@@ -203,40 +240,43 @@ __global__ void __launch_bounds__(32 * (grad_warps<NE, LAYER, POST, CHANNEL>() +
 
   RingReader reader = {ring, plan, a.err, group};
   const long long step = ring.step * plan.groups;
-  long long row = producer ? plan.rows : ring.first * plan.groups + group;
-  float stat[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // this row's, loaded under the row before
-  const auto load_stats = [&](long long r) {
-    if (r >= plan.rows) return;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if ((k < 2 || POST) && (LAYER || k % 2)) stat[k] = __ldg(a.stats + k * plan.rows + r);
-  };
-  load_stats(row);
+  long long row = group < plan.groups ? ring.first * plan.groups + group : plan.rows;
   for (; row < plan.rows; row += step) {
     reader.wait();
-    const float mean = stat[0], rstd = stat[1], mean_b = stat[2], rstd_b = stat[3];
-    load_stats(row + step);
-    Pair c[NP], g[NP], d[NP];
-    if (a.in[kGradHExponents].p)
-      mine.load_saved(reader.at(a.in[kGradH], row, true), reader.at(a.in[kGradHExponents], row, true), c);
-    else
-      mine.load(reader.at(a.in[kGradH], row, VEC), c);
-    mine.load(reader.at(a.in[kGradDy], row, VEC), g);
+    const float4 stats = reader.stats();
+    const float mean = stats.x, rstd = stats.y, mean_b = stats.z, rstd_b = stats.w;
     // c = h - mean in place of hat = c rstd: where rstd is 0 (squares that
     // overflowed) or c is, hat is 0 and never 0 times infinity
-    Pair sg = 0, sgc = 0;
-    mine.each(vector(kWeight), [&](int j, Pair w) {
-      if (LAYER) {
-        c[j] = add2(c[j], both(-mean));
-        total[kSumBias][j] = add2(total[kSumBias][j], g[j]);
+    Pair c[NP], g[NP], sg = 0, sgc = 0;
+    {
+      const uint8_t* const dy = reader.at(a.in[kGradDy], row, VEC);
+      const bool saved = a.in[kGradHExponents].p != nullptr;
+      const uint8_t* const h = reader.at(a.in[kGradH], row, VEC || saved);
+      const uint8_t* const exponents = saved ? reader.at(a.in[kGradHExponents], row, true) : nullptr;
+#pragma unroll
+      for (int v = 0; v < NC; ++v) {
+        Pair x[CP], y[CP], w[CP];
+        if (saved)
+          mine.load_saved(h, exponents, v, x);
+        else
+          mine.load(h, v, x);
+        mine.load(dy, v, y);
+        mine.columns(vector(kWeight), v, w);
+#pragma unroll
+        for (int k = 0; k < CP; ++k) {
+          const int j = v * CP + k;
+          c[j] = LAYER ? add2(x[k], both(-mean)) : x[k];
+          total[kSumWeight][j] = fma2(mul2(y[k], both(rstd)), c[j], total[kSumWeight][j]);
+          if (LAYER) total[kSumBias][j] = add2(total[kSumBias][j], y[k]);
+          g[j] = mul2(y[k], w[k]);
+          if (LAYER) sg = add2(sg, g[j]);
+          sgc = fma2(g[j], c[j], sgc);
+        }
       }
-      total[kSumWeight][j] = fma2(mul2(g[j], both(rstd)), c[j], total[kSumWeight][j]);
-      g[j] = mul2(g[j], w);
-      if (LAYER) sg = add2(sg, g[j]);
-      sgc = fma2(g[j], c[j], sgc);
-    });
-    // sums of (g - c's share), of g alone for LAYER: the row's share of its mean
-    const auto sum = [&](Pair ones, Pair along, float by, float& c1, float& c2) {
+    }
+    // a norm's two means over the row: of its gradients and, along hat, of
+    // their products, with the factors that they get
+    const auto means = [&](Pair ones, Pair along, float by, float& c1, float& c2) {
       const float s = by != 0.0f ? sum_of(along) * by : 0.0f;
       if constexpr (LAYER) {
         float v[2] = {sum_of(ones), s};
@@ -251,98 +291,129 @@ __global__ void __launch_bounds__(32 * (grad_warps<NE, LAYER, POST, CHANNEL>() +
       }
     };
     float c1, c2;
-    sum(sg, sgc, rstd, c1, c2);
-    if (a.in[kGradDh].p) {
-      mine.load(reader.at(a.in[kGradDh], row, VEC), d);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NP; ++j) d[j] = 0;
-    }
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      if (LAYER) g[j] = add2(g[j], both(c1));
-      d[j] = fma2(fma2(c[j], both(c2), g[j]), both(rstd), d[j]);
-    }
+    means(sg, sgc, rstd, c1, c2);
+    Pair(&d)[NP] = g;                    // in place of g, as the branch's rows are of h's
     Pair(&b)[NP] = c;
-    if (branch) {
-      if (a.in[kGradBranchExponents].p)
-        mine.load_saved(reader.at(a.in[kGradBranch], row, true), reader.at(a.in[kGradBranchExponents], row, true), b);
-      else
-        mine.load(reader.at(a.in[kGradBranch], row, VEC), b);
-    }
-    Pair(&gate)[NP] = g;
-    if (!CHANNEL && a.gate == kElementGate) mine.load(reader.at(a.in[kGradGate], row, VEC), gate);
-    reader.release();
-    if (a.dresidual.p && output_ok<T>(a.dresidual, plan, row, a.err)) {
-      Pair out[NP];
+    {
+      const uint8_t* const dh = a.in[kGradDh].p ? reader.at(a.in[kGradDh], row, VEC) : nullptr;
+      T* const to = static_cast<T*>(a.dresidual.p) + row * a.dresidual.ld + ring.col0;
+      const bool store = a.dresidual.p && output_ok<T>(a.dresidual, plan, row, a.err);
 #pragma unroll
-      for (int j = 0; j < NP; ++j) out[j] = mul2(d[j], both(a.alpha));
-      mine.store(static_cast<T*>(a.dresidual.p) + row * a.dresidual.ld + ring.col0, out);
-    }
+      for (int v = 0; v < NC; ++v) {
+        Pair x[CP];
 #pragma unroll
-    for (int j = 0; j < NP; ++j) d[j] = mul2(d[j], both(a.beta));
-    if (branch) {
-      mine.drop(d);
-      if (POST && LAYER) {
+        for (int k = 0; k < CP; ++k) x[k] = 0;
+        if (dh) mine.load(dh, v, x);
 #pragma unroll
-        for (int j = 0; j < NP; ++j) b[j] = add2(b[j], both(-mean_b));
+        for (int k = 0; k < CP; ++k) {
+          const int j = v * CP + k;
+          if (LAYER) g[j] = add2(g[j], both(c1));
+          d[j] = fma2(fma2(c[j], both(c2), g[j]), both(rstd), x[k]);
+          x[k] = mul2(d[j], both(a.alpha));
+          d[j] = mul2(d[j], both(a.beta));
+        }
+        // an output that is an input: this row's part of it has been read, but for the gate's and the branch's
+        if (store) mine.store(to, v, x);
       }
-      if (gated) {
-        Pair p[NP];
+    }
+    if (branch) {
+      const bool saved = a.in[kGradBranchExponents].p != nullptr;
+      const uint8_t* const from = reader.at(a.in[kGradBranch], row, VEC || saved);
+      const uint8_t* const exponents = saved ? reader.at(a.in[kGradBranchExponents], row, true) : nullptr;
+      const uint8_t* const gate = a.gate == kElementGate ? reader.at(a.in[kGradGate], row, VEC) : nullptr;
+      T* const to = static_cast<T*>(a.dgate.p) + row * a.dgate.ld + ring.col0;
+      const bool store = a.dgate.p && output_ok<T>(a.dgate, plan, row, a.err);
+      Pair se = 0, seb = 0;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) p[j] = b[j];
+      for (int v = 0; v < NC; ++v) {
+        Pair x[CP], w[CP], p[CP];
+        if (saved)
+          mine.load_saved(from, exponents, v, x);
+        else
+          mine.load(from, v, x);
+        Pair e[CP];
+#pragma unroll
+        for (int k = 0; k < CP; ++k) e[k] = d[v * CP + k];
+        mine.drop(v, e);
         if (POST) {
-          mine.each(vector(kPostWeight), [&](int j, Pair w) { p[j] = mul2(mul2(p[j], both(rstd_b)), w); });
-          if (LAYER && a.vectors.slot[kPostBias] >= 0)
-            mine.each(vector(kPostBias), [&](int j, Pair w) { p[j] = add2(p[j], w); });
-        }
-        if (CHANNEL) {
-          mine.each(vector(kGateVector), [&](int j, Pair w) {
-            total[kSumGate][j] = fma2(d[j], p[j], total[kSumGate][j]);
-            d[j] = mul2(d[j], w);
-          });
-        } else {
-          if (a.dgate.p && output_ok<T>(a.dgate, plan, row, a.err)) {
+          mine.columns(vector(kPostWeight), v, w);
+          if (LAYER) {
 #pragma unroll
-            for (int j = 0; j < NP; ++j) p[j] = mul2(d[j], p[j]);
-            mine.store(static_cast<T*>(a.dgate.p) + row * a.dgate.ld + ring.col0, p);
+            for (int k = 0; k < CP; ++k) x[k] = add2(x[k], both(-mean_b));
           }
+        }
+        if (gated) {
 #pragma unroll
-          for (int j = 0; j < NP; ++j) d[j] = mul2(d[j], gate[j]);
+          for (int k = 0; k < CP; ++k) p[k] = POST ? mul2(mul2(x[k], both(rstd_b)), w[k]) : x[k];
+          Pair by[CP];
+          if (POST && LAYER && a.vectors.slot[kPostBias] >= 0) {
+            mine.columns(vector(kPostBias), v, by);
+#pragma unroll
+            for (int k = 0; k < CP; ++k) p[k] = add2(p[k], by[k]);
+          }
+          if (CHANNEL)
+            mine.columns(vector(kGateVector), v, by);
+          else
+            mine.load(gate, v, by);
+#pragma unroll
+          for (int k = 0; k < CP; ++k) {
+            if (CHANNEL)
+              total[kSumGate][v * CP + k] = fma2(e[k], p[k], total[kSumGate][v * CP + k]);
+            else
+              p[k] = mul2(e[k], p[k]);
+            e[k] = mul2(e[k], by[k]);
+          }
+          if (!CHANNEL && store) mine.store(to, v, p);
+        }
+#pragma unroll
+        for (int k = 0; k < CP; ++k) {
+          const int j = v * CP + k;
+          if (POST) {
+            b[j] = x[k];
+            total[kSumPostWeight][j] = fma2(mul2(e[k], both(rstd_b)), x[k], total[kSumPostWeight][j]);
+            if (LAYER) total[kSumPostBias][j] = add2(total[kSumPostBias][j], e[k]);
+            e[k] = mul2(e[k], w[k]);
+            if (LAYER) se = add2(se, e[k]);
+            seb = fma2(e[k], x[k], seb);
+          }
+          d[j] = e[k];
         }
       }
+      reader.release();
       if (POST) {
-        Pair se = 0, seb = 0;
-        mine.each(vector(kPostWeight), [&](int j, Pair w) {
-          total[kSumPostWeight][j] = fma2(mul2(d[j], both(rstd_b)), b[j], total[kSumPostWeight][j]);
-          if (LAYER) total[kSumPostBias][j] = add2(total[kSumPostBias][j], d[j]);
-          d[j] = mul2(d[j], w);
-          if (LAYER) se = add2(se, d[j]);
-          seb = fma2(d[j], b[j], seb);
-        });
-        sum(se, seb, rstd_b, c1, c2);
+        means(se, seb, rstd_b, c1, c2);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           if (LAYER) d[j] = add2(d[j], both(c1));
           d[j] = mul2(fma2(b[j], both(c2), d[j]), both(rstd_b));
         }
       }
+    } else {
+      reader.release();
     }
-    if (a.dbranch.p && output_ok<T>(a.dbranch, plan, row, a.err))
-      mine.store(static_cast<T*>(a.dbranch.p) + row * a.dbranch.ld + ring.col0, d);
+    if (a.dbranch.p && output_ok<T>(a.dbranch, plan, row, a.err)) {
+#pragma unroll
+      for (int v = 0; v < NC; ++v) {
+        Pair x[CP];
+#pragma unroll
+        for (int k = 0; k < CP; ++k) x[k] = d[v * CP + k];
+        mine.store(static_cast<T*>(a.dbranch.p) + row * a.dbranch.ld + ring.col0, v, x);
+      }
+    }
   }
   if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
   if (!a.sums) return;
   // the groups' sums, added in group order: one row of partials per CTA (or
   // cluster) and vector; what was the ring makes room
-  const int slots = Part::slots(plan.lanes);
+  const int threads = static_cast<int>(blockDim.x) - kProducerThreads, slots = Part::slots(plan.lanes);
+  const auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"n"(kComputeBarrier), "r"(threads) : "memory"); };
 #pragma unroll
   for (int k = 0; k < kSums; ++k) {
     const bool there = k == kSumWeight || (k == kSumBias && LAYER) || (k == kSumGate && CHANNEL) ||
                        (k == kSumPostWeight && POST) || (k == kSumPostBias && POST && LAYER);
     if (!there || a.sum[k] < 0) continue;
-    __syncthreads();
-    if (!producer) {
+    meet();
+    if (group < plan.groups) {
 #pragma unroll
       for (int q = 0; q < NE / 4; ++q) {
         float4 f;
@@ -351,10 +422,10 @@ __global__ void __launch_bounds__(32 * (grad_warps<NE, LAYER, POST, CHANNEL>() +
         *reinterpret_cast<float4*>(mine.quad(columns + group * slots, q)) = f;
       }
     }
-    __syncthreads();
+    meet();
     float* const to = a.partials +
                       (static_cast<size_t>(blockIdx.x / plan.ctas) * a.sums + a.sum[k]) * plan.width + ring.col0;
-    for (int slot = threadIdx.x; slot < slots; slot += blockDim.x) {
+    for (int slot = threadIdx.x; slot < slots; slot += threads) {
       const int col = Part::column_of_slot(slot, plan.lanes);
       if (col >= ring.width) continue;
       float v = columns[slot];
@@ -567,8 +638,8 @@ constexpr int kMostStages = 8;
 
 // Lays out the rows of `in` over `warps` warps of lanes of `ne` elements,
 // groups and ring; false where a row is too wide.
-bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ne, int warps, bool aligned, int num_sms,
-               size_t* bytes, int* grid) {
+bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ne, int warps, bool stats, bool aligned,
+               int num_sms, size_t* bytes, int* grid) {
   for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
     if (ctas > num_sms) return false;
     const int slice = ctas == 1 ? plan.width : ((plan.width - 1) / ctas / kSliceUnit + 1) * kSliceUnit;
@@ -590,6 +661,8 @@ bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ne, int war
         in[i].at = static_cast<uint32_t>(stage);
         stage += (static_cast<size_t>(plan.groups) * in[i].pitch + 15) / 16 * 16 + (in[i].packed && !aligned ? 16 : 0);
       }
+      plan.stats_at = stats ? static_cast<uint32_t>(stage) : 0u;
+      stage += stats ? static_cast<size_t>(plan.groups) * kStats * sizeof(float) : 0;
       stages = columns < kMostShared ? (kMostShared - columns) / (stage + 16) : 0;
       if (stages >= 2 || plan.groups == 1) break;
     }
@@ -622,13 +695,13 @@ constexpr int kMaxDevices = 64;
 // CTAs form clusters, with no more of them than run at once (`grid` is
 // reduced to that).
 template <auto Kernel, class Args>
-int launch_rows(const Args& a, int device, int* grid, size_t bytes, cudaStream_t stream) {
+int launch_rows(const Args& a, int threads, int device, int* grid, size_t bytes, cudaStream_t stream) {
   static std::atomic<int> clusters[kMaxDevices][4];   // at a time, per log2 of their CTAs; 1 for single CTAs
   const RowPlan& plan = a.plan;
   std::atomic<int>& kept = clusters[device % kMaxDevices][plan.ctas == 1 ? 0 : plan.ctas == 2 ? 1 : plan.ctas == 4 ? 2 : 3];
   int most = kept.load();
   cudaLaunchConfig_t config = {};
-  config.blockDim = dim3(plan.groups * plan.lanes + 32);
+  config.blockDim = dim3(threads);
   config.dynamicSmemBytes = bytes;
   config.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -647,7 +720,7 @@ int launch_rows(const Args& a, int device, int* grid, size_t bytes, cudaStream_t
     if (plan.ctas > 1) {
       cudaLaunchConfig_t full = config;
       full.gridDim = dim3(512 / plan.ctas * plan.ctas);
-      full.dynamicSmemBytes = kMostShared;
+      full.dynamicSmemBytes = kMostShared;       // one CTA per SM
       full.attrs = attr + 1;
       full.numAttrs = 1;
       if (cudaOccupancyMaxActiveClusters(&most, Kernel, &full) != cudaSuccess || most < 1) {
@@ -686,10 +759,10 @@ struct Layout {
   int grid = 0, ne = 0;
 };
 
-// The cheapest of the layouts with `ne[i]` elements a thread on `warps[i]`
-// warps; ne 0: there is none.
+// The cheapest of the layouts with `ne[i]` elements a thread on `warps` warps;
+// ne 0: there is none.
 template <int N, int K>
-Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], const int (&warps)[K],
+Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], int warps, bool stats,
                       const BlockLaunch& l) {
   Layout<N> best = {};
   long long least = 0;
@@ -698,7 +771,7 @@ Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (
     c.plan = plan;
     std::copy(in, in + N, c.in);
     c.ne = ne[i];
-    if (!plan_rows(c.plan, c.in, N, l.vectors, ne[i], warps[i], l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
+    if (!plan_rows(c.plan, c.in, N, l.vectors, ne[i], warps, stats, l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
     const long long cost = price(c.plan, ne[i]);
     if (best.ne == 0 || cost < least) {
       best = c;
@@ -710,14 +783,15 @@ Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (
 
 template <class T, int NE>
 int forward_form(const BlockArgs& a, const BlockLaunch& l, Layout<kInputs>& best) {
-  return l.aligned ? launch_rows<block_norm_kernel<T, NE, true>>(a, l.device, &best.grid, best.bytes, l.stream)
-                   : launch_rows<block_norm_kernel<T, NE, false>>(a, l.device, &best.grid, best.bytes, l.stream);
+  const int threads = a.plan.groups * a.plan.lanes + 32;
+  return l.aligned ? launch_rows<block_norm_kernel<T, NE, true>>(a, threads, l.device, &best.grid, best.bytes, l.stream)
+                   : launch_rows<block_norm_kernel<T, NE, false>>(a, threads, l.device, &best.grid, best.bytes, l.stream);
 }
 
 template <class T>
 int forward(BlockArgs& a, const BlockLaunch& l) {
-  const int ne[3] = {8, 16, 32}, warps[3] = {kRowWarps, kRowWarps, kRowWarps};
-  Layout<kInputs> best = best_layout(a.plan, a.in, ne, warps, l);
+  const int ne[3] = {8, 16, 32};
+  Layout<kInputs> best = best_layout(a.plan, a.in, ne, kForwardWarps, false, l);
   ++*l.launches;
   if (best.ne == 0) {
     *l.kernel = "block_norm_wide_kernel";
@@ -733,9 +807,12 @@ int forward(BlockArgs& a, const BlockLaunch& l) {
 
 template <class T, int NE, bool LAYER, bool POST, bool CHANNEL>
 int gradient_form(const BlockGradArgs& a, const BlockLaunch& l, Layout<kGradInputs>& best) {
-  return l.aligned
-             ? launch_rows<block_norm_grad_kernel<T, NE, true, LAYER, POST, CHANNEL>>(a, l.device, &best.grid, best.bytes, l.stream)
-             : launch_rows<block_norm_grad_kernel<T, NE, false, LAYER, POST, CHANNEL>>(a, l.device, &best.grid, best.bytes, l.stream);
+  // warpgroups of threads that compute, and the producer's
+  const int threads = (a.plan.groups * a.plan.lanes + 127) / 128 * 128 + kProducerThreads;
+  return l.aligned ? launch_rows<block_norm_grad_kernel<T, NE, true, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
+                                                                                            best.bytes, l.stream)
+                   : launch_rows<block_norm_grad_kernel<T, NE, false, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
+                                                                                             best.bytes, l.stream);
 }
 
 // f with the three choices as template arguments.
@@ -759,8 +836,10 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
   if (a.plan.rows > 0) {
     rc = with_form(!a.rms, a.post, a.gate == kChannelGate, [&](auto layer, auto post, auto channel) -> int {
       constexpr bool kLayer = decltype(layer)::value, kPost = decltype(post)::value, kChannel = decltype(channel)::value;
-      const int ne[2] = {8, 16}, warps[2] = {grad_warps<8, kLayer, kPost, kChannel>(), grad_warps<16, kLayer, kPost, kChannel>()};
-      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, warps, l);
+      // 16 elements' sums of four or five vectors leave too few registers
+      constexpr bool kTwo = !(kLayer && kPost);
+      const int ne[2] = {8, kTwo ? 16 : 8};
+      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, kRowWarps, true, l);
       c.ctas = best.ne ? best.grid / best.plan.ctas : static_cast<int>(std::min<long long>(a.plan.rows, 2LL * l.num_sms));
       if (a.sums) {
         a.partials = static_cast<float*>(acquire_scratch(
@@ -776,7 +855,7 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
       a.plan = best.plan;
       std::copy(best.in, best.in + kGradInputs, a.in);
       const int got = best.ne == 8 ? gradient_form<T, 8, kLayer, kPost, kChannel>(a, l, best)
-                                   : gradient_form<T, 16, kLayer, kPost, kChannel>(a, l, best);
+                                   : gradient_form<T, kTwo ? 16 : 8, kLayer, kPost, kChannel>(a, l, best);
       c.ctas = best.grid / best.plan.ctas;
       return got;
     });

@@ -62,12 +62,21 @@ struct RingPlace {
   // One thread, before the CTA's first barrier.
   __device__ __forceinline__ void init(const RowPlan& p) const {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(full + 8u * i, 1);
+      mbar_init(full + 8u * i, p.stats_at ? 33 : 1);        // the producer's lanes, where they copy statistics
       mbar_init(empty + 8u * i, static_cast<uint32_t>(p.groups * (p.lanes / 32)));
     }
     fence_mbar_init();
   }
 };
+
+// 4 bytes of global memory into shared memory, and this thread's arrival at a
+// barrier once all such copies of its own have landed.
+__device__ __forceinline__ void copy_word(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 // One copy: the bytes [first, last) of a matrix, to the place in a stage that
 // lies as far above a 16-byte boundary as they do.  The whole 16-byte blocks
@@ -111,9 +120,12 @@ struct RowCopy {
 // flight.  It gives up at a wait that runs out (recorded), and in any case
 // waits, with a limit, for its last copies: none lands in memory that is no
 // longer the kernel's.  filled(): a barrier of the CTA, behind the first copies.
+// Statistics come the same way (those of stats_mask, rows of `rows` values):
+// loaded by the threads that use them, even a row ahead, they were what half
+// of the gradient's issue slots waited for.
 template <int N, class F>
 __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const RowPlan& plan, const RingPlace& ring,
-                                             unsigned* err, F filled) {
+                                             const float* stats, uint32_t stats_mask, unsigned* err, F filled) {
   bool met = false;                      // the others, who fill the vectors under the first copies
   const int lane = threadIdx.x & 31;
   int s = 0, issued = 0;
@@ -128,6 +140,15 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
     const int rows = static_cast<int>(min(static_cast<long long>(plan.groups), plan.rows - row0));
     uint8_t* const stage = ring.data + static_cast<size_t>(s) * plan.stage_bytes;
     const uint32_t bar = ring.full + 8u * s;
+    // statistics: 4 bytes each, counted by the lanes' own arrivals
+    if (stats_mask) {
+      const uint32_t to = smem_addr(stage) + plan.stats_at;
+      for (int i = lane; i < kStats * rows; i += 32) {
+        const int k = i / rows, r = i - k * rows;
+        if (stats_mask >> k & 1u) copy_word(to + 4u * (r * kStats + k), stats + k * plan.rows + row0 + r);
+      }
+      copies_arrive(bar);
+    }
     // lane i < N: matrix i's chunk, where it is one copy; then, matrix by
     // matrix, the others' rows
     const int mine = lane < N ? lane : 0;
@@ -209,6 +230,11 @@ struct RingReader {
       ph ^= 1u;
     }
   }
+  // The row's statistics.
+  __device__ __forceinline__ float4 stats() const {
+    return *reinterpret_cast<const float4*>(ring.data + static_cast<uint32_t>(s) * plan.stage_bytes + plan.stats_at +
+                                            static_cast<uint32_t>(group) * (kStats * 4u));
+  }
   // The group's row of a matrix in the current stage; what lies `shift` bytes
   // behind a 16-byte boundary in memory lies so in the stage.
   __device__ __forceinline__ const uint8_t* at(const RowSource& m, long long row, bool vec) const {
@@ -220,14 +246,18 @@ struct RingReader {
 };
 
 // ---------------------------------------------------------------- a thread's part of a row
-// NE elements of type T.  VEC: 16-byte vectors, vector v of thread t from
-// column (v lanes + t) V on, which takes rows on 16-byte boundaries of whole
-// vectors.  Else single elements, element i of thread t in column i lanes + t:
-// 2 or 4 bytes apart from lane to lane, so that rows may start anywhere.
+// NE elements of type T, in chunks of CP pairs.  VEC: a chunk is a 16-byte
+// vector, chunk v of thread t from column (v lanes + t) V on, which takes rows
+// on 16-byte boundaries of whole vectors.  Else single elements, element i of
+// thread t in column i lanes + t: 2 or 4 bytes apart from lane to lane, so that
+// rows may start anywhere.
 template <class T, int NE, bool VEC>
 struct RowPart {
   static constexpr int V = 16 / static_cast<int>(sizeof(T));
   static constexpr int NP = NE / 2;      // pairs
+  static constexpr int CP = VEC ? V / 2 : 2;
+  static constexpr int NC = NP / CP;
+  using Chunk = Pair[CP];
   int t, lanes, width;
   bool full;                             // every thread's elements are all columns of the slice
 
@@ -240,89 +270,86 @@ struct RowPart {
   __device__ __forceinline__ bool in(int i) const { return col(i) < width; }
 
   // The row's elements, 0 for what lies outside it.
-  __device__ __forceinline__ void load(const uint8_t* row, Pair (&x)[NP]) const {
+  __device__ __forceinline__ void load(const uint8_t* row, int v, Chunk& x) const {
     if constexpr (VEC) {
 #pragma unroll
-      for (int v = 0; v < NE / V; ++v) {
-        Pair p[V / 2];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) p[j] = 0;
-        if (in(v * V)) pairs_of<T>(*reinterpret_cast<const uint4*>(row + col(v * V) * sizeof(T)), p);
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) x[v * (V / 2) + j] = p[j];
-      }
+      for (int j = 0; j < CP; ++j) x[j] = 0;
+      if (in(v * V)) pairs_of<T>(*reinterpret_cast<const uint4*>(row + col(v * V) * sizeof(T)), x);
     } else {
       const T* const p = reinterpret_cast<const T*>(row);
-      float f[NE];
 #pragma unroll
-      for (int i = 0; i < NE; ++i) f[i] = in(i) ? to_f32(p[col(i)]) : 0.0f;
-#pragma unroll
-      for (int j = 0; j < NP; ++j) x[j] = pair_of(f[2 * j], f[2 * j + 1]);
+      for (int j = 0; j < CP; ++j) {
+        const int i = 2 * (v * CP + j);
+        x[j] = pair_of(in(i) ? to_f32(p[col(i)]) : 0.0f, in(i + 1) ? to_f32(p[col(i + 1)]) : 0.0f);
+      }
     }
   }
   // The same of a row kept in 8 bits.
-  __device__ __forceinline__ void load_saved(const uint8_t* codes, const uint8_t* exponents, Pair (&x)[NP]) const {
+  __device__ __forceinline__ void load_saved(const uint8_t* codes, const uint8_t* exponents, int v, Chunk& x) const {
     if constexpr (VEC) {
+      uint32_t w[V / 4];
+      float by = 0.0f;
 #pragma unroll
-      for (int v = 0; v < NE / V; ++v) {
-        uint32_t w[V / 4];
-        float by = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V / 4; ++j) w[j] = 0u;
-        if (in(v * V)) {
-          const int c = col(v * V);
-#pragma unroll
-          for (int j = 0; j < V / 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(codes + c + 4 * j);
-          by = power_of(exponents[c / kSavedBlock]);
+      for (int j = 0; j < V / 4; ++j) w[j] = 0u;
+      if (in(v * V)) {
+        const int c = col(v * V);
+        if constexpr (V == 8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(codes + c);
+          w[0] = q.x;
+          w[V / 4 - 1] = q.y;
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t*>(codes + c);
         }
-        const Pair power = pair_of(by, by);
+        by = power_of(exponents[c / kSavedBlock]);
+      }
+      const Pair power = pair_of(by, by);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const float2 f = values_of((w[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
-          x[v * (V / 2) + j] = mul2(pair_of(f.x, f.y), power);
-        }
+      for (int j = 0; j < CP; ++j) {
+        const float2 f = values_of((w[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+        x[j] = mul2(pair_of(f.x, f.y), power);
       }
     } else {
-      float f[NE];
 #pragma unroll
-      for (int i = 0; i < NE; ++i)
-        f[i] = in(i) ? values_of(codes[col(i)]).x * power_of(exponents[col(i) / kSavedBlock]) : 0.0f;
+      for (int j = 0; j < CP; ++j) {
+        float f[2];
 #pragma unroll
-      for (int j = 0; j < NP; ++j) x[j] = pair_of(f[2 * j], f[2 * j + 1]);
+        for (int k = 0; k < 2; ++k) {
+          const int i = 2 * (v * CP + j) + k;
+          f[k] = in(i) ? values_of(codes[col(i)]).x * power_of(exponents[col(i) / kSavedBlock]) : 0.0f;
+        }
+        x[j] = pair_of(f[0], f[1]);
+      }
     }
   }
   // 0 for what lies outside the row.
-  __device__ __forceinline__ void drop(Pair (&x)[NP]) const {
+  __device__ __forceinline__ void drop(int v, Chunk& x) const {
     if (full) return;
     if constexpr (VEC) {
+      if (!in(v * V)) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j)
-        if (!in(2 * j / V * V)) x[j] = 0;
+        for (int j = 0; j < CP; ++j) x[j] = 0;
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
+      for (int j = 0; j < CP; ++j) {
+        const int i = 2 * (v * CP + j);
         float a, b;
         unpair(x[j], a, b);
-        x[j] = pair_of(in(2 * j) ? a : 0.0f, in(2 * j + 1) ? b : 0.0f);
+        x[j] = pair_of(in(i) ? a : 0.0f, in(i + 1) ? b : 0.0f);
       }
     }
   }
-  __device__ __forceinline__ void store(T* row, const Pair (&x)[NP]) const {
+  __device__ __forceinline__ void store(T* row, int v, const Chunk& x) const {
     if constexpr (VEC) {
-#pragma unroll
-      for (int v = 0; v < NE / V; ++v) {
-        Pair p[V / 2];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) p[j] = x[v * (V / 2) + j];
-        if (in(v * V)) store_pairs(row + col(v * V), p);
-      }
+      if (in(v * V)) store_pairs(row + col(v * V), x);
     } else {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
+      for (int j = 0; j < CP; ++j) {
+        const int i = 2 * (v * CP + j);
         float a, b;
         unpair(x[j], a, b);
-        if (in(2 * j)) row[col(2 * j)] = from_f32<T>(a);
-        if (in(2 * j + 1)) row[col(2 * j + 1)] = from_f32<T>(b);
+        if (in(i)) row[col(i)] = from_f32<T>(a);
+        if (in(i + 1)) row[col(i + 1)] = from_f32<T>(b);
       }
     }
   }
@@ -336,24 +363,22 @@ struct RowPart {
     return column(quad % lanes, quad / lanes * 4 + slot % 4, lanes);
   }
   __device__ __forceinline__ float* quad(float* values, int q) const { return values + 4 * (q * lanes + t); }
-  // Calls f(j, w) for every pair j of elements with the pair's two values.
-  template <class F>
-  __device__ __forceinline__ void each(const float* values, F f) const {
+  __device__ __forceinline__ void columns(const float* values, int v, Chunk& w) const {
 #pragma unroll
-    for (int q = 0; q < NE / 4; ++q) {
-      const float4 v = *reinterpret_cast<const float4*>(values + 4 * (q * lanes + t));
-      f(2 * q, pair_of(v.x, v.y));
-      f(2 * q + 1, pair_of(v.z, v.w));
+    for (int k = 0; k < CP / 2; ++k) {
+      const float4 f = *reinterpret_cast<const float4*>(values + 4 * ((v * (CP / 2) + k) * lanes + t));
+      w[2 * k] = pair_of(f.x, f.y);
+      w[2 * k + 1] = pair_of(f.z, f.w);
     }
   }
 };
 
 // A vector of `width` values (fp32, or T where `f32` is not set; null: `none`)
-// from column col0 on, into slots.  All threads of the CTA but the producer's.
+// from column col0 on, into slots, by the first `threads` of the CTA.
 template <class T, class Part>
-__device__ __forceinline__ void fill_columns(float* values, const void* p, bool f32, float none, int lanes, int col0,
-                                             int width) {
-  for (int slot = threadIdx.x; slot < Part::slots(lanes); slot += blockDim.x - 32) {
+__device__ __forceinline__ void fill_columns(float* values, const void* p, bool f32, float none, int lanes,
+                                             int threads, int col0, int width) {
+  for (int slot = threadIdx.x; slot < Part::slots(lanes); slot += threads) {
     const int c = Part::column_of_slot(slot, lanes);
     float v = 0.0f;
     if (c < width)
