@@ -12,10 +12,10 @@
 namespace gemm_f32_impl {
 
 constexpr int kRowWarps = 16;            // that compute, at most
-constexpr int kForwardWarps = 12;        // in the forward pass: with the producer 13, four for each quarter
-                                         // of an SM, which leaves 128 registers a thread
 constexpr int kMostCtas = 8;             // of a cluster
 constexpr int kStats = 4;                // per row: mean and rstd of h, of the branch
+constexpr int kMostChunk = 8;            // rows of a stage, where all rows lie one behind the other
+constexpr int kMostLoose = 4;            // and where they do not
 constexpr int kSliceUnit = 512;          // columns: their exponents fill 16 bytes
 
 // One matrix that a row is read from.  size: bytes per element, or 0 for the
@@ -34,6 +34,7 @@ struct RowSource {
 struct RowPlan {
   int width, slice;                      // columns of a row, of a CTA's part
   int lanes, groups, stages, ctas;
+  int chunk;                             // rows of a stage: a divisor of groups
   uint32_t stage_bytes;
   uint32_t ring_at;                      // in dynamic shared memory, behind the weights
   uint32_t stats_at;                     // of the rows' statistics within a stage; 0: they do not come this way

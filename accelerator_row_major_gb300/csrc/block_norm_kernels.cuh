@@ -57,17 +57,38 @@ __device__ __forceinline__ void fill_vectors(float* columns, const VectorArgs& v
                             i == kWeight || i == kPostWeight ? 1.0f : 0.0f, plan.lanes, threads, ring.col0, ring.width);
 }
 
+// 16 warps compute with 112 registers a thread, some of them left by the
+// warpgroup whose first warp is the producer: with that as a 17th warp of a
+// plain launch there would be 96.
+constexpr int kProducerThreads = 128;
+constexpr int kProducerRegisters = 32, kComputeRegisters = 112;
+static_assert(kProducerThreads * kProducerRegisters + 32 * kRowWarps * kComputeRegisters <=
+                  96 * (kProducerThreads + 32 * kRowWarps),
+              "registers of a launch of 96 a thread");
+constexpr int kComputeBarrier = 15;      // of the threads that compute; no group has it (at most 8 groups meet at theirs)
+
+// The producer's warpgroup, to its end.
+template <bool ALIGNED, int N>
+__device__ __forceinline__ void producer_warps(const RowSource (&in)[N], const RowPlan& plan, const RingPlace& ring,
+                                               const float* stats, uint32_t stats_mask, unsigned* err) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegisters));
+  if (threadIdx.x < blockDim.x - kProducerThreads + 32)
+    produce_rows<ALIGNED>(in, plan, ring, stats, stats_mask, err, [] { __syncthreads(); });
+  else
+    __syncthreads();
+  if (plan.ctas > 1) cluster_sync();
+}
+
 // ---------------------------------------------------------------- forward
 template <class T, int NE, bool VEC>
-__global__ void __launch_bounds__(32 * (kForwardWarps + 1), 1) block_norm_kernel(const __grid_constant__ BlockArgs a) {
+__global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
+    block_norm_kernel(const __grid_constant__ BlockArgs a) {
   using Part = RowPart<T, NE, VEC>;
   constexpr int NP = Part::NP, NC = Part::NC, CP = Part::CP;
   extern __shared__ __align__(128) uint8_t smem_rows[];
   __shared__ RowShared shared;
   const RowPlan& plan = a.plan;
-  const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
   const int rank = plan.ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const bool producer = group == plan.groups;            // the last warp
   const RingPlace ring(plan, smem_rows, rank);
   if (threadIdx.x == 0) {
     if (plan.ctas > 1) RowSums::init(shared, plan);
@@ -77,13 +98,15 @@ __global__ void __launch_bounds__(32 * (kForwardWarps + 1), 1) block_norm_kernel
   if (plan.ctas > 1) cluster_sync();     // every CTA of the cluster runs
   grid_launch_dependents();
   grid_dependency_wait();
-  float* const columns = reinterpret_cast<float*>(smem_rows);
-  if (producer) {
-    produce_rows(a.in, plan, ring, nullptr, 0u, a.err, [&] { __syncthreads(); });
-  } else {
-    fill_vectors<T, Part>(columns, a.vectors, plan, ring);
-    __syncthreads();
+  if (threadIdx.x >= blockDim.x - kProducerThreads) {
+    producer_warps<VEC>(a.in, plan, ring, nullptr, 0u, a.err);
+    return;
   }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegisters));
+  const int group = threadIdx.x / plan.lanes, t = threadIdx.x % plan.lanes;
+  float* const columns = reinterpret_cast<float*>(smem_rows);
+  fill_vectors<T, Part>(columns, a.vectors, plan, ring);
+  __syncthreads();
   const Part mine(t, plan.lanes, ring.width);
   const float inv = 1.0f / static_cast<float>(plan.width);
   const auto vector = [&](int v) { return columns + a.vectors.slot[v] * Part::slots(plan.lanes); };
@@ -127,8 +150,9 @@ __global__ void __launch_bounds__(32 * (kForwardWarps + 1), 1) block_norm_kernel
   };
   const auto chunk = [](Pair(&x)[NP], int v) -> Pair(&)[CP] { return *reinterpret_cast<Pair(*)[CP]>(&x[v * CP]); };
 
-  RingReader reader = {ring, plan, a.err, group};
-  for (long long row = ring.first * plan.groups + group; !producer && row < plan.rows; row += ring.step * plan.groups) {
+  RingReader reader(ring, plan, a.err, group);
+  long long row = group < plan.groups ? ring.first * plan.groups + group : plan.rows;
+  for (; row < plan.rows; row += ring.step * plan.groups) {
     reader.wait();
     Pair x[NP];
     float mean, rstd, mean_b = 0.0f, rstd_b = 0.0f;
@@ -184,16 +208,7 @@ __global__ void __launch_bounds__(32 * (kForwardWarps + 1), 1) block_norm_kernel
 // ---------------------------------------------------------------- gradient
 // LAYER: around the means; POST: the branch was normed; CHANNEL: a gate per
 // channel (a gate per element is the launch's choice).  What a form does not
-// have costs no registers.  16 warps compute with 112 registers a thread, of
-// which the warps beside the producer leave them theirs: with the producer as
-// a 17th warp of a plain launch there would be 96.
-constexpr int kProducerThreads = 128;    // a warpgroup, whose first warp works
-constexpr int kProducerRegisters = 32, kComputeRegisters = 112;
-static_assert(kProducerThreads * kProducerRegisters + 32 * kRowWarps * kComputeRegisters <=
-                  96 * (kProducerThreads + 32 * kRowWarps),
-              "registers of a launch of 96 a thread");
-constexpr int kComputeBarrier = 15;      // of the threads that compute; no group has it (at most 8 groups meet at theirs)
-
+// have costs no registers.
 template <class T, int NE, bool VEC, bool LAYER, bool POST, bool CHANNEL>
 __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
@@ -213,13 +228,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
   grid_launch_dependents();
   grid_dependency_wait();
   if (threadIdx.x >= blockDim.x - kProducerThreads) {
-    // ------------------------------------------------------------ producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegisters));
-    if (threadIdx.x < blockDim.x - kProducerThreads + 32)
-      produce_rows(a.in, plan, ring, a.stats, (LAYER ? 3u : 2u) * (POST ? 5u : 1u), a.err, [&] { __syncthreads(); });
-    else
-      __syncthreads();
-    if (plan.ctas > 1) cluster_sync();
+    producer_warps<VEC>(a.in, plan, ring, a.stats, (LAYER ? 3u : 2u) * (POST ? 5u : 1u), a.err);
     return;
   }
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegisters));
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
 #pragma unroll
     for (int j = 0; j < NP; ++j) total[k][j] = 0;
 
-  RingReader reader = {ring, plan, a.err, group};
+  RingReader reader(ring, plan, a.err, group);
   const long long step = ring.step * plan.groups;
   long long row = group < plan.groups ? ring.first * plan.groups + group : plan.rows;
   for (; row < plan.rows; row += step) {
@@ -634,59 +643,67 @@ __global__ void __launch_bounds__(1024) block_columns_kernel(const ColumnArgs a)
 
 // ---------------------------------------------------------------- host side
 constexpr size_t kMostShared = 220 * 1024;   // dynamic; RowShared fits beside it
-constexpr int kMostStages = 8;
+constexpr int kMostStages = 16;
+constexpr size_t kLeastChunk = 8 * 1024;     // bytes of a stage, where there are rows enough
 
-// Lays out the rows of `in` over `warps` warps of lanes of `ne` elements,
-// groups and ring; false where a row is too wide.
-bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ne, int warps, bool stats, bool aligned,
-               int num_sms, size_t* bytes, int* grid) {
-  for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
-    if (ctas > num_sms) return false;
-    const int slice = ctas == 1 ? plan.width : ((plan.width - 1) / ctas / kSliceUnit + 1) * kSliceUnit;
-    if (slice > warps * 32 * ne) continue;
-    plan.ctas = ctas;
-    plan.slice = slice;
-    plan.lanes = 32 * ((slice - 1) / (32 * ne) + 1);
-    const long long units = num_sms / ctas;
-    plan.groups = static_cast<int>(std::min<long long>(warps * 32 / plan.lanes, (plan.rows - 1) / units + 1));
-    const size_t columns = static_cast<size_t>(vectors) * ne * plan.lanes * sizeof(float);
-    size_t stage = 0, stages = 0;
-    for (;; --plan.groups) {             // two chunks in flight, or fewer groups
-      stage = 0;
-      for (int i = 0; i < n; ++i) {
-        if (!in[i].p) continue;
-        const size_t row = source_bytes(in[i].size, slice);
-        in[i].packed = ctas == 1 && in[i].ld == static_cast<long long>(row);
-        in[i].pitch = static_cast<uint32_t>(in[i].packed ? row : (row + 15) / 16 * 16 + (aligned || in[i].size < 2 ? 0 : 16));
-        in[i].at = static_cast<uint32_t>(stage);
-        stage += (static_cast<size_t>(plan.groups) * in[i].pitch + 15) / 16 * 16 + (in[i].packed && !aligned ? 16 : 0);
-      }
-      plan.stats_at = stats ? static_cast<uint32_t>(stage) : 0u;
-      stage += stats ? static_cast<size_t>(plan.groups) * kStats * sizeof(float) : 0;
-      stages = columns < kMostShared ? (kMostShared - columns) / (stage + 16) : 0;
-      if (stages >= 2 || plan.groups == 1) break;
+// Lays out the rows of `in` over `ctas` CTAs and lanes of `ne` elements,
+// groups and ring; false where that cannot be.
+bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int ne, bool stats, bool aligned, int num_sms,
+               size_t* bytes, int* grid) {
+  const int slice = ctas == 1 ? plan.width : ((plan.width - 1) / ctas / kSliceUnit + 1) * kSliceUnit;
+  if (ctas > num_sms || slice > kRowWarps * 32 * ne) return false;
+  plan.ctas = ctas;
+  plan.slice = slice;
+  plan.lanes = 32 * ((slice - 1) / (32 * ne) + 1);
+  const long long units = num_sms / ctas;
+  const size_t columns = static_cast<size_t>(vectors) * ne * plan.lanes * sizeof(float);
+  plan.groups = static_cast<int>(std::min<long long>(kRowWarps * 32 / plan.lanes, (plan.rows - 1) / units + 1));
+  // a stage of `rows` rows
+  const auto stage_of = [&](int rows) {
+    size_t stage = 0;
+    for (int i = 0; i < n; ++i) {
+      if (!in[i].p) continue;
+      const size_t row = source_bytes(in[i].size, slice);
+      in[i].packed = ctas == 1 && in[i].ld == static_cast<long long>(row);
+      in[i].pitch = static_cast<uint32_t>(in[i].packed ? row : (row + 15) / 16 * 16 + (aligned || in[i].size < 2 ? 0 : 16));
+      in[i].at = static_cast<uint32_t>(stage);
+      stage += (static_cast<size_t>(rows) * in[i].pitch + 15) / 16 * 16 + (in[i].packed && !aligned ? 16 : 0);
     }
-    if (stages < 2) continue;
-    plan.stages = static_cast<int>(std::min<size_t>(stages, kMostStages));
-    plan.stage_bytes = static_cast<uint32_t>(stage);
-    plan.ring_at = static_cast<uint32_t>(columns);
-    const long long need = (plan.rows - 1) / plan.groups + 1;
-    *grid = static_cast<int>(std::min<long long>(units, need)) * ctas;
-    // the groups' sums take the place of the ring
-    *bytes = std::max(columns + static_cast<size_t>(plan.stages) * (stage + 16),
-                      static_cast<size_t>(plan.groups) * ne * plan.lanes * sizeof(float));
-    return true;
+    plan.stats_at = stats ? static_cast<uint32_t>(stage) : 0u;
+    return stage + (stats ? rows * kStats * sizeof(float) : 0);
+  };
+  size_t stage = 0, stages = 0;
+  for (;; --plan.groups) {               // two rows in flight per group, or fewer groups
+    plan.chunk = 1;
+    for (int rows = 2; rows <= plan.groups && stage_of(plan.chunk) < kLeastChunk; ++rows) {
+      bool loose = false;
+      for (int i = 0; i < n; ++i) loose = loose || (in[i].p && !in[i].packed);
+      if (plan.groups % rows == 0 && rows <= (loose ? kMostLoose : kMostChunk)) plan.chunk = rows;
+    }
+    stage = stage_of(plan.chunk);
+    stages = columns < kMostShared ? (kMostShared - columns) / (stage + 16) : 0;
+    if (stages >= 2u * (plan.groups / plan.chunk) || plan.groups == 1) break;
   }
-  return false;
+  if (stages < 2) return false;
+  plan.stages = static_cast<int>(std::min<size_t>(stages, std::max(kMostStages, 2 * plan.groups / plan.chunk)));
+  plan.stage_bytes = static_cast<uint32_t>(stage);
+  plan.ring_at = static_cast<uint32_t>(columns);
+  *grid = static_cast<int>(std::min<long long>(units, (plan.rows - 1) / plan.groups + 1)) * ctas;
+  // the groups' sums take the place of the ring
+  *bytes = std::max(columns + static_cast<size_t>(plan.stages) * (stage + 16),
+                    static_cast<size_t>(plan.groups) * ne * plan.lanes * sizeof(float));
+  return true;
 }
 
 // A layout's price: what a row takes its threads, by the rows that are worked
 // on at a time.  A row costs a warp some 250 instructions besides 16 for each
-// of its elements (counted: 380 of 8 elements).
-constexpr int kRowCost = 250, kElementCost = 16;
+// of its elements (counted: 380 of 8 elements), and more where CTAs exchange
+// sums; a group that is alone waits for all of them.
+constexpr int kRowCost = 250, kExchangeCost = 300, kElementCost = 16;
 
 long long price(const RowPlan& plan, int ne) {
-  return (kRowCost + static_cast<long long>(kElementCost) * ne) * plan.ctas * kRowWarps / plan.groups;
+  const long long row = kRowCost + (plan.ctas > 1 ? kExchangeCost : 0) + static_cast<long long>(kElementCost) * ne;
+  return row * plan.ctas * (plan.groups == 1 ? 24 : 16) / plan.groups;
 }
 
 constexpr int kMaxDevices = 64;
@@ -750,6 +767,9 @@ int launch_plain(Kernel kernel, dim3 grid, int threads, cudaStream_t stream, con
   return GEMM_F32_OK;
 }
 
+// Warpgroups of threads that compute, and the producer's.
+int cta_threads(const RowPlan& plan) { return (plan.groups * plan.lanes + 127) / 128 * 128 + kProducerThreads; }
+
 // A row layout that a call may take.
 template <int N>
 struct Layout {
@@ -759,23 +779,24 @@ struct Layout {
   int grid = 0, ne = 0;
 };
 
-// The cheapest of the layouts with `ne[i]` elements a thread on `warps` warps;
-// ne 0: there is none.
+// The cheapest of the layouts with `ne[i]` elements a thread; ne 0: there is
+// none.
 template <int N, int K>
-Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], int warps, bool stats,
-                      const BlockLaunch& l) {
+Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], bool stats, const BlockLaunch& l) {
   Layout<N> best = {};
   long long least = 0;
-  for (int i = 0; i < K; ++i) {
-    Layout<N> c = {};
-    c.plan = plan;
-    std::copy(in, in + N, c.in);
-    c.ne = ne[i];
-    if (!plan_rows(c.plan, c.in, N, l.vectors, ne[i], warps, stats, l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
-    const long long cost = price(c.plan, ne[i]);
-    if (best.ne == 0 || cost < least) {
-      best = c;
-      least = cost;
+  for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
+    for (int i = 0; i < K; ++i) {
+      Layout<N> c = {};
+      c.plan = plan;
+      std::copy(in, in + N, c.in);
+      c.ne = ne[i];
+      if (!plan_rows(c.plan, c.in, N, l.vectors, ctas, ne[i], stats, l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
+      const long long cost = price(c.plan, ne[i]);
+      if (best.ne == 0 || cost < least) {
+        best = c;
+        least = cost;
+      }
     }
   }
   return best;
@@ -783,7 +804,7 @@ Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (
 
 template <class T, int NE>
 int forward_form(const BlockArgs& a, const BlockLaunch& l, Layout<kInputs>& best) {
-  const int threads = a.plan.groups * a.plan.lanes + 32;
+  const int threads = cta_threads(a.plan);
   return l.aligned ? launch_rows<block_norm_kernel<T, NE, true>>(a, threads, l.device, &best.grid, best.bytes, l.stream)
                    : launch_rows<block_norm_kernel<T, NE, false>>(a, threads, l.device, &best.grid, best.bytes, l.stream);
 }
@@ -791,7 +812,7 @@ int forward_form(const BlockArgs& a, const BlockLaunch& l, Layout<kInputs>& best
 template <class T>
 int forward(BlockArgs& a, const BlockLaunch& l) {
   const int ne[3] = {8, 16, 32};
-  Layout<kInputs> best = best_layout(a.plan, a.in, ne, kForwardWarps, false, l);
+  Layout<kInputs> best = best_layout(a.plan, a.in, ne, false, l);
   ++*l.launches;
   if (best.ne == 0) {
     *l.kernel = "block_norm_wide_kernel";
@@ -807,8 +828,7 @@ int forward(BlockArgs& a, const BlockLaunch& l) {
 
 template <class T, int NE, bool LAYER, bool POST, bool CHANNEL>
 int gradient_form(const BlockGradArgs& a, const BlockLaunch& l, Layout<kGradInputs>& best) {
-  // warpgroups of threads that compute, and the producer's
-  const int threads = (a.plan.groups * a.plan.lanes + 127) / 128 * 128 + kProducerThreads;
+  const int threads = cta_threads(a.plan);
   return l.aligned ? launch_rows<block_norm_grad_kernel<T, NE, true, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
                                                                                             best.bytes, l.stream)
                    : launch_rows<block_norm_grad_kernel<T, NE, false, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
@@ -839,7 +859,7 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
       // 16 elements' sums of four or five vectors leave too few registers
       constexpr bool kTwo = !(kLayer && kPost);
       const int ne[2] = {8, kTwo ? 16 : 8};
-      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, kRowWarps, true, l);
+      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, true, l);
       c.ctas = best.ne ? best.grid / best.plan.ctas : static_cast<int>(std::min<long long>(a.plan.rows, 2LL * l.num_sms));
       if (a.sums) {
         a.partials = static_cast<float*>(acquire_scratch(

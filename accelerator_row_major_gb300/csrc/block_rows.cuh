@@ -8,8 +8,9 @@
 // its columns, where they are wide.  Lanes, groups, ring depth and cluster are
 // the launch's: a width costs the next whole warp, not the next power of 2.
 //
-// A stage of the ring holds a chunk: one row for each group, of consecutive
-// rows.  One more warp issues the copies, a lane for each matrix (or for each
+// The groups work on consecutive rows.  A stage of the ring holds a chunk of
+// them: a row where rows are long, so that no group waits for another, several
+// where they are short, so that the copies keep up.  One more warp issues the copies, a lane for each matrix (or for each
 // matrix and row, where rows do not lie one behind the other): as work of the
 // threads that compute, the copies' addresses were most of a row's time
 // (65536 x 1024 bfloat16 265 us, gradient 509, against @FWD@ and @GRAD@).
@@ -48,7 +49,7 @@ struct RingPlace {
   uint8_t* data;
   uint32_t full, empty;                  // barriers: the copies have landed; all warps have read
   int col0, width;                       // of this CTA's slice (no columns: width 0)
-  long long first, step;                 // of its chunks
+  long long first, step;                 // of its turns: a row for each group
 
   __device__ __forceinline__ RingPlace(const RowPlan& p, uint8_t* smem, int rank) {
     data = smem + p.ring_at;
@@ -63,11 +64,16 @@ struct RingPlace {
   __device__ __forceinline__ void init(const RowPlan& p) const {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(full + 8u * i, p.stats_at ? 33 : 1);        // the producer's lanes, where they copy statistics
-      mbar_init(empty + 8u * i, static_cast<uint32_t>(p.groups * (p.lanes / 32)));
+      mbar_init(empty + 8u * i, static_cast<uint32_t>(p.chunk * (p.lanes / 32)));
     }
     fence_mbar_init();
   }
 };
+
+// Bytes that a barrier's phase has to wait for besides.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 
 // 4 bytes of global memory into shared memory, and this thread's arrival at a
 // barrier once all such copies of its own have landed.
@@ -120,75 +126,69 @@ struct RowCopy {
 // flight.  It gives up at a wait that runs out (recorded), and in any case
 // waits, with a limit, for its last copies: none lands in memory that is no
 // longer the kernel's.  filled(): a barrier of the CTA, behind the first copies.
-// Statistics come the same way (those of stats_mask, rows of `rows` values):
-// loaded by the threads that use them, even a row ahead, they were what half
-// of the gradient's issue slots waited for.
-template <int N, class F>
+//
+// Each lane has one matrix's part of every chunk (a packed one's whole, of
+// others the row r; kMostChunk and kMostLoose see to it that there are enough
+// lanes) and one statistic, those of stats_mask, of one of its rows.  All but
+// the row's address is worked out before the loop: with it inside, reading the
+// matrices' descriptions by lane, a chunk took some 2700 clocks, more than
+// 32 KB of rows.  Loaded by the threads that use them, even a row ahead, the
+// statistics were what half of the gradient's issue slots waited for.
+// ALIGNED: all rows are whole blocks.
+template <bool ALIGNED, int N, class F>
 __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const RowPlan& plan, const RingPlace& ring,
                                              const float* stats, uint32_t stats_mask, unsigned* err, F filled) {
+  static_assert(N * kMostLoose <= 32 && kStats * kMostChunk <= 32, "a lane each");
+  const int lane = threadIdx.x & 31, row_of = lane / N;
+  RowSource m = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane % N == i) m = in[i];
+  const bool mine = m.p && row_of < (m.packed ? 1 : plan.chunk);
+  const uintptr_t base = mine ? first_byte(m, row_of, ring.col0) : 0;
+  const uint32_t row_bytes = mine ? source_bytes(m.size, ring.width) : 0;
+  const uint32_t more = m.packed ? m.pitch : 0;            // bytes of a further row of the chunk
+  uint8_t* const to = ring.data + m.at + (m.packed ? 0u : static_cast<uint32_t>(row_of) * m.pitch);
+  const bool stat = stats_mask >> (lane % kStats) & 1u;
+  const float* const stat_from = stats + (lane % kStats) * plan.rows + lane / kStats;
+  const uint32_t stat_to = smem_addr(ring.data) + plan.stats_at + 4u * lane;
   bool met = false;                      // the others, who fill the vectors under the first copies
-  const int lane = threadIdx.x & 31;
-  int s = 0, issued = 0;
+  int s = 0, issued = 0, sub = 0;
   uint32_t ph = 0;
-  for (long long chunk = ring.first; chunk * plan.groups < plan.rows; chunk += ring.step) {
+  for (long long turn = ring.first;;) {
+    const long long row0 = turn * plan.groups + sub;
+    if (row0 >= plan.rows) break;
+    const int rows = static_cast<int>(min(static_cast<long long>(plan.chunk), plan.rows - row0));
+    if ((sub += plan.chunk) == plan.groups) {
+      sub = 0;
+      turn += ring.step;
+    }
     if (!met && issued == plan.stages) {
       filled();
       met = true;
     }
     if (!__all_sync(0xFFFFFFFFu, mbar_wait(ring.empty + 8u * s, ph ^ 1u, err, kSiteProducerEmpty))) break;
-    const long long row0 = chunk * plan.groups;
-    const int rows = static_cast<int>(min(static_cast<long long>(plan.groups), plan.rows - row0));
-    uint8_t* const stage = ring.data + static_cast<size_t>(s) * plan.stage_bytes;
-    const uint32_t bar = ring.full + 8u * s;
-    // statistics: 4 bytes each, counted by the lanes' own arrivals
-    if (stats_mask) {
-      const uint32_t to = smem_addr(stage) + plan.stats_at;
-      for (int i = lane; i < kStats * rows; i += 32) {
-        const int k = i / rows, r = i - k * rows;
-        if (stats_mask >> k & 1u) copy_word(to + 4u * (r * kStats + k), stats + k * plan.rows + row0 + r);
-      }
+    const uint32_t bar = ring.full + 8u * s, offset = static_cast<uint32_t>(s) * plan.stage_bytes;
+    if (stats_mask) {                    // counted by the lanes' own arrivals
+      if (stat && lane / kStats < rows) copy_word(stat_to + offset, stat_from + row0);
       copies_arrive(bar);
     }
-    // lane i < N: matrix i's chunk, where it is one copy; then, matrix by
-    // matrix, the others' rows
-    const int mine = lane < N ? lane : 0;
-    const RowSource& m = in[mine];
-    const bool one = lane < N && m.p && m.packed;
-    const uintptr_t from = one ? first_byte(m, row0, ring.col0) : 0;
-    const RowCopy chunk_copy(m, stage + (one ? m.at : 0), from,
-                             one ? from + static_cast<uint32_t>(rows - 1) * m.pitch + source_bytes(m.size, ring.width) : from);
-    uint32_t bytes = chunk_copy.bytes();
-    bool rest = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) rest = rest || (in[i].p && !in[i].packed);
-    if (rest) {
-      for (int pass = 0; pass < 2; ++pass) {
-        if (pass == 1) {
-          __syncwarp();
-          bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);   // releases the elements copied here, too
-          __syncwarp();
-          chunk_copy.issue(bar);
-        }
-#pragma unroll 1
-        for (int i = 0; i < N; ++i) {
-          const RowSource& r = in[i];
-          if (!r.p || r.packed || lane >= rows) continue;
-          const uintptr_t at = first_byte(r, row0 + lane, ring.col0);
-          const RowCopy copy(r, stage + r.at + static_cast<uint32_t>(lane) * r.pitch, at,
-                             at + source_bytes(r.size, ring.width));
-          if (pass == 0)
-            bytes += copy.bytes();
-          else
-            copy.issue(bar);
-        }
-      }
+    const bool active = mine && (m.packed || row_of < rows);
+    const uintptr_t from = base + row0 * m.ld;
+    const uint32_t bytes = active ? row_bytes + static_cast<uint32_t>(rows - 1) * more : 0u;
+    if constexpr (ALIGNED) {
+      const uint32_t whole = (bytes + 15u) & ~15u;         // 8-bit rows are padded
+      const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, whole);
+      if (lane == 0) mbar_arrive_expect_tx(bar, all);
+      __syncwarp();
+      if (whole) bulk_load(smem_addr(to) + offset, reinterpret_cast<const void*>(from), whole, bar);
     } else {
+      const RowCopy copy(m, to + offset, active ? from : 0, active ? from + bytes : 0);
+      const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, copy.bytes());   // behind the elements copied here
       __syncwarp();
-      bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
-      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      if (lane == 0) mbar_arrive_expect_tx(bar, all);
       __syncwarp();
-      chunk_copy.issue(bar);
+      copy.issue(bar);
     }
     issued = min(issued + 1, plan.stages);
     if (++s == plan.stages) {
@@ -207,15 +207,18 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
   }
 }
 
-// A computing thread's view of the ring.
+// A computing thread's view of the ring: of its group's stages, every
+// groups / chunk'th.
 struct RingReader {
   const RingPlace& ring;
   const RowPlan& plan;
   unsigned* err;
-  int group, s = 0;
+  int at_row, s, step;                   // the group's row within the stage
   uint32_t ph = 0;
   bool lost = false;
 
+  __device__ __forceinline__ RingReader(const RingPlace& r, const RowPlan& p, unsigned* e, int group)
+      : ring(r), plan(p), err(e), at_row(group % p.chunk), s(group / p.chunk), step(p.groups / p.chunk) {}
   // A wait that runs out is recorded, and the thread goes on (the result is
   // undefined, as the status says): its group's barriers need all of it.
   __device__ __forceinline__ void wait() {
@@ -225,23 +228,23 @@ struct RingReader {
   __device__ __forceinline__ void release() {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(ring.empty + 8u * s);
-    if (++s == plan.stages) {
-      s = 0;
+    if ((s += step) >= plan.stages) {    // at least as many stages as steps
+      s -= plan.stages;
       ph ^= 1u;
     }
   }
   // The row's statistics.
   __device__ __forceinline__ float4 stats() const {
     return *reinterpret_cast<const float4*>(ring.data + static_cast<uint32_t>(s) * plan.stage_bytes + plan.stats_at +
-                                            static_cast<uint32_t>(group) * (kStats * 4u));
+                                            static_cast<uint32_t>(at_row) * (kStats * 4u));
   }
   // The group's row of a matrix in the current stage; what lies `shift` bytes
   // behind a 16-byte boundary in memory lies so in the stage.
   __device__ __forceinline__ const uint8_t* at(const RowSource& m, long long row, bool vec) const {
     const uint8_t* const p = ring.data + static_cast<uint32_t>(s) * plan.stage_bytes + m.at +
-                             static_cast<uint32_t>(group) * m.pitch;
+                             static_cast<uint32_t>(at_row) * m.pitch;
     if (vec) return p;
-    return p + (static_cast<uint32_t>(first_byte(m, m.packed ? row - group : row, ring.col0)) & 15u);
+    return p + (static_cast<uint32_t>(first_byte(m, m.packed ? row - at_row : row, ring.col0)) & 15u);
   }
 };
 
