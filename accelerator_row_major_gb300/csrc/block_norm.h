@@ -12,6 +12,7 @@
 namespace gemm_f32_impl {
 
 constexpr int kRowWarps = 16;            // that compute, at most
+constexpr int kProducers = 4;            // warps that fill the ring, at most
 constexpr int kMostCtas = 8;             // of a cluster
 constexpr int kStats = 4;                // per row: mean and rstd of h, of the branch
 constexpr int kMostChunk = 8;            // rows of a stage, where all rows lie one behind the other
@@ -35,6 +36,7 @@ struct RowPlan {
   int width, slice;                      // columns of a row, of a CTA's part
   int lanes, groups, stages, ctas;
   int chunk;                             // rows of a stage: a divisor of groups
+  int producers;                         // 4, 2 or 1, a divisor of stages
   uint32_t stage_bytes;
   uint32_t ring_at;                      // in dynamic shared memory, behind the weights
   uint32_t stats_at;                     // of the rows' statistics within a stage; 0: they do not come this way
@@ -83,7 +85,8 @@ struct BlockGradArgs {
   float alpha, beta;
   const float* stats;
   Output dbranch, dresidual, dgate;      // dgate: of a matrix
-  float* partials;                       // [CTA or cluster][sums][width]
+  float* partials;                       // [CTA or cluster][sums][ld_partials]
+  long long ld_partials;                 // width rounded up to 4
   int sum[kSums];                        // a vector's place in the partials, -1: not wanted
   int sums;
   unsigned* err;

@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <numeric>
 #include <type_traits>
 
 #include "../../include/gemm_f32_block.h"
@@ -44,23 +45,37 @@ __device__ __forceinline__ bool output_ok(const Output& o, const RowPlan& plan, 
                         kSiteBoundsRows);
 }
 
-// The vectors into shared memory, by the threads that compute.
+// The vectors into shared memory, by the threads that compute: of four columns
+// all vectors' values are on their way before the first is stored (value by
+// value, vector after vector, this took 5 us for each vector of 4096).
 template <class T, class Part>
-__device__ __forceinline__ void fill_vectors(float* columns, const VectorArgs& v, const RowPlan& plan,
+__device__ __forceinline__ void fill_vectors(float* columns, const VectorArgs& a, const RowPlan& plan,
                                              const RingPlace& ring) {
-  const int threads = plan.groups * plan.lanes;
+  const int threads = plan.groups * plan.lanes, slots = Part::slots(plan.lanes);
   if (static_cast<int>(threadIdx.x) >= threads) return;
-#pragma unroll 1
-  for (int i = 0; i < kVectors; ++i)
-    if (v.slot[i] >= 0)
-      fill_columns<T, Part>(columns + v.slot[i] * Part::slots(plan.lanes), v.p[i], v.f32,
-                            i == kWeight || i == kPostWeight ? 1.0f : 0.0f, plan.lanes, threads, ring.col0, ring.width);
+  for (int slot = 4 * threadIdx.x; slot < slots; slot += 4 * threads) {
+    float f[kVectors][4];
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v) {
+      if (a.slot[v] < 0) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = Part::column_of_slot(slot + j);
+        f[v][j] = c >= ring.width ? 0.0f
+                  : a.p[v]        ? vector_value<T>(a.p[v], a.f32, ring.col0 + c)
+                                  : (v == kWeight || v == kPostWeight ? 1.0f : 0.0f);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v)
+      if (a.slot[v] >= 0)
+        *reinterpret_cast<float4*>(columns + a.slot[v] * slots + slot) = make_float4(f[v][0], f[v][1], f[v][2], f[v][3]);
+  }
 }
 
 // 16 warps compute with 112 registers a thread, some of them left by the
-// warpgroup whose first warp is the producer: with that as a 17th warp of a
-// plain launch there would be 96.
-constexpr int kProducerThreads = 128;
+// warpgroup of the producers: in a plain launch of as many there would be 96.
+constexpr int kProducerThreads = 32 * kProducers;
 constexpr int kProducerRegisters = 32, kComputeRegisters = 112;
 static_assert(kProducerThreads * kProducerRegisters + 32 * kRowWarps * kComputeRegisters <=
                   96 * (kProducerThreads + 32 * kRowWarps),
@@ -72,10 +87,8 @@ template <bool ALIGNED, int N>
 __device__ __forceinline__ void producer_warps(const RowSource (&in)[N], const RowPlan& plan, const RingPlace& ring,
                                                const float* stats, uint32_t stats_mask, unsigned* err) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegisters));
-  if (threadIdx.x < blockDim.x - kProducerThreads + 32)
-    produce_rows<ALIGNED>(in, plan, ring, stats, stats_mask, err, [] { __syncthreads(); });
-  else
-    __syncthreads();
+  const int warp = static_cast<int>(threadIdx.x - (blockDim.x - kProducerThreads)) / 32;
+  produce_rows<ALIGNED>(in, plan, ring, stats, stats_mask, err, warp, [] { __syncthreads(); });
   if (plan.ctas > 1) cluster_sync();
 }
 
@@ -107,7 +120,8 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
   float* const columns = reinterpret_cast<float*>(smem_rows);
   fill_vectors<T, Part>(columns, a.vectors, plan, ring);
   __syncthreads();
-  const Part mine(t, plan.lanes, ring.width);
+  const Part mine(t, ring.width);
+  const bool full = mine.full();
   const float inv = 1.0f / static_cast<float>(plan.width);
   const auto vector = [&](int v) { return columns + a.vectors.slot[v] * Part::slots(plan.lanes); };
   RowSums sums = {shared, plan, a.err, group, t, rank};
@@ -123,11 +137,10 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
       sums.add<1>(s);
       mean = s[0] * inv;
 #pragma unroll
-      for (int v = 0; v < NC; ++v) {
-        Pair(&c)[CP] = *reinterpret_cast<Pair(*)[CP]>(&x[v * CP]);
+      for (int j = 0; j < NP; ++j) x[j] = add2(x[j], both(-mean));
+      if (!full) {
 #pragma unroll
-        for (int j = 0; j < CP; ++j) c[j] = add2(c[j], both(-mean));
-        mine.drop(v, c);
+        for (int v = 0; v < NC; ++v) mine.drop(v, x + v * CP);
       }
     }
     Pair sum = 0;
@@ -137,18 +150,37 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     sums.add<1>(s);
     rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
   };
-  // a chunk of x rstd times a vector, plus another where it is there
-  const auto scale = [&](int v, Pair(&x)[CP], float rstd, int weight, int bias) {
-    Pair w[CP];
-    mine.columns(vector(weight), v, w);
+  // f(j, value) for every pair of elements, of a vector or of a row
+  const auto each = [&](int vector_at, auto f) {
+    const float* const from = vector(vector_at);
 #pragma unroll
-    for (int j = 0; j < CP; ++j) x[j] = mul2(mul2(x[j], both(rstd)), w[j]);
-    if (a.vectors.slot[bias] < 0) return;
-    mine.columns(vector(bias), v, w);
+    for (int v = 0; v < NC; ++v) {
+      Pair w[CP];
+      mine.columns(from, v, w);
 #pragma unroll
-    for (int j = 0; j < CP; ++j) x[j] = add2(x[j], w[j]);
+      for (int k = 0; k < CP; ++k) f(v * CP + k, w[k]);
+    }
   };
-  const auto chunk = [](Pair(&x)[NP], int v) -> Pair(&)[CP] { return *reinterpret_cast<Pair(*)[CP]>(&x[v * CP]); };
+  const auto each_of = [&](const uint8_t* row, auto f) {
+#pragma unroll
+    for (int v = 0; v < NC; ++v) {
+      Pair w[CP];
+      mine.load(row, v, w);
+#pragma unroll
+      for (int k = 0; k < CP; ++k) f(v * CP + k, w[k]);
+    }
+  };
+  const auto store = [&](const Output& o, long long row, const Pair(&x)[NP]) {
+    if (!o.p || !output_ok<T>(o, plan, row, a.err)) return;
+    T* const to = static_cast<T*>(o.p) + row * o.ld + ring.col0;
+#pragma unroll
+    for (int v = 0; v < NC; ++v) {
+      Pair w[CP];
+#pragma unroll
+      for (int k = 0; k < CP; ++k) w[k] = x[v * CP + k];
+      mine.store(to, v, w);
+    }
+  };
 
   RingReader reader(ring, plan, a.err, group);
   long long row = group < plan.groups ? ring.first * plan.groups + group : plan.rows;
@@ -156,43 +188,24 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     reader.wait();
     Pair x[NP];
     float mean, rstd, mean_b = 0.0f, rstd_b = 0.0f;
-    const uint8_t* const branch = reader.at(a.in[kInBranch], row, VEC);
-    const uint8_t* const residual = reader.at(a.in[kInResidual], row, VEC);
-    const uint8_t* const gate = a.gate == kElementGate ? reader.at(a.in[kInGate], row, VEC) : nullptr;
-#pragma unroll
-    for (int v = 0; v < NC; ++v) mine.load(branch, v, chunk(x, v));
-    if (a.post) normalise(x, mean_b, rstd_b);
-#pragma unroll
-    for (int v = 0; v < NC; ++v) {
-      Pair(&p)[CP] = chunk(x, v);
-      Pair w[CP];
-      if (a.post) scale(v, p, rstd_b, kPostWeight, kPostBias);
-      if (a.gate != kNoGate) {
-        if (a.gate == kElementGate)
-          mine.load(gate, v, w);
-        else
-          mine.columns(vector(kGateVector), v, w);
-#pragma unroll
-        for (int j = 0; j < CP; ++j) p[j] = mul2(p[j], w[j]);
-      }
-      mine.load(residual, v, w);
-#pragma unroll
-      for (int j = 0; j < CP; ++j) p[j] = fma2(p[j], both(a.beta), mul2(w[j], both(a.alpha)));
+    each_of(reader.at(a.in[kInBranch], row, VEC), [&](int j, Pair v) { x[j] = v; });
+    if (a.post) {
+      normalise(x, mean_b, rstd_b);
+      each(kPostWeight, [&](int j, Pair w) { x[j] = mul2(mul2(x[j], both(rstd_b)), w); });
+      if (a.vectors.slot[kPostBias] >= 0) each(kPostBias, [&](int j, Pair w) { x[j] = add2(x[j], w); });
     }
+    if (a.gate == kElementGate)
+      each_of(reader.at(a.in[kInGate], row, VEC), [&](int j, Pair w) { x[j] = mul2(x[j], w); });
+    else if (a.gate == kChannelGate)
+      each(kGateVector, [&](int j, Pair w) { x[j] = mul2(x[j], w); });
+    each_of(reader.at(a.in[kInResidual], row, VEC),
+            [&](int j, Pair w) { x[j] = fma2(x[j], both(a.beta), mul2(w, both(a.alpha))); });
     reader.release();
-    // an h that is an input: all of this row has been read
-    if (a.h.p && output_ok<T>(a.h, plan, row, a.err)) {
-#pragma unroll
-      for (int v = 0; v < NC; ++v) mine.store(static_cast<T*>(a.h.p) + row * a.h.ld + ring.col0, v, chunk(x, v));
-    }
+    store(a.h, row, x);                  // an h that is an input: all of this row has been read
     normalise(x, mean, rstd);
-    if (output_ok<T>(a.y, plan, row, a.err)) {
-#pragma unroll
-      for (int v = 0; v < NC; ++v) {
-        scale(v, chunk(x, v), rstd, kWeight, kBias);
-        mine.store(static_cast<T*>(a.y.p) + row * a.y.ld + ring.col0, v, chunk(x, v));
-      }
-    }
+    each(kWeight, [&](int j, Pair w) { x[j] = mul2(mul2(x[j], both(rstd)), w); });
+    if (a.vectors.slot[kBias] >= 0) each(kBias, [&](int j, Pair w) { x[j] = add2(x[j], w); });
+    store(a.y, row, x);
     if (t == 0 && rank == 0 && a.stats) {
       a.stats[row] = mean;
       a.stats[plan.rows + row] = rstd;
@@ -236,16 +249,43 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
   float* const columns = reinterpret_cast<float*>(smem_rows);
   fill_vectors<T, Part>(columns, a.vectors, plan, ring);
   __syncthreads();
-  const Part mine(t, plan.lanes, ring.width);
+  const Part mine(t, ring.width);
+  const bool full = mine.full();
   const float inv = 1.0f / static_cast<float>(plan.width);
   const auto vector = [&](int v) { return columns + a.vectors.slot[v] * Part::slots(plan.lanes); };
   RowSums sums = {shared, plan, a.err, group, t, rank};
-  const bool gated = CHANNEL || a.gate == kElementGate, branch = POST || gated;
   Pair total[kSums][NP];
 #pragma unroll
   for (int k = 0; k < kSums; ++k)
 #pragma unroll
     for (int j = 0; j < NP; ++j) total[k][j] = 0;
+  // The two means over the row of a norm's gradient: of the gradients `ones`
+  // and, along hat, of their products, as factors of 1 and of c.
+  const auto means = [&](Pair ones, Pair along, float by, float& c1, float& c2) {
+    const float s = by != 0.0f ? sum_of(along) * by : 0.0f;
+    if constexpr (LAYER) {
+      float v[2] = {sum_of(ones), s};
+      sums.add<2>(v);
+      c1 = -v[0] * inv;
+      c2 = -v[1] * inv * by;
+    } else {
+      float v[1] = {s};
+      sums.add<1>(v);
+      c1 = 0.0f;
+      c2 = -v[0] * inv * by;
+    }
+  };
+  const auto store = [&](const Output& o, long long row, const Pair(&x)[NP], float by) {
+    if (!o.p || !output_ok<T>(o, plan, row, a.err)) return;
+    T* const to = static_cast<T*>(o.p) + row * o.ld + ring.col0;
+#pragma unroll
+    for (int v = 0; v < NC; ++v) {
+      Pair w[CP];
+#pragma unroll
+      for (int k = 0; k < CP; ++k) w[k] = mul2(x[v * CP + k], both(by));
+      mine.store(to, v, w);
+    }
+  };
 
   RingReader reader(ring, plan, a.err, group);
   const long long step = ring.step * plan.groups;
@@ -254,23 +294,29 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     reader.wait();
     const float4 stats = reader.stats();
     const float mean = stats.x, rstd = stats.y, mean_b = stats.z, rstd_b = stats.w;
+    // a row of h or of the branch, as it is or in 8 bits: f(chunk's loader)
+    const auto rows_of = [&](int at, int exponents_at, auto f) {
+      if (a.in[exponents_at].p) {
+        const uint8_t* const codes = reader.at(a.in[at], row, true);
+        const uint8_t* const exponents = reader.at(a.in[exponents_at], row, true);
+        f([&](int v, Pair(&x)[CP]) { mine.load_saved(codes, exponents, v, x); });
+      } else {
+        const uint8_t* const from = reader.at(a.in[at], row, VEC);
+        f([&](int v, Pair(&x)[CP]) { mine.load(from, v, x); });
+      }
+    };
     // c = h - mean in place of hat = c rstd: where rstd is 0 (squares that
     // overflowed) or c is, hat is 0 and never 0 times infinity
     Pair c[NP], g[NP], sg = 0, sgc = 0;
-    {
+    rows_of(kGradH, kGradHExponents, [&](auto load_h) {
       const uint8_t* const dy = reader.at(a.in[kGradDy], row, VEC);
-      const bool saved = a.in[kGradHExponents].p != nullptr;
-      const uint8_t* const h = reader.at(a.in[kGradH], row, VEC || saved);
-      const uint8_t* const exponents = saved ? reader.at(a.in[kGradHExponents], row, true) : nullptr;
+      const float* const weight = vector(kWeight);
 #pragma unroll
       for (int v = 0; v < NC; ++v) {
         Pair x[CP], y[CP], w[CP];
-        if (saved)
-          mine.load_saved(h, exponents, v, x);
-        else
-          mine.load(h, v, x);
+        load_h(v, x);
         mine.load(dy, v, y);
-        mine.columns(vector(kWeight), v, w);
+        mine.columns(weight, v, w);
 #pragma unroll
         for (int k = 0; k < CP; ++k) {
           const int j = v * CP + k;
@@ -282,68 +328,51 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
           sgc = fma2(g[j], c[j], sgc);
         }
       }
-    }
-    // a norm's two means over the row: of its gradients and, along hat, of
-    // their products, with the factors that they get
-    const auto means = [&](Pair ones, Pair along, float by, float& c1, float& c2) {
-      const float s = by != 0.0f ? sum_of(along) * by : 0.0f;
-      if constexpr (LAYER) {
-        float v[2] = {sum_of(ones), s};
-        sums.add<2>(v);
-        c1 = -v[0] * inv;
-        c2 = -v[1] * inv * by;
-      } else {
-        float v[1] = {s};
-        sums.add<1>(v);
-        c1 = 0.0f;
-        c2 = -v[0] * inv * by;
-      }
-    };
+    });
     float c1, c2;
     means(sg, sgc, rstd, c1, c2);
-    Pair(&d)[NP] = g;                    // in place of g, as the branch's rows are of h's
-    Pair(&b)[NP] = c;
-    {
-      const uint8_t* const dh = a.in[kGradDh].p ? reader.at(a.in[kGradDh], row, VEC) : nullptr;
-      T* const to = static_cast<T*>(a.dresidual.p) + row * a.dresidual.ld + ring.col0;
-      const bool store = a.dresidual.p && output_ok<T>(a.dresidual, plan, row, a.err);
+    Pair(&d)[NP] = g;                    // in place of g
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      if (LAYER) g[j] = add2(g[j], both(c1));
+      d[j] = mul2(fma2(c[j], both(c2), g[j]), both(rstd));
+    }
+    if (a.in[kGradDh].p) {
+      const uint8_t* const dh = reader.at(a.in[kGradDh], row, VEC);
 #pragma unroll
       for (int v = 0; v < NC; ++v) {
         Pair x[CP];
+        mine.load(dh, v, x);
 #pragma unroll
-        for (int k = 0; k < CP; ++k) x[k] = 0;
-        if (dh) mine.load(dh, v, x);
-#pragma unroll
-        for (int k = 0; k < CP; ++k) {
-          const int j = v * CP + k;
-          if (LAYER) g[j] = add2(g[j], both(c1));
-          d[j] = fma2(fma2(c[j], both(c2), g[j]), both(rstd), x[k]);
-          x[k] = mul2(d[j], both(a.alpha));
-          d[j] = mul2(d[j], both(a.beta));
-        }
-        // an output that is an input: this row's part of it has been read, but for the gate's and the branch's
-        if (store) mine.store(to, v, x);
+        for (int k = 0; k < CP; ++k) d[v * CP + k] = add2(d[v * CP + k], x[k]);
       }
     }
-    if (branch) {
-      const bool saved = a.in[kGradBranchExponents].p != nullptr;
-      const uint8_t* const from = reader.at(a.in[kGradBranch], row, VEC || saved);
-      const uint8_t* const exponents = saved ? reader.at(a.in[kGradBranchExponents], row, true) : nullptr;
-      const uint8_t* const gate = a.gate == kElementGate ? reader.at(a.in[kGradGate], row, VEC) : nullptr;
+    // an output that is an input: the ring has all of this row
+    store(a.dresidual, row, d, a.alpha);
+    if (!(POST || CHANNEL) && a.gate == kNoGate) {
+      reader.release();
+      store(a.dbranch, row, d, a.beta);
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) d[j] = mul2(d[j], both(a.beta));
+    if (!full) {
+#pragma unroll
+      for (int v = 0; v < NC; ++v) mine.drop(v, d + v * CP);
+    }
+    Pair(&b)[NP] = c;                    // the branch's rows in place of h's
+    Pair se = 0, seb = 0;
+    const auto through_gate = [&](auto load_branch, auto element) {
+      constexpr bool kElement = decltype(element)::value, kGated = CHANNEL || kElement;
+      const bool bias = POST && LAYER && kGated && a.vectors.slot[kPostBias] >= 0;
+      const uint8_t* const gate = kElement ? reader.at(a.in[kGradGate], row, VEC) : nullptr;
       T* const to = static_cast<T*>(a.dgate.p) + row * a.dgate.ld + ring.col0;
-      const bool store = a.dgate.p && output_ok<T>(a.dgate, plan, row, a.err);
-      Pair se = 0, seb = 0;
+      const bool stores = kElement && a.dgate.p && output_ok<T>(a.dgate, plan, row, a.err);
 #pragma unroll
       for (int v = 0; v < NC; ++v) {
-        Pair x[CP], w[CP], p[CP];
-        if (saved)
-          mine.load_saved(from, exponents, v, x);
-        else
-          mine.load(from, v, x);
-        Pair e[CP];
-#pragma unroll
-        for (int k = 0; k < CP; ++k) e[k] = d[v * CP + k];
-        mine.drop(v, e);
+        Pair x[CP], w[CP];
+        Pair* const e = d + v * CP;
+        load_branch(v, x);
         if (POST) {
           mine.columns(vector(kPostWeight), v, w);
           if (LAYER) {
@@ -351,11 +380,11 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
             for (int k = 0; k < CP; ++k) x[k] = add2(x[k], both(-mean_b));
           }
         }
-        if (gated) {
+        if (kGated) {
+          Pair p[CP], by[CP];
 #pragma unroll
           for (int k = 0; k < CP; ++k) p[k] = POST ? mul2(mul2(x[k], both(rstd_b)), w[k]) : x[k];
-          Pair by[CP];
-          if (POST && LAYER && a.vectors.slot[kPostBias] >= 0) {
+          if (bias) {
             mine.columns(vector(kPostBias), v, by);
 #pragma unroll
             for (int k = 0; k < CP; ++k) p[k] = add2(p[k], by[k]);
@@ -372,12 +401,12 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
               p[k] = mul2(e[k], p[k]);
             e[k] = mul2(e[k], by[k]);
           }
-          if (!CHANNEL && store) mine.store(to, v, p);
+          if (stores) mine.store(to, v, p);
         }
+        if (POST) {
 #pragma unroll
-        for (int k = 0; k < CP; ++k) {
-          const int j = v * CP + k;
-          if (POST) {
+          for (int k = 0; k < CP; ++k) {
+            const int j = v * CP + k;
             b[j] = x[k];
             total[kSumPostWeight][j] = fma2(mul2(e[k], both(rstd_b)), x[k], total[kSumPostWeight][j]);
             if (LAYER) total[kSumPostBias][j] = add2(total[kSumPostBias][j], e[k]);
@@ -385,61 +414,68 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
             if (LAYER) se = add2(se, e[k]);
             seb = fma2(e[k], x[k], seb);
           }
-          d[j] = e[k];
         }
       }
-      reader.release();
-      if (POST) {
-        means(se, seb, rstd_b, c1, c2);
+    };
+    rows_of(kGradBranch, kGradBranchExponents, [&](auto load_branch) {
+      if (!CHANNEL && a.gate == kElementGate)
+        through_gate(load_branch, std::integral_constant<bool, !CHANNEL>{});
+      else
+        through_gate(load_branch, std::false_type{});
+    });
+    reader.release();
+    if (POST) {
+      means(se, seb, rstd_b, c1, c2);
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          if (LAYER) d[j] = add2(d[j], both(c1));
-          d[j] = mul2(fma2(b[j], both(c2), d[j]), both(rstd_b));
-        }
+      for (int j = 0; j < NP; ++j) {
+        if (LAYER) d[j] = add2(d[j], both(c1));
+        d[j] = fma2(b[j], both(c2), d[j]);
       }
+      store(a.dbranch, row, d, rstd_b);
     } else {
-      reader.release();
-    }
-    if (a.dbranch.p && output_ok<T>(a.dbranch, plan, row, a.err)) {
-#pragma unroll
-      for (int v = 0; v < NC; ++v) {
-        Pair x[CP];
-#pragma unroll
-        for (int k = 0; k < CP; ++k) x[k] = d[v * CP + k];
-        mine.store(static_cast<T*>(a.dbranch.p) + row * a.dbranch.ld + ring.col0, v, x);
-      }
+      store(a.dbranch, row, d, 1.0f);
     }
   }
   if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
   if (!a.sums) return;
-  // the groups' sums, added in group order: one row of partials per CTA (or
-  // cluster) and vector; what was the ring makes room
+  // The groups' sums, added in group order: one row of partials per CTA (or
+  // cluster) and vector; what was the ring makes room for those of all groups.
   const int threads = static_cast<int>(blockDim.x) - kProducerThreads, slots = Part::slots(plan.lanes);
   const auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"n"(kComputeBarrier), "r"(threads) : "memory"); };
+  meet();
+  if (group < plan.groups) {
 #pragma unroll
-  for (int k = 0; k < kSums; ++k) {
-    const bool there = k == kSumWeight || (k == kSumBias && LAYER) || (k == kSumGate && CHANNEL) ||
-                       (k == kSumPostWeight && POST) || (k == kSumPostBias && POST && LAYER);
-    if (!there || a.sum[k] < 0) continue;
-    meet();
-    if (group < plan.groups) {
+    for (int k = 0; k < kSums; ++k) {
+      const bool there = k == kSumWeight || (k == kSumBias && LAYER) || (k == kSumGate && CHANNEL) ||
+                         (k == kSumPostWeight && POST) || (k == kSumPostBias && POST && LAYER);
+      if (!there || a.sum[k] < 0) continue;
 #pragma unroll
       for (int q = 0; q < NE / 4; ++q) {
         float4 f;
         unpair(total[k][2 * q], f.x, f.y);
         unpair(total[k][2 * q + 1], f.z, f.w);
-        *reinterpret_cast<float4*>(mine.quad(columns + group * slots, q)) = f;
+        *reinterpret_cast<float4*>(columns + (a.sum[k] * plan.groups + group) * slots + mine.slot(q)) = f;
       }
     }
-    meet();
-    float* const to = a.partials +
-                      (static_cast<size_t>(blockIdx.x / plan.ctas) * a.sums + a.sum[k]) * plan.width + ring.col0;
-    for (int slot = threadIdx.x; slot < slots; slot += threads) {
-      const int col = Part::column_of_slot(slot, plan.lanes);
-      if (col >= ring.width) continue;
-      float v = columns[slot];
-      for (int i = 1; i < plan.groups; ++i) v += columns[i * slots + slot];
-      to[col] = v;
+  }
+  meet();
+  float* const to = a.partials + static_cast<size_t>(blockIdx.x / plan.ctas) * a.sums * a.ld_partials + ring.col0;
+  for (int k = 0; k < a.sums; ++k) {
+    for (int slot = 4 * threadIdx.x; slot < slots; slot += 4 * threads) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i = 0; i < plan.groups; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(columns + (k * plan.groups + i) * slots + slot);
+        v.x += f.x;
+        v.y += f.y;
+        v.z += f.z;
+        v.w += f.w;
+      }
+      const float values[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = Part::column_of_slot(slot + j);
+        if (col < ring.width) to[k * a.ld_partials + col] = values[j];
+      }
     }
   }
 }
@@ -465,7 +501,7 @@ template <class T>
 __device__ __forceinline__ float vector_at(const VectorArgs& a, int v, int d) {
   if (a.slot[v] < 0) return 0.0f;
   if (!a.p[v]) return v == kWeight || v == kPostWeight ? 1.0f : 0.0f;
-  return a.f32 ? __ldg(static_cast<const float*>(a.p[v]) + d) : to_f32(static_cast<const T*>(a.p[v])[d]);
+  return vector_value<T>(a.p[v], a.f32, d);
 }
 
 template <int N>
@@ -594,7 +630,7 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_grad_wide_kernel(cons
       const float p = a.post ? b * rstd_b * pw + vector_at<T>(a.vectors, kPostBias, d) : b;
       auto add = [&](int k, float v) {
         if (a.sum[k] < 0) return;
-        float* const to = a.partials + (static_cast<size_t>(blockIdx.x) * a.sums + a.sum[k]) * width + d;
+        float* const to = a.partials + (static_cast<size_t>(blockIdx.x) * a.sums + a.sum[k]) * a.ld_partials + d;
         *to = row == blockIdx.x ? v : *to + v;
       };
       add(kSumWeight, dy * rstd * c);
@@ -614,42 +650,55 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_grad_wide_kernel(cons
 }
 
 // ---------------------------------------------------------------- vectors' gradients
-// Partial sums of 32 columns of one vector per CTA, added in CTA order: 32
-// chains of every 32nd CTA, then the chains in order.
+// Partial sums of 128 columns of one vector: chains of every 16th CTA, then the
+// chains in order.
 struct ColumnArgs {
   const float* partials;
+  long long ld;
   void* out[kSums];                      // by their place in the partials
   int sums, ctas, width;
 };
 
+constexpr int kColumnChains = 16;
+
 template <class WT>
-__global__ void __launch_bounds__(1024) block_columns_kernel(const ColumnArgs a) {
-  __shared__ float chains[32][33];
+__global__ void __launch_bounds__(32 * kColumnChains) block_columns_kernel(const __grid_constant__ ColumnArgs a) {
+  __shared__ float4 chains[kColumnChains][32];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, chain = threadIdx.x >> 5;
-  const int k = blockIdx.y;
-  const long long d = blockIdx.x * 32LL + lane;
-  float v = 0.0f;
-  if (d < a.width)
-    for (int c = chain; c < a.ctas; c += 32) v += __ldcg(a.partials + (static_cast<size_t>(c) * a.sums + k) * a.width + d);
+  const int lane = threadIdx.x & 31, chain = threadIdx.x >> 5, k = blockIdx.y;
+  const long long d = blockIdx.x * 128LL + 4 * lane;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (d < a.width) {                     // a row of partials has whole vectors
+    const float* from = a.partials + (static_cast<size_t>(chain) * a.sums + k) * a.ld + d;
+#pragma unroll 10
+    for (int c = chain; c < a.ctas; c += kColumnChains, from += kColumnChains * a.sums * a.ld) {
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(from));
+      v.x += f.x;
+      v.y += f.y;
+      v.z += f.z;
+      v.w += f.w;
+    }
+  }
   chains[chain][lane] = v;
   __syncthreads();
-  float s[1] = {chains[lane][chain]};    // lane: the chain
-  warp_sum<1>(s);
-  const long long to = blockIdx.x * 32LL + chain;
-  if (lane == 0 && to < a.width) static_cast<WT*>(a.out[k])[to] = from_f32<WT>(s[0]);
+  if (threadIdx.x < 128 && blockIdx.x * 128LL + threadIdx.x < a.width) {
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kColumnChains; ++c) s += reinterpret_cast<const float*>(chains[c])[threadIdx.x];
+    static_cast<WT*>(a.out[k])[blockIdx.x * 128LL + threadIdx.x] = from_f32<WT>(s);
+  }
 }
 
 // ---------------------------------------------------------------- host side
 constexpr size_t kMostShared = 220 * 1024;   // dynamic; RowShared fits beside it
 constexpr int kMostStages = 16;
-constexpr size_t kLeastChunk = 8 * 1024;     // bytes of a stage, where there are rows enough
+constexpr size_t kLeastChunk = 16 * 1024;    // bytes of a stage, where there are rows enough
 
 // Lays out the rows of `in` over `ctas` CTAs and lanes of `ne` elements,
 // groups and ring; false where that cannot be.
-bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int ne, bool stats, bool aligned, int num_sms,
-               size_t* bytes, int* grid) {
+bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int ne, bool stats, int sums, bool aligned,
+               int num_sms, size_t* bytes, int* grid) {
   const int slice = ctas == 1 ? plan.width : ((plan.width - 1) / ctas / kSliceUnit + 1) * kSliceUnit;
   if (ctas > num_sms || slice > kRowWarps * 32 * ne) return false;
   plan.ctas = ctas;
@@ -685,13 +734,20 @@ bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int n
     if (stages >= 2u * (plan.groups / plan.chunk) || plan.groups == 1) break;
   }
   if (stages < 2) return false;
-  plan.stages = static_cast<int>(std::min<size_t>(stages, std::max(kMostStages, 2 * plan.groups / plan.chunk)));
+  // a multiple of the chunks of a turn, and of as many producers as cost no more than a quarter of the stages
+  const int step = plan.groups / plan.chunk;
+  const int most = static_cast<int>(std::min<size_t>(stages, std::max(kMostStages, 2 * step)));
+  for (plan.producers = kProducers; plan.producers >= 1; plan.producers /= 2) {
+    const int unit = std::lcm(step, plan.producers);
+    plan.stages = most / unit * unit;
+    if (plan.stages >= 2 * step && (4 * plan.stages >= 3 * most || plan.producers == 1)) break;
+  }
   plan.stage_bytes = static_cast<uint32_t>(stage);
   plan.ring_at = static_cast<uint32_t>(columns);
   *grid = static_cast<int>(std::min<long long>(units, (plan.rows - 1) / plan.groups + 1)) * ctas;
   // the groups' sums take the place of the ring
   *bytes = std::max(columns + static_cast<size_t>(plan.stages) * (stage + 16),
-                    static_cast<size_t>(plan.groups) * ne * plan.lanes * sizeof(float));
+                    static_cast<size_t>(sums) * plan.groups * ne * plan.lanes * sizeof(float));
   return true;
 }
 
@@ -782,7 +838,8 @@ struct Layout {
 // The cheapest of the layouts with `ne[i]` elements a thread; ne 0: there is
 // none.
 template <int N, int K>
-Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], bool stats, const BlockLaunch& l) {
+Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], bool stats, int sums,
+                      const BlockLaunch& l) {
   Layout<N> best = {};
   long long least = 0;
   for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
@@ -791,7 +848,7 @@ Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (
       c.plan = plan;
       std::copy(in, in + N, c.in);
       c.ne = ne[i];
-      if (!plan_rows(c.plan, c.in, N, l.vectors, ctas, ne[i], stats, l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
+      if (!plan_rows(c.plan, c.in, N, l.vectors, ctas, ne[i], stats, sums, l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
       const long long cost = price(c.plan, ne[i]);
       if (best.ne == 0 || cost < least) {
         best = c;
@@ -812,7 +869,7 @@ int forward_form(const BlockArgs& a, const BlockLaunch& l, Layout<kInputs>& best
 template <class T>
 int forward(BlockArgs& a, const BlockLaunch& l) {
   const int ne[3] = {8, 16, 32};
-  Layout<kInputs> best = best_layout(a.plan, a.in, ne, false, l);
+  Layout<kInputs> best = best_layout(a.plan, a.in, ne, false, 0, l);
   ++*l.launches;
   if (best.ne == 0) {
     *l.kernel = "block_norm_wide_kernel";
@@ -847,6 +904,7 @@ template <class T>
 int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLaunch& l) {
   ColumnArgs c = {};
   c.width = a.plan.width;
+  c.ld = a.ld_partials = (a.plan.width + 3LL) / 4 * 4;
   for (int k = 0; k < kSums; ++k) {
     a.sum[k] = vectors_out[k] ? a.sums++ : -1;
     if (vectors_out[k]) c.out[a.sum[k]] = vectors_out[k];
@@ -859,11 +917,11 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
       // 16 elements' sums of four or five vectors leave too few registers
       constexpr bool kTwo = !(kLayer && kPost);
       const int ne[2] = {8, kTwo ? 16 : 8};
-      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, true, l);
+      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, true, a.sums, l);
       c.ctas = best.ne ? best.grid / best.plan.ctas : static_cast<int>(std::min<long long>(a.plan.rows, 2LL * l.num_sms));
       if (a.sums) {
         a.partials = static_cast<float*>(acquire_scratch(
-            l.device, l.stream, sizeof(float) * static_cast<size_t>(c.ctas) * a.sums * a.plan.width));
+            l.device, l.stream, sizeof(float) * static_cast<size_t>(c.ctas) * a.sums * a.ld_partials));
         if (!a.partials) return GEMM_F32_ESCRATCH;
       }
       ++*l.launches;
@@ -883,9 +941,9 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
   if (rc == GEMM_F32_OK && a.sums) {
     c.partials = a.partials;
     c.sums = a.sums;
-    const dim3 blocks(static_cast<unsigned>((c.width + 31LL) / 32), a.sums);
-    rc = l.weights_f32 ? launch_plain(block_columns_kernel<float>, blocks, 1024, l.stream, c)
-                       : launch_plain(block_columns_kernel<T>, blocks, 1024, l.stream, c);
+    const dim3 blocks(static_cast<unsigned>((c.width + 127LL) / 128), a.sums);
+    rc = l.weights_f32 ? launch_plain(block_columns_kernel<float>, blocks, 32 * kColumnChains, l.stream, c)
+                       : launch_plain(block_columns_kernel<T>, blocks, 32 * kColumnChains, l.stream, c);
     ++*l.launches;
   }
   return rc;

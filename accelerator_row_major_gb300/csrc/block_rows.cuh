@@ -10,7 +10,7 @@
 //
 // The groups work on consecutive rows.  A stage of the ring holds a chunk of
 // them: a row where rows are long, so that no group waits for another, several
-// where they are short, so that the copies keep up.  One more warp issues the copies, a lane for each matrix (or for each
+// where they are short, so that the copies keep up.  Warps of their own issue the copies, a lane for each matrix (or for each
 // matrix and row, where rows do not lie one behind the other): as work of the
 // threads that compute, the copies' addresses were most of a row's time
 // (65536 x 1024 bfloat16 265 us, gradient 509, against @FWD@ and @GRAD@).
@@ -122,22 +122,27 @@ struct RowCopy {
   }
 };
 
-// The producer warp's work: all of the CTA's chunks, `stages` of them in
-// flight.  It gives up at a wait that runs out (recorded), and in any case
-// waits, with a limit, for its last copies: none lands in memory that is no
-// longer the kernel's.  filled(): a barrier of the CTA, behind the first copies.
+// The work of producer warp `warp`: every plan.producers'th of the CTA's
+// chunks, `stages` of all of them in flight.  A wait for a barrier's phase
+// passes wrongly when the barrier is a whole phase behind, so each stage has
+// one producer and the groups of one chunk: the producers and the chunks of a
+// turn (groups / chunk) divide the stages, and whoever waits for a stage's
+// phase has seen the phase before it.  A producer gives up at a wait that runs out
+// (recorded), and in any case waits, with a limit, for its last copies: none
+// lands in memory that is no longer the kernel's.  filled(): a barrier of the
+// CTA, behind the first copies.
 //
-// Each lane has one matrix's part of every chunk (a packed one's whole, of
-// others the row r; kMostChunk and kMostLoose see to it that there are enough
-// lanes) and one statistic, those of stats_mask, of one of its rows.  All but
-// the row's address is worked out before the loop: with it inside, reading the
-// matrices' descriptions by lane, a chunk took some 2700 clocks, more than
-// 32 KB of rows.  Loaded by the threads that use them, even a row ahead, the
-// statistics were what half of the gradient's issue slots waited for.
+// Each lane has one matrix's part of a chunk (a packed one's whole, of others
+// the row r; kMostChunk and kMostLoose see to it that there are enough lanes)
+// and one statistic, those of stats_mask, of one of its rows.  A chunk takes a
+// warp some 900 clocks (bulk copies of different lanes go one after the other):
+// one producer for chunks of one row of 1024 columns made the gradient of
+// 65536 of them 212 us.  Statistics that the threads loaded by themselves,
+// even a row ahead, were what half of its issue slots waited for.
 // ALIGNED: all rows are whole blocks.
 template <bool ALIGNED, int N, class F>
 __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const RowPlan& plan, const RingPlace& ring,
-                                             const float* stats, uint32_t stats_mask, unsigned* err, F filled) {
+                                             const float* stats, uint32_t stats_mask, unsigned* err, int warp, F filled) {
   static_assert(N * kMostLoose <= 32 && kStats * kMostChunk <= 32, "a lane each");
   const int lane = threadIdx.x & 31, row_of = lane / N;
   RowSource m = {};
@@ -153,17 +158,23 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
   const float* const stat_from = stats + (lane % kStats) * plan.rows + lane / kStats;
   const uint32_t stat_to = smem_addr(ring.data) + plan.stats_at + 4u * lane;
   bool met = false;                      // the others, who fill the vectors under the first copies
-  int s = 0, issued = 0, sub = 0;
+  int s = 0, sub = 0;
   uint32_t ph = 0;
-  for (long long turn = ring.first;;) {
+  long long turn = ring.first, chunk = warp;
+  const auto advance = [&](int chunks) {
+    for (sub += chunks * plan.chunk; sub >= plan.groups; sub -= plan.groups) turn += ring.step;
+    for (s += chunks; s >= plan.stages; s -= plan.stages) ph ^= 1u;
+  };
+  if (warp >= plan.producers) {          // has no chunks
+    filled();
+    return;
+  }
+  advance(warp);
+  for (;; chunk += plan.producers, advance(plan.producers)) {
     const long long row0 = turn * plan.groups + sub;
     if (row0 >= plan.rows) break;
     const int rows = static_cast<int>(min(static_cast<long long>(plan.chunk), plan.rows - row0));
-    if ((sub += plan.chunk) == plan.groups) {
-      sub = 0;
-      turn += ring.step;
-    }
-    if (!met && issued == plan.stages) {
+    if (!met && chunk >= plan.stages) {
       filled();
       met = true;
     }
@@ -190,21 +201,13 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
       __syncwarp();
       copy.issue(bar);
     }
-    issued = min(issued + 1, plan.stages);
-    if (++s == plan.stages) {
-      s = 0;
-      ph ^= 1u;
-    }
   }
   if (!met) filled();
   __syncwarp();
-  for (; issued > 0; --issued) {
-    if (--s < 0) {
-      s = plan.stages - 1;
-      ph ^= 1u;
-    }
-    mbar_wait(ring.full + 8u * s, ph, err, kSiteDrainTma);
-  }
+  // earlier chunks than these had landed when their stages were filled again
+  for (const long long last = chunk; (chunk -= plan.producers) >= 0 && chunk >= last - plan.stages;)
+    mbar_wait(ring.full + 8u * static_cast<uint32_t>(chunk % plan.stages), static_cast<uint32_t>(chunk / plan.stages) & 1u, err,
+              kSiteDrainTma);
 }
 
 // A computing thread's view of the ring: of its group's stages, every
@@ -249,11 +252,12 @@ struct RingReader {
 };
 
 // ---------------------------------------------------------------- a thread's part of a row
-// NE elements of type T, in chunks of CP pairs.  VEC: a chunk is a 16-byte
-// vector, chunk v of thread t from column (v lanes + t) V on, which takes rows
-// on 16-byte boundaries of whole vectors.  Else single elements, element i of
-// thread t in column i lanes + t: 2 or 4 bytes apart from lane to lane, so that
-// rows may start anywhere.
+// NE elements of type T, in chunks of CP pairs.  A warp has 32 NE columns side
+// by side, so that a thread's places lie a fixed distance apart, in shared and
+// in global memory.  VEC: a chunk is a 16-byte vector, the warp's chunks one
+// behind the other, which takes rows on 16-byte boundaries of whole vectors.
+// Else single elements, 2 or 4 bytes apart from lane to lane, so that rows may
+// start anywhere.
 template <class T, int NE, bool VEC>
 struct RowPart {
   static constexpr int V = 16 / static_cast<int>(sizeof(T));
@@ -261,49 +265,51 @@ struct RowPart {
   static constexpr int CP = VEC ? V / 2 : 2;
   static constexpr int NC = NP / CP;
   using Chunk = Pair[CP];
-  int t, lanes, width;
-  bool full;                             // every thread's elements are all columns of the slice
+  int t, first, left;                    // column of the first element; columns from there on
 
-  __device__ __forceinline__ RowPart(int thread, int n, int w) : t(thread), lanes(n), width(w), full(n * NE == w) {}
+  __device__ __forceinline__ RowPart(int thread, int width)
+      : t(thread), first(column(thread, 0)), left(width - first) {}
 
-  static __device__ __forceinline__ int column(int t, int i, int lanes) {
-    return VEC ? ((i / V) * lanes + t) * V + i % V : i * lanes + t;
+  // Columns from element 0 to element i.
+  static __device__ __forceinline__ constexpr int offset(int i) { return VEC ? i / V * (32 * V) + i % V : i * 32; }
+  static __device__ __forceinline__ int column(int t, int i) {
+    return t / 32 * (32 * NE) + t % 32 * (VEC ? V : 1) + offset(i);
   }
-  __device__ __forceinline__ int col(int i) const { return column(t, i, lanes); }
-  __device__ __forceinline__ bool in(int i) const { return col(i) < width; }
+  __device__ __forceinline__ bool in(int i) const { return offset(i) < left; }
+  __device__ __forceinline__ bool full() const { return in(NE - 1); }
 
-  // The row's elements, 0 for what lies outside it.
+  // Elements of the row whose first column is at `row`; 0 for what lies outside it.
   __device__ __forceinline__ void load(const uint8_t* row, int v, Chunk& x) const {
+    const T* const p = reinterpret_cast<const T*>(row) + first;
     if constexpr (VEC) {
 #pragma unroll
       for (int j = 0; j < CP; ++j) x[j] = 0;
-      if (in(v * V)) pairs_of<T>(*reinterpret_cast<const uint4*>(row + col(v * V) * sizeof(T)), x);
+      if (in(v * V)) pairs_of<T>(*reinterpret_cast<const uint4*>(p + offset(v * V)), x);
     } else {
-      const T* const p = reinterpret_cast<const T*>(row);
 #pragma unroll
       for (int j = 0; j < CP; ++j) {
         const int i = 2 * (v * CP + j);
-        x[j] = pair_of(in(i) ? to_f32(p[col(i)]) : 0.0f, in(i + 1) ? to_f32(p[col(i + 1)]) : 0.0f);
+        x[j] = pair_of(in(i) ? to_f32(p[offset(i)]) : 0.0f, in(i + 1) ? to_f32(p[offset(i + 1)]) : 0.0f);
       }
     }
   }
   // The same of a row kept in 8 bits.
   __device__ __forceinline__ void load_saved(const uint8_t* codes, const uint8_t* exponents, int v, Chunk& x) const {
+    const uint8_t* const p = codes + first;
     if constexpr (VEC) {
       uint32_t w[V / 4];
       float by = 0.0f;
 #pragma unroll
       for (int j = 0; j < V / 4; ++j) w[j] = 0u;
       if (in(v * V)) {
-        const int c = col(v * V);
         if constexpr (V == 8) {
-          const uint2 q = *reinterpret_cast<const uint2*>(codes + c);
+          const uint2 q = *reinterpret_cast<const uint2*>(p + offset(v * V));
           w[0] = q.x;
           w[V / 4 - 1] = q.y;
         } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(codes + c);
+          w[0] = *reinterpret_cast<const uint32_t*>(p + offset(v * V));
         }
-        by = power_of(exponents[c / kSavedBlock]);
+        by = power_of(exponents[(first + offset(v * V)) / kSavedBlock]);
       }
       const Pair power = pair_of(by, by);
 #pragma unroll
@@ -318,15 +324,14 @@ struct RowPart {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int i = 2 * (v * CP + j) + k;
-          f[k] = in(i) ? values_of(codes[col(i)]).x * power_of(exponents[col(i) / kSavedBlock]) : 0.0f;
+          f[k] = in(i) ? values_of(p[offset(i)]).x * power_of(exponents[(first + offset(i)) / kSavedBlock]) : 0.0f;
         }
         x[j] = pair_of(f[0], f[1]);
       }
     }
   }
   // 0 for what lies outside the row.
-  __device__ __forceinline__ void drop(int v, Chunk& x) const {
-    if (full) return;
+  __device__ __forceinline__ void drop(int v, Pair* x) const {
     if constexpr (VEC) {
       if (!in(v * V)) {
 #pragma unroll
@@ -342,54 +347,46 @@ struct RowPart {
       }
     }
   }
+  // To the row whose first column is at `row`.
   __device__ __forceinline__ void store(T* row, int v, const Chunk& x) const {
+    T* const p = row + first;
     if constexpr (VEC) {
-      if (in(v * V)) store_pairs(row + col(v * V), x);
+      if (in(v * V)) store_pairs(p + offset(v * V), x);
     } else {
 #pragma unroll
       for (int j = 0; j < CP; ++j) {
         const int i = 2 * (v * CP + j);
         float a, b;
         unpair(x[j], a, b);
-        if (in(i)) row[col(i)] = from_f32<T>(a);
-        if (in(i + 1)) row[col(i + 1)] = from_f32<T>(b);
+        if (in(i)) p[offset(i)] = from_f32<T>(a);
+        if (in(i + 1)) p[offset(i + 1)] = from_f32<T>(b);
       }
     }
   }
 
-  // Values per column in shared memory, laid out as the threads hold them:
-  // elements 4q .. 4q + 3 of thread t at 4 (q lanes + t), 16 bytes from lane
-  // to lane.
+  // Values per column in shared memory, laid out as the threads hold them: a
+  // warp's 32 NE side by side, of these elements 4q .. 4q + 3 of its lane l at
+  // 128 q + 4 l.
   static __device__ __forceinline__ int slots(int lanes) { return NE * lanes; }
-  static __device__ __forceinline__ int column_of_slot(int slot, int lanes) {
-    const int quad = slot / 4;
-    return column(quad % lanes, quad / lanes * 4 + slot % 4, lanes);
+  static __device__ __forceinline__ int column_of_slot(int slot) {
+    const int warp = slot / (32 * NE), of = slot % (32 * NE);
+    return column(warp * 32 + of % 128 / 4, of / 128 * 4 + of % 4);
   }
-  __device__ __forceinline__ float* quad(float* values, int q) const { return values + 4 * (q * lanes + t); }
+  __device__ __forceinline__ int slot(int q) const { return t / 32 * (32 * NE) + 128 * q + 4 * (t % 32); }
   __device__ __forceinline__ void columns(const float* values, int v, Chunk& w) const {
 #pragma unroll
     for (int k = 0; k < CP / 2; ++k) {
-      const float4 f = *reinterpret_cast<const float4*>(values + 4 * ((v * (CP / 2) + k) * lanes + t));
+      const float4 f = *reinterpret_cast<const float4*>(values + slot(v * (CP / 2) + k));
       w[2 * k] = pair_of(f.x, f.y);
       w[2 * k + 1] = pair_of(f.z, f.w);
     }
   }
 };
 
-// A vector of `width` values (fp32, or T where `f32` is not set; null: `none`)
-// from column col0 on, into slots, by the first `threads` of the CTA.
-template <class T, class Part>
-__device__ __forceinline__ void fill_columns(float* values, const void* p, bool f32, float none, int lanes,
-                                             int threads, int col0, int width) {
-  for (int slot = threadIdx.x; slot < Part::slots(lanes); slot += threads) {
-    const int c = Part::column_of_slot(slot, lanes);
-    float v = 0.0f;
-    if (c < width)
-      v = !p    ? none
-          : f32 ? __ldg(static_cast<const float*>(p) + col0 + c)
-                : to_f32(static_cast<const T*>(p)[col0 + c]);
-    values[slot] = v;
-  }
+// Value c of a vector of fp32, or of T where `f32` is not set.
+template <class T>
+__device__ __forceinline__ float vector_value(const void* p, bool f32, long long c) {
+  return f32 ? __ldg(static_cast<const float*>(p) + c) : to_f32(static_cast<const T*>(p)[c]);
 }
 
 // ---------------------------------------------------------------- sums over a row
