@@ -35,7 +35,8 @@ struct RowSource {
 struct RowPlan {
   int width, slice;                      // columns of a row, of a CTA's part
   int lanes, groups, stages, ctas;
-  int chunk;                             // rows of a stage: a divisor of groups
+  int turn;                              // rows of all groups at a time
+  int chunk;                             // rows of a stage: of whole groups, a divisor of turn
   int producers;                         // 4, 2 or 1, a divisor of stages
   uint32_t stage_bytes;
   uint32_t ring_at;                      // in dynamic shared memory, behind the weights

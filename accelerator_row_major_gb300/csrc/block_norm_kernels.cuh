@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     for (int j = 0; j < NP; ++j) sum = fma2(x[j], x[j], sum);
     s[0] = sum_of(sum);
     sums.add<1>(s);
-    rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+    rstd = rsqrtf(s[0] * inv + a.eps);
   };
   // f(j, value) for every pair of elements, of a vector or of a row
   const auto each = [&](int vector_at, auto f) {
@@ -183,22 +183,22 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
   };
 
   RingReader reader(ring, plan, a.err, group);
-  long long row = group < plan.groups ? ring.first * plan.groups + group : plan.rows;
-  for (; row < plan.rows; row += ring.step * plan.groups) {
+  long long row = group < plan.groups ? ring.first * plan.turn + group : plan.rows;
+  for (; row < plan.rows; row += ring.step * plan.turn) {
     reader.wait();
     Pair x[NP];
     float mean, rstd, mean_b = 0.0f, rstd_b = 0.0f;
-    each_of(reader.at(a.in[kInBranch], row, VEC), [&](int j, Pair v) { x[j] = v; });
+    each_of(reader.at(a.in[kInBranch], row, 0, VEC), [&](int j, Pair v) { x[j] = v; });
     if (a.post) {
       normalise(x, mean_b, rstd_b);
       each(kPostWeight, [&](int j, Pair w) { x[j] = mul2(mul2(x[j], both(rstd_b)), w); });
       if (a.vectors.slot[kPostBias] >= 0) each(kPostBias, [&](int j, Pair w) { x[j] = add2(x[j], w); });
     }
     if (a.gate == kElementGate)
-      each_of(reader.at(a.in[kInGate], row, VEC), [&](int j, Pair w) { x[j] = mul2(x[j], w); });
+      each_of(reader.at(a.in[kInGate], row, 0, VEC), [&](int j, Pair w) { x[j] = mul2(x[j], w); });
     else if (a.gate == kChannelGate)
       each(kGateVector, [&](int j, Pair w) { x[j] = mul2(x[j], w); });
-    each_of(reader.at(a.in[kInResidual], row, VEC),
+    each_of(reader.at(a.in[kInResidual], row, 0, VEC),
             [&](int j, Pair w) { x[j] = fma2(x[j], both(a.beta), mul2(w, both(a.alpha))); });
     reader.release();
     store(a.h, row, x);                  // an h that is an input: all of this row has been read
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
 // LAYER: around the means; POST: the branch was normed; CHANNEL: a gate per
 // channel (a gate per element is the launch's choice).  What a form does not
 // have costs no registers.
-template <class T, int NE, bool VEC, bool LAYER, bool POST, bool CHANNEL>
+template <class T, int NE, int ROWS, bool VEC, bool LAYER, bool POST, bool CHANNEL>
 __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
   using Part = RowPart<T, NE, VEC>;
@@ -259,181 +259,247 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
   for (int k = 0; k < kSums; ++k)
 #pragma unroll
     for (int j = 0; j < NP; ++j) total[k][j] = 0;
-  // The two means over the row of a norm's gradient: of the gradients `ones`
-  // and, along hat, of their products, as factors of 1 and of c.
-  const auto means = [&](Pair ones, Pair along, float by, float& c1, float& c2) {
-    const float s = by != 0.0f ? sum_of(along) * by : 0.0f;
-    if constexpr (LAYER) {
-      float v[2] = {sum_of(ones), s};
-      sums.add<2>(v);
-      c1 = -v[0] * inv;
-      c2 = -v[1] * inv * by;
-    } else {
-      float v[1] = {s};
-      sums.add<1>(v);
-      c1 = 0.0f;
-      c2 = -v[0] * inv * by;
+  // The two means over a row of a norm's gradient, of the gradients `ones` and
+  // of their products with hat, negative.
+  const auto means = [&](const Pair(&ones)[ROWS], const Pair(&along)[ROWS], float(&c1)[ROWS], float(&c2)[ROWS]) {
+    constexpr int N = LAYER ? 2 : 1;
+    float v[N * ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      v[N * r] = sum_of(along[r]);
+      if (LAYER) v[N * r + N - 1] = sum_of(ones[r]);
+    }
+    sums.add<N * ROWS>(v);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      c1[r] = LAYER ? -v[N * r + N - 1] * inv : 0.0f;
+      c2[r] = -v[N * r] * inv;
     }
   };
   const auto store = [&](const Output& o, long long row, const Pair(&x)[NP], float by) {
-    if (!o.p || !output_ok<T>(o, plan, row, a.err)) return;
+    if (!o.p || row >= plan.rows || !output_ok<T>(o, plan, row, a.err)) return;
     T* const to = static_cast<T*>(o.p) + row * o.ld + ring.col0;
+    const auto all = [&](auto scaled) {
 #pragma unroll
-    for (int v = 0; v < NC; ++v) {
-      Pair w[CP];
+      for (int v = 0; v < NC; ++v) {
+        Pair w[CP];
 #pragma unroll
-      for (int k = 0; k < CP; ++k) w[k] = mul2(x[v * CP + k], both(by));
-      mine.store(to, v, w);
-    }
-  };
-
-  RingReader reader(ring, plan, a.err, group);
-  const long long step = ring.step * plan.groups;
-  long long row = group < plan.groups ? ring.first * plan.groups + group : plan.rows;
-  for (; row < plan.rows; row += step) {
-    reader.wait();
-    const float4 stats = reader.stats();
-    const float mean = stats.x, rstd = stats.y, mean_b = stats.z, rstd_b = stats.w;
-    // a row of h or of the branch, as it is or in 8 bits: f(chunk's loader)
-    const auto rows_of = [&](int at, int exponents_at, auto f) {
-      if (a.in[exponents_at].p) {
-        const uint8_t* const codes = reader.at(a.in[at], row, true);
-        const uint8_t* const exponents = reader.at(a.in[exponents_at], row, true);
-        f([&](int v, Pair(&x)[CP]) { mine.load_saved(codes, exponents, v, x); });
-      } else {
-        const uint8_t* const from = reader.at(a.in[at], row, VEC);
-        f([&](int v, Pair(&x)[CP]) { mine.load(from, v, x); });
+        for (int k = 0; k < CP; ++k) w[k] = decltype(scaled)::value ? mul2(x[v * CP + k], both(by)) : x[v * CP + k];
+        mine.store(to, v, w);
       }
     };
-    // c = h - mean in place of hat = c rstd: where rstd is 0 (squares that
-    // overflowed) or c is, hat is 0 and never 0 times infinity
-    Pair c[NP], g[NP], sg = 0, sgc = 0;
-    rows_of(kGradH, kGradHExponents, [&](auto load_h) {
-      const uint8_t* const dy = reader.at(a.in[kGradDy], row, VEC);
+    if (by == 1.0f)
+      all(std::false_type{});
+    else
+      all(std::true_type{});
+  };
+  // f(r, v, loader) for every row r and chunk v, the loader filling a chunk of
+  // the row of h or of the branch, which is as it is or in 8 bits.  What a turn
+  // has no row for counts as zeros.
+  const auto rows_of = [&](const RingReader& reader, long long row, int at, int exponents_at, auto f) {
+    const uint8_t* from[ROWS];
+    const uint8_t* exponents[ROWS];
+    const bool saved = a.in[exponents_at].p != nullptr;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      from[r] = reader.at(a.in[at], row + r, r, VEC || saved);
+      exponents[r] = saved ? reader.at(a.in[exponents_at], row + r, r, true) : nullptr;
+    }
+    if (saved)
+      f([&](int r, int v, Pair(&x)[CP]) { mine.load_saved(from[r], exponents[r], v, x); });
+    else
+      f([&](int r, int v, Pair(&x)[CP]) { mine.load(from[r], v, x); });
+  };
+
+  // a norm's hat
+  const auto normed = [](Pair x, float mean, float rstd) {
+    return LAYER ? fma2(x, both(rstd), both(-mean * rstd)) : mul2(x, both(rstd));
+  };
+  const auto nothing = [](Pair(&x)[CP]) {
+#pragma unroll
+    for (int k = 0; k < CP; ++k) x[k] = 0;
+  };
+
+  RingReader reader(ring, plan, a.err, group * ROWS);
+  long long row = group < plan.groups ? ring.first * plan.turn + group * ROWS : plan.rows;
+  for (; row < plan.rows; row += ring.step * plan.turn) {
+    reader.wait();
+    const bool whole = ROWS == 1 || row + ROWS <= plan.rows;
+    const auto there = [&](int r) { return r == 0 || whole; };
+    float mean[ROWS], rstd[ROWS], mean_b[ROWS], rstd_b[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const float4 stats = reader.stats(r);
+      mean[r] = there(r) ? stats.x : 0.0f;
+      rstd[r] = there(r) ? stats.y : 0.0f;
+      mean_b[r] = there(r) ? stats.z : 0.0f;
+      rstd_b[r] = there(r) ? stats.w : 0.0f;
+    }
+    // hat = h rstd - mean rstd in one operation; finite wherever h and rstd are
+    Pair hat[ROWS][NP], g[ROWS][NP], sg[ROWS], sgh[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) sg[r] = sgh[r] = 0;
+    rows_of(reader, row, kGradH, kGradHExponents, [&](auto load_h) {
+      const uint8_t* dy[ROWS];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) dy[r] = reader.at(a.in[kGradDy], row + r, r, VEC);
       const float* const weight = vector(kWeight);
 #pragma unroll
       for (int v = 0; v < NC; ++v) {
-        Pair x[CP], y[CP], w[CP];
-        load_h(v, x);
-        mine.load(dy, v, y);
+        Pair w[CP];
         mine.columns(weight, v, w);
 #pragma unroll
-        for (int k = 0; k < CP; ++k) {
-          const int j = v * CP + k;
-          c[j] = LAYER ? add2(x[k], both(-mean)) : x[k];
-          total[kSumWeight][j] = fma2(mul2(y[k], both(rstd)), c[j], total[kSumWeight][j]);
-          if (LAYER) total[kSumBias][j] = add2(total[kSumBias][j], y[k]);
-          g[j] = mul2(y[k], w[k]);
-          if (LAYER) sg = add2(sg, g[j]);
-          sgc = fma2(g[j], c[j], sgc);
-        }
-      }
-    });
-    float c1, c2;
-    means(sg, sgc, rstd, c1, c2);
-    Pair(&d)[NP] = g;                    // in place of g
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      if (LAYER) g[j] = add2(g[j], both(c1));
-      d[j] = mul2(fma2(c[j], both(c2), g[j]), both(rstd));
-    }
-    if (a.in[kGradDh].p) {
-      const uint8_t* const dh = reader.at(a.in[kGradDh], row, VEC);
-#pragma unroll
-      for (int v = 0; v < NC; ++v) {
-        Pair x[CP];
-        mine.load(dh, v, x);
-#pragma unroll
-        for (int k = 0; k < CP; ++k) d[v * CP + k] = add2(d[v * CP + k], x[k]);
-      }
-    }
-    // an output that is an input: the ring has all of this row
-    store(a.dresidual, row, d, a.alpha);
-    if (!(POST || CHANNEL) && a.gate == kNoGate) {
-      reader.release();
-      store(a.dbranch, row, d, a.beta);
-      continue;
-    }
-#pragma unroll
-    for (int j = 0; j < NP; ++j) d[j] = mul2(d[j], both(a.beta));
-    if (!full) {
-#pragma unroll
-      for (int v = 0; v < NC; ++v) mine.drop(v, d + v * CP);
-    }
-    Pair(&b)[NP] = c;                    // the branch's rows in place of h's
-    Pair se = 0, seb = 0;
-    const auto through_gate = [&](auto load_branch, auto element) {
-      constexpr bool kElement = decltype(element)::value, kGated = CHANNEL || kElement;
-      const bool bias = POST && LAYER && kGated && a.vectors.slot[kPostBias] >= 0;
-      const uint8_t* const gate = kElement ? reader.at(a.in[kGradGate], row, VEC) : nullptr;
-      T* const to = static_cast<T*>(a.dgate.p) + row * a.dgate.ld + ring.col0;
-      const bool stores = kElement && a.dgate.p && output_ok<T>(a.dgate, plan, row, a.err);
-#pragma unroll
-      for (int v = 0; v < NC; ++v) {
-        Pair x[CP], w[CP];
-        Pair* const e = d + v * CP;
-        load_branch(v, x);
-        if (POST) {
-          mine.columns(vector(kPostWeight), v, w);
-          if (LAYER) {
-#pragma unroll
-            for (int k = 0; k < CP; ++k) x[k] = add2(x[k], both(-mean_b));
+        for (int r = 0; r < ROWS; ++r) {
+          Pair x[CP], y[CP];
+          if (there(r)) {
+            load_h(r, v, x);
+            mine.load(dy[r], v, y);
+          } else {
+            nothing(x);
+            nothing(y);
           }
-        }
-        if (kGated) {
-          Pair p[CP], by[CP];
-#pragma unroll
-          for (int k = 0; k < CP; ++k) p[k] = POST ? mul2(mul2(x[k], both(rstd_b)), w[k]) : x[k];
-          if (bias) {
-            mine.columns(vector(kPostBias), v, by);
-#pragma unroll
-            for (int k = 0; k < CP; ++k) p[k] = add2(p[k], by[k]);
-          }
-          if (CHANNEL)
-            mine.columns(vector(kGateVector), v, by);
-          else
-            mine.load(gate, v, by);
-#pragma unroll
-          for (int k = 0; k < CP; ++k) {
-            if (CHANNEL)
-              total[kSumGate][v * CP + k] = fma2(e[k], p[k], total[kSumGate][v * CP + k]);
-            else
-              p[k] = mul2(e[k], p[k]);
-            e[k] = mul2(e[k], by[k]);
-          }
-          if (stores) mine.store(to, v, p);
-        }
-        if (POST) {
 #pragma unroll
           for (int k = 0; k < CP; ++k) {
             const int j = v * CP + k;
-            b[j] = x[k];
-            total[kSumPostWeight][j] = fma2(mul2(e[k], both(rstd_b)), x[k], total[kSumPostWeight][j]);
-            if (LAYER) total[kSumPostBias][j] = add2(total[kSumPostBias][j], e[k]);
-            e[k] = mul2(e[k], w[k]);
-            if (LAYER) se = add2(se, e[k]);
-            seb = fma2(e[k], x[k], seb);
+            hat[r][j] = normed(x[k], mean[r], rstd[r]);
+            total[kSumWeight][j] = fma2(y[k], hat[r][j], total[kSumWeight][j]);
+            if (LAYER) total[kSumBias][j] = add2(total[kSumBias][j], y[k]);
+            g[r][j] = mul2(y[k], w[k]);
+            if (LAYER) sg[r] = add2(sg[r], g[r][j]);
+            sgh[r] = fma2(g[r][j], hat[r][j], sgh[r]);
+          }
+        }
+      }
+    });
+    float c1[ROWS], c2[ROWS];
+    means(sg, sgh, c1, c2);
+    // d = dh + rstd (g + c1 + hat c2), in place of g
+    Pair(&d)[ROWS][NP] = g;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        d[r][j] = fma2(g[r][j], both(rstd[r]),
+                       LAYER ? fma2(hat[r][j], both(c2[r] * rstd[r]), both(c1[r] * rstd[r])) : mul2(hat[r][j], both(c2[r] * rstd[r])));
+      if (a.in[kGradDh].p && there(r)) {
+        const uint8_t* const dh = reader.at(a.in[kGradDh], row + r, r, VEC);
+#pragma unroll
+        for (int v = 0; v < NC; ++v) {
+          Pair x[CP];
+          mine.load(dh, v, x);
+#pragma unroll
+          for (int k = 0; k < CP; ++k) d[r][v * CP + k] = add2(d[r][v * CP + k], x[k]);
+        }
+      }
+      // an output that is an input: the ring has all of this row
+      store(a.dresidual, row + r, d[r], a.alpha);
+    }
+    if (!(POST || CHANNEL) && a.gate == kNoGate) {
+      reader.release();
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) store(a.dbranch, row + r, d[r], a.beta);
+      continue;
+    }
+    if (!full) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int v = 0; v < NC; ++v) mine.drop(v, d[r] + v * CP);
+    }
+    // e = d gate, without beta: what is linear in it gets that at its end
+    Pair(&hat_b)[ROWS][NP] = hat;        // the branch's in place of h's
+    Pair se[ROWS], seh[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) se[r] = seh[r] = 0;
+    const auto through_gate = [&](auto load_branch, auto element) {
+      constexpr bool kElement = decltype(element)::value, kGated = CHANNEL || kElement;
+      const bool bias = POST && LAYER && kGated && a.vectors.slot[kPostBias] >= 0;
+      const uint8_t* gate[ROWS];
+      T* to[ROWS];
+      const bool stores = kElement && a.dgate.p;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        gate[r] = kElement ? reader.at(a.in[kGradGate], row + r, r, VEC) : nullptr;
+        to[r] = static_cast<T*>(a.dgate.p) + (row + r) * a.dgate.ld + ring.col0;
+      }
+#pragma unroll
+      for (int v = 0; v < NC; ++v) {
+        Pair w[CP], post_bias[CP], channel[CP];
+        if (POST) mine.columns(vector(kPostWeight), v, w);
+        if (kGated && POST) {
+          if (bias) {
+            mine.columns(vector(kPostBias), v, post_bias);
+          } else {
+            nothing(post_bias);
+          }
+        }
+        if (CHANNEL) mine.columns(vector(kGateVector), v, channel);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          Pair x[CP];
+          Pair* const e = d[r] + v * CP;
+          if (there(r))
+            load_branch(r, v, x);
+          else
+            nothing(x);
+          if (POST) {
+#pragma unroll
+            for (int k = 0; k < CP; ++k) x[k] = hat_b[r][v * CP + k] = normed(x[k], mean_b[r], rstd_b[r]);
+          }
+          if (kGated) {
+            Pair p[CP], by[CP];
+#pragma unroll
+            for (int k = 0; k < CP; ++k) p[k] = POST ? fma2(x[k], w[k], post_bias[k]) : x[k];
+            if (CHANNEL) {
+#pragma unroll
+              for (int k = 0; k < CP; ++k) by[k] = channel[k];
+            } else if (there(r)) {
+              mine.load(gate[r], v, by);
+            } else {
+              nothing(by);
+            }
+#pragma unroll
+            for (int k = 0; k < CP; ++k) {
+              if (CHANNEL)
+                total[kSumGate][v * CP + k] = fma2(e[k], p[k], total[kSumGate][v * CP + k]);
+              else
+                p[k] = mul2(mul2(e[k], p[k]), both(a.beta));
+              e[k] = mul2(e[k], by[k]);
+            }
+            if (stores && there(r) && output_ok<T>(a.dgate, plan, row + r, a.err)) mine.store(to[r], v, p);
+          }
+          if (POST) {
+#pragma unroll
+            for (int k = 0; k < CP; ++k) {
+              const int j = v * CP + k;
+              total[kSumPostWeight][j] = fma2(e[k], x[k], total[kSumPostWeight][j]);
+              if (LAYER) total[kSumPostBias][j] = add2(total[kSumPostBias][j], e[k]);
+              e[k] = mul2(e[k], w[k]);
+              if (LAYER) se[r] = add2(se[r], e[k]);
+              seh[r] = fma2(e[k], x[k], seh[r]);
+            }
           }
         }
       }
     };
-    rows_of(kGradBranch, kGradBranchExponents, [&](auto load_branch) {
+    rows_of(reader, row, kGradBranch, kGradBranchExponents, [&](auto load_branch) {
       if (!CHANNEL && a.gate == kElementGate)
         through_gate(load_branch, std::integral_constant<bool, !CHANNEL>{});
       else
         through_gate(load_branch, std::false_type{});
     });
     reader.release();
-    if (POST) {
-      means(se, seb, rstd_b, c1, c2);
+    if (POST) means(se, seh, c1, c2);
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        if (LAYER) d[j] = add2(d[j], both(c1));
-        d[j] = fma2(b[j], both(c2), d[j]);
+    for (int r = 0; r < ROWS; ++r) {
+      if (POST) {
+        const float by = rstd_b[r] * a.beta;
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+          d[r][j] = fma2(d[r][j], both(by),
+                         LAYER ? fma2(hat_b[r][j], both(c2[r] * by), both(c1[r] * by)) : mul2(hat_b[r][j], both(c2[r] * by)));
       }
-      store(a.dbranch, row, d, rstd_b);
-    } else {
-      store(a.dbranch, row, d, 1.0f);
+      store(a.dbranch, row + r, d[r], POST ? 1.0f : a.beta);
     }
   }
   if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
@@ -451,9 +517,10 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
       if (!there || a.sum[k] < 0) continue;
 #pragma unroll
       for (int q = 0; q < NE / 4; ++q) {
+        const Pair by = both(k == kSumWeight || k == kSumBias ? 1.0f : a.beta);
         float4 f;
-        unpair(total[k][2 * q], f.x, f.y);
-        unpair(total[k][2 * q + 1], f.z, f.w);
+        unpair(mul2(total[k][2 * q], by), f.x, f.y);
+        unpair(mul2(total[k][2 * q + 1], by), f.z, f.w);
         *reinterpret_cast<float4*>(columns + (a.sum[k] * plan.groups + group) * slots + mine.slot(q)) = f;
       }
     }
@@ -695,10 +762,16 @@ constexpr size_t kMostShared = 220 * 1024;   // dynamic; RowShared fits beside i
 constexpr int kMostStages = 16;
 constexpr size_t kLeastChunk = 16 * 1024;    // bytes of a stage, where there are rows enough
 
-// Lays out the rows of `in` over `ctas` CTAs and lanes of `ne` elements,
-// groups and ring; false where that cannot be.
-bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int ne, bool stats, int sums, bool aligned,
+// What a thread has of a turn: elements of a row, rows.
+struct Lane {
+  int ne, rows;
+};
+
+// Lays out the rows of `in` over `ctas` CTAs, lanes, groups and ring; false
+// where that cannot be.
+bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, Lane lane, bool stats, int sums, bool aligned,
                int num_sms, size_t* bytes, int* grid) {
+  const int ne = lane.ne;
   const int slice = ctas == 1 ? plan.width : ((plan.width - 1) / ctas / kSliceUnit + 1) * kSliceUnit;
   if (ctas > num_sms || slice > kRowWarps * 32 * ne) return false;
   plan.ctas = ctas;
@@ -706,7 +779,12 @@ bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int n
   plan.lanes = 32 * ((slice - 1) / (32 * ne) + 1);
   const long long units = num_sms / ctas;
   const size_t columns = static_cast<size_t>(vectors) * ne * plan.lanes * sizeof(float);
-  plan.groups = static_cast<int>(std::min<long long>(kRowWarps * 32 / plan.lanes, (plan.rows - 1) / units + 1));
+  // rows enough for all SMs; a thread's rows at a time only where there are so many
+  plan.groups = static_cast<int>(std::min<long long>(kRowWarps * 32 / plan.lanes, (plan.rows - 1) / (units * lane.rows) + 1));
+  if (lane.rows > 1 && plan.rows < units * lane.rows) return false;
+  // copies of a forward turn that start at multiples of 32 KB all over the GPU meet on the same channels: 16 rows of
+  // 1024 in bfloat16 101 us (65536 of them), 12 rows 89; 8 of 2048 101, 6 90
+  if (!stats && plan.groups >= 8 && source_bytes(in[0].size, slice) * plan.groups % 32768 == 0) plan.groups -= plan.groups / 4;
   // a stage of `rows` rows
   const auto stage_of = [&](int rows) {
     size_t stage = 0;
@@ -722,20 +800,21 @@ bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int n
     return stage + (stats ? rows * kStats * sizeof(float) : 0);
   };
   size_t stage = 0, stages = 0;
-  for (;; --plan.groups) {               // two rows in flight per group, or fewer groups
-    plan.chunk = 1;
-    for (int rows = 2; rows <= plan.groups && stage_of(plan.chunk) < kLeastChunk; ++rows) {
+  for (;; --plan.groups) {               // two turns in flight, or fewer groups
+    plan.turn = plan.groups * lane.rows;
+    plan.chunk = lane.rows;
+    for (int rows = 2 * lane.rows; rows <= plan.turn && stage_of(plan.chunk) < kLeastChunk; rows += lane.rows) {
       bool loose = false;
       for (int i = 0; i < n; ++i) loose = loose || (in[i].p && !in[i].packed);
-      if (plan.groups % rows == 0 && rows <= (loose ? kMostLoose : kMostChunk)) plan.chunk = rows;
+      if (plan.turn % rows == 0 && rows <= (loose ? kMostLoose : kMostChunk)) plan.chunk = rows;
     }
     stage = stage_of(plan.chunk);
     stages = columns < kMostShared ? (kMostShared - columns) / (stage + 16) : 0;
-    if (stages >= 2u * (plan.groups / plan.chunk) || plan.groups == 1) break;
+    if (stages >= 2u * (plan.turn / plan.chunk) || plan.groups == 1) break;
   }
   if (stages < 2) return false;
   // a multiple of the chunks of a turn, and of as many producers as cost no more than a quarter of the stages
-  const int step = plan.groups / plan.chunk;
+  const int step = plan.turn / plan.chunk;
   const int most = static_cast<int>(std::min<size_t>(stages, std::max(kMostStages, 2 * step)));
   for (plan.producers = kProducers; plan.producers >= 1; plan.producers /= 2) {
     const int unit = std::lcm(step, plan.producers);
@@ -744,22 +823,22 @@ bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, int n
   }
   plan.stage_bytes = static_cast<uint32_t>(stage);
   plan.ring_at = static_cast<uint32_t>(columns);
-  *grid = static_cast<int>(std::min<long long>(units, (plan.rows - 1) / plan.groups + 1)) * ctas;
+  *grid = static_cast<int>(std::min<long long>(units, (plan.rows - 1) / plan.turn + 1)) * ctas;
   // the groups' sums take the place of the ring
   *bytes = std::max(columns + static_cast<size_t>(plan.stages) * (stage + 16),
                     static_cast<size_t>(sums) * plan.groups * ne * plan.lanes * sizeof(float));
   return true;
 }
 
-// A layout's price: what a row takes its threads, by the rows that are worked
-// on at a time.  A row costs a warp some 250 instructions besides 16 for each
-// of its elements (counted: 380 of 8 elements), and more where CTAs exchange
-// sums; a group that is alone waits for all of them.
-constexpr int kRowCost = 250, kExchangeCost = 300, kElementCost = 16;
+// A layout's price: what a turn takes its threads, by its rows.  A turn costs a
+// warp some 250 instructions besides 16 for each of its elements (counted: 380
+// of 8 elements), and more where CTAs exchange sums; a group that is alone
+// waits for all of them, half as long for each of two rows.
+constexpr int kTurnCost = 250, kExchangeCost = 300, kElementCost = 16;
 
-long long price(const RowPlan& plan, int ne) {
-  const long long row = kRowCost + (plan.ctas > 1 ? kExchangeCost : 0) + static_cast<long long>(kElementCost) * ne;
-  return row * plan.ctas * (plan.groups == 1 ? 24 : 16) / plan.groups;
+long long price(const RowPlan& plan, Lane lane) {
+  const long long turn = kTurnCost + (plan.ctas > 1 ? kExchangeCost : 0) + static_cast<long long>(kElementCost) * lane.ne * lane.rows;
+  return turn * plan.ctas * (plan.groups == 1 ? (lane.rows == 1 ? 24 : 20) : 16) / plan.turn;
 }
 
 constexpr int kMaxDevices = 64;
@@ -832,14 +911,14 @@ struct Layout {
   RowPlan plan;
   RowSource in[N];
   size_t bytes = 0;
-  int grid = 0, ne = 0;
+  int grid = 0;
+  Lane lane = {0, 0};                    // ne 0: there is none
 };
 
-// The cheapest of the layouts with `ne[i]` elements a thread; ne 0: there is
-// none.
+// The cheapest layout.
 template <int N, int K>
-Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (&ne)[K], bool stats, int sums,
-                      const BlockLaunch& l) {
+Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const Lane (&lanes)[K], bool stats,
+                      int sums, const BlockLaunch& l) {
   Layout<N> best = {};
   long long least = 0;
   for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
@@ -847,10 +926,10 @@ Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const int (
       Layout<N> c = {};
       c.plan = plan;
       std::copy(in, in + N, c.in);
-      c.ne = ne[i];
-      if (!plan_rows(c.plan, c.in, N, l.vectors, ctas, ne[i], stats, sums, l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
-      const long long cost = price(c.plan, ne[i]);
-      if (best.ne == 0 || cost < least) {
+      c.lane = lanes[i];
+      if (!plan_rows(c.plan, c.in, N, l.vectors, ctas, lanes[i], stats, sums, l.aligned, l.num_sms, &c.bytes, &c.grid)) continue;
+      const long long cost = price(c.plan, lanes[i]);
+      if (best.lane.ne == 0 || cost < least) {
         best = c;
         least = cost;
       }
@@ -868,10 +947,10 @@ int forward_form(const BlockArgs& a, const BlockLaunch& l, Layout<kInputs>& best
 
 template <class T>
 int forward(BlockArgs& a, const BlockLaunch& l) {
-  const int ne[3] = {8, 16, 32};
-  Layout<kInputs> best = best_layout(a.plan, a.in, ne, false, 0, l);
+  const Lane lanes[3] = {{8, 1}, {16, 1}, {32, 1}};
+  Layout<kInputs> best = best_layout(a.plan, a.in, lanes, false, 0, l);
   ++*l.launches;
-  if (best.ne == 0) {
+  if (best.lane.ne == 0) {
     *l.kernel = "block_norm_wide_kernel";
     return launch_plain(block_norm_wide_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>(a.plan.rows, 4LL * l.num_sms))),
                         kWideThreads, l.stream, a);
@@ -879,17 +958,24 @@ int forward(BlockArgs& a, const BlockLaunch& l) {
   *l.kernel = "block_norm_kernel";
   a.plan = best.plan;
   std::copy(best.in, best.in + kInputs, a.in);
-  if (best.ne == 8) return forward_form<T, 8>(a, l, best);
-  return best.ne == 16 ? forward_form<T, 16>(a, l, best) : forward_form<T, 32>(a, l, best);
+  if (best.lane.ne == 8) return forward_form<T, 8>(a, l, best);
+  return best.lane.ne == 16 ? forward_form<T, 16>(a, l, best) : forward_form<T, 32>(a, l, best);
 }
 
-template <class T, int NE, bool LAYER, bool POST, bool CHANNEL>
+template <class T, int NE, int ROWS, bool LAYER, bool POST, bool CHANNEL>
 int gradient_form(const BlockGradArgs& a, const BlockLaunch& l, Layout<kGradInputs>& best) {
   const int threads = cta_threads(a.plan);
-  return l.aligned ? launch_rows<block_norm_grad_kernel<T, NE, true, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
+  return l.aligned ? launch_rows<block_norm_grad_kernel<T, NE, ROWS, true, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
                                                                                             best.bytes, l.stream)
-                   : launch_rows<block_norm_grad_kernel<T, NE, false, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
+                   : launch_rows<block_norm_grad_kernel<T, NE, ROWS, false, LAYER, POST, CHANNEL>>(a, threads, l.device, &best.grid,
                                                                                              best.bytes, l.stream);
+}
+
+// What a thread has of many rows, besides the 8 elements of one: two rows of
+// them, or one row of 16, by the registers that the form's sums leave
+// (8192 x 4096 bfloat16, with a gate per channel 85 us against 119).
+constexpr Lane grad_lane(bool layer, bool post, bool channel) {
+  return layer && post ? Lane{8, 1} : post && !channel ? Lane{16, 1} : Lane{8, 2};
 }
 
 // f with the three choices as template arguments.
@@ -914,26 +1000,26 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
   if (a.plan.rows > 0) {
     rc = with_form(!a.rms, a.post, a.gate == kChannelGate, [&](auto layer, auto post, auto channel) -> int {
       constexpr bool kLayer = decltype(layer)::value, kPost = decltype(post)::value, kChannel = decltype(channel)::value;
-      // 16 elements' sums of four or five vectors leave too few registers
-      constexpr bool kTwo = !(kLayer && kPost);
-      const int ne[2] = {8, kTwo ? 16 : 8};
-      Layout<kGradInputs> best = best_layout(a.plan, a.in, ne, true, a.sums, l);
-      c.ctas = best.ne ? best.grid / best.plan.ctas : static_cast<int>(std::min<long long>(a.plan.rows, 2LL * l.num_sms));
+      constexpr Lane kMore = grad_lane(kLayer, kPost, kChannel);
+      const Lane lanes[2] = {{8, 1}, kMore};
+      Layout<kGradInputs> best = best_layout(a.plan, a.in, lanes, true, a.sums, l);
+      c.ctas = best.lane.ne ? best.grid / best.plan.ctas : static_cast<int>(std::min<long long>(a.plan.rows, 2LL * l.num_sms));
       if (a.sums) {
         a.partials = static_cast<float*>(acquire_scratch(
             l.device, l.stream, sizeof(float) * static_cast<size_t>(c.ctas) * a.sums * a.ld_partials));
         if (!a.partials) return GEMM_F32_ESCRATCH;
       }
       ++*l.launches;
-      if (best.ne == 0) {
+      if (best.lane.ne == 0) {
         *l.kernel = "block_norm_grad_wide_kernel";
         return launch_plain(block_norm_grad_wide_kernel<T>, dim3(c.ctas), kWideThreads, l.stream, a);
       }
       *l.kernel = "block_norm_grad_kernel";
       a.plan = best.plan;
       std::copy(best.in, best.in + kGradInputs, a.in);
-      const int got = best.ne == 8 ? gradient_form<T, 8, kLayer, kPost, kChannel>(a, l, best)
-                                   : gradient_form<T, kTwo ? 16 : 8, kLayer, kPost, kChannel>(a, l, best);
+      const bool more = best.lane.ne != 8 || best.lane.rows != 1;
+      const int got = more ? gradient_form<T, kMore.ne, kMore.rows, kLayer, kPost, kChannel>(a, l, best)
+                           : gradient_form<T, 8, 1, kLayer, kPost, kChannel>(a, l, best);
       c.ctas = best.grid / best.plan.ctas;
       return got;
     });

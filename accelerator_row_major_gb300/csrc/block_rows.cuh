@@ -49,7 +49,7 @@ struct RingPlace {
   uint8_t* data;
   uint32_t full, empty;                  // barriers: the copies have landed; all warps have read
   int col0, width;                       // of this CTA's slice (no columns: width 0)
-  long long first, step;                 // of its turns: a row for each group
+  long long first, step;                 // of its turns
 
   __device__ __forceinline__ RingPlace(const RowPlan& p, uint8_t* smem, int rank) {
     data = smem + p.ring_at;
@@ -64,7 +64,7 @@ struct RingPlace {
   __device__ __forceinline__ void init(const RowPlan& p) const {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(full + 8u * i, p.stats_at ? 33 : 1);        // the producer's lanes, where they copy statistics
-      mbar_init(empty + 8u * i, static_cast<uint32_t>(p.chunk * (p.lanes / 32)));
+      mbar_init(empty + 8u * i, static_cast<uint32_t>(p.chunk / (p.turn / p.groups) * (p.lanes / 32)));
     }
     fence_mbar_init();
   }
@@ -126,7 +126,7 @@ struct RowCopy {
 // chunks, `stages` of all of them in flight.  A wait for a barrier's phase
 // passes wrongly when the barrier is a whole phase behind, so each stage has
 // one producer and the groups of one chunk: the producers and the chunks of a
-// turn (groups / chunk) divide the stages, and whoever waits for a stage's
+// turn divide the stages, and whoever waits for a stage's
 // phase has seen the phase before it.  A producer gives up at a wait that runs out
 // (recorded), and in any case waits, with a limit, for its last copies: none
 // lands in memory that is no longer the kernel's.  filled(): a barrier of the
@@ -162,7 +162,7 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
   uint32_t ph = 0;
   long long turn = ring.first, chunk = warp;
   const auto advance = [&](int chunks) {
-    for (sub += chunks * plan.chunk; sub >= plan.groups; sub -= plan.groups) turn += ring.step;
+    for (sub += chunks * plan.chunk; sub >= plan.turn; sub -= plan.turn) turn += ring.step;
     for (s += chunks; s >= plan.stages; s -= plan.stages) ph ^= 1u;
   };
   if (warp >= plan.producers) {          // has no chunks
@@ -171,7 +171,7 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
   }
   advance(warp);
   for (;; chunk += plan.producers, advance(plan.producers)) {
-    const long long row0 = turn * plan.groups + sub;
+    const long long row0 = turn * plan.turn + sub;
     if (row0 >= plan.rows) break;
     const int rows = static_cast<int>(min(static_cast<long long>(plan.chunk), plan.rows - row0));
     if (!met && chunk >= plan.stages) {
@@ -211,17 +211,17 @@ __device__ __forceinline__ void produce_rows(const RowSource (&in)[N], const Row
 }
 
 // A computing thread's view of the ring: of its group's stages, every
-// groups / chunk'th.
+// turn / chunk'th.
 struct RingReader {
   const RingPlace& ring;
   const RowPlan& plan;
   unsigned* err;
-  int at_row, s, step;                   // the group's row within the stage
+  int at_row, s, step;                   // the group's first row within the stage
   uint32_t ph = 0;
   bool lost = false;
 
-  __device__ __forceinline__ RingReader(const RingPlace& r, const RowPlan& p, unsigned* e, int group)
-      : ring(r), plan(p), err(e), at_row(group % p.chunk), s(group / p.chunk), step(p.groups / p.chunk) {}
+  __device__ __forceinline__ RingReader(const RingPlace& r, const RowPlan& p, unsigned* e, int first)
+      : ring(r), plan(p), err(e), at_row(first % p.chunk), s(first / p.chunk), step(p.turn / p.chunk) {}
   // A wait that runs out is recorded, and the thread goes on (the result is
   // undefined, as the status says): its group's barriers need all of it.
   __device__ __forceinline__ void wait() {
@@ -236,18 +236,18 @@ struct RingReader {
       ph ^= 1u;
     }
   }
-  // The row's statistics.
-  __device__ __forceinline__ float4 stats() const {
+  // The statistics of the group's row i.
+  __device__ __forceinline__ float4 stats(int i) const {
     return *reinterpret_cast<const float4*>(ring.data + static_cast<uint32_t>(s) * plan.stage_bytes + plan.stats_at +
-                                            static_cast<uint32_t>(at_row) * (kStats * 4u));
+                                            static_cast<uint32_t>(at_row + i) * (kStats * 4u));
   }
-  // The group's row of a matrix in the current stage; what lies `shift` bytes
-  // behind a 16-byte boundary in memory lies so in the stage.
-  __device__ __forceinline__ const uint8_t* at(const RowSource& m, long long row, bool vec) const {
+  // The group's row i, `row`, of a matrix in the current stage; what lies so
+  // many bytes behind a 16-byte boundary in memory lies so in the stage.
+  __device__ __forceinline__ const uint8_t* at(const RowSource& m, long long row, int i, bool vec) const {
     const uint8_t* const p = ring.data + static_cast<uint32_t>(s) * plan.stage_bytes + m.at +
-                             static_cast<uint32_t>(at_row) * m.pitch;
+                             static_cast<uint32_t>(at_row + i) * m.pitch;
     if (vec) return p;
-    return p + (static_cast<uint32_t>(first_byte(m, m.packed ? row - at_row : row, ring.col0)) & 15u);
+    return p + (static_cast<uint32_t>(first_byte(m, m.packed ? row - at_row - i : row, ring.col0)) & 15u);
   }
 };
 
@@ -390,18 +390,20 @@ __device__ __forceinline__ float vector_value(const void* p, bool f32, long long
 }
 
 // ---------------------------------------------------------------- sums over a row
+constexpr int kMostSums = 4;             // at a time
+
 struct RowShared {
-  float2 warps[2][kRowWarps];            // two sets of buffers, which take turns
-  float2 ctas[2][kRowWarps][kMostCtas];  // of each group
+  alignas(16) float warps[2][kRowWarps][kMostSums];        // two sets of buffers, which take turns
+  float2 ctas[2][kRowWarps][kMostCtas][kMostSums / 2];     // of each group
   uint64_t bars[2][kRowWarps];
 };
 
-// Sums of one or two values over the threads of a group and, with a cluster,
-// over the CTAs that share its row; every thread gets them.  A set of buffers
-// is written again only after a barrier that every reader has passed.  CTAs
-// exchange theirs by asynchronous stores that a barrier at the destination
-// counts, and add them in order: a barrier of the cluster would wait for every
-// store in flight.
+// Sums of N values (1, 2 or 4) over the threads of a group and, with a
+// cluster, over the CTAs that share its rows; every thread gets them.  A set
+// of buffers is written again only after a barrier that every reader has
+// passed.  CTAs exchange theirs by asynchronous stores that a barrier at the
+// destination counts, and add them in order: a barrier of the cluster would
+// wait for every store in flight.
 struct RowSums {
   RowShared& shared;
   const RowPlan& plan;
@@ -417,45 +419,58 @@ struct RowSums {
   }
   template <int N>
   __device__ __forceinline__ void add(float (&v)[N]) {
-    static_assert(N == 1 || N == 2, "one or two values");
+    static_assert(N == 1 || N == 2 || N == 4, "values");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = plan.lanes >> 5;
-    float x;                             // N == 2: lanes below 16 sum the first value, the others the second
-    if constexpr (N == 2) {
+    // halves of the warp go on with half of the values each, until each has
+    // one: value i ends up in the lanes from 32 i / N on
+    float x;
+    if constexpr (N == 4) {
+      const bool up = lane & 16, upper = lane & 8;
+      float y[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) y[i] = (up ? v[N - 2 + i] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[N - 2 + i], 16);
+      x = (upper ? y[1] : y[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? y[0] : y[1], 8);
+    } else if constexpr (N == 2) {
       x = (lane < 16 ? v[0] : v[1]) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? v[1] : v[0], 16);
     } else {
       x = v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    for (int o = N == 4 ? 4 : 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    constexpr int kLanes = 32 / N;
     if (warps > 1) {
-      if (lane % 16 == 0 && (N == 2 || lane == 0)) (&shared.warps[flip][warp].x)[lane / 16] = x;
+      if (lane % kLanes == 0) shared.warps[flip][warp][lane / kLanes] = x;
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(plan.lanes) : "memory");
-      const float2* const of = shared.warps[flip] + group * warps;
       if (warps <= 4) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j >= warps) break;
-          const float2 f = of[j];
-          v[0] += f.x;
-          if (N == 2) v[N - 1] += f.y;
+          const float* const of = shared.warps[flip][group * warps + j];
+          float f[kMostSums];
+          if constexpr (N == 4)
+            *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(of);
+          else
+            *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(of);
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[i] += f[i];
         }
       } else {
-        const int j = lane & 15;
-        const float2 f = j < warps ? of[j] : make_float2(0.0f, 0.0f);
-        v[0] = f.x;
-        if (N == 2) v[N - 1] = f.y;
+        // lane: value lane % N of a warp, of two with N = 4
+        constexpr int kOf = N == 4 ? 8 : 16;
+        const float* const of = shared.warps[flip][group * warps] + lane % N;
+        const int w = lane / N % kOf;
+        x = w < warps ? of[w * kMostSums] : 0.0f;
+        if (N == 4 && w + kOf < warps) x += of[(w + kOf) * kMostSums];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
+        for (int o = N * kOf / 2; o >= N; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
 #pragma unroll
-          for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+        for (int i = 0; i < N; ++i) v[i] = N == 1 ? x : __shfl_sync(0xFFFFFFFFu, x, i);
       }
-    } else if constexpr (N == 2) {
-      v[0] = __shfl_sync(0xFFFFFFFFu, x, 0);
-      v[1] = __shfl_sync(0xFFFFFFFFu, x, 16);
     } else {
-      v[0] = x;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = N == 1 ? x : __shfl_sync(0xFFFFFFFFu, x, i * kLanes);
     }
     if (plan.ctas > 1) exchange<N>(v);
     flip ^= 1u;
@@ -464,19 +479,26 @@ struct RowSums {
  private:
   template <int N>
   __device__ __forceinline__ void exchange(float (&v)[N]) {
+    constexpr int kPairs = (N + 1) / 2, kNext = N > 1 ? 1 : 0;
     const uint32_t bar = smem_addr(&shared.bars[flip][group]);
-    if (t == 0) mbar_arrive_expect_tx(bar, plan.ctas * 8u);
-    if (t < plan.ctas)
-      store_async(map_rank(smem_addr(&shared.ctas[flip][group][rank]), static_cast<uint32_t>(t)), v[0],
-                  N > 1 ? v[N - 1] : 0.0f, map_rank(bar, static_cast<uint32_t>(t)));
+    if (t == 0) mbar_arrive_expect_tx(bar, plan.ctas * kPairs * 8u);
+    if (t < plan.ctas) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+        store_async(map_rank(smem_addr(&shared.ctas[flip][group][rank][i]), static_cast<uint32_t>(t)), v[2 * i],
+                    N > 1 ? v[2 * i + kNext] : 0.0f, map_rank(bar, static_cast<uint32_t>(t)));
+    }
     if (!lost) lost = !mbar_wait_cluster(bar, round, err, kSiteTransformFull);
     round ^= flip;                       // both have been waited for
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.0f;
     for (int r = 0; r < plan.ctas; ++r) {
-      const float2 f = shared.ctas[flip][group][r];
-      v[0] += f.x;
-      if (N > 1) v[N - 1] += f.y;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 f = shared.ctas[flip][group][r][i];
+        v[2 * i] += f.x;
+        if (N > 1) v[2 * i + kNext] += f.y;
+      }
     }
   }
 };
