@@ -3,10 +3,9 @@
 //
 // Both conversions are bound by memory traffic: 3 bytes an element in bfloat16,
 // 5 in fp32, and a byte per 32 elements.  A warp takes 256 columns of a row at
-// a time, four such pieces in flight: of rows on 16-byte boundaries each lane
-// 8 columns (a block is four lanes), of others each lane one column of every
-// 32 (a block is a warp), so that loads and stores of single elements lie side
-// by side.
+// a time, four such pieces in flight, a lane 8 columns (a block is four lanes).
+// Codes start on 16-byte boundaries; rows of the matrix that do not are moved
+// in 16-byte blocks all the same, and shifted against the codes in registers.
 //
 // The weight gradient dw = dy^T x is a product on the tensor cores
 // (half_gemm.cu) that reads both operands as they are stored.  e4m3 codes
@@ -19,6 +18,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/gemm_f32_block.h"
 #include "device_common.cuh"
@@ -53,23 +53,28 @@ struct ConvertArgs {
   unsigned* err;
 };
 
-// The pieces of one warp: every `warps`-th of rows x pieces, without a
-// division per piece.
+// The pieces of one warp: kFlight side by side at a time, the CTA's warps side
+// by side, and on by a grid of them.  One division at the start.
 struct Pieces {
-  long long row;
+  long long row, d_row;
   int piece, per_row, d_piece;
-  long long d_row;
 
   __device__ __forceinline__ Pieces(int per) : per_row(per) {
     constexpr int kWarps = kConvertThreads / 32;
-    const long long first = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5);
-    const long long warps = gridDim.x * static_cast<long long>(kWarps);
+    const long long first = (blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5)) * kFlight;
+    const long long skip = (gridDim.x * static_cast<long long>(kWarps) - 1) * kFlight;
     row = first / per;
     piece = static_cast<int>(first - row * per);
-    d_row = warps / per;
-    d_piece = static_cast<int>(warps - d_row * per);
+    d_row = skip / per;
+    d_piece = static_cast<int>(skip - d_row * per);
   }
   __device__ __forceinline__ void next() {
+    if (++piece == per_row) {
+      piece = 0;
+      ++row;
+    }
+  }
+  __device__ __forceinline__ void next_grid() {
     row += d_row;
     piece += d_piece;
     if (piece >= per_row) {
@@ -89,140 +94,214 @@ __device__ __forceinline__ bool codes_ok(const ConvertArgs& a, long long row, in
 }
 
 // ---------------------------------------------------------------- keeping
+// 8 elements of a row that starts `off` bytes above a 16-byte boundary, from
+// the whole blocks that they lie in: the lane's own ones and the first of the
+// next lane's (the last lane loads it), shifted.  The same off for all lanes.
+template <class T>
+__device__ __forceinline__ void load_shifted(const T* p, uint32_t off, Raw<T, 8>& x) {
+  constexpr int kWords = Raw<T, 8>::kWords;
+  const int lane = threadIdx.x & 31;
+  const uint4* const from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{15});
+  uint32_t w[kWords + 4];
+#pragma unroll
+  for (int i = 0; i < kWords / 4; ++i) {
+    const uint4 q = __ldcs(from + i);
+    w[4 * i] = q.x;
+    w[4 * i + 1] = q.y;
+    w[4 * i + 2] = q.z;
+    w[4 * i + 3] = q.w;
+  }
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  if (lane == 31) q = __ldcs(from + kWords / 4);
+  const uint32_t last[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
+    w[kWords + i] = lane == 31 ? last[i] : next;
+  }
+  const auto take = [&](auto words) {
+    constexpr int kFrom = decltype(words)::value;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      x.w[i] = sizeof(T) == 2 ? __funnelshift_r(w[i + kFrom], w[min(i + kFrom + 1, kWords + 3)], off % 4 * 8) : w[i + kFrom];
+  };
+  switch (off / 4) {
+    case 0: take(std::integral_constant<int, 0>{}); break;
+    case 1: take(std::integral_constant<int, 1>{}); break;
+    case 2: take(std::integral_constant<int, 2>{}); break;
+    default: take(std::integral_constant<int, 3>{}); break;
+  }
+}
+
+// VEC: rows on 16-byte boundaries of whole vectors; else rows that start
+// anywhere, shifted into place (by single elements where the blocks around
+// them are not all the matrix's: at its two ends).
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kConvertThreads) checkpoint_kernel(const ConvertArgs a) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  Pieces at(a.pieces);
-  while (at.row < a.rows) {
+  for (Pieces at(a.pieces); at.row < a.rows; at.next_grid()) {
     // all pieces' loads first
     long long row[kFlight];
-    int col0[kFlight];
-    Raw<T, VEC ? V : 1> x[kFlight][VEC ? 8 / V : 8];
+    int col[kFlight];                    // of the lane's first element
+    Raw<T, 8> x[kFlight];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       row[f] = at.row;
-      col0[f] = at.piece * kPiece;
+      const int col0 = at.piece * kPiece;
+      col[f] = col0 + lane * 8;
       at.next();
-      const T* const p = static_cast<const T*>(a.x) + row[f] * a.ld;
-#pragma unroll
-      for (int i = 0; i < (VEC ? 8 / V : 8); ++i) {
-        const int c = VEC ? col0[f] + lane * 8 + i * V : col0[f] + i * 32 + lane;
-        x[f][i].zero();
-        if (row[f] < a.rows && c < a.width && x_ok<T>(a, row[f], c + (VEC ? V - 1 : 0))) x[f][i].load_once(p + c);
-      }
-    }
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      if (row[f] >= a.rows) break;                        // the warp's
-      uint8_t* const codes = a.codes + row[f] * a.ld_codes;
-      uint8_t* const exponents = a.exponents + row[f] * a.ld_exponents;
+      x[f].zero();
+      if (row[f] >= a.rows) continue;    // the warp's
+      const T* const p = static_cast<const T*>(a.x) + row[f] * a.ld + col[f];
       if constexpr (VEC) {
-        const int c = col0[f] + lane * 8;
-        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = x[f][j / V].at(j % V);
-        uint32_t top = 0;
+        for (int i = 0; i < 8 / V; ++i) {
+          Raw<T, V> q;
+          q.zero();
+          if (col[f] + i * V < a.width && x_ok<T>(a, row[f], col[f] + i * V + V - 1)) q.load_once(p + i * V);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, finite_bits(v[j]));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const uint32_t e = block_exponent(top);
-        const float by = inverse_of(e);
-        uint32_t w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          w[j] = codes_of(v[4 * j] * by, v[4 * j + 1] * by) | codes_of(v[4 * j + 2] * by, v[4 * j + 3] * by) << 16;
-        if (c - lane % 4 * 8 >= a.width || !codes_ok(a, row[f], c + 7)) continue;   // no such block
-        *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
-        if (lane % 4 == 0) exponents[c / kSavedBlock] = static_cast<uint8_t>(e);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col0[f] + i * 32 + lane;
-          const float v = x[f][i].at(0);
-          const uint32_t e = block_exponent(__reduce_max_sync(0xFFFFFFFFu, finite_bits(v)));
-          if (c - lane >= a.width || !codes_ok(a, row[f], c)) continue;
-          codes[c] = static_cast<uint8_t>(codes_of(v * inverse_of(e), 0.0f));
-          if (lane == 0) exponents[c / kSavedBlock] = static_cast<uint8_t>(e);
-        }
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------- bringing back
-// VEC: a row's last vector may reach past its last column, where its codes
-// are 0 (scratch rows).
-template <class T, bool VEC>
-__global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertArgs a) {
-  constexpr int V = 16 / static_cast<int>(sizeof(T));
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  Pieces at(a.pieces);
-  while (at.row < a.rows) {
-    long long row[kFlight];
-    int col0[kFlight];
-    uint2 w[kFlight];
-    uint8_t code[kFlight][VEC ? 1 : 8], e[kFlight][VEC ? 1 : 8];
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      row[f] = at.row;
-      col0[f] = at.piece * kPiece;
-      at.next();
-      const uint8_t* const codes = a.codes + row[f] * a.ld_codes;
-      const uint8_t* const exponents = a.exponents + row[f] * a.ld_exponents;
-      if constexpr (VEC) {
-        const int c = col0[f] + lane * 8;
-        w[f] = make_uint2(0u, 0u);
-        e[f][0] = 1;
-        if (row[f] < a.rows && c < a.width && codes_ok(a, row[f], c + 7)) {
-          w[f] = __ldcs(reinterpret_cast<const uint2*>(codes + c));
-          e[f][0] = __ldg(exponents + c / kSavedBlock);
+          for (int j = 0; j < 4; ++j) x[f].w[4 * i + j] = q.w[j];
         }
       } else {
+        // bytes from the matrix's first to this piece's blocks and to their end
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+        const long long before = (row[f] * a.ld + col0) * static_cast<long long>(sizeof(T)) - off;
+        const long long end = before + kPiece * static_cast<long long>(sizeof(T)) + 16;
+        const bool inside = before >= 0 && end <= static_cast<long long>(stored_extent(a.rows, a.width, a.ld) * sizeof(T));
+        if (inside) {
+          load_shifted<T>(p, off, x[f]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col0[f] + i * 32 + lane;
-          code[f][i] = 0;
-          e[f][i] = 1;
-          if (row[f] < a.rows && c < a.width && codes_ok(a, row[f], c)) {
-            code[f][i] = __ldcs(codes + c);
-            e[f][i] = __ldg(exponents + c / kSavedBlock);
+          for (int j = 0; j < 8; ++j) {
+            Raw<T, 1> e;
+            e.zero();
+            if (col[f] + j < a.width && x_ok<T>(a, row[f], col[f] + j)) e.load_once(p + j);
+            if constexpr (sizeof(T) == 4)
+              x[f].w[j] = e.w[0];
+            else
+              x[f].w[j / 2] |= e.w[0] << (16 * (j & 1));
           }
+        }
+        if (col0 + kPiece > a.width) {   // the row's last piece: nothing behind its end
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col[f] + j >= a.width) x[f].w[sizeof(T) == 4 ? j : j / 2] &= sizeof(T) == 4 ? 0u : (j & 1 ? 0xFFFFu : 0xFFFF0000u);
         }
       }
     }
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       if (row[f] >= a.rows) break;
+      const int c = col[f];
+      uint32_t top = largest_bits(x[f]);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const bool odd = __any_sync(0xFFFFFFFFu, top >= kOddBits);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = x[f].at(j);
+      if (odd) {                         // perhaps not finite
+        top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, finite_bits(v[j]));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      }
+      const uint32_t e = block_exponent(top);
+      const float by = inverse_of(e);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = odd ? codes_of(v[2 * j] * by, v[2 * j + 1] * by, e == kLargestExponent ? 240.0f : 448.0f)
+                   : finite_codes(v[2 * j] * by, v[2 * j + 1] * by);
+      if (c - lane % 4 * 8 >= a.width || !codes_ok(a, row[f], c + 7)) continue;   // no such block
+      *reinterpret_cast<uint2*>(a.codes + row[f] * a.ld_codes + c) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      if (lane % 4 == 0) a.exponents[row[f] * a.ld_exponents + c / kSavedBlock] = static_cast<uint8_t>(e);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- bringing back
+// VEC: rows on 16-byte boundaries; a row's last vector may reach past its last
+// column, where its codes are 0 (scratch rows).  Else a lane has the 8
+// elements of whole 16-byte blocks of the output, `above` elements before the
+// 8 of its codes, which it takes with those before (the lane's before).
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertArgs a) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  for (Pieces at(a.pieces); at.row < a.rows; at.next_grid()) {
+    long long row[kFlight];
+    int col[kFlight];                    // of the lane's codes
+    uint2 w[kFlight], before[kFlight];
+    uint8_t e[kFlight], e_before[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      row[f] = at.row;
+      col[f] = at.piece * kPiece + lane * 8;
+      at.next();
+      w[f] = before[f] = make_uint2(0u, 0u);
+      e[f] = e_before[f] = 1;
+      if (row[f] >= a.rows) continue;
+      const uint8_t* const codes = a.codes + row[f] * a.ld_codes;
+      const uint8_t* const exponents = a.exponents + row[f] * a.ld_exponents;
+      const int c = col[f];
+      if (c < a.width && codes_ok(a, row[f], c + 7)) {
+        w[f] = __ldcs(reinterpret_cast<const uint2*>(codes + c));
+        e[f] = __ldg(exponents + c / kSavedBlock);
+      }
+      if (!VEC && c > 0 && c - 8 < a.width && codes_ok(a, row[f], c - 1)) {
+        if (lane == 0) before[f] = __ldcs(reinterpret_cast<const uint2*>(codes + c - 8));
+        e_before[f] = __ldg(exponents + (c - 8) / kSavedBlock);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      if (row[f] >= a.rows) break;
       T* const out = static_cast<T*>(a.out) + row[f] * a.ld;
+      int c = col[f];
+      float v[8];
       if constexpr (VEC) {
-        const int c = col0[f] + lane * 8;
-        const float by = power_of(e[f][0]);
-        float v[8];
+        const float by = power_of(e[f]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 p = values_of(((j < 2 ? w[f].x : w[f].y) >> (16 * (j & 1))) & 0xFFFFu);
           v[2 * j] = p.x * by;
           v[2 * j + 1] = p.y * by;
         }
-#pragma unroll
-        for (int i = 0; i < 8 / V; ++i) {
-          float part[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) part[j] = v[i * V + j];
-          if (c + i * V < a.width && x_ok<T>(a, row[f], c + i * V + V - 1)) store_vec<T, V>(out + c + i * V, part);
-        }
       } else {
+        const int above = static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T));
+        const uint2 left = make_uint2(__shfl_up_sync(0xFFFFFFFFu, w[f].x, 1), __shfl_up_sync(0xFFFFFFFFu, w[f].y, 1));
+        if (lane > 0) before[f] = left;
+        // bytes 8 - above .. 15 - above of the 16
+        const unsigned long long lo = static_cast<unsigned long long>(before[f].y) << 32 | before[f].x;
+        const unsigned long long hi = static_cast<unsigned long long>(w[f].y) << 32 | w[f].x;
+        const unsigned long long q = above ? lo >> (8 * (8 - above)) | hi << (8 * above) : hi;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col0[f] + i * 32 + lane;
-          if (c < a.width && x_ok<T>(a, row[f], c))
-            out[c] = from_f32<T>(values_of(code[f][i]).x * power_of(e[f][i]));
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = values_of(static_cast<uint32_t>(q >> (16 * j)) & 0xFFFFu);
+          v[2 * j] = p.x * power_of(2 * j < above ? e_before[f] : e[f]);
+          v[2 * j + 1] = p.y * power_of(2 * j + 1 < above ? e_before[f] : e[f]);
+        }
+        c -= above;
+      }
+#pragma unroll
+      for (int i = 0; i < 8 / V; ++i) {
+        float part[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) part[j] = v[i * V + j];
+        const int first = c + i * V;
+        if (VEC ? first < a.width : first >= 0 && first + V <= a.width) {
+          if (x_ok<T>(a, row[f], first + V - 1)) store_vec<T, V>(out + first, part);
+        } else if (!VEC) {               // the row's ends
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (first + j >= 0 && first + j < a.width && x_ok<T>(a, row[f], first + j)) out[first + j] = from_f32<T>(part[j]);
         }
       }
     }
@@ -262,11 +341,13 @@ bool apart(const void* p, size_t bytes, const void* codes, long long ld_codes, c
          !ranges_overlap(p, bytes, exponents, static_cast<size_t>(rows) * ld_exponents);
 }
 
-int launch_convert(void (*kernel)(ConvertArgs), ConvertArgs& a, int num_sms, cudaStream_t stream, int* launches) {
-  a.pieces = (a.width - 1) / kPiece + 1;
+int launch_convert(void (*kernel)(ConvertArgs), ConvertArgs& a, int spare, cudaStream_t stream, int* launches) {
+  // bringing rows back that start above a boundary takes what a piece lacks of its last block
+  a.pieces = static_cast<int>((a.width - 1LL + spare) / kPiece + 1);
+  // as many CTAs as there is work for: a fixed number would leave the last ones of a wave alone
   constexpr long long kPerCta = kConvertThreads / 32 * kFlight;
   const long long ctas = a.rows > LLONG_MAX / a.pieces ? LLONG_MAX : (a.rows * a.pieces - 1) / kPerCta + 1;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(ctas, 8LL * num_sms));
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(ctas, INT_MAX));
   if (launch_dependent(kernel, dim3(grid), dim3(kConvertThreads), 0, stream, a) != cudaSuccess) {
     (void)cudaGetLastError();
     return GEMM_F32_ELAUNCH;
@@ -308,7 +389,7 @@ extern "C" int gemm_f32_checkpoint(int type, long long rows, int width, const vo
   const int rc = launch_convert(type == GEMM_F32_TYPE_F32
                                     ? vec ? checkpoint_kernel<float, true> : checkpoint_kernel<float, false>
                                     : vec ? checkpoint_kernel<bf16, true> : checkpoint_kernel<bf16, false>,
-                                a, num_sms, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+                                a, 0, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
   if (rc == GEMM_F32_OK) note_launches(launches, "checkpoint_kernel");
   return rc;
 }
@@ -330,7 +411,7 @@ extern "C" int gemm_f32_restore(int type, long long rows, int width, const unsig
   const bool vec = on_boundaries(out, ldo, es) && width * es % 16 == 0;
   const int rc = launch_convert(type == GEMM_F32_TYPE_F32 ? vec ? restore_kernel<float, true> : restore_kernel<float, false>
                                                           : vec ? restore_kernel<bf16, true> : restore_kernel<bf16, false>,
-                                a, num_sms, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+                                a, vec ? 0 : 7, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
   if (rc == GEMM_F32_OK) note_launches(launches, "restore_kernel");
   return rc;
 }
@@ -370,7 +451,7 @@ int run_weight_grad(const WeightGrad& c, cudaStream_t stream, int* launches) {
   if (!scratch) return GEMM_F32_ESCRATCH;
   ConvertArgs x = {c.rows,      static_cast<int>(ldx), nullptr, scratch + at_x, ldx, const_cast<uint8_t*>(c.codes), c.ld_codes,
                    const_cast<uint8_t*>(c.exponents), c.ld_exponents,   0,       err};
-  int rc = launch_convert(restore_kernel<bf16, true>, x, num_sms, stream, launches);
+  int rc = launch_convert(restore_kernel<bf16, true>, x, 0, stream, launches);
   if (rc != GEMM_F32_OK) return rc;
   const long long plane = lddy * c.rows;
   if (packed) {

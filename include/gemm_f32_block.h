@@ -11,9 +11,10 @@
  * scratch and CUDA graphs as in gemm_f32_lm.h.
  *
  * gemm_f32_last_kernel() names the kernel of a call's main pass:
- * "block_norm_kernel" or "block_norm_grad_kernel" (rows of up to 32768
- * columns), "block_norm_wide_kernel" or "block_norm_grad_wide_kernel" (wider
- * ones), "block_columns_kernel" (gradient of no rows), "checkpoint_kernel",
+ * "block_norm_kernel" (rows of up to 32768 columns at least, 131072 of them
+ * with one vector) or "block_norm_grad_kernel" (up to 32768),
+ * "block_norm_wide_kernel" or "block_norm_grad_wide_kernel" (wider ones),
+ * "block_columns_kernel" (gradient of no rows), "checkpoint_kernel",
  * "restore_kernel", "half_gemm_kernel" (weight gradient), "memset" (weight
  * gradient of no rows).
  *
@@ -119,8 +120,9 @@ int gemm_f32_block_norm_grad(const gemm_f32_block_t* block, const void* dy, long
 /* Keeps x (rows x width) in 8 bits.  Every 32 columns of a row share a power
  * of two, the least that takes their largest finite magnitude to 448 or below
  * (and no less than 2^-126); a code is x over that power, rounded to the
- * nearest e4m3 value, ties to even.  So a value is off by at most 2^-4 of
- * itself or 2^-10 of the power.  Infinities and NaN are kept as NaN.
+ * nearest e4m3 value, ties to even (to the one below where that would stand
+ * for 2^128).  So a value is off by at most 2^-4 of itself or 2^-10 of the
+ * power.  Infinities and NaN are kept as NaN.
  * codes: rows of ld_codes bytes, a multiple of 16 and at least width rounded
  * up to 32, on a 16-byte boundary; all codes of a block are written, 0 from
  * column `width` on.  exponents: rows of ld_exponents bytes, a multiple of 16
