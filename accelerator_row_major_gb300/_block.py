@@ -71,44 +71,48 @@ def _saved(name, saved):
 
 def _rows(name, t, x):
     """The C description of a matrix of x's shape, type and device, or of a checkpoint of such a one."""
-    r = Rows()
-    if isinstance(t, Checkpoint):
-        kind, dev, rows, width = _saved(name, t)
-        if (rows, width) != tuple(x.shape) or t.dtype is not x.dtype or dev != x.get_device():
-            raise ValueError("%s must be kept from a %s matrix of shape %s on %s" % (name, x.dtype, tuple(x.shape), x.device))
-        r.codes, r.ld_codes = t.codes.data_ptr(), t.codes.shape[1]
-        r.exponents, r.ld_exponents = t.exponents.data_ptr(), t.exponents.shape[1]
-    else:
-        r.data, r.ld = t.data_ptr(), _like(name, t, x)
-    return r
+    if not isinstance(t, Checkpoint):
+        return Rows(t.data_ptr(), _like(name, t, x))
+    kind, dev, rows, width = _saved(name, t)
+    if (rows, width) != tuple(x.shape) or t.dtype is not x.dtype or dev != x.get_device():
+        raise ValueError("%s must be kept from a %s matrix of shape %s on %s" % (name, x.dtype, tuple(x.shape), x.device))
+    return Rows(None, 0, t.codes.data_ptr(), t.codes.shape[1], t.exponents.data_ptr(), t.exponents.shape[1])
 
 
 def _block(x, matrix, kind, eps, weight, bias, post, post_weight, post_bias, gate, residual_scale, branch_scale):
     """(the C description, the vectors' type) of a block's end on matrices like x."""
     code, dev, rows, width, _ = matrix
-    if kind not in NORMS:
+    norm = NORMS.get(kind)
+    if norm is None:
         raise ValueError("kind must be one of %s" % ", ".join(sorted(NORMS)))
     if not post and (post_weight is not None or post_bias is not None):
         raise ValueError("post_weight and post_bias belong to post=True")
-    if kind == "rms" and (bias is not None or post_bias is not None):
+    if norm and (bias is not None or post_bias is not None):
         raise ValueError("an rms norm has no bias")
-    b = Block()
-    wtype = None
-    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias),
-                    ("gate", gate)):
-        if t is None:
-            continue
-        if name == "gate" and t.dim() == 2:
-            b.gate, b.ld_gate = t.data_ptr(), _like("gate", t, x)
-            continue
-        if wtype is None:
-            wtype = _weight_type(x, t)
-        setattr(b, name, _vector(name, t, width, dev, (wtype,)))
+    wtype = types = None
+    pw = pb = ppw = ppb = pg = ldg = 0
+    if weight is not None:
+        types = (wtype := _weight_type(x, weight),)
+        pw = _vector("weight", weight, width, dev, types)
+    if bias is not None:
+        types = types or (wtype := _weight_type(x, bias),)
+        pb = _vector("bias", bias, width, dev, types)
+    if post_weight is not None:
+        types = types or (wtype := _weight_type(x, post_weight),)
+        ppw = _vector("post_weight", post_weight, width, dev, types)
+    if post_bias is not None:
+        types = types or (wtype := _weight_type(x, post_bias),)
+        ppb = _vector("post_bias", post_bias, width, dev, types)
+    if gate is not None:
+        if gate.dim() == 2:
+            pg, ldg = gate.data_ptr(), _like("gate", gate, x)
+        else:
+            types = types or (wtype := _weight_type(x, gate),)
+            pg = _vector("gate", gate, width, dev, types)
     if wtype is None:
         wtype = _F32
-    b.type, b.weight_type, b.norm, b.post, b.rows, b.width = code, _TYPES[wtype], NORMS[kind], bool(post), rows, width
-    b.eps, b.residual_scale, b.branch_scale = eps, residual_scale, branch_scale
-    return b, wtype
+    return Block(code, _TYPES[wtype], norm, 1 if post else 0, rows, width, eps, residual_scale, branch_scale, pw, pb, ppw, ppb, pg,
+                 ldg), wtype
 
 
 def block_norm(branch, residual, weight=None, bias=None, kind="layer", eps=1e-5, gate=None, post=False, post_weight=None,
@@ -171,7 +175,8 @@ def block_norm_grad(dy, dh, h, branch, stats, weight=None, kind="layer", gate=No
     otherwise); stats and the other arguments are the forward call's
     (post_bias matters with both post and a gate).  dbranch, dresidual and the
     dgate of a matrix hold dy's type, the vectors' gradients the vectors' type
-    (float32 where there is none).  An rms norm has no dbias or dpost_bias.
+    (float32 where there is none), as rows of one matrix.  An rms norm has no
+    dbias or dpost_bias.
     Where nothing stands between branch and h and both scales are equal,
     dbranch and dresidual are one tensor.  `out`, the tensor for dresidual,
     may be dy, dh, h, branch or a gate matrix."""
@@ -198,22 +203,18 @@ def block_norm_grad(dy, dh, h, branch, stats, weight=None, kind="layer", gate=No
         dresidual, ldr = out, _like("out", out, dy)
     same = not uses_branch and residual_scale == branch_scale
     dbranch = dresidual if same else torch.empty_like(dy, memory_format=torch.contiguous_format)
-    layer = kind == "layer"
-
-    def vector(wanted):
-        return torch.empty(width, dtype=wtype, device=dy.device) if wanted else None
-
-    dweight, dbias, dpost_weight, dpost_bias = vector(True), vector(layer), vector(post), vector(post and layer)
-    dgate = None
-    if gate is not None:
-        dgate = torch.empty_like(dy, memory_format=torch.contiguous_format) if gate.dim() == 2 else vector(True)
-
-    def at(t):
-        return 0 if t is None else t.data_ptr()
-
-    _call("gemm_f32_block_norm_grad", _byref(b), dy.data_ptr(), lddy, at(dh), lddh, _byref(c_h),
+    layer, channel = kind == "layer", gate is not None and gate.dim() == 1
+    # the vectors' gradients are rows of one matrix
+    vectors = iter(torch.empty(((2 if layer else 1) * (2 if post else 1) + channel, width), dtype=wtype, device=dy.device).unbind(0))
+    dweight, dbias = next(vectors), next(vectors) if layer else None
+    dpost_weight, dpost_bias = next(vectors) if post else None, next(vectors) if post and layer else None
+    dgate = next(vectors) if channel else None
+    if gate is not None and not channel:
+        dgate = torch.empty_like(dy, memory_format=torch.contiguous_format)
+    _call("gemm_f32_block_norm_grad", _byref(b), dy.data_ptr(), lddy, 0 if dh is None else dh.data_ptr(), lddh, _byref(c_h),
           _byref(c_branch) if uses_branch else None, stats.data_ptr(), 0 if same else dbranch.data_ptr(), width,
-          dresidual.data_ptr(), ldr, at(dgate), width, dweight.data_ptr(), at(dbias), at(dpost_weight), at(dpost_bias),
+          dresidual.data_ptr(), ldr, 0 if dgate is None else dgate.data_ptr(), width, dweight.data_ptr(),
+          dbias.data_ptr() if layer else 0, dpost_weight.data_ptr() if post else 0, dpost_bias.data_ptr() if post and layer else 0,
           _lm._raw_stream(dev))
     return BlockNormGrads(dbranch, dresidual, dweight, dbias, dgate, dpost_weight, dpost_bias)
 

@@ -934,6 +934,8 @@ Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const Lane 
         least = cost;
       }
     }
+    // more CTAs a row are for rows that leave a CTA no second group, where there are rows for one
+    if (best.lane.ne && (best.plan.groups > 1 || plan.rows <= l.num_sms)) break;
   }
   return best;
 }
