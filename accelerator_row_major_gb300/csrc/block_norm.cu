@@ -15,6 +15,8 @@ namespace gemm_f32_impl {
 
 namespace {
 
+constexpr int kMostWidth = INT_MAX - 1024;   // a step beyond the last column stays within an int
+
 size_t type_size(int type) { return type == GEMM_F32_TYPE_F32 ? 4 : 2; }
 
 bool aligned_to(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -65,7 +67,7 @@ bool block_ok(const gemm_f32_block_t* b) {
   if (b->type != GEMM_F32_TYPE_F32 && b->type != GEMM_F32_TYPE_BF16) return false;
   if (b->weight_type != GEMM_F32_TYPE_F32 && b->weight_type != b->type) return false;
   if (b->norm != GEMM_F32_NORM_LAYER && b->norm != GEMM_F32_NORM_RMS) return false;
-  if ((b->post != 0 && b->post != 1) || b->rows < 0 || b->width < 1) return false;
+  if ((b->post != 0 && b->post != 1) || b->rows < 0 || b->width < 1 || b->width > kMostWidth) return false;
   if (!std::isfinite(b->residual_scale) || !std::isfinite(b->branch_scale)) return false;
   if (b->norm == GEMM_F32_NORM_RMS && (b->bias || b->post_bias)) return false;
   if (!b->post && (b->post_weight || b->post_bias)) return false;

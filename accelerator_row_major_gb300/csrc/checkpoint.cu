@@ -309,6 +309,8 @@ __global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertA
 }
 
 // ---------------------------------------------------------------- host side
+constexpr int kMost = INT_MAX - 1024;    // tiles and pieces rounded up stay within an int
+
 size_t type_size(int type) { return type == GEMM_F32_TYPE_F32 ? 4 : 2; }
 
 bool aligned_to(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -374,7 +376,7 @@ extern "C" int gemm_f32_checkpoint(int type, long long rows, int width, const vo
                                    unsigned char* codes, long long ld_codes, unsigned char* exponents,
                                    long long ld_exponents, gemm_f32_stream_t stream_handle) {
   note_launches(0, "none");
-  if (!type_ok(type) || rows < 0 || width < 1) return GEMM_F32_EINVAL;
+  if (!type_ok(type) || rows < 0 || width < 1 || width > kMost) return GEMM_F32_EINVAL;
   if (rows == 0) return GEMM_F32_OK;
   const size_t es = type_size(type);
   if (!matrix_ok(x, ldx, rows, width, es) || !saved_ok(codes, ld_codes, exponents, ld_exponents, rows, width))
@@ -398,7 +400,7 @@ extern "C" int gemm_f32_restore(int type, long long rows, int width, const unsig
                                 const unsigned char* exponents, long long ld_exponents, void* out, long long ldo,
                                 gemm_f32_stream_t stream_handle) {
   note_launches(0, "none");
-  if (!type_ok(type) || rows < 0 || width < 1) return GEMM_F32_EINVAL;
+  if (!type_ok(type) || rows < 0 || width < 1 || width > kMost) return GEMM_F32_EINVAL;
   if (rows == 0) return GEMM_F32_OK;
   const size_t es = type_size(type);
   if (!matrix_ok(out, ldo, rows, width, es) || !saved_ok(codes, ld_codes, exponents, ld_exponents, rows, width) ||
@@ -489,7 +491,6 @@ extern "C" int gemm_f32_weight_grad(int type, long long rows, int width, int out
                                     long long ld_exponents, int dw_type, void* dw, long long lddw, int accumulate,
                                     gemm_f32_stream_t stream_handle) {
   note_launches(0, "none");
-  constexpr int kMost = INT_MAX - 256;   // tiles rounded up stay within an int
   if (!type_ok(type) || (dw_type != type && dw_type != GEMM_F32_TYPE_F32)) return GEMM_F32_EINVAL;
   if (accumulate != 0 && (accumulate != 1 || dw_type != GEMM_F32_TYPE_F32)) return GEMM_F32_EINVAL;
   if (rows < 0 || rows > kMost || width < 1 || width > kMost || out < 1 || out > kMost) return GEMM_F32_EINVAL;

@@ -78,9 +78,9 @@ typedef struct gemm_f32_rows {
  * of h and, with `post`, mean_b and rstd_b.  y and h may each be branch,
  * residual or a gate matrix itself, with the same stride; they overlap
  * nothing else.  rows == 0 does nothing.
- * Returns 0, GEMM_F32_EINVAL (an unknown type or norm, width < 1, rows < 0, a
- * stride below width, eps negative, or eps or a scale not finite, a null or
- * misaligned pointer, a bias with GEMM_F32_NORM_RMS, post_weight or post_bias
+ * Returns 0, GEMM_F32_EINVAL (an unknown type or norm, width < 1 or above
+ * 2^31 - 1025, rows < 0, a stride below width, eps negative, or eps or a
+ * scale not finite, a null or misaligned pointer, a bias with GEMM_F32_NORM_RMS, post_weight or post_bias
  * without `post`, outputs that overlap), GEMM_F32_EDEVICE or
  * GEMM_F32_ELAUNCH. */
 int gemm_f32_block_norm(const gemm_f32_block_t* block, const void* branch, long long ld_branch,
@@ -144,12 +144,13 @@ int gemm_f32_restore(int type, long long rows, int width, const unsigned char* c
  *     dw = dy^T x            dy: rows x out, dw: out x width
  * dy holds `type`; dw holds dw_type, `type` or fp32, and with `accumulate`
  * (fp32 only) is added to.  The values of x are exact on the tensor cores; a
- * dy of fp32 goes in three parts of bfloat16, to about fp32's own rounding.
+ * dy of fp32 goes in three parts of bfloat16, to about fp32's own rounding (an
+ * infinite one gives NaN).
  * Scratch: x in bfloat16 (2 bytes an element), the three parts of an fp32 dy
  * (6 bytes an element) or a copy of a dy whose rows are not on 16-byte
  * boundaries, and partial tiles.  rows == 0 gives zeros (or adds nothing).
  * Returns as gemm_f32_block_norm (and GEMM_F32_EINVAL for rows, width or out
- * above 2^31 - 257), and GEMM_F32_ESCRATCH. */
+ * above 2^31 - 1025), and GEMM_F32_ESCRATCH. */
 int gemm_f32_weight_grad(int type, long long rows, int width, int out, const void* dy, long long lddy,
                          const unsigned char* codes, long long ld_codes,
                          const unsigned char* exponents, long long ld_exponents, int dw_type, void* dw,

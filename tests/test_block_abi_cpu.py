@@ -70,7 +70,7 @@ BAD_BLOCK = [dict(type=2), dict(weight_type=1), dict(type=1, weight_type=3), dic
              dict(width=0), dict(residual_scale=float("nan")), dict(branch_scale=float("inf")), dict(weight=A[0] + 2),
              dict(bias=A[1] + 1), dict(post_weight=A[2] + 2), dict(post_bias=A[3] + 1), dict(gate=A[4] + 2),
              dict(gate=A[4] + 2, ld_gate=0), dict(ld_gate=39), dict(ld_gate=-40), dict(norm=1), dict(norm=1, bias=0),
-             dict(norm=1, post_bias=0), dict(post=0), dict(post=0, post_bias=0), dict(rows=1 << 62, ld_gate=1 << 40)]
+             dict(norm=1, post_bias=0), dict(post=0), dict(post=0, post_bias=0), dict(rows=1 << 62, ld_gate=1 << 40), dict(width=2 ** 31 - 1, ld_gate=0)]
 
 
 @pytest.mark.parametrize("kw", BAD_BLOCK + [
@@ -132,7 +132,8 @@ def _keep(restore=False, **kw):
 @pytest.mark.parametrize("kw", [dict(type=2), dict(rows=-1), dict(width=0), dict(x=0), dict(ldx=39), dict(x=A[0] + 2), dict(codes=0),
                                 dict(codes=A[1] + 8), dict(ldc=40), dict(ldc=48), dict(ldc=72), dict(exponents=0),
                                 dict(exponents=A[2] + 4), dict(lde=2), dict(lde=0), dict(width=1000, ldx=1000, ldc=1024),
-                                dict(codes=A[0]), dict(codes=A[0] + 16 * 39), dict(exponents=A[0] - 16), dict(rows=1 << 60, ldc=1 << 30)])
+                                dict(codes=A[0]), dict(codes=A[0] + 16 * 39), dict(exponents=A[0] - 16), dict(rows=1 << 60, ldc=1 << 30),
+                                dict(width=2 ** 31 - 1000, ldx=1 << 31, ldc=1 << 31, lde=1 << 26)])
 def test_checkpoint_and_restore_reject(g, kw, restore):
     assert _keep(restore, **kw) == g.GEMM_F32_EINVAL
     assert g.gemm_f32_last_launches() == 0 and g.gemm_f32_last_kernel() == "none"
@@ -151,7 +152,7 @@ def _dw(**kw):
                                                                 "exponents", "lde", "dw_type", "dw", "lddw", "accumulate")], 0)
 
 
-@pytest.mark.parametrize("kw", [dict(type=3), dict(dw_type=1), dict(dw_type=2), dict(rows=-1), dict(rows=2 ** 31 - 256), dict(width=0),
+@pytest.mark.parametrize("kw", [dict(type=3), dict(dw_type=1), dict(dw_type=2), dict(rows=-1), dict(rows=2 ** 31 - 1024), dict(width=0),
                                 dict(out=0), dict(out=2 ** 31 - 1, lddy=2 ** 31), dict(dy=0), dict(dy=A[0] + 1), dict(lddy=23),
                                 dict(codes=0), dict(ldc=32), dict(exponents=0), dict(dw=0), dict(dw=A[3] + 2), dict(lddw=39),
                                 dict(accumulate=2), dict(type=1, dw_type=1, accumulate=1), dict(dw=A[0]), dict(dw=A[0] + 4 * 24 * 4 - 4),
