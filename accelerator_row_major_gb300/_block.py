@@ -175,8 +175,7 @@ def block_norm_grad(dy, dh, h, branch, stats, weight=None, kind="layer", gate=No
     otherwise); stats and the other arguments are the forward call's
     (post_bias matters with both post and a gate).  dbranch, dresidual and the
     dgate of a matrix hold dy's type, the vectors' gradients the vectors' type
-    (float32 where there is none), as rows of one matrix.  An rms norm has no
-    dbias or dpost_bias.
+    (float32 where there is none).  An rms norm has no dbias or dpost_bias.
     Where nothing stands between branch and h and both scales are equal,
     dbranch and dresidual are one tensor.  `out`, the tensor for dresidual,
     may be dy, dh, h, branch or a gate matrix."""
@@ -204,11 +203,12 @@ def block_norm_grad(dy, dh, h, branch, stats, weight=None, kind="layer", gate=No
     same = not uses_branch and residual_scale == branch_scale
     dbranch = dresidual if same else torch.empty_like(dy, memory_format=torch.contiguous_format)
     layer, channel = kind == "layer", gate is not None and gate.dim() == 1
-    # the vectors' gradients are rows of one matrix
-    vectors = iter(torch.empty(((2 if layer else 1) * (2 if post else 1) + channel, width), dtype=wtype, device=dy.device).unbind(0))
-    dweight, dbias = next(vectors), next(vectors) if layer else None
-    dpost_weight, dpost_bias = next(vectors) if post else None, next(vectors) if post and layer else None
-    dgate = next(vectors) if channel else None
+    device = dy.device
+    dweight = torch.empty(width, dtype=wtype, device=device)
+    dbias = torch.empty_like(dweight) if layer else None
+    dpost_weight = torch.empty_like(dweight) if post else None
+    dpost_bias = torch.empty_like(dweight) if post and layer else None
+    dgate = torch.empty_like(dweight) if channel else None
     if gate is not None and not channel:
         dgate = torch.empty_like(dy, memory_format=torch.contiguous_format)
     _call("gemm_f32_block_norm_grad", _byref(b), dy.data_ptr(), lddy, 0 if dh is None else dh.data_ptr(), lddh, _byref(c_h),

@@ -8,7 +8,6 @@ torch = pytest.importorskip("torch")
 
 from tests.test_lm_placement_cpu import Stream, Tensor, world  # noqa: E402,F401
 
-Tensor.unbind = lambda self, dim: [Tensor(self.shape[1:], self.dtype, self.dev) for _ in range(self.shape[0])]
 F8, U8, BF16 = torch.float8_e4m3fn, torch.uint8, torch.bfloat16
 
 
