@@ -3,7 +3,7 @@
 //
 // Both conversions are bound by memory traffic: 3 bytes an element in bfloat16,
 // 5 in fp32, and a byte per 32 elements.  A warp takes 256 columns of a row at
-// a time, four such pieces in flight, a lane 8 columns (a block is four lanes).
+// a time, some such pieces in flight, a lane 8 columns (a block is four lanes).
 // Codes start on 16-byte boundaries; rows of the matrix that do not are moved
 // in 16-byte blocks all the same, and shifted against the codes in registers.
 //
@@ -37,7 +37,16 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kConvertThreads = 256;
 constexpr int kPiece = 256;              // columns of a warp's piece
-constexpr int kFlight = 4;               // pieces in flight per warp
+
+// Pieces in flight per warp.  Keeping other rows than bfloat16 ones on
+// boundaries, more warps are worth more than more pieces a warp (65536 x 1024
+// fp32 52 us with two against 56, bfloat16 44 against 42; 65536 x 1001 bfloat16
+// 63 against 72, fp32 72 against 93).
+constexpr int kRestoreFlight = 4;
+template <class T, bool VEC>
+constexpr int keep_flight() {
+  return sizeof(T) == 2 && VEC ? 4 : 2;
+}
 
 struct ConvertArgs {
   long long rows;
@@ -53,16 +62,16 @@ struct ConvertArgs {
   unsigned* err;
 };
 
-// The pieces of one warp: kFlight side by side at a time, the CTA's warps side
+// The pieces of one warp: `flight` side by side at a time, the CTA's warps side
 // by side, and on by a grid of them.  One division at the start.
 struct Pieces {
   long long row, d_row;
   int piece, per_row, d_piece;
 
-  __device__ __forceinline__ Pieces(int per) : per_row(per) {
+  __device__ __forceinline__ Pieces(int per, int flight) : per_row(per) {
     constexpr int kWarps = kConvertThreads / 32;
-    const long long first = (blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5)) * kFlight;
-    const long long skip = (gridDim.x * static_cast<long long>(kWarps) - 1) * kFlight;
+    const long long first = (blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5)) * flight;
+    const long long skip = (gridDim.x * static_cast<long long>(kWarps) - 1) * flight;
     row = first / per;
     piece = static_cast<int>(first - row * per);
     d_row = skip / per;
@@ -137,12 +146,14 @@ __device__ __forceinline__ void load_shifted(const T* p, uint32_t off, Raw<T, 8>
 // anywhere, shifted into place (by single elements where the blocks around
 // them are not all the matrix's: at its two ends).
 template <class T, bool VEC>
-__global__ void __launch_bounds__(kConvertThreads) checkpoint_kernel(const ConvertArgs a) {
+__global__ void __launch_bounds__(kConvertThreads, keep_flight<T, VEC>() == 2 ? 6 : 4)
+    checkpoint_kernel(const ConvertArgs a) {
+  constexpr int kFlight = keep_flight<T, VEC>();
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  for (Pieces at(a.pieces); at.row < a.rows; at.next_grid()) {
+  for (Pieces at(a.pieces, kFlight); at.row < a.rows; at.next_grid()) {
     // all pieces' loads first
     long long row[kFlight];
     int col[kFlight];                    // of the lane's first element
@@ -214,9 +225,11 @@ __global__ void __launch_bounds__(kConvertThreads) checkpoint_kernel(const Conve
       const float by = inverse_of(e);
       uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = odd ? codes_of(v[2 * j] * by, v[2 * j + 1] * by, e == kLargestExponent ? 240.0f : 448.0f)
-                   : finite_codes(v[2 * j] * by, v[2 * j + 1] * by);
+      for (int j = 0; j < 4; ++j) {
+        float q, r;
+        unpair(mul2(pair_of(v[2 * j], v[2 * j + 1]), pair_of(by, by)), q, r);
+        w[j] = odd ? codes_of(q, r, e == kLargestExponent ? 240.0f : 448.0f) : finite_codes(q, r);
+      }
       if (c - lane % 4 * 8 >= a.width || !codes_ok(a, row[f], c + 7)) continue;   // no such block
       *reinterpret_cast<uint2*>(a.codes + row[f] * a.ld_codes + c) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
       if (lane % 4 == 0) a.exponents[row[f] * a.ld_exponents + c / kSavedBlock] = static_cast<uint8_t>(e);
@@ -231,11 +244,12 @@ __global__ void __launch_bounds__(kConvertThreads) checkpoint_kernel(const Conve
 // 8 of its codes, which it takes with those before (the lane's before).
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertArgs a) {
+  constexpr int kFlight = kRestoreFlight;
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  for (Pieces at(a.pieces); at.row < a.rows; at.next_grid()) {
+  for (Pieces at(a.pieces, kFlight); at.row < a.rows; at.next_grid()) {
     long long row[kFlight];
     int col[kFlight];                    // of the lane's codes
     uint2 w[kFlight], before[kFlight];
@@ -343,12 +357,12 @@ bool apart(const void* p, size_t bytes, const void* codes, long long ld_codes, c
          !ranges_overlap(p, bytes, exponents, static_cast<size_t>(rows) * ld_exponents);
 }
 
-int launch_convert(void (*kernel)(ConvertArgs), ConvertArgs& a, int spare, cudaStream_t stream, int* launches) {
+int launch_convert(void (*kernel)(ConvertArgs), ConvertArgs& a, int flight, int spare, cudaStream_t stream, int* launches) {
   // bringing rows back that start above a boundary takes what a piece lacks of its last block
   a.pieces = static_cast<int>((a.width - 1LL + spare) / kPiece + 1);
   // as many CTAs as there is work for: a fixed number would leave the last ones of a wave alone
-  constexpr long long kPerCta = kConvertThreads / 32 * kFlight;
-  const long long ctas = a.rows > LLONG_MAX / a.pieces ? LLONG_MAX : (a.rows * a.pieces - 1) / kPerCta + 1;
+  const long long per_cta = kConvertThreads / 32 * flight;
+  const long long ctas = a.rows > LLONG_MAX / a.pieces ? LLONG_MAX : (a.rows * a.pieces - 1) / per_cta + 1;
   const unsigned grid = static_cast<unsigned>(std::min<long long>(ctas, INT_MAX));
   if (launch_dependent(kernel, dim3(grid), dim3(kConvertThreads), 0, stream, a) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -391,7 +405,8 @@ extern "C" int gemm_f32_checkpoint(int type, long long rows, int width, const vo
   const int rc = launch_convert(type == GEMM_F32_TYPE_F32
                                     ? vec ? checkpoint_kernel<float, true> : checkpoint_kernel<float, false>
                                     : vec ? checkpoint_kernel<bf16, true> : checkpoint_kernel<bf16, false>,
-                                a, 0, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+                                a, type == GEMM_F32_TYPE_BF16 && vec ? keep_flight<bf16, true>() : keep_flight<float, true>(), 0,
+                                reinterpret_cast<cudaStream_t>(stream_handle), &launches);
   if (rc == GEMM_F32_OK) note_launches(launches, "checkpoint_kernel");
   return rc;
 }
@@ -413,7 +428,7 @@ extern "C" int gemm_f32_restore(int type, long long rows, int width, const unsig
   const bool vec = on_boundaries(out, ldo, es) && width * es % 16 == 0;
   const int rc = launch_convert(type == GEMM_F32_TYPE_F32 ? vec ? restore_kernel<float, true> : restore_kernel<float, false>
                                                           : vec ? restore_kernel<bf16, true> : restore_kernel<bf16, false>,
-                                a, vec ? 0 : 7, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+                                a, kRestoreFlight, vec ? 0 : 7, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
   if (rc == GEMM_F32_OK) note_launches(launches, "restore_kernel");
   return rc;
 }
@@ -453,7 +468,7 @@ int run_weight_grad(const WeightGrad& c, cudaStream_t stream, int* launches) {
   if (!scratch) return GEMM_F32_ESCRATCH;
   ConvertArgs x = {c.rows,      static_cast<int>(ldx), nullptr, scratch + at_x, ldx, const_cast<uint8_t*>(c.codes), c.ld_codes,
                    const_cast<uint8_t*>(c.exponents), c.ld_exponents,   0,       err};
-  int rc = launch_convert(restore_kernel<bf16, true>, x, 0, stream, launches);
+  int rc = launch_convert(restore_kernel<bf16, true>, x, kRestoreFlight, 0, stream, launches);
   if (rc != GEMM_F32_OK) return rc;
   const long long plane = lddy * c.rows;
   if (packed) {
