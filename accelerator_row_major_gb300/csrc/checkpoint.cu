@@ -68,10 +68,10 @@ struct Pieces {
   long long row, d_row;
   int piece, per_row, d_piece;
 
-  __device__ __forceinline__ Pieces(int per, int flight) : per_row(per) {
+  __device__ __forceinline__ Pieces(int per, int flight, unsigned cta, unsigned ctas) : per_row(per) {
     constexpr int kWarps = kConvertThreads / 32;
-    const long long first = (blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5)) * flight;
-    const long long skip = (gridDim.x * static_cast<long long>(kWarps) - 1) * flight;
+    const long long first = (cta * static_cast<long long>(kWarps) + (threadIdx.x >> 5)) * flight;
+    const long long skip = (ctas * static_cast<long long>(kWarps) - 1) * flight;
     row = first / per;
     piece = static_cast<int>(first - row * per);
     d_row = skip / per;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kConvertThreads, keep_flight<T, VEC>() == 2 ? 
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  for (Pieces at(a.pieces, kFlight); at.row < a.rows; at.next_grid()) {
+  for (Pieces at(a.pieces, kFlight, blockIdx.x, gridDim.x); at.row < a.rows; at.next_grid()) {
     // all pieces' loads first
     long long row[kFlight];
     int col[kFlight];                    // of the lane's first element
@@ -243,13 +243,11 @@ __global__ void __launch_bounds__(kConvertThreads, keep_flight<T, VEC>() == 2 ? 
 // elements of whole 16-byte blocks of the output, `above` elements before the
 // 8 of its codes, which it takes with those before (the lane's before).
 template <class T, bool VEC>
-__global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertArgs a) {
+__device__ __forceinline__ void restore_rows(const ConvertArgs& a, unsigned cta, unsigned ctas) {
   constexpr int kFlight = kRestoreFlight;
   constexpr int V = 16 / static_cast<int>(sizeof(T));
-  grid_launch_dependents();
-  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  for (Pieces at(a.pieces, kFlight); at.row < a.rows; at.next_grid()) {
+  for (Pieces at(a.pieces, kFlight, cta, ctas); at.row < a.rows; at.next_grid()) {
     long long row[kFlight];
     int col[kFlight];                    // of the lane's codes
     uint2 w[kFlight], before[kFlight];
@@ -322,6 +320,79 @@ __global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertA
   }
 }
 
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kConvertThreads) restore_kernel(const ConvertArgs a) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  restore_rows<T, VEC>(a, blockIdx.x, gridDim.x);
+}
+
+// ---------------------------------------------------------------- operands of the weight gradient
+// dy as the tensor cores read it: bfloat16 copied into rows on 16-byte
+// boundaries, or fp32 in three planes of bfloat16.  hi is the value truncated
+// (so that it never overflows), mid and lo round what is left to nearest; the
+// rest is below 2^-25 of the value.
+struct SplitArgs {
+  const void* src;
+  bf16* dst;
+  long long ld, ld_dst, plane, vectors;  // vectors of 8 in all rows of dst
+  int rows, cols, aligned;
+};
+
+template <class T>
+__device__ __forceinline__ void split_rows(const SplitArgs& m, unsigned cta, unsigned ctas, unsigned* err) {
+  const int per_row = static_cast<int>(m.ld_dst / 8);
+  for (long long i = cta * static_cast<long long>(kConvertThreads) + threadIdx.x; i < m.vectors;
+       i += ctas * static_cast<long long>(kConvertThreads)) {
+    const int row = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<long long>(row) * per_row) * 8;
+    const long long at = row * m.ld + c;
+    const T* const src = static_cast<const T*>(m.src) + at;
+    [[maybe_unused]] const size_t extent = stored_extent(m.rows, m.cols, m.ld);
+    float v[8];
+    if (m.aligned && c + 8 <= m.cols && GEMM_IN_EXTENT(at + 7, extent, err, kSiteBoundsRows)) {
+      Raw<T, 8> raw;
+      raw.load_once(src);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = raw.at(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = c + j < m.cols && GEMM_IN_EXTENT(at + j, extent, err, kSiteBoundsRows) ? to_f32(src[j]) : 0.0f;
+    }
+    bf16* const out = m.dst + row * m.ld_dst + c;
+    if constexpr (sizeof(T) == 2) {
+      store_vec<bf16, 8>(out, v);
+    } else {
+      float hi[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        hi[j] = __uint_as_float(__float_as_uint(v[j]) & 0xFFFF0000u);
+        v[j] -= hi[j];
+      }
+      store_vec<bf16, 8>(out, hi);
+#pragma unroll
+      for (int part = 1; part < 3; ++part) {
+        store_vec<bf16, 8>(out + part * m.plane, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+      }
+    }
+  }
+}
+
+// Both operands at once: the first `x_ctas` CTAs bring x back, the others
+// prepare dy (rows 4096, 1024 x 1024 fp32: the whole call 41 us, 44 with two
+// launches).
+template <class T>
+__global__ void __launch_bounds__(kConvertThreads) operands_kernel(const ConvertArgs x, const SplitArgs dy, unsigned x_ctas) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (blockIdx.x < x_ctas)
+    restore_rows<bf16, true>(x, blockIdx.x, x_ctas);
+  else
+    split_rows<T>(dy, blockIdx.x - x_ctas, gridDim.x - x_ctas, x.err);
+}
+
 // ---------------------------------------------------------------- host side
 constexpr int kMost = INT_MAX - 1024;    // tiles and pieces rounded up stay within an int
 
@@ -357,14 +428,19 @@ bool apart(const void* p, size_t bytes, const void* codes, long long ld_codes, c
          !ranges_overlap(p, bytes, exponents, static_cast<size_t>(rows) * ld_exponents);
 }
 
-int launch_convert(void (*kernel)(ConvertArgs), ConvertArgs& a, int flight, int spare, cudaStream_t stream, int* launches) {
-  // bringing rows back that start above a boundary takes what a piece lacks of its last block
+// Pieces of the rows, and as many CTAs as there is work for: a fixed number
+// would leave the last ones of a wave alone.  `spare`: columns that rows which
+// start above a boundary are taken to be longer by.
+unsigned plan_convert(ConvertArgs& a, int flight, int spare) {
   a.pieces = static_cast<int>((a.width - 1LL + spare) / kPiece + 1);
-  // as many CTAs as there is work for: a fixed number would leave the last ones of a wave alone
   const long long per_cta = kConvertThreads / 32 * flight;
   const long long ctas = a.rows > LLONG_MAX / a.pieces ? LLONG_MAX : (a.rows * a.pieces - 1) / per_cta + 1;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(ctas, INT_MAX));
-  if (launch_dependent(kernel, dim3(grid), dim3(kConvertThreads), 0, stream, a) != cudaSuccess) {
+  return static_cast<unsigned>(std::min<long long>(ctas, INT_MAX));
+}
+
+template <class Kernel, class... Args>
+int launch(Kernel kernel, unsigned grid, cudaStream_t stream, int* launches, const Args&... args) {
+  if (launch_dependent(kernel, dim3(grid), dim3(kConvertThreads), 0, stream, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return GEMM_F32_ELAUNCH;
   }
@@ -402,11 +478,11 @@ extern "C" int gemm_f32_checkpoint(int type, long long rows, int width, const vo
   ConvertArgs a = {rows, width, x, nullptr, ldx, codes, ld_codes, exponents, ld_exponents, 0, nullptr};
   if (!current_device(&device, &num_sms, &a.err)) return GEMM_F32_EDEVICE;
   const bool vec = on_boundaries(x, ldx, es) && width * es % 16 == 0;
-  const int rc = launch_convert(type == GEMM_F32_TYPE_F32
-                                    ? vec ? checkpoint_kernel<float, true> : checkpoint_kernel<float, false>
-                                    : vec ? checkpoint_kernel<bf16, true> : checkpoint_kernel<bf16, false>,
-                                a, type == GEMM_F32_TYPE_BF16 && vec ? keep_flight<bf16, true>() : keep_flight<float, true>(), 0,
-                                reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+  const int flight = type == GEMM_F32_TYPE_BF16 && vec ? keep_flight<bf16, true>() : keep_flight<float, true>();
+  const unsigned grid = plan_convert(a, flight, 0);
+  const auto kernel = type == GEMM_F32_TYPE_F32 ? vec ? checkpoint_kernel<float, true> : checkpoint_kernel<float, false>
+                                                : vec ? checkpoint_kernel<bf16, true> : checkpoint_kernel<bf16, false>;
+  const int rc = launch(kernel, grid, reinterpret_cast<cudaStream_t>(stream_handle), &launches, a);
   if (rc == GEMM_F32_OK) note_launches(launches, "checkpoint_kernel");
   return rc;
 }
@@ -426,9 +502,10 @@ extern "C" int gemm_f32_restore(int type, long long rows, int width, const unsig
                    ld_exponents, 0,     nullptr};
   if (!current_device(&device, &num_sms, &a.err)) return GEMM_F32_EDEVICE;
   const bool vec = on_boundaries(out, ldo, es) && width * es % 16 == 0;
-  const int rc = launch_convert(type == GEMM_F32_TYPE_F32 ? vec ? restore_kernel<float, true> : restore_kernel<float, false>
-                                                          : vec ? restore_kernel<bf16, true> : restore_kernel<bf16, false>,
-                                a, kRestoreFlight, vec ? 0 : 7, reinterpret_cast<cudaStream_t>(stream_handle), &launches);
+  const unsigned grid = plan_convert(a, kRestoreFlight, vec ? 0 : 7);
+  const auto kernel = type == GEMM_F32_TYPE_F32 ? vec ? restore_kernel<float, true> : restore_kernel<float, false>
+                                                : vec ? restore_kernel<bf16, true> : restore_kernel<bf16, false>;
+  const int rc = launch(kernel, grid, reinterpret_cast<cudaStream_t>(stream_handle), &launches, a);
   if (rc == GEMM_F32_OK) note_launches(launches, "restore_kernel");
   return rc;
 }
@@ -468,13 +545,21 @@ int run_weight_grad(const WeightGrad& c, cudaStream_t stream, int* launches) {
   if (!scratch) return GEMM_F32_ESCRATCH;
   ConvertArgs x = {c.rows,      static_cast<int>(ldx), nullptr, scratch + at_x, ldx, const_cast<uint8_t*>(c.codes), c.ld_codes,
                    const_cast<uint8_t*>(c.exponents), c.ld_exponents,   0,       err};
-  int rc = launch_convert(restore_kernel<bf16, true>, x, kRestoreFlight, 0, stream, launches);
-  if (rc != GEMM_F32_OK) return rc;
+  const unsigned x_ctas = plan_convert(x, kRestoreFlight, 0);
   const long long plane = lddy * c.rows;
+  int rc;
   if (packed) {
-    rc = pack_operand_half(c.f32, c.dy, c.lddy, c.rows, c.out, scratch + at_dy, lddy, plane, num_sms, err, stream, launches);
-    if (rc != GEMM_F32_OK) return rc;
+    const SplitArgs dy = {c.dy, reinterpret_cast<bf16*>(scratch + at_dy), c.lddy, lddy, plane, plane / 8, c.rows, c.out,
+                          on_boundaries(c.dy, c.lddy, c.f32 ? 4 : 2)};
+    const long long all = (dy.vectors - 1) / kConvertThreads + 1;
+    const unsigned dy_ctas = static_cast<unsigned>(std::min<long long>(all, 16LL * num_sms));
+    const unsigned first = std::min(x_ctas, 1u << 30);   // the sum stays within a grid
+    rc = c.f32 ? launch(operands_kernel<float>, first + dy_ctas, stream, launches, x, dy, first)
+               : launch(operands_kernel<bf16>, first + dy_ctas, stream, launches, x, dy, first);
+  } else {
+    rc = launch(restore_kernel<bf16, true>, x_ctas, stream, launches, x);
   }
+  if (rc != GEMM_F32_OK) return rc;
   HalfGemm g = {};
   g.M = c.out;
   g.N = c.width;

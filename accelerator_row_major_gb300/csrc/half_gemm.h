@@ -61,12 +61,6 @@ size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms, bool sum_f
 // Returns 0 or a negative GEMM_F32_E* code; counts its kernels in *launches.
 int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
 
-// Stores a matrix as an operand that TMA can read: bfloat16 (copied), or fp32
-// in three parts of bfloat16 `plane` elements apart, in rows of ld_dst
-// elements (a multiple of 8), zero from column `cols` on.
-int pack_operand_half(bool f32, const void* src, long long ld, int rows, int cols, void* dst, long long ld_dst,
-                      long long plane, int num_sms, unsigned* err, cudaStream_t stream, int* launches);
-
 // The same two products for few rows (at most kFewRows), where reading w is
 // what takes the time (few_gemm.cu).  w is read as it is stored, fp32
 // included (f32: its three parts are made on the way to the tensor cores).

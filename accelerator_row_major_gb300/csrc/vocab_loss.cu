@@ -764,18 +764,6 @@ int checked(Call& c, long long rows, gemm_f32_stream_t stream_handle) {
 }  // namespace
 }  // namespace gemm_f32_impl
 
-namespace gemm_f32_impl {
-
-int pack_operand_half(bool f32, const void* src, long long ld, int rows, int cols, void* dst, long long ld_dst,
-                      long long plane, int num_sms, unsigned* err, cudaStream_t stream, int* launches) {
-  const Packing m = {src, dst, ld, ld_dst, plane, rows, cols, on_boundaries(src, ld, f32 ? 4 : 2), 1, 0, 0, 0};
-  const dim3 grid(static_cast<unsigned>(std::min<long long>((m.vecs() + 255) / 256, 16LL * num_sms)));
-  return f32 ? launch(loss_pack_kernel<float, 3, bf16>, grid, 256, stream, launches, m, Packing{}, err)
-             : launch(loss_pack_kernel<bf16, 1, bf16>, grid, 256, stream, launches, m, Packing{}, err);
-}
-
-}  // namespace gemm_f32_impl
-
 using namespace gemm_f32_impl;
 
 extern "C" int gemm_f32_vocab_loss(int type, long long rows, int width, int vocab, const void* x,
