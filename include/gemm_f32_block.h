@@ -79,10 +79,10 @@ typedef struct gemm_f32_rows {
  * residual or a gate matrix itself, with the same stride; they overlap
  * nothing else.  rows == 0 does nothing.
  * Returns 0, GEMM_F32_EINVAL (an unknown type or norm, width < 1 or above
- * 2^31 - 1025, rows < 0, a stride below width, eps negative, or eps or a
- * scale not finite, a null or misaligned pointer, a bias with GEMM_F32_NORM_RMS, post_weight or post_bias
- * without `post`, outputs that overlap), GEMM_F32_EDEVICE or
- * GEMM_F32_ELAUNCH. */
+ * 2^31 - 1025, rows < 0, a stride below width, eps negative, eps or a scale
+ * not finite, a null or misaligned pointer, a bias with GEMM_F32_NORM_RMS,
+ * post_weight or post_bias without `post`, outputs that overlap),
+ * GEMM_F32_EDEVICE or GEMM_F32_ELAUNCH. */
 int gemm_f32_block_norm(const gemm_f32_block_t* block, const void* branch, long long ld_branch,
                         const void* residual, long long ld_residual, void* y, long long ldy, void* h,
                         long long ldh, float* stats, gemm_f32_stream_t stream);
