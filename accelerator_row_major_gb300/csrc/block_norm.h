@@ -51,6 +51,7 @@ struct VectorArgs {
   const void* p[kVectors];               // null where `there`: the default
   int slot[kVectors];                    // of the vectors in shared memory, -1: not there
   int f32;
+  int joined;                            // the post weight's place holds it times the gate
 };
 
 enum { kNoGate, kChannelGate, kElementGate };

@@ -64,6 +64,8 @@ __device__ __forceinline__ void fill_vectors(float* columns, const VectorArgs& a
         f[v][j] = c >= ring.width ? 0.0f
                   : a.p[v]        ? vector_value<T>(a.p[v], a.f32, ring.col0 + c)
                                   : (v == kWeight || v == kPostWeight ? 1.0f : 0.0f);
+        if (v == kPostWeight && a.joined && a.p[kGateVector] && c < ring.width)
+          f[v][j] *= vector_value<T>(a.p[kGateVector], a.f32, ring.col0 + c);
       }
     }
 #pragma unroll
@@ -221,7 +223,13 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
 // ---------------------------------------------------------------- gradient
 // LAYER: around the means; POST: the branch was normed; CHANNEL: a gate per
 // channel (a gate per element is the launch's choice).  What a form does not
-// have costs no registers.
+// have costs no registers.  With POST and CHANNEL the sums over the rows are
+// of d and d hat_b: the gate, the same for all rows, and the weights come to
+// them at the end (dpost_weight = gate sum d hat_b, dpost_bias = gate sum d,
+// dgate = post_weight sum d hat_b + post_bias sum d): two sums for three and
+// one vector, gate post_weight, for three on the way, which leaves room for two
+// rows at a time (layer norms, 8192 columns: 4096 rows of bfloat16 171 -> 120
+// us, 8192 of fp32 334 -> 280).
 template <class T, int NE, int ROWS, bool VEC, bool LAYER, bool POST, bool CHANNEL>
 __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
@@ -254,6 +262,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
   const float inv = 1.0f / static_cast<float>(plan.width);
   const auto vector = [&](int v) { return columns + a.vectors.slot[v] * Part::slots(plan.lanes); };
   RowSums sums = {shared, plan, a.err, group, t, rank};
+  constexpr bool kJoined = POST && CHANNEL;
   Pair total[kSums][NP];
 #pragma unroll
   for (int k = 0; k < kSums; ++k)
@@ -309,6 +318,25 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
       f([&](int r, int v, Pair(&x)[CP]) { mine.load_saved(from[r], exponents[r], v, x); });
     else
       f([&](int r, int v, Pair(&x)[CP]) { mine.load(from[r], v, x); });
+  };
+
+  // Both norms take sums over the row, one after the other.  With a gate per
+  // element, the second ones go with the next row's first: one exchange a row,
+  // of the same sums, what the end of a row needs in registers meanwhile
+  // (4096 x 8192 bfloat16 163 -> 143 us).  Where two rows fit instead, they are
+  // as good, and a wide fp32 row has no room for both (8192 x 8192, a gate per
+  // channel, 302 with it, 280 without).
+  constexpr bool kLate = LAYER && POST && !CHANNEL;
+  constexpr int kLatePairs = kLate ? NP : 1;
+  Pair late_e[kLatePairs], late_hat[kLatePairs], late_se = 0, late_seh = 0;
+  float late_rstd = 0.0f;
+  long long late_row = -1;               // none
+  // dbranch of the row r: e through the branch's norm
+  const auto end_row = [&](Pair* e, const Pair* hat_b, float rstd_b, float c1, float c2) {
+    const float by = rstd_b * a.beta;
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+      e[j] = fma2(e[j], both(by), LAYER ? fma2(hat_b[j], both(c2 * by), both(c1 * by)) : mul2(hat_b[j], both(c2 * by)));
   };
 
   // a norm's hat
@@ -372,7 +400,25 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
       }
     });
     float c1[ROWS], c2[ROWS];
-    means(sg, sgh, c1, c2);
+    if constexpr (kLate) {
+      constexpr int N = LAYER ? 2 : 1;
+      float v[2 * N];
+      v[0] = sum_of(sgh[0]);
+      v[N] = sum_of(late_seh);
+      if (LAYER) {
+        v[N - 1] = sum_of(sg[0]);
+        v[2 * N - 1] = sum_of(late_se);
+      }
+      sums.add<2 * N>(v);
+      c1[0] = LAYER ? -v[N - 1] * inv : 0.0f;
+      c2[0] = -v[0] * inv;
+      if (late_row >= 0) {
+        end_row(late_e, late_hat, late_rstd, LAYER ? -v[2 * N - 1] * inv : 0.0f, -v[N] * inv);
+        store(a.dbranch, late_row, late_e, 1.0f);
+      }
+    } else {
+      means(sg, sgh, c1, c2);
+    }
     // d = dh + rstd (g + c1 + hat c2), in place of g
     Pair(&d)[ROWS][NP] = g;
 #pragma unroll
@@ -406,13 +452,14 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
 #pragma unroll
         for (int v = 0; v < NC; ++v) mine.drop(v, d[r] + v * CP);
     }
-    // e = d gate, without beta: what is linear in it gets that at its end
+    // e = d gate (joined to the post weight where that is a vector), without
+    // beta: what is linear in it gets that at its end
     Pair(&hat_b)[ROWS][NP] = hat;        // the branch's in place of h's
     Pair se[ROWS], seh[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) se[r] = seh[r] = 0;
     const auto through_gate = [&](auto load_branch, auto element) {
-      constexpr bool kElement = decltype(element)::value, kGated = CHANNEL || kElement;
+      constexpr bool kElement = decltype(element)::value, kGated = (CHANNEL && !kJoined) || kElement;
       const bool bias = POST && LAYER && kGated && a.vectors.slot[kPostBias] >= 0;
       const uint8_t* gate[ROWS];
       T* to[ROWS];
@@ -433,7 +480,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
             nothing(post_bias);
           }
         }
-        if (CHANNEL) mine.columns(vector(kGateVector), v, channel);
+        if (CHANNEL && !kJoined) mine.columns(vector(kGateVector), v, channel);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
           Pair x[CP];
@@ -489,17 +536,32 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
         through_gate(load_branch, std::false_type{});
     });
     reader.release();
-    if (POST) means(se, seh, c1, c2);
+    if constexpr (kLate) {
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      if (POST) {
-        const float by = rstd_b[r] * a.beta;
-#pragma unroll
-        for (int j = 0; j < NP; ++j)
-          d[r][j] = fma2(d[r][j], both(by),
-                         LAYER ? fma2(hat_b[r][j], both(c2[r] * by), both(c1[r] * by)) : mul2(hat_b[r][j], both(c2[r] * by)));
+      for (int j = 0; j < NP; ++j) {
+        late_e[j] = d[0][j];
+        late_hat[j] = hat_b[0][j];
       }
-      store(a.dbranch, row + r, d[r], POST ? 1.0f : a.beta);
+      late_se = se[0];
+      late_seh = seh[0];
+      late_rstd = rstd_b[0];
+      late_row = row;
+    } else {
+      if (POST) means(se, seh, c1, c2);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        if (POST) end_row(d[r], hat_b[r], rstd_b[r], c1[r], c2[r]);
+        store(a.dbranch, row + r, d[r], POST ? 1.0f : a.beta);
+      }
+    }
+  }
+  if constexpr (kLate) {
+    if (late_row >= 0) {                 // the group's, on every CTA of the cluster
+      Pair se[1] = {late_se}, seh[1] = {late_seh};
+      float c1[1], c2[1];
+      means(se, seh, c1, c2);
+      end_row(late_e, late_hat, late_rstd, c1[0], c2[0]);
+      store(a.dbranch, late_row, late_e, 1.0f);
     }
   }
   if (plan.ctas > 1) cluster_sync();     // no CTA leaves while another may write to it
@@ -518,6 +580,30 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
 #pragma unroll
       for (int q = 0; q < NE / 4; ++q) {
         const Pair by = both(k == kSumWeight || k == kSumBias ? 1.0f : a.beta);
+        if (kJoined && (k == kSumGate || k == kSumPostWeight || k == kSumPostBias)) {
+          // sums of d and d hat_b become those of the vectors
+          const int base = mine.slot(q);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const auto pair = [&](int vector, float otherwise) {
+              float f[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int c = Part::column_of_slot(base + 2 * j + i);
+                f[i] = c < ring.width && a.vectors.p[vector] ? vector_value<T>(a.vectors.p[vector], a.vectors.f32, ring.col0 + c)
+                                                             : otherwise;
+              }
+              return pair_of(f[0], f[1]);
+            };
+            if (k == kSumGate) {
+              const Pair along = mul2(pair(kPostWeight, 1.0f), total[kSumPostWeight][2 * q + j]);
+              total[kSumGate][2 * q + j] =
+                  LAYER ? fma2(pair(kPostBias, 0.0f), total[kSumPostBias][2 * q + j], along) : along;
+            } else {
+              total[k][2 * q + j] = mul2(pair(kGateVector, 1.0f), total[k][2 * q + j]);
+            }
+          }
+        }
         float4 f;
         unpair(mul2(total[k][2 * q], by), f.x, f.y);
         unpair(mul2(total[k][2 * q + 1], by), f.z, f.w);
@@ -975,9 +1061,10 @@ int gradient_form(const BlockGradArgs& a, const BlockLaunch& l, Layout<kGradInpu
 
 // What a thread has of many rows, besides the 8 elements of one: two rows of
 // them, or one row of 16, by the registers that the form's sums leave
-// (8192 x 4096 bfloat16, with a gate per channel 85 us against 119).
+// (8192 x 4096 bfloat16, with a gate per channel 85 us against 119; rms norms
+// on both ends 86 with 16, 91 with 8).
 constexpr Lane grad_lane(bool layer, bool post, bool channel) {
-  return layer && post ? Lane{8, 1} : post && !channel ? Lane{16, 1} : Lane{8, 2};
+  return channel || !post ? Lane{8, 2} : layer ? Lane{8, 1} : Lane{16, 1};
 }
 
 // f with the three choices as template arguments.
@@ -1000,11 +1087,16 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
   int rc = GEMM_F32_OK;
   *l.kernel = "block_columns_kernel";
   if (a.plan.rows > 0) {
-    rc = with_form(!a.rms, a.post, a.gate == kChannelGate, [&](auto layer, auto post, auto channel) -> int {
-      constexpr bool kLayer = decltype(layer)::value, kPost = decltype(post)::value, kChannel = decltype(channel)::value;
+    // two layer norms without a gate: the form with a gate of ones, whose sums leave room for two rows (4096 x 8192
+    // bfloat16 117 us against 130 with the form of any gate)
+    const bool channel = a.gate == kChannelGate || (!a.rms && a.post && a.gate == kNoGate);
+    rc = with_form(!a.rms, a.post, channel, [&](auto layer, auto post, auto by_channel) -> int {
+      constexpr bool kLayer = decltype(layer)::value, kPost = decltype(post)::value, kChannel = decltype(by_channel)::value;
       constexpr Lane kMore = grad_lane(kLayer, kPost, kChannel);
       const Lane lanes[2] = {{8, 1}, kMore};
-      Layout<kGradInputs> best = best_layout(a.plan, a.in, lanes, true, a.sums, l);
+      BlockLaunch rows = l;
+      if (kPost && kChannel) rows.vectors = 2;             // the weight, and the gate's joined to the post weight
+      Layout<kGradInputs> best = best_layout(a.plan, a.in, lanes, true, a.sums, rows);
       c.ctas = best.lane.ne ? best.grid / best.plan.ctas : static_cast<int>(std::min<long long>(a.plan.rows, 2LL * l.num_sms));
       if (a.sums) {
         a.partials = static_cast<float*>(acquire_scratch(
@@ -1017,6 +1109,11 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
         return launch_plain(block_norm_grad_wide_kernel<T>, dim3(c.ctas), kWideThreads, l.stream, a);
       }
       *l.kernel = "block_norm_grad_kernel";
+      if (kPost && kChannel) {
+        const int slots[kVectors] = {0, -1, 1, -1, -1};
+        std::copy(slots, slots + kVectors, a.vectors.slot);
+        a.vectors.joined = 1;
+      }
       a.plan = best.plan;
       std::copy(best.in, best.in + kGradInputs, a.in);
       const bool more = best.lane.ne != 8 || best.lane.rows != 1;

@@ -71,6 +71,37 @@ def test_rows_around_whole_turns(rows, post):
         b.both(g, b.inputs(rows, width, kind, "f32", "rms", "channel", post, rows))
 
 
+@pytest.mark.parametrize("rows", [1, 2, 151, 153, 305, 607, 1217])
+@pytest.mark.parametrize("gate", ["none", "channel", "element"])
+def test_rows_of_two_layer_norms(rows, gate):
+    """Sums of a row that go with the next one's, rows in pairs: a row more or less than whole turns, clusters."""
+    from tests import _block as b
+    g = lib()
+    for width, kind in ((512, "bf16"), (1001, "f32"), (4096, "bf16"), (8192, "f32"), (9000, "bf16")):
+        b.both(g, b.inputs(rows, width, kind, "f32", "layer", gate, True, rows, (1.25, 0.5)))
+
+
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+@pytest.mark.parametrize("rows,width,kind", [(1, 40, "f32"), (900, 1024, "bf16"), (700, 1001, "f32"), (500, 8192, "f32")])
+def test_vectors_with_zeros(rows, width, kind, norm):
+    """Columns whose gate or weight is 0: the gradients of either come from the sums all the same."""
+    from tests import _block as b
+    g = lib()
+    for gate in ("channel", "none"):
+        s = b.inputs(rows, width, kind, "f32", norm, gate, True, width, (1.0, -0.5))
+        if gate == "channel":
+            s["how"]["gate"][::3] = 0
+        s["how"]["post_weight"][1::4] = 0
+        s["weight"][2::5] = 0
+        if norm == "layer":
+            s["how"]["post_bias"] *= 8
+        _, grads = b.both(g, s)
+        if gate == "channel":
+            assert (grads["dpost_weight"][::3] == 0).all() and grads["dpost_weight"][1::3].abs().min() > 0
+            unweighted = grads["dgate"][1::4]          # the bias alone is left of the branch there
+            assert unweighted.abs().min() > 0 if norm == "layer" else (unweighted == 0).all()
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("width,ld,first", [(1000, 1003, 1), (1000, 1008, 8), (1000, 1008, 3), (5000, 5120, 0), (64, 65, 5),
                                             (9, 10, 1), (3, 3, 1), (1, 5, 2), (33000, 33001, 1), (140000, 140004, 3)])
@@ -130,6 +161,31 @@ def test_in_place(rows, width, kind):
         got = b.call_grad(g, c, c["h"], c["branch"], want["stats"], out=out)
         assert got["dresidual"] is out
         assert all(torch.equal(got[k], v) for k, v in grads.items() if v is not None)
+
+
+@pytest.mark.parametrize("rows,width,kind", [(700, 1024, "bf16"), (1500, 1001, "f32"), (300, 8192, "f32"), (20, 40000, "bf16")])
+def test_branch_gradient_in_place(rows, width, kind):
+    """dbranch over what it came from, by the C call: rows that are written behind the next one's sums included."""
+    import ctypes
+    from accelerator_row_major_gb300 import _binding, _block, _lm
+    import torch
+    from tests import _block as b
+    g = lib()
+    for gate in ("none", "channel", "element"):
+        s = b.inputs(rows, width, kind, "f32", "layer", gate, True, width, (1.25, 0.5))
+        fwd = b.call(g, s)
+        want = b.call_grad(g, s, fwd["h"], s["branch"], fwd["stats"])["dbranch"]
+        for name in ("dy", "dh", "h", "branch") + (("gate",) if gate == "element" else ()):
+            c = {k: v.clone() if torch.is_tensor(v) else v for k, v in dict(s, h=fwd["h"]).items()}
+            c["gate"] = None if gate == "none" else s["how"]["gate"].clone()
+            how, out = dict(c["how"], gate=c["gate"]), c[name]
+            block, _ = _block._block(c["dy"], _lm._matrix("dy", c["dy"]), how["kind"], 0.0, c["weight"], None, True,
+                                     how["post_weight"], how["post_bias"], how["gate"], how["residual_scale"], how["branch_scale"])
+            at = [ctypes.byref(_binding.Rows(c[k].data_ptr(), width)) for k in ("h", "branch")]
+            g.check(_binding.lib().gemm_f32_block_norm_grad(
+                ctypes.byref(block), c["dy"].data_ptr(), width, c["dh"].data_ptr(), width, *at, fwd["stats"].data_ptr(),
+                out.data_ptr(), width, None, 0, None, 0, None, None, None, None, torch.cuda.current_stream().cuda_stream))
+            assert torch.equal(out, want), (gate, name)
 
 
 def test_what_is_not_there():
