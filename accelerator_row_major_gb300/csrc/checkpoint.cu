@@ -536,11 +536,10 @@ int run_weight_grad(const WeightGrad& c, cudaStream_t stream, int* launches) {
   const long long ldx = (c.width + 7LL) / 8 * 8;
   const bool packed = c.f32 || !on_boundaries(c.dy, c.lddy, 2);
   const long long lddy = packed ? (c.out + 7LL) / 8 * 8 : c.lddy;
-  const bool sum_f32 = c.dw_f32 && !c.f32;
   Layout layout;
   const size_t at_x = layout.take(static_cast<size_t>(c.rows) * ldx * 2);
   const size_t at_dy = packed ? layout.take(static_cast<size_t>(c.rows) * lddy * 2 * parts) : 0;
-  const size_t at_partials = layout.take(half_gemm_scratch(c.out, c.width, c.rows, parts, num_sms, sum_f32));
+  const size_t at_partials = layout.take(half_gemm_scratch(c.out, c.width, c.rows, parts, num_sms, !c.f32));
   char* const scratch = static_cast<char*>(acquire_scratch(device, stream, layout.bytes));
   if (!scratch) return GEMM_F32_ESCRATCH;
   ConvertArgs x = {c.rows,      static_cast<int>(ldx), nullptr, scratch + at_x, ldx, const_cast<uint8_t*>(c.codes), c.ld_codes,
@@ -568,7 +567,7 @@ int run_weight_grad(const WeightGrad& c, cudaStream_t stream, int* launches) {
   g.a = {packed ? scratch + at_dy : c.dy, lddy, plane, true};
   g.b = {scratch + at_x, ldx, 0, true};
   g.b_whole = true;
-  g.sum_f32 = sum_f32;
+  g.summed = !c.f32;
   g.c = c.dw;
   g.ldc = c.lddw;
   g.c_f32 = c.dw_f32;

@@ -80,11 +80,11 @@ constexpr int kSplitRaster = 2;          // where all tiles are split
 constexpr int kMinSplitBlocks = 16;      // least K blocks per pair in the split tail
 constexpr int kMostTeam = 4;
 // K blocks that one accumulator sums before its sum goes on in registers:
-// 256 of K for fp32 operands, and 1024 for the logits of bfloat16 ones with
-// more than kWholeLogits of K (0: the whole of K).
+// 256 of K for fp32 operands, and 1024 for the logits of bfloat16 ones, and
+// their products that ask for it, where a pair has more of a tile than that
+// (0: all of it).
 constexpr int kSumF32 = 4;
-constexpr int kSumLogits = 16;
-constexpr int kWholeLogits = 1024;
+constexpr int kSumHalf = 16;
 constexpr int kLeftParts = 2;            // PARTS: the left operand alone comes in three
 
 // Epilogues
@@ -730,7 +730,7 @@ int blocks_of(int n, int per) { return (n - 1) / per + 1; }
 
 // Tiles, K units and the split of the last wave; returns the bytes of
 // partial tiles.
-size_t plan(Params& p, int M, int N, int K, int sum, int num_sms, bool split) {
+size_t plan_tiles(Params& p, int M, int N, int K, int sum, int num_sms, bool split) {
   p.M = M;
   p.N = N;
   p.tiles_m = blocks_of(M, kTile);
@@ -754,6 +754,21 @@ size_t plan(Params& p, int M, int N, int K, int sum, int num_sms, bool split) {
   p.dp_tiles = bytes ? p.dp_tiles * p.team : static_cast<int>(tiles);
   if (p.dp_tiles == 0) p.raster = kSplitRaster;
   return bytes;
+}
+
+// The same, and the K blocks that one accumulator sums.
+enum Product { kLogitsOf, kStored, kSummed };
+size_t plan(Params& p, int M, int N, int K, int parts, Product product, int num_sms, int* sum) {
+  const bool split = product != kLogitsOf;
+  *sum = parts == 3 ? kSumF32 : 0;
+  const size_t bytes = plan_tiles(p, M, N, K, *sum, num_sms, split);
+  if (parts == 3 || product == kStored) return bytes;
+  // the most that a pair has of one tile: in units of 1024 of K the work splits less finely (2048 x 1024 x 1024 bfloat16
+  // 22.3 us against 21.4 with as little as that of a tile anyway, 65536 x 256 x 256 52 against 35)
+  const long long most = p.dp_tiles > 0 || p.sk_ctas == 0 ? p.k_blocks : (p.sk_work - 1) / p.sk_ctas + 1;
+  if (most <= kSumHalf) return bytes;
+  *sum = kSumHalf;
+  return plan_tiles(p, M, N, K, *sum, num_sms, split);
 }
 
 // 2-D map of what the epilogue writes (rows on 16-byte boundaries): boxes of
@@ -812,19 +827,12 @@ int launch_one(const HalfGemm& g, const Params& p, const Maps& m, int grid, cuda
   return GEMM_F32_OK;
 }
 
-int sum_blocks(bool logits, int parts, int K, bool sum_f32) {
-  if (parts == 3) return kSumF32;
-  if (sum_f32) return kSumLogits;
-  return logits && K > kWholeLogits ? kSumLogits : 0;
-}
-
 // The forms the vocabulary loss and the weight gradient need: logits of
 // K-major operands, and products with an MN-major right operand.
-int launch_form(const HalfGemm& g, const Params& p, const Maps& m, int grid, cudaStream_t stream) {
-  const int sum = sum_blocks(!g.c, g.parts, g.K, g.sum_f32);
+int launch_form(const HalfGemm& g, const Params& p, const Maps& m, int sum, int grid, cudaStream_t stream) {
   if (!g.c) {
     if (g.parts == 3) return launch_one<false, false, 3, kSumF32, kLogits>(g, p, m, grid, stream);
-    if (sum) return launch_one<false, false, 1, kSumLogits, kLogits>(g, p, m, grid, stream);
+    if (sum) return launch_one<false, false, 1, kSumHalf, kLogits>(g, p, m, grid, stream);
     return launch_one<false, false, 1, 0, kLogits>(g, p, m, grid, stream);
   }
   if (g.parts == 3) {
@@ -835,18 +843,21 @@ int launch_form(const HalfGemm& g, const Params& p, const Maps& m, int grid, cud
   }
   if (g.c_f32) {
     if (!g.a.mn_major) return GEMM_F32_EINVAL;
-    return sum ? launch_one<true, true, 1, kSumLogits, kStoreF32>(g, p, m, grid, stream)
+    return sum ? launch_one<true, true, 1, kSumHalf, kStoreF32>(g, p, m, grid, stream)
                : launch_one<true, true, 1, 0, kStoreF32>(g, p, m, grid, stream);
   }
+  if (sum && !g.a.mn_major) return GEMM_F32_EINVAL;
+  if (sum) return launch_one<true, true, 1, kSumHalf, kStoreBf16>(g, p, m, grid, stream);
   return g.a.mn_major ? launch_one<true, true, 1, 0, kStoreBf16>(g, p, m, grid, stream)
                       : launch_one<false, true, 1, 0, kStoreBf16>(g, p, m, grid, stream);
 }
 
 }  // namespace
 
-size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms, bool sum_f32) {
+size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms, bool summed) {
   Params p = {};
-  return plan(p, M, N, K, sum_blocks(false, parts, K, sum_f32), num_sms, true);
+  int sum = 0;
+  return plan(p, M, N, K, parts, summed ? kSummed : kStored, num_sms, &sum);
 }
 
 int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
@@ -854,7 +865,8 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
   if (pairs < 1) return GEMM_F32_EDEVICE;
   if (g.c ? !g.b.mn_major : g.a.mn_major || g.b.mn_major) return GEMM_F32_EINVAL;
   Params p = {};
-  plan(p, g.M, g.N, g.K, sum_blocks(!g.c, g.parts, g.K, g.sum_f32), g.num_sms, g.c != nullptr);
+  int sum = 0;
+  plan(p, g.M, g.N, g.K, g.parts, !g.c ? kLogitsOf : g.summed ? kSummed : kStored, g.num_sms, &sum);
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x7fffffffLL) return GEMM_F32_EINVAL;
   p.partials = g.partials;
@@ -893,7 +905,7 @@ int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches) {
     p.c_tma = 1;
   }
   const int units = p.sk_ctas > 0 ? pairs : static_cast<int>(std::min<long long>(tiles, pairs));
-  const int rc = launch_form(g, p, m, 2 * units, stream);
+  const int rc = launch_form(g, p, m, sum, 2 * units, stream);
   if (rc != GEMM_F32_OK) return rc;
   ++*launches;
   if (p.sk_ctas > 0) {

@@ -29,8 +29,8 @@ struct HalfGemm {
   int parts;                    // 1, or 3 (fp32 operands split into three parts)
   HalfOperand a, b;
   bool b_whole = false;         // of parts 3: b is one part, bfloat16 as it is
-  bool sum_f32 = false;         // fp32 C of one part: 1024 of K at a time are summed on the tensor cores,
-                                // these sums in registers, rounded to nearest
+  bool summed = false;          // of a C of one part: at most 1024 of K at a time are summed on the tensor
+                                // cores, these sums in registers, rounded to nearest (a and b MN-major)
   // -- a stored product: C = *scale * D (+ add)
   void* c = nullptr;
   long long ldc = 0;
@@ -56,7 +56,7 @@ struct HalfGemm {
 
 // Bytes of partial tiles that the stored product of this shape needs (0 when
 // its last wave is not split along K).
-size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms, bool sum_f32 = false);
+size_t half_gemm_scratch(int M, int N, int K, int parts, int num_sms, bool summed = false);
 
 // Returns 0 or a negative GEMM_F32_E* code; counts its kernels in *launches.
 int launch_half_gemm(const HalfGemm& g, cudaStream_t stream, int* launches);
