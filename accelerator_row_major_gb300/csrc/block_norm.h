@@ -9,15 +9,24 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "../../include/gemm_f32_block.h"
+
 namespace gemm_f32_impl {
 
 constexpr int kRowWarps = 16;            // that compute, at most
 constexpr int kProducers = 4;            // warps that fill the ring, at most
+constexpr int kProducerThreads = 32 * kProducers;
 constexpr int kMostCtas = 8;             // of a cluster
 constexpr int kStats = 4;                // per row: mean and rstd of h, of the branch
 constexpr int kMostChunk = 8;            // rows of a stage, where all rows lie one behind the other
 constexpr int kMostLoose = 4;            // and where they do not
 constexpr int kSliceUnit = 512;          // columns: their exponents fill 16 bytes
+
+// Bytes of `cols` columns of a matrix whose elements take `size` (0: exponents).
+__host__ __device__ inline uint32_t source_bytes(int size, int cols) {
+  return size ? static_cast<uint32_t>(size) * cols
+              : static_cast<uint32_t>(cols + GEMM_F32_SAVED_BLOCK - 1) / GEMM_F32_SAVED_BLOCK;
+}
 
 // One matrix that a row is read from.  size: bytes per element, or 0 for the
 // exponents of 8-bit rows (a byte per 32 columns).
@@ -40,6 +49,8 @@ struct RowPlan {
   int producers;                         // 4, 2 or 1, a divisor of stages
   uint32_t stage_bytes;
   uint32_t ring_at;                      // in dynamic shared memory, behind the weights
+  uint32_t bars_at;                      // the ring's barriers: behind it and behind the groups' sums that take its place,
+                                         // since producers may still be at their last waits then
   uint32_t stats_at;                     // of the rows' statistics within a stage; 0: they do not come this way
   long long rows;
 };

@@ -36,10 +36,6 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-__host__ __device__ __forceinline__ uint32_t source_bytes(int size, int cols) {
-  return size ? static_cast<uint32_t>(size) * cols : static_cast<uint32_t>(cols + kSavedBlock - 1) / kSavedBlock;
-}
-
 // ---------------------------------------------------------------- ring
 // The first byte of a row's (or slice's) part of a matrix.
 __device__ __forceinline__ uintptr_t first_byte(const RowSource& m, long long row, int col0) {
@@ -55,7 +51,7 @@ struct RingPlace {
 
   __device__ __forceinline__ RingPlace(const RowPlan& p, uint8_t* smem, int rank) {
     data = smem + p.ring_at;
-    full = smem_addr(data) + static_cast<uint32_t>(p.stages) * p.stage_bytes;
+    full = smem_addr(smem) + p.bars_at;
     empty = full + 8u * p.stages;
     first = static_cast<int>(blockIdx.x) / p.ctas;
     step = static_cast<int>(gridDim.x) / p.ctas;
