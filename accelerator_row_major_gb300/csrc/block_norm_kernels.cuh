@@ -338,9 +338,11 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
       e[j] = fma2(e[j], both(by), LAYER ? fma2(hat_b[j], both(c2 * by), both(c1 * by)) : mul2(hat_b[j], both(c2 * by)));
   };
 
-  // a norm's hat
-  const auto normed = [](Pair x, float mean, float rstd) {
-    return LAYER ? fma2(x, both(rstd), both(-mean * rstd)) : mul2(x, both(rstd));
+  // A norm's hat, of pair k of chunk v, from what is left of x without the mean:
+  // x rstd - mean rstd would be off by a rounding of mean rstd, however small hat
+  // is, and leave the range where hat does not.  0 outside the row.
+  const auto normed = [&](int v, int k, Pair x, float mean, float rstd) {
+    return mul2(LAYER ? add2(x, mine.within(v, k, -mean)) : x, both(rstd));
   };
   const auto nothing = [](Pair(&x)[CP]) {
 #pragma unroll
@@ -362,7 +364,6 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
       mean_b[r] = there(r) ? stats.z : 0.0f;
       rstd_b[r] = there(r) ? stats.w : 0.0f;
     }
-    // hat = h rstd - mean rstd in one operation; finite wherever h and rstd are
     Pair hat[ROWS][NP], g[ROWS][NP], sg[ROWS], sgh[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) sg[r] = sgh[r] = 0;
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
 #pragma unroll
           for (int k = 0; k < CP; ++k) {
             const int j = v * CP + k;
-            hat[r][j] = normed(x[k], mean[r], rstd[r]);
+            hat[r][j] = normed(v, k, x[k], mean[r], rstd[r]);
             total[kSumWeight][j] = fma2(y[k], hat[r][j], total[kSumWeight][j]);
             if (LAYER) total[kSumBias][j] = add2(total[kSumBias][j], y[k]);
             g[r][j] = mul2(y[k], w[k]);
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
             nothing(x);
           if (POST) {
 #pragma unroll
-            for (int k = 0; k < CP; ++k) x[k] = hat_b[r][v * CP + k] = normed(x[k], mean_b[r], rstd_b[r]);
+            for (int k = 0; k < CP; ++k) x[k] = hat_b[r][v * CP + k] = normed(v, k, x[k], mean_b[r], rstd_b[r]);
           }
           if (kGated) {
             Pair p[CP], by[CP];

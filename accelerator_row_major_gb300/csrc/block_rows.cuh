@@ -271,6 +271,13 @@ struct RowPart {
   __device__ __forceinline__ bool in(int i) const { return offset(i) < left; }
   __device__ __forceinline__ bool full() const { return in(NE - 1); }
 
+  // x for pair k of chunk v, 0 for what lies outside the row.
+  __device__ __forceinline__ Pair within(int v, int k, float x) const {
+    const int i = VEC ? v * V : 2 * (v * CP + k);
+    const float a = in(i) ? x : 0.0f;
+    return pair_of(a, VEC ? a : in(i + 1) ? x : 0.0f);
+  }
+
   // Elements of the row whose first column is at `row`; 0 for what lies outside it.
   __device__ __forceinline__ void load(const uint8_t* row, int v, Chunk& x) const {
     const T* const p = reinterpret_cast<const T*>(row) + first;
