@@ -40,7 +40,11 @@ bool plan_rows(RowPlan& plan, RowSource* in, int n, int vectors, int ctas, Lane 
   if (lane.rows > 1 && plan.rows < units * lane.rows) return false;
   // copies of a forward turn that start at multiples of 32 KB all over the GPU meet on the same channels: 16 rows of
   // 1024 in bfloat16 101 us (65536 of them), 12 rows 89; 8 of 2048 101, 6 90
-  if (!stats && plan.groups >= 8 && source_bytes(in[0].size, slice) * plan.groups % 32768 == 0) plan.groups -= plan.groups / 4;
+  const uint32_t turn_bytes = source_bytes(in[0].size, slice) * plan.groups;
+  if (!stats && plan.groups >= 8 && turn_bytes % 32768 == 0) plan.groups -= plan.groups / 4;
+  // the same of a gradient's turns of 16 elements a thread at 16 KB: 8 rows of 1024 in bfloat16 150 us (65536 of them),
+  // 7 rows 130; 16 of 512 77 (as many of them), 15 74; with 8 elements a thread 181 against 190 for 8 rows of 512 in fp32
+  if (stats && ne == 16 && plan.groups >= 8 && turn_bytes % 16384 == 0) --plan.groups;
   // a stage of `rows` rows
   const auto stage_of = [&](int rows) {
     size_t stage = 0;
