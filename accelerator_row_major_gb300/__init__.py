@@ -27,7 +27,7 @@ gate, activations kept in 8 bits, and the gradients computed from them:
 from ._binding import (FLAG_CTA_PAIR, FLAG_FORCE_STAGED, FLAG_SINGLE_CTA, FLAG_TILE64, FLAG_TILE128, FLAG_TILE256,  # noqa: F401
                        FLAG_NO_SPLIT_K, FLAG_ONE_TILE_PER_CTA, FLAG_TEST_DROP_COPY, GEMM_F32_EDEVICE, GEMM_F32_EINVAL,
                        GEMM_F32_ELAUNCH, GEMM_F32_ESCRATCH, GEMM_F32_ETARGET, GEMM_F32_ETIMEOUT, GEMM_F32_OK, LIB_PATH, MODE_FFMA,
-                       MODE_TC1X, MODE_TC3X, MODES, GemmError, check, declared_symbols,
+                       MODE_TC1X, MODE_TC3X, MODES, MOST_INT, GemmError, check, declared_symbols,
                        elsewhere as _elsewhere,
                        gemm_f32, gemm_f32_ex, gemm_f32_general, gemm_f32_host, gemm_f32_ladder, gemm_f32_last_kernel, gemm_f32_last_launches,
                        gemm_f32_noalloc, LADDER_STEPS,
@@ -62,6 +62,8 @@ def matmul(A, B, out=None, mode="tc3x", flags: int = 0, stream=None):
 
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[0]:
         raise ValueError("shapes %s and %s do not chain" % (tuple(A.shape), tuple(B.shape)))
+    if max(*A.shape, *B.shape) > MOST_INT:
+        raise ValueError("A and B must have at most %d rows and columns" % MOST_INT)
     for name, t in (("A", A), ("B", B)):
         if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError("%s must be a contiguous float32 CUDA tensor" % name)

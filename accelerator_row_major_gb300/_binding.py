@@ -37,6 +37,7 @@ TYPE_BF16 = 1
 SUM = 0
 MEAN = 1
 REDUCTIONS = {"sum": SUM, "mean": MEAN}
+MOST_INT = 2 ** 31 - 1             # ctypes would pass a larger one on without its upper bits
 NORMS = {"layer": 0, "rms": 1}
 
 FLAG_FORCE_STAGED = 0x1

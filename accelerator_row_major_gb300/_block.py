@@ -14,7 +14,7 @@ import typing
 import torch
 
 from . import _lm
-from ._binding import Block, NORMS, Rows, check, elsewhere
+from ._binding import Block, MOST_INT, NORMS, Rows, check, elsewhere
 from ._lm import _F32, _TYPES, _call, _like, _matrix, _vector, _weight_type
 
 BLOCK = 32                                            # columns that share an exponent
@@ -56,8 +56,8 @@ def _padded(width):
 def _saved(name, saved):
     """(type, device index, rows, width) of a checkpoint whose tensors are as checkpoint() makes them."""
     kind, width = _TYPES.get(saved.dtype), saved.width
-    if kind is None or type(width) is not int or width < 1:
-        raise ValueError("%s must hold a float32 or bfloat16 matrix" % name)
+    if kind is None or type(width) is not int or not 1 <= width <= MOST_INT:
+        raise ValueError("%s must hold a float32 or bfloat16 matrix of at most %d columns" % (name, MOST_INT))
     codes, exponents = saved.codes, saved.exponents
     rows, dev = codes.shape[0], codes.get_device()
     ldc, lde = _padded(width)

@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import torch
 
-from ._binding import GEMM_F32_ESCRATCH, REDUCTIONS, TYPE_BF16, TYPE_F32, check, elsewhere, lib
+from ._binding import GEMM_F32_ESCRATCH, MOST_INT, REDUCTIONS, TYPE_BF16, TYPE_F32, check, elsewhere, lib
 
 _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
 _F32 = torch.float32
@@ -44,6 +44,8 @@ def _matrix(name, t):
     rows, width = t.shape
     if width < 1:
         raise ValueError("%s must have at least one column" % name)
+    if width > MOST_INT:
+        raise ValueError("%s must have at most %d columns" % (name, MOST_INT))
     return kind, t.get_device(), rows, width, width if t.is_contiguous() else _stride(name, t, width)
 
 
@@ -143,8 +145,8 @@ def _loss_args(x, w, targets, reduction, matrix):
     wkind, wdev, vocab, wwidth, ldw = _matrix("w", w)
     if wkind != kind or wdev != dev or wwidth != width:
         raise ValueError("w must be a %s matrix on %s with x's %d columns" % (x.dtype, x.device, width))
-    if vocab < 1:
-        raise ValueError("w must have at least one row")
+    if not 1 <= vocab <= MOST_INT:
+        raise ValueError("w must have at least one row, and at most %d" % MOST_INT)
     pt = _vector("targets", targets, rows, dev, (torch.int64, torch.int32))
     if reduction not in REDUCTIONS:
         raise ValueError("reduction must be one of %s" % ", ".join(sorted(REDUCTIONS)))
