@@ -11,12 +11,15 @@
  * scratch and CUDA graphs as in gemm_f32_lm.h.
  *
  * gemm_f32_last_kernel() names the kernel of a call's main pass:
- * "block_norm_kernel" (rows of up to 32768 columns at least, 131072 of them
- * with one vector) or "block_norm_grad_kernel" (up to 32768),
- * "block_norm_wide_kernel" or "block_norm_grad_wide_kernel" (wider ones),
- * "block_columns_kernel" (gradient of no rows), "checkpoint_kernel",
- * "restore_kernel", "half_gemm_kernel" (weight gradient), "memset" (weight
- * gradient of no rows).
+ * "block_norm_kernel" or "block_norm_grad_kernel" for rows of up to 32768
+ * columns and for wider ones where eight SMs hold two rows of each matrix and
+ * the vectors: forward up to 131072 (bfloat16, one vector, no gate) and 40960
+ * (fp32, four vectors and a gate matrix); the gradient for rms norms on both
+ * ends without a gate per channel alone, up to 65536 (bfloat16 without a gate)
+ * and 36864 (fp32 with a gate matrix).  "block_norm_wide_kernel" or
+ * "block_norm_grad_wide_kernel" beyond that, "block_columns_kernel" (gradient
+ * of no rows), "checkpoint_kernel", "restore_kernel", "half_gemm_kernel"
+ * (weight gradient), "memset" (weight gradient of no rows).
  *
  * Every sum is fp32 and taken in a fixed order: the same call on the same
  * inputs gives the same bits.
