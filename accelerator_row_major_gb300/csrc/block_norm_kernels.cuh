@@ -401,19 +401,12 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     });
     float c1[ROWS], c2[ROWS];
     if constexpr (kLate) {
-      constexpr int N = LAYER ? 2 : 1;
-      float v[2 * N];
-      v[0] = sum_of(sgh[0]);
-      v[N] = sum_of(late_seh);
-      if (LAYER) {
-        v[N - 1] = sum_of(sg[0]);
-        v[2 * N - 1] = sum_of(late_se);
-      }
-      sums.add<2 * N>(v);
-      c1[0] = LAYER ? -v[N - 1] * inv : 0.0f;
+      float v[4] = {sum_of(sgh[0]), sum_of(sg[0]), sum_of(late_seh), sum_of(late_se)};
+      sums.add<4>(v);
+      c1[0] = -v[1] * inv;
       c2[0] = -v[0] * inv;
       if (late_row >= 0) {
-        end_row(late_e, late_hat, late_rstd, LAYER ? -v[2 * N - 1] * inv : 0.0f, -v[N] * inv);
+        end_row(late_e, late_hat, late_rstd, -v[3] * inv, -v[2] * inv);
         store(a.dbranch, late_row, late_e, 1.0f);
       }
     } else {
