@@ -1,7 +1,7 @@
 // Private interface of the norms at a block's ends: how their rows are laid
 // out over threads and shared memory, and what the kernels are given
-// (block_norm.cu plans and checks, block_norm_f32.cu and block_norm_bf16.cu
-// hold the kernels of one type each).
+// (block_norm.cu checks, block_plan.h lays rows out, block_norm_f32.cu and
+// block_norm_bf16.cu hold the kernels of one type each).
 #pragma once
 
 #include <cuda_runtime.h>

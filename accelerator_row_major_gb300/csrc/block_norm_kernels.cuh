@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
 // them at the end (dpost_weight = gate sum d hat_b, dpost_bias = gate sum d,
 // dgate = post_weight sum d hat_b + post_bias sum d): two sums for three and
 // one vector, gate post_weight, for three on the way, which leaves room for two
-// rows at a time (layer norms, 8192 columns: 4096 rows of bfloat16 171 -> 120
-// us, 8192 of fp32 334 -> 280).
+// rows at a time (layer norms, 8192 columns: 4096 rows of bfloat16 126 us, 151
+// with one row at a time; 8192 of fp32 334 -> 280 with the fewer sums, 282 now).
 template <class T, int NE, int ROWS, bool VEC, bool LAYER, bool POST, bool CHANNEL>
 __global__ void __launch_bounds__(kProducerThreads + 32 * kRowWarps, 1)
     block_norm_grad_kernel(const __grid_constant__ BlockGradArgs a) {
@@ -952,7 +952,7 @@ int gradient(BlockGradArgs& a, void* const (&vectors_out)[kSums], const BlockLau
   *l.kernel = "block_columns_kernel";
   if (a.plan.rows > 0) {
     // two layer norms without a gate: the form with a gate of ones, whose sums leave room for two rows (4096 x 8192
-    // bfloat16 117 us against 130 with the form of any gate)
+    // bfloat16 123 us against 129 with the form of any gate; fp32 rows of 8192 are 10 % faster with that)
     const bool channel = a.gate == kChannelGate || (!a.rms && a.post && a.gate == kNoGate);
     rc = with_form(!a.rms, a.post, channel, [&](auto layer, auto post, auto by_channel) -> int {
       constexpr bool kLayer = decltype(layer)::value, kPost = decltype(post)::value, kChannel = decltype(by_channel)::value;

@@ -143,8 +143,8 @@ Layout<N> best_layout(const RowPlan& plan, const RowSource (&in)[N], const Lane 
 
 // What a thread has of many rows, besides the 8 elements of one: two rows of
 // them, or one row of 16, by the registers that the form's sums leave
-// (8192 x 4096 bfloat16, with a gate per channel 85 us against 119; rms norms
-// on both ends 86 with 16, 91 with 8).
+// (8192 x 4096 bfloat16, with a gate per channel 83 us against 92 with one row
+// of 8 and 119 with one of 16; rms norms on both ends 79 with 16, 104 with 8).
 constexpr Lane grad_lane(bool layer, bool post, bool channel) {
   return channel || !post ? Lane{8, 2} : layer ? Lane{8, 1} : Lane{16, 1};
 }
